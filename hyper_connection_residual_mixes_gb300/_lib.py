@@ -46,6 +46,10 @@ SIGNATURES = {
     "hc_chain_side": [P, P, P, P, P, P, P, I64, I32, I32, I32, F32, F32, P, P, P, ctypes.c_size_t,
                       P, P, P],
     "hc_chain_norm": [P, P, P, I64, I32, P, P, P, P],
+    "hc_layer_norm": [P, I64, I32, P, P, I32, I64, I32, F32, P, I64, P, P, P],
+    "hc_layer_norm_backward_workspace_bytes": [I64, I32],
+    "hc_layer_norm_backward": [P, I64, I32, P, I64, I32, P, I32, P, P, I64, I32, P, I64, P, P, P,
+                               ctypes.c_size_t, P],
 }
 
 STATUS = {
@@ -84,6 +88,7 @@ def load():
         lib.hc_status_string.restype = ctypes.c_char_p
         lib.hc_block_step_backward_workspace_bytes.restype = ctypes.c_size_t
         lib.hc_chain_state_bytes.restype = ctypes.c_size_t
+        lib.hc_layer_norm_backward_workspace_bytes.restype = ctypes.c_size_t
         _lib = lib
         return lib
 

@@ -8,6 +8,7 @@
 #include "../../include/hc.h"
 #include "hc_backward_generic.h"
 #include "hc_launch.h"
+#include "hc_sublayer.h"
 
 namespace {
 
@@ -63,6 +64,29 @@ hc_status check_alias(const Span *outs, int n_out, const Span *ins, int n_in) {
         for (int j = i + 1; j < n_out; ++j)
             if (overlaps(outs[i], outs[j])) return HC_ERR_ALIAS;
     }
+    return HC_OK;
+}
+
+// ---- sublayer operators: typed rows with a stride
+bool known(hc_dtype t) { return t == HC_F32 || t == HC_BF16 || t == HC_F16; }
+
+int64_t size_of(hc_dtype t) { return t == HC_F32 ? 4 : 2; }
+
+bool aligned_to(const void *p, int64_t bytes) { return (reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes) == 0; }
+
+// n rows of d elements, `stride` elements apart
+Span rows_span(const void *p, int64_t n, int64_t d, int64_t stride, hc_dtype t) {
+    return span(p, n > 0 ? ((n - 1) * stride + d) * size_of(t) : 0);
+}
+
+// rows whose extent in bytes stays far inside 64 bits
+bool rows_fit(int64_t n, int64_t d, int64_t stride) {
+    return stride >= 0 && n <= INT64_MAX / 64 / (stride > d ? stride : d > 0 ? d : 1);
+}
+
+hc_status check_norm(int64_t n, int d, hc_dtype x_type, hc_dtype w_type) {
+    if (n < 0 || d <= 0 || !known(x_type) || !known(w_type)) return HC_ERR_INVALID_ARG;
+    if (d > kMaxD || n > INT32_MAX || (w_type != HC_F32 && w_type != x_type)) return HC_ERR_UNSUPPORTED;
     return HC_OK;
 }
 
@@ -424,6 +448,64 @@ hc_status hc_chain_norm(const uint16_t *h_pre, const float *state, const float *
     hc_status st = check_alias(outs, 3, ins, 3);
     if (st != HC_OK) return st;
     return cuda_status(hc::launch_chain_norm(h_pre, state, norm_w, n, d, h_norm, codes, scales, stream));
+}
+
+hc_status hc_layer_norm(const void *x, int64_t x_stride, hc_dtype x_type, const void *norm_w,
+                        const void *norm_b, hc_dtype w_type, int64_t n, int d, float eps, void *y,
+                        int64_t y_stride, float *mean, float *rstd, cudaStream_t stream) {
+    hc_status st = check_norm(n, d, x_type, w_type);
+    if (st != HC_OK) return st;
+    if (!finite_nonneg(eps) || !rows_fit(n, d, x_stride) || !rows_fit(n, d, y_stride) || (n > 1 && y_stride < d))
+        return HC_ERR_INVALID_ARG;
+    if (n == 0) return HC_OK;
+    if (!x || !norm_w || !y) return HC_ERR_INVALID_ARG;
+    const int64_t xb = size_of(x_type), wb = size_of(w_type);
+    if (!aligned_to(x, xb) || !aligned_to(y, xb) || !aligned_to(norm_w, wb) || !aligned_to(norm_b, wb) ||
+        !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+        return HC_ERR_MISALIGNED;
+    const Span ins[] = {rows_span(x, n, d, x_stride, x_type), span(norm_w, d * wb), span(norm_b, norm_b ? d * wb : 0)};
+    const Span outs[] = {rows_span(y, n, d, y_stride, x_type), span(mean, mean ? n * 4 : 0),
+                         span(rstd, rstd ? n * 4 : 0)};
+    if ((st = check_alias(outs, 3, ins, 3)) != HC_OK) return st;
+    return cuda_status(hc::launch_layer_norm(x, x_stride, x_type, norm_w, norm_b, w_type, n, d, eps, y, y_stride,
+                                             mean, rstd, stream));
+}
+
+size_t hc_layer_norm_backward_workspace_bytes(int64_t n, int d) {
+    if (check_norm(n, d, HC_F32, HC_F32) != HC_OK) return 0;
+    return hc::layer_norm_backward_workspace_bytes(n, d);
+}
+
+hc_status hc_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dtype g_type, const void *x,
+                                 int64_t x_stride, hc_dtype x_type, const void *norm_w,
+                                 hc_dtype w_type, const float *mean, const float *rstd, int64_t n,
+                                 int d, void *g_x, int64_t gx_stride, float *g_norm_w,
+                                 float *g_norm_b, void *workspace, size_t workspace_bytes,
+                                 cudaStream_t stream) {
+    hc_status st = check_norm(n, d, x_type, w_type);
+    if (st != HC_OK) return st;
+    if (!known(g_type)) return HC_ERR_INVALID_ARG;
+    if (g_type != HC_F32 && g_type != x_type) return HC_ERR_UNSUPPORTED;
+    if (!rows_fit(n, d, x_stride) || !rows_fit(n, d, g_stride) || !rows_fit(n, d, gx_stride) ||
+        (n > 1 && gx_stride < d) || !g_norm_w)
+        return HC_ERR_INVALID_ARG;
+    if (n > 0 && (!g_y || !x || !norm_w || !mean || !rstd || !g_x || !workspace ||
+                  workspace_bytes < hc_layer_norm_backward_workspace_bytes(n, d)))
+        return HC_ERR_INVALID_ARG;
+    const int64_t xb = size_of(x_type), gb = size_of(g_type), wb = size_of(w_type);
+    if (!aligned_to(g_y, gb) || !aligned_to(x, xb) || !aligned_to(norm_w, wb) || !aligned_to(mean, 4) ||
+        !aligned_to(rstd, 4) || !aligned_to(g_x, gb) || !aligned_to(g_norm_w, 4) || !aligned_to(g_norm_b, 4) ||
+        (n > 0 && !aligned16(workspace)))
+        return HC_ERR_MISALIGNED;
+    const Span ins[] = {rows_span(g_y, n, d, g_stride, g_type), rows_span(x, n, d, x_stride, x_type),
+                        span(norm_w, n > 0 ? d * wb : 0), span(mean, n * 4), span(rstd, n * 4)};
+    const Span outs[] = {rows_span(g_x, n, d, gx_stride, g_type), span(g_norm_w, (int64_t)d * 4),
+                         span(g_norm_b, g_norm_b ? (int64_t)d * 4 : 0),
+                         span(workspace, (int64_t)hc_layer_norm_backward_workspace_bytes(n, d))};
+    if ((st = check_alias(outs, 4, ins, 5)) != HC_OK) return st;
+    return cuda_status(hc::launch_layer_norm_backward(g_y, g_stride, g_type, x, x_stride, x_type, norm_w, w_type,
+                                                      mean, rstd, n, d, g_x, gx_stride, g_norm_w, g_norm_b,
+                                                      workspace, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,26 @@
+// hc_sublayer.h -- internal launcher prototypes of the sublayer operators
+// (layer norm, experts' matrix products, AdamW).  Arguments have been
+// validated by hc_api_sublayer.cu before any of these is called.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/hc.h"
+
+namespace hc {
+
+// ------------------------------------------------------------ layer norm (hc_layer_norm.cu)
+cudaError_t launch_layer_norm(const void *x, int64_t x_stride, hc_dtype x_type, const void *w, const void *b,
+                              hc_dtype w_type, int64_t n, int d, float eps, void *y, int64_t y_stride,
+                              float *mean, float *rstd, cudaStream_t s);
+
+size_t layer_norm_backward_workspace_bytes(int64_t n, int d);
+cudaError_t launch_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dtype g_type, const void *x,
+                                       int64_t x_stride, hc_dtype x_type, const void *w, hc_dtype w_type,
+                                       const float *mean, const float *rstd, int64_t n, int d, void *g_x,
+                                       int64_t gx_stride, float *g_w, float *g_b, void *workspace,
+                                       cudaStream_t s);
+
+}  // namespace hc

@@ -342,6 +342,56 @@ hc_status hc_chain_norm(const uint16_t *h_pre, const float *state, const float *
                         int d, uint16_t *h_norm, uint8_t *codes, uint8_t *scales,
                         cudaStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Sublayer operators: what stands between two steps of the path when a model
+ * is trained or served.  Element types are given by an hc_dtype; pointers need
+ * the alignment of their elements only (HC_ERR_MISALIGNED otherwise) unless
+ * stated; rows may be further apart than their length (strides in elements).
+ */
+typedef enum {
+    HC_F32 = 0,
+    HC_BF16 = 1,
+    HC_F16 = 2
+} hc_dtype;
+
+/*
+ * Layer norm of n rows of d values (1 <= d <= 16384), e.g. of the bf16 h that a
+ * chain launch writes (h_pre_out):
+ *   mean = sum x / d,  rstd = 1 / sqrt(sum (x - mean)^2 / d + eps),
+ *   y = (x - mean) rstd norm_w + norm_b,
+ * sums and statistics in fp32, y rounded once to x's type.
+ *   x [n, d] of x_type, rows x_stride apart (0 <= x_stride)               in
+ *   norm_w [d], norm_b [d] of w_type: fp32 or x_type; norm_b may be NULL   in
+ *   y [n, d] of x_type, rows y_stride >= d apart                          out
+ *   mean, rstd [n] fp32, each may be NULL (for the backward)              out
+ */
+hc_status hc_layer_norm(const void *x, int64_t x_stride, hc_dtype x_type, const void *norm_w,
+                        const void *norm_b, hc_dtype w_type, int64_t n, int d, float eps, void *y,
+                        int64_t y_stride, float *mean, float *rstd, cudaStream_t stream);
+
+/*
+ * The backward of hc_layer_norm.  With xh = (x - mean) rstd and wg = g_y norm_w:
+ *   g_x = rstd (wg - mean(wg) - xh mean(wg xh)),
+ *   g_norm_w = sum over rows of g_y xh,  g_norm_b = sum over rows of g_y,
+ * all sums in fp32 and in an order fixed by n, d, the strides' alignment and the device (the same call
+ * gives the same bits).  With n = 0 the sums are written as zeros.
+ *   g_y [n, d] of g_type: fp32 or x_type                                   in
+ *   x, norm_w as in the forward; mean, rstd [n] as it wrote them           in
+ *   g_x [n, d] of g_type, rows gx_stride >= d apart                        out
+ *   g_norm_w [d] fp32; g_norm_b [d] fp32, may be NULL                      out
+ *   workspace of hc_layer_norm_backward_workspace_bytes(n, d) bytes,
+ *   16-byte aligned: scratch of this call, free for others once it has completed.
+ */
+size_t hc_layer_norm_backward_workspace_bytes(int64_t n, int d);
+
+hc_status hc_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dtype g_type, const void *x,
+                                 int64_t x_stride, hc_dtype x_type, const void *norm_w,
+                                 hc_dtype w_type, const float *mean, const float *rstd, int64_t n,
+                                 int d, void *g_x, int64_t gx_stride, float *g_norm_w,
+                                 float *g_norm_b, void *workspace, size_t workspace_bytes,
+                                 cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
