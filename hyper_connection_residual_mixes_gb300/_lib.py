@@ -21,6 +21,7 @@ P = ctypes.c_void_p
 I64 = ctypes.c_int64
 I32 = ctypes.c_int
 F32 = ctypes.c_float
+F64 = ctypes.c_double
 
 # name -> argtypes, in the order of include/hc.h
 SIGNATURES = {
@@ -50,7 +51,16 @@ SIGNATURES = {
     "hc_layer_norm_backward_workspace_bytes": [I64, I32],
     "hc_layer_norm_backward": [P, I64, I32, P, I64, I32, P, I32, P, P, I64, I32, P, I64, P, P, P,
                                ctypes.c_size_t, P],
+    "hc_adamw_step": [P, I64, F64, F64, F64, F64, F64, I64, P, P, P, P],
 }
+
+
+class AdamwTensor(ctypes.Structure):
+    """hc_adamw_tensor."""
+    _fields_ = [("p", P), ("g", P), ("m", P), ("v", P), ("m_scales", P), ("v_scales", P), ("p_copy", P),
+                ("numel", I64), ("p_type", ctypes.c_int32), ("g_type", ctypes.c_int32),
+                ("copy_type", ctypes.c_int32)]
+
 
 STATUS = {
     0: "HC_OK",

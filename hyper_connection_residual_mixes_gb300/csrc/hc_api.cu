@@ -1,9 +1,11 @@
 // hc_api.cu -- the C ABI of libhc: host-side validation, then dispatch to the
 // kernels.  Nothing here allocates device memory; every launch goes on the
 // caller's stream.  See include/hc.h for the contract of each entry point.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <new>
 
 #include "../../include/hc.h"
 #include "hc_backward_generic.h"
@@ -82,6 +84,41 @@ Span rows_span(const void *p, int64_t n, int64_t d, int64_t stride, hc_dtype t) 
 // rows whose extent in bytes stays far inside 64 bits
 bool rows_fit(int64_t n, int64_t d, int64_t stride) {
     return stride >= 0 && n <= INT64_MAX / 64 / (stride > d ? stride : d > 0 ? d : 1);
+}
+
+// A range of memory that a call reads or writes, for checks over many tensors.
+struct Use {
+    uintptr_t lo, hi;
+    bool written;
+};
+
+// Whether a written range meets any other range: sorted by start, each range is
+// compared with the furthest end so far, of the written ones or (if it is
+// written itself) of all.
+bool any_overlap(Use *u, int64_t n) {
+    std::sort(u, u + n, [](const Use &a, const Use &b) { return a.lo < b.lo; });
+    uintptr_t written_end = 0, end = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (u[i].lo < (u[i].written ? end : written_end)) return true;
+        if (u[i].hi > end) end = u[i].hi;
+        if (u[i].written && u[i].hi > written_end) written_end = u[i].hi;
+    }
+    return false;
+}
+
+hc_status check_adamw_tensor(const hc_adamw_tensor &t) {
+    const hc_dtype pt = (hc_dtype)t.p_type, gt = (hc_dtype)t.g_type, ct = (hc_dtype)t.copy_type;
+    if (t.numel < 0 || t.numel > (int64_t)1 << 42 || !known(pt) || !known(gt)) return HC_ERR_INVALID_ARG;
+    if (!t.m_scales != !t.v_scales) return HC_ERR_INVALID_ARG;
+    if (gt != HC_F32 && gt != pt) return HC_ERR_UNSUPPORTED;
+    if (t.p_copy && (pt != HC_F32 || (ct != HC_BF16 && ct != HC_F16))) return HC_ERR_UNSUPPORTED;
+    if (t.numel == 0) return HC_OK;
+    if (!t.p || !t.g || !t.m || !t.v) return HC_ERR_INVALID_ARG;
+    const int64_t state = t.m_scales ? 1 : 4;
+    if (!aligned_to(t.p, size_of(pt)) || !aligned_to(t.g, size_of(gt)) || !aligned_to(t.m, state) ||
+        !aligned_to(t.v, state) || !aligned_to(t.p_copy, 2))
+        return HC_ERR_MISALIGNED;
+    return HC_OK;
 }
 
 hc_status check_norm(int64_t n, int d, hc_dtype x_type, hc_dtype w_type) {
@@ -506,6 +543,51 @@ hc_status hc_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dtype g_t
     return cuda_status(hc::launch_layer_norm_backward(g_y, g_stride, g_type, x, x_stride, x_type, norm_w, w_type,
                                                       mean, rstd, n, d, g_x, gx_stride, g_norm_w, g_norm_b,
                                                       workspace, stream));
+}
+
+hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr, double beta1,
+                        double beta2, double eps, double weight_decay, int64_t step,
+                        const float *lr_dev, const int64_t *step_dev, const float *grad_scale,
+                        cudaStream_t stream) {
+    const bool beta_ok = beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0;
+    if (count < 0 || count > (1 << 24) || !beta_ok || step < 1 || !(std::isfinite(lr) && lr >= 0.0) ||
+        !(std::isfinite(eps) && eps >= 0.0) || !(std::isfinite(weight_decay) && weight_decay >= 0.0))
+        return HC_ERR_INVALID_ARG;
+    if (count == 0) return HC_OK;
+    if (!tensors) return HC_ERR_INVALID_ARG;
+    if (!aligned_to(lr_dev, 4) || !aligned_to(step_dev, 8) || !aligned_to(grad_scale, 4)) return HC_ERR_MISALIGNED;
+    for (int64_t i = 0; i < count; ++i) {
+        const hc_status st = check_adamw_tensor(tensors[i]);
+        if (st != HC_OK) return st;
+    }
+    Use few[64];
+    Use *const use = 7 * count + 3 <= 64 ? few : new (std::nothrow) Use[7 * count + 3];
+    if (!use) return cuda_status(cudaErrorMemoryAllocation);
+    int64_t k = 0;
+    const auto add = [&](const void *p, int64_t bytes, bool written) {
+        if (!p || bytes <= 0) return;
+        const Span r = span(p, bytes);
+        use[k++] = Use{r.lo, r.hi, written};
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        const hc_adamw_tensor &t = tensors[i];
+        const int64_t state = t.m_scales ? 1 : 4, groups = (t.numel + 31) / 32;
+        add(t.p, t.numel * size_of((hc_dtype)t.p_type), true);
+        add(t.g, t.numel * size_of((hc_dtype)t.g_type), false);
+        add(t.m, t.numel * state, true);
+        add(t.v, t.numel * state, true);
+        add(t.m_scales, groups, true);
+        add(t.v_scales, groups, true);
+        add(t.p_copy, t.numel * 2, true);
+    }
+    add(lr_dev, 4, false);
+    add(step_dev, 8, false);
+    add(grad_scale, 4, false);
+    const bool clash = any_overlap(use, k);
+    if (use != few) delete[] use;
+    if (clash) return HC_ERR_ALIAS;
+    return cuda_status(hc::launch_adamw(tensors, count, lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev,
+                                        grad_scale, stream));
 }
 
 }  // extern "C"

@@ -23,4 +23,9 @@ cudaError_t launch_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dty
                                        int64_t gx_stride, float *g_w, float *g_b, void *workspace,
                                        cudaStream_t s);
 
+// ------------------------------------------------------------ AdamW (hc_adamw.cu)
+cudaError_t launch_adamw(const hc_adamw_tensor *tensors, int64_t count, double lr, double beta1, double beta2,
+                         double eps, double weight_decay, int64_t step, const float *lr_dev, const int64_t *step_dev,
+                         const float *grad_scale, cudaStream_t s);
+
 }  // namespace hc

@@ -14,7 +14,7 @@ import torch
 
 from . import _lib
 
-__all__ = ["hc_layer_norm", "hc_layer_norm_backward"]
+__all__ = ["hc_layer_norm", "hc_layer_norm_backward", "adamw_state", "adamw_plan", "hc_adamw_step"]
 
 LAYER_NORM_EPS = 1e-5
 
@@ -171,3 +171,111 @@ def hc_layer_norm_backward(g_y, x, norm_w, mean, rstd, bias=True, g_x=None, work
     if bias:
         out["g_norm_b"] = g_b
     return out
+
+
+STATE_GROUP = 32  # values of a tensor that share a scale in the 8-bit states
+
+
+def adamw_state(p, mxfp8=False):
+    """Zero states (m, v) for a parameter: fp32 tensors of its shape, or with mxfp8
+    pairs (codes uint8 of its shape, scales uint8 [ceil(numel / 32)])."""
+    if not mxfp8:
+        return (torch.zeros(p.shape, dtype=torch.float32, device=p.device),
+                torch.zeros(p.shape, dtype=torch.float32, device=p.device))
+    groups = -(-p.numel() // STATE_GROUP)
+    return tuple((torch.zeros(p.shape, dtype=torch.uint8, device=p.device),
+                  torch.zeros((groups,), dtype=torch.uint8, device=p.device)) for _ in range(2))
+
+
+class AdamwPlan:
+    """The tensors of hc_adamw_step, checked and described once (adamw_plan).  It
+    keeps them alive; a tensor whose storage has moved since (t.data = ...) is
+    described anew by the next step, one of another shape or type is refused."""
+
+    def __init__(self, fields, device):
+        self._fields = fields      # (tensor, index of the description, its member, numel, dtype)
+        self.device = device
+        self.count = 1 + max((f[1] for f in fields), default=-1)
+        self._array = (_lib.AdamwTensor * self.count)()
+        self._at = []
+
+    def _describe(self):
+        at = [f[0].data_ptr() for f in self._fields]
+        if at == self._at:
+            return
+        for (t, i, member, numel, dtype), ptr in zip(self._fields, at):
+            if t.numel() != numel or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
+                raise ValueError("%s of tensor %d has changed since the plan was made" % (member, i))
+            setattr(self._array[i], member, ptr)
+            if member == "p":
+                self._array[i].numel = numel
+            if member in ("p", "g", "p_copy"):
+                setattr(self._array[i], "copy_type" if member == "p_copy" else member + "_type", _DTYPE[dtype])
+        self._at = at
+
+
+def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None):
+    """The plan of hc_adamw_step: lists of equal length of contiguous CUDA tensors
+    on one device.  params[i] fp32, bf16 or fp16; grads[i] of its shape, fp32 or
+    its type; exp_avg[i], exp_avg_sq[i] as adamw_state makes them (fp32, or
+    (codes, scales) pairs); copies[i] (optional, None where there is none): a
+    bf16 or fp16 tensor that receives an fp32 parameter's new value rounded."""
+    params, grads, exp_avg, exp_avg_sq = list(params), list(grads), list(exp_avg), list(exp_avg_sq)
+    copies = [None] * len(params) if copies is None else list(copies)
+    if not params:
+        raise ValueError("params is empty")
+    if not len(params) == len(grads) == len(exp_avg) == len(exp_avg_sq) == len(copies):
+        raise ValueError("params, grads, exp_avg, exp_avg_sq and copies must have one entry per parameter")
+    for i, (p, g, m, v, c) in enumerate(zip(params, grads, exp_avg, exp_avg_sq, copies)):
+        for t, name in ((p, "params"), (g, "grads")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("%s[%d] must be a torch.Tensor" % (name, i))
+        if p.dtype not in _DTYPE:
+            raise TypeError("params[%d] must be %s, got %s" % (i, _NAMES, p.dtype))
+        if isinstance(m, torch.Tensor) != isinstance(v, torch.Tensor):
+            raise TypeError("exp_avg[%d] and exp_avg_sq[%d] must be of one kind" % (i, i))
+        if c is not None and p.dtype != torch.float32:
+            raise TypeError("copies[%d]: only fp32 parameters have one" % i)
+    dev = params[0].device if isinstance(params[0], torch.Tensor) else None
+    fields = []
+    for i, (p, g, m, v, c) in enumerate(zip(params, grads, exp_avg, exp_avg_sq, copies)):
+        def field(t, name, member, dtypes, shape):
+            _dense(t, "%s[%d]" % (name, i), dtypes, shape, dev)
+            fields.append((t, i, member, t.numel(), t.dtype))
+        field(p, "params", "p", (p.dtype,), p.shape)
+        field(g, "grads", "g", (torch.float32, p.dtype) if p.dtype != torch.float32 else (torch.float32,), p.shape)
+        for s, name, member in ((m, "exp_avg", "m"), (v, "exp_avg_sq", "v")):
+            if isinstance(s, torch.Tensor):
+                field(s, name, member, (torch.float32,), p.shape)
+            else:
+                field(s[0], name, member, (torch.uint8,), p.shape)
+                field(s[1], name + " scales", member + "_scales", (torch.uint8,), (-(-p.numel() // STATE_GROUP),))
+        if c is not None:
+            field(c, "copies", "p_copy", (torch.bfloat16, torch.float16), p.shape)
+    return AdamwPlan(fields, dev)
+
+
+def hc_adamw_step(plan, lr, step, betas=(0.9, 0.999), adam_eps=1e-8, weight_decay=0.01, grad_scale=None, stream=None):
+    """One AdamW step over the plan's tensors, in place.  lr is a number or a
+    one-element fp32 CUDA tensor, step a number from 1 on or a one-element int64
+    CUDA tensor (so that a captured step reads the current ones); grad_scale, a
+    one-element fp32 CUDA tensor, multiplies the gradients."""
+    if not isinstance(plan, AdamwPlan):
+        raise TypeError("plan must come from adamw_plan")
+    dev = plan.device
+    on_device = []
+    for t, name, dtype in ((lr, "lr", torch.float32), (step, "step", torch.int64), (grad_scale, "grad_scale", torch.float32)):
+        if isinstance(t, torch.Tensor):
+            _tensor(t, name, (dtype,), dev)
+            if t.numel() != 1:
+                raise ValueError("%s must have one element" % name)
+            on_device.append(t.data_ptr())
+        else:
+            on_device.append(None)
+    if grad_scale is not None and on_device[2] is None:
+        raise TypeError("grad_scale must be a CUDA tensor")
+    plan._describe()
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        _lib.call("hc_adamw_step", plan._array, plan.count, 0.0 if on_device[0] else lr, betas[0], betas[1], adam_eps,
+                  weight_decay, 1 if on_device[1] else step, on_device[0], on_device[1], on_device[2], raw)

@@ -392,6 +392,49 @@ hc_status hc_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dtype g_t
                                  float *g_norm_b, void *workspace, size_t workspace_bytes,
                                  cudaStream_t stream);
 
+/*
+ * One AdamW step over many tensors, in place.  Per value, t the step number:
+ *   g <- g * grad_scale (when given)
+ *   m <- m beta1 + g (1 - beta1),  v <- v beta2 + g g (1 - beta2)
+ *   p <- p (1 - lr weight_decay)
+ *        - m / (sqrt(v) / sqrt(1 - beta2^t) + eps) * lr / (1 - beta1^t)
+ * in fp32, every operation rounded once in the order written (the coefficients
+ * in 64 bits, then rounded once); p is rounded to nearest in its own type.
+ *
+ * A tensor's states are fp32 (m_scales and v_scales NULL), or 8 bits: m [numel]
+ * E4M3 codes and v [numel] E4M3 codes of r = sqrt(v), with a UE8M0 scale byte per
+ * group of 32 values (the last group may be shorter) in m_scales, v_scales
+ * [ceil(numel / 32)].  The value of a code is its E4M3 value times
+ * 2^(byte - 127); the step writes as scale the smallest power of two at or above
+ * amax / 448 (from 2^-126 on), codes to nearest, ties to even, and for a positive
+ * r at least the smallest positive code.  All bytes zero stand for zero states.
+ *
+ *   tensors [count], an array in HOST memory; it is read during the call only
+ *   p of p_type; g of g_type: fp32 or p_type; p_copy (optional, p_type HC_F32
+ *   only) receives the new p rounded to copy_type, HC_BF16 or HC_F16
+ *   lr >= 0, 0 <= beta < 1, eps >= 0, weight_decay >= 0, step >= 1
+ *   lr_dev [1] fp32, step_dev [1] int64, DEVICE, each may be NULL: used in place of
+ *   lr and step, so that a captured graph reads the current ones (a step below 1
+ *   counts as 1; the bias corrections then come from fp32 functions)
+ *   grad_scale [1] fp32, DEVICE, may be NULL
+ * Everything a tensor's step writes must be disjoint from all that the call
+ * reads or writes otherwise, a tensor given twice included (HC_ERR_ALIAS).
+ */
+typedef struct {
+    void *p;
+    const void *g;
+    void *m, *v;
+    uint8_t *m_scales, *v_scales;
+    void *p_copy;
+    int64_t numel;
+    int32_t p_type, g_type, copy_type; /* hc_dtype */
+} hc_adamw_tensor;
+
+hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr, double beta1,
+                        double beta2, double eps, double weight_decay, int64_t step,
+                        const float *lr_dev, const int64_t *step_dev, const float *grad_scale,
+                        cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
