@@ -121,6 +121,16 @@ hc_status check_adamw_tensor(const hc_adamw_tensor &t) {
     return HC_OK;
 }
 
+hc_status check_grouped(int64_t n, int experts, int N, int K, hc_dtype type, hc_dtype out_type) {
+    if (n < 0 || experts <= 0 || N <= 0 || K <= 0 || !known(type) || !known(out_type)) return HC_ERR_INVALID_ARG;
+    if (type == HC_F32 || (out_type != HC_F32 && out_type != type) || experts > 1024 || N % 8 || K % 8 || n > INT32_MAX)
+        return HC_ERR_UNSUPPORTED;
+    // sizes that no device memory holds (and whose tile counts would not fit 32 bits)
+    const int64_t most = (int64_t)1 << 40;
+    if (n * N > most || n * K > most || (int64_t)N * K > most / experts) return HC_ERR_UNSUPPORTED;
+    return HC_OK;
+}
+
 hc_status check_norm(int64_t n, int d, hc_dtype x_type, hc_dtype w_type) {
     if (n < 0 || d <= 0 || !known(x_type) || !known(w_type)) return HC_ERR_INVALID_ARG;
     if (d > kMaxD || n > INT32_MAX || (w_type != HC_F32 && w_type != x_type)) return HC_ERR_UNSUPPORTED;
@@ -149,7 +159,7 @@ int hc_last_cuda_error(void) { return g_last_cuda_error; }
 int hc_version(void) { return 100; }
 
 hc_status hc_consume_device_error(cudaStream_t stream) {
-    unsigned int flag = 0, flag_chain = 0, flag_bwd = 0, flag_proj = 0;
+    unsigned int flag = 0, flag_chain = 0, flag_bwd = 0, flag_proj = 0, flag_grouped = 0;
     hc_status st = cuda_status(hc::consume_device_error(stream, &flag));
     if (st != HC_OK) return st;
     st = cuda_status(hc::consume_slices_device_error(stream, &flag_chain));
@@ -158,7 +168,11 @@ hc_status hc_consume_device_error(cudaStream_t stream) {
     if (st != HC_OK) return st;
     st = cuda_status(hc::consume_proj_device_error(stream, &flag_proj));
     if (st != HC_OK) return st;
-    return (flag | flag_chain | flag_bwd | flag_proj) ? HC_ERR_TIMEOUT : HC_OK;
+    st = cuda_status(hc::consume_grouped_mm_device_error(stream, &flag_grouped));
+    if (st != HC_OK) return st;
+    // (bit 0 of each: a wait ran out; bit 1 of the grouped products': bad offsets)
+    if (flag | flag_chain | flag_bwd | flag_proj | (flag_grouped & 1u)) return HC_ERR_TIMEOUT;
+    return flag_grouped ? HC_ERR_INVALID_ARG : HC_OK;
 }
 
 hc_status hc_selftest_barrier_timeout(cudaStream_t stream) {
@@ -588,6 +602,51 @@ hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr
     if (clash) return HC_ERR_ALIAS;
     return cuda_status(hc::launch_adamw(tensors, count, lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev,
                                         grad_scale, stream));
+}
+
+hc_status hc_grouped_mm(const void *x, int64_t x_stride, const void *w, int transposed,
+                        const int32_t *offsets, int64_t n, int experts, int N, int K, hc_dtype type,
+                        void *y, int64_t y_stride, hc_dtype y_type, int zero_rest,
+                        cudaStream_t stream) {
+    hc_status st = check_grouped(n, experts, N, K, type, y_type);
+    if (st != HC_OK) return st;
+    if (x_stride < K || y_stride < N || !rows_fit(n, K, x_stride) || !rows_fit(n, N, y_stride)) return HC_ERR_INVALID_ARG;
+    if (n == 0) return HC_OK;
+    if (!x || !w || !offsets || !y) return HC_ERR_INVALID_ARG;
+    if (x_stride % 8 || x_stride >= (int64_t)1 << 38) return HC_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(w) || !aligned_to(offsets, 4) || !aligned_to(y, size_of(y_type)))
+        return HC_ERR_MISALIGNED;
+    const Span ins[] = {rows_span(x, n, K, x_stride, type), span(w, (int64_t)experts * N * K * 2),
+                        span(offsets, ((int64_t)experts + 1) * 4)};
+    const Span outs[] = {rows_span(y, n, N, y_stride, y_type)};
+    if ((st = check_alias(outs, 1, ins, 3)) != HC_OK) return st;
+    return cuda_status(hc::launch_grouped_mm(x, x_stride, w, transposed != 0, offsets, n, experts, N, K, type == HC_F16, y,
+                                             y_stride, y_type == HC_F32, zero_rest != 0, stream));
+}
+
+hc_status hc_grouped_mm_weights(const void *g_y, int64_t g_stride, const void *x, int64_t x_stride,
+                                const int32_t *offsets, int64_t n, int experts, int N, int K,
+                                hc_dtype type, void *g_w, int transposed, hc_dtype g_type,
+                                cudaStream_t stream) {
+    hc_status st = check_grouped(n, experts, N, K, type, g_type);
+    if (st != HC_OK) return st;
+    if (x_stride < K || g_stride < N || !rows_fit(n, K, x_stride) || !rows_fit(n, N, g_stride)) return HC_ERR_INVALID_ARG;
+    if (!g_w || (n > 0 && (!g_y || !x || !offsets))) return HC_ERR_INVALID_ARG;
+    if (x_stride % 8 || g_stride % 8 || x_stride >= (int64_t)1 << 38 || g_stride >= (int64_t)1 << 38)
+        return HC_ERR_UNSUPPORTED;
+    if (!aligned16(g_y) || !aligned16(x) || !aligned_to(offsets, 4) || !aligned_to(g_w, size_of(g_type)))
+        return HC_ERR_MISALIGNED;
+    const int64_t bytes = (int64_t)experts * N * K * size_of(g_type);
+    if (n == 0) return cuda_status(cudaMemsetAsync(g_w, 0, (size_t)bytes, stream));  // sums over no rows
+    const Span ins[] = {rows_span(g_y, n, N, g_stride, type), rows_span(x, n, K, x_stride, type),
+                        span(offsets, ((int64_t)experts + 1) * 4)};
+    const Span outs[] = {span(g_w, bytes)};
+    if ((st = check_alias(outs, 1, ins, 3)) != HC_OK) return st;
+    // the innermost axis of g_w goes on the MMA's M side
+    const bool f16 = type == HC_F16, f32 = g_type == HC_F32;
+    return cuda_status(transposed
+                           ? hc::launch_grouped_mm_weights(x, x_stride, K, g_y, g_stride, N, offsets, n, experts, f16, g_w, f32, stream)
+                           : hc::launch_grouped_mm_weights(g_y, g_stride, N, x, x_stride, K, offsets, n, experts, f16, g_w, f32, stream));
 }
 
 }  // extern "C"

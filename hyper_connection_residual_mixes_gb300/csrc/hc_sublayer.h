@@ -28,4 +28,16 @@ cudaError_t launch_adamw(const hc_adamw_tensor *tensors, int64_t count, double l
                          double eps, double weight_decay, int64_t step, const float *lr_dev, const int64_t *step_dev,
                          const float *grad_scale, cudaStream_t s);
 
+// ------------------------------------------------------------ experts' products (hc_grouped_mm.cu)
+// y [n, N] = x [n, K] w[e]^T, w [experts][N][K] (w_kn: [experts][K][N]).
+cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bool w_kn, const int32_t *offsets, int64_t n,
+                              int experts, int N, int K, bool fp16, void *y, int64_t y_stride, bool y_f32,
+                              bool zero_rest, cudaStream_t s);
+// g_w [experts][C][F] = sum over the expert's rows of b[r][c] a[r][f].
+cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, const void *a, int64_t a_stride, int F,
+                                      const int32_t *offsets, int64_t n, int experts, bool fp16, void *g_w,
+                                      bool g_f32, cudaStream_t s);
+// as the other files' (hc_launch.h); bit 2: offsets out of order or out of range
+cudaError_t consume_grouped_mm_device_error(cudaStream_t s, unsigned int *flag);
+
 }  // namespace hc

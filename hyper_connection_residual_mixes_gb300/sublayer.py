@@ -14,7 +14,8 @@ import torch
 
 from . import _lib
 
-__all__ = ["hc_layer_norm", "hc_layer_norm_backward", "adamw_state", "adamw_plan", "hc_adamw_step"]
+__all__ = ["hc_layer_norm", "hc_layer_norm_backward", "hc_grouped_mm", "hc_grouped_mm_weights",
+           "hc_grouped_mm_backward", "adamw_state", "adamw_plan", "hc_adamw_step"]
 
 LAYER_NORM_EPS = 1e-5
 
@@ -171,6 +172,97 @@ def hc_layer_norm_backward(g_y, x, norm_w, mean, rstd, bias=True, g_x=None, work
     if bias:
         out["g_norm_b"] = g_b
     return out
+
+
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _grouped(rows, name, w_shape, offsets):
+    """The checks shared by the grouped products: rows [n, width] of 16-bit values,
+    the weights' shape, offsets.  Returns (n, row stride)."""
+    if not isinstance(rows, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if rows.dtype not in _HALF:
+        raise TypeError("%s must be torch.bfloat16 or torch.float16, got %s" % (name, rows.dtype))
+    if rows.dim() != 2 or len(w_shape) != 3:
+        raise ValueError("%s must be [n, width] and the weights [experts, ., .]" % name)
+    n, step = _rows(rows, name)
+    _tensor(rows, name)
+    _dense(offsets, "offsets", (torch.int32,), (w_shape[0] + 1,), rows.device)
+    # (a single row may carry any stride)
+    return n, step if n > 1 else rows.shape[1]
+
+
+def _out_rows(y, name, shape, types, dev):
+    _tensor(y, name, types, dev)
+    if tuple(y.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(y.shape), tuple(shape)))
+    n, step = _rows(y, name)
+    return step if n > 1 else shape[-1]
+
+
+def hc_grouped_mm(x, w, offsets, transposed=False, y=None, out_dtype=None, stream=None):
+    """Products of rows grouped by expert: x [n, K] (bf16 or fp16, rows sorted by
+    expert), w [experts, N, K] of x's type (with transposed [experts, K, N]),
+    offsets [experts + 1] int32 on the device -> y [n, N] of out_dtype (x's type
+    or fp32), y[r] = w[e] x[r] for offsets[e] <= r < offsets[e + 1].  Rows of no
+    expert are zeros in a y made here and stay as they are in a y given."""
+    _tensor(w, "w")
+    n, xs = _grouped(x, "x", w.shape, offsets)
+    dev = x.device
+    E, K = w.shape[0], x.shape[1]
+    N = w.shape[2] if transposed else w.shape[1]
+    _dense(w, "w", (x.dtype,), (E, K, N) if transposed else (E, N, K), dev)
+    if out_dtype is None:
+        out_dtype = x.dtype if y is None else y.dtype
+    if out_dtype not in (x.dtype, torch.float32):
+        raise TypeError("out_dtype must be %s or torch.float32, got %s" % (x.dtype, out_dtype))
+    zero = y is None
+    ys = N if zero else _out_rows(y, "y", (n, N), (out_dtype,), dev)
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        if zero:
+            y = torch.empty((n, N), dtype=out_dtype, device=dev)
+        _lib.call("hc_grouped_mm", x.data_ptr(), xs, w.data_ptr(), int(transposed), offsets.data_ptr(), n, E, N, K,
+                  _DTYPE[x.dtype], y.data_ptr(), ys, _DTYPE[out_dtype], int(zero), raw)
+    return y
+
+
+def hc_grouped_mm_weights(g_y, x, offsets, transposed=False, g_w=None, out_dtype=None, stream=None):
+    """The weights' gradient of hc_grouped_mm: g_y [n, N] and x [n, K] of one type ->
+    g_w [experts, N, K] (transposed: [experts, K, N]) of out_dtype (x's type or
+    fp32), the sum over each expert's rows of g_y[r] x[r]^T."""
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be [experts + 1]")
+    E = offsets.shape[0] - 1
+    n, xs = _grouped(x, "x", (E, 0, 0), offsets)
+    dev = x.device
+    _tensor(g_y, "g_y", (x.dtype,), dev)
+    if g_y.dim() != 2 or g_y.shape[0] != n:
+        raise ValueError("g_y has shape %s, expected (%d, N)" % (tuple(g_y.shape), n))
+    gs = _grouped(g_y, "g_y", (E, 0, 0), offsets)[1]
+    N, K = g_y.shape[1], x.shape[1]
+    shape = (E, K, N) if transposed else (E, N, K)
+    if out_dtype is None:
+        out_dtype = x.dtype if g_w is None else g_w.dtype
+    if out_dtype not in (x.dtype, torch.float32):
+        raise TypeError("out_dtype must be %s or torch.float32, got %s" % (x.dtype, out_dtype))
+    if g_w is not None:
+        _dense(g_w, "g_w", (out_dtype,), shape, dev)
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        if g_w is None:
+            g_w = torch.empty(shape, dtype=out_dtype, device=dev)
+        _lib.call("hc_grouped_mm_weights", g_y.data_ptr(), gs, x.data_ptr(), xs, offsets.data_ptr(), n, E, N, K,
+                  _DTYPE[x.dtype], g_w.data_ptr(), int(transposed), _DTYPE[out_dtype], raw)
+    return g_w
+
+
+def hc_grouped_mm_backward(g_y, x, w, offsets, transposed=False, g_x=None, g_w=None, stream=None):
+    """Both gradients of hc_grouped_mm(x, w, offsets, transposed): a dict of g_x
+    [n, K] (rows of no expert as hc_grouped_mm's) and g_w of w's shape."""
+    return {"g_x": hc_grouped_mm(g_y, w, offsets, not transposed, y=g_x, stream=stream),
+            "g_w": hc_grouped_mm_weights(g_y, x, offsets, transposed, g_w=g_w, stream=stream)}
 
 
 STATE_GROUP = 32  # values of a tensor that share a scale in the 8-bit states

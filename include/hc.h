@@ -79,11 +79,13 @@ int hc_version(void);
 
 /*
  * Synchronise `stream`, then report and clear the library's device-side
- * error flag.  Kernels never spin without bound: a barrier wait that runs out
+ * error flags.  Kernels never spin without bound: a barrier wait that runs out
  * (a peer that never arrives) records a flag and the kernel returns early
  * with its outputs incomplete.  Returns HC_ERR_TIMEOUT if any kernel on this
- * device set the flag since the last call, HC_ERR_CUDA if synchronising
- * failed, HC_OK otherwise.  Not part of the method: a health check.
+ * device set the flag since the last call, HC_ERR_INVALID_ARG if
+ * hc_grouped_mm or hc_grouped_mm_weights met offsets out of order or out of
+ * range, HC_ERR_CUDA if synchronising failed, HC_OK otherwise.  Not part of the
+ * method: a health check.
  */
 hc_status hc_consume_device_error(cudaStream_t stream);
 
@@ -434,6 +436,43 @@ hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr
                         double beta2, double eps, double weight_decay, int64_t step,
                         const float *lr_dev, const int64_t *step_dev, const float *grad_scale,
                         cudaStream_t stream);
+
+/*
+ * Matrix products grouped by expert: the rows of a batch sorted by expert, rows
+ * offsets[e] <= r < offsets[e + 1] belong to expert e.
+ *
+ * hc_grouped_mm: y[r] = w[e] x[r], i.e. y[r][f] = sum_k x[r][k] w[e][f][k].  The
+ * gradient of x is the same call on the gradient of y with N and K swapped and
+ * the other `transposed`.
+ * hc_grouped_mm_weights: g_w[e][f][k] = sum over e's rows of g_y[r][f] x[r][k]; an
+ * expert without rows gets zeros.
+ * Products of bf16 or fp16 values are summed in fp32 in tensor memory (the
+ * tensor cores' additions, which may cut off rather than round the last bit of
+ * a partial sum) and rounded once to the output's type.
+ *
+ *   x [n, K] of type, rows x_stride >= K apart                               in
+ *   w [experts, N, K] of type, or with transposed [experts, K, N]            in
+ *   offsets [experts + 1] int32, DEVICE, ascending within [0, n]: read by the
+ *   kernel, so the host need not know them.  An expert whose range is out of order
+ *   or out of the rows counts as empty and is reported by hc_consume_device_error.
+ *   y [n, N] of y_type: type or fp32, rows y_stride >= N apart               out
+ *   Rows of y that belong to no expert (before offsets[0], from offsets[experts]
+ *   on) are left as they are, or with zero_rest written as zeros.
+ *   g_y [n, N] of type, rows g_stride >= N apart                             in
+ *   g_w [experts, N, K] (transposed: [experts, K, N]) of g_type: type or fp32    out
+ * type is HC_BF16 or HC_F16.  experts <= 1024; N and K multiples of 8; x, g_y and w
+ * start on 16 bytes and x_stride, g_stride are multiples of 8 (the tensor
+ * copies' rule; HC_ERR_UNSUPPORTED, HC_ERR_MISALIGNED otherwise).
+ */
+hc_status hc_grouped_mm(const void *x, int64_t x_stride, const void *w, int transposed,
+                        const int32_t *offsets, int64_t n, int experts, int N, int K, hc_dtype type,
+                        void *y, int64_t y_stride, hc_dtype y_type, int zero_rest,
+                        cudaStream_t stream);
+
+hc_status hc_grouped_mm_weights(const void *g_y, int64_t g_stride, const void *x, int64_t x_stride,
+                                const int32_t *offsets, int64_t n, int experts, int N, int K,
+                                hc_dtype type, void *g_w, int transposed, hc_dtype g_type,
+                                cudaStream_t stream);
 
 #ifdef __cplusplus
 }

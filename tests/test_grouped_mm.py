@@ -1,0 +1,64 @@
+"""The experts' products on the host: refusals of the C entry points (before any
+CUDA call; the pointers are not allocations) and of the binding."""
+import pytest
+import torch
+
+import hyper_connection_residual_mixes_gb300 as hcg
+from hyper_connection_residual_mixes_gb300 import _lib
+from hyper_connection_residual_mixes_gb300 import build as hc_build
+
+F32, BF16, F16 = 0, 1, 2
+A, STEP = 0x1000000, 0x10000000
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    hc_build.build()
+
+
+def _mm(**kw):
+    a = dict(x=A, xs=64, w=A + STEP, transposed=0, offsets=A + 2 * STEP, n=16, experts=4, N=32, K=64, type=BF16,
+             y=A + 3 * STEP, ys=32, yt=BF16, zero=0, stream=None)
+    a.update(kw)
+    return _lib.raw("hc_grouped_mm", *a.values())
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(n=-1), 1), (dict(experts=0), 1), (dict(N=0), 1), (dict(K=-8), 1), (dict(type=5), 1), (dict(yt=-1), 1),
+    (dict(type=F32, yt=F32), 2), (dict(type=F16), 2), (dict(experts=1025), 2), (dict(N=33, ys=40), 2), (dict(K=63), 2),
+    (dict(n=1 << 31), 2), (dict(xs=68), 2), (dict(xs=1 << 38), 2), (dict(N=1 << 30, K=1 << 30, xs=1 << 30, ys=1 << 30), 2),
+    (dict(xs=56), 1), (dict(ys=31), 1), (dict(x=None), 1), (dict(w=None), 1), (dict(offsets=None), 1), (dict(y=None), 1),
+    (dict(x=A + 8), 3), (dict(w=A + STEP + 2), 3), (dict(offsets=A + 2 * STEP + 2), 3), (dict(y=A + 3 * STEP + 1), 3),
+    (dict(yt=F32, y=A + 3 * STEP + 2), 3),
+    (dict(y=A + 64), 4), (dict(y=A + STEP + 100), 4), (dict(y=A + 2 * STEP + 16), 4),
+    (dict(n=0), 0), (dict(n=0, x=None, y=None), 0),
+])
+def test_product_refusals(kw, expect):
+    assert _mm(**kw) == expect
+
+
+def _weights(**kw):
+    a = dict(g=A, gs=32, x=A + STEP, xs=64, offsets=A + 2 * STEP, n=16, experts=4, N=32, K=64, type=F16, gw=A + 3 * STEP,
+             transposed=0, gt=F32, stream=None)
+    a.update(kw)
+    return _lib.raw("hc_grouped_mm_weights", *a.values())
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(n=-1), 1), (dict(experts=-3), 1), (dict(gt=9), 1), (dict(gt=BF16), 2), (dict(type=F32), 2), (dict(N=36, gs=40), 2),
+    (dict(gs=24), 1), (dict(gs=36), 2), (dict(xs=65), 2), (dict(g=None), 1), (dict(gw=None), 1), (dict(offsets=None), 1),
+    (dict(g=A + 2), 3), (dict(x=A + STEP + 8), 3), (dict(gw=A + 3 * STEP + 2), 3),
+    (dict(gw=A + 32), 4), (dict(gw=A + 2 * STEP), 4),
+])
+def test_weights_refusals(kw, expect):
+    assert _weights(**kw) == expect
+
+
+def test_binding_refusals():
+    x, w, off = torch.zeros(4, 64).bfloat16(), torch.zeros(2, 32, 64).bfloat16(), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        hcg.hc_grouped_mm(x, w, off)
+    with pytest.raises(ValueError, match="CUDA"):
+        hcg.hc_grouped_mm_weights(x[:, :32], x, off)
+    with pytest.raises(ValueError, match="experts"):
+        hcg.hc_grouped_mm_weights(x, x, off[:1])
