@@ -4,9 +4,14 @@
 //   g <- g * grad_scale                                  (when given)
 //   m <- m beta1 + g (1 - beta1),   v <- v beta2 + g g (1 - beta2),
 //   p <- p (1 - lr wd) - m / (sqrt(v) / sqrt(1 - beta2^t) + eps) * lr / (1 - beta1^t).
-// Every operation is an fp32 operation rounded once, in the order written
-// (no fused multiply-adds), so the result does not depend on how the tensors
-// are laid out or split over launches; p is rounded once more to its own type.
+// With fp32 states every operation is an fp32 operation rounded once, in the
+// order written (no fused multiply-adds); with 8-bit states products and sums
+// are fused, and the root and the reciprocal of the denominator are the
+// hardware's approximations (each within 2^-23 of its value, far below what the
+// codes resolve; a v below 2^-126 counts as zero): the exact ones made the step
+// bound by its instructions.
+// Either way a value's result does not depend on how the tensors are laid out or
+// split over launches.  p is rounded once more to its own type.
 //
 // States are fp32, or 8 bits in the format of the MXFP8 cast: groups of 32
 // values of a tensor share a power-of-two scale, each value is an E4M3 number
@@ -17,8 +22,8 @@
 //
 // The step reads and writes each value once and is bound by that: 28 bytes a
 // value for fp32 parameters, gradients and states, 10.1 for bf16 parameters
-// and gradients with 8-bit states.  All tensors of a call go in one launch
-// (their descriptions are kernel parameters, 448 at the most).
+// and gradients with 8-bit states.  All tensors of a call with one kind of states
+// go in one launch (their descriptions are kernel parameters, 448 at the most).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -31,9 +36,8 @@ namespace hc {
 namespace aw {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 4;      // values a thread holds at a time: 16 bytes of fp32, an eighth of a group of 32
-constexpr int kUnroll = 4;
-constexpr int kChunk = kThreads * kVec * kUnroll;  // values per block
+constexpr int kEach = 16;                 // values per thread and block
+constexpr int kChunk = kThreads * kEach;  // values per block
 
 struct Desc {
     void *p;
@@ -43,7 +47,7 @@ struct Desc {
     void *copy;
     int64_t numel;
     uint32_t first_block;
-    uint8_t p_type, g_type, copy_type, vec;  // vec: every pointer takes kVec-wide accesses
+    uint8_t p_type, g_type, copy_type, vec;  // vec: every pointer takes accesses of a thread's whole run
 };
 
 template <int CAP>
@@ -74,33 +78,37 @@ __device__ __forceinline__ T from_f(float v) {
     else if constexpr (__is_same(T, __half)) return __float2half_rn(v);
     else return __float2bfloat16_rn(v);
 }
-template <typename T>
-struct alignas(sizeof(T) * kVec) Vec {
-    T v[kVec];
+// Values a thread holds side by side: 16 bytes of the widest of p and g.
+template <typename TP, typename TG>
+constexpr int run_of() { return sizeof(TP) == 2 && sizeof(TG) == 2 ? 8 : 4; }
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+    T v[V];
 };
 
-// values [i, i + kVec) of p, those below n (the others read as zero)
-template <typename T>
-__device__ __forceinline__ Vec<T> load(const void *p, int64_t i, int64_t n, bool vec) {
+// values [i, i + V) of p, those below n (the others read as zero); kFull: all
+// are there and aligned, so that the loads of a chunk go out together
+template <bool kFull, typename T, int V>
+__device__ __forceinline__ Vec<T, V> load(const void *p, int64_t i, int64_t n) {
     const T *q = static_cast<const T *>(p) + i;
-    Vec<T> r{};
-    if (vec && i + kVec <= n) {
-        r = *reinterpret_cast<const Vec<T> *>(q);
+    Vec<T, V> r;
+    if constexpr (kFull) {
+        r = *reinterpret_cast<const Vec<T, V> *>(q);
     } else {
 #pragma unroll
-        for (int k = 0; k < kVec; ++k)
-            if (i + k < n) r.v[k] = q[k];
+        for (int k = 0; k < V; ++k) r.v[k] = i + k < n ? q[k] : T(0.0f);
     }
     return r;
 }
-template <typename T>
-__device__ __forceinline__ void store(void *p, int64_t i, int64_t n, bool vec, const Vec<T> &r) {
+template <bool kFull, typename T, int V>
+__device__ __forceinline__ void store(void *p, int64_t i, int64_t n, const Vec<T, V> &r) {
     T *q = static_cast<T *>(p) + i;
-    if (vec && i + kVec <= n) {
-        *reinterpret_cast<Vec<T> *>(q) = r;
+    if constexpr (kFull) {
+        *reinterpret_cast<Vec<T, V> *>(q) = r;
     } else {
 #pragma unroll
-        for (int k = 0; k < kVec; ++k)
+        for (int k = 0; k < V; ++k)
             if (i + k < n) q[k] = r.v[k];
     }
 }
@@ -109,140 +117,207 @@ __device__ __forceinline__ void store(void *p, int64_t i, int64_t n, bool vec, c
 __device__ __forceinline__ float scale_of(uint32_t byte) {  // 2^(byte - 127)
     return __uint_as_float(byte ? byte << 23 : 0x00400000u);
 }
-__device__ __forceinline__ void decode(const Vec<uint8_t> &c, float s, float (&o)[kVec]) {
-#pragma unroll
-    for (int k = 0; k < kVec; k += 2) {
-        const __half2_raw h =
-            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c.v[k] | (uint32_t)c.v[k + 1] << 8), __NV_E4M3);
-        const float2 f = __half22float2(__half2(h));
-        o[k] = __fmul_rn(f.x, s), o[k + 1] = __fmul_rn(f.y, s);
+// A thread's 16-bit values and codes in words, two or four to a word.
+template <typename T, int V>
+union Words {
+    Vec<T, V> v;
+    uint32_t w[sizeof(T) * V / 4];
+};
+template <typename T, int V>
+__device__ __forceinline__ f32x2 pair(const Vec<T, V> &x, int k) {  // values k, k + 1 (k even)
+    if constexpr (sizeof(T) == 4) {
+        return f2_make(x.v[k], x.v[k + 1]);
+    } else {
+        Words<T, V> u;
+        u.v = x;
+        if constexpr (__is_same(T, __half)) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u.w[k / 2]));
+            return f2_make(f.x, f.y);
+        } else {
+            return f2_from_bf16x2(u.w[k / 2]);
+        }
     }
 }
-// codes of a thread's four values; the eight threads of a group agree on its scale
-template <bool kRoot>
-__device__ __forceinline__ Vec<uint8_t> encode(const float (&x)[kVec], uint8_t &byte) {
-    float a = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+template <typename T, int V>
+__device__ __forceinline__ void put_pair(Vec<T, V> &x, int k, f32x2 v) {
+    float a, b;
+    f2_split(v, a, b);
+    if constexpr (sizeof(T) == 4) {
+        x.v[k] = a, x.v[k + 1] = b;
+    } else {
+        Words<T, V> u;
+        u.v = x;
+        if constexpr (__is_same(T, __half)) {
+            const __half2 h = __floats2half2_rn(a, b);
+            u.w[k / 2] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            u.w[k / 2] = pack_bf16x2(a, b);
+        }
+        x = u.v;
+    }
+}
+template <int V>
+__device__ __forceinline__ f32x2 pair_of_codes(const Vec<uint8_t, V> &c, int k) {
+    Words<uint8_t, V> u;
+    u.v = c;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u.w[k / 4] >> (k % 4 * 8)), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    return f2_make(f.x, f.y);
+}
+// Codes of a thread's values; the 32 / V threads of a group agree on its scale,
+// the smallest power of two at or above a / 448.  448 is 1.75 * 2^8, so with
+// a = 1.f * 2^E that power is 2^(E - 8), or 2^(E - 7) where 1.f > 1.75: adding
+// 0x1fffff to the bits carries into the exponent exactly then.
+template <bool kRoot, int V>
+__device__ __forceinline__ Vec<uint8_t, V> encode(const f32x2 (&x)[V / 2], uint8_t &byte) {
+    float a = 0.0f;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    // the smallest power of two at or above a / 448; no finite a needs one above 2^120
-    const uint32_t bits = __float_as_uint(__fdiv_rn(a, 448.0f));
-    int e = (int)(bits >> 23) + ((bits & 0x7fffffu) != 0);
-    e = e < 1 ? 1 : e > 247 ? 247 : e;
+    for (int k = 0; k < V / 2; ++k) {
+        float x0, x1;
+        f2_split(x[k], x0, x1);
+        a = kRoot ? fmaxf(a, fmaxf(x0, x1)) : fmaxf(a, fmaxf(fabsf(x0), fabsf(x1)));
+    }
+#pragma unroll
+    for (int o = 1; o < 32 / V; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    int e = (int)((__float_as_uint(a) + 0x1fffffu) >> 23) - 8;
+    e = e < 1 ? 1 : e > 247 ? 247 : e;  // (247: an infinite a)
     byte = (uint8_t)e;
-    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-    Vec<uint8_t> c;
+    const f32x2 inv = f2_dup(__uint_as_float((uint32_t)(254 - e) << 23));
+    Words<uint8_t, V> u;
 #pragma unroll
-    for (int k = 0; k < kVec; k += 2) {
-        const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(x[k] * inv, x[k + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        c.v[k] = (uint8_t)(two & 0xffu), c.v[k + 1] = (uint8_t)(two >> 8);
-    }
-    if (kRoot) {
+    for (int k = 0; k < V; k += 4) {
+        uint32_t two[2];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k)
-            if (c.v[k] == 0 && x[k] > 0.0f) c.v[k] = 1;
+        for (int h = 0; h < 2; ++h) {
+            float q0, q1;
+            f2_split(f2_mul(x[k / 2 + h], inv), q0, q1);
+            if (kRoot) {
+                // the smallest code stands for 2^-9; x 2^110, cut off at 1, is 1 for every
+                // positive root (they are at least 2^-75) and 0 for zero
+                float x0, x1;
+                f2_split(x[k / 2 + h], x0, x1);
+                q0 = fmaxf(q0, __saturatef(x0 * 0x1p110f) * 0x1p-9f);
+                q1 = fmaxf(q1, __saturatef(x1 * 0x1p110f) * 0x1p-9f);
+            }
+            two[h] = __nv_cvt_float2_to_fp8x2(make_float2(q0, q1), __NV_SATFINITE, __NV_E4M3);
+        }
+        u.w[k / 4] = two[0] | two[1] << 16;
     }
-    return c;
+    return u.v;
+}
+// Approximations of root and reciprocal, within 2^-23 of the value; numbers
+// below 2^-126 count as zero.
+__device__ __forceinline__ f32x2 sqrt_approx(f32x2 x) {
+    float a, b;
+    f2_split(x, a, b);
+    asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return f2_make(a, b);
+}
+__device__ __forceinline__ f32x2 rcp_approx(f32x2 x) {
+    float a, b;
+    f2_split(x, a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return f2_make(a, b);
 }
 
 struct Rates {
     float decay, rate, root, gscale;
 };
 
-template <typename TP, typename TG, bool kPacked>
+template <typename TP, typename TG, bool kPacked, bool kFull>
 __device__ __forceinline__ void chunk(const Desc &d, int64_t base, const Scalars &c, const Rates &r, bool scaled) {
+    constexpr int V = run_of<TP, TG>(), U = kEach / V;
     const int64_t n = d.numel;
-    const bool vec = d.vec;
-    Vec<TP> pv[kUnroll];
-    Vec<TG> gv[kUnroll];
-    Vec<float> mv[kPacked ? 1 : kUnroll], vv[kPacked ? 1 : kUnroll];
-    Vec<uint8_t> mc[kPacked ? kUnroll : 1], vc[kPacked ? kUnroll : 1];
-    uint8_t mb[kPacked ? kUnroll : 1], vb[kPacked ? kUnroll : 1];
+    Vec<TP, V> pv[U];
+    Vec<TG, V> gv[U];
+    Vec<float, V> mv[kPacked ? 1 : U], vv[kPacked ? 1 : U];
+    Vec<uint8_t, V> mc[kPacked ? U : 1], vc[kPacked ? U : 1];
+    uint8_t mb[kPacked ? U : 1], vb[kPacked ? U : 1];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const int64_t i = base + (int64_t)(u * kThreads + (int)threadIdx.x) * kVec;
-        pv[u] = load<TP>(d.p, i, n, vec);
-        gv[u] = load<TG>(d.g, i, n, vec);
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = base + (u * kThreads + (int)threadIdx.x) * V;
+        pv[u] = load<kFull, TP, V>(d.p, i, n);
+        gv[u] = load<kFull, TG, V>(d.g, i, n);
         if constexpr (kPacked) {
-            mc[u] = load<uint8_t>(d.m, i, n, vec);
-            vc[u] = load<uint8_t>(d.v, i, n, vec);
-            mb[u] = i < n ? d.ms[i >> 5] : 0;
-            vb[u] = i < n ? d.vs[i >> 5] : 0;
+            mc[u] = load<kFull, uint8_t, V>(d.m, i, n);
+            vc[u] = load<kFull, uint8_t, V>(d.v, i, n);
+            mb[u] = kFull || i < n ? d.ms[i >> 5] : 0;
+            vb[u] = kFull || i < n ? d.vs[i >> 5] : 0;
         } else {
-            mv[u] = load<float>(d.m, i, n, vec);
-            vv[u] = load<float>(d.v, i, n, vec);
+            mv[u] = load<kFull, float, V>(d.m, i, n);
+            vv[u] = load<kFull, float, V>(d.v, i, n);
         }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const int64_t i = base + (int64_t)(u * kThreads + (int)threadIdx.x) * kVec;
-        float m[kVec], v[kVec], root[kVec], p[kVec];
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = base + (u * kThreads + (int)threadIdx.x) * V;
+        float p[V];
         if constexpr (kPacked) {
-            decode(mc[u], scale_of(mb[u]), m);
-            decode(vc[u], scale_of(vb[u]), v);
+            f32x2 m[V / 2], root[V / 2];
+            const f32x2 ms = f2_dup(scale_of(mb[u])), rs = f2_dup(scale_of(vb[u]));
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = __fmul_rn(v[k], v[k]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) m[k] = mv[u].v[k], v[k] = vv[u].v[k];
-        }
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-            float g = to_f(gv[u].v[k]);
-            if (scaled) g = __fmul_rn(g, r.gscale);
-            m[k] = __fadd_rn(__fmul_rn(m[k], c.beta1), __fmul_rn(g, c.rest1));
-            v[k] = __fadd_rn(__fmul_rn(v[k], c.beta2), __fmul_rn(__fmul_rn(g, g), c.rest2));
-            root[k] = __fsqrt_rn(v[k]);
-            const float den = __fadd_rn(__fmul_rn(root[k], r.root), c.eps);
-            p[k] = __fsub_rn(__fmul_rn(to_f(pv[u].v[k]), r.decay), __fmul_rn(__fdiv_rn(m[k], den), r.rate));
-            pv[u].v[k] = from_f<TP>(p[k]);
-        }
-        if constexpr (kPacked) {
+            for (int k = 0; k < V / 2; ++k) {
+                const f32x2 g = f2_mul(pair(gv[u], 2 * k), f2_dup(r.gscale));
+                const f32x2 r0 = f2_mul(pair_of_codes(vc[u], 2 * k), rs);
+                m[k] = f2_fma(f2_mul(pair_of_codes(mc[u], 2 * k), ms), f2_dup(c.beta1), f2_mul(g, f2_dup(c.rest1)));
+                root[k] = sqrt_approx(f2_fma(f2_mul(g, f2_dup(c.rest2)), g, f2_mul(f2_mul(r0, r0), f2_dup(c.beta2))));
+                const f32x2 step = f2_mul(m[k], rcp_approx(f2_fma(root[k], f2_dup(r.root), f2_dup(c.eps))));
+                const f32x2 q = f2_fma(step, f2_dup(-r.rate), f2_mul(pair(pv[u], 2 * k), f2_dup(r.decay)));
+                put_pair(pv[u], 2 * k, q);
+                f2_split(q, p[2 * k], p[2 * k + 1]);
+            }
             // values behind the tensor's end read as zero and stay zero: they do not count in the group's scale
             uint8_t bm, br;
-            const Vec<uint8_t> cm = encode<false>(m, bm), cr = encode<true>(root, br);
-            if (i >= n) continue;
-            store(d.m, i, n, vec, cm);
-            store(d.v, i, n, vec, cr);
-            if ((threadIdx.x & 7) == 0) d.ms[i >> 5] = bm, d.vs[i >> 5] = br;
+            const Vec<uint8_t, V> cm = encode<false, V>(m, bm), cr = encode<true, V>(root, br);
+            if (kFull || i < n) {
+                store<kFull>(d.m, i, n, cm);
+                store<kFull>(d.v, i, n, cr);
+                if (threadIdx.x % (32 / V) == 0) d.ms[i >> 5] = bm, d.vs[i >> 5] = br;
+            }
         } else {
-            if (i >= n) continue;
-            Vec<float> om, ov;
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) om.v[k] = m[k], ov.v[k] = v[k];
-            store(d.m, i, n, vec, om);
-            store(d.v, i, n, vec, ov);
+            for (int k = 0; k < V; ++k) {
+                float g = to_f(gv[u].v[k]);
+                if (scaled) g = __fmul_rn(g, r.gscale);
+                const float m = __fadd_rn(__fmul_rn(mv[u].v[k], c.beta1), __fmul_rn(g, c.rest1));
+                const float v = __fadd_rn(__fmul_rn(vv[u].v[k], c.beta2), __fmul_rn(__fmul_rn(g, g), c.rest2));
+                const float den = __fadd_rn(__fmul_rn(__fsqrt_rn(v), r.root), c.eps);
+                p[k] = __fsub_rn(__fmul_rn(to_f(pv[u].v[k]), r.decay), __fmul_rn(__fdiv_rn(m, den), r.rate));
+                mv[u].v[k] = m, vv[u].v[k] = v;
+                pv[u].v[k] = from_f<TP>(p[k]);
+            }
+            store<kFull>(d.m, i, n, mv[u]);
+            store<kFull>(d.v, i, n, vv[u]);
         }
-        store(d.p, i, n, vec, pv[u]);
+        store<kFull>(d.p, i, n, pv[u]);
         if (sizeof(TP) == 4 && d.copy) {
             if (d.copy_type == HC_BF16) {
-                Vec<__nv_bfloat16> o;
+                Vec<__nv_bfloat16, V> o;
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) o.v[k] = __float2bfloat16_rn(p[k]);
-                store(d.copy, i, n, vec, o);
+                for (int k = 0; k < V; ++k) o.v[k] = __float2bfloat16_rn(p[k]);
+                store<kFull>(d.copy, i, n, o);
             } else {
-                Vec<__half> o;
+                Vec<__half, V> o;
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) o.v[k] = __float2half_rn(p[k]);
-                store(d.copy, i, n, vec, o);
+                for (int k = 0; k < V; ++k) o.v[k] = __float2half_rn(p[k]);
+                store<kFull>(d.copy, i, n, o);
             }
         }
     }
 }
 
-template <bool kPacked>
-__device__ __forceinline__ void by_type(const Desc &d, int64_t base, const Scalars &c, const Rates &r, bool scaled) {
-    if (d.p_type == HC_F32) chunk<float, float, kPacked>(d, base, c, r, scaled);
-    else if (d.p_type == HC_BF16) {
-        if (d.g_type == HC_F32) chunk<__nv_bfloat16, float, kPacked>(d, base, c, r, scaled);
-        else chunk<__nv_bfloat16, __nv_bfloat16, kPacked>(d, base, c, r, scaled);
-    } else {
-        if (d.g_type == HC_F32) chunk<__half, float, kPacked>(d, base, c, r, scaled);
-        else chunk<__half, __half, kPacked>(d, base, c, r, scaled);
-    }
+template <typename TP, typename TG, bool kPacked>
+__device__ __forceinline__ void whole_or_end(const Desc &d, int64_t base, const Scalars &c, const Rates &r, bool scaled) {
+    if (d.vec && base + kChunk <= d.numel) chunk<TP, TG, kPacked, true>(d, base, c, r, scaled);
+    else chunk<TP, TG, kPacked, false>(d, base, c, r, scaled);
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+// One kernel per kind of states: the 8-bit step needs half the registers, and
+// with four blocks on an SM instead of two its loads hide behind one another.
+template <int CAP, bool kPacked>
+__global__ void __launch_bounds__(kThreads, kPacked ? 4 : 2)
 k_adamw(const __grid_constant__ Descs<CAP> t, int count, const __grid_constant__ Scalars c) {
     // the last tensor whose first block is not behind this one
     int lo = 0, hi = count;
@@ -265,24 +340,31 @@ k_adamw(const __grid_constant__ Descs<CAP> t, int count, const __grid_constant__
     const bool scaled = c.grad_scale != nullptr;
     if (scaled) r.gscale = __ldg(c.grad_scale);
     const int64_t base = (int64_t)(blockIdx.x - d.first_block) * kChunk;
-    if (d.ms) by_type<true>(d, base, c, r, scaled);
-    else by_type<false>(d, base, c, r, scaled);
+    if (d.p_type == HC_F32) whole_or_end<float, float, kPacked>(d, base, c, r, scaled);
+    else if (d.p_type == HC_BF16) {
+        if (d.g_type == HC_F32) whole_or_end<__nv_bfloat16, float, kPacked>(d, base, c, r, scaled);
+        else whole_or_end<__nv_bfloat16, __nv_bfloat16, kPacked>(d, base, c, r, scaled);
+    } else {
+        if (d.g_type == HC_F32) whole_or_end<__half, float, kPacked>(d, base, c, r, scaled);
+        else whole_or_end<__half, __half, kPacked>(d, base, c, r, scaled);
+    }
 }
 
-bool vec_ok(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)(bytes * kVec) == 0; }
+bool run_ok(const void *p, int64_t bytes, int run) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)(bytes * run) == 0; }
 
 Desc describe(const hc_adamw_tensor &t) {
     Desc d{};
     d.p = t.p, d.g = t.g, d.m = t.m, d.v = t.v, d.ms = t.m_scales, d.vs = t.v_scales, d.copy = t.p_copy;
     d.numel = t.numel;
     d.p_type = (uint8_t)t.p_type, d.g_type = (uint8_t)t.g_type, d.copy_type = (uint8_t)t.copy_type;
-    const int64_t state = t.m_scales ? 1 : 4;
-    d.vec = vec_ok(t.p, t.p_type == HC_F32 ? 4 : 2) && vec_ok(t.g, t.g_type == HC_F32 ? 4 : 2) && vec_ok(t.m, state) &&
-            vec_ok(t.v, state) && (!t.p_copy || vec_ok(t.p_copy, 2));
+    const int64_t pb = t.p_type == HC_F32 ? 4 : 2, gb = t.g_type == HC_F32 ? 4 : 2, state = t.m_scales ? 1 : 4;
+    const int run = pb == 2 && gb == 2 ? 8 : 4;  // run_of
+    d.vec = run_ok(t.p, pb, run) && run_ok(t.g, gb, run) && run_ok(t.m, state, run) && run_ok(t.v, state, run) &&
+            (!t.p_copy || run_ok(t.p_copy, 2, run));
     return d;
 }
 
-template <int CAP>
+template <int CAP, bool kPacked>
 cudaError_t launch(const hc_adamw_tensor *t, int64_t count, const Scalars &c, cudaStream_t s) {
     static_assert(sizeof(Descs<CAP>) + sizeof(Scalars) + 16 <= 32764, "kernel parameters");
     Descs<CAP> ds;
@@ -291,7 +373,7 @@ cudaError_t launch(const hc_adamw_tensor *t, int64_t count, const Scalars &c, cu
         int k = 0;
         int64_t blocks = 0;
         for (; at < count && k < CAP; ++at) {
-            if (t[at].numel == 0) continue;
+            if (t[at].numel == 0 || (t[at].m_scales != nullptr) != kPacked) continue;
             const int64_t b = (t[at].numel + kChunk - 1) / kChunk;
             if (blocks + b > INT32_MAX) break;
             ds.d[k] = describe(t[at]);
@@ -299,11 +381,19 @@ cudaError_t launch(const hc_adamw_tensor *t, int64_t count, const Scalars &c, cu
             blocks += b;
         }
         if (k == 0) break;
-        k_adamw<CAP><<<(unsigned)blocks, kThreads, 0, s>>>(ds, k, c);
+        k_adamw<CAP, kPacked><<<(unsigned)blocks, kThreads, 0, s>>>(ds, k, c);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+template <bool kPacked>
+cudaError_t launch_kind(const hc_adamw_tensor *t, int64_t count, const Scalars &c, cudaStream_t s) {
+    // (fewer parameter bytes for fewer tensors: they are copied with every launch)
+    if (count <= 8) return launch<8, kPacked>(t, count, c, s);
+    if (count <= 64) return launch<64, kPacked>(t, count, c, s);
+    return launch<448, kPacked>(t, count, c, s);
 }
 
 }  // namespace aw
@@ -320,10 +410,13 @@ cudaError_t launch_adamw(const hc_adamw_tensor *tensors, int64_t count, double l
     c.log_beta1 = log(beta1), c.log_beta2 = log(beta2);
     c.lr = (float)lr, c.wd = (float)weight_decay, c.step = step;
     c.lr_dev = lr_dev, c.step_dev = step_dev, c.grad_scale = grad_scale;
-    // (fewer parameter bytes for fewer tensors: they are copied with every launch)
-    if (count <= 8) return aw::launch<8>(tensors, count, c, s);
-    if (count <= 64) return aw::launch<64>(tensors, count, c, s);
-    return aw::launch<448>(tensors, count, c, s);
+    int64_t packed = 0;
+    for (int64_t i = 0; i < count; ++i) packed += tensors[i].m_scales != nullptr;
+    if (packed < count) {
+        const cudaError_t e = aw::launch_kind<false>(tensors, count, c, s);
+        if (e != cudaSuccess) return e;
+    }
+    return packed ? aw::launch_kind<true>(tensors, count, c, s) : cudaSuccess;
 }
 
 }  // namespace hc

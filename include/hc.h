@@ -400,8 +400,11 @@ hc_status hc_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dtype g_t
  *   m <- m beta1 + g (1 - beta1),  v <- v beta2 + g g (1 - beta2)
  *   p <- p (1 - lr weight_decay)
  *        - m / (sqrt(v) / sqrt(1 - beta2^t) + eps) * lr / (1 - beta1^t)
- * in fp32, every operation rounded once in the order written (the coefficients
- * in 64 bits, then rounded once); p is rounded to nearest in its own type.
+ * in fp32 (the coefficients in 64 bits, then rounded once); p is rounded to
+ * nearest in its own type.  With fp32 states every operation is rounded once in
+ * the order written; with 8-bit states products and sums are fused and the root
+ * and the reciprocal are the hardware's approximations, each within 2^-23 of its
+ * value (and a v below 2^-126 counts as zero).
  *
  * A tensor's states are fp32 (m_scales and v_scales NULL), or 8 bits: m [numel]
  * E4M3 codes and v [numel] E4M3 codes of r = sqrt(v), with a UE8M0 scale byte per
