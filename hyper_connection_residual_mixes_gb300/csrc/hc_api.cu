@@ -92,11 +92,26 @@ struct Use {
     bool written;
 };
 
-// Whether a written range meets any other range: sorted by start, each range is
-// compared with the furthest end so far, of the written ones or (if it is
-// written itself) of all.
-bool any_overlap(Use *u, int64_t n) {
-    std::sort(u, u + n, [](const Use &a, const Use &b) { return a.lo < b.lo; });
+// Whether a written range meets any other range.  u holds `runs` runs of ranges
+// (run r ends before at[r]), each most often ascending already, as tensors made one
+// after the other are: only those that are not get sorted, then the runs are
+// merged pairwise (`spare` has room for all).  In order of their starts each
+// range is compared with the furthest end so far, of the written ones or (if it
+// is written itself) of all.
+bool any_overlap(Use *u, Use *spare, int64_t *at, int runs) {
+    const auto before = [](const Use &a, const Use &b) { return a.lo < b.lo; };
+    for (int r = 0; r < runs; ++r) {
+        Use *first = u + (r ? at[r - 1] : 0), *last = u + at[r];
+        if (!std::is_sorted(first, last, before)) std::sort(first, last, before);
+    }
+    for (; runs > 1; runs = (runs + 1) / 2, std::swap(u, spare)) {
+        for (int r = 0; r < runs; r += 2) {
+            Use *first = u + (r ? at[r - 1] : 0), *mid = u + at[r], *last = r + 1 < runs ? u + at[r + 1] : mid;
+            std::merge(first, mid, mid, last, spare + (first - u), before);
+        }
+        for (int r = 0; r < (runs + 1) / 2; ++r) at[r] = at[2 * r + 1 < runs ? 2 * r + 1 : 2 * r];
+    }
+    const int64_t n = at[0];
     uintptr_t written_end = 0, end = 0;
     for (int64_t i = 0; i < n; ++i) {
         if (u[i].lo < (u[i].written ? end : written_end)) return true;
@@ -574,30 +589,37 @@ hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr
         const hc_status st = check_adamw_tensor(tensors[i]);
         if (st != HC_OK) return st;
     }
-    Use few[64];
-    Use *const use = 7 * count + 3 <= 64 ? few : new (std::nothrow) Use[7 * count + 3];
+    const int64_t most = 7 * count + 3;
+    Use few[128];
+    Use *const use = 2 * most <= 128 ? few : new (std::nothrow) Use[2 * most];
     if (!use) return cuda_status(cudaErrorMemoryAllocation);
-    int64_t k = 0;
+    int64_t k = 0, at[8];
     const auto add = [&](const void *p, int64_t bytes, bool written) {
         if (!p || bytes <= 0) return;
         const Span r = span(p, bytes);
         use[k++] = Use{r.lo, r.hi, written};
     };
-    for (int64_t i = 0; i < count; ++i) {
-        const hc_adamw_tensor &t = tensors[i];
-        const int64_t state = t.m_scales ? 1 : 4, groups = (t.numel + 31) / 32;
-        add(t.p, t.numel * size_of((hc_dtype)t.p_type), true);
-        add(t.g, t.numel * size_of((hc_dtype)t.g_type), false);
-        add(t.m, t.numel * state, true);
-        add(t.v, t.numel * state, true);
-        add(t.m_scales, groups, true);
-        add(t.v_scales, groups, true);
-        add(t.p_copy, t.numel * 2, true);
-    }
+    const hc_adamw_tensor *const end = tensors + count;
+    const auto state = [](const hc_adamw_tensor &t) { return t.m_scales ? t.numel : t.numel * 4; };
+    for (auto t = tensors; t != end; ++t) add(t->p, t->numel * size_of((hc_dtype)t->p_type), true);
+    at[0] = k;
+    for (auto t = tensors; t != end; ++t) add(t->g, t->numel * size_of((hc_dtype)t->g_type), false);
+    at[1] = k;
+    for (auto t = tensors; t != end; ++t) add(t->m, state(*t), true);
+    at[2] = k;
+    for (auto t = tensors; t != end; ++t) add(t->v, state(*t), true);
+    at[3] = k;
+    for (auto t = tensors; t != end; ++t) add(t->m_scales, (t->numel + 31) / 32, true);
+    at[4] = k;
+    for (auto t = tensors; t != end; ++t) add(t->v_scales, (t->numel + 31) / 32, true);
+    at[5] = k;
+    for (auto t = tensors; t != end; ++t) add(t->p_copy, t->numel * 2, true);
+    at[6] = k;
     add(lr_dev, 4, false);
     add(step_dev, 8, false);
     add(grad_scale, 4, false);
-    const bool clash = any_overlap(use, k);
+    at[7] = k;
+    const bool clash = any_overlap(use, use + most, at, 8);
     if (use != few) delete[] use;
     if (clash) return HC_ERR_ALIAS;
     return cuda_status(hc::launch_adamw(tensors, count, lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev,

@@ -286,13 +286,14 @@ class AdamwPlan:
 
     def __init__(self, fields, device):
         self._fields = fields      # (tensor, index of the description, its member, numel, dtype)
+        self._tensors = [f[0] for f in fields]
         self.device = device
         self.count = 1 + max((f[1] for f in fields), default=-1)
         self._array = (_lib.AdamwTensor * self.count)()
         self._at = []
 
     def _describe(self):
-        at = [f[0].data_ptr() for f in self._fields]
+        at = list(map(torch.Tensor.data_ptr, self._tensors))
         if at == self._at:
             return
         for (t, i, member, numel, dtype), ptr in zip(self._fields, at):
