@@ -24,12 +24,10 @@
 // value for fp32 parameters, gradients and states, 10.1 for bf16 parameters
 // and gradients with 8-bit states.  All tensors of a call with one kind of states
 // go in one launch (their descriptions are kernel parameters, 448 at the most).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "hc_device.cuh"
 #include "hc_sublayer.h"
+#include "hc_types.cuh"
 
 namespace hc {
 
@@ -66,26 +64,9 @@ struct Scalars {
     const float *grad_scale;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v) {
-    if constexpr (sizeof(T) == 4) return v;
-    else if constexpr (__is_same(T, __half)) return __half2float(v);
-    else return __bfloat162float(v);
-}
-template <typename T>
-__device__ __forceinline__ T from_f(float v) {
-    if constexpr (sizeof(T) == 4) return v;
-    else if constexpr (__is_same(T, __half)) return __float2half_rn(v);
-    else return __float2bfloat16_rn(v);
-}
 // Values a thread holds side by side: 16 bytes of the widest of p and g.
 template <typename TP, typename TG>
 constexpr int run_of() { return sizeof(TP) == 2 && sizeof(TG) == 2 ? 8 : 4; }
-
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-    T v[V];
-};
 
 // values [i, i + V) of p, those below n (the others read as zero); kFull: all
 // are there and aligned, so that the loads of a chunk go out together
@@ -116,45 +97,6 @@ __device__ __forceinline__ void store(void *p, int64_t i, int64_t n, const Vec<T
 // ---- the 8-bit states
 __device__ __forceinline__ float scale_of(uint32_t byte) {  // 2^(byte - 127)
     return __uint_as_float(byte ? byte << 23 : 0x00400000u);
-}
-// A thread's 16-bit values and codes in words, two or four to a word.
-template <typename T, int V>
-union Words {
-    Vec<T, V> v;
-    uint32_t w[sizeof(T) * V / 4];
-};
-template <typename T, int V>
-__device__ __forceinline__ f32x2 pair(const Vec<T, V> &x, int k) {  // values k, k + 1 (k even)
-    if constexpr (sizeof(T) == 4) {
-        return f2_make(x.v[k], x.v[k + 1]);
-    } else {
-        Words<T, V> u;
-        u.v = x;
-        if constexpr (__is_same(T, __half)) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u.w[k / 2]));
-            return f2_make(f.x, f.y);
-        } else {
-            return f2_from_bf16x2(u.w[k / 2]);
-        }
-    }
-}
-template <typename T, int V>
-__device__ __forceinline__ void put_pair(Vec<T, V> &x, int k, f32x2 v) {
-    float a, b;
-    f2_split(v, a, b);
-    if constexpr (sizeof(T) == 4) {
-        x.v[k] = a, x.v[k + 1] = b;
-    } else {
-        Words<T, V> u;
-        u.v = x;
-        if constexpr (__is_same(T, __half)) {
-            const __half2 h = __floats2half2_rn(a, b);
-            u.w[k / 2] = *reinterpret_cast<const uint32_t *>(&h);
-        } else {
-            u.w[k / 2] = pack_bf16x2(a, b);
-        }
-        x = u.v;
-    }
 }
 template <int V>
 __device__ __forceinline__ f32x2 pair_of_codes(const Vec<uint8_t, V> &c, int k) {

@@ -174,7 +174,7 @@ int hc_last_cuda_error(void) { return g_last_cuda_error; }
 int hc_version(void) { return 100; }
 
 hc_status hc_consume_device_error(cudaStream_t stream) {
-    unsigned int flag = 0, flag_chain = 0, flag_bwd = 0, flag_proj = 0, flag_grouped = 0;
+    unsigned int flag = 0, flag_chain = 0, flag_bwd = 0, flag_proj = 0, flag_grouped = 0, flag_norm = 0;
     hc_status st = cuda_status(hc::consume_device_error(stream, &flag));
     if (st != HC_OK) return st;
     st = cuda_status(hc::consume_slices_device_error(stream, &flag_chain));
@@ -185,8 +185,10 @@ hc_status hc_consume_device_error(cudaStream_t stream) {
     if (st != HC_OK) return st;
     st = cuda_status(hc::consume_grouped_mm_device_error(stream, &flag_grouped));
     if (st != HC_OK) return st;
+    st = cuda_status(hc::consume_layer_norm_device_error(stream, &flag_norm));
+    if (st != HC_OK) return st;
     // (bit 0 of each: a wait ran out; bit 1 of the grouped products': bad offsets)
-    if (flag | flag_chain | flag_bwd | flag_proj | (flag_grouped & 1u)) return HC_ERR_TIMEOUT;
+    if (flag | flag_norm | flag_chain | flag_bwd | flag_proj | (flag_grouped & 1u)) return HC_ERR_TIMEOUT;
     return flag_grouped ? HC_ERR_INVALID_ARG : HC_OK;
 }
 

@@ -10,34 +10,16 @@
 //
 // Both directions move each row across HBM once and are bound by that.
 #include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
-#include "hc_device.cuh"
 #include "hc_ptx.cuh"
 #include "hc_sublayer.h"
+#include "hc_types.cuh"
 
 namespace hc {
 
 namespace ln {
 
-// ------------------------------------------------------------ element types
-template <typename T>
-__device__ __forceinline__ float to_f(T v) {
-    if constexpr (sizeof(T) == 4) return v;
-    else if constexpr (__is_same(T, __half)) return __half2float(v);
-    else return __bfloat162float(v);
-}
-template <typename T>
-__device__ __forceinline__ T from_f(float v) {  // round to nearest even
-    if constexpr (sizeof(T) == 4) return v;
-    else if constexpr (__is_same(T, __half)) return __float2half_rn(v);
-    else return __float2bfloat16_rn(v);
-}
-template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Vec {
-    T v[VEC];
-};
+constexpr int kSlots = 8;  // most ring slots
 
 // a parameter value (norm_w, norm_b): fp32 or 16 bits, by its type code
 __device__ __forceinline__ float param(const void *p, int type, int i) {
@@ -104,7 +86,7 @@ __device__ __forceinline__ float team_sum(float v, int tpr, float *red) {
 // tpr threads hold a row in registers: thread t the vectors t + i * tpr.  With
 // tpr == 32 each warp of the block has a row of its own, else the block has one.
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(VEC > 1 && NV >= 8 ? 128 : 1024, 1)
+__global__ void __launch_bounds__(1024, 1)
 k_layer_norm(const T *__restrict__ x, int64_t xs, const void *__restrict__ w, const void *__restrict__ b, int wt,
              int64_t n, int d, float eps, T *__restrict__ y, int64_t ys, float *__restrict__ mean_out,
              float *__restrict__ rstd_out, int tpr) {
@@ -155,6 +137,118 @@ k_layer_norm(const T *__restrict__ x, int64_t xs, const void *__restrict__ w, co
         if (mean_out) mean_out[row] = mean;
         if (rstd_out) rstd_out[row] = rstd;
     }
+}
+
+// ------------------------------------------------------------ rows through a ring
+// Long aligned rows, many of them: a block keeps its columns' weights in
+// registers and walks over rows, which bulk copies bring into a ring of
+// shared-memory slots ahead of it (one thread issues them; the block barrier
+// of a row's reduction says that a slot has been read).
+struct Ring {
+    uint64_t full[kSlots];
+    volatile int abort;
+};
+// All threads wait for slot `it % slots`; a wait that runs out is reported and
+// the block goes on (its rows are then wrong, but every barrier is met).
+__device__ __forceinline__ void ring_wait(Ring &r, int64_t it, int slots) {
+    mbar_wait<false>(smem_u32(&r.full[it % slots]), (uint32_t)(it / slots) & 1u, &r.abort);
+}
+__device__ __forceinline__ void ring_init(Ring &r, int slots) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < slots; ++i) mbar_init(smem_u32(&r.full[i]), 1);
+        r.abort = 0;
+        fence_mbar_init_cluster();
+    }
+    __syncthreads();
+}
+// After a wait that ran out: the copies still in flight must land before the block leaves.
+__device__ __forceinline__ void ring_leave(Ring &r, int64_t its, int slots) {
+    if (threadIdx.x == 0 && r.abort)
+        for (int64_t k = its > slots ? its - slots : 0; k < its; ++k)
+            for (uint32_t i = 0; i < (1u << 22); ++i) {
+                if (mbar_try_wait(smem_u32(&r.full[k % slots]), (uint32_t)(k / slots) & 1u)) break;
+                __nanosleep(128);
+            }
+}
+
+template <typename T, int NV, int kMaxThreads, int kMinBlocks>
+__global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
+k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ w, const void *__restrict__ b, int wt,
+                  int64_t n, int d, float eps, T *__restrict__ y, int64_t ys, float *__restrict__ mean_out,
+                  float *__restrict__ rstd_out, int slots) {
+    constexpr int V = 16 / sizeof(T);
+    extern __shared__ __align__(16) uint8_t s_rows[];
+    __shared__ Ring ring;
+    __shared__ float red[2][32];
+    const int t = threadIdx.x, tpr = blockDim.x;
+    const uint32_t row_bytes = (uint32_t)d * sizeof(T);
+    ring_init(ring, slots);
+    const int64_t rows = (n - 1 - blockIdx.x) / gridDim.x + 1;  // of this block (the grid has at most n)
+    const auto fetch = [&](int64_t it) {
+        const uint32_t bar = smem_u32(&ring.full[it % slots]);
+        mbar_arrive_expect_tx(bar, row_bytes);
+        bulk_load(smem_u32(s_rows) + (uint32_t)(it % slots) * row_bytes, x + (blockIdx.x + it * gridDim.x) * xs, row_bytes, bar);
+    };
+    if (t == 0)
+        for (int it = 0; it < slots && it < rows; ++it) fetch(it);
+    f32x2 wv[NV][V / 2], bv[NV][V / 2];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * tpr) * V;
+        float f[V] = {}, h[V] = {};
+        if (c < d) {
+            params<V>(w, wt, c, f);
+            if (b) params<V>(b, wt, c, h);
+        }
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) wv[i][k] = f2_make(f[2 * k], f[2 * k + 1]), bv[i][k] = f2_make(h[2 * k], h[2 * k + 1]);
+    }
+    for (int64_t it = 0; it < rows; ++it) {
+        const int64_t row = blockIdx.x + it * gridDim.x;
+        ring_wait(ring, it, slots);
+        const T *xr = reinterpret_cast<const T *>(s_rows + (uint32_t)(it % slots) * row_bytes);
+        Vec<T, V> v[NV];
+        f32x2 acc = f2_dup(0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * V;
+            if (c >= d) continue;
+            v[i] = *reinterpret_cast<const Vec<T, V> *>(xr + c);
+#pragma unroll
+            for (int k = 0; k < V; k += 2) acc = f2_add(acc, pair(v[i], k));
+        }
+        const float mean = team_sum(f2_hsum(acc), tpr, red[0]) / (float)d;
+        // (every thread has read the slot: it can be filled again)
+        if (t == 0 && it + slots < rows) fetch(it + slots);
+        const f32x2 neg = f2_dup(-mean);
+        acc = f2_dup(0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if ((t + i * tpr) * V >= d) continue;
+#pragma unroll
+            for (int k = 0; k < V; k += 2) {
+                const f32x2 c = f2_add(pair(v[i], k), neg);
+                acc = f2_fma(c, c, acc);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(team_sum(f2_hsum(acc), tpr, red[1]) / (float)d + eps);
+        T *yr = y + row * ys;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * V;
+            if (c >= d) continue;
+            Vec<T, V> o;
+#pragma unroll
+            for (int k = 0; k < V; k += 2)
+                put_pair(o, k, f2_fma(f2_mul(f2_add(pair(v[i], k), neg), f2_dup(rstd)), wv[i][k / 2], bv[i][k / 2]));
+            *reinterpret_cast<Vec<T, V> *>(yr + c) = o;
+        }
+        if (t == 0) {
+            if (mean_out) mean_out[row] = mean;
+            if (rstd_out) rstd_out[row] = rstd;
+        }
+    }
+    ring_leave(ring, rows, slots);
 }
 
 // ------------------------------------------------------------ backward
@@ -262,6 +356,109 @@ k_ln_backward(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, i
     for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) pw[c] = s_cols[c];
 }
 
+// The same with the rows of x and g through a ring.  Each thread owns 4 columns in
+// each of NV places; both passes over a row read it from its slot, which is
+// filled again once the next row's barrier has passed.
+template <typename TX, typename TG, int NV, int kMaxThreads, int kMinBlocks>
+__global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
+k_ln_backward_ring(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, int64_t xs,
+                   const void *__restrict__ w, int wt, const float *__restrict__ mean_in,
+                   const float *__restrict__ rstd_in, int64_t n, int d, TG *__restrict__ gx, int64_t gxs,
+                   float *__restrict__ part, int slots) {
+    constexpr int V = 4;
+    extern __shared__ __align__(16) uint8_t s_rows[];
+    __shared__ Ring ring;
+    __shared__ float2 red[2][32];
+    const int t = threadIdx.x, tpr = blockDim.x, warp = t >> 5, lane = t & 31, nw = tpr >> 5;
+    const uint32_t x_bytes = (uint32_t)d * sizeof(TX), g_bytes = (uint32_t)d * sizeof(TG), slot_bytes = x_bytes + g_bytes;
+    const float inv_d = 1.0f / (float)d;
+    ring_init(ring, slots);
+    const int64_t rows = (n - 1 - blockIdx.x) / gridDim.x + 1;
+    const auto fetch = [&](int64_t it) {
+        const uint32_t bar = smem_u32(&ring.full[it % slots]), at = smem_u32(s_rows) + (uint32_t)(it % slots) * slot_bytes;
+        const int64_t row = blockIdx.x + it * gridDim.x;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        bulk_load(at, x + row * xs, x_bytes, bar);
+        bulk_load(at + x_bytes, gy + row * gs, g_bytes, bar);
+    };
+    if (t == 0)
+        for (int it = 0; it < slots && it < rows; ++it) fetch(it);
+    f32x2 wv[NV][V / 2], aw[NV][V / 2], ab[NV][V / 2];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * tpr) * V;
+        float f[V] = {};
+        if (c < d) params<V>(w, wt, c, f);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) {
+            wv[i][k] = f2_make(f[2 * k], f[2 * k + 1]);
+            aw[i][k] = ab[i][k] = f2_dup(0.0f);
+        }
+    }
+    for (int64_t it = 0; it < rows; ++it) {
+        const int64_t row = blockIdx.x + it * gridDim.x;
+        const float mean = __ldg(mean_in + row), rstd = __ldg(rstd_in + row);
+        const f32x2 neg = f2_dup(-mean), rs = f2_dup(rstd);
+        ring_wait(ring, it, slots);
+        const uint8_t *slot = s_rows + (uint32_t)(it % slots) * slot_bytes;
+        const TX *xr = reinterpret_cast<const TX *>(slot);
+        const TG *gr = reinterpret_cast<const TG *>(slot + x_bytes);
+        f32x2 a1 = f2_dup(0.0f), a2 = f2_dup(0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * V;
+            if (c >= d) continue;
+            const Vec<TX, V> xv = *reinterpret_cast<const Vec<TX, V> *>(xr + c);
+            const Vec<TG, V> gv = *reinterpret_cast<const Vec<TG, V> *>(gr + c);
+#pragma unroll
+            for (int k = 0; k < V; k += 2) {
+                const f32x2 xh = f2_mul(f2_add(pair(xv, k), neg), rs), g = pair(gv, k);
+                const f32x2 wg = f2_mul(g, wv[i][k / 2]);
+                a1 = f2_add(a1, wg);
+                a2 = f2_fma(wg, xh, a2);
+                aw[i][k / 2] = f2_fma(g, xh, aw[i][k / 2]);
+                ab[i][k / 2] = f2_add(ab[i][k / 2], g);
+            }
+        }
+        float s1 = warp_sum(f2_hsum(a1)), s2 = warp_sum(f2_hsum(a2));
+        // (two buffers: a warp writes the next row's sums while a slow one still reads these)
+        if (lane == 0) red[it & 1][warp] = make_float2(s1, s2);
+        __syncthreads();
+        // every thread is done with the row before: its slot can be filled again
+        if (t == 0 && it > 0 && it - 1 + slots < rows) fetch(it - 1 + slots);
+        const float2 r = lane < nw ? red[it & 1][lane] : make_float2(0.0f, 0.0f);
+        s1 = warp_sum(r.x), s2 = warp_sum(r.y);
+        const f32x2 m1 = f2_dup(-s1 * inv_d), m2 = f2_dup(-s2 * inv_d);
+        TG *o_row = gx + row * gxs;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * V;
+            if (c >= d) continue;
+            const Vec<TX, V> xv = *reinterpret_cast<const Vec<TX, V> *>(xr + c);
+            const Vec<TG, V> gv = *reinterpret_cast<const Vec<TG, V> *>(gr + c);
+            Vec<TG, V> o;
+#pragma unroll
+            for (int k = 0; k < V; k += 2) {
+                const f32x2 xh = f2_mul(f2_add(pair(xv, k), neg), rs);
+                put_pair(o, k, f2_mul(rs, f2_fma(xh, m2, f2_fma(pair(gv, k), wv[i][k / 2], m1))));
+            }
+            *reinterpret_cast<Vec<TG, V> *>(o_row + c) = o;
+        }
+    }
+    ring_leave(ring, rows, slots);
+    float *pw = part + (int64_t)blockIdx.x * 2 * d, *pb = pw + d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * tpr) * V;
+        if (c >= d) continue;
+        Vec<float, V> o;
+        put_pair(o, 0, aw[i][0]), put_pair(o, 2, aw[i][1]);
+        *reinterpret_cast<Vec<float, V> *>(pw + c) = o;
+        put_pair(o, 0, ab[i][0]), put_pair(o, 2, ab[i][1]);
+        *reinterpret_cast<Vec<float, V> *>(pb + c) = o;
+    }
+}
+
 // g_w, g_b [d] from the blocks' partial rows [blocks][2][d]: 32 columns per
 // block, the rows shared among 16 warps.
 constexpr int kColWarps = 16;
@@ -313,21 +510,52 @@ cudaError_t fwd_launch(const FwdCall &c, int tpr, int threads) {
 template <typename T, int VEC>
 cudaError_t fwd_vec(const FwdCall &c) {
     const int vecs = (c.d + VEC - 1) / VEC;
-    // A warp per row needs no block barrier and keeps the most bytes in flight;
-    // it takes over once the rows fill the SMs with warps.
-    const bool many = c.n >= 8 * (int64_t)sm_count_of_device();
     if (vecs <= 32) return fwd_launch<T, VEC, 1>(c, 32, 128);
     if (vecs <= 64) return fwd_launch<T, VEC, 2>(c, 32, 128);
     if (vecs <= 128) return fwd_launch<T, VEC, 4>(c, 32, 128);
-    if constexpr (VEC > 1) if (many) {
-        if (vecs <= 256) return fwd_launch<T, VEC, 8>(c, 32, 128);
-        if (vecs <= 512) return fwd_launch<T, VEC, 16>(c, 32, 128);
-        if (vecs <= 640) return fwd_launch<T, VEC, 20>(c, 32, 128);
-    }
     const int tpr1 = (vecs + 31) / 32 * 32, tpr4 = (vecs + 127) / 128 * 32, tpr16 = (vecs + 511) / 512 * 32;
     if (vecs <= 1024) return fwd_launch<T, VEC, 1>(c, tpr1, tpr1);
     if (vecs <= 4096) return fwd_launch<T, VEC, 4>(c, tpr4, tpr4);
     return fwd_launch<T, 1, 16>(c, tpr16, tpr16);  // single values only: 4096 vectors hold the longest row
+}
+
+// Slots of a ring and blocks of a launch: as many slots as fit beside the SM's
+// other blocks, and a grid that fills the SMs once.
+template <typename K>
+cudaError_t ring_shape(K kernel, int threads, int slot_bytes, int64_t rows, int64_t most, int *slots, int *blocks) {
+    int dev = 0, sms = 0, smem_sm = 0, smem_block = 0, per_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&smem_block, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+    if (e != cudaSuccess) return e;
+    const int extra = 2048;  // a block's other shared memory
+    while (per_sm > 1 && (smem_sm / per_sm - extra) / slot_bytes < 3) --per_sm;
+    int room = smem_sm / per_sm - extra;
+    if (room > smem_block - extra) room = smem_block - extra;
+    *slots = room / slot_bytes < kSlots ? room / slot_bytes : kSlots;
+    int64_t grid = (int64_t)per_sm * sms;
+    if (grid > most) grid = most;
+    if (grid > rows) grid = rows;
+    *blocks = (int)grid;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, *slots * slot_bytes);
+}
+
+template <typename T>
+cudaError_t fwd_ring(const FwdCall &c) {
+    constexpr int V = 16 / sizeof(T), NV = 16 / V;  // 16 columns a thread
+    const int threads = (c.d + 511) / 512 * 32;
+    int slots = 0, blocks = 0;
+    const auto go = [&](auto kernel) {
+        cudaError_t e = ring_shape(kernel, threads, c.d * (int)sizeof(T), c.n, INT32_MAX, &slots, &blocks);
+        if (e != cudaSuccess) return e;
+        kernel<<<blocks, threads, slots * c.d * sizeof(T), c.s>>>(static_cast<const T *>(c.x), c.xs, c.w, c.b, c.wt, c.n,
+                                                                  c.d, c.eps, static_cast<T *>(c.y), c.ys, c.mean, c.rstd, slots);
+        return cudaGetLastError();
+    };
+    if (threads <= 320) return go(k_layer_norm_ring<T, NV, 320, 3>);
+    return go(k_layer_norm_ring<T, NV, 1024, 1>);
 }
 
 template <typename T>
@@ -335,8 +563,10 @@ cudaError_t fwd_type(const FwdCall &c) {
     constexpr int VEC = 16 / sizeof(T);
     const size_t pa = c.wt == HC_F32 ? 16 : 8;
     if (c.d % VEC == 0 && aligned(c.x, c.xs * (int64_t)sizeof(T), 16) && aligned(c.y, c.ys * (int64_t)sizeof(T), 16) &&
-        aligned(c.w, 0, pa) && aligned(c.b, 0, pa))
+        aligned(c.w, 0, pa) && aligned(c.b, 0, pa)) {
+        if (c.d >= 1024 && c.n >= 4 * (int64_t)sm_count_of_device()) return fwd_ring<T>(c);
         return fwd_vec<T, VEC>(c);
+    }
     return fwd_vec<T, 1>(c);
 }
 
@@ -368,12 +598,34 @@ cudaError_t bwd_launch(const BwdCall &c, int tpr) {
 }
 
 template <typename TX, typename TG>
+cudaError_t bwd_ring(const BwdCall &c) {
+    const int slot = c.d * (int)(sizeof(TX) + sizeof(TG));
+    int slots = 0, blocks = 0;
+    const auto go = [&](auto kernel, int threads) {
+        cudaError_t e = ring_shape(kernel, threads, slot, c.n, max_blocks(c.d), &slots, &blocks);
+        if (e != cudaSuccess) return e;
+        kernel<<<blocks, threads, slots * slot, c.s>>>(
+            static_cast<const TG *>(c.gy), c.gs, static_cast<const TX *>(c.x), c.xs, c.w, c.wt, c.mean, c.rstd, c.n, c.d,
+            static_cast<TG *>(c.gx), c.gxs, c.part, slots);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        k_ln_columns<<<(unsigned)((2 * c.d + 31) / 32), 32 * kColWarps, 0, c.s>>>(c.part, blocks, c.d, c.g_w, c.g_b);
+        return cudaGetLastError();
+    };
+    // 16 columns a thread leave room for two blocks an SM up to 352 threads; wider rows take 8
+    if (c.d <= 16 * 352) return go(k_ln_backward_ring<TX, TG, 4, 352, 2>, (c.d + 511) / 512 * 32);
+    return go(k_ln_backward_ring<TX, TG, 2, 1024, 1>, (c.d + 255) / 256 * 32);
+}
+
+template <typename TX, typename TG>
 cudaError_t bwd_type(const BwdCall &c) {
     const size_t pa = c.wt == HC_F32 ? 16 : 8;
     const int d = c.d;
     if (d % 4 == 0 && d > 128 && aligned(c.x, c.xs * (int64_t)sizeof(TX), 4 * sizeof(TX)) &&
         aligned(c.gy, c.gs * (int64_t)sizeof(TG), 4 * sizeof(TG)) &&
         aligned(c.gx, c.gxs * (int64_t)sizeof(TG), 4 * sizeof(TG)) && aligned(c.w, 0, pa)) {
+        const bool bulk = (int64_t)d * sizeof(TX) % 16 == 0 && (int64_t)d * sizeof(TG) % 16 == 0 &&
+                          aligned(c.x, c.xs * (int64_t)sizeof(TX), 16) && aligned(c.gy, c.gs * (int64_t)sizeof(TG), 16);
+        if (bulk && d >= 1024 && d <= 8192 && c.n >= 2 * (int64_t)sm_count_of_device()) return bwd_ring<TX, TG>(c);
         if (d <= 256) return bwd_launch<TX, TG, 4, 2>(c, 32);
         if (d <= 8192) return bwd_launch<TX, TG, 4, 2>(c, (d + 255) / 256 * 32);
         return bwd_launch<TX, TG, 4, 4>(c, (d + 511) / 512 * 32);
@@ -421,6 +673,20 @@ cudaError_t launch_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dty
     }
     if (x_type == HC_BF16) return ln::bwd_type<__nv_bfloat16, __nv_bfloat16>(c);
     return ln::bwd_type<__half, __half>(c);
+}
+
+cudaError_t consume_layer_norm_device_error(cudaStream_t s, unsigned int *flag) {
+    cudaError_t e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return e;
+    unsigned int v = 0;
+    e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof v);
+    if (e != cudaSuccess) return e;
+    *flag = v;
+    if (v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof zero);
+    }
+    return e;
 }
 
 }  // namespace hc

@@ -28,6 +28,9 @@ cudaError_t launch_adamw(const hc_adamw_tensor *tensors, int64_t count, double l
                          double eps, double weight_decay, int64_t step, const float *lr_dev, const int64_t *step_dev,
                          const float *grad_scale, cudaStream_t s);
 
+// as the other files' (hc_launch.h)
+cudaError_t consume_layer_norm_device_error(cudaStream_t s, unsigned int *flag);
+
 // ------------------------------------------------------------ experts' products (hc_grouped_mm.cu)
 // y [n, N] = x [n, K] w[e]^T, w [experts][N][K] (w_kn: [experts][K][N]).
 cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bool w_kn, const int32_t *offsets, int64_t n,
