@@ -148,10 +148,18 @@ struct Ring {
     uint64_t full[kSlots];
     volatile int abort;
 };
-// All threads wait for slot `it % slots`; a wait that runs out is reported and
-// the block goes on (its rows are then wrong, but every barrier is met).
-__device__ __forceinline__ void ring_wait(Ring &r, int64_t it, int slots) {
-    mbar_wait<false>(smem_u32(&r.full[it % slots]), (uint32_t)(it / slots) & 1u, &r.abort);
+// Where a row of the block stands in the ring.
+struct Place {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int slots) {
+        if (++slot == slots) slot = 0, parity ^= 1u;
+    }
+};
+// All threads wait for a row; a wait that runs out is reported and the block
+// goes on (its rows are then wrong, but every barrier is met).
+__device__ __forceinline__ void ring_wait(Ring &r, const Place &p) {
+    mbar_wait<false>(smem_u32(&r.full[p.slot]), p.parity, &r.abort);
 }
 __device__ __forceinline__ void ring_init(Ring &r, int slots) {
     if (threadIdx.x == 0) {
@@ -171,7 +179,17 @@ __device__ __forceinline__ void ring_leave(Ring &r, int64_t its, int slots) {
             }
 }
 
-template <typename T, int NV, int kMaxThreads, int kMinBlocks>
+// 1 / sqrt(a): the approximation and a Newton step, which leaves about a unit.
+__device__ __forceinline__ float rsqrt_newton(float a) {
+    const float r = rsqrtf(a);
+    return isinf(r) ? r : fmaf(r * 0.5f, fmaf(-a * r, r, 1.0f), r);
+}
+
+// kFull: the block's threads hold exactly d columns, 16 each.  Mean and sum of
+// squares are taken per warp first (about the warp's own mean), then joined over
+// the warps, so that a row costs one block barrier:
+//   mean = sum c_w m_w / d,  M2 = sum M2_w + c_w (m_w - mean)^2.
+template <typename T, int NV, bool kFull, int kMaxThreads, int kMinBlocks>
 __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
 k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ w, const void *__restrict__ b, int wt,
                   int64_t n, int d, float eps, T *__restrict__ y, int64_t ys, float *__restrict__ mean_out,
@@ -179,71 +197,95 @@ k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ 
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(16) uint8_t s_rows[];
     __shared__ Ring ring;
-    __shared__ float red[2][32];
-    const int t = threadIdx.x, tpr = blockDim.x;
+    __shared__ float2 red[2][32];
+    const int t = threadIdx.x, tpr = blockDim.x, warp = t >> 5, lane = t & 31, nw = tpr >> 5;
     const uint32_t row_bytes = (uint32_t)d * sizeof(T);
     ring_init(ring, slots);
     const int64_t rows = (n - 1 - blockIdx.x) / gridDim.x + 1;  // of this block (the grid has at most n)
-    const auto fetch = [&](int64_t it) {
-        const uint32_t bar = smem_u32(&ring.full[it % slots]);
+    const auto fetch = [&](int slot, int64_t it) {
+        const uint32_t bar = smem_u32(&ring.full[slot]);
         mbar_arrive_expect_tx(bar, row_bytes);
-        bulk_load(smem_u32(s_rows) + (uint32_t)(it % slots) * row_bytes, x + (blockIdx.x + it * gridDim.x) * xs, row_bytes, bar);
+        bulk_load(smem_u32(s_rows) + (uint32_t)slot * row_bytes, x + (blockIdx.x + it * gridDim.x) * xs, row_bytes, bar);
     };
     if (t == 0)
-        for (int it = 0; it < slots && it < rows; ++it) fetch(it);
+        for (int it = 0; it < slots && it < rows; ++it) fetch(it, it);
+    const float inv_d = 1.0f / (float)d;
     f32x2 wv[NV][V / 2], bv[NV][V / 2];
+    const auto columns_of = [&](int wp) {  // of a warp
+        int c = 0;
+        for (int i = 0; i < NV; ++i) {
+            const int left = d - (i * tpr + 32 * wp) * V;
+            c += left < 0 ? 0 : left > 32 * V ? 32 * V : left;
+        }
+        return c;
+    };
+    const float own = kFull ? (float)(32 * V * NV) : (float)columns_of(warp);
+    const float inv_own = own > 0.0f ? 1.0f / own : 0.0f;
+    // what lane w weighs warp w's mean with
+    const float weight = lane < nw ? (kFull ? (float)(32 * V * NV) : (float)columns_of(lane)) : 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * tpr) * V;
         float f[V] = {}, h[V] = {};
-        if (c < d) {
+        if (kFull || c < d) {
             params<V>(w, wt, c, f);
             if (b) params<V>(b, wt, c, h);
         }
 #pragma unroll
         for (int k = 0; k < V / 2; ++k) wv[i][k] = f2_make(f[2 * k], f[2 * k + 1]), bv[i][k] = f2_make(h[2 * k], h[2 * k + 1]);
     }
-    for (int64_t it = 0; it < rows; ++it) {
-        const int64_t row = blockIdx.x + it * gridDim.x;
-        ring_wait(ring, it, slots);
-        const T *xr = reinterpret_cast<const T *>(s_rows + (uint32_t)(it % slots) * row_bytes);
-        Vec<T, V> v[NV];
+    Place place;
+    const T *own_cols = reinterpret_cast<const T *>(s_rows) + t * V;
+    T *yr = y + blockIdx.x * ys + t * V;
+    for (int64_t it = 0; it < rows; ++it, yr += gridDim.x * ys) {
+        ring_wait(ring, place);
+        const T *xr = own_cols + place.slot * d;
+        f32x2 v[NV][V / 2];
         f32x2 acc = f2_dup(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (t + i * tpr) * V;
-            if (c >= d) continue;
-            v[i] = *reinterpret_cast<const Vec<T, V> *>(xr + c);
+            if (!kFull && (t + i * tpr) * V >= d) continue;
+            const Vec<T, V> u = *reinterpret_cast<const Vec<T, V> *>(xr + i * tpr * V);
 #pragma unroll
-            for (int k = 0; k < V; k += 2) acc = f2_add(acc, pair(v[i], k));
+            for (int k = 0; k < V / 2; ++k) {
+                v[i][k] = pair(u, 2 * k);
+                acc = f2_add(acc, v[i][k]);
+            }
         }
-        const float mean = team_sum(f2_hsum(acc), tpr, red[0]) / (float)d;
-        // (every thread has read the slot: it can be filled again)
-        if (t == 0 && it + slots < rows) fetch(it + slots);
-        const f32x2 neg = f2_dup(-mean);
+        const float m_w = warp_sum(f2_hsum(acc)) * inv_own;
+        const f32x2 neg = f2_dup(-m_w);
         acc = f2_dup(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if ((t + i * tpr) * V >= d) continue;
+            if (!kFull && (t + i * tpr) * V >= d) continue;
 #pragma unroll
-            for (int k = 0; k < V; k += 2) {
-                const f32x2 c = f2_add(pair(v[i], k), neg);
-                acc = f2_fma(c, c, acc);
+            for (int k = 0; k < V / 2; ++k) {
+                v[i][k] = f2_add(v[i][k], neg);
+                acc = f2_fma(v[i][k], v[i][k], acc);
             }
         }
-        const float rstd = 1.0f / sqrtf(team_sum(f2_hsum(acc), tpr, red[1]) / (float)d + eps);
-        T *yr = y + row * ys;
+        const float m2_w = warp_sum(f2_hsum(acc));
+        // (two buffers: a warp writes the next row's pair while a slow one still reads these)
+        if (lane == 0) red[it & 1][warp] = make_float2(m_w, m2_w);
+        __syncthreads();
+        // (every thread has read the slot: it can be filled again)
+        if (t == 0 && it + slots < rows) fetch(place.slot, it + slots);
+        place.next(slots);
+        const float2 r = lane < nw ? red[it & 1][lane] : make_float2(0.0f, 0.0f);
+        const float mean = warp_sum(weight * r.x) * inv_d;
+        const float off = r.x - mean;
+        const float rstd = rsqrt_newton(fmaf(warp_sum(fmaf(weight * off, off, r.y)), inv_d, eps));
+        const f32x2 rs = f2_dup(rstd), shift = f2_dup((m_w - mean) * rstd);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (t + i * tpr) * V;
-            if (c >= d) continue;
+            if (!kFull && (t + i * tpr) * V >= d) continue;
             Vec<T, V> o;
 #pragma unroll
-            for (int k = 0; k < V; k += 2)
-                put_pair(o, k, f2_fma(f2_mul(f2_add(pair(v[i], k), neg), f2_dup(rstd)), wv[i][k / 2], bv[i][k / 2]));
-            *reinterpret_cast<Vec<T, V> *>(yr + c) = o;
+            for (int k = 0; k < V / 2; ++k) put_pair(o, 2 * k, f2_fma(f2_fma(v[i][k], rs, shift), wv[i][k], bv[i][k]));
+            *reinterpret_cast<Vec<T, V> *>(yr + i * tpr * V) = o;
         }
         if (t == 0) {
+            const int64_t row = blockIdx.x + it * gridDim.x;
             if (mean_out) mean_out[row] = mean;
             if (rstd_out) rstd_out[row] = rstd;
         }
@@ -359,7 +401,7 @@ k_ln_backward(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, i
 // The same with the rows of x and g through a ring.  Each thread owns 4 columns in
 // each of NV places; both passes over a row read it from its slot, which is
 // filled again once the next row's barrier has passed.
-template <typename TX, typename TG, int NV, int kMaxThreads, int kMinBlocks>
+template <typename TX, typename TG, int NV, bool kFull, int kMaxThreads, int kMinBlocks>
 __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
 k_ln_backward_ring(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, int64_t xs,
                    const void *__restrict__ w, int wt, const float *__restrict__ mean_in,
@@ -374,40 +416,43 @@ k_ln_backward_ring(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__
     const float inv_d = 1.0f / (float)d;
     ring_init(ring, slots);
     const int64_t rows = (n - 1 - blockIdx.x) / gridDim.x + 1;
-    const auto fetch = [&](int64_t it) {
-        const uint32_t bar = smem_u32(&ring.full[it % slots]), at = smem_u32(s_rows) + (uint32_t)(it % slots) * slot_bytes;
+    const auto fetch = [&](int slot, int64_t it) {
+        const uint32_t bar = smem_u32(&ring.full[slot]), at = smem_u32(s_rows) + (uint32_t)slot * slot_bytes;
         const int64_t row = blockIdx.x + it * gridDim.x;
         mbar_arrive_expect_tx(bar, slot_bytes);
         bulk_load(at, x + row * xs, x_bytes, bar);
         bulk_load(at + x_bytes, gy + row * gs, g_bytes, bar);
     };
     if (t == 0)
-        for (int it = 0; it < slots && it < rows; ++it) fetch(it);
+        for (int it = 0; it < slots && it < rows; ++it) fetch(it, it);
+    Place place;
     f32x2 wv[NV][V / 2], aw[NV][V / 2], ab[NV][V / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * tpr) * V;
         float f[V] = {};
-        if (c < d) params<V>(w, wt, c, f);
+        if (kFull || c < d) params<V>(w, wt, c, f);
 #pragma unroll
         for (int k = 0; k < V / 2; ++k) {
             wv[i][k] = f2_make(f[2 * k], f[2 * k + 1]);
             aw[i][k] = ab[i][k] = f2_dup(0.0f);
         }
     }
+    float mean_next = __ldg(mean_in + blockIdx.x), rstd_next = __ldg(rstd_in + blockIdx.x);
     for (int64_t it = 0; it < rows; ++it) {
         const int64_t row = blockIdx.x + it * gridDim.x;
-        const float mean = __ldg(mean_in + row), rstd = __ldg(rstd_in + row);
+        const float mean = mean_next, rstd = rstd_next;
+        if (it + 1 < rows) mean_next = __ldg(mean_in + row + gridDim.x), rstd_next = __ldg(rstd_in + row + gridDim.x);
         const f32x2 neg = f2_dup(-mean), rs = f2_dup(rstd);
-        ring_wait(ring, it, slots);
-        const uint8_t *slot = s_rows + (uint32_t)(it % slots) * slot_bytes;
+        ring_wait(ring, place);
+        const uint8_t *slot = s_rows + (uint32_t)place.slot * slot_bytes;
         const TX *xr = reinterpret_cast<const TX *>(slot);
         const TG *gr = reinterpret_cast<const TG *>(slot + x_bytes);
         f32x2 a1 = f2_dup(0.0f), a2 = f2_dup(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t + i * tpr) * V;
-            if (c >= d) continue;
+            if (!kFull && c >= d) continue;
             const Vec<TX, V> xv = *reinterpret_cast<const Vec<TX, V> *>(xr + c);
             const Vec<TG, V> gv = *reinterpret_cast<const Vec<TG, V> *>(gr + c);
 #pragma unroll
@@ -425,7 +470,8 @@ k_ln_backward_ring(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__
         if (lane == 0) red[it & 1][warp] = make_float2(s1, s2);
         __syncthreads();
         // every thread is done with the row before: its slot can be filled again
-        if (t == 0 && it > 0 && it - 1 + slots < rows) fetch(it - 1 + slots);
+        if (t == 0 && it > 0 && it - 1 + slots < rows) fetch(place.slot ? place.slot - 1 : slots - 1, it - 1 + slots);
+        place.next(slots);
         const float2 r = lane < nw ? red[it & 1][lane] : make_float2(0.0f, 0.0f);
         s1 = warp_sum(r.x), s2 = warp_sum(r.y);
         const f32x2 m1 = f2_dup(-s1 * inv_d), m2 = f2_dup(-s2 * inv_d);
@@ -433,7 +479,7 @@ k_ln_backward_ring(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t + i * tpr) * V;
-            if (c >= d) continue;
+            if (!kFull && c >= d) continue;
             const Vec<TX, V> xv = *reinterpret_cast<const Vec<TX, V> *>(xr + c);
             const Vec<TG, V> gv = *reinterpret_cast<const Vec<TG, V> *>(gr + c);
             Vec<TG, V> o;
@@ -554,8 +600,9 @@ cudaError_t fwd_ring(const FwdCall &c) {
                                                                   c.d, c.eps, static_cast<T *>(c.y), c.ys, c.mean, c.rstd, slots);
         return cudaGetLastError();
     };
-    if (threads <= 320) return go(k_layer_norm_ring<T, NV, 320, 3>);
-    return go(k_layer_norm_ring<T, NV, 1024, 1>);
+    if (threads <= 320)
+        return c.d == threads * 16 ? go(k_layer_norm_ring<T, NV, true, 320, 3>) : go(k_layer_norm_ring<T, NV, false, 320, 3>);
+    return go(k_layer_norm_ring<T, NV, false, 1024, 1>);
 }
 
 template <typename T>
@@ -612,8 +659,10 @@ cudaError_t bwd_ring(const BwdCall &c) {
         return cudaGetLastError();
     };
     // 16 columns a thread leave room for two blocks an SM up to 352 threads; wider rows take 8
-    if (c.d <= 16 * 352) return go(k_ln_backward_ring<TX, TG, 4, 352, 2>, (c.d + 511) / 512 * 32);
-    return go(k_ln_backward_ring<TX, TG, 2, 1024, 1>, (c.d + 255) / 256 * 32);
+    const int t16 = (c.d + 511) / 512 * 32;
+    if (c.d == 16 * t16 && t16 <= 352) return go(k_ln_backward_ring<TX, TG, 4, true, 352, 2>, t16);
+    if (t16 <= 352) return go(k_ln_backward_ring<TX, TG, 4, false, 352, 2>, t16);
+    return go(k_ln_backward_ring<TX, TG, 2, false, 1024, 1>, (c.d + 255) / 256 * 32);
 }
 
 template <typename TX, typename TG>
