@@ -86,6 +86,8 @@ class HcError(RuntimeError):
 def load():
     """Load libhc.so once; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -9,6 +9,8 @@
 // All sums run in fp32; y (and g_x) are rounded once, on the way out.
 //
 // Both directions move each row across HBM once and are bound by that.
+#include <atomic>
+
 #include <cuda.h>
 
 #include "hc_ptx.cuh"
@@ -169,6 +171,10 @@ __device__ __forceinline__ void ring_init(Ring &r, int slots) {
     }
     __syncthreads();
 }
+// A kernel launched to follow this one may start its blocks now (it waits for
+// this grid's end, and so for its writes, before it reads anything).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_grid_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // After a wait that ran out: the copies still in flight must land before the block leaves.
 __device__ __forceinline__ void ring_leave(Ring &r, int64_t its, int slots) {
     if (threadIdx.x == 0 && r.abort)
@@ -185,11 +191,12 @@ __device__ __forceinline__ float rsqrt_newton(float a) {
     return isinf(r) ? r : fmaf(r * 0.5f, fmaf(-a * r, r, 1.0f), r);
 }
 
-// kFull: the block's threads hold exactly d columns, 16 each.  Mean and sum of
-// squares are taken per warp first (about the warp's own mean), then joined over
-// the warps, so that a row costs one block barrier:
+// kFull: the block's threads hold exactly d columns, 16 each.  R rows go through
+// a pass together, so that their reductions overlap and share the barrier.  Mean
+// and sum of squares are taken per warp first (about the warp's own mean), then
+// joined over the warps, so that a pass costs one block barrier:
 //   mean = sum c_w m_w / d,  M2 = sum M2_w + c_w (m_w - mean)^2.
-template <typename T, int NV, bool kFull, int kMaxThreads, int kMinBlocks>
+template <typename T, int NV, int R, bool kFull, int kMaxThreads, int kMinBlocks>
 __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
 k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ w, const void *__restrict__ b, int wt,
                   int64_t n, int d, float eps, T *__restrict__ y, int64_t ys, float *__restrict__ mean_out,
@@ -197,7 +204,7 @@ k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ 
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(16) uint8_t s_rows[];
     __shared__ Ring ring;
-    __shared__ float2 red[2][32];
+    __shared__ float2 red[2][R][32];
     const int t = threadIdx.x, tpr = blockDim.x, warp = t >> 5, lane = t & 31, nw = tpr >> 5;
     const uint32_t row_bytes = (uint32_t)d * sizeof(T);
     ring_init(ring, slots);
@@ -237,57 +244,87 @@ k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ 
     Place place;
     const T *own_cols = reinterpret_cast<const T *>(s_rows) + t * V;
     T *yr = y + blockIdx.x * ys + t * V;
-    for (int64_t it = 0; it < rows; ++it, yr += gridDim.x * ys) {
-        ring_wait(ring, place);
-        const T *xr = own_cols + place.slot * d;
-        f32x2 v[NV][V / 2];
-        f32x2 acc = f2_dup(0.0f);
+    int buf = 0;
+    for (int64_t it = 0; it < rows; it += R, buf ^= 1) {
+        f32x2 v[R][NV][V / 2];
+        float m_w[R], m2_w[R];
+        const Place first = place;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!kFull && (t + i * tpr) * V >= d) continue;
-            const Vec<T, V> u = *reinterpret_cast<const Vec<T, V> *>(xr + i * tpr * V);
+        for (int r = 0; r < R; ++r) {
+            m_w[r] = m2_w[r] = 0.0f;
+            if (it + r >= rows) break;  // the block's last pass
+            ring_wait(ring, place);
+            const T *xr = own_cols + place.slot * d;
+            place.next(slots);
+            f32x2 acc = f2_dup(0.0f);
 #pragma unroll
-            for (int k = 0; k < V / 2; ++k) {
-                v[i][k] = pair(u, 2 * k);
-                acc = f2_add(acc, v[i][k]);
+            for (int i = 0; i < NV; ++i) {
+                if (!kFull && (t + i * tpr) * V >= d) continue;
+                const Vec<T, V> u = *reinterpret_cast<const Vec<T, V> *>(xr + i * tpr * V);
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) {
+                    v[r][i][k] = pair(u, 2 * k);
+                    acc = f2_add(acc, v[r][i][k]);
+                }
             }
+            m_w[r] = f2_hsum(acc);
         }
-        const float m_w = warp_sum(f2_hsum(acc)) * inv_own;
-        const f32x2 neg = f2_dup(-m_w);
-        acc = f2_dup(0.0f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!kFull && (t + i * tpr) * V >= d) continue;
+        for (int r = 0; r < R; ++r) m_w[r] = warp_sum(m_w[r]) * inv_own;
 #pragma unroll
-            for (int k = 0; k < V / 2; ++k) {
-                v[i][k] = f2_add(v[i][k], neg);
-                acc = f2_fma(v[i][k], v[i][k], acc);
+        for (int r = 0; r < R; ++r) {
+            const f32x2 neg = f2_dup(-m_w[r]);
+            f32x2 acc = f2_dup(0.0f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!kFull && (t + i * tpr) * V >= d) continue;
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) {
+                    v[r][i][k] = f2_add(v[r][i][k], neg);
+                    acc = f2_fma(v[r][i][k], v[r][i][k], acc);
+                }
             }
+            m2_w[r] = f2_hsum(acc);
         }
-        const float m2_w = warp_sum(f2_hsum(acc));
-        // (two buffers: a warp writes the next row's pair while a slow one still reads these)
-        if (lane == 0) red[it & 1][warp] = make_float2(m_w, m2_w);
+#pragma unroll
+        for (int r = 0; r < R; ++r) m2_w[r] = warp_sum(m2_w[r]);
+        // (two buffers: a warp writes the next pass's while a slow one still reads these)
+        if (lane == 0)
+#pragma unroll
+            for (int r = 0; r < R; ++r) red[buf][r][warp] = make_float2(m_w[r], m2_w[r]);
         __syncthreads();
-        // (every thread has read the slot: it can be filled again)
-        if (t == 0 && it + slots < rows) fetch(place.slot, it + slots);
-        place.next(slots);
-        const float2 r = lane < nw ? red[it & 1][lane] : make_float2(0.0f, 0.0f);
-        const float mean = warp_sum(weight * r.x) * inv_d;
-        const float off = r.x - mean;
-        const float rstd = rsqrt_newton(fmaf(warp_sum(fmaf(weight * off, off, r.y)), inv_d, eps));
-        const f32x2 rs = f2_dup(rstd), shift = f2_dup((m_w - mean) * rstd);
+        if (t == 0) {  // every thread has read the slots: they can be filled again
+            Place p = first;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!kFull && (t + i * tpr) * V >= d) continue;
-            Vec<T, V> o;
-#pragma unroll
-            for (int k = 0; k < V / 2; ++k) put_pair(o, 2 * k, f2_fma(f2_fma(v[i][k], rs, shift), wv[i][k], bv[i][k]));
-            *reinterpret_cast<Vec<T, V> *>(yr + i * tpr * V) = o;
+            for (int r = 0; r < R; ++r, p.next(slots))
+                if (it + r + slots < rows) fetch(p.slot, it + r + slots);
         }
-        if (t == 0) {
-            const int64_t row = blockIdx.x + it * gridDim.x;
-            if (mean_out) mean_out[row] = mean;
-            if (rstd_out) rstd_out[row] = rstd;
+        float mean[R], rstd[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float2 q = lane < nw ? red[buf][r][lane] : make_float2(0.0f, 0.0f);
+            mean[r] = warp_sum(weight * q.x) * inv_d;
+            const float off = q.x - mean[r];
+            rstd[r] = rsqrt_newton(fmaf(warp_sum(fmaf(weight * off, off, q.y)), inv_d, eps));
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (it + r >= rows) break;
+            const f32x2 rs = f2_dup(rstd[r]), shift = f2_dup((m_w[r] - mean[r]) * rstd[r]);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!kFull && (t + i * tpr) * V >= d) continue;
+                Vec<T, V> o;
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) put_pair(o, 2 * k, f2_fma(f2_fma(v[r][i][k], rs, shift), wv[i][k], bv[i][k]));
+                *reinterpret_cast<Vec<T, V> *>(yr + i * tpr * V) = o;
+            }
+            yr += gridDim.x * ys;
+            if (t == 0) {
+                const int64_t row = blockIdx.x + (it + r) * gridDim.x;
+                if (mean_out) mean_out[row] = mean[r];
+                if (rstd_out) rstd_out[row] = rstd[r];
+            }
         }
     }
     ring_leave(ring, rows, slots);
@@ -297,8 +334,8 @@ k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ 
 // Each thread owns the same columns of every row its block takes, with their
 // sums of g xh and g in registers; a block leaves one row of partial sums in
 // the workspace, k_ln_columns adds the blocks' rows in a fixed order.
-template <typename TX, typename TG, int VEC, int NV>
-__global__ void __launch_bounds__(1024, 1)
+template <typename TX, typename TG, int VEC, int NV, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, 1)
 k_ln_backward(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, int64_t xs,
               const void *__restrict__ w, int wt, const float *__restrict__ mean_in,
               const float *__restrict__ rstd_in, int64_t n, int d, TG *__restrict__ gx, int64_t gxs,
@@ -316,21 +353,33 @@ k_ln_backward(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, i
         for (int k = 0; k < VEC; ++k) wv[i][k] = aw[i][k] = ab[i][k] = 0.0f;
         if (c < d) params<VEC>(w, wt, c, wv[i]);
     }
-    int buf = 0;
-    for (int64_t row = (int64_t)blockIdx.x * teams + team; row < n; row += (int64_t)gridDim.x * teams, buf ^= 1) {
+    // the next row's values are on their way while this one is worked on
+    Vec<TX, VEC> xn[NV];
+    Vec<TG, VEC> gn[NV];
+    float mean_next = 0.0f, rstd_next = 0.0f;
+    const int64_t first = (int64_t)blockIdx.x * teams + team, step = (int64_t)gridDim.x * teams;
+    const auto fetch = [&](int64_t row) {
         const TX *xr = x + row * xs;
         const TG *gr = gy + row * gs;
-        Vec<TX, VEC> xv[NV];
-        Vec<TG, VEC> gv[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t + i * tpr) * VEC;
             if (c < d) {
-                xv[i] = load_stream<TX, VEC>(xr + c);
-                gv[i] = load_stream<TG, VEC>(gr + c);
+                xn[i] = load_stream<TX, VEC>(xr + c);
+                gn[i] = load_stream<TG, VEC>(gr + c);
             }
         }
-        const float mean = __ldg(mean_in + row), rstd = __ldg(rstd_in + row);
+        mean_next = __ldg(mean_in + row), rstd_next = __ldg(rstd_in + row);
+    };
+    if (first < n) fetch(first);
+    int buf = 0;
+    for (int64_t row = first; row < n; row += step, buf ^= 1) {
+        Vec<TX, VEC> xv[NV];
+        Vec<TG, VEC> gv[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) xv[i] = xn[i], gv[i] = gn[i];
+        const float mean = mean_next, rstd = rstd_next;
+        if (row + step < n) fetch(row + step);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -492,6 +541,7 @@ k_ln_backward_ring(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__
         }
     }
     ring_leave(ring, rows, slots);
+    launch_dependents();
     float *pw = part + (int64_t)blockIdx.x * 2 * d, *pb = pw + d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -513,9 +563,12 @@ k_ln_columns(const float *__restrict__ part, int blocks, int d, float *__restric
     __shared__ float s[kColWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
+    wait_for_grid_before();
     float a = 0.0f;
-    if (c < 2 * d)
+    if (c < 2 * d) {
+#pragma unroll 10
         for (int r = warp; r < blocks; r += kColWarps) a += __ldcg(part + (int64_t)r * 2 * d + c);
+    }
     s[warp][lane] = a;
     __syncthreads();
     if (warp == 0 && c < 2 * d) {
@@ -525,12 +578,41 @@ k_ln_columns(const float *__restrict__ part, int blocks, int d, float *__restric
     }
 }
 
+constexpr int kDevices = 64;
+constexpr int kSmemBlock = 227 * 1024, kSmemSm = 228 * 1024;  // shared memory of a block, of an SM
+
+int current_device() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices ? dev : 0;
+}
 int sm_count_of_device() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 152;
-    return sms;
+    static int sms[kDevices] = {0};
+    const int dev = current_device();
+    if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    return sms[dev];
+}
+// Blocks of a kernel that an SM holds by its threads and registers (handed out to
+// warps in units of 256), and the most dynamic shared memory allowed to it; asked
+// for and set once per kernel and device.
+template <auto kKernel>
+cudaError_t blocks_per_sm(int threads, int *per_sm) {
+    static std::atomic<int> regs[kDevices];
+    const int dev = current_device();
+    int r = regs[dev].load(std::memory_order_relaxed);
+    if (!r) {
+        cudaFuncAttributes fa{};
+        cudaError_t e = cudaFuncGetAttributes(&fa, kKernel);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kSmemBlock - (int)fa.sharedSizeBytes);
+        if (e != cudaSuccess) return e;
+        r = fa.numRegs;
+        regs[dev].store(r, std::memory_order_relaxed);
+    }
+    const int warps = threads / 32, by_regs = 65536 / ((r * 32 + 255) / 256 * 256 * warps), by_threads = 64 / warps;
+    *per_sm = by_regs < by_threads ? by_regs : by_threads;
+    if (*per_sm < 1) *per_sm = 1;
+    return cudaSuccess;
 }
 
 bool aligned(const void *p, int64_t stride_bytes, size_t to) {
@@ -567,42 +649,39 @@ cudaError_t fwd_vec(const FwdCall &c) {
 
 // Slots of a ring and blocks of a launch: as many slots as fit beside the SM's
 // other blocks, and a grid that fills the SMs once.
-template <typename K>
-cudaError_t ring_shape(K kernel, int threads, int slot_bytes, int64_t rows, int64_t most, int *slots, int *blocks) {
-    int dev = 0, sms = 0, smem_sm = 0, smem_block = 0, per_sm = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&smem_block, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+template <auto kKernel>
+cudaError_t ring_shape(int threads, int slot_bytes, int64_t rows, int64_t most, int *slots, int *blocks) {
+    int per_sm = 0;
+    const cudaError_t e = blocks_per_sm<kKernel>(threads, &per_sm);
     if (e != cudaSuccess) return e;
     const int extra = 2048;  // a block's other shared memory
-    while (per_sm > 1 && (smem_sm / per_sm - extra) / slot_bytes < 3) --per_sm;
-    int room = smem_sm / per_sm - extra;
-    if (room > smem_block - extra) room = smem_block - extra;
+    while (per_sm > 1 && (kSmemSm / per_sm - extra) / slot_bytes < 3) --per_sm;
+    const int room = (per_sm > 1 ? kSmemSm / per_sm : kSmemBlock) - extra;
     *slots = room / slot_bytes < kSlots ? room / slot_bytes : kSlots;
-    int64_t grid = (int64_t)per_sm * sms;
+    int64_t grid = (int64_t)per_sm * sm_count_of_device();
     if (grid > most) grid = most;
     if (grid > rows) grid = rows;
     *blocks = (int)grid;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, *slots * slot_bytes);
+    return cudaSuccess;
 }
 
+template <auto kKernel, typename T>
+cudaError_t fwd_ring_launch(const FwdCall &c, int threads) {
+    int slots = 0, blocks = 0;
+    const cudaError_t e = ring_shape<kKernel>(threads, c.d * (int)sizeof(T), c.n, INT32_MAX, &slots, &blocks);
+    if (e != cudaSuccess) return e;
+    kKernel<<<blocks, threads, slots * c.d * sizeof(T), c.s>>>(static_cast<const T *>(c.x), c.xs, c.w, c.b, c.wt, c.n, c.d,
+                                                               c.eps, static_cast<T *>(c.y), c.ys, c.mean, c.rstd, slots);
+    return cudaGetLastError();
+}
 template <typename T>
 cudaError_t fwd_ring(const FwdCall &c) {
     constexpr int V = 16 / sizeof(T), NV = 16 / V;  // 16 columns a thread
     const int threads = (c.d + 511) / 512 * 32;
-    int slots = 0, blocks = 0;
-    const auto go = [&](auto kernel) {
-        cudaError_t e = ring_shape(kernel, threads, c.d * (int)sizeof(T), c.n, INT32_MAX, &slots, &blocks);
-        if (e != cudaSuccess) return e;
-        kernel<<<blocks, threads, slots * c.d * sizeof(T), c.s>>>(static_cast<const T *>(c.x), c.xs, c.w, c.b, c.wt, c.n,
-                                                                  c.d, c.eps, static_cast<T *>(c.y), c.ys, c.mean, c.rstd, slots);
-        return cudaGetLastError();
-    };
     if (threads <= 320)
-        return c.d == threads * 16 ? go(k_layer_norm_ring<T, NV, true, 320, 3>) : go(k_layer_norm_ring<T, NV, false, 320, 3>);
-    return go(k_layer_norm_ring<T, NV, false, 1024, 1>);
+        return c.d == threads * 16 ? fwd_ring_launch<k_layer_norm_ring<T, NV, 2, true, 320, 2>, T>(c, threads)
+                                   : fwd_ring_launch<k_layer_norm_ring<T, NV, 2, false, 320, 2>, T>(c, threads);
+    return fwd_ring_launch<k_layer_norm_ring<T, NV, 1, false, 1024, 1>, T>(c, threads);
 }
 
 template <typename T>
@@ -625,44 +704,56 @@ struct BwdCall {
 // blocks of partial sums a launch may use
 int64_t max_blocks(int d) { return d < 1024 ? 1216 : d <= 2048 ? 608 : 304; }
 
-template <typename TX, typename TG, int VEC, int NV>
+// The second launch starts while the first one's last blocks run (its blocks are
+// small, and wait for the first grid's end themselves).
+cudaError_t launch_columns(const BwdCall &c, int blocks) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((2 * c.d + 31) / 32)), cfg.blockDim = dim3(32 * kColWarps);
+    cfg.stream = c.s, cfg.attrs = &early, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_ln_columns, (const float *)c.part, blocks, c.d, c.g_w, c.g_b);
+}
+
+template <typename TX, typename TG, int VEC, int NV, int kMaxThreads>
 cudaError_t bwd_launch(const BwdCall &c, int tpr) {
+    constexpr auto kKernel = k_ln_backward<TX, TG, VEC, NV, kMaxThreads>;
     const int threads = tpr == 32 ? 256 : tpr;
     const int teams = tpr == 32 ? threads / 32 : 1;
     const size_t smem = teams > 1 ? (size_t)c.d * 8 : 0;
     int per_sm = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_ln_backward<TX, TG, VEC, NV>, threads, smem);
+    cudaError_t e = blocks_per_sm<kKernel>(threads, &per_sm);
     if (e != cudaSuccess) return e;
-    int64_t blocks = (int64_t)(per_sm > 0 ? per_sm : 1) * sm_count_of_device();
+    int64_t blocks = (int64_t)per_sm * sm_count_of_device();
     if (blocks > max_blocks(c.d)) blocks = max_blocks(c.d);
     if (blocks > (c.n + teams - 1) / teams) blocks = (c.n + teams - 1) / teams;
-    k_ln_backward<TX, TG, VEC, NV><<<(unsigned)blocks, threads, smem, c.s>>>(
+    kKernel<<<(unsigned)blocks, threads, smem, c.s>>>(
         static_cast<const TG *>(c.gy), c.gs, static_cast<const TX *>(c.x), c.xs, c.w, c.wt, c.mean, c.rstd, c.n, c.d,
         static_cast<TG *>(c.gx), c.gxs, c.part, tpr);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    k_ln_columns<<<(unsigned)((2 * c.d + 31) / 32), 32 * kColWarps, 0, c.s>>>(c.part, (int)blocks, c.d, c.g_w, c.g_b);
-    return cudaGetLastError();
+    return launch_columns(c, (int)blocks);
 }
 
-template <typename TX, typename TG>
-cudaError_t bwd_ring(const BwdCall &c) {
+template <auto kKernel, typename TX, typename TG>
+cudaError_t bwd_ring_launch(const BwdCall &c, int threads) {
     const int slot = c.d * (int)(sizeof(TX) + sizeof(TG));
     int slots = 0, blocks = 0;
-    const auto go = [&](auto kernel, int threads) {
-        cudaError_t e = ring_shape(kernel, threads, slot, c.n, max_blocks(c.d), &slots, &blocks);
-        if (e != cudaSuccess) return e;
-        kernel<<<blocks, threads, slots * slot, c.s>>>(
-            static_cast<const TG *>(c.gy), c.gs, static_cast<const TX *>(c.x), c.xs, c.w, c.wt, c.mean, c.rstd, c.n, c.d,
-            static_cast<TG *>(c.gx), c.gxs, c.part, slots);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        k_ln_columns<<<(unsigned)((2 * c.d + 31) / 32), 32 * kColWarps, 0, c.s>>>(c.part, blocks, c.d, c.g_w, c.g_b);
-        return cudaGetLastError();
-    };
+    cudaError_t e = ring_shape<kKernel>(threads, slot, c.n, max_blocks(c.d), &slots, &blocks);
+    if (e != cudaSuccess) return e;
+    kKernel<<<blocks, threads, slots * slot, c.s>>>(
+        static_cast<const TG *>(c.gy), c.gs, static_cast<const TX *>(c.x), c.xs, c.w, c.wt, c.mean, c.rstd, c.n, c.d,
+        static_cast<TG *>(c.gx), c.gxs, c.part, slots);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_columns(c, blocks);
+}
+template <typename TX, typename TG>
+cudaError_t bwd_ring(const BwdCall &c) {
     // 16 columns a thread leave room for two blocks an SM up to 352 threads; wider rows take 8
     const int t16 = (c.d + 511) / 512 * 32;
-    if (c.d == 16 * t16 && t16 <= 352) return go(k_ln_backward_ring<TX, TG, 4, true, 352, 2>, t16);
-    if (t16 <= 352) return go(k_ln_backward_ring<TX, TG, 4, false, 352, 2>, t16);
-    return go(k_ln_backward_ring<TX, TG, 2, false, 1024, 1>, (c.d + 255) / 256 * 32);
+    if (c.d == 16 * t16 && t16 <= 352) return bwd_ring_launch<k_ln_backward_ring<TX, TG, 4, true, 352, 2>, TX, TG>(c, t16);
+    if (t16 <= 352) return bwd_ring_launch<k_ln_backward_ring<TX, TG, 4, false, 352, 2>, TX, TG>(c, t16);
+    return bwd_ring_launch<k_ln_backward_ring<TX, TG, 2, false, 1024, 1>, TX, TG>(c, (c.d + 255) / 256 * 32);
 }
 
 template <typename TX, typename TG>
@@ -675,13 +766,15 @@ cudaError_t bwd_type(const BwdCall &c) {
         const bool bulk = (int64_t)d * sizeof(TX) % 16 == 0 && (int64_t)d * sizeof(TG) % 16 == 0 &&
                           aligned(c.x, c.xs * (int64_t)sizeof(TX), 16) && aligned(c.gy, c.gs * (int64_t)sizeof(TG), 16);
         if (bulk && d >= 1024 && d <= 8192 && c.n >= 2 * (int64_t)sm_count_of_device()) return bwd_ring<TX, TG>(c);
-        if (d <= 256) return bwd_launch<TX, TG, 4, 2>(c, 32);
-        if (d <= 8192) return bwd_launch<TX, TG, 4, 2>(c, (d + 255) / 256 * 32);
-        return bwd_launch<TX, TG, 4, 4>(c, (d + 511) / 512 * 32);
+        if (d <= 256) return bwd_launch<TX, TG, 4, 2, 512>(c, 32);
+        if (d <= 4096) return bwd_launch<TX, TG, 4, 2, 512>(c, (d + 255) / 256 * 32);
+        if (d <= 8192) return bwd_launch<TX, TG, 4, 2, 1024>(c, (d + 255) / 256 * 32);
+        return bwd_launch<TX, TG, 4, 4, 1024>(c, (d + 511) / 512 * 32);
     }
-    if (d <= 128) return bwd_launch<TX, TG, 1, 4>(c, 32);
-    if (d <= 8192) return bwd_launch<TX, TG, 1, 8>(c, (d + 255) / 256 * 32);
-    return bwd_launch<TX, TG, 1, 16>(c, (d + 511) / 512 * 32);
+    if (d <= 128) return bwd_launch<TX, TG, 1, 4, 512>(c, 32);
+    if (d <= 4096) return bwd_launch<TX, TG, 1, 8, 512>(c, (d + 255) / 256 * 32);
+    if (d <= 8192) return bwd_launch<TX, TG, 1, 8, 1024>(c, (d + 255) / 256 * 32);
+    return bwd_launch<TX, TG, 1, 16, 1024>(c, (d + 511) / 512 * 32);
 }
 
 }  // namespace ln

@@ -8,8 +8,6 @@ enqueues the call on the current CUDA stream of the tensors' device, or on
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _lib
@@ -24,7 +22,7 @@ _NAMES = "torch.float32, torch.bfloat16 or torch.float16"
 
 
 def _tensor(t, name, dtypes=None, device=None):
-    if not isinstance(t, torch.Tensor):
+    if t.__class__ is not torch.Tensor and not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if dtypes is not None and t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
@@ -38,7 +36,7 @@ def _tensor(t, name, dtypes=None, device=None):
 def _dense(t, name, dtypes, shape, device):
     """A contiguous tensor of a given shape."""
     _tensor(t, name, dtypes, device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -51,6 +49,8 @@ def _rows(t, name):
     buffer, a broadcast row); anything else is refused."""
     shape, strides = t.shape, t.stride()
     d = shape[-1]
+    if len(shape) == 2 and strides[1] == 1 and shape[0] > 1:
+        return shape[0], strides[0]
     if d > 1 and strides[-1] != 1:
         raise ValueError("%s must be dense along its last axis" % name)
     n, step = 1, None
@@ -67,23 +67,28 @@ def _rows(t, name):
     return n, d if step is None else step
 
 
-def _on(device, stream):
-    """The device and stream a call runs on, as a context and the raw stream."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
-        return torch.cuda.stream(stream), stream.cuda_stream
-    raw = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext(), raw
-    return torch.cuda.device(device), raw
+# the stream a device's current work goes to, as the number the C ABI takes
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch.cuda.current_device
+
+
+def _at(device, stream):
+    """The context in which a call for `device` runs on `stream` (None: the
+    device's current stream); what is allocated inside belongs to that stream."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
 
 
 def _norm_weights(norm_w, norm_b, x, d):
-    types = (torch.float32, x.dtype) if x.dtype != torch.float32 else (torch.float32,)
-    _dense(norm_w, "norm_w", types, (d,), x.device)
-    if norm_b is not None:
-        _dense(norm_b, "norm_b", (norm_w.dtype,), (d,), x.device)
+    types = (torch.float32, x.dtype)
+    for t, name in ((norm_w, "norm_w"), (norm_b, "norm_b")):
+        if t is None and name == "norm_b":
+            continue
+        _dense(t, name, types if t is norm_w else (norm_w.dtype,), (d,), x.device)
 
 
 def _norm_input(x):
@@ -93,84 +98,76 @@ def _norm_input(x):
         raise TypeError("x must be %s, got %s" % (_NAMES, x.dtype))
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be [..., d] with d >= 1")
-    return x
+    n, step = _rows(x, "x")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor (libhc has no CPU path)")
+    return n, step, x.shape[-1]
+
+
+def _like(t, name, x, dtypes):
+    """Rows of x's shape; returns their stride."""
+    _tensor(t, name, dtypes, x.device)
+    if t.shape != x.shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(x.shape)))
+    return _rows(t, name)[1]
 
 
 def hc_layer_norm(x, norm_w, norm_b=None, norm_eps=LAYER_NORM_EPS, y=None, return_stats=False, stream=None):
     """Layer norm of x [..., d] (fp32, bf16 or fp16; evenly spaced rows) with
     norm_w, norm_b [d] (fp32 or x's type; norm_b optional) -> y [..., d] of x's
     type [+ (mean, rstd) [...] fp32 for the backward when return_stats]."""
-    _norm_input(x)
-    n, xs = _rows(x, "x")
-    d = x.shape[-1]
-    _tensor(x, "x")
+    n, xs, d = _norm_input(x)
     _norm_weights(norm_w, norm_b, x, d)
     dev = x.device
-    if y is not None:
-        _tensor(y, "y", (x.dtype,), dev)
-        if y.shape != x.shape:
-            raise ValueError("y has shape %s, expected %s" % (tuple(y.shape), tuple(x.shape)))
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-            ys = d
-        else:
-            ys = _rows(y, "y")[1]
-        mean = rstd = None
-        if return_stats:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        _lib.call("hc_layer_norm", x.data_ptr(), xs, _DTYPE[x.dtype], norm_w.data_ptr(),
-                  None if norm_b is None else norm_b.data_ptr(), _DTYPE[norm_w.dtype], n, d, norm_eps,
-                  y.data_ptr(), ys, None if mean is None else mean.data_ptr(),
-                  None if rstd is None else rstd.data_ptr(), raw)
+    ys = d if y is None else _like(y, "y", x, (x.dtype,))
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_layer_norm(x, norm_w, norm_b, norm_eps, y, return_stats)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev).unbind(0)
+    _lib.call("hc_layer_norm", x.data_ptr(), xs, _DTYPE[x.dtype], norm_w.data_ptr(),
+              None if norm_b is None else norm_b.data_ptr(), _DTYPE[norm_w.dtype], n, d, norm_eps, y.data_ptr(), ys,
+              None if mean is None else mean.data_ptr(), None if rstd is None else rstd.data_ptr(),
+              _raw_stream(dev.index))
     return (y, mean, rstd) if return_stats else y
 
 
 def hc_layer_norm_backward(g_y, x, norm_w, mean, rstd, bias=True, g_x=None, workspace=None, stream=None):
     """The backward of hc_layer_norm: g_y [..., d] (fp32 or x's type), x, norm_w and
     the forward's mean, rstd -> dict of g_x [..., d] of g_y's type and the sums
-    over all rows g_norm_w [d] and (unless bias is False) g_norm_b [d], fp32."""
-    _norm_input(x)
-    n, xs = _rows(x, "x")
-    d = x.shape[-1]
-    _tensor(x, "x")
+    over all rows g_norm_w [d] and (unless bias is False) g_norm_b [d], fp32.
+    workspace: a uint8 device tensor of at least the size the library asks for
+    (allocated here when None)."""
+    n, xs, d = _norm_input(x)
     dev = x.device
     _norm_weights(norm_w, None, x, d)
-    _tensor(g_y, "g_y", (torch.float32, x.dtype), dev)
-    if g_y.shape != x.shape:
-        raise ValueError("g_y has shape %s, expected %s" % (tuple(g_y.shape), tuple(x.shape)))
-    gs = _rows(g_y, "g_y")[1]
+    gs = _like(g_y, "g_y", x, (torch.float32, x.dtype))
     _dense(mean, "mean", (torch.float32,), x.shape[:-1], dev)
     _dense(rstd, "rstd", (torch.float32,), x.shape[:-1], dev)
-    if g_x is not None:
-        _tensor(g_x, "g_x", (g_y.dtype,), dev)
-        if g_x.shape != x.shape:
-            raise ValueError("g_x has shape %s, expected %s" % (tuple(g_x.shape), tuple(x.shape)))
+    gxs = d if g_x is None else _like(g_x, "g_x", x, (g_y.dtype,))
     if workspace is not None:
         _tensor(workspace, "workspace", (torch.uint8,), dev)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    need = _lib.load().hc_layer_norm_backward_workspace_bytes(n, d)
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        if g_x is None:
-            g_x = torch.empty(x.shape, dtype=g_y.dtype, device=dev)
-            gxs = d
-        else:
-            gxs = _rows(g_x, "g_x")[1]
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        sums = torch.empty((2 if bias else 1, d), dtype=torch.float32, device=dev)
-        g_w, g_b = sums[0], sums[1] if bias else None
-        _lib.call("hc_layer_norm_backward", g_y.data_ptr(), gs, _DTYPE[g_y.dtype], x.data_ptr(), xs,
-                  _DTYPE[x.dtype], norm_w.data_ptr(), _DTYPE[norm_w.dtype], mean.data_ptr(), rstd.data_ptr(),
-                  n, d, g_x.data_ptr(), gxs, g_w.data_ptr(), None if g_b is None else g_b.data_ptr(),
-                  workspace.data_ptr(), workspace.numel(), raw)
-    out = {"g_x": g_x, "g_norm_w": g_w}
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_layer_norm_backward(g_y, x, norm_w, mean, rstd, bias, g_x, workspace)
+    if g_x is None:
+        g_x = torch.empty(x.shape, dtype=g_y.dtype, device=dev)
+    if workspace is None:
+        need = _lib.load().hc_layer_norm_backward_workspace_bytes(n, d)
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+    sums = torch.empty((2 if bias else 1, d), dtype=torch.float32, device=dev).unbind(0)
+    _lib.call("hc_layer_norm_backward", g_y.data_ptr(), gs, _DTYPE[g_y.dtype], x.data_ptr(), xs, _DTYPE[x.dtype],
+              norm_w.data_ptr(), _DTYPE[norm_w.dtype], mean.data_ptr(), rstd.data_ptr(), n, d, g_x.data_ptr(), gxs,
+              sums[0].data_ptr(), sums[1].data_ptr() if bias else None, workspace.data_ptr(), workspace.numel(),
+              _raw_stream(dev.index))
+    out = {"g_x": g_x, "g_norm_w": sums[0]}
     if bias:
-        out["g_norm_b"] = g_b
+        out["g_norm_b"] = sums[1]
     return out
 
 
@@ -187,7 +184,8 @@ def _grouped(rows, name, w_shape, offsets):
     if rows.dim() != 2 or len(w_shape) != 3:
         raise ValueError("%s must be [n, width] and the weights [experts, ., .]" % name)
     n, step = _rows(rows, name)
-    _tensor(rows, name)
+    if not rows.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (libhc has no CPU path)" % name)
     _dense(offsets, "offsets", (torch.int32,), (w_shape[0] + 1,), rows.device)
     # (a single row may carry any stride)
     return n, step if n > 1 else rows.shape[1]
@@ -215,16 +213,17 @@ def hc_grouped_mm(x, w, offsets, transposed=False, y=None, out_dtype=None, strea
     _dense(w, "w", (x.dtype,), (E, K, N) if transposed else (E, N, K), dev)
     if out_dtype is None:
         out_dtype = x.dtype if y is None else y.dtype
-    if out_dtype not in (x.dtype, torch.float32):
+    if out_dtype is not x.dtype and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be %s or torch.float32, got %s" % (x.dtype, out_dtype))
+    ys = N if y is None else _out_rows(y, "y", (n, N), (out_dtype,), dev)
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_grouped_mm(x, w, offsets, transposed, y, out_dtype)
     zero = y is None
-    ys = N if zero else _out_rows(y, "y", (n, N), (out_dtype,), dev)
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        if zero:
-            y = torch.empty((n, N), dtype=out_dtype, device=dev)
-        _lib.call("hc_grouped_mm", x.data_ptr(), xs, w.data_ptr(), int(transposed), offsets.data_ptr(), n, E, N, K,
-                  _DTYPE[x.dtype], y.data_ptr(), ys, _DTYPE[out_dtype], int(zero), raw)
+    if zero:
+        y = torch.empty((n, N), dtype=out_dtype, device=dev)
+    _lib.call("hc_grouped_mm", x.data_ptr(), xs, w.data_ptr(), transposed, offsets.data_ptr(), n, E, N, K,
+              _DTYPE[x.dtype], y.data_ptr(), ys, _DTYPE[out_dtype], zero, _raw_stream(dev.index))
     return y
 
 
@@ -240,21 +239,22 @@ def hc_grouped_mm_weights(g_y, x, offsets, transposed=False, g_w=None, out_dtype
     _tensor(g_y, "g_y", (x.dtype,), dev)
     if g_y.dim() != 2 or g_y.shape[0] != n:
         raise ValueError("g_y has shape %s, expected (%d, N)" % (tuple(g_y.shape), n))
-    gs = _grouped(g_y, "g_y", (E, 0, 0), offsets)[1]
+    gs = _rows(g_y, "g_y")[1] if n > 1 else g_y.shape[1]
     N, K = g_y.shape[1], x.shape[1]
     shape = (E, K, N) if transposed else (E, N, K)
     if out_dtype is None:
         out_dtype = x.dtype if g_w is None else g_w.dtype
-    if out_dtype not in (x.dtype, torch.float32):
+    if out_dtype is not x.dtype and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be %s or torch.float32, got %s" % (x.dtype, out_dtype))
     if g_w is not None:
         _dense(g_w, "g_w", (out_dtype,), shape, dev)
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        if g_w is None:
-            g_w = torch.empty(shape, dtype=out_dtype, device=dev)
-        _lib.call("hc_grouped_mm_weights", g_y.data_ptr(), gs, x.data_ptr(), xs, offsets.data_ptr(), n, E, N, K,
-                  _DTYPE[x.dtype], g_w.data_ptr(), int(transposed), _DTYPE[out_dtype], raw)
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_grouped_mm_weights(g_y, x, offsets, transposed, g_w, out_dtype)
+    if g_w is None:
+        g_w = torch.empty(shape, dtype=out_dtype, device=dev)
+    _lib.call("hc_grouped_mm_weights", g_y.data_ptr(), gs, x.data_ptr(), xs, offsets.data_ptr(), n, E, N, K,
+              _DTYPE[x.dtype], g_w.data_ptr(), transposed, _DTYPE[out_dtype], _raw_stream(dev.index))
     return g_w
 
 
@@ -358,7 +358,7 @@ def hc_adamw_step(plan, lr, step, betas=(0.9, 0.999), adam_eps=1e-8, weight_deca
     dev = plan.device
     on_device = []
     for t, name, dtype in ((lr, "lr", torch.float32), (step, "step", torch.int64), (grad_scale, "grad_scale", torch.float32)):
-        if isinstance(t, torch.Tensor):
+        if t.__class__ is not float and t.__class__ is not int and isinstance(t, torch.Tensor):
             _tensor(t, name, (dtype,), dev)
             if t.numel() != 1:
                 raise ValueError("%s must have one element" % name)
@@ -367,8 +367,10 @@ def hc_adamw_step(plan, lr, step, betas=(0.9, 0.999), adam_eps=1e-8, weight_deca
             on_device.append(None)
     if grad_scale is not None and on_device[2] is None:
         raise TypeError("grad_scale must be a CUDA tensor")
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_adamw_step(plan, lr, step, betas, adam_eps, weight_decay, grad_scale)
     plan._describe()
-    ctx, raw = _on(dev, stream)
-    with ctx:
-        _lib.call("hc_adamw_step", plan._array, plan.count, 0.0 if on_device[0] else lr, betas[0], betas[1], adam_eps,
-                  weight_decay, 1 if on_device[1] else step, on_device[0], on_device[1], on_device[2], raw)
+    _lib.call("hc_adamw_step", plan._array, plan.count, 0.0 if on_device[0] else lr, betas[0], betas[1], adam_eps,
+              weight_decay, 1 if on_device[1] else step, on_device[0], on_device[1], on_device[2],
+              _raw_stream(dev.index))
