@@ -84,11 +84,9 @@ def _at(device, stream):
 
 
 def _norm_weights(norm_w, norm_b, x, d):
-    types = (torch.float32, x.dtype)
-    for t, name in ((norm_w, "norm_w"), (norm_b, "norm_b")):
-        if t is None and name == "norm_b":
-            continue
-        _dense(t, name, types if t is norm_w else (norm_w.dtype,), (d,), x.device)
+    _dense(norm_w, "norm_w", (torch.float32, x.dtype), (d,), x.device)
+    if norm_b is not None:
+        _dense(norm_b, "norm_b", (norm_w.dtype,), (d,), x.device)
 
 
 def _norm_input(x):
@@ -127,7 +125,8 @@ def hc_layer_norm(x, norm_w, norm_b=None, norm_eps=LAYER_NORM_EPS, y=None, retur
         y = torch.empty(x.shape, dtype=x.dtype, device=dev)
     mean = rstd = None
     if return_stats:
-        mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev).unbind(0)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
     _lib.call("hc_layer_norm", x.data_ptr(), xs, _DTYPE[x.dtype], norm_w.data_ptr(),
               None if norm_b is None else norm_b.data_ptr(), _DTYPE[norm_w.dtype], n, d, norm_eps, y.data_ptr(), ys,
               None if mean is None else mean.data_ptr(), None if rstd is None else rstd.data_ptr(),
@@ -160,15 +159,13 @@ def hc_layer_norm_backward(g_y, x, norm_w, mean, rstd, bias=True, g_x=None, work
     if workspace is None:
         need = _lib.load().hc_layer_norm_backward_workspace_bytes(n, d)
         workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
-    sums = torch.empty((2 if bias else 1, d), dtype=torch.float32, device=dev).unbind(0)
+    g_w = torch.empty((d,), dtype=torch.float32, device=dev)
+    g_b = torch.empty((d,), dtype=torch.float32, device=dev) if bias else None
     _lib.call("hc_layer_norm_backward", g_y.data_ptr(), gs, _DTYPE[g_y.dtype], x.data_ptr(), xs, _DTYPE[x.dtype],
               norm_w.data_ptr(), _DTYPE[norm_w.dtype], mean.data_ptr(), rstd.data_ptr(), n, d, g_x.data_ptr(), gxs,
-              sums[0].data_ptr(), sums[1].data_ptr() if bias else None, workspace.data_ptr(), workspace.numel(),
+              g_w.data_ptr(), None if g_b is None else g_b.data_ptr(), workspace.data_ptr(), workspace.numel(),
               _raw_stream(dev.index))
-    out = {"g_x": g_x, "g_norm_w": sums[0]}
-    if bias:
-        out["g_norm_b"] = sums[1]
-    return out
+    return {"g_x": g_x, "g_norm_w": g_w, "g_norm_b": g_b} if bias else {"g_x": g_x, "g_norm_w": g_w}
 
 
 _HALF = (torch.bfloat16, torch.float16)
