@@ -16,7 +16,13 @@
 //
 // One CTA per SM walks the tiles (warp 0 loads by TMA, warp 1 issues
 // tcgen05.mma, warps 2-5 write finished tiles); two accumulators alternate, so
-// that a tile is written while the next one's products run.
+// that a tile is written while the next one's products run.  Where the tiles are
+// large two CTAs work on one (cta_group::2: 256 of f, each CTA with half of A's
+// rows and half of B's columns in its shared memory), because one SM's MMA of
+// 128 x 256 reads 12 KB of shared memory every 64 cycles, half again of what it
+// delivers, and the pair's reads 8 KB.
+#include <atomic>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,10 +42,14 @@ constexpr int kThreads = 192;
 constexpr int kMaxExperts = 1024;
 constexpr unsigned int kErrOffsets = 2u;  // device error bit: offsets out of order or out of range
 
-template <int BN>
+template <int BN, bool kPair>
 struct Cfg {
-    static constexpr int kABytes = kM * kBK * 2, kBBytes = BN * kBK * 2, kStage = kABytes + kBBytes;
-    static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : BN >= 64 ? 8 : 10;
+    static constexpr int kCtas = kPair ? 2 : 1;
+    static constexpr int kTileF = kM * kCtas;           // f of a tile
+    static constexpr int kOwn = BN / kCtas;             // columns whose B a CTA holds
+    static constexpr int kGrain = 16 * kCtas;           // an MMA's columns come in these
+    static constexpr int kABytes = kM * kBK * 2, kBBytes = kOwn * kBK * 2, kStage = kABytes + kBBytes;
+    static constexpr int kStages = kOwn >= 256 ? 4 : kOwn >= 128 ? 6 : kOwn >= 64 ? 8 : 10;
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kSmem = kStages * kStage + 1024 + 3 * (kMaxExperts + 1) * 4;
     static_assert(kSmem <= 227 * 1024 - 512, "shared memory");
@@ -64,28 +74,96 @@ __device__ __forceinline__ uint64_t desc(uint32_t saddr, bool mn_major) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (chunk << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
            ((uint64_t)2 << 61);
 }
-__device__ __forceinline__ uint32_t idesc(bool fp16, bool a_mn, bool b_mn, int n) {
+__device__ __forceinline__ uint32_t idesc(bool fp16, bool a_mn, bool b_mn, int m, int n) {
     const uint32_t t = fp16 ? 0u : 1u;
     return (1u << 4) | (t << 7) | (t << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+// One thread of the (converged) warp issues; the same one every time.  The other
+// operands are the warp's common values, so that they can stay in uniform
+// registers: issued from a branch for lane 0 alone an MMA took 150 cycles to
+// issue, more than the 128 it runs.
+template <bool kPair>
 __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(id),
-        "r"(accumulate)
-        : "memory");
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(id),
+            "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(id),
+            "r"(accumulate)
+            : "memory");
 }
+// One arrival on `bar` (of a pair: of both CTAs) once the MMAs issued so far are done.
+template <bool kPair>
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+            : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, int c2,
-                                            uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
-        : "memory");
+// An arrival at the other CTA's barrier that orders nothing: the loads themselves
+// complete on the barrier.  (The releasing form waits for everything this thread
+// has in flight, 2,000 cycles a stage, four times a stage's products.)
+__device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Tensor loads; of a pair the barrier may be the other CTA's.
+template <bool kPair>
+__device__ __forceinline__ void load_2d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, uint64_t policy) {
+    if constexpr (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+            " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        tma_load_2d(dst, tmap, bar, c0, c1, policy);
+}
+template <bool kPair>
+__device__ __forceinline__ void load_3d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, int c2,
+                                        uint64_t policy) {
+    if constexpr (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+            : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_get(uint32_t smem_dst, uint32_t ncols) {
+    if constexpr (kPair) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(smem_dst, ncols);
+        tmem_relinquish();
+    }
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_give_back(uint32_t taddr, uint32_t ncols) {
+    if constexpr (kPair)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+    else
+        tmem_dealloc(taddr, ncols);
 }
 // 16 columns of this lane, waited for in the same statement (no register copy
 // can slip between the load and the wait).
@@ -123,7 +201,7 @@ struct Tile {
     int e, f0, c0, cols;  // cols: columns of the tile that count (rows of the product)
     int k0, klen;         // contraction: rows [k0, k0 + klen) of the weights', [0, K) of the product
 };
-template <int BN, bool kWeights>
+template <int BN, bool kPair, bool kWeights>
 __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, int &e) {
     while (tile >= p.first[e + 1]) ++e;
     const int local = tile - p.first[e];
@@ -132,15 +210,16 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
     t.e = e;
     if (kWeights) {
         const int nc = (a.C + BN - 1) / BN;
-        t.f0 = local / nc * kM;
+        t.f0 = local / nc * Cfg<BN, kPair>::kTileF;
         t.c0 = local % nc * BN;
         t.cols = a.C - t.c0 < BN ? a.C - t.c0 : BN;
         t.k0 = p.start[e];
         t.klen = rows;
     } else {
         const int nt = (rows + BN - 1) / BN;
-        const int per = ((rows + nt - 1) / nt + 15) / 16 * 16;
-        t.f0 = local / nt * kM;
+        constexpr int kGrain = Cfg<BN, kPair>::kGrain;
+        const int per = ((rows + nt - 1) / nt + kGrain - 1) / kGrain * kGrain;
+        t.f0 = local / nt * Cfg<BN, kPair>::kTileF;
         const int at = local % nt * per;
         t.c0 = p.start[e] + at;
         t.cols = rows - at < per ? rows - at : per;
@@ -150,33 +229,52 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
     return t;
 }
 
+// Whether a stage of the weights' gradient ends among the rows of 16 that one
+// MMA reads: the rows behind the expert's last, up to the next 16, are another
+// expert's (or anything) and are made zero in both operands before the MMA.
+__device__ __forceinline__ int rows_to_clear(int left) { return left < kBK ? (16 - left % 16) % 16 : 0; }
+// ... a warp clears them in `chunks` tiles of 64 columns each from `tiles` on.
+__device__ __forceinline__ void clear_rows(uint32_t tiles, int chunks, int left, int rest, int lane) {
+    for (int i = lane; i < chunks * rest * 8; i += 32) {
+        const int ch = i / (rest * 8), r = left + i % (rest * 8) / 8;
+        const uint32_t p = tiles + (uint32_t)(ch * 64 * kBK * 2 + r * 128 + (i & 7) * 16);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 // kAMn: the M side's operand lies MN-major in global memory (w[e][k][f], or the
 // rows of the weights' gradient); kWeights: the weights' gradient (B is MN-major too).
-template <int BN, bool kAMn, bool kWeights>
+// Of a pair the first CTA issues the MMAs and its barriers collect both CTAs'
+// loads and both epilogues' arrivals; commits arrive at both CTAs' barriers.
+template <int BN, bool kPair, bool kAMn, bool kWeights>
 __global__ void __launch_bounds__(kThreads, 1)
 k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a) {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, kPair>;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     int *const s_start = reinterpret_cast<int *>(smem_raw + (sbase - smem_u32(smem_raw)) + S * C::kStage);
     int *const s_end = s_start + kMaxExperts, *const s_first = s_end + kMaxExperts;
     __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], acc_full[2], acc_empty[2], done_bar;
+    __shared__ __align__(8) uint64_t clear_bar[kPair && kWeights ? S : 1];  // the second CTA's loads of a stage to clear
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = kPair ? (int)cluster_ctarank() : 0;
+    const int worker = kPair ? (int)blockIdx.x >> 1 : (int)blockIdx.x, workers = kPair ? (int)gridDim.x >> 1 : (int)gridDim.x;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(smem_u32(&full_bar[s]), 1), mbar_init(smem_u32(&empty_bar[s]), 1);
-        for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&acc_full[b]), 1), mbar_init(smem_u32(&acc_empty[b]), 4);
+        for (int s = 0; s < S; ++s) mbar_init(smem_u32(&full_bar[s]), C::kCtas), mbar_init(smem_u32(&empty_bar[s]), 1);
+        for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&acc_full[b]), 1), mbar_init(smem_u32(&acc_empty[b]), 4 * C::kCtas);
+        if (kPair && kWeights)
+            for (int s = 0; s < S; ++s) mbar_init(smem_u32(&clear_bar[s]), 1);
         mbar_init(smem_u32(&done_bar), 1);
         s_abort = 0;
         fence_mbar_init_cluster();
     }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(&s_tmem), C::kTmemCols);
-        tmem_relinquish();
-    }
+    if (warp == 1) tmem_get<kPair>(smem_u32(&s_tmem), C::kTmemCols);
     // every expert's rows and how many tiles they make; a range that is out of
     // order or out of the rows counts as empty and is reported
     for (int e = threadIdx.x; e < a.experts; e += kThreads) {
@@ -186,7 +284,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             s = t = 0;
         }
         s_start[e] = (int)s, s_end[e] = (int)t;
-        const int mt = (a.F + kM - 1) / kM;
+        const int mt = (a.F + C::kTileF - 1) / C::kTileF;
         s_first[e + 1] = kWeights ? mt * ((a.C + BN - 1) / BN) : mt * (int)((t - s + BN - 1) / BN);
     }
     __syncthreads();
@@ -206,6 +304,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     }
     tmem_fence_before_sync();
     __syncthreads();
+    if (kPair) cluster_sync_all();  // the other CTA's barriers and tensor memory are ready
     tmem_fence_after_sync();
     const uint32_t tbase = s_tmem;
     const Plan plan{s_start, s_end, s_first};
@@ -218,85 +317,128 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             prefetch_tmap(&tm_b);
             const uint64_t pol = policy_evict_normal();
             int it = 0;
-            for (int tile = blockIdx.x; tile < tiles && !s_abort; tile += gridDim.x) {
-                const Tile t = tile_of<BN, kWeights>(a, plan, tile, e);
+            for (int tile = worker; tile < tiles && !s_abort; tile += workers) {
+                const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
                 const int nkb = (t.klen + kBK - 1) / kBK;
-                const int boxes = kWeights ? (t.cols + 63) / 64 : (t.cols + kRowBox - 1) / kRowBox;
+                // this CTA's columns of B, and how many boxes each CTA loads
+                const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
+                const int c0 = t.c0 + rank * own, f0 = t.f0 + rank * kM;
+                const int boxes = kWeights ? (own + 63) / 64 : (own + kRowBox - 1) / kRowBox;
                 constexpr int kBox = kWeights ? 64 * kBK * 2 : kRowBox * kBK * 2;
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     const int slot = it % S;
                     if (!mbar_wait<false>(smem_u32(&empty_bar[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, &s_abort)) break;
                     const uint32_t sa = sbase + (uint32_t)slot * C::kStage, sb = sa + C::kABytes;
-                    const uint32_t bar = smem_u32(&full_bar[slot]);
-                    mbar_arrive_expect_tx(bar, (uint32_t)(C::kABytes + boxes * kBox));
                     const int k = t.k0 + kb * kBK;
+                    const uint32_t bytes = (uint32_t)(C::kABytes + boxes * kBox);
+                    uint32_t bar = smem_u32(&full_bar[slot]);
+                    if (kPair) {
+                        // both CTAs' bytes are expected at the first one's barrier, unless the
+                        // second one's rows are cleared first
+                        const bool apart = kWeights && rows_to_clear(t.klen - kb * kBK) != 0;
+                        if (rank == 0) {
+                            mbar_arrive_expect_tx(bar, apart ? bytes : 2 * bytes);
+                        } else if (apart) {
+                            bar = smem_u32(&clear_bar[slot]);
+                            mbar_arrive_expect_tx(bar, bytes);
+                        } else {
+                            bar = mapa(bar, 0);
+                            arrive_remote_relaxed(bar);
+                        }
+                    } else {
+                        mbar_arrive_expect_tx(bar, bytes);
+                    }
                     if (kWeights) {
-                        tma_load_2d(sa, &tm_a, bar, t.f0, k, pol);
-                        tma_load_2d(sa + 64 * kBK * 2, &tm_a, bar, t.f0 + 64, k, pol);
-                        for (int i = 0; i < boxes; ++i) tma_load_2d(sb + i * kBox, &tm_b, bar, t.c0 + i * 64, k, pol);
+                        load_2d<kPair>(sa, &tm_a, bar, f0, k, pol);
+                        load_2d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, pol);
+                        for (int i = 0; i < boxes; ++i) load_2d<kPair>(sb + i * kBox, &tm_b, bar, c0 + i * 64, k, pol);
                     } else {
                         if (kAMn) {
-                            tma_load_3d(sa, &tm_a, bar, t.f0, k, t.e, pol);
-                            tma_load_3d(sa + 64 * kBK * 2, &tm_a, bar, t.f0 + 64, k, t.e, pol);
+                            load_3d<kPair>(sa, &tm_a, bar, f0, k, t.e, pol);
+                            load_3d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, t.e, pol);
                         } else {
-                            tma_load_3d(sa, &tm_a, bar, k, t.f0, t.e, pol);
+                            load_3d<kPair>(sa, &tm_a, bar, k, f0, t.e, pol);
                         }
                         for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(sb + i * kBox, &tm_b, bar, k, t.c0 + i * kRowBox, pol);
+                            load_2d<kPair>(sb + i * kBox, &tm_b, bar, k, c0 + i * kRowBox, pol);
                     }
                 }
             }
-            // the last stages issued must land before the CTA leaves
-            for (int k = (it > S ? it - S : 0); k < it; ++k)
-                wait_exit(smem_u32(&full_bar[k % S]), (uint32_t)(k / S) & 1u);
+            // the last stages issued must land before the CTA leaves (of a pair, the
+            // second CTA's land when their MMAs have read them: its empty barriers say so)
+            for (int k = (it > S ? it - S : 0); k < it; ++k) {
+                if (rank == 0) wait_exit(smem_u32(&full_bar[k % S]), (uint32_t)(k / S) & 1u);
+                else wait_exit(smem_u32(&empty_bar[k % S]), (uint32_t)(k / S) & 1u);
+            }
         }
-    } else if (warp == 1) {
-        int it = 0, c = 0;
+    } else if (warp == 1 && rank == 0) {
+        int c = 0, slot = 0;
+        uint32_t parity = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-            const Tile t = tile_of<BN, kWeights>(a, plan, tile, e);
-            if (t.klen == 0) continue;  // an expert without rows: its gradient is zero
+        // the first stage's descriptors; a stage and 16 of k are steps of their addresses
+        const uint64_t da0 = desc(sbase, kAMn || kWeights), db0 = desc(sbase + C::kABytes, kWeights);
+        constexpr uint32_t kStepA = (kAMn || kWeights ? 2048 : 32) >> 4, kStepB = (kWeights ? 2048 : 32) >> 4;
+        for (int tile = worker; tile < tiles && ok; tile += workers) {
+            const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
+            const int klen = __shfl_sync(0xffffffffu, t.klen, 0), cols = __shfl_sync(0xffffffffu, t.cols, 0);
+            if (klen == 0) continue;  // an expert without rows: its gradient is zero
             const int b = c & 1;
-            if (!(ok = mbar_wait_warp<false>(smem_u32(&acc_empty[b]), ((uint32_t)(c >> 1) & 1u) ^ 1u, &s_abort))) break;
+            if (!(ok = mbar_wait_warp<kPair>(smem_u32(&acc_empty[b]), ((uint32_t)(c >> 1) & 1u) ^ 1u, &s_abort))) break;
             tmem_fence_after_sync();
             const uint32_t d = tbase + (uint32_t)(b * BN);
-            const uint32_t id = idesc(a.fp16, kAMn || kWeights, kWeights, (t.cols + 15) / 16 * 16);
-            const int nkb = (t.klen + kBK - 1) / kBK;
-            for (int kb = 0; kb < nkb; ++kb, ++it) {
-                const int slot = it % S;
-                if (!(ok = mbar_wait_warp<false>(smem_u32(&full_bar[slot]), (uint32_t)(it / S) & 1u, &s_abort))) break;
-                const uint32_t sa = sbase + (uint32_t)slot * C::kStage, sb = sa + C::kABytes;
-                const int left = t.klen - kb * kBK, steps = left >= kBK ? kBK / 16 : (left + 15) / 16;
-                if (kWeights && left < steps * 16) {
-                    // rows behind the expert's last, up to the next 16: another expert's (or
-                    // anything), made zero in both operands before the MMA reads them
-                    const int rest = steps * 16 - left, chunks = 2 + (t.cols + 63) / 64;
-                    for (int i = lane; i < chunks * rest * 8; i += 32) {
-                        const int ch = i / (rest * 8), r = left + i % (rest * 8) / 8;
-                        const uint32_t p = sa + (uint32_t)(ch * 64 * kBK * 2 + r * 128 + (i & 7) * 16);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
+            const int n = (cols + C::kGrain - 1) / C::kGrain * C::kGrain;
+            const uint32_t id = idesc(a.fp16, kAMn || kWeights, kWeights, C::kTileF, n);
+            uint32_t accumulate = 0;
+            for (int left = klen; left > 0; left -= kBK) {
+                if (!(ok = mbar_wait_warp<false>(smem_u32(&full_bar[slot]), parity, &s_abort))) break;
+                if (kWeights && rows_to_clear(left)) {
+                    // (the second CTA's clearing is seen by an acquire at cluster scope, too slow for every stage)
+                    if (kPair) mbar_wait_warp<true>(smem_u32(&full_bar[slot]), parity, &s_abort);
+                    clear_rows(sbase + (uint32_t)slot * C::kStage, 2 + (n / C::kCtas + 63) / 64, left, rows_to_clear(left), lane);
                 }
                 tmem_fence_after_sync();
-                if (lane == 0) {
-                    for (int ks = 0; ks < steps; ++ks)
-                        umma(d, desc(sa + (uint32_t)ks * (kAMn || kWeights ? 2048 : 32), kAMn || kWeights),
-                             desc(sb + (uint32_t)ks * (kWeights ? 2048 : 32), kWeights), id, kb > 0 || ks > 0);
-                    umma_commit(smem_u32(&empty_bar[slot]));
+                const uint64_t da = da0 + (uint32_t)slot * (C::kStage >> 4), db = db0 + (uint32_t)slot * (C::kStage >> 4);
+                if (left >= kBK) {
+#pragma unroll
+                    for (uint32_t ks = 0; ks < kBK / 16; ++ks)
+                        umma<kPair>(d, da + ks * kStepA, db + ks * kStepB, id, ks ? 1u : accumulate);
+                } else {
+                    for (uint32_t ks = 0; ks * 16 < (uint32_t)left; ++ks)
+                        umma<kPair>(d, da + ks * kStepA, db + ks * kStepB, id, ks ? 1u : accumulate);
                 }
-                __syncwarp();
+                umma_commit<kPair>(smem_u32(&empty_bar[slot]));
+                accumulate = 1;
+                if (++slot == S) slot = 0, parity ^= 1u;
             }
-            if (ok && lane == 0) umma_commit(smem_u32(&acc_full[b]));
+            if (ok) umma_commit<kPair>(smem_u32(&acc_full[b]));
             ++c;
         }
         // every MMA issued has completed before the tensor memory is freed
-        if (lane == 0) {
-            umma_commit(smem_u32(&done_bar));
-            wait_exit(smem_u32(&done_bar), 0u);
-        }
+        umma_commit<kPair>(smem_u32(&done_bar));
+        wait_exit(smem_u32(&done_bar), 0u);
         __syncwarp();
+    } else if (warp == 1) {
+        // the second CTA of a pair: clears the rows of a gradient's last stages in its
+        // own tiles, then tells the first CTA that the stage is ready
+        if constexpr (kPair && kWeights) {
+            int it = 0;
+            uint32_t parity = 0;
+            bool ok = true;
+            for (int tile = worker; tile < tiles && ok; tile += workers) {
+                const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
+                if (t.klen == 0) continue;
+                const int nkb = (t.klen + kBK - 1) / kBK, left = t.klen - (nkb - 1) * kBK;
+                it += nkb;
+                if (!rows_to_clear(left)) continue;
+                const int slot = (it - 1) % S;
+                if (!(ok = mbar_wait_warp<false>(smem_u32(&clear_bar[slot]), parity >> slot & 1u, &s_abort))) break;
+                parity ^= 1u << slot;
+                const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
+                clear_rows(sbase + (uint32_t)slot * C::kStage, 2 + (own + 63) / 64, left, rows_to_clear(left), lane);
+                if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&full_bar[slot]), 0));
+                __syncwarp();
+            }
+        }
     } else {
         const int q = warp & 3;  // the warp's quadrant of tensor-memory lanes
         const int64_t esize = a.out_f32 ? 4 : 2;
@@ -311,9 +453,9 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             }
         }
         int c = 0;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const Tile t = tile_of<BN, kWeights>(a, plan, tile, e);
-            const int f = t.f0 + q * 32 + lane;
+        for (int tile = worker; tile < tiles; tile += workers) {
+            const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
+            const int f = t.f0 + rank * kM + q * 32 + lane;
             uint8_t *o = static_cast<uint8_t *>(a.out) +
                          ((kWeights ? (int64_t)t.e * a.C + t.c0 : (int64_t)t.c0) * a.out_stride + f) * esize;
             const int64_t step = a.out_stride * esize;
@@ -336,14 +478,18 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             }
             tmem_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&acc_empty[b]));
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(smem_u32(&acc_empty[b]));
+                else mbar_arrive_remote(mapa(smem_u32(&acc_empty[b]), 0));
+            }
             ++c;
         }
     }
     tmem_fence_before_sync();
     __syncthreads();
+    if (kPair) cluster_sync_all();  // nothing of either CTA reaches into the other any more
     tmem_fence_after_sync();
-    if (warp == 1) tmem_dealloc(tbase, C::kTmemCols);
+    if (warp == 1) tmem_give_back<kPair>(tbase, C::kTmemCols);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -372,20 +518,40 @@ bool make_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, int64_t d
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 148;
-    return sms;
-}
+constexpr int kDevices = 64;
 
-template <int BN, bool kAMn, bool kWeights>
+// Launches on every SM (pairs: every two SMs that can work together), once per
+// kernel and device finding out how many and allowing the shared memory.
+template <int BN, bool kPair, bool kAMn, bool kWeights>
 cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_t s) {
-    const auto k = k_grouped_mm<BN, kAMn, kWeights>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmem);
+    using C = Cfg<BN, kPair>;
+    const auto k = k_grouped_mm<BN, kPair, kAMn, kWeights>;
+    static std::atomic<int> ctas[kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)sm_count(), kThreads, Cfg<BN>::kSmem, s>>>(ta, tb, a);
-    return cudaGetLastError();
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    cudaLaunchAttribute pair{};
+    pair.id = cudaLaunchAttributeClusterDimension;
+    pair.val.clusterDim.x = 2, pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = C::kSmem, cfg.stream = s;
+    cfg.attrs = &pair, cfg.numAttrs = kPair ? 1 : 0;
+    int grid = ctas[dev].load(std::memory_order_relaxed);
+    if (!grid) {
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess) return e;
+        if ((e = cudaDeviceGetAttribute(&grid, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        if (kPair) {
+            int clusters = 0;
+            cfg.gridDim = dim3((unsigned)grid / 2 * 2);
+            if ((e = cudaOccupancyMaxActiveClusters(&clusters, k, &cfg)) != cudaSuccess) return e;
+            if (clusters < 1) return cudaErrorLaunchOutOfResources;
+            grid = grid / 2 < clusters ? grid / 2 * 2 : clusters * 2;
+        }
+        ctas[dev].store(grid, std::memory_order_relaxed);
+    }
+    cfg.gridDim = dim3((unsigned)grid);
+    return cudaLaunchKernelEx(&cfg, k, ta, tb, a);
 }
 
 }  // namespace gm
@@ -401,8 +567,8 @@ cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bo
     const gm::Args a{offsets, experts, n, N, 0, K, y, y_stride, y_f32, fp16, zero_rest};
     // Few rows an expert: narrow row tiles leave room for more stages of weights in flight.
     if (n <= 32 * (int64_t)experts)
-        return w_kn ? gm::launch<32, true, false>(ta, tb, a, s) : gm::launch<32, false, false>(ta, tb, a, s);
-    return w_kn ? gm::launch<256, true, false>(ta, tb, a, s) : gm::launch<256, false, false>(ta, tb, a, s);
+        return w_kn ? gm::launch<32, false, true, false>(ta, tb, a, s) : gm::launch<32, false, false, false>(ta, tb, a, s);
+    return w_kn ? gm::launch<256, true, true, false>(ta, tb, a, s) : gm::launch<256, true, false, false>(ta, tb, a, s);
 }
 
 cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, const void *am, int64_t a_stride, int F,
@@ -412,7 +578,7 @@ cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, co
     if (!gm::make_map(&ta, am, fp16, F, n, a_stride, 0, gm::kBK) || !gm::make_map(&tb, b, fp16, C, n, b_stride, 0, gm::kBK))
         return cudaErrorInvalidValue;
     const gm::Args a{offsets, experts, n, F, C, 0, g_w, F, g_f32, fp16, false};
-    return gm::launch<256, true, true>(ta, tb, a, s);
+    return gm::launch<256, true, true, true>(ta, tb, a, s);
 }
 
 cudaError_t consume_grouped_mm_device_error(cudaStream_t s, unsigned int *flag) {
