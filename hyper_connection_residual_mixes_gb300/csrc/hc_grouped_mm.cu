@@ -37,7 +37,8 @@ namespace gm {
 
 constexpr int kM = 128;       // f per tile
 constexpr int kBK = 64;       // k per stage: one 128-byte swizzled row of 16-bit values
-constexpr int kRowBox = 32;   // rows of a K-major B box
+constexpr int kRowBox = 32;   // rows of a small K-major B box (a large one holds a CTA's whole share)
+constexpr int kGroup = 8;     // tiles of c that are walked together
 constexpr int kThreads = 192;
 constexpr int kMaxExperts = 1024;
 constexpr unsigned int kErrOffsets = 2u;  // device error bit: offsets out of order or out of range
@@ -201,6 +202,15 @@ struct Tile {
     int e, f0, c0, cols;  // cols: columns of the tile that count (rows of the product)
     int k0, klen;         // contraction: rows [k0, k0 + klen) of the weights', [0, K) of the product
 };
+// An expert's tiles are walked in groups of kGroup tiles of c, through all of f
+// before the next group: what the CTAs read at one time (some 80 tiles) is then
+// about as wide as long, and stays in L2 where a long expert's rows do not.
+__device__ __forceinline__ void place_of(int local, int ft, int ct, int &f, int &c) {
+    const int g = local / (kGroup * ft), rest = local - g * (kGroup * ft);
+    const int w = ct - g * kGroup < kGroup ? ct - g * kGroup : kGroup;
+    f = rest / w;
+    c = g * kGroup + rest - f * w;
+}
 template <int BN, bool kPair, bool kWeights>
 __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, int &e) {
     while (tile >= p.first[e + 1]) ++e;
@@ -208,10 +218,11 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
     const int rows = p.end[e] - p.start[e];
     Tile t;
     t.e = e;
+    const int ft = (a.F + Cfg<BN, kPair>::kTileF - 1) / Cfg<BN, kPair>::kTileF;
+    int f, c;
     if (kWeights) {
-        const int nc = (a.C + BN - 1) / BN;
-        t.f0 = local / nc * Cfg<BN, kPair>::kTileF;
-        t.c0 = local % nc * BN;
+        place_of(local, ft, (a.C + BN - 1) / BN, f, c);
+        t.c0 = c * BN;
         t.cols = a.C - t.c0 < BN ? a.C - t.c0 : BN;
         t.k0 = p.start[e];
         t.klen = rows;
@@ -219,13 +230,14 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
         const int nt = (rows + BN - 1) / BN;
         constexpr int kGrain = Cfg<BN, kPair>::kGrain;
         const int per = ((rows + nt - 1) / nt + kGrain - 1) / kGrain * kGrain;
-        t.f0 = local / nt * Cfg<BN, kPair>::kTileF;
-        const int at = local % nt * per;
+        place_of(local, ft, nt, f, c);
+        const int at = c * per;
         t.c0 = p.start[e] + at;
         t.cols = rows - at < per ? rows - at : per;
         t.k0 = 0;
         t.klen = a.K;
     }
+    t.f0 = f * Cfg<BN, kPair>::kTileF;
     return t;
 }
 
@@ -250,7 +262,8 @@ __device__ __forceinline__ void clear_rows(uint32_t tiles, int chunks, int left,
 // loads and both epilogues' arrivals; commits arrive at both CTAs' barriers.
 template <int BN, bool kPair, bool kAMn, bool kWeights>
 __global__ void __launch_bounds__(kThreads, 1)
-k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Args a) {
+k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+             const __grid_constant__ CUtensorMap tm_rows, const Args a) {
     using C = Cfg<BN, kPair>;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -323,14 +336,16 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 // this CTA's columns of B, and how many boxes each CTA loads
                 const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
                 const int c0 = t.c0 + rank * own, f0 = t.f0 + rank * kM;
-                const int boxes = kWeights ? (own + 63) / 64 : (own + kRowBox - 1) / kRowBox;
-                constexpr int kBox = kWeights ? 64 * kBK * 2 : kRowBox * kBK * 2;
+                // (of the product's rows one large box, or small ones where most of it would not count)
+                const bool large = !kWeights && own > C::kOwn / 2;
+                const int boxes = kWeights ? (own + 63) / 64 : large ? 1 : (own + kRowBox - 1) / kRowBox;
+                const int box = kWeights ? 64 * kBK * 2 : large ? C::kBBytes : kRowBox * kBK * 2;
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     const int slot = it % S;
                     if (!mbar_wait<false>(smem_u32(&empty_bar[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, &s_abort)) break;
                     const uint32_t sa = sbase + (uint32_t)slot * C::kStage, sb = sa + C::kABytes;
                     const int k = t.k0 + kb * kBK;
-                    const uint32_t bytes = (uint32_t)(C::kABytes + boxes * kBox);
+                    const uint32_t bytes = (uint32_t)(C::kABytes + boxes * box);
                     uint32_t bar = smem_u32(&full_bar[slot]);
                     if (kPair) {
                         // both CTAs' bytes are expected at the first one's barrier, unless the
@@ -351,7 +366,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     if (kWeights) {
                         load_2d<kPair>(sa, &tm_a, bar, f0, k, pol);
                         load_2d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, pol);
-                        for (int i = 0; i < boxes; ++i) load_2d<kPair>(sb + i * kBox, &tm_b, bar, c0 + i * 64, k, pol);
+                        for (int i = 0; i < boxes; ++i) load_2d<kPair>(sb + i * box, &tm_b, bar, c0 + i * 64, k, pol);
                     } else {
                         if (kAMn) {
                             load_3d<kPair>(sa, &tm_a, bar, f0, k, t.e, pol);
@@ -359,8 +374,10 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                         } else {
                             load_3d<kPair>(sa, &tm_a, bar, k, f0, t.e, pol);
                         }
-                        for (int i = 0; i < boxes; ++i)
-                            load_2d<kPair>(sb + i * kBox, &tm_b, bar, k, c0 + i * kRowBox, pol);
+                        if (large) load_2d<kPair>(sb, &tm_b, bar, k, c0, pol);
+                        else
+                            for (int i = 0; i < boxes; ++i)
+                                load_2d<kPair>(sb + i * box, &tm_rows, bar, k, c0 + i * kRowBox, pol);
                     }
                 }
             }
@@ -523,7 +540,7 @@ constexpr int kDevices = 64;
 // Launches on every SM (pairs: every two SMs that can work together), once per
 // kernel and device finding out how many and allowing the shared memory.
 template <int BN, bool kPair, bool kAMn, bool kWeights>
-cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &rows, const Args &a, cudaStream_t s) {
     using C = Cfg<BN, kPair>;
     const auto k = k_grouped_mm<BN, kPair, kAMn, kWeights>;
     static std::atomic<int> ctas[kDevices];
@@ -551,7 +568,23 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, 
         ctas[dev].store(grid, std::memory_order_relaxed);
     }
     cfg.gridDim = dim3((unsigned)grid);
-    return cudaLaunchKernelEx(&cfg, k, ta, tb, a);
+    return cudaLaunchKernelEx(&cfg, k, ta, tb, rows, a);
+}
+
+}  // namespace gm
+
+namespace gm {
+
+template <int BN, bool kPair>
+cudaError_t product(const void *x, int64_t x_stride, const void *w, bool w_kn, const Args &a, int64_t n, cudaStream_t s) {
+    using C = Cfg<BN, kPair>;
+    CUtensorMap ta, tb, rows;
+    const bool ok = (w_kn ? make_map(&ta, w, a.fp16, a.F, a.K, a.F, a.experts, kBK)
+                          : make_map(&ta, w, a.fp16, a.K, a.F, a.K, a.experts, kM)) &&
+                    make_map(&tb, x, a.fp16, a.K, n, x_stride, 0, C::kOwn) &&
+                    make_map(&rows, x, a.fp16, a.K, n, x_stride, 0, kRowBox);
+    if (!ok) return cudaErrorInvalidValue;
+    return w_kn ? launch<BN, kPair, true, false>(ta, tb, rows, a, s) : launch<BN, kPair, false, false>(ta, tb, rows, a, s);
 }
 
 }  // namespace gm
@@ -559,16 +592,10 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, 
 cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bool w_kn, const int32_t *offsets, int64_t n,
                               int experts, int N, int K, bool fp16, void *y, int64_t y_stride, bool y_f32,
                               bool zero_rest, cudaStream_t s) {
-    CUtensorMap ta, tb;
-    const bool ok = (w_kn ? gm::make_map(&ta, w, fp16, N, K, N, experts, gm::kBK)
-                          : gm::make_map(&ta, w, fp16, K, N, K, experts, gm::kM)) &&
-                    gm::make_map(&tb, x, fp16, K, n, x_stride, 0, gm::kRowBox);
-    if (!ok) return cudaErrorInvalidValue;
     const gm::Args a{offsets, experts, n, N, 0, K, y, y_stride, y_f32, fp16, zero_rest};
     // Few rows an expert: narrow row tiles leave room for more stages of weights in flight.
-    if (n <= 32 * (int64_t)experts)
-        return w_kn ? gm::launch<32, false, true, false>(ta, tb, a, s) : gm::launch<32, false, false, false>(ta, tb, a, s);
-    return w_kn ? gm::launch<256, true, true, false>(ta, tb, a, s) : gm::launch<256, true, false, false>(ta, tb, a, s);
+    if (n <= 32 * (int64_t)experts) return gm::product<32, false>(x, x_stride, w, w_kn, a, n, s);
+    return gm::product<256, true>(x, x_stride, w, w_kn, a, n, s);
 }
 
 cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, const void *am, int64_t a_stride, int F,
@@ -578,7 +605,7 @@ cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, co
     if (!gm::make_map(&ta, am, fp16, F, n, a_stride, 0, gm::kBK) || !gm::make_map(&tb, b, fp16, C, n, b_stride, 0, gm::kBK))
         return cudaErrorInvalidValue;
     const gm::Args a{offsets, experts, n, F, C, 0, g_w, F, g_f32, fp16, false};
-    return gm::launch<256, true, true, true>(ta, tb, a, s);
+    return gm::launch<256, true, true, true>(ta, tb, tb, a, s);
 }
 
 cudaError_t consume_grouped_mm_device_error(cudaStream_t s, unsigned int *flag) {
