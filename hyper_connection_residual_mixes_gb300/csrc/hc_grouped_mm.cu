@@ -118,33 +118,50 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
 // complete on the barrier.  (The releasing form waits for everything this thread
 // has in flight, 2,000 cycles a stage, four times a stage's products.)
 __device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+        : "memory");
 }
 // Tensor loads; of a pair the barrier may be the other CTA's.
 template <bool kPair>
 __device__ __forceinline__ void load_2d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, uint64_t policy) {
     if constexpr (kPair)
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
-            " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+            " [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
             : "memory");
     else
-        tma_load_2d(dst, tmap, bar, c0, c1, policy);
+        asm volatile(
+            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+            : "memory");
 }
 template <bool kPair>
 __device__ __forceinline__ void load_3d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, int c2,
                                         uint64_t policy) {
     if constexpr (kPair)
         asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
-            " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
             : "memory");
     else
         asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-            " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
             : "memory");
 }
@@ -328,66 +345,75 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         if (lane == 0) {
             prefetch_tmap(&tm_a);
             prefetch_tmap(&tm_b);
-            const uint64_t pol = policy_evict_normal();
-            int it = 0;
-            for (int tile = worker; tile < tiles && !s_abort; tile += workers) {
-                const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
-                const int nkb = (t.klen + kBK - 1) / kBK;
-                // this CTA's columns of B, and how many boxes each CTA loads
-                const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
-                const int c0 = t.c0 + rank * own, f0 = t.f0 + rank * kM;
-                // (of the product's rows one large box, or small ones where most of it would not count)
-                const bool large = !kWeights && own > C::kOwn / 2;
-                const int boxes = kWeights ? (own + 63) / 64 : large ? 1 : (own + kRowBox - 1) / kRowBox;
-                const int box = kWeights ? 64 * kBK * 2 : large ? C::kBBytes : kRowBox * kBK * 2;
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const int slot = it % S;
-                    if (!mbar_wait<false>(smem_u32(&empty_bar[slot]), ((uint32_t)(it / S) & 1u) ^ 1u, &s_abort)) break;
-                    const uint32_t sa = sbase + (uint32_t)slot * C::kStage, sb = sa + C::kABytes;
-                    const int k = t.k0 + kb * kBK;
-                    const uint32_t bytes = (uint32_t)(C::kABytes + boxes * box);
-                    uint32_t bar = smem_u32(&full_bar[slot]);
-                    if (kPair) {
-                        // both CTAs' bytes are expected at the first one's barrier, unless the
-                        // second one's rows are cleared first
-                        const bool apart = kWeights && rows_to_clear(t.klen - kb * kBK) != 0;
-                        if (rank == 0) {
-                            mbar_arrive_expect_tx(bar, apart ? bytes : 2 * bytes);
-                        } else if (apart) {
-                            bar = smem_u32(&clear_bar[slot]);
-                            mbar_arrive_expect_tx(bar, bytes);
-                        } else {
-                            bar = mapa(bar, 0);
-                            arrive_remote_relaxed(bar);
-                        }
+        }
+        __syncwarp();
+        const uint64_t pol = policy_evict_normal();
+        int slot = 0, issued = 0;
+        uint32_t parity = 1;
+        bool ok = true;
+        for (int tile = worker; tile < tiles && ok; tile += workers) {
+            Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
+            // (one value for the warp: what the issuing thread reads stays in uniform registers)
+            t.klen = __shfl_sync(0xffffffffu, t.klen, 0), t.k0 = __shfl_sync(0xffffffffu, t.k0, 0);
+            t.f0 = __shfl_sync(0xffffffffu, t.f0, 0), t.c0 = __shfl_sync(0xffffffffu, t.c0, 0);
+            t.cols = __shfl_sync(0xffffffffu, t.cols, 0), t.e = __shfl_sync(0xffffffffu, t.e, 0);
+            // this CTA's columns of B, and how many boxes each CTA loads (of the product's
+            // rows one large box, or small ones where most of it would not count)
+            const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
+            const int c0 = t.c0 + rank * own, f0 = t.f0 + rank * kM;
+            const bool large = !kWeights && own > C::kOwn / 2;
+            const int boxes = kWeights ? (own + 63) / 64 : large ? 1 : (own + kRowBox - 1) / kRowBox;
+            const int box = kWeights ? 64 * kBK * 2 : large ? C::kBBytes : kRowBox * kBK * 2;
+            const uint32_t bytes = (uint32_t)(C::kABytes + boxes * box);
+            for (int kb = 0; kb < t.klen; kb += kBK) {
+                if (!(ok = mbar_wait_warp<false>(smem_u32(&empty_bar[slot]), parity, &s_abort))) break;
+                const uint32_t sa = sbase + (uint32_t)slot * C::kStage, sb = sa + C::kABytes;
+                const int k = t.k0 + kb;
+                uint32_t bar = smem_u32(&full_bar[slot]);
+                if (kPair) {
+                    // both CTAs' bytes are expected at the first one's barrier, unless the
+                    // second one's rows are cleared first
+                    const bool apart = kWeights && rows_to_clear(t.klen - kb) != 0;
+                    if (rank == 0) {
+                        expect_bytes(bar, apart ? bytes : 2 * bytes);
+                    } else if (apart) {
+                        bar = smem_u32(&clear_bar[slot]);
+                        expect_bytes(bar, bytes);
                     } else {
-                        mbar_arrive_expect_tx(bar, bytes);
+                        bar = mapa(bar, 0);
+                        arrive_remote_relaxed(bar);
                     }
-                    if (kWeights) {
-                        load_2d<kPair>(sa, &tm_a, bar, f0, k, pol);
-                        load_2d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, pol);
-                        for (int i = 0; i < boxes; ++i) load_2d<kPair>(sb + i * box, &tm_b, bar, c0 + i * 64, k, pol);
-                    } else {
-                        if (kAMn) {
-                            load_3d<kPair>(sa, &tm_a, bar, f0, k, t.e, pol);
-                            load_3d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, t.e, pol);
-                        } else {
-                            load_3d<kPair>(sa, &tm_a, bar, k, f0, t.e, pol);
-                        }
-                        if (large) load_2d<kPair>(sb, &tm_b, bar, k, c0, pol);
-                        else
-                            for (int i = 0; i < boxes; ++i)
-                                load_2d<kPair>(sb + i * box, &tm_rows, bar, k, c0 + i * kRowBox, pol);
-                    }
+                } else {
+                    expect_bytes(bar, bytes);
                 }
-            }
-            // the last stages issued must land before the CTA leaves (of a pair, the
-            // second CTA's land when their MMAs have read them: its empty barriers say so)
-            for (int k = (it > S ? it - S : 0); k < it; ++k) {
-                if (rank == 0) wait_exit(smem_u32(&full_bar[k % S]), (uint32_t)(k / S) & 1u);
-                else wait_exit(smem_u32(&empty_bar[k % S]), (uint32_t)(k / S) & 1u);
+                if (kWeights) {
+                    load_2d<kPair>(sa, &tm_a, bar, f0, k, pol);
+                    load_2d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, pol);
+                    for (int i = 0; i < boxes; ++i) load_2d<kPair>(sb + i * box, &tm_b, bar, c0 + i * 64, k, pol);
+                } else {
+                    if (kAMn) {
+                        load_3d<kPair>(sa, &tm_a, bar, f0, k, t.e, pol);
+                        load_3d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, t.e, pol);
+                    } else {
+                        load_3d<kPair>(sa, &tm_a, bar, k, f0, t.e, pol);
+                    }
+                    if (large) load_2d<kPair>(sb, &tm_b, bar, k, c0, pol);
+                    else
+                        for (int i = 0; i < boxes; ++i)
+                            load_2d<kPair>(sb + i * box, &tm_rows, bar, k, c0 + i * kRowBox, pol);
+                }
+                ++issued;
+                if (++slot == S) slot = 0, parity ^= 1u;
             }
         }
+        // the last stages issued must land before the CTA leaves (of a pair, the second
+        // CTA's have when the MMAs have read them: its empty barriers say so)
+        for (int k = 0; k < S && k < issued; ++k) {
+            if (--slot < 0) slot = S - 1, parity ^= 1u;
+            if (rank == 0) wait_exit(smem_u32(&full_bar[slot]), parity ^ 1u);
+            else wait_exit(smem_u32(&empty_bar[slot]), parity ^ 1u);
+        }
+        __syncwarp();
     } else if (warp == 1 && rank == 0) {
         int c = 0, slot = 0;
         uint32_t parity = 0;
