@@ -36,7 +36,8 @@ namespace hc {
 namespace gm {
 
 constexpr int kM = 128;       // f per tile
-constexpr int kBK = 64;       // k per stage: one 128-byte swizzled row of 16-bit values
+constexpr int kBK = 64;       // k per block: one 128-byte swizzled row of 16-bit values
+constexpr int kSub = 2;       // blocks per stage
 constexpr int kRowBox = 32;   // rows of a small K-major B box (a large one holds a CTA's whole share)
 constexpr int kGroup = 8;     // tiles of c that are walked together
 constexpr int kThreads = 192;
@@ -49,8 +50,12 @@ struct Cfg {
     static constexpr int kTileF = kM * kCtas;           // f of a tile
     static constexpr int kOwn = BN / kCtas;             // columns whose B a CTA holds
     static constexpr int kGrain = 16 * kCtas;           // an MMA's columns come in these
-    static constexpr int kABytes = kM * kBK * 2, kBBytes = kOwn * kBK * 2, kStage = kABytes + kBBytes;
-    static constexpr int kStages = kOwn >= 256 ? 4 : kOwn >= 128 ? 6 : kOwn >= 64 ? 8 : 10;
+    static constexpr int kABytes = kM * kBK * 2, kBBytes = kOwn * kBK * 2, kBlock = kABytes + kBBytes;
+    // A stage, what a barrier stands for, is two blocks of k: waiting for one, fencing and
+    // committing takes the issuing warp some 350 cycles beside 60 an MMA, and four MMAs of
+    // 128 cycles do not cover that.
+    static constexpr int kStage = kSub * kBlock;
+    static constexpr int kStages = kOwn >= 256 ? 2 : kOwn >= 128 ? 3 : kOwn >= 64 ? 4 : 5;
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kSmem = kStages * kStage + 1024 + 3 * (kMaxExperts + 1) * 4;
     static_assert(kSmem <= 227 * 1024 - 512, "shared memory");
@@ -97,6 +102,36 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
             "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
             "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(id),
             "r"(accumulate)
+            : "memory");
+}
+// The four MMAs of a block of 64 of k, their operands kStepA and kStepB (in
+// descriptor units) apart, with one election.
+template <bool kPair, uint32_t kStepA, uint32_t kStepB>
+__device__ __forceinline__ void umma4(uint32_t d, uint64_t a0, uint64_t b0, uint32_t id, uint32_t accumulate) {
+    static_assert(kBK == 64, "four MMAs of 16");
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a, b;\n\t"
+            "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+            "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d), "l"(a0), "l"(b0), "r"(id), "r"(accumulate), "n"(kStepA), "n"(kStepB)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a, b;\n\t"
+            "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+            "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d), "l"(a0), "l"(b0), "r"(id), "r"(accumulate), "n"(kStepA), "n"(kStepB)
             : "memory");
 }
 // One arrival on `bar` (of a pair: of both CTAs) once the MMAs issued so far are done.
@@ -258,10 +293,12 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
     return t;
 }
 
-// Whether a stage of the weights' gradient ends among the rows of 16 that one
-// MMA reads: the rows behind the expert's last, up to the next 16, are another
-// expert's (or anything) and are made zero in both operands before the MMA.
-__device__ __forceinline__ int rows_to_clear(int left) { return left < kBK ? (16 - left % 16) % 16 : 0; }
+// Whether the stage from k0 on ends among the rows of 16 that one MMA of the
+// weights' gradient reads: the rows behind the expert's last, up to the next 16,
+// are another expert's (or anything) and are made zero in both operands first.
+__device__ __forceinline__ int rows_to_clear(int klen, int k0) {
+    return klen - k0 <= kSub * kBK ? (16 - klen % 16) % 16 : 0;
+}
 // ... a warp clears them in `chunks` tiles of 64 columns each from `tiles` on.
 __device__ __forceinline__ void clear_rows(uint32_t tiles, int chunks, int left, int rest, int lane) {
     for (int i = lane; i < chunks * rest * 8; i += 32) {
@@ -365,42 +402,45 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const int boxes = kWeights ? (own + 63) / 64 : large ? 1 : (own + kRowBox - 1) / kRowBox;
             const int box = kWeights ? 64 * kBK * 2 : large ? C::kBBytes : kRowBox * kBK * 2;
             const uint32_t bytes = (uint32_t)(C::kABytes + boxes * box);
-            for (int kb = 0; kb < t.klen; kb += kBK) {
+            for (int k0 = 0; k0 < t.klen; k0 += kSub * kBK) {
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&empty_bar[slot]), parity, &s_abort))) break;
-                const uint32_t sa = sbase + (uint32_t)slot * C::kStage, sb = sa + C::kABytes;
-                const int k = t.k0 + kb;
+                const int blocks = t.klen - k0 > kBK ? kSub : 1;
                 uint32_t bar = smem_u32(&full_bar[slot]);
                 if (kPair) {
                     // both CTAs' bytes are expected at the first one's barrier, unless the
                     // second one's rows are cleared first
-                    const bool apart = kWeights && rows_to_clear(t.klen - kb) != 0;
+                    const bool apart = kWeights && rows_to_clear(t.klen, k0) != 0;
                     if (rank == 0) {
-                        expect_bytes(bar, apart ? bytes : 2 * bytes);
+                        expect_bytes(bar, (apart ? 1 : 2) * blocks * bytes);
                     } else if (apart) {
                         bar = smem_u32(&clear_bar[slot]);
-                        expect_bytes(bar, bytes);
+                        expect_bytes(bar, blocks * bytes);
                     } else {
                         bar = mapa(bar, 0);
                         arrive_remote_relaxed(bar);
                     }
                 } else {
-                    expect_bytes(bar, bytes);
+                    expect_bytes(bar, blocks * bytes);
                 }
-                if (kWeights) {
-                    load_2d<kPair>(sa, &tm_a, bar, f0, k, pol);
-                    load_2d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, pol);
-                    for (int i = 0; i < boxes; ++i) load_2d<kPair>(sb + i * box, &tm_b, bar, c0 + i * 64, k, pol);
-                } else {
-                    if (kAMn) {
-                        load_3d<kPair>(sa, &tm_a, bar, f0, k, t.e, pol);
-                        load_3d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, t.e, pol);
+                for (int s = 0; s < blocks; ++s) {
+                    const uint32_t sa = sbase + (uint32_t)(slot * C::kStage + s * C::kBlock), sb = sa + C::kABytes;
+                    const int k = t.k0 + k0 + s * kBK;
+                    if (kWeights) {
+                        load_2d<kPair>(sa, &tm_a, bar, f0, k, pol);
+                        load_2d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, pol);
+                        for (int i = 0; i < boxes; ++i) load_2d<kPair>(sb + i * box, &tm_b, bar, c0 + i * 64, k, pol);
                     } else {
-                        load_3d<kPair>(sa, &tm_a, bar, k, f0, t.e, pol);
+                        if (kAMn) {
+                            load_3d<kPair>(sa, &tm_a, bar, f0, k, t.e, pol);
+                            load_3d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, t.e, pol);
+                        } else {
+                            load_3d<kPair>(sa, &tm_a, bar, k, f0, t.e, pol);
+                        }
+                        if (large) load_2d<kPair>(sb, &tm_b, bar, k, c0, pol);
+                        else
+                            for (int i = 0; i < boxes; ++i)
+                                load_2d<kPair>(sb + i * box, &tm_rows, bar, k, c0 + i * kRowBox, pol);
                     }
-                    if (large) load_2d<kPair>(sb, &tm_b, bar, k, c0, pol);
-                    else
-                        for (int i = 0; i < boxes; ++i)
-                            load_2d<kPair>(sb + i * box, &tm_rows, bar, k, c0 + i * kRowBox, pol);
                 }
                 ++issued;
                 if (++slot == S) slot = 0, parity ^= 1u;
@@ -432,25 +472,29 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const int n = (cols + C::kGrain - 1) / C::kGrain * C::kGrain;
             const uint32_t id = idesc(a.fp16, kAMn || kWeights, kWeights, C::kTileF, n);
             uint32_t accumulate = 0;
-            for (int left = klen; left > 0; left -= kBK) {
+            for (int k0 = 0; k0 < klen; k0 += kSub * kBK) {
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&full_bar[slot]), parity, &s_abort))) break;
-                if (kWeights && rows_to_clear(left)) {
+                if (kWeights && rows_to_clear(klen, k0)) {
                     // (the second CTA's clearing is seen by an acquire at cluster scope, too slow for every stage)
                     if (kPair) mbar_wait_warp<true>(smem_u32(&full_bar[slot]), parity, &s_abort);
-                    clear_rows(sbase + (uint32_t)slot * C::kStage, 2 + (n / C::kCtas + 63) / 64, left, rows_to_clear(left), lane);
+                    const int at = (klen - k0 - 1) / kBK;
+                    clear_rows(sbase + (uint32_t)(slot * C::kStage + at * C::kBlock), 2 + (n / C::kCtas + 63) / 64,
+                               klen - k0 - at * kBK, rows_to_clear(klen, k0), lane);
                 }
                 tmem_fence_after_sync();
-                const uint64_t da = da0 + (uint32_t)slot * (C::kStage >> 4), db = db0 + (uint32_t)slot * (C::kStage >> 4);
-                if (left >= kBK) {
 #pragma unroll
-                    for (uint32_t ks = 0; ks < kBK / 16; ++ks)
-                        umma<kPair>(d, da + ks * kStepA, db + ks * kStepB, id, ks ? 1u : accumulate);
-                } else {
-                    for (uint32_t ks = 0; ks * 16 < (uint32_t)left; ++ks)
-                        umma<kPair>(d, da + ks * kStepA, db + ks * kStepB, id, ks ? 1u : accumulate);
+                for (int s = 0; s < kSub; ++s) {
+                    const int left = klen - k0 - s * kBK;
+                    const uint32_t at = (uint32_t)(slot * C::kStage + s * C::kBlock) >> 4;
+                    if (left >= kBK) {
+                        umma4<kPair, kStepA, kStepB>(d, da0 + at, db0 + at, id, accumulate);
+                    } else {
+                        for (int ks = 0; ks * 16 < left; ++ks)
+                            umma<kPair>(d, da0 + at + ks * kStepA, db0 + at + ks * kStepB, id, ks ? 1u : accumulate);
+                    }
+                    accumulate = 1;
                 }
                 umma_commit<kPair>(smem_u32(&empty_bar[slot]));
-                accumulate = 1;
                 if (++slot == S) slot = 0, parity ^= 1u;
             }
             if (ok) umma_commit<kPair>(smem_u32(&acc_full[b]));
@@ -470,14 +514,15 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             for (int tile = worker; tile < tiles && ok; tile += workers) {
                 const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
                 if (t.klen == 0) continue;
-                const int nkb = (t.klen + kBK - 1) / kBK, left = t.klen - (nkb - 1) * kBK;
-                it += nkb;
-                if (!rows_to_clear(left)) continue;
+                const int stages = (t.klen + kSub * kBK - 1) / (kSub * kBK), k0 = (stages - 1) * kSub * kBK;
+                it += stages;
+                if (!rows_to_clear(t.klen, k0)) continue;
                 const int slot = (it - 1) % S;
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&clear_bar[slot]), parity >> slot & 1u, &s_abort))) break;
                 parity ^= 1u << slot;
-                const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
-                clear_rows(sbase + (uint32_t)slot * C::kStage, 2 + (own + 63) / 64, left, rows_to_clear(left), lane);
+                const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16, at = (t.klen - k0 - 1) / kBK;
+                clear_rows(sbase + (uint32_t)(slot * C::kStage + at * C::kBlock), 2 + (own + 63) / 64, t.klen - k0 - at * kBK,
+                           rows_to_clear(t.klen, k0), lane);
                 if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&full_bar[slot]), 0));
                 __syncwarp();
             }
