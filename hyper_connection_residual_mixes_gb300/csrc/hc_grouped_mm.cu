@@ -38,7 +38,6 @@ namespace gm {
 constexpr int kM = 128;       // f per tile
 constexpr int kBK = 64;       // k per block: one 128-byte swizzled row of 16-bit values
 constexpr int kSub = 2;       // blocks per stage
-constexpr int kRowBox = 32;   // rows of a small K-major B box (a large one holds a CTA's whole share)
 constexpr int kGroup = 8;     // tiles of c that are walked together
 constexpr int kThreads = 192;
 constexpr int kMaxExperts = 1024;
@@ -50,6 +49,7 @@ struct Cfg {
     static constexpr int kTileF = kM * kCtas;           // f of a tile
     static constexpr int kOwn = BN / kCtas;             // columns whose B a CTA holds
     static constexpr int kGrain = 16 * kCtas;           // an MMA's columns come in these
+    static constexpr int kRowBox = kOwn < 64 ? kOwn : 64;  // rows of a small box of B's (a large one holds kOwn)
     static constexpr int kABytes = kM * kBK * 2, kBBytes = kOwn * kBK * 2, kBlock = kABytes + kBBytes;
     // A stage, what a barrier stands for, is two blocks of k: waiting for one, fencing and
     // committing takes the issuing warp some 350 cycles beside 60 an MMA, and four MMAs of
@@ -69,6 +69,7 @@ struct Args {
     void *out;
     int64_t out_stride; // between consecutive c (product: rows of y; weights': rows of g_w[e])
     int out_f32, fp16, zero_rest;
+    int a_whole, b_whole; // whether an MN-major operand's tensor map takes all of a block's chunks of 64 in one box
 };
 
 // Shared-memory matrix descriptors, 128-byte swizzle.  K-major: rows of 128
@@ -180,6 +181,24 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const void *tmap, uint32_t
             "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
             " [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+            : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void load_4d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, int c2, int c3,
+                                        uint64_t policy) {
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
             : "memory");
 }
 template <bool kPair>
@@ -399,8 +418,9 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
             const int c0 = t.c0 + rank * own, f0 = t.f0 + rank * kM;
             const bool large = !kWeights && own > C::kOwn / 2;
-            const int boxes = kWeights ? (own + 63) / 64 : large ? 1 : (own + kRowBox - 1) / kRowBox;
-            const int box = kWeights ? 64 * kBK * 2 : large ? C::kBBytes : kRowBox * kBK * 2;
+            const bool b_whole = kWeights && a.b_whole && own == C::kOwn;  // (then c0 is a multiple of 64)
+            const int boxes = kWeights ? (own + 63) / 64 : large ? 1 : (own + C::kRowBox - 1) / C::kRowBox;
+            const int box = kWeights ? 64 * kBK * 2 : large ? C::kBBytes : C::kRowBox * kBK * 2;
             const uint32_t bytes = (uint32_t)(C::kABytes + boxes * box);
             for (int k0 = 0; k0 < t.klen; k0 += kSub * kBK) {
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&empty_bar[slot]), parity, &s_abort))) break;
@@ -426,11 +446,19 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     const uint32_t sa = sbase + (uint32_t)(slot * C::kStage + s * C::kBlock), sb = sa + C::kABytes;
                     const int k = t.k0 + k0 + s * kBK;
                     if (kWeights) {
-                        load_2d<kPair>(sa, &tm_a, bar, f0, k, pol);
-                        load_2d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, pol);
-                        for (int i = 0; i < boxes; ++i) load_2d<kPair>(sb + i * box, &tm_b, bar, c0 + i * 64, k, pol);
+                        if (a.a_whole) {
+                            load_3d<kPair>(sa, &tm_a, bar, 0, k, f0 / 64, pol);
+                        } else {
+                            load_2d<kPair>(sa, &tm_a, bar, f0, k, pol);
+                            load_2d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, pol);
+                        }
+                        if (b_whole) load_3d<kPair>(sb, &tm_rows, bar, 0, k, c0 / 64, pol);
+                        else
+                            for (int i = 0; i < boxes; ++i) load_2d<kPair>(sb + i * box, &tm_b, bar, c0 + i * 64, k, pol);
                     } else {
-                        if (kAMn) {
+                        if (kAMn && a.a_whole) {
+                            load_4d<kPair>(sa, &tm_a, bar, 0, k, f0 / 64, t.e, pol);
+                        } else if (kAMn) {
                             load_3d<kPair>(sa, &tm_a, bar, f0, k, t.e, pol);
                             load_3d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, t.e, pol);
                         } else {
@@ -439,7 +467,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                         if (large) load_2d<kPair>(sb, &tm_b, bar, k, c0, pol);
                         else
                             for (int i = 0; i < boxes; ++i)
-                                load_2d<kPair>(sb + i * box, &tm_rows, bar, k, c0 + i * kRowBox, pol);
+                                load_2d<kPair>(sb + i * box, &tm_rows, bar, k, c0 + i * C::kRowBox, pol);
                     }
                 }
                 ++issued;
@@ -592,18 +620,32 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
+bool encode(CUtensorMap *m, const void *base, bool fp16, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
+    const auto enc = encoder();
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return enc && enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+                      const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // A tensor of 16-bit values [d2][d1][d0] (d2 = 0: two axes), rows of d1 `stride1`
 // values apart, boxes of b1 x 64 values, 128-byte swizzle, zeros outside.
 bool make_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, int64_t d1, int64_t stride1, int64_t d2, int b1) {
-    const auto enc = encoder();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
-    cuuint64_t strides[2] = {(cuuint64_t)stride1 * 2, (cuuint64_t)stride1 * (cuuint64_t)d1 * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)b1, 1}, one[3] = {1, 1, 1};
-    return enc(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 ? 3 : 2,
-               const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+    const cuuint64_t strides[2] = {(cuuint64_t)stride1 * 2, (cuuint64_t)stride1 * (cuuint64_t)d1 * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)b1, 1};
+    return encode(m, base, fp16, d2 ? 3 : 2, dims, strides, box);
+}
+// The same with d0, a multiple of 64, as an axis of its own of chunks of 64
+// between d1 and d2: one box is `chunks` tiles of kBK x 64, as an MN-major operand
+// wants them.
+bool make_chunk_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, int64_t d1, int64_t stride1, int64_t d2,
+                    int chunks) {
+    const cuuint64_t dims[4] = {64, (cuuint64_t)d1, (cuuint64_t)d0 / 64, (cuuint64_t)d2};
+    const cuuint64_t strides[3] = {(cuuint64_t)stride1 * 2, 128, (cuuint64_t)stride1 * (cuuint64_t)d1 * 2};
+    const cuuint32_t box[4] = {64, kBK, (cuuint32_t)chunks, 1};
+    return encode(m, base, fp16, d2 ? 4 : 3, dims, strides, box);
 }
 
 constexpr int kDevices = 64;
@@ -647,13 +689,15 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorM
 namespace gm {
 
 template <int BN, bool kPair>
-cudaError_t product(const void *x, int64_t x_stride, const void *w, bool w_kn, const Args &a, int64_t n, cudaStream_t s) {
+cudaError_t product(const void *x, int64_t x_stride, const void *w, bool w_kn, Args a, int64_t n, cudaStream_t s) {
     using C = Cfg<BN, kPair>;
     CUtensorMap ta, tb, rows;
-    const bool ok = (w_kn ? make_map(&ta, w, a.fp16, a.F, a.K, a.F, a.experts, kBK)
-                          : make_map(&ta, w, a.fp16, a.K, a.F, a.K, a.experts, kM)) &&
+    a.a_whole = a.F % 64 == 0;
+    const bool ok = (!w_kn       ? make_map(&ta, w, a.fp16, a.K, a.F, a.K, a.experts, kM)
+                     : a.a_whole ? make_chunk_map(&ta, w, a.fp16, a.F, a.K, a.F, a.experts, kM / 64)
+                                 : make_map(&ta, w, a.fp16, a.F, a.K, a.F, a.experts, kBK)) &&
                     make_map(&tb, x, a.fp16, a.K, n, x_stride, 0, C::kOwn) &&
-                    make_map(&rows, x, a.fp16, a.K, n, x_stride, 0, kRowBox);
+                    make_map(&rows, x, a.fp16, a.K, n, x_stride, 0, C::kRowBox);
     if (!ok) return cudaErrorInvalidValue;
     return w_kn ? launch<BN, kPair, true, false>(ta, tb, rows, a, s) : launch<BN, kPair, false, false>(ta, tb, rows, a, s);
 }
@@ -663,7 +707,7 @@ cudaError_t product(const void *x, int64_t x_stride, const void *w, bool w_kn, c
 cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bool w_kn, const int32_t *offsets, int64_t n,
                               int experts, int N, int K, bool fp16, void *y, int64_t y_stride, bool y_f32,
                               bool zero_rest, cudaStream_t s) {
-    const gm::Args a{offsets, experts, n, N, 0, K, y, y_stride, y_f32, fp16, zero_rest};
+    const gm::Args a{offsets, experts, n, N, 0, K, y, y_stride, y_f32, fp16, zero_rest, 0, 0};
     // Few rows an expert: narrow row tiles leave room for more stages of weights in flight.
     if (n <= 32 * (int64_t)experts) return gm::product<32, false>(x, x_stride, w, w_kn, a, n, s);
     return gm::product<256, true>(x, x_stride, w, w_kn, a, n, s);
@@ -672,11 +716,17 @@ cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bo
 cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, const void *am, int64_t a_stride, int F,
                                       const int32_t *offsets, int64_t n, int experts, bool fp16, void *g_w,
                                       bool g_f32, cudaStream_t s) {
-    CUtensorMap ta, tb;
-    if (!gm::make_map(&ta, am, fp16, F, n, a_stride, 0, gm::kBK) || !gm::make_map(&tb, b, fp16, C, n, b_stride, 0, gm::kBK))
+    using Cf = gm::Cfg<256, true>;
+    CUtensorMap ta, tb, whole;
+    const bool a_whole = F % 64 == 0, b_whole = C % 64 == 0;
+    if (!(a_whole ? gm::make_chunk_map(&ta, am, fp16, F, n, a_stride, 0, gm::kM / 64)
+                  : gm::make_map(&ta, am, fp16, F, n, a_stride, 0, gm::kBK)) ||
+        !gm::make_map(&tb, b, fp16, C, n, b_stride, 0, gm::kBK))
         return cudaErrorInvalidValue;
-    const gm::Args a{offsets, experts, n, F, C, 0, g_w, F, g_f32, fp16, false};
-    return gm::launch<256, true, true, true>(ta, tb, tb, a, s);
+    if (!b_whole) whole = tb;  // (not read)
+    else if (!gm::make_chunk_map(&whole, b, fp16, C, n, b_stride, 0, Cf::kOwn / 64)) return cudaErrorInvalidValue;
+    const gm::Args a{offsets, experts, n, F, C, 0, g_w, F, g_f32, fp16, false, a_whole, b_whole};
+    return gm::launch<256, true, true, true>(ta, tb, whole, a, s);
 }
 
 cudaError_t consume_grouped_mm_device_error(cudaStream_t s, unsigned int *flag) {
