@@ -50,11 +50,11 @@ struct Cfg {
     static constexpr int kOwn = BN / kCtas;             // columns whose B a CTA holds
     static constexpr int kGrain = 16 * kCtas;           // an MMA's columns come in these
     static constexpr int kRowBox = kOwn < 64 ? kOwn : 64;  // rows of a small box of B's (a large one holds kOwn)
-    static constexpr int kABytes = kM * kBK * 2, kBBytes = kOwn * kBK * 2, kBlock = kABytes + kBBytes;
     // A stage, what a barrier stands for, is two blocks of k: waiting for one, fencing and
     // committing takes the issuing warp some 350 cycles beside 60 an MMA, and four MMAs of
-    // 128 cycles do not cover that.
-    static constexpr int kStage = kSub * kBlock;
+    // 128 cycles do not cover that.  Each operand of a stage comes in one box where
+    // the sizes allow it (a box costs the TMA unit some 90 cycles beside its bytes).
+    static constexpr int kABytes = kSub * kM * kBK * 2, kBBytes = kSub * kOwn * kBK * 2, kStage = kABytes + kBBytes;
     static constexpr int kStages = kOwn >= 256 ? 2 : kOwn >= 128 ? 3 : kOwn >= 64 ? 4 : 5;
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kSmem = kStages * kStage + 1024 + 3 * (kMaxExperts + 1) * 4;
@@ -69,15 +69,16 @@ struct Args {
     void *out;
     int64_t out_stride; // between consecutive c (product: rows of y; weights': rows of g_w[e])
     int out_f32, fp16, zero_rest;
-    int a_whole, b_whole; // whether an MN-major operand's tensor map takes all of a block's chunks of 64 in one box
+    int a_whole, b_whole; // whether an operand's stage comes in one box
 };
 
-// Shared-memory matrix descriptors, 128-byte swizzle.  K-major: rows of 128
-// bytes (64 k), 8-row groups 1024 bytes apart, 16 k = 32 bytes.  MN-major: rows of
-// 128 bytes (64 f or c) per k, 8 k = 1024 bytes, the next 64 f or c `chunk`
-// bytes on, 16 k = 2048 bytes.
+// Shared-memory matrix descriptors, 128-byte swizzle.  K-major: a block is rows of
+// 128 bytes (64 k), 8-row groups 1024 bytes apart, 16 k = 32 bytes.  MN-major: a
+// chunk of 64 f or c is rows of 128 bytes per k, 8 k = 1024 bytes, the stage's
+// kSub * kBK of k; the next chunk follows; 16 k = 2048 bytes.
+constexpr int kChunk = kSub * kBK * 128;
 __device__ __forceinline__ uint64_t desc(uint32_t saddr, bool mn_major) {
-    const uint64_t chunk = mn_major ? (kBK * 128) >> 4 : 1;
+    const uint64_t chunk = mn_major ? kChunk >> 4 : 1;
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (chunk << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
            ((uint64_t)2 << 61);
 }
@@ -282,6 +283,13 @@ __device__ __forceinline__ void place_of(int local, int ft, int ct, int &f, int 
     f = rest / w;
     c = g * kGroup + rest - f * w;
 }
+// Bytes between the blocks of a stage's K-major rows: a large box holds a CTA's
+// whole share of a tile's columns, a small one the first rows, where they are all.
+template <int BN, bool kPair>
+__device__ __forceinline__ int row_block(int own) {
+    using C = Cfg<BN, kPair>;
+    return (own > C::kRowBox ? C::kOwn : C::kRowBox) * kBK * 2;
+}
 template <int BN, bool kPair, bool kWeights>
 __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, int &e) {
     while (tile >= p.first[e + 1]) ++e;
@@ -318,11 +326,11 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
 __device__ __forceinline__ int rows_to_clear(int klen, int k0) {
     return klen - k0 <= kSub * kBK ? (16 - klen % 16) % 16 : 0;
 }
-// ... a warp clears them in `chunks` tiles of 64 columns each from `tiles` on.
-__device__ __forceinline__ void clear_rows(uint32_t tiles, int chunks, int left, int rest, int lane) {
+// ... a warp clears them in a stage's `chunks` from `chunk0` on: its rows [left, left + rest).
+__device__ __forceinline__ void clear_rows(uint32_t chunk0, int chunks, int left, int rest, int lane) {
     for (int i = lane; i < chunks * rest * 8; i += 32) {
         const int ch = i / (rest * 8), r = left + i % (rest * 8) / 8;
-        const uint32_t p = tiles + (uint32_t)(ch * 64 * kBK * 2 + r * 128 + (i & 7) * 16);
+        const uint32_t p = chunk0 + (uint32_t)(ch * kChunk + r * 128 + (i & 7) * 16);
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
     }
     fence_proxy_async_smem();
@@ -336,7 +344,7 @@ __device__ __forceinline__ void clear_rows(uint32_t tiles, int chunks, int left,
 template <int BN, bool kPair, bool kAMn, bool kWeights>
 __global__ void __launch_bounds__(kThreads, 1)
 k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-             const __grid_constant__ CUtensorMap tm_rows, const Args a) {
+             const __grid_constant__ CUtensorMap tm_small, const Args a) {
     using C = Cfg<BN, kPair>;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -413,62 +421,56 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             t.klen = __shfl_sync(0xffffffffu, t.klen, 0), t.k0 = __shfl_sync(0xffffffffu, t.k0, 0);
             t.f0 = __shfl_sync(0xffffffffu, t.f0, 0), t.c0 = __shfl_sync(0xffffffffu, t.c0, 0);
             t.cols = __shfl_sync(0xffffffffu, t.cols, 0), t.e = __shfl_sync(0xffffffffu, t.e, 0);
-            // this CTA's columns of B, and how many boxes each CTA loads (of the product's
-            // rows one large box, or small ones where most of it would not count)
+            // this CTA's columns of B
             const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
             const int c0 = t.c0 + rank * own, f0 = t.f0 + rank * kM;
-            const bool large = !kWeights && own > C::kOwn / 2;
-            const bool b_whole = kWeights && a.b_whole && own == C::kOwn;  // (then c0 is a multiple of 64)
-            const int boxes = kWeights ? (own + 63) / 64 : large ? 1 : (own + C::kRowBox - 1) / C::kRowBox;
-            const int box = kWeights ? 64 * kBK * 2 : large ? C::kBBytes : C::kRowBox * kBK * 2;
-            const uint32_t bytes = (uint32_t)(C::kABytes + boxes * box);
+            const int block = row_block<BN, kPair>(own), chunks = (own + 63) / 64;
+            const CUtensorMap *tm_rows = block == C::kOwn * kBK * 2 ? &tm_b : &tm_small;
+            const bool b_whole = a.b_whole && (!kWeights || own == C::kOwn);  // (of the gradient: then c0 % 64 == 0)
+            const uint32_t bytes = (uint32_t)(C::kABytes + (kWeights ? chunks * kChunk : kSub * block));
             for (int k0 = 0; k0 < t.klen; k0 += kSub * kBK) {
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&empty_bar[slot]), parity, &s_abort))) break;
-                const int blocks = t.klen - k0 > kBK ? kSub : 1;
                 uint32_t bar = smem_u32(&full_bar[slot]);
                 if (kPair) {
                     // both CTAs' bytes are expected at the first one's barrier, unless the
                     // second one's rows are cleared first
                     const bool apart = kWeights && rows_to_clear(t.klen, k0) != 0;
                     if (rank == 0) {
-                        expect_bytes(bar, (apart ? 1 : 2) * blocks * bytes);
+                        expect_bytes(bar, (apart ? 1 : 2) * bytes);
                     } else if (apart) {
                         bar = smem_u32(&clear_bar[slot]);
-                        expect_bytes(bar, blocks * bytes);
+                        expect_bytes(bar, bytes);
                     } else {
                         bar = mapa(bar, 0);
                         arrive_remote_relaxed(bar);
                     }
                 } else {
-                    expect_bytes(bar, blocks * bytes);
+                    expect_bytes(bar, bytes);
                 }
-                for (int s = 0; s < blocks; ++s) {
-                    const uint32_t sa = sbase + (uint32_t)(slot * C::kStage + s * C::kBlock), sb = sa + C::kABytes;
-                    const int k = t.k0 + k0 + s * kBK;
-                    if (kWeights) {
-                        if (a.a_whole) {
-                            load_3d<kPair>(sa, &tm_a, bar, 0, k, f0 / 64, pol);
-                        } else {
-                            load_2d<kPair>(sa, &tm_a, bar, f0, k, pol);
-                            load_2d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, pol);
-                        }
-                        if (b_whole) load_3d<kPair>(sb, &tm_rows, bar, 0, k, c0 / 64, pol);
+                const uint32_t sa = sbase + (uint32_t)slot * C::kStage, sb = sa + C::kABytes;
+                const int k = t.k0 + k0;
+                if (kWeights) {
+                    if (a.a_whole) load_3d<kPair>(sa, &tm_a, bar, 0, k, f0 / 64, pol);
+                    else
+                        for (int i = 0; i < kM / 64; ++i) load_2d<kPair>(sa + i * kChunk, &tm_a, bar, f0 + i * 64, k, pol);
+                    if (b_whole) load_3d<kPair>(sb, &tm_b, bar, 0, k, c0 / 64, pol);
+                    else
+                        for (int i = 0; i < chunks; ++i) load_2d<kPair>(sb + i * kChunk, &tm_small, bar, c0 + i * 64, k, pol);
+                } else {
+                    if (kAMn) {
+                        if (a.a_whole) load_4d<kPair>(sa, &tm_a, bar, 0, k, f0 / 64, t.e, pol);
                         else
-                            for (int i = 0; i < boxes; ++i) load_2d<kPair>(sb + i * box, &tm_b, bar, c0 + i * 64, k, pol);
+                            for (int i = 0; i < kM / 64; ++i)
+                                load_3d<kPair>(sa + i * kChunk, &tm_a, bar, f0 + i * 64, k, t.e, pol);
                     } else {
-                        if (kAMn && a.a_whole) {
-                            load_4d<kPair>(sa, &tm_a, bar, 0, k, f0 / 64, t.e, pol);
-                        } else if (kAMn) {
-                            load_3d<kPair>(sa, &tm_a, bar, f0, k, t.e, pol);
-                            load_3d<kPair>(sa + 64 * kBK * 2, &tm_a, bar, f0 + 64, k, t.e, pol);
-                        } else {
-                            load_3d<kPair>(sa, &tm_a, bar, k, f0, t.e, pol);
-                        }
-                        if (large) load_2d<kPair>(sb, &tm_b, bar, k, c0, pol);
+                        if (a.a_whole) load_4d<kPair>(sa, &tm_a, bar, 0, f0, k / kBK, t.e, pol);
                         else
-                            for (int i = 0; i < boxes; ++i)
-                                load_2d<kPair>(sb + i * box, &tm_rows, bar, k, c0 + i * C::kRowBox, pol);
+                            for (int i = 0; i < kSub; ++i)
+                                load_3d<kPair>(sa + i * (kM * kBK * 2), &tm_a, bar, k + i * kBK, f0, t.e, pol);
                     }
+                    if (b_whole) load_3d<kPair>(sb, tm_rows, bar, 0, c0, k / kBK, pol);
+                    else
+                        for (int i = 0; i < kSub; ++i) load_2d<kPair>(sb + i * block, tm_rows, bar, k + i * kBK, c0, pol);
                 }
                 ++issued;
                 if (++slot == S) slot = 0, parity ^= 1u;
@@ -499,26 +501,29 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const uint32_t d = tbase + (uint32_t)(b * BN);
             const int n = (cols + C::kGrain - 1) / C::kGrain * C::kGrain;
             const uint32_t id = idesc(a.fp16, kAMn || kWeights, kWeights, C::kTileF, n);
+            // bytes between the blocks of a stage
+            constexpr int a_block = kAMn || kWeights ? kBK * 128 : kM * kBK * 2;
+            const int b_block = kWeights ? kBK * 128 : row_block<BN, kPair>(n / C::kCtas);
             uint32_t accumulate = 0;
             for (int k0 = 0; k0 < klen; k0 += kSub * kBK) {
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&full_bar[slot]), parity, &s_abort))) break;
                 if (kWeights && rows_to_clear(klen, k0)) {
                     // (the second CTA's clearing is seen by an acquire at cluster scope, too slow for every stage)
                     if (kPair) mbar_wait_warp<true>(smem_u32(&full_bar[slot]), parity, &s_abort);
-                    const int at = (klen - k0 - 1) / kBK;
-                    clear_rows(sbase + (uint32_t)(slot * C::kStage + at * C::kBlock), 2 + (n / C::kCtas + 63) / 64,
-                               klen - k0 - at * kBK, rows_to_clear(klen, k0), lane);
+                    clear_rows(sbase + (uint32_t)slot * C::kStage, kM / 64 + (n / C::kCtas + 63) / 64, klen - k0,
+                               rows_to_clear(klen, k0), lane);
                 }
                 tmem_fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < kSub; ++s) {
                     const int left = klen - k0 - s * kBK;
-                    const uint32_t at = (uint32_t)(slot * C::kStage + s * C::kBlock) >> 4;
+                    const uint64_t da = da0 + (uint32_t)(slot * C::kStage + s * a_block) / 16;
+                    const uint64_t db = db0 + (uint32_t)(slot * C::kStage + s * b_block) / 16;
                     if (left >= kBK) {
-                        umma4<kPair, kStepA, kStepB>(d, da0 + at, db0 + at, id, accumulate);
+                        umma4<kPair, kStepA, kStepB>(d, da, db, id, accumulate);
                     } else {
                         for (int ks = 0; ks * 16 < left; ++ks)
-                            umma<kPair>(d, da0 + at + ks * kStepA, db0 + at + ks * kStepB, id, ks ? 1u : accumulate);
+                            umma<kPair>(d, da + ks * kStepA, db + ks * kStepB, id, ks ? 1u : accumulate);
                     }
                     accumulate = 1;
                 }
@@ -548,9 +553,9 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 const int slot = (it - 1) % S;
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&clear_bar[slot]), parity >> slot & 1u, &s_abort))) break;
                 parity ^= 1u << slot;
-                const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16, at = (t.klen - k0 - 1) / kBK;
-                clear_rows(sbase + (uint32_t)(slot * C::kStage + at * C::kBlock), 2 + (own + 63) / 64, t.klen - k0 - at * kBK,
-                           rows_to_clear(t.klen, k0), lane);
+                const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
+                clear_rows(sbase + (uint32_t)slot * C::kStage, kM / 64 + (own + 63) / 64, t.klen - k0, rows_to_clear(t.klen, k0),
+                           lane);
                 if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&full_bar[slot]), 0));
                 __syncwarp();
             }
@@ -638,14 +643,20 @@ bool make_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, int64_t d
     return encode(m, base, fp16, d2 ? 3 : 2, dims, strides, box);
 }
 // The same with d0, a multiple of 64, as an axis of its own of chunks of 64
-// between d1 and d2: one box is `chunks` tiles of kBK x 64, as an MN-major operand
-// wants them.
+// between d1 and d2: one box is `chunks` tiles of b1 x 64, one after the other.
 bool make_chunk_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, int64_t d1, int64_t stride1, int64_t d2,
-                    int chunks) {
+                    int b1, int chunks) {
     const cuuint64_t dims[4] = {64, (cuuint64_t)d1, (cuuint64_t)d0 / 64, (cuuint64_t)d2};
     const cuuint64_t strides[3] = {(cuuint64_t)stride1 * 2, 128, (cuuint64_t)stride1 * (cuuint64_t)d1 * 2};
-    const cuuint32_t box[4] = {64, kBK, (cuuint32_t)chunks, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)b1, (cuuint32_t)chunks, 1};
     return encode(m, base, fp16, d2 ? 4 : 3, dims, strides, box);
+}
+// One box a stage where d0 is a multiple of 64 (*whole), else boxes of 64 columns.
+bool make_operand_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, int64_t d1, int64_t stride1, int64_t d2,
+                      int b1, int chunks, int *whole) {
+    *whole = d0 % 64 == 0;
+    return *whole ? make_chunk_map(m, base, fp16, d0, d1, stride1, d2, b1, chunks)
+                  : make_map(m, base, fp16, d0, d1, stride1, d2, b1);
 }
 
 constexpr int kDevices = 64;
@@ -653,7 +664,7 @@ constexpr int kDevices = 64;
 // Launches on every SM (pairs: every two SMs that can work together), once per
 // kernel and device finding out how many and allowing the shared memory.
 template <int BN, bool kPair, bool kAMn, bool kWeights>
-cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &rows, const Args &a, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &small, const Args &a, cudaStream_t s) {
     using C = Cfg<BN, kPair>;
     const auto k = k_grouped_mm<BN, kPair, kAMn, kWeights>;
     static std::atomic<int> ctas[kDevices];
@@ -681,7 +692,7 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorM
         ctas[dev].store(grid, std::memory_order_relaxed);
     }
     cfg.gridDim = dim3((unsigned)grid);
-    return cudaLaunchKernelEx(&cfg, k, ta, tb, rows, a);
+    return cudaLaunchKernelEx(&cfg, k, ta, tb, small, a);
 }
 
 }  // namespace gm
@@ -691,15 +702,13 @@ namespace gm {
 template <int BN, bool kPair>
 cudaError_t product(const void *x, int64_t x_stride, const void *w, bool w_kn, Args a, int64_t n, cudaStream_t s) {
     using C = Cfg<BN, kPair>;
-    CUtensorMap ta, tb, rows;
-    a.a_whole = a.F % 64 == 0;
-    const bool ok = (!w_kn       ? make_map(&ta, w, a.fp16, a.K, a.F, a.K, a.experts, kM)
-                     : a.a_whole ? make_chunk_map(&ta, w, a.fp16, a.F, a.K, a.F, a.experts, kM / 64)
-                                 : make_map(&ta, w, a.fp16, a.F, a.K, a.F, a.experts, kBK)) &&
-                    make_map(&tb, x, a.fp16, a.K, n, x_stride, 0, C::kOwn) &&
-                    make_map(&rows, x, a.fp16, a.K, n, x_stride, 0, C::kRowBox);
+    CUtensorMap ta, tb, small;
+    const bool ok = (w_kn ? make_operand_map(&ta, w, a.fp16, a.F, a.K, a.F, a.experts, kSub * kBK, kM / 64, &a.a_whole)
+                          : make_operand_map(&ta, w, a.fp16, a.K, a.F, a.K, a.experts, kM, kSub, &a.a_whole)) &&
+                    make_operand_map(&tb, x, a.fp16, a.K, n, x_stride, 0, C::kOwn, kSub, &a.b_whole) &&
+                    make_operand_map(&small, x, a.fp16, a.K, n, x_stride, 0, C::kRowBox, kSub, &a.b_whole);
     if (!ok) return cudaErrorInvalidValue;
-    return w_kn ? launch<BN, kPair, true, false>(ta, tb, rows, a, s) : launch<BN, kPair, false, false>(ta, tb, rows, a, s);
+    return w_kn ? launch<BN, kPair, true, false>(ta, tb, small, a, s) : launch<BN, kPair, false, false>(ta, tb, small, a, s);
 }
 
 }  // namespace gm
@@ -717,16 +726,14 @@ cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, co
                                       const int32_t *offsets, int64_t n, int experts, bool fp16, void *g_w,
                                       bool g_f32, cudaStream_t s) {
     using Cf = gm::Cfg<256, true>;
-    CUtensorMap ta, tb, whole;
-    const bool a_whole = F % 64 == 0, b_whole = C % 64 == 0;
-    if (!(a_whole ? gm::make_chunk_map(&ta, am, fp16, F, n, a_stride, 0, gm::kM / 64)
-                  : gm::make_map(&ta, am, fp16, F, n, a_stride, 0, gm::kBK)) ||
-        !gm::make_map(&tb, b, fp16, C, n, b_stride, 0, gm::kBK))
+    CUtensorMap ta, tb, chunk;
+    gm::Args a{offsets, experts, n, F, C, 0, g_w, F, g_f32, fp16, false, 0, 0};
+    constexpr int rows = gm::kSub * gm::kBK;
+    if (!gm::make_operand_map(&ta, am, fp16, F, n, a_stride, 0, rows, gm::kM / 64, &a.a_whole) ||
+        !gm::make_operand_map(&tb, b, fp16, C, n, b_stride, 0, rows, Cf::kOwn / 64, &a.b_whole) ||
+        !gm::make_map(&chunk, b, fp16, C, n, b_stride, 0, rows))
         return cudaErrorInvalidValue;
-    if (!b_whole) whole = tb;  // (not read)
-    else if (!gm::make_chunk_map(&whole, b, fp16, C, n, b_stride, 0, Cf::kOwn / 64)) return cudaErrorInvalidValue;
-    const gm::Args a{offsets, experts, n, F, C, 0, g_w, F, g_f32, fp16, false, a_whole, b_whole};
-    return gm::launch<256, true, true, true>(ta, tb, whole, a, s);
+    return gm::launch<256, true, true, true>(ta, tb, chunk, a, s);
 }
 
 cudaError_t consume_grouped_mm_device_error(cudaStream_t s, unsigned int *flag) {
