@@ -15,7 +15,8 @@
 // the device, so the host never waits for the router.
 //
 // One CTA per SM walks the tiles (warp 0 loads by TMA, warp 1 issues
-// tcgen05.mma, warps 2-5 write finished tiles); two accumulators alternate, so
+// tcgen05.mma, warps 2-5 write finished tiles, warp 6 clears the rows behind an
+// expert's last one in the gradient's operands); two accumulators alternate, so
 // that a tile is written while the next one's products run.  Where the tiles are
 // large two CTAs work on one (cta_group::2: 256 of f, each CTA with half of A's
 // rows and half of B's columns in its shared memory), because one SM's MMA of
@@ -30,6 +31,7 @@
 
 #include "hc_ptx.cuh"
 #include "hc_sublayer.h"
+#include "hc_types.cuh"
 
 namespace hc {
 
@@ -39,7 +41,7 @@ constexpr int kM = 128;       // f per tile
 constexpr int kBK = 64;       // k per block: one 128-byte swizzled row of 16-bit values
 constexpr int kSub = 2;       // blocks per stage
 constexpr int kGroup = 8;     // tiles of c that are walked together
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kMaxExperts = 1024;
 constexpr unsigned int kErrOffsets = 2u;  // device error bit: offsets out of order or out of range
 
@@ -238,15 +240,13 @@ __device__ __forceinline__ void tmem_give_back(uint32_t taddr, uint32_t ncols) {
     else
         tmem_dealloc(taddr, ncols);
 }
-// 16 columns of this lane, waited for in the same statement (no register copy
+// 32 columns of this lane, waited for in the same statement (no register copy
 // can slip between the load and the wait).
-__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t (&v)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(t)
         : "memory");
 }
@@ -264,6 +264,29 @@ __device__ __forceinline__ void put(void *out, int64_t i, float v, int f32, int 
     if (f32) static_cast<float *>(out)[i] = v;
     else if (fp16) static_cast<__half *>(out)[i] = __float2half_rn(v);
     else static_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
+}
+
+// 32 columns of a tile, `step` bytes apart in memory: column j of this lane's f at
+// o + j * step, those below `cols`.  16-bit outputs in pairs of f where every pair
+// is aligned: neighbouring lanes trade a column, so that each stores two f of one.
+template <typename T>
+__device__ __forceinline__ void put32(uint8_t *o, int64_t step, const uint32_t (&v)[32], int cols, bool in) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j, o += step)
+        if (in && j < cols) *reinterpret_cast<T *>(o) = from_f<T>(__uint_as_float(v[j]));
+}
+template <typename T>
+__device__ __forceinline__ void put32_paired(uint8_t *o, int64_t step, const uint32_t (&v)[32], int cols, bool in, int lane) {
+    const bool odd = lane & 1;
+    if (odd) o += step - 2;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2, o += 2 * step) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+        Vec<T, 2> p;
+        put_pair(p, 0, odd ? f2_make(__uint_as_float(got), __uint_as_float(v[j + 1]))
+                           : f2_make(__uint_as_float(v[j]), __uint_as_float(got)));
+        if (in && j + odd < cols) *reinterpret_cast<Vec<T, 2> *>(o) = p;
+    }
 }
 
 // The experts' row ranges and tiles, in shared memory.
@@ -320,6 +343,12 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
     return t;
 }
 
+// Where the i-th stage of `stages` starts.  The gradient begins with an expert's
+// last rows: their clearing then runs while the tile before is still multiplied.
+template <bool kWeights>
+__device__ __forceinline__ int stage_start(int i, int stages) {
+    return kSub * kBK * (!kWeights ? i : i == 0 ? stages - 1 : i - 1);
+}
 // Whether the stage from k0 on ends among the rows of 16 that one MMA of the
 // weights' gradient reads: the rows behind the expert's last, up to the next 16,
 // are another expert's (or anything) and are made zero in both operands first.
@@ -352,7 +381,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     int *const s_start = reinterpret_cast<int *>(smem_raw + (sbase - smem_u32(smem_raw)) + S * C::kStage);
     int *const s_end = s_start + kMaxExperts, *const s_first = s_end + kMaxExperts;
     __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], acc_full[2], acc_empty[2], done_bar;
-    __shared__ __align__(8) uint64_t clear_bar[kPair && kWeights ? S : 1];  // the second CTA's loads of a stage to clear
+    __shared__ __align__(8) uint64_t clear_bar[kWeights ? S : 1];  // this CTA's loads of a stage to clear
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -362,7 +391,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) mbar_init(smem_u32(&full_bar[s]), C::kCtas), mbar_init(smem_u32(&empty_bar[s]), 1);
         for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&acc_full[b]), 1), mbar_init(smem_u32(&acc_empty[b]), 4 * C::kCtas);
-        if (kPair && kWeights)
+        if (kWeights)
             for (int s = 0; s < S; ++s) mbar_init(smem_u32(&clear_bar[s]), 1);
         mbar_init(smem_u32(&done_bar), 1);
         s_abort = 0;
@@ -428,24 +457,20 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const CUtensorMap *tm_rows = block == C::kOwn * kBK * 2 ? &tm_b : &tm_small;
             const bool b_whole = a.b_whole && (!kWeights || own == C::kOwn);  // (of the gradient: then c0 % 64 == 0)
             const uint32_t bytes = (uint32_t)(C::kABytes + (kWeights ? chunks * kChunk : kSub * block));
-            for (int k0 = 0; k0 < t.klen; k0 += kSub * kBK) {
+            const int stages = (t.klen + kSub * kBK - 1) / (kSub * kBK);
+            for (int i = 0; i < stages; ++i) {
+                const int k0 = stage_start<kWeights>(i, stages);
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&empty_bar[slot]), parity, &s_abort))) break;
                 uint32_t bar = smem_u32(&full_bar[slot]);
-                if (kPair) {
-                    // both CTAs' bytes are expected at the first one's barrier, unless the
-                    // second one's rows are cleared first
-                    const bool apart = kWeights && rows_to_clear(t.klen, k0) != 0;
-                    if (rank == 0) {
-                        expect_bytes(bar, (apart ? 1 : 2) * bytes);
-                    } else if (apart) {
-                        bar = smem_u32(&clear_bar[slot]);
-                        expect_bytes(bar, bytes);
-                    } else {
-                        bar = mapa(bar, 0);
-                        arrive_remote_relaxed(bar);
-                    }
-                } else {
+                if (kWeights && rows_to_clear(t.klen, k0)) {
+                    // the clearing warp passes the stage on to the (first CTA's) full barrier
+                    bar = smem_u32(&clear_bar[slot]);
                     expect_bytes(bar, bytes);
+                } else if (rank == 0) {
+                    expect_bytes(bar, C::kCtas * bytes);  // of a pair both CTAs' bytes
+                } else {
+                    bar = mapa(bar, 0);
+                    arrive_remote_relaxed(bar);
                 }
                 const uint32_t sa = sbase + (uint32_t)slot * C::kStage, sb = sa + C::kABytes;
                 const int k = t.k0 + k0;
@@ -505,14 +530,15 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             constexpr int a_block = kAMn || kWeights ? kBK * 128 : kM * kBK * 2;
             const int b_block = kWeights ? kBK * 128 : row_block<BN, kPair>(n / C::kCtas);
             uint32_t accumulate = 0;
-            for (int k0 = 0; k0 < klen; k0 += kSub * kBK) {
-                if (!(ok = mbar_wait_warp<false>(smem_u32(&full_bar[slot]), parity, &s_abort))) break;
-                if (kWeights && rows_to_clear(klen, k0)) {
-                    // (the second CTA's clearing is seen by an acquire at cluster scope, too slow for every stage)
-                    if (kPair) mbar_wait_warp<true>(smem_u32(&full_bar[slot]), parity, &s_abort);
-                    clear_rows(sbase + (uint32_t)slot * C::kStage, kM / 64 + (n / C::kCtas + 63) / 64, klen - k0,
-                               rows_to_clear(klen, k0), lane);
-                }
+            const int stages = (klen + kSub * kBK - 1) / (kSub * kBK);
+            for (int i = 0; i < stages; ++i) {
+                const int k0 = stage_start<kWeights>(i, stages);
+                // (the second CTA's clearing is seen by an acquire at cluster scope, too slow for every stage)
+                if (kPair && kWeights && rows_to_clear(klen, k0))
+                    ok = mbar_wait_warp<true>(smem_u32(&full_bar[slot]), parity, &s_abort);
+                else
+                    ok = mbar_wait_warp<false>(smem_u32(&full_bar[slot]), parity, &s_abort);
+                if (!ok) break;
                 tmem_fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < kSub; ++s) {
@@ -537,32 +563,34 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         umma_commit<kPair>(smem_u32(&done_bar));
         wait_exit(smem_u32(&done_bar), 0u);
         __syncwarp();
-    } else if (warp == 1) {
-        // the second CTA of a pair: clears the rows of a gradient's last stages in its
-        // own tiles, then tells the first CTA that the stage is ready
-        if constexpr (kPair && kWeights) {
-            int it = 0;
+    } else if (warp == 6) {
+        if constexpr (kWeights) {
+            int uses = 0;  // stages of the tiles before
             uint32_t parity = 0;
             bool ok = true;
             for (int tile = worker; tile < tiles && ok; tile += workers) {
                 const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
-                if (t.klen == 0) continue;
-                const int stages = (t.klen + kSub * kBK - 1) / (kSub * kBK), k0 = (stages - 1) * kSub * kBK;
-                it += stages;
-                if (!rows_to_clear(t.klen, k0)) continue;
-                const int slot = (it - 1) % S;
+                const int stages = (t.klen + kSub * kBK - 1) / (kSub * kBK);
+                const int slot = uses % S, k0 = stage_start<kWeights>(0, stages);
+                uses += stages;
+                if (stages == 0 || !rows_to_clear(t.klen, k0)) continue;
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&clear_bar[slot]), parity >> slot & 1u, &s_abort))) break;
                 parity ^= 1u << slot;
                 const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
                 clear_rows(sbase + (uint32_t)slot * C::kStage, kM / 64 + (own + 63) / 64, t.klen - k0, rows_to_clear(t.klen, k0),
                            lane);
-                if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&full_bar[slot]), 0));
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(smem_u32(&full_bar[slot]));
+                    else mbar_arrive_remote(mapa(smem_u32(&full_bar[slot]), 0));
+                }
                 __syncwarp();
             }
         }
-    } else {
+    } else if (warp >= 2) {
         const int q = warp & 3;  // the warp's quadrant of tensor-memory lanes
         const int64_t esize = a.out_f32 ? 4 : 2;
+        // (F is a multiple of 8, so pairs end with a row)
+        const bool paired = a.out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
         if (!kWeights && a.zero_rest) {
             // rows of no expert: before offsets[0] and from offsets[experts] on
             int64_t lo = __ldg(a.offsets), hi = __ldg(a.offsets + a.experts);
@@ -590,12 +618,13 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             if (!mbar_wait_warp<false>(smem_u32(&acc_full[b]), (uint32_t)(c >> 1) & 1u, &s_abort)) break;
             tmem_fence_after_sync();
             const uint32_t ta = tbase + (uint32_t)(b * BN) + ((uint32_t)(32 * q) << 16);
-            for (int j0 = 0; j0 < t.cols; j0 += 16) {
-                uint32_t v[16];
-                tmem_ld16(ta + (uint32_t)j0, v);
-#pragma unroll
-                for (int j = 0; j < 16; ++j, o += step)
-                    if (in && j0 + j < t.cols) put(o, 0, __uint_as_float(v[j]), a.out_f32, a.fp16);
+            for (int j0 = 0; j0 < t.cols; j0 += 32, o += 32 * step) {
+                uint32_t v[32];
+                tmem_ld32(ta + (uint32_t)j0, v);
+                if (a.out_f32) put32<float>(o, step, v, t.cols - j0, in);
+                else if (!paired) a.fp16 ? put32<__half>(o, step, v, t.cols - j0, in) : put32<__nv_bfloat16>(o, step, v, t.cols - j0, in);
+                else if (a.fp16) put32_paired<__half>(o, step, v, t.cols - j0, in, lane);
+                else put32_paired<__nv_bfloat16>(o, step, v, t.cols - j0, in, lane);
             }
             tmem_fence_before_sync();
             __syncwarp();
