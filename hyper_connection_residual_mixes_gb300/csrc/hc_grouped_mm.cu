@@ -52,10 +52,12 @@ struct Cfg {
     static constexpr int kOwn = BN / kCtas;             // columns whose B a CTA holds
     static constexpr int kGrain = 16 * kCtas;           // an MMA's columns come in these
     static constexpr int kRowBox = kOwn < 64 ? kOwn : 64;  // rows of a small box of B's (a large one holds kOwn)
-    // A stage, what a barrier stands for, is two blocks of k: waiting for one, fencing and
-    // committing takes the issuing warp some 350 cycles beside 60 an MMA, and four MMAs of
-    // 128 cycles do not cover that.  Each operand of a stage comes in one box where
-    // the sizes allow it (a box costs the TMA unit some 90 cycles beside its bytes).
+    // A stage, what a full barrier stands for, is two blocks of k: waiting for one and
+    // fencing takes the issuing warp some 300 cycles beside 60 an MMA, and four MMAs of 128
+    // cycles do not cover that.  Its blocks are handed back one by one.  K-major
+    // operands are loaded block by block as they come free, so that five of six are on
+    // their way while one is multiplied; MN-major ones a stage at a time, because boxes
+    // of 64 k load a fifth slower than boxes of 128 (both gradients 500 us against 455).
     static constexpr int kABytes = kSub * kM * kBK * 2, kBBytes = kSub * kOwn * kBK * 2, kStage = kABytes + kBBytes;
     static constexpr int kStages = kOwn >= 256 ? 2 : kOwn >= 128 ? 3 : kOwn >= 64 ? 4 : 5;
     static constexpr int kTmemCols = 2 * BN;
@@ -71,7 +73,7 @@ struct Args {
     void *out;
     int64_t out_stride; // between consecutive c (product: rows of y; weights': rows of g_w[e])
     int out_f32, fp16, zero_rest;
-    int a_whole, b_whole; // whether an operand's stage comes in one box
+    int a_whole, b_whole; // whether an MN-major operand's stage comes in one box
 };
 
 // Shared-memory matrix descriptors, 128-byte swizzle.  K-major: a block is rows of
@@ -380,7 +382,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     int *const s_start = reinterpret_cast<int *>(smem_raw + (sbase - smem_u32(smem_raw)) + S * C::kStage);
     int *const s_end = s_start + kMaxExperts, *const s_first = s_end + kMaxExperts;
-    __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], acc_full[2], acc_empty[2], done_bar;
+    __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S * kSub], acc_full[2], acc_empty[2], done_bar;
     __shared__ __align__(8) uint64_t clear_bar[kWeights ? S : 1];  // this CTA's loads of a stage to clear
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
@@ -389,7 +391,8 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const int worker = kPair ? (int)blockIdx.x >> 1 : (int)blockIdx.x, workers = kPair ? (int)gridDim.x >> 1 : (int)gridDim.x;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(smem_u32(&full_bar[s]), C::kCtas), mbar_init(smem_u32(&empty_bar[s]), 1);
+        for (int s = 0; s < S; ++s) mbar_init(smem_u32(&full_bar[s]), C::kCtas);
+        for (int s = 0; s < S * kSub; ++s) mbar_init(smem_u32(&empty_bar[s]), 1);
         for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&acc_full[b]), 1), mbar_init(smem_u32(&acc_empty[b]), 4 * C::kCtas);
         if (kWeights)
             for (int s = 0; s < S; ++s) mbar_init(smem_u32(&clear_bar[s]), 1);
@@ -455,49 +458,49 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const int c0 = t.c0 + rank * own, f0 = t.f0 + rank * kM;
             const int block = row_block<BN, kPair>(own), chunks = (own + 63) / 64;
             const CUtensorMap *tm_rows = block == C::kOwn * kBK * 2 ? &tm_b : &tm_small;
-            const bool b_whole = a.b_whole && (!kWeights || own == C::kOwn);  // (of the gradient: then c0 % 64 == 0)
-            const uint32_t bytes = (uint32_t)(C::kABytes + (kWeights ? chunks * kChunk : kSub * block));
+            const bool b_whole = kWeights && a.b_whole && own == C::kOwn;  // (then c0 is a multiple of 64)
+            constexpr bool kByStage = kAMn || kWeights;
+            // bytes of a block (of an MN-major operand: of half a stage)
+            const uint32_t bytes = (uint32_t)(kM * kBK * 2 + (kWeights ? chunks * kChunk / 2 : block));
             const int stages = (t.klen + kSub * kBK - 1) / (kSub * kBK);
-            for (int i = 0; i < stages; ++i) {
+            for (int i = 0; i < stages && ok; ++i) {
                 const int k0 = stage_start<kWeights>(i, stages);
-                if (!(ok = mbar_wait_warp<false>(smem_u32(&empty_bar[slot]), parity, &s_abort))) break;
-                uint32_t bar = smem_u32(&full_bar[slot]);
-                if (kWeights && rows_to_clear(t.klen, k0)) {
-                    // the clearing warp passes the stage on to the (first CTA's) full barrier
-                    bar = smem_u32(&clear_bar[slot]);
-                    expect_bytes(bar, bytes);
-                } else if (rank == 0) {
-                    expect_bytes(bar, C::kCtas * bytes);  // of a pair both CTAs' bytes
-                } else {
-                    bar = mapa(bar, 0);
-                    arrive_remote_relaxed(bar);
-                }
+                const int blocks = kByStage || t.klen - k0 > kBK ? kSub : 1;
                 const uint32_t sa = sbase + (uint32_t)slot * C::kStage, sb = sa + C::kABytes;
+                uint32_t bar = smem_u32(&full_bar[slot]);
                 const int k = t.k0 + k0;
-                if (kWeights) {
-                    if (a.a_whole) load_3d<kPair>(sa, &tm_a, bar, 0, k, f0 / 64, pol);
-                    else
-                        for (int i = 0; i < kM / 64; ++i) load_2d<kPair>(sa + i * kChunk, &tm_a, bar, f0 + i * 64, k, pol);
-                    if (b_whole) load_3d<kPair>(sb, &tm_b, bar, 0, k, c0 / 64, pol);
-                    else
-                        for (int i = 0; i < chunks; ++i) load_2d<kPair>(sb + i * kChunk, &tm_small, bar, c0 + i * 64, k, pol);
-                } else {
-                    if (kAMn) {
-                        if (a.a_whole) load_4d<kPair>(sa, &tm_a, bar, 0, k, f0 / 64, t.e, pol);
-                        else
-                            for (int i = 0; i < kM / 64; ++i)
-                                load_3d<kPair>(sa + i * kChunk, &tm_a, bar, f0 + i * 64, k, t.e, pol);
-                    } else {
-                        if (a.a_whole) load_4d<kPair>(sa, &tm_a, bar, 0, f0, k / kBK, t.e, pol);
-                        else
-                            for (int i = 0; i < kSub; ++i)
-                                load_3d<kPair>(sa + i * (kM * kBK * 2), &tm_a, bar, k + i * kBK, f0, t.e, pol);
+                for (int s = 0; s < blocks; ++s) {
+                    if (!(ok = mbar_wait_warp<false>(smem_u32(&empty_bar[slot * kSub + s]), parity, &s_abort))) break;
+                    if (s == 0) {
+                        if (kWeights && rows_to_clear(t.klen, k0)) {
+                            // the clearing warp passes the stage on to the (first CTA's) full barrier
+                            bar = smem_u32(&clear_bar[slot]);
+                            expect_bytes(bar, blocks * bytes);
+                        } else if (rank == 0) {
+                            expect_bytes(bar, C::kCtas * blocks * bytes);  // of a pair both CTAs' bytes
+                        } else {
+                            bar = mapa(bar, 0);
+                            arrive_remote_relaxed(bar);
+                        }
+                        ++issued;
                     }
-                    if (b_whole) load_3d<kPair>(sb, tm_rows, bar, 0, c0, k / kBK, pol);
-                    else
-                        for (int i = 0; i < kSub; ++i) load_2d<kPair>(sb + i * block, tm_rows, bar, k + i * kBK, c0, pol);
+                    if (!kByStage) load_3d<kPair>(sa + s * (kM * kBK * 2), &tm_a, bar, k + s * kBK, f0, t.e, pol);
+                    if (!kWeights) load_2d<kPair>(sb + s * block, tm_rows, bar, k + s * kBK, c0, pol);
                 }
-                ++issued;
+                if (kByStage && ok) {
+                    if (kWeights) {
+                        if (a.a_whole) load_3d<kPair>(sa, &tm_a, bar, 0, k, f0 / 64, pol);
+                        else
+                            for (int j = 0; j < kM / 64; ++j) load_2d<kPair>(sa + j * kChunk, &tm_a, bar, f0 + j * 64, k, pol);
+                        if (b_whole) load_3d<kPair>(sb, &tm_b, bar, 0, k, c0 / 64, pol);
+                        else
+                            for (int j = 0; j < chunks; ++j) load_2d<kPair>(sb + j * kChunk, &tm_small, bar, c0 + j * 64, k, pol);
+                    } else if (a.a_whole) {
+                        load_4d<kPair>(sa, &tm_a, bar, 0, k, f0 / 64, t.e, pol);
+                    } else {
+                        for (int j = 0; j < kM / 64; ++j) load_3d<kPair>(sa + j * kChunk, &tm_a, bar, f0 + j * 64, k, t.e, pol);
+                    }
+                }
                 if (++slot == S) slot = 0, parity ^= 1u;
             }
         }
@@ -506,7 +509,8 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         for (int k = 0; k < S && k < issued; ++k) {
             if (--slot < 0) slot = S - 1, parity ^= 1u;
             if (rank == 0) wait_exit(smem_u32(&full_bar[slot]), parity ^ 1u);
-            else wait_exit(smem_u32(&empty_bar[slot]), parity ^ 1u);
+            else
+                for (int s = 0; s < kSub; ++s) wait_exit(smem_u32(&empty_bar[slot * kSub + s]), parity ^ 1u);
         }
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
@@ -552,8 +556,9 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                             umma<kPair>(d, da + ks * kStepA, db + ks * kStepB, id, ks ? 1u : accumulate);
                     }
                     accumulate = 1;
+                    // (also of a block that a last stage does not have, so that all barriers keep step)
+                    umma_commit<kPair>(smem_u32(&empty_bar[slot * kSub + s]));
                 }
-                umma_commit<kPair>(smem_u32(&empty_bar[slot]));
                 if (++slot == S) slot = 0, parity ^= 1u;
             }
             if (ok) umma_commit<kPair>(smem_u32(&acc_full[b]));
@@ -671,21 +676,17 @@ bool make_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, int64_t d
     const cuuint32_t box[3] = {64, (cuuint32_t)b1, 1};
     return encode(m, base, fp16, d2 ? 3 : 2, dims, strides, box);
 }
-// The same with d0, a multiple of 64, as an axis of its own of chunks of 64
-// between d1 and d2: one box is `chunks` tiles of b1 x 64, one after the other.
-bool make_chunk_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, int64_t d1, int64_t stride1, int64_t d2,
-                    int b1, int chunks) {
+// An MN-major operand.  With d0 a multiple of 64 (*whole) it is an axis of its own of
+// chunks of 64 between d1 and d2, and one box is a stage's `chunks` tiles of 64
+// values by kSub * kBK of k, one after the other; else one box is one such tile.
+bool make_operand_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, int64_t d1, int64_t stride1, int64_t d2,
+                      int chunks, int *whole) {
+    *whole = d0 % 64 == 0;
+    if (!*whole) return make_map(m, base, fp16, d0, d1, stride1, d2, kSub * kBK);
     const cuuint64_t dims[4] = {64, (cuuint64_t)d1, (cuuint64_t)d0 / 64, (cuuint64_t)d2};
     const cuuint64_t strides[3] = {(cuuint64_t)stride1 * 2, 128, (cuuint64_t)stride1 * (cuuint64_t)d1 * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)b1, (cuuint32_t)chunks, 1};
+    const cuuint32_t box[4] = {64, kSub * kBK, (cuuint32_t)chunks, 1};
     return encode(m, base, fp16, d2 ? 4 : 3, dims, strides, box);
-}
-// One box a stage where d0 is a multiple of 64 (*whole), else boxes of 64 columns.
-bool make_operand_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, int64_t d1, int64_t stride1, int64_t d2,
-                      int b1, int chunks, int *whole) {
-    *whole = d0 % 64 == 0;
-    return *whole ? make_chunk_map(m, base, fp16, d0, d1, stride1, d2, b1, chunks)
-                  : make_map(m, base, fp16, d0, d1, stride1, d2, b1);
 }
 
 constexpr int kDevices = 64;
@@ -732,10 +733,10 @@ template <int BN, bool kPair>
 cudaError_t product(const void *x, int64_t x_stride, const void *w, bool w_kn, Args a, int64_t n, cudaStream_t s) {
     using C = Cfg<BN, kPair>;
     CUtensorMap ta, tb, small;
-    const bool ok = (w_kn ? make_operand_map(&ta, w, a.fp16, a.F, a.K, a.F, a.experts, kSub * kBK, kM / 64, &a.a_whole)
-                          : make_operand_map(&ta, w, a.fp16, a.K, a.F, a.K, a.experts, kM, kSub, &a.a_whole)) &&
-                    make_operand_map(&tb, x, a.fp16, a.K, n, x_stride, 0, C::kOwn, kSub, &a.b_whole) &&
-                    make_operand_map(&small, x, a.fp16, a.K, n, x_stride, 0, C::kRowBox, kSub, &a.b_whole);
+    const bool ok = (w_kn ? make_operand_map(&ta, w, a.fp16, a.F, a.K, a.F, a.experts, kM / 64, &a.a_whole)
+                          : make_map(&ta, w, a.fp16, a.K, a.F, a.K, a.experts, kM)) &&
+                    make_map(&tb, x, a.fp16, a.K, n, x_stride, 0, C::kOwn) &&
+                    make_map(&small, x, a.fp16, a.K, n, x_stride, 0, C::kRowBox);
     if (!ok) return cudaErrorInvalidValue;
     return w_kn ? launch<BN, kPair, true, false>(ta, tb, small, a, s) : launch<BN, kPair, false, false>(ta, tb, small, a, s);
 }
@@ -757,10 +758,9 @@ cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, co
     using Cf = gm::Cfg<256, true>;
     CUtensorMap ta, tb, chunk;
     gm::Args a{offsets, experts, n, F, C, 0, g_w, F, g_f32, fp16, false, 0, 0};
-    constexpr int rows = gm::kSub * gm::kBK;
-    if (!gm::make_operand_map(&ta, am, fp16, F, n, a_stride, 0, rows, gm::kM / 64, &a.a_whole) ||
-        !gm::make_operand_map(&tb, b, fp16, C, n, b_stride, 0, rows, Cf::kOwn / 64, &a.b_whole) ||
-        !gm::make_map(&chunk, b, fp16, C, n, b_stride, 0, rows))
+    if (!gm::make_operand_map(&ta, am, fp16, F, n, a_stride, 0, gm::kM / 64, &a.a_whole) ||
+        !gm::make_operand_map(&tb, b, fp16, C, n, b_stride, 0, Cf::kOwn / 64, &a.b_whole) ||
+        !gm::make_map(&chunk, b, fp16, C, n, b_stride, 0, gm::kSub * gm::kBK))
         return cudaErrorInvalidValue;
     return gm::launch<256, true, true, true>(ta, tb, chunk, a, s);
 }
