@@ -15,7 +15,7 @@
 // the device, so the host never waits for the router.
 //
 // One CTA per SM walks the tiles (warp 0 loads by TMA, warp 1 issues
-// tcgen05.mma, warps 2-5 write finished tiles, warp 6 clears the rows behind an
+// tcgen05.mma, warps 2-9 write finished tiles, warp 10 clears the rows behind an
 // expert's last one in the gradient's operands); two accumulators alternate, so
 // that a tile is written while the next one's products run.  Where the tiles are
 // large two CTAs work on one (cta_group::2: 256 of f, each CTA with half of A's
@@ -41,7 +41,8 @@ constexpr int kM = 128;       // f per tile
 constexpr int kBK = 64;       // k per block: one 128-byte swizzled row of 16-bit values
 constexpr int kSub = 2;       // blocks per stage
 constexpr int kGroup = 8;     // tiles of c that are walked together
-constexpr int kThreads = 224;
+constexpr int kEpilogue = 8;  // warps that write tiles: two for each quarter of the tensor memory's lanes
+constexpr int kClear = 2 + kEpilogue, kThreads = 32 * (kClear + 1);
 constexpr int kMaxExperts = 1024;
 constexpr unsigned int kErrOffsets = 2u;  // device error bit: offsets out of order or out of range
 
@@ -308,13 +309,6 @@ __device__ __forceinline__ void place_of(int local, int ft, int ct, int &f, int 
     f = rest / w;
     c = g * kGroup + rest - f * w;
 }
-// Bytes between the blocks of a stage's K-major rows: a large box holds a CTA's
-// whole share of a tile's columns, a small one the first rows, where they are all.
-template <int BN, bool kPair>
-__device__ __forceinline__ int row_block(int own) {
-    using C = Cfg<BN, kPair>;
-    return (own > C::kRowBox ? C::kOwn : C::kRowBox) * kBK * 2;
-}
 template <int BN, bool kPair, bool kWeights>
 __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, int &e) {
     while (tile >= p.first[e + 1]) ++e;
@@ -383,6 +377,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     int *const s_start = reinterpret_cast<int *>(smem_raw + (sbase - smem_u32(smem_raw)) + S * C::kStage);
     int *const s_end = s_start + kMaxExperts, *const s_first = s_end + kMaxExperts;
     __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S * kSub], acc_full[2], acc_empty[2], done_bar;
+    __shared__ __align__(8) uint64_t acc_read[2];  // of a pair's second CTA: an accumulator has been read
     __shared__ __align__(8) uint64_t clear_bar[kWeights ? S : 1];  // this CTA's loads of a stage to clear
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
@@ -393,7 +388,11 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) mbar_init(smem_u32(&full_bar[s]), C::kCtas);
         for (int s = 0; s < S * kSub; ++s) mbar_init(smem_u32(&empty_bar[s]), 1);
-        for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&acc_full[b]), 1), mbar_init(smem_u32(&acc_empty[b]), 4 * C::kCtas);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&acc_full[b]), 1);
+            mbar_init(smem_u32(&acc_empty[b]), kEpilogue + (kPair ? 1 : 0));
+            mbar_init(smem_u32(&acc_read[b]), kEpilogue);
+        }
         if (kWeights)
             for (int s = 0; s < S; ++s) mbar_init(smem_u32(&clear_bar[s]), 1);
         mbar_init(smem_u32(&done_bar), 1);
@@ -401,6 +400,8 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         fence_mbar_init_cluster();
     }
     if (warp == 1) tmem_get<kPair>(smem_u32(&s_tmem), C::kTmemCols);
+    // (launched before the kernel in front of it has ended: from here on its results are read)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // every expert's rows and how many tiles they make; a range that is out of
     // order or out of the rows counts as empty and is reported
     for (int e = threadIdx.x; e < a.experts; e += kThreads) {
@@ -456,12 +457,15 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             // this CTA's columns of B
             const int own = (t.cols + C::kGrain - 1) / C::kGrain * 16;
             const int c0 = t.c0 + rank * own, f0 = t.f0 + rank * kM;
-            const int block = row_block<BN, kPair>(own), chunks = (own + 63) / 64;
-            const CUtensorMap *tm_rows = block == C::kOwn * kBK * 2 ? &tm_b : &tm_small;
+            const int chunks = (own + 63) / 64;
+            // (of the product's rows a box for all that a CTA can hold, or a small one where it
+            // holds them; a block's place is the same for both: the tiles follow one another in it)
+            const bool small = own <= C::kRowBox;
+            const CUtensorMap *tm_rows = small ? &tm_small : &tm_b;
             const bool b_whole = kWeights && a.b_whole && own == C::kOwn;  // (then c0 is a multiple of 64)
             constexpr bool kByStage = kAMn || kWeights;
             // bytes of a block (of an MN-major operand: of half a stage)
-            const uint32_t bytes = (uint32_t)(kM * kBK * 2 + (kWeights ? chunks * kChunk / 2 : block));
+            const uint32_t bytes = (uint32_t)(kM * kBK * 2 + (kWeights ? chunks * kChunk / 2 : (small ? C::kRowBox : C::kOwn) * kBK * 2));
             const int stages = (t.klen + kSub * kBK - 1) / (kSub * kBK);
             for (int i = 0; i < stages && ok; ++i) {
                 const int k0 = stage_start<kWeights>(i, stages);
@@ -485,7 +489,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                         ++issued;
                     }
                     if (!kByStage) load_3d<kPair>(sa + s * (kM * kBK * 2), &tm_a, bar, k + s * kBK, f0, t.e, pol);
-                    if (!kWeights) load_2d<kPair>(sb + s * block, tm_rows, bar, k + s * kBK, c0, pol);
+                    if (!kWeights) load_2d<kPair>(sb + s * (C::kBBytes / kSub), tm_rows, bar, k + s * kBK, c0, pol);
                 }
                 if (kByStage && ok) {
                     if (kWeights) {
@@ -504,6 +508,8 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 if (++slot == S) slot = 0, parity ^= 1u;
             }
         }
+        // (this CTA needs nothing but its own: a kernel launched to follow may take its place)
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         // the last stages issued must land before the CTA leaves (of a pair, the second
         // CTA's have when the MMAs have read them: its empty barriers say so)
         for (int k = 0; k < S && k < issued; ++k) {
@@ -532,7 +538,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const uint32_t id = idesc(a.fp16, kAMn || kWeights, kWeights, C::kTileF, n);
             // bytes between the blocks of a stage
             constexpr int a_block = kAMn || kWeights ? kBK * 128 : kM * kBK * 2;
-            const int b_block = kWeights ? kBK * 128 : row_block<BN, kPair>(n / C::kCtas);
+            constexpr int b_block = kWeights ? kBK * 128 : C::kBBytes / kSub;
             uint32_t accumulate = 0;
             const int stages = (klen + kSub * kBK - 1) / (kSub * kBK);
             for (int i = 0; i < stages; ++i) {
@@ -568,7 +574,21 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         umma_commit<kPair>(smem_u32(&done_bar));
         wait_exit(smem_u32(&done_bar), 0u);
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == 1) {
+        // The second CTA of a pair passes on that its accumulators have been read.  An
+        // arrival at the other CTA waits for what its thread has stored; this one's has
+        // stored nothing, the writing warps' would wait for their tiles (1,500 cycles).
+        int c = 0;
+        for (int tile = worker; tile < tiles; tile += workers) {
+            const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
+            if (t.klen == 0) continue;
+            const int b = c & 1;
+            if (!mbar_wait_warp<false>(smem_u32(&acc_read[b]), (uint32_t)(c >> 1) & 1u, &s_abort)) break;
+            if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&acc_empty[b]), 0));
+            __syncwarp();
+            ++c;
+        }
+    } else if (warp == kClear) {
         if constexpr (kWeights) {
             int uses = 0;  // stages of the tiles before
             uint32_t parity = 0;
@@ -591,8 +611,8 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 __syncwarp();
             }
         }
-    } else if (warp >= 2) {
-        const int q = warp & 3;  // the warp's quadrant of tensor-memory lanes
+    } else {
+        const int q = warp & 3, half = (warp - 2) / 4;  // the warp's quadrant of tensor-memory lanes; which of its two
         const int64_t esize = a.out_f32 ? 4 : 2;
         // (F is a multiple of 8, so pairs end with a row)
         const bool paired = a.out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
@@ -603,7 +623,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             hi = hi < lo ? lo : hi > a.n ? a.n : hi;
             for (int64_t r = blockIdx.x; r < lo + (a.n - hi); r += gridDim.x) {
                 const int64_t row = r < lo ? r : hi + (r - lo);
-                for (int f = threadIdx.x - 64; f < a.F; f += 128) put(a.out, row * a.out_stride + f, 0.0f, a.out_f32, a.fp16);
+                for (int f = threadIdx.x - 64; f < a.F; f += 32 * kEpilogue) put(a.out, row * a.out_stride + f, 0.0f, a.out_f32, a.fp16);
             }
         }
         int c = 0;
@@ -615,15 +635,16 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const int64_t step = a.out_stride * esize;
             const bool in = f < a.F;
             if (t.klen == 0) {
-                for (int j = 0; j < t.cols; ++j, o += step)
-                    if (in) put(o, 0, 0.0f, a.out_f32, a.fp16);
+                for (int j = half; j < t.cols; j += 2)
+                    if (in) put(o + j * step, 0, 0.0f, a.out_f32, a.fp16);
                 continue;
             }
             const int b = c & 1;
             if (!mbar_wait_warp<false>(smem_u32(&acc_full[b]), (uint32_t)(c >> 1) & 1u, &s_abort)) break;
             tmem_fence_after_sync();
             const uint32_t ta = tbase + (uint32_t)(b * BN) + ((uint32_t)(32 * q) << 16);
-            for (int j0 = 0; j0 < t.cols; j0 += 32, o += 32 * step) {
+            o += half * 32 * step;
+            for (int j0 = half * 32; j0 < t.cols; j0 += 64, o += 64 * step) {
                 uint32_t v[32];
                 tmem_ld32(ta + (uint32_t)j0, v);
                 if (a.out_f32) put32<float>(o, step, v, t.cols - j0, in);
@@ -633,10 +654,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             }
             tmem_fence_before_sync();
             __syncwarp();
-            if (lane == 0) {
-                if (rank == 0) mbar_arrive(smem_u32(&acc_empty[b]));
-                else mbar_arrive_remote(mapa(smem_u32(&acc_empty[b]), 0));
-            }
+            if (lane == 0) mbar_arrive(smem_u32(rank == 0 ? &acc_empty[b] : &acc_read[b]));
             ++c;
         }
     }
@@ -702,12 +720,14 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorM
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
-    cudaLaunchAttribute pair{};
-    pair.id = cudaLaunchAttributeClusterDimension;
-    pair.val.clusterDim.x = 2, pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = 2, attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = C::kSmem, cfg.stream = s;
-    cfg.attrs = &pair, cfg.numAttrs = kPair ? 1 : 0;
+    cfg.attrs = attrs, cfg.numAttrs = kPair ? 2 : 1;
     int grid = ctas[dev].load(std::memory_order_relaxed);
     if (!grid) {
         if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess) return e;

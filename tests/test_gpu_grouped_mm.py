@@ -121,6 +121,22 @@ def test_many_experts_and_long_contractions():
     _check_weights(g, x, off, False, got["g_w"])
 
 
+@pytest.mark.parametrize("kn", [False, True])
+def test_narrow_and_wide_tiles_in_turn(kn):
+    """Experts of a few rows between experts of many: tiles of different widths
+    follow one another through the same stages.  Every repeat gives the same bits."""
+    counts = [5, 700, 3, 260, 9, 600, 1, 40, 500]
+    x, w, g, off = _inputs(counts, 1536, 320, "bf16", kn, seed=9)
+    y, got = hcg.hc_grouped_mm(x, w, off, transposed=kn), hcg.hc_grouped_mm_backward(g, x, w, off, transposed=kn)
+    _check(x, w, off, kn, y)
+    _check(g, w, off, not kn, got["g_x"])
+    _check_weights(g, x, off, kn, got["g_w"])
+    for _ in range(20):
+        assert torch.equal(hcg.hc_grouped_mm(x, w, off, transposed=kn), y)
+        again = hcg.hc_grouped_mm_backward(g, x, w, off, transposed=kn)
+        assert torch.equal(again["g_x"], got["g_x"]) and torch.equal(again["g_w"], got["g_w"])
+
+
 @pytest.mark.parametrize("pitch", [8, 56])
 def test_strides_and_rows_of_no_expert(pitch):
     """Inputs cut out of wider rows; rows before the first and behind the last
