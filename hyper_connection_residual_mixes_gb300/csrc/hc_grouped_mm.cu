@@ -444,7 +444,9 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             prefetch_tmap(&tm_b);
         }
         __syncwarp();
-        const uint64_t pol = policy_evict_normal();
+        // (operands are read again by other tiles, outputs by none: 620 -> 613 us, 470 -> 453 us
+        // for the prefill's product and the training batch's gradients)
+        const uint64_t pol = policy_evict_last();
         int slot = 0, issued = 0;
         uint32_t parity = 1;
         bool ok = true;
