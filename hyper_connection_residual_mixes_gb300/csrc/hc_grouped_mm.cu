@@ -353,11 +353,12 @@ __device__ __forceinline__ int rows_to_clear(int klen, int k0) {
 }
 // ... a warp clears them in a stage's `chunks` from `chunk0` on: its rows [left, left + rest).
 __device__ __forceinline__ void clear_rows(uint32_t chunk0, int chunks, int left, int rest, int lane) {
-    for (int i = lane; i < chunks * rest * 8; i += 32) {
-        const int ch = i / (rest * 8), r = left + i % (rest * 8) / 8;
-        const uint32_t p = chunk0 + (uint32_t)(ch * kChunk + r * 128 + (i & 7) * 16);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
-    }
+    // eight lanes a row of 128 bytes, four rows at a time
+    for (int ch = 0; ch < chunks; ++ch)
+        for (int r = left + (lane >> 3); r < left + rest; r += 4)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk0 + (uint32_t)(ch * kChunk + r * 128 + (lane & 7) * 16)),
+                         "r"(0)
+                         : "memory");
     fence_proxy_async_smem();
     __syncwarp();
 }
