@@ -160,8 +160,8 @@ const char *hc_status_string(hc_status status) {
     switch (status) {
         case HC_OK: return "HC_OK";
         case HC_ERR_INVALID_ARG: return "HC_ERR_INVALID_ARG: null pointer, bad size or bad scalar";
-        case HC_ERR_UNSUPPORTED: return "HC_ERR_UNSUPPORTED: needs hc == 4 and d a multiple of 64 in [64, 16384]";
-        case HC_ERR_MISALIGNED: return "HC_ERR_MISALIGNED: every pointer must be 16-byte aligned";
+        case HC_ERR_UNSUPPORTED: return "HC_ERR_UNSUPPORTED: a size or type that this entry point does not serve";
+        case HC_ERR_MISALIGNED: return "HC_ERR_MISALIGNED: a pointer without the alignment that this entry point needs";
         case HC_ERR_ALIAS: return "HC_ERR_ALIAS: an output overlaps an input or another output";
         case HC_ERR_CUDA: return "HC_ERR_CUDA: a CUDA call failed (see hc_last_cuda_error)";
         case HC_ERR_TIMEOUT: return "HC_ERR_TIMEOUT: a kernel gave up waiting on a barrier";
@@ -171,7 +171,7 @@ const char *hc_status_string(hc_status status) {
 
 int hc_last_cuda_error(void) { return g_last_cuda_error; }
 
-int hc_version(void) { return 100; }
+int hc_version(void) { return 200; }
 
 hc_status hc_consume_device_error(cudaStream_t stream) {
     unsigned int flag = 0, flag_chain = 0, flag_bwd = 0, flag_proj = 0, flag_grouped = 0, flag_norm = 0;

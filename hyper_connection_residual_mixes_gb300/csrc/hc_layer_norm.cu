@@ -188,7 +188,7 @@ __device__ __forceinline__ void ring_leave(Ring &r, int64_t its, int slots) {
 // 1 / sqrt(a): the approximation and a Newton step, which leaves about a unit.
 __device__ __forceinline__ float rsqrt_newton(float a) {
     const float r = rsqrtf(a);
-    return isinf(r) ? r : fmaf(r * 0.5f, fmaf(-a * r, r, 1.0f), r);
+    return r > 0.0f && r < INFINITY ? fmaf(r * 0.5f, fmaf(-a * r, r, 1.0f), r) : r;  // (0 and infinity stay)
 }
 
 // kFull: the block's threads hold exactly d columns, 16 each.  R rows go through

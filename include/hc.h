@@ -61,8 +61,9 @@ extern "C" {
 typedef enum {
     HC_OK = 0,
     HC_ERR_INVALID_ARG = 1,  /* null pointer, negative size, iters < 1, non-finite or negative eps */
-    HC_ERR_UNSUPPORTED = 2,  /* hc not 2, 4 or 8, or d not a multiple of 64 in [64, 16384] */
-    HC_ERR_MISALIGNED = 3,   /* a pointer that is not 16-byte aligned */
+    HC_ERR_UNSUPPORTED = 2,  /* a size or type that the entry point does not serve (the path: hc not 2, 4 or 8, or
+                                d not a multiple of 64 in [64, 16384]) */
+    HC_ERR_MISALIGNED = 3,   /* a pointer without the entry point's alignment (the path: 16 bytes) */
     HC_ERR_ALIAS = 4,        /* an output range overlaps an input or another output */
     HC_ERR_CUDA = 5,         /* a CUDA runtime call failed; see hc_last_cuda_error() */
     HC_ERR_TIMEOUT = 6       /* a kernel's bounded barrier wait ran out (reported by hc_consume_device_error) */
@@ -413,6 +414,8 @@ hc_status hc_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dtype g_t
  * 2^(byte - 127); the step writes as scale the smallest power of two at or above
  * amax / 448 (from 2^-126 on), codes to nearest, ties to even, and for a positive
  * r at least the smallest positive code.  All bytes zero stand for zero states.
+ * A gradient that is not finite spoils its own value; an infinite one with 8-bit
+ * states also the states of its group of 32.
  *
  *   tensors [count], an array in HOST memory; it is read during the call only
  *   p of p_type; g of g_type: fp32 or p_type; p_copy (optional, p_type HC_F32

@@ -203,6 +203,16 @@ def test_mixed_types_in_one_call():
         c.check(w)
 
 
+def test_hundreds_of_tensors_of_both_kinds():
+    """More tensors than one launch describes, fp32 and 8-bit states in turn."""
+    a, b = Case([17 * k + 1 for k in range(460)], "fp32", "fp32", False, None, 1), Case([5 * k + 40 for k in range(460)], "bf16", "bf16", True, None, 2)
+    mix = lambda k: [t for two in zip(getattr(a, k), getattr(b, k)) for t in two]
+    want = [c.expected(9) for c in (a, b)]
+    hcg.hc_adamw_step(hcg.adamw_plan(mix("p"), mix("g"), mix("m"), mix("v")), step=9, **HYPER)
+    a.check(want[0])
+    b.check(want[1])
+
+
 @pytest.mark.parametrize("packed", [False, True])
 def test_zero_states_and_zero_gradients(packed):
     c = Case([100, 5000], "fp32", "fp32", packed, zero=True)

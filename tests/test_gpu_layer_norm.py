@@ -145,7 +145,8 @@ def _check_backward(x, w, g_y, mean, rstd, got=None, bias=True):
     return got
 
 
-@pytest.mark.parametrize("n,d", CASES + [(1, 5120), (300, 128), (1300, 40), (700, 1024), (1000, 5120), (400, 2176)])
+@pytest.mark.parametrize("n,d", CASES + [(1, 5120), (300, 128), (1300, 40), (700, 1024), (1000, 5120), (400, 2176),
+                                         (305, 6152), (350, 8192)])
 @pytest.mark.parametrize("x,g,w", [("bf16", "fp32", "fp32"), ("bf16", "bf16", "bf16"), ("fp16", "fp16", "fp32"),
                                    ("fp16", "fp32", "fp16"), ("fp32", "fp32", "fp32")])
 def test_backward(n, d, x, g, w):
@@ -196,6 +197,21 @@ def test_rows_of_one_value_and_offsets():
     _check_forward(x, w, b)
     one = torch.tensor([[3.0], [-2.0]], device="cuda")
     assert torch.equal(hcg.hc_layer_norm(one, w[:1], b[:1]), b[:1].expand(2, 1))
+
+
+@pytest.mark.parametrize("n,d", [(700, 1024), (1000, 5120), (650, 1304)])
+def test_infinite_and_nan_rows_among_many(n, d):
+    """The same where rows stream through a block one after the other."""
+    x, w, b, g_y = _inputs(n, d, "bf16", "fp32", seed=10)
+    clean = hcg.hc_layer_norm(x, w, b)
+    x = x.clone()
+    x[3, 5], x[n - 2, d - 1], x[400] = float("inf"), float("nan"), float("-inf")
+    y, mean, rstd = hcg.hc_layer_norm(x, w, b, return_stats=True)
+    rows = torch.ones((n,), dtype=torch.bool, device="cuda")
+    rows[[3, n - 2, 400]] = False
+    assert torch.equal(y[rows], clean[rows]) and y[~rows].isnan().all()
+    got = hcg.hc_layer_norm_backward(g_y, x, w, mean, rstd)
+    assert got["g_x"][rows].isfinite().all() and got["g_x"][n - 2].isnan().all()
 
 
 def test_infinite_and_nan_rows_stay_in_their_row():
