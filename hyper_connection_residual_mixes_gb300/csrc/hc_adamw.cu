@@ -45,7 +45,8 @@ struct Desc {
     void *copy;
     int64_t numel;
     uint32_t first_block;
-    uint8_t p_type, g_type, copy_type, vec;  // vec: every pointer takes accesses of a thread's whole run
+    uint8_t p_type : 2, g_type : 2, copy_type : 2;
+    uint8_t vec, head;  // vec: from value `head` on every pointer takes accesses of a thread's whole run
 };
 
 template <int CAP>
@@ -169,9 +170,8 @@ struct Rates {
 };
 
 template <typename TP, typename TG, bool kPacked, bool kFull>
-__device__ __forceinline__ void chunk(const Desc &d, int64_t base, const Scalars &c, const Rates &r, bool scaled) {
+__device__ __forceinline__ void chunk(const Desc &d, int64_t base, int64_t n, const Scalars &c, const Rates &r, bool scaled) {
     constexpr int V = run_of<TP, TG>(), U = kEach / V;
-    const int64_t n = d.numel;
     Vec<TP, V> pv[U];
     Vec<TG, V> gv[U];
     Vec<float, V> mv[kPacked ? 1 : U], vv[kPacked ? 1 : U];
@@ -252,8 +252,9 @@ __device__ __forceinline__ void chunk(const Desc &d, int64_t base, const Scalars
 
 template <typename TP, typename TG, bool kPacked>
 __device__ __forceinline__ void whole_or_end(const Desc &d, int64_t base, const Scalars &c, const Rates &r, bool scaled) {
-    if (d.vec && base + kChunk <= d.numel) chunk<TP, TG, kPacked, true>(d, base, c, r, scaled);
-    else chunk<TP, TG, kPacked, false>(d, base, c, r, scaled);
+    if (!kPacked && d.head && base == d.head) chunk<TP, TG, kPacked, false>(d, 0, d.head, c, r, scaled);
+    if (d.vec && base + kChunk <= d.numel) chunk<TP, TG, kPacked, true>(d, base, d.numel, c, r, scaled);
+    else chunk<TP, TG, kPacked, false>(d, base, d.numel, c, r, scaled);
 }
 
 // One kernel per kind of states: the 8-bit step needs half the registers, and
@@ -281,7 +282,7 @@ k_adamw(const __grid_constant__ Descs<CAP> t, int count, const __grid_constant__
     }
     const bool scaled = c.grad_scale != nullptr;
     if (scaled) r.gscale = __ldg(c.grad_scale);
-    const int64_t base = (int64_t)(blockIdx.x - d.first_block) * kChunk;
+    const int64_t base = (kPacked ? 0 : d.head) + (int64_t)(blockIdx.x - d.first_block) * kChunk;
     if (d.p_type == HC_F32) whole_or_end<float, float, kPacked>(d, base, c, r, scaled);
     else if (d.p_type == HC_BF16) {
         if (d.g_type == HC_F32) whole_or_end<__nv_bfloat16, float, kPacked>(d, base, c, r, scaled);
@@ -292,17 +293,27 @@ k_adamw(const __grid_constant__ Descs<CAP> t, int count, const __grid_constant__
     }
 }
 
-bool run_ok(const void *p, int64_t bytes, int run) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)(bytes * run) == 0; }
+// Values of `bytes` each to pass before a run is aligned.
+int values_to_run(const void *p, int64_t bytes, int run) {
+    const int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(p) % (uintptr_t)(bytes * run));
+    return (int)((run - off / bytes) % run);
+}
 
 Desc describe(const hc_adamw_tensor &t) {
     Desc d{};
     d.p = t.p, d.g = t.g, d.m = t.m, d.v = t.v, d.ms = t.m_scales, d.vs = t.v_scales, d.copy = t.p_copy;
     d.numel = t.numel;
-    d.p_type = (uint8_t)t.p_type, d.g_type = (uint8_t)t.g_type, d.copy_type = (uint8_t)t.copy_type;
+    d.p_type = (uint8_t)t.p_type & 3, d.g_type = (uint8_t)t.g_type & 3, d.copy_type = (uint8_t)t.copy_type & 3;
     const int64_t pb = t.p_type == HC_F32 ? 4 : 2, gb = t.g_type == HC_F32 ? 4 : 2, state = t.m_scales ? 1 : 4;
     const int run = pb == 2 && gb == 2 ? 8 : 4;  // run_of
-    d.vec = run_ok(t.p, pb, run) && run_ok(t.g, gb, run) && run_ok(t.m, state, run) && run_ok(t.v, state, run) &&
-            (!t.p_copy || run_ok(t.p_copy, 2, run));
+    // Tensors cut out of flat buffers at the same odd place are aligned again after the
+    // same few values, which the first block takes one by one (with 8-bit states the
+    // groups begin with the tensor, so only a tensor that is aligned itself will do).
+    const int head = values_to_run(t.p, pb, run);
+    d.vec = head == values_to_run(t.g, gb, run) && head == values_to_run(t.m, state, run) &&
+            head == values_to_run(t.v, state, run) && (!t.p_copy || head == values_to_run(t.p_copy, 2, run)) &&
+            (head == 0 || !t.m_scales) && head <= t.numel;
+    d.head = d.vec ? (uint8_t)head : 0;
     return d;
 }
 
@@ -316,9 +327,10 @@ cudaError_t launch(const hc_adamw_tensor *t, int64_t count, const Scalars &c, cu
         int64_t blocks = 0;
         for (; at < count && k < CAP; ++at) {
             if (t[at].numel == 0 || (t[at].m_scales != nullptr) != kPacked) continue;
-            const int64_t b = (t[at].numel + kChunk - 1) / kChunk;
+            const Desc d = describe(t[at]);
+            const int64_t rest = d.numel - d.head, b = rest > kChunk ? (rest + kChunk - 1) / kChunk : 1;
             if (blocks + b > INT32_MAX) break;
-            ds.d[k] = describe(t[at]);
+            ds.d[k] = d;
             ds.d[k++].first_block = (uint32_t)blocks;
             blocks += b;
         }

@@ -53,24 +53,41 @@ __device__ __forceinline__ void params(const void *p, int type, int i, float (&o
             }
         }
     } else {
-        o[0] = param(p, type, i);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) o[k] = param(p, type, i + k);
     }
 }
 
-// Read-only streaming load of a vector (each x, g value is read once per launch).
+// Read-only streaming load of a vector (each x, g value is read once per launch),
+// volatile so that a load for the next row stays in front of this row's work.
 template <typename T, int VEC>
 __device__ __forceinline__ Vec<T, VEC> load_stream(const T *p) {
-    Vec<T, VEC> r;
-    if constexpr (sizeof(r) == 16) {
-        uint4 u;
+    constexpr int kBytes = sizeof(T) * VEC;
+    union {
+        Vec<T, VEC> v;
+        uint4 u4;
+        uint2 u2;
+        uint32_t u1;
+        uint16_t h;
+    } r;
+    if constexpr (kBytes == 16)
         asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "=r"(r.u4.x), "=r"(r.u4.y), "=r"(r.u4.z), "=r"(r.u4.w)
                      : "l"(p));
-        r = *reinterpret_cast<Vec<T, VEC> *>(&u);
-    } else {
-        r = *reinterpret_cast<const Vec<T, VEC> *>(p);
-    }
-    return r;
+    else if constexpr (kBytes == 8)
+        asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(r.u2.x), "=r"(r.u2.y) : "l"(p));
+    else if constexpr (kBytes == 4)
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r.u1) : "l"(p));
+    else
+        asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(r.h) : "l"(p));
+    static_assert(kBytes == 16 || kBytes == 8 || kBytes == 4 || kBytes == 2, "loads of 2 to 16 bytes");
+    return r.v;
+}
+
+__device__ __forceinline__ float f2_lo(f32x2 v) {
+    float a, b;
+    f2_split(v, a, b);
+    return a;
 }
 
 // Sum over the row's threads: the warp, or (tpr > 32) the whole block, whose
@@ -84,60 +101,143 @@ __device__ __forceinline__ float team_sum(float v, int tpr, float *red) {
     return warp_sum(lane < nw ? red[lane] : 0.0f);
 }
 
+// 1 / sqrt(a): the approximation and a Newton step, which leaves about a unit.
+__device__ __forceinline__ float rsqrt_newton(float a) {
+    const float r = rsqrtf(a);
+    return r > 0.0f && r < INFINITY ? fmaf(r * 0.5f, fmaf(-a * r, r, 1.0f), r) : r;  // (0 and infinity stay)
+}
+
 // ------------------------------------------------------------ forward
-// tpr threads hold a row in registers: thread t the vectors t + i * tpr.  With
-// tpr == 32 each warp of the block has a row of its own, else the block has one.
+// A row whose values a team of tpr threads holds in registers, thread t the
+// vectors t + i * tpr: statistics and output.
+template <typename T, int VEC, int NV>
+struct Row {
+    Vec<T, VEC> v[NV];
+    __device__ __forceinline__ void load(const T *x, int t, int tpr, int d) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * VEC;
+            if (c < d) v[i] = load_stream<T, VEC>(x + c);
+        }
+    }
+    __device__ __forceinline__ void statistics(int t, int tpr, int d, float eps, float (*red)[32], float &mean,
+                                               float &rstd) const {
+        const float inv_d = 1.0f / (float)d;
+        f32x2 sum = f2_dup(0.0f), sq = f2_dup(0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if ((t + i * tpr) * VEC >= d) continue;
+#pragma unroll
+            for (int k = 0; k < VEC; k += 2) sum = f2_add(sum, at(i, k));
+        }
+        mean = team_sum(f2_hsum(sum), tpr, red[0]) * inv_d;
+        const f32x2 neg = f2_dup(-mean);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if ((t + i * tpr) * VEC >= d) continue;
+#pragma unroll
+            for (int k = 0; k < VEC; k += 2) {
+                f32x2 c = f2_add(at(i, k), neg);
+                if (VEC == 1) c = f2_make(f2_lo(c), 0.0f);
+                sq = f2_fma(c, c, sq);
+            }
+        }
+        rstd = rsqrt_newton(fmaf(team_sum(f2_hsum(sq), tpr, red[1]), inv_d, eps));
+    }
+    // values k, k + 1 of vector i (of single values: the value and 0)
+    __device__ __forceinline__ f32x2 at(int i, int k) const {
+        if constexpr (VEC == 1) return f2_make(to_f(v[i].v[0]), 0.0f);
+        else return pair(v[i], k);
+    }
+    __device__ __forceinline__ Vec<T, VEC> normed(int i, float mean, float rstd, const float (&w)[VEC],
+                                                  const float (&b)[VEC]) const {
+        Vec<T, VEC> o;
+        if constexpr (VEC == 1) {
+            o.v[0] = from_f<T>(fmaf((to_f(v[i].v[0]) - mean) * rstd, w[0], b[0]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; k += 2)
+                put_pair(o, k, f2_fma(f2_mul(f2_add(pair(v[i], k), f2_dup(-mean)), f2_dup(rstd)), f2_make(w[k], w[k + 1]),
+                                      f2_make(b[k], b[k + 1])));
+        }
+        return o;
+    }
+};
+
+// One block per row.
 template <typename T, int VEC, int NV>
 __global__ void __launch_bounds__(1024, 1)
 k_layer_norm(const T *__restrict__ x, int64_t xs, const void *__restrict__ w, const void *__restrict__ b, int wt,
              int64_t n, int d, float eps, T *__restrict__ y, int64_t ys, float *__restrict__ mean_out,
-             float *__restrict__ rstd_out, int tpr) {
+             float *__restrict__ rstd_out) {
     __shared__ float red[2][32];
-    const int t = tpr == 32 ? (threadIdx.x & 31) : threadIdx.x;
-    const int64_t row = tpr == 32 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-    if (row >= n) return;  // whole warps; with tpr > 32 never (one block per row)
-    const T *xr = x + row * xs;
-    Vec<T, VEC> v[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * tpr) * VEC;
-        if (c < d) v[i] = load_stream<T, VEC>(xr + c);
+    const int t = threadIdx.x, tpr = blockDim.x;
+    const int64_t row = blockIdx.x;
+    Row<T, VEC, NV> r;
+    r.load(x + row * xs, t, tpr, d);
+    // (a thread's only vector: its weights come while the row does)
+    float w0[VEC] = {}, b0[VEC] = {};
+    if (NV == 1 && t * VEC < d) {
+        params<VEC>(w, wt, t * VEC, w0);
+        if (b) params<VEC>(b, wt, t * VEC, b0);
     }
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if ((t + i * tpr) * VEC >= d) continue;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) sum += to_f(v[i].v[k]);
-    }
-    const float mean = team_sum(sum, tpr, red[0]) / (float)d;
-    float sq = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if ((t + i * tpr) * VEC >= d) continue;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            const float c = to_f(v[i].v[k]) - mean;
-            sq = fmaf(c, c, sq);
-        }
-    }
-    const float rstd = 1.0f / sqrtf(team_sum(sq, tpr, red[1]) / (float)d + eps);
+    float mean, rstd;
+    r.statistics(t, tpr, d, eps, red, mean, rstd);
     T *yr = y + row * ys;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * tpr) * VEC;
         if (c >= d) continue;
-        float wv[VEC], bv[VEC] = {};
-        params<VEC>(w, wt, c, wv);
-        if (b) params<VEC>(b, wt, c, bv);
-        Vec<T, VEC> o;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) o.v[k] = from_f<T>(fmaf((to_f(v[i].v[k]) - mean) * rstd, wv[k], bv[k]));
-        *reinterpret_cast<Vec<T, VEC> *>(yr + c) = o;
+        if (NV > 1) {
+            params<VEC>(w, wt, c, w0);
+            if (b) params<VEC>(b, wt, c, b0);
+        }
+        *reinterpret_cast<Vec<T, VEC> *>(yr + c) = r.normed(i, mean, rstd, w0, b0);
     }
     if (t == 0) {
         if (mean_out) mean_out[row] = mean;
         if (rstd_out) rstd_out[row] = rstd;
+    }
+}
+
+// Short rows: a warp per row, which keeps its columns' weights and walks over rows,
+// the next one on its way while this one is worked on.
+constexpr int kWarpRowThreads = 128;
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(kWarpRowThreads)
+k_layer_norm_warps(const T *__restrict__ x, int64_t xs, const void *__restrict__ w, const void *__restrict__ b, int wt,
+                   int64_t n, int d, float eps, T *__restrict__ y, int64_t ys, float *__restrict__ mean_out,
+                   float *__restrict__ rstd_out) {
+    const int t = threadIdx.x & 31;
+    const int64_t first = (int64_t)blockIdx.x * (kWarpRowThreads / 32) + (threadIdx.x >> 5);
+    const int64_t step = (int64_t)gridDim.x * (kWarpRowThreads / 32);
+    Row<T, VEC, NV> next;
+    if (first < n) next.load(x + first * xs, t, 32, d);
+    float wv[NV][VEC], bv[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + 32 * i) * VEC;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) wv[i][k] = bv[i][k] = 0.0f;
+        if (c >= d) continue;
+        params<VEC>(w, wt, c, wv[i]);
+        if (b) params<VEC>(b, wt, c, bv[i]);
+    }
+    for (int64_t row = first; row < n; row += step) {
+        const Row<T, VEC, NV> r = next;
+        if (row + step < n) next.load(x + (row + step) * xs, t, 32, d);
+        float mean, rstd;
+        r.statistics(t, 32, d, eps, nullptr, mean, rstd);
+        T *yr = y + row * ys;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + 32 * i) * VEC;
+            if (c < d) *reinterpret_cast<Vec<T, VEC> *>(yr + c) = r.normed(i, mean, rstd, wv[i], bv[i]);
+        }
+        if (t == 0) {
+            if (mean_out) mean_out[row] = mean;
+            if (rstd_out) rstd_out[row] = rstd;
+        }
     }
 }
 
@@ -183,12 +283,6 @@ __device__ __forceinline__ void ring_leave(Ring &r, int64_t its, int slots) {
                 if (mbar_try_wait(smem_u32(&r.full[k % slots]), (uint32_t)(k / slots) & 1u)) break;
                 __nanosleep(128);
             }
-}
-
-// 1 / sqrt(a): the approximation and a Newton step, which leaves about a unit.
-__device__ __forceinline__ float rsqrt_newton(float a) {
-    const float r = rsqrtf(a);
-    return r > 0.0f && r < INFINITY ? fmaf(r * 0.5f, fmaf(-a * r, r, 1.0f), r) : r;  // (0 and infinity stay)
 }
 
 // kFull: the block's threads hold exactly d columns, 16 each.  R rows go through
@@ -334,8 +428,8 @@ k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ 
 // Each thread owns the same columns of every row its block takes, with their
 // sums of g xh and g in registers; a block leaves one row of partial sums in
 // the workspace, k_ln_columns adds the blocks' rows in a fixed order.
-template <typename TX, typename TG, int VEC, int NV, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+template <typename TX, typename TG, int VEC, int NV>
+__global__ void __launch_bounds__(512, 1)
 k_ln_backward(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, int64_t xs,
               const void *__restrict__ w, int wt, const float *__restrict__ mean_in,
               const float *__restrict__ rstd_in, int64_t n, int d, TG *__restrict__ gx, int64_t gxs,
@@ -445,6 +539,78 @@ k_ln_backward(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, i
         __syncthreads();
     }
     for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) pw[c] = s_cols[c];
+}
+
+// Rows too long for that: the second pass over a row reads it (and the weights)
+// again, from L2, so that the registers hold the column sums alone.
+template <typename TX, typename TG, int VEC, int NV>
+__global__ void __launch_bounds__(1024, 1)
+k_ln_backward_wide(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, int64_t xs,
+                   const void *__restrict__ w, int wt, const float *__restrict__ mean_in,
+                   const float *__restrict__ rstd_in, int64_t n, int d, TG *__restrict__ gx, int64_t gxs,
+                   float *__restrict__ part) {
+    __shared__ float2 red[2][32];
+    const int t = threadIdx.x, tpr = blockDim.x, warp = t >> 5, lane = t & 31, nw = tpr >> 5;
+    const float inv_d = 1.0f / (float)d;
+    float aw[NV][VEC], ab[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) aw[i][k] = ab[i][k] = 0.0f;
+    int buf = 0;
+    for (int64_t row = blockIdx.x; row < n; row += gridDim.x, buf ^= 1) {
+        const TX *xr = x + row * xs;
+        const TG *gr = gy + row * gs;
+        const float mean = __ldg(mean_in + row), rstd = __ldg(rstd_in + row);
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * VEC;
+            if (c >= d) continue;
+            const Vec<TX, VEC> xv = *reinterpret_cast<const Vec<TX, VEC> *>(xr + c);
+            const Vec<TG, VEC> gv = *reinterpret_cast<const Vec<TG, VEC> *>(gr + c);
+            float wv[VEC];
+            params<VEC>(w, wt, c, wv);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const float xh = (to_f(xv.v[k]) - mean) * rstd, g = to_f(gv.v[k]), wg = g * wv[k];
+                s1 += wg;
+                s2 = fmaf(wg, xh, s2);
+                aw[i][k] = fmaf(g, xh, aw[i][k]);
+                ab[i][k] += g;
+            }
+        }
+        s1 = warp_sum(s1), s2 = warp_sum(s2);
+        if (lane == 0) red[buf][warp] = make_float2(s1, s2);
+        __syncthreads();
+        const float2 r = lane < nw ? red[buf][lane] : make_float2(0.0f, 0.0f);
+        const float m1 = warp_sum(r.x) * inv_d, m2 = warp_sum(r.y) * inv_d;
+        TG *o_row = gx + row * gxs;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * VEC;
+            if (c >= d) continue;
+            const Vec<TX, VEC> xv = *reinterpret_cast<const Vec<TX, VEC> *>(xr + c);
+            const Vec<TG, VEC> gv = *reinterpret_cast<const Vec<TG, VEC> *>(gr + c);
+            float wv[VEC];
+            params<VEC>(w, wt, c, wv);
+            Vec<TG, VEC> o;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const float xh = (to_f(xv.v[k]) - mean) * rstd;
+                o.v[k] = from_f<TG>(rstd * (to_f(gv.v[k]) * wv[k] - m1 - xh * m2));
+            }
+            *reinterpret_cast<Vec<TG, VEC> *>(o_row + c) = o;
+        }
+    }
+    float *pw = part + (int64_t)blockIdx.x * 2 * d, *pb = pw + d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const int c = (t + i * tpr) * VEC + k;
+            if (c < d) pw[c] = aw[i][k], pb[c] = ab[i][k];
+        }
 }
 
 // The same with the rows of x and g through a ring.  Each thread owns 4 columns in
@@ -625,26 +791,33 @@ struct FwdCall {
 };
 
 template <typename T, int VEC, int NV>
-cudaError_t fwd_launch(const FwdCall &c, int tpr, int threads) {
-    const int64_t per = tpr == 32 ? threads / 32 : 1;
-    const int64_t blocks = (c.n + per - 1) / per;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    k_layer_norm<T, VEC, NV><<<(unsigned)blocks, threads, 0, c.s>>>(
-        static_cast<const T *>(c.x), c.xs, c.w, c.b, c.wt, c.n, c.d, c.eps, static_cast<T *>(c.y), c.ys, c.mean,
-        c.rstd, tpr);
+cudaError_t fwd_warps(const FwdCall &c) {
+    constexpr auto kKernel = k_layer_norm_warps<T, VEC, NV>;
+    int per_sm = 0;
+    const cudaError_t e = blocks_per_sm<kKernel>(kWarpRowThreads, &per_sm);
+    if (e != cudaSuccess) return e;
+    const int64_t need = (c.n + kWarpRowThreads / 32 - 1) / (kWarpRowThreads / 32);
+    const int64_t most = (int64_t)per_sm * sm_count_of_device();
+    kKernel<<<(unsigned)(need < most ? need : most), kWarpRowThreads, 0, c.s>>>(
+        static_cast<const T *>(c.x), c.xs, c.w, c.b, c.wt, c.n, c.d, c.eps, static_cast<T *>(c.y), c.ys, c.mean, c.rstd);
+    return cudaGetLastError();
+}
+template <typename T, int VEC, int NV>
+cudaError_t fwd_blocks(const FwdCall &c, int threads) {
+    k_layer_norm<T, VEC, NV><<<(unsigned)c.n, threads, 0, c.s>>>(
+        static_cast<const T *>(c.x), c.xs, c.w, c.b, c.wt, c.n, c.d, c.eps, static_cast<T *>(c.y), c.ys, c.mean, c.rstd);
     return cudaGetLastError();
 }
 
 template <typename T, int VEC>
 cudaError_t fwd_vec(const FwdCall &c) {
     const int vecs = (c.d + VEC - 1) / VEC;
-    if (vecs <= 32) return fwd_launch<T, VEC, 1>(c, 32, 128);
-    if (vecs <= 64) return fwd_launch<T, VEC, 2>(c, 32, 128);
-    if (vecs <= 128) return fwd_launch<T, VEC, 4>(c, 32, 128);
-    const int tpr1 = (vecs + 31) / 32 * 32, tpr4 = (vecs + 127) / 128 * 32, tpr16 = (vecs + 511) / 512 * 32;
-    if (vecs <= 1024) return fwd_launch<T, VEC, 1>(c, tpr1, tpr1);
-    if (vecs <= 4096) return fwd_launch<T, VEC, 4>(c, tpr4, tpr4);
-    return fwd_launch<T, 1, 16>(c, tpr16, tpr16);  // single values only: 4096 vectors hold the longest row
+    if (vecs <= 32) return fwd_warps<T, VEC, 1>(c);
+    if (vecs <= 64) return fwd_warps<T, VEC, 2>(c);
+    if (vecs <= 128) return fwd_warps<T, VEC, 4>(c);
+    if (vecs <= 1024) return fwd_blocks<T, VEC, 1>(c, (vecs + 31) / 32 * 32);
+    if (vecs <= 4096) return fwd_blocks<T, VEC, 4>(c, (vecs + 127) / 128 * 32);
+    return fwd_blocks<T, VEC < 4 ? VEC : 1, 16>(c, (vecs + 511) / 512 * 32);  // (runs of 4 and 8 never are so many)
 }
 
 // Slots of a ring and blocks of a launch: as many slots as fit beside the SM's
@@ -681,6 +854,7 @@ cudaError_t fwd_ring(const FwdCall &c) {
     if (threads <= 320)
         return c.d == threads * 16 ? fwd_ring_launch<k_layer_norm_ring<T, NV, 2, true, 320, 2>, T>(c, threads)
                                    : fwd_ring_launch<k_layer_norm_ring<T, NV, 2, false, 320, 2>, T>(c, threads);
+    if (threads <= 704) return fwd_ring_launch<k_layer_norm_ring<T, NV, 2, false, 704, 1>, T>(c, threads);
     return fwd_ring_launch<k_layer_norm_ring<T, NV, 1, false, 1024, 1>, T>(c, threads);
 }
 
@@ -693,6 +867,9 @@ cudaError_t fwd_type(const FwdCall &c) {
         if (c.d >= 1024 && c.n >= 4 * (int64_t)sm_count_of_device()) return fwd_ring<T>(c);
         return fwd_vec<T, VEC>(c);
     }
+    // (16-bit rows of even width and spacing: two values at a time)
+    if constexpr (sizeof(T) == 2)
+        if (c.d % 2 == 0 && aligned(c.x, c.xs * 2, 4) && aligned(c.y, c.ys * 2, 4)) return fwd_vec<T, 2>(c);
     return fwd_vec<T, 1>(c);
 }
 
@@ -716,9 +893,9 @@ cudaError_t launch_columns(const BwdCall &c, int blocks) {
     return cudaLaunchKernelEx(&cfg, k_ln_columns, (const float *)c.part, blocks, c.d, c.g_w, c.g_b);
 }
 
-template <typename TX, typename TG, int VEC, int NV, int kMaxThreads>
+template <typename TX, typename TG, int VEC, int NV>
 cudaError_t bwd_launch(const BwdCall &c, int tpr) {
-    constexpr auto kKernel = k_ln_backward<TX, TG, VEC, NV, kMaxThreads>;
+    constexpr auto kKernel = k_ln_backward<TX, TG, VEC, NV>;
     const int threads = tpr == 32 ? 256 : tpr;
     const int teams = tpr == 32 ? threads / 32 : 1;
     const size_t smem = teams > 1 ? (size_t)c.d * 8 : 0;
@@ -731,6 +908,22 @@ cudaError_t bwd_launch(const BwdCall &c, int tpr) {
     kKernel<<<(unsigned)blocks, threads, smem, c.s>>>(
         static_cast<const TG *>(c.gy), c.gs, static_cast<const TX *>(c.x), c.xs, c.w, c.wt, c.mean, c.rstd, c.n, c.d,
         static_cast<TG *>(c.gx), c.gxs, c.part, tpr);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_columns(c, (int)blocks);
+}
+
+template <typename TX, typename TG, int VEC, int NV>
+cudaError_t bwd_wide(const BwdCall &c, int threads) {
+    constexpr auto kKernel = k_ln_backward_wide<TX, TG, VEC, NV>;
+    int per_sm = 0;
+    cudaError_t e = blocks_per_sm<kKernel>(threads, &per_sm);
+    if (e != cudaSuccess) return e;
+    int64_t blocks = (int64_t)per_sm * sm_count_of_device();
+    if (blocks > max_blocks(c.d)) blocks = max_blocks(c.d);
+    if (blocks > c.n) blocks = c.n;
+    kKernel<<<(unsigned)blocks, threads, 0, c.s>>>(
+        static_cast<const TG *>(c.gy), c.gs, static_cast<const TX *>(c.x), c.xs, c.w, c.wt, c.mean, c.rstd, c.n, c.d,
+        static_cast<TG *>(c.gx), c.gxs, c.part);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_columns(c, (int)blocks);
 }
@@ -767,15 +960,20 @@ cudaError_t bwd_type(const BwdCall &c) {
         const bool bulk = (int64_t)d * sizeof(TX) % 16 == 0 && (int64_t)d * sizeof(TG) % 16 == 0 &&
                           aligned(c.x, c.xs * (int64_t)sizeof(TX), 16) && aligned(c.gy, c.gs * (int64_t)sizeof(TG), 16);
         if (bulk && d >= 1024 && d <= 8192 && c.n >= 2 * (int64_t)sm_count_of_device()) return bwd_ring<TX, TG>(c);
-        if (d <= 256) return bwd_launch<TX, TG, 4, 2, 512>(c, 32);
-        if (d <= 4096) return bwd_launch<TX, TG, 4, 2, 512>(c, (d + 255) / 256 * 32);
-        if (d <= 8192) return bwd_launch<TX, TG, 4, 2, 1024>(c, (d + 255) / 256 * 32);
-        return bwd_launch<TX, TG, 4, 4, 1024>(c, (d + 511) / 512 * 32);
+        if (d <= 256) return bwd_launch<TX, TG, 4, 2>(c, 32);
+        if (d <= 4096) return bwd_launch<TX, TG, 4, 2>(c, (d + 255) / 256 * 32);
+        return bwd_wide<TX, TG, 4, 4>(c, (d + 511) / 512 * 32);
     }
-    if (d <= 128) return bwd_launch<TX, TG, 1, 4, 512>(c, 32);
-    if (d <= 4096) return bwd_launch<TX, TG, 1, 8, 512>(c, (d + 255) / 256 * 32);
-    if (d <= 8192) return bwd_launch<TX, TG, 1, 8, 1024>(c, (d + 255) / 256 * 32);
-    return bwd_launch<TX, TG, 1, 16, 1024>(c, (d + 511) / 512 * 32);
+    // (16-bit rows of even width and spacing: two values at a time)
+    if constexpr (sizeof(TX) == 2)
+        if (d % 2 == 0 && d > 256 && aligned(c.x, c.xs * 2, 4) && aligned(c.gy, c.gs * (int64_t)sizeof(TG), 2 * sizeof(TG)) &&
+            aligned(c.gx, c.gxs * (int64_t)sizeof(TG), 2 * sizeof(TG))) {
+            if (d <= 4096) return bwd_launch<TX, TG, 2, 4>(c, (d + 255) / 256 * 32);
+            return bwd_wide<TX, TG, 2, 8>(c, (d + 511) / 512 * 32);
+        }
+    if (d <= 128) return bwd_launch<TX, TG, 1, 4>(c, 32);
+    if (d <= 4096) return bwd_launch<TX, TG, 1, 8>(c, (d + 255) / 256 * 32);
+    return bwd_wide<TX, TG, 1, 16>(c, (d + 511) / 512 * 32);
 }
 
 }  // namespace ln
