@@ -46,7 +46,7 @@ constexpr int kClear = 2 + kEpilogue, kThreads = 32 * (kClear + 1);
 constexpr int kMaxExperts = 1024;
 constexpr unsigned int kErrOffsets = 2u;  // device error bit: offsets out of order or out of range
 
-template <int BN, bool kPair>
+template <int BN, bool kPair, bool kDeep>
 struct Cfg {
     static constexpr int kCtas = kPair ? 2 : 1;
     static constexpr int kTileF = kM * kCtas;           // f of a tile
@@ -60,10 +60,14 @@ struct Cfg {
     // their way while one is multiplied; MN-major ones a stage at a time, because boxes
     // of 64 k load a fifth slower than boxes of 128 (both gradients 500 us against 455).
     static constexpr int kABytes = kSub * kM * kBK * 2, kBBytes = kSub * kOwn * kBK * 2, kStage = kABytes + kBBytes;
-    static constexpr int kStages = kOwn >= 256 ? 2 : kOwn >= 128 ? 3 : kOwn >= 64 ? 4 : 5;
+    // CTAs that share an SM.  Two, with half the stages each, even out the last round of
+    // tiles (17 experts' 1224 x 6608: 52 us against 65 with one); but where every tile has
+    // an SM to itself, all the stages do better (17 experts' 776 x 2096: 13 us against 16).
+    static constexpr int kPerSm = kPair || kDeep ? 1 : 2;
+    static constexpr int kStages = kPair ? 3 : kDeep ? 5 : 2;
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kSmem = kStages * kStage + 1024 + 3 * (kMaxExperts + 1) * 4;
-    static_assert(kSmem <= 227 * 1024 - 512, "shared memory");
+    static_assert(kPerSm * (kSmem + 1024 + 512) <= 228 * 1024 && kPerSm * kTmemCols <= 512, "an SM's memory");
 };
 
 struct Args {
@@ -309,14 +313,14 @@ __device__ __forceinline__ void place_of(int local, int ft, int ct, int &f, int 
     f = rest / w;
     c = g * kGroup + rest - f * w;
 }
-template <int BN, bool kPair, bool kWeights>
+template <int BN, bool kPair, bool kDeep, bool kWeights>
 __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, int &e) {
     while (tile >= p.first[e + 1]) ++e;
     const int local = tile - p.first[e];
     const int rows = p.end[e] - p.start[e];
     Tile t;
     t.e = e;
-    const int ft = (a.F + Cfg<BN, kPair>::kTileF - 1) / Cfg<BN, kPair>::kTileF;
+    const int ft = (a.F + Cfg<BN, kPair, kDeep>::kTileF - 1) / Cfg<BN, kPair, kDeep>::kTileF;
     int f, c;
     if (kWeights) {
         place_of(local, ft, (a.C + BN - 1) / BN, f, c);
@@ -326,7 +330,7 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
         t.klen = rows;
     } else {
         const int nt = (rows + BN - 1) / BN;
-        constexpr int kGrain = Cfg<BN, kPair>::kGrain;
+        constexpr int kGrain = Cfg<BN, kPair, kDeep>::kGrain;
         const int per = ((rows + nt - 1) / nt + kGrain - 1) / kGrain * kGrain;
         place_of(local, ft, nt, f, c);
         const int at = c * per;
@@ -335,7 +339,7 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
         t.k0 = 0;
         t.klen = a.K;
     }
-    t.f0 = f * Cfg<BN, kPair>::kTileF;
+    t.f0 = f * Cfg<BN, kPair, kDeep>::kTileF;
     return t;
 }
 
@@ -367,11 +371,11 @@ __device__ __forceinline__ void clear_rows(uint32_t chunk0, int chunks, int left
 // rows of the weights' gradient); kWeights: the weights' gradient (B is MN-major too).
 // Of a pair the first CTA issues the MMAs and its barriers collect both CTAs'
 // loads and both epilogues' arrivals; commits arrive at both CTAs' barriers.
-template <int BN, bool kPair, bool kAMn, bool kWeights>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int BN, bool kPair, bool kDeep, bool kAMn, bool kWeights>
+__global__ void __launch_bounds__(kThreads, Cfg<BN, kPair, kDeep>::kPerSm)
 k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
              const __grid_constant__ CUtensorMap tm_small, const Args a) {
-    using C = Cfg<BN, kPair>;
+    using C = Cfg<BN, kPair, kDeep>;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -452,7 +456,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         uint32_t parity = 1;
         bool ok = true;
         for (int tile = worker; tile < tiles && ok; tile += workers) {
-            Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
+            Tile t = tile_of<BN, kPair, kDeep, kWeights>(a, plan, tile, e);
             // (one value for the warp: what the issuing thread reads stays in uniform registers)
             t.klen = __shfl_sync(0xffffffffu, t.klen, 0), t.k0 = __shfl_sync(0xffffffffu, t.k0, 0);
             t.f0 = __shfl_sync(0xffffffffu, t.f0, 0), t.c0 = __shfl_sync(0xffffffffu, t.c0, 0);
@@ -530,7 +534,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         const uint64_t da0 = desc(sbase, kAMn || kWeights), db0 = desc(sbase + C::kABytes, kWeights);
         constexpr uint32_t kStepA = (kAMn || kWeights ? 2048 : 32) >> 4, kStepB = (kWeights ? 2048 : 32) >> 4;
         for (int tile = worker; tile < tiles && ok; tile += workers) {
-            const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
+            const Tile t = tile_of<BN, kPair, kDeep, kWeights>(a, plan, tile, e);
             const int klen = __shfl_sync(0xffffffffu, t.klen, 0), cols = __shfl_sync(0xffffffffu, t.cols, 0);
             if (klen == 0) continue;  // an expert without rows: its gradient is zero
             const int b = c & 1;
@@ -583,7 +587,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         // stored nothing, the writing warps' would wait for their tiles (1,500 cycles).
         int c = 0;
         for (int tile = worker; tile < tiles; tile += workers) {
-            const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
+            const Tile t = tile_of<BN, kPair, kDeep, kWeights>(a, plan, tile, e);
             if (t.klen == 0) continue;
             const int b = c & 1;
             if (!mbar_wait_warp<false>(smem_u32(&acc_read[b]), (uint32_t)(c >> 1) & 1u, &s_abort)) break;
@@ -597,7 +601,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             uint32_t parity = 0;
             bool ok = true;
             for (int tile = worker; tile < tiles && ok; tile += workers) {
-                const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
+                const Tile t = tile_of<BN, kPair, kDeep, kWeights>(a, plan, tile, e);
                 const int stages = (t.klen + kSub * kBK - 1) / (kSub * kBK);
                 const int slot = uses % S, k0 = stage_start<kWeights>(0, stages);
                 uses += stages;
@@ -631,7 +635,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         }
         int c = 0;
         for (int tile = worker; tile < tiles; tile += workers) {
-            const Tile t = tile_of<BN, kPair, kWeights>(a, plan, tile, e);
+            const Tile t = tile_of<BN, kPair, kDeep, kWeights>(a, plan, tile, e);
             const int f = t.f0 + rank * kM + q * 32 + lane;
             uint8_t *o = static_cast<uint8_t *>(a.out) +
                          ((kWeights ? (int64_t)t.e * a.C + t.c0 : (int64_t)t.c0) * a.out_stride + f) * esize;
@@ -712,12 +716,22 @@ bool make_operand_map(CUtensorMap *m, const void *base, bool fp16, int64_t d0, i
 
 constexpr int kDevices = 64;
 
+int sm_count() {
+    static std::atomic<int> sms[kDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 148;
+    if ((n = sms[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    sms[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // Launches on every SM (pairs: every two SMs that can work together), once per
 // kernel and device finding out how many and allowing the shared memory.
-template <int BN, bool kPair, bool kAMn, bool kWeights>
+template <int BN, bool kPair, bool kDeep, bool kAMn, bool kWeights>
 cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &small, const Args &a, cudaStream_t s) {
-    using C = Cfg<BN, kPair>;
-    const auto k = k_grouped_mm<BN, kPair, kAMn, kWeights>;
+    using C = Cfg<BN, kPair, kDeep>;
+    const auto k = k_grouped_mm<BN, kPair, kDeep, kAMn, kWeights>;
     static std::atomic<int> ctas[kDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -742,6 +756,7 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorM
             if (clusters < 1) return cudaErrorLaunchOutOfResources;
             grid = grid / 2 < clusters ? grid / 2 * 2 : clusters * 2;
         }
+        grid *= C::kPerSm;
         ctas[dev].store(grid, std::memory_order_relaxed);
     }
     cfg.gridDim = dim3((unsigned)grid);
@@ -752,16 +767,17 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorM
 
 namespace gm {
 
-template <int BN, bool kPair>
+template <int BN, bool kPair, bool kDeep>
 cudaError_t product(const void *x, int64_t x_stride, const void *w, bool w_kn, Args a, int64_t n, cudaStream_t s) {
-    using C = Cfg<BN, kPair>;
+    using C = Cfg<BN, kPair, kDeep>;
     CUtensorMap ta, tb, small;
     const bool ok = (w_kn ? make_operand_map(&ta, w, a.fp16, a.F, a.K, a.F, a.experts, kM / 64, &a.a_whole)
                           : make_map(&ta, w, a.fp16, a.K, a.F, a.K, a.experts, kM)) &&
                     make_map(&tb, x, a.fp16, a.K, n, x_stride, 0, C::kOwn) &&
                     make_map(&small, x, a.fp16, a.K, n, x_stride, 0, C::kRowBox);
     if (!ok) return cudaErrorInvalidValue;
-    return w_kn ? launch<BN, kPair, true, false>(ta, tb, small, a, s) : launch<BN, kPair, false, false>(ta, tb, small, a, s);
+    return w_kn ? launch<BN, kPair, kDeep, true, false>(ta, tb, small, a, s)
+                : launch<BN, kPair, kDeep, false, false>(ta, tb, small, a, s);
 }
 
 }  // namespace gm
@@ -770,22 +786,25 @@ cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bo
                               int experts, int N, int K, bool fp16, void *y, int64_t y_stride, bool y_f32,
                               bool zero_rest, cudaStream_t s) {
     const gm::Args a{offsets, experts, n, N, 0, K, y, y_stride, y_f32, fp16, zero_rest, 0, 0};
-    // Few rows an expert: narrow row tiles leave room for more stages of weights in flight.
-    if (n <= 32 * (int64_t)experts) return gm::product<32, false>(x, x_stride, w, w_kn, a, n, s);
-    return gm::product<256, true>(x, x_stride, w, w_kn, a, n, s);
+    if (n > 32 * (int64_t)experts) return gm::product<256, true, false>(x, x_stride, w, w_kn, a, n, s);
+    // Few rows an expert: narrow row tiles leave room for more of the weights in flight.  The
+    // tiles are at most one for each 128 outputs of each expert (and of each 32 rows of one).
+    const int64_t with_rows = n < experts ? n : experts + n / 32, tiles = (N + gm::kM - 1) / gm::kM * with_rows;
+    if (tiles <= gm::sm_count()) return gm::product<32, false, true>(x, x_stride, w, w_kn, a, n, s);
+    return gm::product<32, false, false>(x, x_stride, w, w_kn, a, n, s);
 }
 
 cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, const void *am, int64_t a_stride, int F,
                                       const int32_t *offsets, int64_t n, int experts, bool fp16, void *g_w,
                                       bool g_f32, cudaStream_t s) {
-    using Cf = gm::Cfg<256, true>;
+    using Cf = gm::Cfg<256, true, false>;
     CUtensorMap ta, tb, chunk;
     gm::Args a{offsets, experts, n, F, C, 0, g_w, F, g_f32, fp16, false, 0, 0};
     if (!gm::make_operand_map(&ta, am, fp16, F, n, a_stride, 0, gm::kM / 64, &a.a_whole) ||
         !gm::make_operand_map(&tb, b, fp16, C, n, b_stride, 0, Cf::kOwn / 64, &a.b_whole) ||
         !gm::make_map(&chunk, b, fp16, C, n, b_stride, 0, gm::kSub * gm::kBK))
         return cudaErrorInvalidValue;
-    return gm::launch<256, true, true, true>(ta, tb, chunk, a, s);
+    return gm::launch<256, true, false, true, true>(ta, tb, chunk, a, s);
 }
 
 cudaError_t consume_grouped_mm_device_error(cudaStream_t s, unsigned int *flag) {
