@@ -24,6 +24,9 @@
 // value for fp32 parameters, gradients and states, 10.1 for bf16 parameters
 // and gradients with 8-bit states.  All tensors of a call with one kind of states
 // go in one launch (their descriptions are kernel parameters, 448 at the most).
+// 320 fp32 tensors of 39.7M values: 163 us, 0.99 of the measured copy rate; 252M
+// bf16 values with 8-bit states: 408 us, 0.92 (some 40 instructions a value, which
+// keep the issue slots 64 % busy).
 #include <cuda_fp8.h>
 
 #include "hc_sublayer.h"

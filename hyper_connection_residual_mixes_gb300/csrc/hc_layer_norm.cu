@@ -8,7 +8,9 @@
 //   g_w = sum over rows of g xh,  g_b = sum over rows of g.
 // All sums run in fp32; y (and g_x) are rounded once, on the way out.
 //
-// Both directions move each row across HBM once and are bound by that.
+// Both directions move each row across HBM once and are bound by that: 65,536 rows
+// of 5,120 bf16 take 207 us forward (0.95 of the measured copy rate), 8,192 rows
+// with fp32 gradients 71 us backward (0.87; 4 of them for the column sums).
 #include <atomic>
 
 #include <cuda.h>
@@ -864,6 +866,8 @@ cudaError_t fwd_type(const FwdCall &c) {
     const size_t pa = c.wt == HC_F32 ? 16 : 8;
     if (c.d % VEC == 0 && aligned(c.x, c.xs * (int64_t)sizeof(T), 16) && aligned(c.y, c.ys * (int64_t)sizeof(T), 16) &&
         aligned(c.w, 0, pa) && aligned(c.b, 0, pa)) {
+        // (us, ring and a block per row: 304 rows of 5,120 3.7 and 3.3, 608 rows 4.2 and 5.4, 4,864 rows
+        // 17.8 and 35.4; of 1,024 columns 608 rows 3.0 and 2.6, 4,864 rows 5.8 and 6.2)
         if (c.d >= 1024 && c.n >= 4 * (int64_t)sm_count_of_device()) return fwd_ring<T>(c);
         return fwd_vec<T, VEC>(c);
     }
@@ -959,7 +963,9 @@ cudaError_t bwd_type(const BwdCall &c) {
         aligned(c.gx, c.gxs * (int64_t)sizeof(TG), 4 * sizeof(TG)) && aligned(c.w, 0, pa)) {
         const bool bulk = (int64_t)d * sizeof(TX) % 16 == 0 && (int64_t)d * sizeof(TG) % 16 == 0 &&
                           aligned(c.x, c.xs * (int64_t)sizeof(TX), 16) && aligned(c.gy, c.gs * (int64_t)sizeof(TG), 16);
-        if (bulk && d >= 1024 && d <= 8192 && c.n >= 2 * (int64_t)sm_count_of_device()) return bwd_ring<TX, TG>(c);
+        // (us, ring and plain loads: 76 rows of 5,120 6.6 and 9.4, 4,864 rows 45.6 and 84.3; of 1,024
+        // columns 4.5 and 4.9, 13.8 and 15.2)
+        if (bulk && d >= 1024 && d <= 8192) return bwd_ring<TX, TG>(c);
         if (d <= 256) return bwd_launch<TX, TG, 4, 2>(c, 32);
         if (d <= 4096) return bwd_launch<TX, TG, 4, 2>(c, (d + 255) / 256 * 32);
         return bwd_wide<TX, TG, 4, 4>(c, (d + 511) / 512 * 32);
