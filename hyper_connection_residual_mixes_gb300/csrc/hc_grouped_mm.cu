@@ -767,10 +767,6 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorM
     return cudaLaunchKernelEx(&cfg, k, ta, tb, small, a);
 }
 
-}  // namespace gm
-
-namespace gm {
-
 template <int BN, bool kPair, bool kDeep>
 cudaError_t product(const void *x, int64_t x_stride, const void *w, bool w_kn, Args a, int64_t n, cudaStream_t s) {
     using C = Cfg<BN, kPair, kDeep>;

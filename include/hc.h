@@ -359,7 +359,7 @@ typedef enum {
 } hc_dtype;
 
 /*
- * Layer norm of n rows of d values (1 <= d <= 16384), e.g. of the bf16 h that a
+ * Layer norm of n rows of d values (1 <= d <= 16384, n < 2^31), e.g. of the bf16 h that a
  * chain launch writes (h_pre_out):
  *   mean = sum x / d,  rstd = 1 / sqrt(sum (x - mean)^2 / d + eps),
  *   y = (x - mean) rstd norm_w + norm_b,
@@ -466,7 +466,7 @@ hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr
  *   on) are left as they are, or with zero_rest written as zeros.
  *   g_y [n, N] of type, rows g_stride >= N apart                             in
  *   g_w [experts, N, K] (transposed: [experts, K, N]) of g_type: type or fp32    out
- * type is HC_BF16 or HC_F16.  experts <= 1024; N and K multiples of 8; x, g_y and w
+ * type is HC_BF16 or HC_F16.  experts <= 1024; n < 2^31 - 4096; N and K multiples of 8; x, g_y and w
  * start on 16 bytes and x_stride, g_stride are multiples of 8 (the tensor
  * copies' rule; HC_ERR_UNSUPPORTED, HC_ERR_MISALIGNED otherwise).
  */
