@@ -139,7 +139,7 @@ hc_status check_adamw_tensor(const hc_adamw_tensor &t) {
 hc_status check_grouped(int64_t n, int experts, int N, int K, hc_dtype type, hc_dtype out_type) {
     if (n < 0 || experts <= 0 || N <= 0 || K <= 0 || !known(type) || !known(out_type)) return HC_ERR_INVALID_ARG;
     if (type == HC_F32 || (out_type != HC_F32 && out_type != type) || experts > 1024 || N % 8 || K % 8 ||
-        n > INT32_MAX - 4096)  // (a tile's last row fits 32 bits)
+        n > INT32_MAX - 4096 || N > INT32_MAX - 4096 || K > INT32_MAX - 4096)  // (a tile's last row and column fit 32 bits)
         return HC_ERR_UNSUPPORTED;
     // sizes that no device memory holds (and whose tile counts would not fit 32 bits)
     const int64_t most = (int64_t)1 << 40;

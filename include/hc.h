@@ -466,8 +466,8 @@ hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr
  *   on) are left as they are, or with zero_rest written as zeros.
  *   g_y [n, N] of type, rows g_stride >= N apart                             in
  *   g_w [experts, N, K] (transposed: [experts, K, N]) of g_type: type or fp32    out
- * type is HC_BF16 or HC_F16.  experts <= 1024; n < 2^31 - 4096; N and K multiples of 8; x, g_y and w
- * start on 16 bytes and x_stride, g_stride are multiples of 8 (the tensor
+ * type is HC_BF16 or HC_F16.  experts <= 1024; n, N and K < 2^31 - 4096; N and K multiples of 8; x, g_y
+ * and w start on 16 bytes and x_stride, g_stride are multiples of 8 (the tensor
  * copies' rule; HC_ERR_UNSUPPORTED, HC_ERR_MISALIGNED otherwise).
  */
 hc_status hc_grouped_mm(const void *x, int64_t x_stride, const void *w, int transposed,

@@ -27,6 +27,8 @@ def _mm(**kw):
     (dict(n=-1), 1), (dict(experts=0), 1), (dict(N=0), 1), (dict(K=-8), 1), (dict(type=5), 1), (dict(yt=-1), 1),
     (dict(type=F32, yt=F32), 2), (dict(type=F16), 2), (dict(experts=1025), 2), (dict(N=33, ys=40), 2), (dict(K=63), 2),
     (dict(n=1 << 31), 2), (dict(n=(1 << 31) - 1), 2), (dict(xs=68), 2), (dict(xs=1 << 38), 2), (dict(N=1 << 30, K=1 << 30, xs=1 << 30, ys=1 << 30), 2),
+    (dict(n=1, experts=1, N=(1 << 31) - 8, K=8, xs=8, ys=(1 << 31) - 8), 2),
+    (dict(n=1, experts=1, N=8, K=(1 << 31) - 8, xs=(1 << 31) - 8, ys=8), 2),
     (dict(xs=56), 1), (dict(ys=31), 1), (dict(x=None), 1), (dict(w=None), 1), (dict(offsets=None), 1), (dict(y=None), 1),
     (dict(x=A + 8), 3), (dict(w=A + STEP + 2), 3), (dict(offsets=A + 2 * STEP + 2), 3), (dict(y=A + 3 * STEP + 1), 3),
     (dict(yt=F32, y=A + 3 * STEP + 2), 3),
@@ -46,6 +48,7 @@ def _weights(**kw):
 
 @pytest.mark.parametrize("kw,expect", [
     (dict(n=-1), 1), (dict(experts=-3), 1), (dict(gt=9), 1), (dict(gt=BF16), 2), (dict(type=F32), 2), (dict(N=36, gs=40), 2),
+    (dict(n=1, experts=1, N=(1 << 31) - 8, K=8, gs=(1 << 31) - 8, xs=8), 2),
     (dict(gs=24), 1), (dict(gs=36), 2), (dict(xs=65), 2), (dict(g=None), 1), (dict(gw=None), 1), (dict(offsets=None), 1),
     (dict(g=A + 2), 3), (dict(x=A + STEP + 8), 3), (dict(gw=A + 3 * STEP + 2), 3),
     (dict(gw=A + 32), 4), (dict(gw=A + 2 * STEP), 4),
