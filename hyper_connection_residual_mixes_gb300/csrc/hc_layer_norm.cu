@@ -10,7 +10,9 @@
 //
 // Both directions move each row across HBM once and are bound by that: 65,536 rows
 // of 5,120 bf16 take 207 us forward (0.95 of the measured copy rate), 8,192 rows
-// with fp32 gradients 71 us backward (0.87; 4 of them for the column sums).
+// with fp32 gradients 70 us backward (0.89; 4 of them for the column sums).  Rows that
+// start anywhere take the same way, with accesses of one or two values: 65,536 rows of
+// 5,119 bf16 395 us, bound by the loads' and stores' issue.
 #include <atomic>
 
 #include <cuda.h>
@@ -22,8 +24,7 @@
 namespace hc {
 
 namespace ln {
-
-constexpr int kSlots = 4;  // most ring slots (more made the backward slower, 73.2 against 71.9 us, the forward no faster)
+constexpr int kSlots = 6;  // most ring slots (the backward at 5120 columns: 4 80, 6 69.5, 8 70.4 us)
 
 // a parameter value (norm_w, norm_b): fp32 or 16 bits, by its type code
 __device__ __forceinline__ float param(const void *p, int type, int i) {
@@ -244,10 +245,10 @@ k_layer_norm_warps(const T *__restrict__ x, int64_t xs, const void *__restrict__
 }
 
 // ------------------------------------------------------------ rows through a ring
-// Long aligned rows, many of them: a block keeps its columns' weights in
-// registers and walks over rows, which bulk copies bring into a ring of
-// shared-memory slots ahead of it (one thread issues them; the block barrier
-// of a row's reduction says that a slot has been read).
+// Long rows, many of them: a block keeps its columns' weights in registers and
+// walks over rows, which bulk copies bring into a ring of shared-memory slots
+// ahead of it (one thread issues them; the block barrier of a row's reduction
+// says that a slot has been read).
 struct Ring {
     uint64_t full[kSlots];
     volatile int abort;
@@ -287,62 +288,172 @@ __device__ __forceinline__ void ring_leave(Ring &r, int64_t its, int slots) {
             }
 }
 
-// kFull: the block's threads hold exactly d columns, 16 each.  R rows go through
-// a pass together, so that their reductions overlap and share the barrier.  Mean
-// and sum of squares are taken per warp first (about the warp's own mean), then
-// joined over the warps, so that a pass costs one block barrier:
+// Room of a row of d values of `size` bytes in a slot.  Bulk copies move whole
+// blocks of 16 bytes; a row that starts anywhere is copied with the blocks it
+// begins and ends in.
+__host__ __device__ constexpr uint32_t room_of(int d, int size, bool anywhere) {
+    return anywhere ? ((uint32_t)(d * size) + 15u & ~15u) + 16u : (uint32_t)(d * size);
+}
+// The rows of a tensor, from the first value of the first row to the last of the last.
+template <typename T, bool kAnywhere>
+struct Rows {
+    const T *x;
+    int64_t stride, n;
+    int d;
+    // A row's copy: whole blocks [from, from + bytes), `skip` bytes into the slot.
+    struct Copy {
+        const uint8_t *from;
+        uint32_t bytes, skip;
+    };
+    __device__ __forceinline__ const T *row(int64_t r) const { return x + r * stride; }
+    // the row where it lies in its slot
+    __device__ __forceinline__ const T *in(const uint8_t *slot, int64_t r) const {
+        return reinterpret_cast<const T *>(slot + (kAnywhere ? reinterpret_cast<uintptr_t>(row(r)) & 15u : 0u));
+    }
+    // Nothing before the first row's start or behind the last one's end is read: the
+    // values of the blocks that reach there are fetched one by one, here.
+    __device__ __forceinline__ Copy copy(int64_t r, uint8_t *slot) const {
+        const uintptr_t first = reinterpret_cast<uintptr_t>(row(r)), end = first + (uint32_t)d * sizeof(T);
+        if (!kAnywhere) return Copy{reinterpret_cast<const uint8_t *>(first), (uint32_t)d * (uint32_t)sizeof(T), 0u};
+        const uintptr_t base = first & ~(uintptr_t)15;
+        uintptr_t lo = base, hi = (end + 15) & ~(uintptr_t)15;
+        if (lo < reinterpret_cast<uintptr_t>(x)) {
+            lo += 16;
+            for (uintptr_t q = first; q < lo; q += sizeof(T))
+                *reinterpret_cast<T *>(slot + (q - base)) = *reinterpret_cast<const T *>(q);
+        }
+        if (hi > reinterpret_cast<uintptr_t>(row(n - 1) + d)) {
+            hi -= 16;
+            for (uintptr_t q = hi; q < end; q += sizeof(T))
+                *reinterpret_cast<T *>(slot + (q - base)) = *reinterpret_cast<const T *>(q);
+        }
+        return Copy{reinterpret_cast<const uint8_t *>(lo), (uint32_t)(hi - lo), (uint32_t)(lo - base)};
+    }
+};
+
+// A thread's share of a row: NV runs of V values, run i from column (t + i tpr) V
+// on, worked on in pieces of Q pairs: a run, or with V = 1 two runs, of which the
+// second may be behind the row.  kFull: the block's threads hold exactly d columns.
+// kSelect (V = 1): no branch around a piece that is behind the row, its values read
+// as zero and are not stored (20,000 rows of 12,287 bf16 forward 428 us, with the
+// branch 671; 6,705 rows of 5,983 fp32 backward 113 us, with the branch 88).
+template <int V, int NV, bool kFull, bool kSelect>
+struct Share {
+    static constexpr int Q = V == 1 ? 1 : V / 2, kPieces = V * NV / 2 / Q;
+    int t, tpr, d;
+    // the share's first column, a piece's distance from it and a piece's first column
+    __device__ __forceinline__ int start() const { return t * V; }
+    __device__ __forceinline__ int ahead(int i) const { return V == 1 ? 2 * i * tpr : i * tpr * V; }
+    __device__ __forceinline__ int column(int i) const { return start() + ahead(i); }
+    __device__ __forceinline__ bool has(int i) const { return kFull || (kSelect && V == 1) || column(i) < d; }
+    __device__ __forceinline__ bool first(int i) const { return !kSelect || column(i) < d; }
+    __device__ __forceinline__ bool second(int i) const { return column(i) + tpr < d; }
+    // a piece that is there; `mine` is the share's start in the row
+    template <typename T>
+    __device__ __forceinline__ void load(const T *mine, int i, f32x2 *o) const {
+        const T *q = mine + ahead(i);
+        if constexpr (V == 1) {
+            o[0] = f2_make(first(i) ? to_f(q[0]) : 0.0f, second(i) ? to_f(q[tpr]) : 0.0f);
+        } else {
+            const Vec<T, V> u = *reinterpret_cast<const Vec<T, V> *>(q);
+#pragma unroll
+            for (int k = 0; k < Q; ++k) o[k] = pair(u, 2 * k);
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T *mine, int i, const f32x2 *o) const {
+        T *q = mine + ahead(i);
+        if constexpr (V == 1) {
+            float a, b;
+            f2_split(o[0], a, b);
+            if (first(i)) q[0] = from_f<T>(a);
+            if (second(i)) q[tpr] = from_f<T>(b);
+        } else {
+            Vec<T, V> u;
+#pragma unroll
+            for (int k = 0; k < Q; ++k) put_pair(u, 2 * k, o[k]);
+            *reinterpret_cast<Vec<T, V> *>(q) = u;
+        }
+    }
+    __device__ __forceinline__ void weights(const void *w, int type, f32x2 *o) const {  // of all pieces
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int c = column(i);
+            if constexpr (V == 1) {
+                o[i] = f2_make(c < d ? param(w, type, c) : 0.0f, second(i) ? param(w, type, c + tpr) : 0.0f);
+            } else {
+                float f[V] = {};
+                if (has(i)) params<V>(w, type, c, f);
+#pragma unroll
+                for (int k = 0; k < Q; ++k) o[i * Q + k] = f2_make(f[2 * k], f[2 * k + 1]);
+            }
+        }
+    }
+    // v, with zeros for absent values
+    __device__ __forceinline__ f32x2 keep(int i, f32x2 v) const {
+        if (kFull || V > 1) return v;
+        float a, b;
+        f2_split(v, a, b);
+        return f2_make(first(i) ? a : 0.0f, second(i) ? b : 0.0f);
+    }
+    // how many columns of the row a warp has
+    __device__ __forceinline__ float of_warp(int warp) const {
+        if (kFull) return (float)(32 * V * NV);
+        int c = 0;
+        for (int i = 0; i < NV; ++i) {
+            const int left = d - (i * tpr + 32 * warp) * V;
+            c += left < 0 ? 0 : left > 32 * V ? 32 * V : left;
+        }
+        return (float)c;
+    }
+};
+
+// 16 columns a thread, in runs of V: 16 bytes, or (rows that start anywhere) one or
+// two values.  R rows go through a pass together, so that their reductions overlap
+// and share the barrier.  Mean and sum of squares are taken per warp first (about
+// the warp's own mean), then joined over the warps, so that a pass costs one block
+// barrier:
 //   mean = sum c_w m_w / d,  M2 = sum M2_w + c_w (m_w - mean)^2.
-template <typename T, int NV, int R, bool kFull, int kMaxThreads, int kMinBlocks>
+template <typename T, int V, int R, bool kFull, int kMaxThreads, int kMinBlocks>
 __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
 k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ w, const void *__restrict__ b, int wt,
                   int64_t n, int d, float eps, T *__restrict__ y, int64_t ys, float *__restrict__ mean_out,
                   float *__restrict__ rstd_out, int slots) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr bool kAnywhere = V * sizeof(T) < 16;
+    constexpr int P = 8;
     extern __shared__ __align__(16) uint8_t s_rows[];
     __shared__ Ring ring;
     __shared__ float2 red[2][R][32];
     const int t = threadIdx.x, tpr = blockDim.x, warp = t >> 5, lane = t & 31, nw = tpr >> 5;
-    const uint32_t row_bytes = (uint32_t)d * sizeof(T);
+    using Own = Share<V, 16 / V, kFull, true>;
+    constexpr int Q = Own::Q, kPieces = Own::kPieces;
+    const Own own{t, tpr, d};
+    const Rows<T, kAnywhere> in{x, xs, n, d};
+    const uint32_t slot_bytes = room_of(d, sizeof(T), kAnywhere);
     ring_init(ring, slots);
     const int64_t rows = (n - 1 - blockIdx.x) / gridDim.x + 1;  // of this block (the grid has at most n)
     const auto fetch = [&](int slot, int64_t it) {
         const uint32_t bar = smem_u32(&ring.full[slot]);
-        mbar_arrive_expect_tx(bar, row_bytes);
-        bulk_load(smem_u32(s_rows) + (uint32_t)slot * row_bytes, x + (blockIdx.x + it * gridDim.x) * xs, row_bytes, bar);
+        uint8_t *at = s_rows + (uint32_t)slot * slot_bytes;
+        const auto c = in.copy(blockIdx.x + it * gridDim.x, at);
+        mbar_arrive_expect_tx(bar, c.bytes);
+        bulk_load(smem_u32(at) + c.skip, c.from, c.bytes, bar);
     };
     if (t == 0)
         for (int it = 0; it < slots && it < rows; ++it) fetch(it, it);
     const float inv_d = 1.0f / (float)d;
-    f32x2 wv[NV][V / 2], bv[NV][V / 2];
-    const auto columns_of = [&](int wp) {  // of a warp
-        int c = 0;
-        for (int i = 0; i < NV; ++i) {
-            const int left = d - (i * tpr + 32 * wp) * V;
-            c += left < 0 ? 0 : left > 32 * V ? 32 * V : left;
-        }
-        return c;
-    };
-    const float own = kFull ? (float)(32 * V * NV) : (float)columns_of(warp);
-    const float inv_own = own > 0.0f ? 1.0f / own : 0.0f;
-    // what lane w weighs warp w's mean with
-    const float weight = lane < nw ? (kFull ? (float)(32 * V * NV) : (float)columns_of(lane)) : 0.0f;
+    const float mine = own.of_warp(warp), inv_mine = mine > 0.0f ? 1.0f / mine : 0.0f;
+    const float weight = lane < nw ? own.of_warp(lane) : 0.0f;  // what lane w weighs warp w's mean with
+    f32x2 wv[P], bv[P];
+    own.weights(w, wt, wv);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * tpr) * V;
-        float f[V] = {}, h[V] = {};
-        if (kFull || c < d) {
-            params<V>(w, wt, c, f);
-            if (b) params<V>(b, wt, c, h);
-        }
-#pragma unroll
-        for (int k = 0; k < V / 2; ++k) wv[i][k] = f2_make(f[2 * k], f[2 * k + 1]), bv[i][k] = f2_make(h[2 * k], h[2 * k + 1]);
-    }
+    for (int p = 0; p < P; ++p) bv[p] = f2_dup(0.0f);
+    if (b) own.weights(b, wt, bv);
     Place place;
-    const T *own_cols = reinterpret_cast<const T *>(s_rows) + t * V;
-    T *yr = y + blockIdx.x * ys + t * V;
+    T *yr = y + blockIdx.x * ys + own.start();
     int buf = 0;
     for (int64_t it = 0; it < rows; it += R, buf ^= 1) {
-        f32x2 v[R][NV][V / 2];
+        f32x2 v[R][P];
         float m_w[R], m2_w[R];
         const Place first = place;
 #pragma unroll
@@ -350,34 +461,32 @@ k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ 
             m_w[r] = m2_w[r] = 0.0f;
             if (it + r >= rows) break;  // the block's last pass
             ring_wait(ring, place);
-            const T *xr = own_cols + place.slot * d;
+            const T *xr = in.in(s_rows + (uint32_t)place.slot * slot_bytes, blockIdx.x + (it + r) * gridDim.x) + own.start();
             place.next(slots);
             f32x2 acc = f2_dup(0.0f);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (!kFull && (t + i * tpr) * V >= d) continue;
-                const Vec<T, V> u = *reinterpret_cast<const Vec<T, V> *>(xr + i * tpr * V);
+            for (int i = 0; i < kPieces; ++i) {
+                if (!own.has(i)) continue;
+                own.load(xr, i, v[r] + i * Q);
 #pragma unroll
-                for (int k = 0; k < V / 2; ++k) {
-                    v[r][i][k] = pair(u, 2 * k);
-                    acc = f2_add(acc, v[r][i][k]);
-                }
+                for (int p = i * Q; p < (i + 1) * Q; ++p) acc = f2_add(acc, v[r][p]);
             }
             m_w[r] = f2_hsum(acc);
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r) m_w[r] = warp_sum(m_w[r]) * inv_own;
+        for (int r = 0; r < R; ++r) m_w[r] = warp_sum(m_w[r]) * inv_mine;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const f32x2 neg = f2_dup(-m_w[r]);
             f32x2 acc = f2_dup(0.0f);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (!kFull && (t + i * tpr) * V >= d) continue;
+            for (int i = 0; i < kPieces; ++i) {
+                if (!own.has(i)) continue;
 #pragma unroll
-                for (int k = 0; k < V / 2; ++k) {
-                    v[r][i][k] = f2_add(v[r][i][k], neg);
-                    acc = f2_fma(v[r][i][k], v[r][i][k], acc);
+                for (int p = i * Q; p < (i + 1) * Q; ++p) {
+                    v[r][p] = f2_add(v[r][p], neg);
+                    const f32x2 c = own.keep(i, v[r][p]);
+                    acc = f2_fma(c, c, acc);
                 }
             }
             m2_w[r] = f2_hsum(acc);
@@ -408,12 +517,11 @@ k_layer_norm_ring(const T *__restrict__ x, int64_t xs, const void *__restrict__ 
             if (it + r >= rows) break;
             const f32x2 rs = f2_dup(rstd[r]), shift = f2_dup((m_w[r] - mean[r]) * rstd[r]);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (!kFull && (t + i * tpr) * V >= d) continue;
-                Vec<T, V> o;
+            for (int i = 0; i < kPieces; ++i) {
+                if (!own.has(i)) continue;
 #pragma unroll
-                for (int k = 0; k < V / 2; ++k) put_pair(o, 2 * k, f2_fma(f2_fma(v[r][i][k], rs, shift), wv[i][k], bv[i][k]));
-                *reinterpret_cast<Vec<T, V> *>(yr + i * tpr * V) = o;
+                for (int p = i * Q; p < (i + 1) * Q; ++p) v[r][p] = f2_fma(f2_fma(v[r][p], rs, shift), wv[p], bv[p]);
+                own.store(yr, i, v[r] + i * Q);
             }
             yr += gridDim.x * ys;
             if (t == 0) {
@@ -615,111 +723,145 @@ k_ln_backward_wide(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__
         }
 }
 
-// The same with the rows of x and g through a ring.  Each thread owns 4 columns in
-// each of NV places; both passes over a row read it from its slot, which is
-// filled again once the next row's barrier has passed.
-template <typename TX, typename TG, int NV, bool kFull, int kMaxThreads, int kMinBlocks>
-__global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
+// The same with the rows of x and g through a ring: 8 columns a thread in runs of V
+// (4 where rows take bulk copies as they are, else 1 or 2), R rows a pass.  Both
+// passes over a row read it from its slot, which is filled again once the next
+// pass's barrier has passed.
+template <typename TX, typename TG, int V, int R, bool kFull, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, 1)
 k_ln_backward_ring(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, int64_t xs,
                    const void *__restrict__ w, int wt, const float *__restrict__ mean_in,
                    const float *__restrict__ rstd_in, int64_t n, int d, TG *__restrict__ gx, int64_t gxs,
                    float *__restrict__ part, int slots) {
-    constexpr int V = 4;
+    constexpr bool kAnywhere = V < 4;
+    constexpr int P = 4;
     extern __shared__ __align__(16) uint8_t s_rows[];
     __shared__ Ring ring;
-    __shared__ float2 red[2][32];
+    __shared__ float2 red[2][R][32];
     const int t = threadIdx.x, tpr = blockDim.x, warp = t >> 5, lane = t & 31, nw = tpr >> 5;
-    const uint32_t x_bytes = (uint32_t)d * sizeof(TX), g_bytes = (uint32_t)d * sizeof(TG), slot_bytes = x_bytes + g_bytes;
+    using Own = Share<V, 8 / V, kFull, false>;
+    constexpr int Q = Own::Q, kPieces = Own::kPieces;
+    const Own own{t, tpr, d};
+    const Rows<TX, kAnywhere> xin{x, xs, n, d};
+    const Rows<TG, kAnywhere> gin{gy, gs, n, d};
+    const uint32_t x_room = room_of(d, sizeof(TX), kAnywhere), slot_bytes = x_room + room_of(d, sizeof(TG), kAnywhere);
     const float inv_d = 1.0f / (float)d;
     ring_init(ring, slots);
     const int64_t rows = (n - 1 - blockIdx.x) / gridDim.x + 1;
     const auto fetch = [&](int slot, int64_t it) {
-        const uint32_t bar = smem_u32(&ring.full[slot]), at = smem_u32(s_rows) + (uint32_t)slot * slot_bytes;
+        const uint32_t bar = smem_u32(&ring.full[slot]);
+        uint8_t *at = s_rows + (uint32_t)slot * slot_bytes;
         const int64_t row = blockIdx.x + it * gridDim.x;
-        mbar_arrive_expect_tx(bar, slot_bytes);
-        bulk_load(at, x + row * xs, x_bytes, bar);
-        bulk_load(at + x_bytes, gy + row * gs, g_bytes, bar);
+        const auto a = xin.copy(row, at);
+        const auto g = gin.copy(row, at + x_room);
+        mbar_arrive_expect_tx(bar, a.bytes + g.bytes);
+        bulk_load(smem_u32(at) + a.skip, a.from, a.bytes, bar);
+        bulk_load(smem_u32(at) + x_room + g.skip, g.from, g.bytes, bar);
     };
     if (t == 0)
         for (int it = 0; it < slots && it < rows; ++it) fetch(it, it);
-    Place place;
-    f32x2 wv[NV][V / 2], aw[NV][V / 2], ab[NV][V / 2];
+    Place place, before;
+    f32x2 wv[P], aw[P], ab[P];
+    own.weights(w, wt, wv);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * tpr) * V;
-        float f[V] = {};
-        if (kFull || c < d) params<V>(w, wt, c, f);
+    for (int p = 0; p < P; ++p) aw[p] = ab[p] = f2_dup(0.0f);
+    float mean_next[R], rstd_next[R];
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k) {
-            wv[i][k] = f2_make(f[2 * k], f[2 * k + 1]);
-            aw[i][k] = ab[i][k] = f2_dup(0.0f);
-        }
+    for (int r = 0; r < R; ++r) {
+        mean_next[r] = rstd_next[r] = 0.0f;
+        if (r < rows) mean_next[r] = __ldg(mean_in + blockIdx.x + r * gridDim.x), rstd_next[r] = __ldg(rstd_in + blockIdx.x + r * gridDim.x);
     }
-    float mean_next = __ldg(mean_in + blockIdx.x), rstd_next = __ldg(rstd_in + blockIdx.x);
-    for (int64_t it = 0; it < rows; ++it) {
-        const int64_t row = blockIdx.x + it * gridDim.x;
-        const float mean = mean_next, rstd = rstd_next;
-        if (it + 1 < rows) mean_next = __ldg(mean_in + row + gridDim.x), rstd_next = __ldg(rstd_in + row + gridDim.x);
-        const f32x2 neg = f2_dup(-mean), rs = f2_dup(rstd);
-        ring_wait(ring, place);
-        const uint8_t *slot = s_rows + (uint32_t)place.slot * slot_bytes;
-        const TX *xr = reinterpret_cast<const TX *>(slot);
-        const TG *gr = reinterpret_cast<const TG *>(slot + x_bytes);
-        f32x2 a1 = f2_dup(0.0f), a2 = f2_dup(0.0f);
+    int buf = 0;
+    for (int64_t it = 0; it < rows; it += R, buf ^= 1) {
+        float mean[R], rstd[R], s1[R], s2[R];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t + i * tpr) * V;
-            if (!kFull && c >= d) continue;
-            const Vec<TX, V> xv = *reinterpret_cast<const Vec<TX, V> *>(xr + c);
-            const Vec<TG, V> gv = *reinterpret_cast<const Vec<TG, V> *>(gr + c);
-#pragma unroll
-            for (int k = 0; k < V; k += 2) {
-                const f32x2 xh = f2_mul(f2_add(pair(xv, k), neg), rs), g = pair(gv, k);
-                const f32x2 wg = f2_mul(g, wv[i][k / 2]);
-                a1 = f2_add(a1, wg);
-                a2 = f2_fma(wg, xh, a2);
-                aw[i][k / 2] = f2_fma(g, xh, aw[i][k / 2]);
-                ab[i][k / 2] = f2_add(ab[i][k / 2], g);
-            }
+        for (int r = 0; r < R; ++r) {
+            mean[r] = mean_next[r], rstd[r] = rstd_next[r];
+            const int64_t next = blockIdx.x + (it + R + r) * gridDim.x;
+            if (it + R + r < rows) mean_next[r] = __ldg(mean_in + next), rstd_next[r] = __ldg(rstd_in + next);
         }
-        float s1 = warp_sum(f2_hsum(a1)), s2 = warp_sum(f2_hsum(a2));
-        // (two buffers: a warp writes the next row's sums while a slow one still reads these)
-        if (lane == 0) red[it & 1][warp] = make_float2(s1, s2);
-        __syncthreads();
-        // every thread is done with the row before: its slot can be filled again
-        if (t == 0 && it > 0 && it - 1 + slots < rows) fetch(place.slot ? place.slot - 1 : slots - 1, it - 1 + slots);
-        place.next(slots);
-        const float2 r = lane < nw ? red[it & 1][lane] : make_float2(0.0f, 0.0f);
-        s1 = warp_sum(r.x), s2 = warp_sum(r.y);
-        const f32x2 m1 = f2_dup(-s1 * inv_d), m2 = f2_dup(-s2 * inv_d);
-        TG *o_row = gx + row * gxs;
+        const Place first = place;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t + i * tpr) * V;
-            if (!kFull && c >= d) continue;
-            const Vec<TX, V> xv = *reinterpret_cast<const Vec<TX, V> *>(xr + c);
-            const Vec<TG, V> gv = *reinterpret_cast<const Vec<TG, V> *>(gr + c);
-            Vec<TG, V> o;
+        for (int r = 0; r < R; ++r) {
+            s1[r] = s2[r] = 0.0f;
+            if (it + r >= rows) break;  // the block's last pass
+            ring_wait(ring, place);
+            const uint8_t *slot = s_rows + (uint32_t)place.slot * slot_bytes;
+            const int64_t row = blockIdx.x + (it + r) * gridDim.x;
+            place.next(slots);
+            const TX *xr = xin.in(slot, row) + own.start();
+            const TG *gr = gin.in(slot + x_room, row) + own.start();
+            f32x2 a1 = f2_dup(0.0f), a2 = f2_dup(0.0f);
+            const f32x2 neg = f2_dup(-mean[r]), rs = f2_dup(rstd[r]);
 #pragma unroll
-            for (int k = 0; k < V; k += 2) {
-                const f32x2 xh = f2_mul(f2_add(pair(xv, k), neg), rs);
-                put_pair(o, k, f2_mul(rs, f2_fma(xh, m2, f2_fma(pair(gv, k), wv[i][k / 2], m1))));
+            for (int i = 0; i < kPieces; ++i) {
+                if (!own.has(i)) continue;
+                f32x2 xv[Q], gv[Q];
+                own.load(xr, i, xv);
+                own.load(gr, i, gv);
+#pragma unroll
+                for (int k = 0; k < Q; ++k) {
+                    const int p = i * Q + k;
+                    const f32x2 xh = own.keep(i, f2_mul(f2_add(xv[k], neg), rs)), wg = f2_mul(gv[k], wv[p]);
+                    a1 = f2_add(a1, wg);
+                    a2 = f2_fma(wg, xh, a2);
+                    aw[p] = f2_fma(gv[k], xh, aw[p]);
+                    ab[p] = f2_add(ab[p], gv[k]);
+                }
             }
-            *reinterpret_cast<Vec<TG, V> *>(o_row + c) = o;
+            s1[r] = f2_hsum(a1), s2[r] = f2_hsum(a2);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) s1[r] = warp_sum(s1[r]), s2[r] = warp_sum(s2[r]);
+        // (two buffers: a warp writes the next pass's sums while a slow one still reads these)
+        if (lane == 0)
+#pragma unroll
+            for (int r = 0; r < R; ++r) red[buf][r][warp] = make_float2(s1[r], s2[r]);
+        __syncthreads();
+        if (t == 0 && it > 0) {  // every thread is done with the rows before: their slots can be filled again
+            Place q = before;
+#pragma unroll
+            for (int r = 0; r < R; ++r, q.next(slots))
+                if (it - R + r + slots < rows) fetch(q.slot, it - R + r + slots);
+        }
+        before = first;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float2 q = lane < nw ? red[buf][r][lane] : make_float2(0.0f, 0.0f);
+            s1[r] = warp_sum(q.x), s2[r] = warp_sum(q.y);
+        }
+        Place here = first;
+#pragma unroll
+        for (int r = 0; r < R; ++r, here.next(slots)) {
+            if (it + r >= rows) break;
+            const uint8_t *slot = s_rows + (uint32_t)here.slot * slot_bytes;
+            const int64_t row = blockIdx.x + (it + r) * gridDim.x;
+            const TX *xr = xin.in(slot, row) + own.start();
+            const TG *gr = gin.in(slot + x_room, row) + own.start();
+            TG *o_row = gx + row * gxs + own.start();
+            const f32x2 neg = f2_dup(-mean[r]), rs = f2_dup(rstd[r]);
+            const f32x2 m1 = f2_dup(-s1[r] * inv_d), m2 = f2_dup(-s2[r] * inv_d);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                if (!own.has(i)) continue;
+                f32x2 xv[Q], gv[Q];
+                own.load(xr, i, xv);
+                own.load(gr, i, gv);
+#pragma unroll
+                for (int k = 0; k < Q; ++k)
+                    gv[k] = f2_mul(rs, f2_fma(f2_mul(f2_add(xv[k], neg), rs), m2, f2_fma(gv[k], wv[i * Q + k], m1)));
+                own.store(o_row, i, gv);
+            }
         }
     }
     ring_leave(ring, rows, slots);
     launch_dependents();
-    float *pw = part + (int64_t)blockIdx.x * 2 * d, *pb = pw + d;
+    float *pw = part + (int64_t)blockIdx.x * 2 * d + own.start();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * tpr) * V;
-        if (c >= d) continue;
-        Vec<float, V> o;
-        put_pair(o, 0, aw[i][0]), put_pair(o, 2, aw[i][1]);
-        *reinterpret_cast<Vec<float, V> *>(pw + c) = o;
-        put_pair(o, 0, ab[i][0]), put_pair(o, 2, ab[i][1]);
-        *reinterpret_cast<Vec<float, V> *>(pb + c) = o;
+    for (int i = 0; i < kPieces; ++i) {
+        if (!own.has(i)) continue;
+        own.store(pw, i, aw + i * Q);
+        own.store(pw + d, i, ab + i * Q);
     }
 }
 
@@ -825,14 +967,14 @@ cudaError_t fwd_vec(const FwdCall &c) {
 // Slots of a ring and blocks of a launch: as many slots as fit beside the SM's
 // other blocks, and a grid that fills the SMs once.
 template <auto kKernel>
-cudaError_t ring_shape(int threads, int slot_bytes, int64_t rows, int64_t most, int *slots, int *blocks) {
+cudaError_t ring_shape(int threads, int slot_bytes, int least, int best, int64_t rows, int64_t most, int *slots, int *blocks) {
     int per_sm = 0;
     const cudaError_t e = blocks_per_sm<kKernel>(threads, &per_sm);
     if (e != cudaSuccess) return e;
     const int extra = 2048;  // a block's other shared memory
-    while (per_sm > 1 && (kSmemSm / per_sm - extra) / slot_bytes < 3) --per_sm;
+    while (per_sm > 1 && (kSmemSm / per_sm - extra) / slot_bytes < least) --per_sm;
     const int room = (per_sm > 1 ? kSmemSm / per_sm : kSmemBlock) - extra;
-    *slots = room / slot_bytes < kSlots ? room / slot_bytes : kSlots;
+    *slots = room / slot_bytes < best ? room / slot_bytes : best;
     int64_t grid = (int64_t)per_sm * sm_count_of_device();
     if (grid > most) grid = most;
     if (grid > rows) grid = rows;
@@ -841,39 +983,47 @@ cudaError_t ring_shape(int threads, int slot_bytes, int64_t rows, int64_t most, 
 }
 
 template <auto kKernel, typename T>
-cudaError_t fwd_ring_launch(const FwdCall &c, int threads) {
+cudaError_t fwd_ring_launch(const FwdCall &c, int threads, int room) {
     int slots = 0, blocks = 0;
-    const cudaError_t e = ring_shape<kKernel>(threads, c.d * (int)sizeof(T), c.n, INT32_MAX, &slots, &blocks);
+    const cudaError_t e = ring_shape<kKernel>(threads, room, 3, 4, c.n, INT32_MAX, &slots, &blocks);
     if (e != cudaSuccess) return e;
-    kKernel<<<blocks, threads, slots * c.d * sizeof(T), c.s>>>(static_cast<const T *>(c.x), c.xs, c.w, c.b, c.wt, c.n, c.d,
-                                                               c.eps, static_cast<T *>(c.y), c.ys, c.mean, c.rstd, slots);
+    kKernel<<<blocks, threads, slots * room, c.s>>>(static_cast<const T *>(c.x), c.xs, c.w, c.b, c.wt, c.n, c.d, c.eps,
+                                                    static_cast<T *>(c.y), c.ys, c.mean, c.rstd, slots);
     return cudaGetLastError();
 }
-template <typename T>
+template <typename T, int V>
 cudaError_t fwd_ring(const FwdCall &c) {
-    constexpr int V = 16 / sizeof(T), NV = 16 / V;  // 16 columns a thread
-    const int threads = (c.d + 511) / 512 * 32;
-    if (threads <= 320)
-        return c.d == threads * 16 ? fwd_ring_launch<k_layer_norm_ring<T, NV, 2, true, 320, 2>, T>(c, threads)
-                                   : fwd_ring_launch<k_layer_norm_ring<T, NV, 2, false, 320, 2>, T>(c, threads);
-    if (threads <= 704) return fwd_ring_launch<k_layer_norm_ring<T, NV, 2, false, 704, 1>, T>(c, threads);
-    return fwd_ring_launch<k_layer_norm_ring<T, NV, 1, false, 1024, 1>, T>(c, threads);
+    const int threads = (c.d + 511) / 512 * 32, room = (int)room_of(c.d, sizeof(T), V * sizeof(T) < 16);
+    if (threads <= 320) {
+        if constexpr (V * sizeof(T) == 16)
+            if (c.d == threads * 16) return fwd_ring_launch<k_layer_norm_ring<T, V, 2, true, 320, 2>, T>(c, threads, room);
+        return fwd_ring_launch<k_layer_norm_ring<T, V, 2, false, 320, 2>, T>(c, threads, room);
+    }
+    if (threads <= 704) return fwd_ring_launch<k_layer_norm_ring<T, V, 2, false, 704, 1>, T>(c, threads, room);
+    return fwd_ring_launch<k_layer_norm_ring<T, V, 1, false, 1024, 1>, T>(c, threads, room);
 }
 
 template <typename T>
 cudaError_t fwd_type(const FwdCall &c) {
     constexpr int VEC = 16 / sizeof(T);
     const size_t pa = c.wt == HC_F32 ? 16 : 8;
+    // The ring from 16,384 values an SM on (us, ring and without: 304 rows of 5,120 3.7 and 3.3, 608 rows 4.2
+    // and 5.4, 4,864 rows 17.8 and 35.4; 608 rows of 1,024 3.0 and 2.6, 4,864 rows 5.8 and 6.2; 2,048
+    // rows of 520 4.7 and 3.7, 65,536 rows 49 and 65, of 264 39 and 30; in any place 65,536 rows of 5,119
+    // 390 and 1,046, of 257 53 and 89, 20,000 rows of 12,287 428 and 1,013).
+    const bool many = c.n * c.d >= 16384 * (int64_t)sm_count_of_device();
     if (c.d % VEC == 0 && aligned(c.x, c.xs * (int64_t)sizeof(T), 16) && aligned(c.y, c.ys * (int64_t)sizeof(T), 16) &&
         aligned(c.w, 0, pa) && aligned(c.b, 0, pa)) {
-        // (us, ring and a block per row: 304 rows of 5,120 3.7 and 3.3, 608 rows 4.2 and 5.4, 4,864 rows
-        // 17.8 and 35.4; of 1,024 columns 608 rows 3.0 and 2.6, 4,864 rows 5.8 and 6.2)
-        if (c.d >= 1024 && c.n >= 4 * (int64_t)sm_count_of_device()) return fwd_ring<T>(c);
+        if (c.d > 512 && many) return fwd_ring<T, VEC>(c);
         return fwd_vec<T, VEC>(c);
     }
     // (16-bit rows of even width and spacing: two values at a time)
     if constexpr (sizeof(T) == 2)
-        if (c.d % 2 == 0 && aligned(c.x, c.xs * 2, 4) && aligned(c.y, c.ys * 2, 4)) return fwd_vec<T, 2>(c);
+        if (c.d % 2 == 0 && aligned(c.x, c.xs * 2, 4) && aligned(c.y, c.ys * 2, 4)) {
+            if (c.d > 256 && many) return fwd_ring<T, 2>(c);
+            return fwd_vec<T, 2>(c);
+        }
+    if (c.d > 128 && many) return fwd_ring<T, 1>(c);
     return fwd_vec<T, 1>(c);
 }
 
@@ -933,25 +1083,32 @@ cudaError_t bwd_wide(const BwdCall &c, int threads) {
 }
 
 template <auto kKernel, typename TX, typename TG>
-cudaError_t bwd_ring_launch(const BwdCall &c, int threads) {
-    const int slot = c.d * (int)(sizeof(TX) + sizeof(TG));
+cudaError_t bwd_ring_launch(const BwdCall &c, int threads, int room, int least) {
     int slots = 0, blocks = 0;
-    cudaError_t e = ring_shape<kKernel>(threads, slot, c.n, max_blocks(c.d), &slots, &blocks);
+    cudaError_t e = ring_shape<kKernel>(threads, room, least, kSlots, c.n, max_blocks(c.d), &slots, &blocks);
     if (e != cudaSuccess) return e;
-    kKernel<<<blocks, threads, slots * slot, c.s>>>(
+    kKernel<<<blocks, threads, slots * room, c.s>>>(
         static_cast<const TG *>(c.gy), c.gs, static_cast<const TX *>(c.x), c.xs, c.w, c.wt, c.mean, c.rstd, c.n, c.d,
         static_cast<TG *>(c.gx), c.gxs, c.part, slots);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_columns(c, blocks);
 }
-template <typename TX, typename TG>
+template <typename TX, typename TG, int V>
 cudaError_t bwd_ring(const BwdCall &c) {
-    // 8 columns a thread: one block of 640 threads an SM at 5120 columns (71.9 us for
-    // 8,192 rows; two blocks of 320 threads with 16 columns each 72.7, and twice the partial sums)
     const int threads = (c.d + 255) / 256 * 32;
-    if (threads > 640) return bwd_ring_launch<k_ln_backward_ring<TX, TG, 2, false, 1024, 1>, TX, TG>(c, threads);
-    if (c.d % 256) return bwd_ring_launch<k_ln_backward_ring<TX, TG, 2, false, 640, 1>, TX, TG>(c, threads);
-    return bwd_ring_launch<k_ln_backward_ring<TX, TG, 2, true, 640, 1>, TX, TG>(c, threads);
+    const int room = (int)(room_of(c.d, sizeof(TX), V < 4) + room_of(c.d, sizeof(TG), V < 4));
+    if (threads > 768) return bwd_ring_launch<k_ln_backward_ring<TX, TG, V, 1, false, 1024>, TX, TG>(c, threads, room, 2);
+    if (threads > 640) return bwd_ring_launch<k_ln_backward_ring<TX, TG, V, 1, false, 768>, TX, TG>(c, threads, room, 2);
+    if constexpr (V == 4) {
+        // (us, two rows a pass and one: 8,192 rows of 5,120 with fp32 gradients 70 and 73, all bf16 16,384 rows
+        // 114 and 124, of 4,096 97 and 106, 32,768 rows of 2,560 118 and 122, of 2,048 100 and 96)
+        if (c.d >= 2560) {
+            if (c.d % 256 == 0) return bwd_ring_launch<k_ln_backward_ring<TX, TG, V, 2, true, 640>, TX, TG>(c, threads, room, 4);
+            return bwd_ring_launch<k_ln_backward_ring<TX, TG, V, 2, false, 640>, TX, TG>(c, threads, room, 4);
+        }
+        if (c.d % 256 == 0) return bwd_ring_launch<k_ln_backward_ring<TX, TG, V, 1, true, 640>, TX, TG>(c, threads, room, 2);
+    }
+    return bwd_ring_launch<k_ln_backward_ring<TX, TG, V, 1, false, 640>, TX, TG>(c, threads, room, 2);
 }
 
 template <typename TX, typename TG>
@@ -961,24 +1118,27 @@ cudaError_t bwd_type(const BwdCall &c) {
     if (d % 4 == 0 && d > 128 && aligned(c.x, c.xs * (int64_t)sizeof(TX), 4 * sizeof(TX)) &&
         aligned(c.gy, c.gs * (int64_t)sizeof(TG), 4 * sizeof(TG)) &&
         aligned(c.gx, c.gxs * (int64_t)sizeof(TG), 4 * sizeof(TG)) && aligned(c.w, 0, pa)) {
+        // (us, ring and plain loads: 76 rows of 5,120 6.6 and 9.4, 4,864 rows 45.6 and 84.3; of 1,024
+        // columns 4.5 and 4.9, 13.8 and 15.2; 53,310 rows of 520 fp32 98 and 77; in any place 41,791 rows
+        // of 1,435 fp16 165 and 211, 6,705 of 5,983 fp32 88 and 311, 53,310 of 519 fp32 128 and 104, in pairs 65,536 of 770 bf16 138 and 216)
         const bool bulk = (int64_t)d * sizeof(TX) % 16 == 0 && (int64_t)d * sizeof(TG) % 16 == 0 &&
                           aligned(c.x, c.xs * (int64_t)sizeof(TX), 16) && aligned(c.gy, c.gs * (int64_t)sizeof(TG), 16);
-        // (us, ring and plain loads: 76 rows of 5,120 6.6 and 9.4, 4,864 rows 45.6 and 84.3; of 1,024
-        // columns 4.5 and 4.9, 13.8 and 15.2)
-        if (bulk && d >= 1024 && d <= 8192) return bwd_ring<TX, TG>(c);
+        if (bulk && d >= 1024 && d <= 8192) return bwd_ring<TX, TG, 4>(c);
         if (d <= 256) return bwd_launch<TX, TG, 4, 2>(c, 32);
-        if (d <= 4096) return bwd_launch<TX, TG, 4, 2>(c, (d + 255) / 256 * 32);
-        return bwd_wide<TX, TG, 4, 4>(c, (d + 511) / 512 * 32);
+        if (d < 1024) return bwd_launch<TX, TG, 4, 2>(c, (d + 255) / 256 * 32);
+        if (d > 8192) return bwd_wide<TX, TG, 4, 4>(c, (d + 511) / 512 * 32);
     }
     // (16-bit rows of even width and spacing: two values at a time)
     if constexpr (sizeof(TX) == 2)
         if (d % 2 == 0 && d > 256 && aligned(c.x, c.xs * 2, 4) && aligned(c.gy, c.gs * (int64_t)sizeof(TG), 2 * sizeof(TG)) &&
             aligned(c.gx, c.gxs * (int64_t)sizeof(TG), 2 * sizeof(TG))) {
-            if (d <= 4096) return bwd_launch<TX, TG, 2, 4>(c, (d + 255) / 256 * 32);
+            if (d < 512) return bwd_launch<TX, TG, 2, 4>(c, (d + 255) / 256 * 32);
+            if (d <= 8192) return bwd_ring<TX, TG, 2>(c);
             return bwd_wide<TX, TG, 2, 8>(c, (d + 511) / 512 * 32);
         }
     if (d <= 128) return bwd_launch<TX, TG, 1, 4>(c, 32);
-    if (d <= 4096) return bwd_launch<TX, TG, 1, 8>(c, (d + 255) / 256 * 32);
+    if (d < 1024) return bwd_launch<TX, TG, 1, 8>(c, (d + 255) / 256 * 32);
+    if (d <= 8192) return bwd_ring<TX, TG, 1>(c);
     return bwd_wide<TX, TG, 1, 16>(c, (d + 511) / 512 * 32);
 }
 

@@ -157,6 +157,50 @@ def test_backward(n, d, x, g, w):
     assert torch.equal(got["g_x"], again["g_x"]) and torch.equal(got["g_norm_w"], again["g_norm_w"])
 
 
+@pytest.mark.parametrize("n,d,pitch,lead", [
+    (2500, 1025, 0, 0), (2500, 1026, 0, 0), (2600, 1028, 0, 4), (1800, 1435, 0, 3), (1800, 1438, 2, 2), (900, 2999, 1, 0),
+    (700, 5119, 1, 0), (700, 5119, 0, 1), (600, 5118, 0, 0), (600, 5121, 0, 0), (500, 6143, 8, 5), (400, 7001, 0, 7),
+    (320, 8191, 0, 0), (320, 8190, 4, 2), (300, 9003, 0, 1), (260, 12286, 0, 2), (170, 16383, 0, 0), (19000, 131, 0, 1),
+    (9800, 257, 0, 0), (9700, 258, 2, 0), (5000, 514, 0, 6), (2450, 1023, 0, 1), (6000, 520, 0, 0), (5, 1031, 0, 3), (1, 2049, 0, 5)])
+@pytest.mark.parametrize("x,g", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32")])
+def test_rows_anywhere(n, d, pitch, lead, x, g):
+    """Many rows that start and end inside 16-byte blocks, with NaN in all that is
+    around them (before the first and behind the last row too)."""
+    v, w, b, gr = _inputs(n, d, x, "fp32", g, seed=5)
+
+    def among_nan(t):
+        step = d + pitch
+        buf = torch.full((lead + n * step + 16,), float("nan"), dtype=t.dtype, device="cuda")
+        rows = buf[lead:lead + n * step].view(n, step)[:, :d]
+        rows.copy_(t)
+        return rows
+
+    v, gr = among_nan(v), among_nan(gr)
+    _, mean, rstd = _check_forward(v, w, b)
+    y = among_nan(torch.zeros((n, d), dtype=v.dtype, device="cuda"))
+    hcg.hc_layer_norm(v, w, b, y=y)
+    assert torch.isfinite(y).all()
+    if pitch:
+        assert torch.isnan(y.as_strided((n - 1, pitch), (d + pitch, 1), y.storage_offset() + d)).all()
+    g_x = among_nan(torch.zeros((n, d), dtype=gr.dtype, device="cuda"))
+    got = hcg.hc_layer_norm_backward(gr, v, w, mean, rstd, g_x=g_x)
+    _check_backward(v, w, gr, mean, rstd, got)
+    if pitch:
+        assert torch.isnan(g_x.as_strided((n - 1, pitch), (d + pitch, 1), g_x.storage_offset() + d)).all()
+
+
+@pytest.mark.parametrize("x", ["bf16", "fp32"])
+def test_overlapping_rows_anywhere(x):
+    """Rows that are one another's neighbours by a single value, and one row for all."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    buf = torch.randn((3 + 2000 + 1301,), generator=gen, device="cuda").to(T[x])
+    w, b = torch.rand((1301,), generator=gen, device="cuda"), torch.rand((1301,), generator=gen, device="cuda")
+    for step in (0, 1):
+        rows = buf.as_strided((2000, 1301), (step, 1), 3)
+        _, mean, rstd = _check_forward(rows, w, b)
+        _check_backward(rows, w, torch.randn((2000, 1301), generator=gen, device="cuda"), mean, rstd)
+
+
 def test_gradients_against_differences():
     """Central differences of the kernel's own forward, in 32 bits, along random
     directions: they may be off by the forward's error over the step, and by
