@@ -649,10 +649,15 @@ hc_status hc_grouped_mm(const void *x, int64_t x_stride, const void *w, int tran
                                              y_stride, y_type == HC_F32, zero_rest != 0, stream));
 }
 
+size_t hc_grouped_mm_weights_workspace_bytes(int64_t n, int experts, int N, int K) {
+    if (check_grouped(n, experts, N, K, HC_BF16, HC_F32) != HC_OK) return 0;
+    return hc::grouped_mm_weights_workspace_bytes(n, experts, N, K);
+}
+
 hc_status hc_grouped_mm_weights(const void *g_y, int64_t g_stride, const void *x, int64_t x_stride,
                                 const int32_t *offsets, int64_t n, int experts, int N, int K,
                                 hc_dtype type, void *g_w, int transposed, hc_dtype g_type,
-                                cudaStream_t stream) {
+                                void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     hc_status st = check_grouped(n, experts, N, K, type, g_type);
     if (st != HC_OK) return st;
     if (x_stride < K || g_stride < N || !rows_fit(n, K, x_stride) || !rows_fit(n, N, g_stride)) return HC_ERR_INVALID_ARG;
@@ -662,16 +667,21 @@ hc_status hc_grouped_mm_weights(const void *g_y, int64_t g_stride, const void *x
     if (!aligned16(g_y) || !aligned16(x) || !aligned_to(offsets, 4) || !aligned_to(g_w, size_of(g_type)))
         return HC_ERR_MISALIGNED;
     const int64_t bytes = (int64_t)experts * N * K * size_of(g_type);
+    const size_t need = hc::grouped_mm_weights_workspace_bytes(n, experts, N, K);
+    if (need && (!workspace || workspace_bytes < need)) return HC_ERR_INVALID_ARG;
+    if (need && !aligned16(workspace)) return HC_ERR_MISALIGNED;
     if (n == 0) return cuda_status(cudaMemsetAsync(g_w, 0, (size_t)bytes, stream));  // sums over no rows
     const Span ins[] = {rows_span(g_y, n, N, g_stride, type), rows_span(x, n, K, x_stride, type),
                         span(offsets, ((int64_t)experts + 1) * 4)};
-    const Span outs[] = {span(g_w, bytes)};
-    if ((st = check_alias(outs, 1, ins, 3)) != HC_OK) return st;
+    const Span outs[] = {span(g_w, bytes), span(need ? workspace : nullptr, (int64_t)need)};
+    if ((st = check_alias(outs, 2, ins, 3)) != HC_OK) return st;
     // the innermost axis of g_w goes on the MMA's M side
     const bool f16 = type == HC_F16, f32 = g_type == HC_F32;
     return cuda_status(transposed
-                           ? hc::launch_grouped_mm_weights(x, x_stride, K, g_y, g_stride, N, offsets, n, experts, f16, g_w, f32, stream)
-                           : hc::launch_grouped_mm_weights(g_y, g_stride, N, x, x_stride, K, offsets, n, experts, f16, g_w, f32, stream));
+                           ? hc::launch_grouped_mm_weights(x, x_stride, K, g_y, g_stride, N, offsets, n, experts, f16, g_w, f32,
+                                                             workspace, stream)
+                           : hc::launch_grouped_mm_weights(g_y, g_stride, N, x, x_stride, K, offsets, n, experts, f16, g_w, f32,
+                                                             workspace, stream));
 }
 
 }  // extern "C"

@@ -17,7 +17,8 @@
 // One CTA per SM walks the tiles (warp 0 loads by TMA, warp 1 issues
 // tcgen05.mma, warps 2-9 write finished tiles, warp 10 clears the rows behind an
 // expert's last one in the gradient's operands); two accumulators alternate, so
-// that a tile is written while the next one's products run.  Where the tiles are
+// that a tile is written while the next one's products run.  The gradient of few
+// and long experts is summed in slices of their rows, joined by a second launch.  Where the tiles are
 // large two CTAs work on one (cta_group::2: 256 of f, each CTA with half of A's
 // rows and half of B's columns in its shared memory): an SM then loads 32 KB for a
 // block of 64 of k instead of 48, and what L2 delivers to an SM (some 60 bytes a
@@ -77,6 +78,7 @@ struct Cfg {
 struct Args {
     const int32_t *offsets;
     int experts;
+    int slices;         // weights': an expert's rows are cut in so many, slice s of expert e goes to out[s experts + e]
     int64_t n;          // rows of the row operands
     int F, C, K;        // product: F outputs, K contraction; weights': F x C outputs
     void *out;
@@ -413,11 +415,19 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // every expert's rows and how many tiles they make; a range that is out of
     // order or out of the rows counts as empty and is reported
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) {
-        int64_t s = __ldg(a.offsets + e), t = __ldg(a.offsets + e + 1);
+    const int parts = kWeights ? a.experts * a.slices : a.experts;
+    for (int e = threadIdx.x; e < parts; e += kThreads) {
+        const int slice = kWeights ? e / a.experts : 0, ex = kWeights ? e - slice * a.experts : e;
+        int64_t s = __ldg(a.offsets + ex), t = __ldg(a.offsets + ex + 1);
         if (s < 0 || t < s || t > a.n) {
             if (blockIdx.x == 0) atomicOr(&g_device_error, kErrOffsets);
             s = t = 0;
+        }
+        if (kWeights && a.slices > 1) {  // whole stages each, the last ones what is left
+            const int64_t per = ((t - s + a.slices - 1) / a.slices + kSub * kBK - 1) / (kSub * kBK) * (kSub * kBK);
+            const int64_t from = s + slice * per;
+            s = from < t ? from : t;
+            t = s + per < t ? s + per : t;
         }
         s_start[e] = (int)s, s_end[e] = (int)t;
         const int mt = (a.F + C::kTileF - 1) / C::kTileF;
@@ -427,14 +437,14 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     if (warp == 0) {  // running sum of the tile counts
         int carry = 0;
         if (lane == 0) s_first[0] = 0;
-        for (int e0 = 0; e0 < a.experts; e0 += 32) {
-            int v = e0 + lane < a.experts ? s_first[e0 + lane + 1] : 0;
+        for (int e0 = 0; e0 < parts; e0 += 32) {
+            int v = e0 + lane < parts ? s_first[e0 + lane + 1] : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int u = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += u;
             }
-            if (e0 + lane < a.experts) s_first[e0 + lane + 1] = carry + v;
+            if (e0 + lane < parts) s_first[e0 + lane + 1] = carry + v;
             carry += __shfl_sync(0xffffffffu, v, 31);
         }
     }
@@ -444,7 +454,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     tmem_fence_after_sync();
     const uint32_t tbase = s_tmem;
     const Plan plan{s_start, s_end, s_first};
-    const int tiles = s_first[a.experts];
+    const int tiles = s_first[parts];
     int e = 0;
 
     if (warp == 0) {
@@ -676,6 +686,54 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     if (warp == 1) tmem_give_back<kPair>(tbase, C::kTmemCols);
 }
 
+// The sum over slices of the weights' gradient, one after the other (the same call
+// gives the same bits), rounded to the output's type.  4 values a thread.
+constexpr int kJoinThreads = 256;
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(kJoinThreads) k_join_slices(const float *part, int64_t count, int slices, T *out) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t i = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
+    if (i >= count) return;  // (count is a multiple of 64)
+    float4 v = __ldcg(reinterpret_cast<const float4 *>(part + i));
+    for (int s = 1; s < slices; ++s) {
+        const float4 u = __ldcg(reinterpret_cast<const float4 *>(part + s * count + i));
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    Vec<T, 4> o;
+    put_pair(o, 0, f2_make(v.x, v.y)), put_pair(o, 2, f2_make(v.z, v.w));
+    if (kAligned) {
+        *reinterpret_cast<Vec<T, 4> *>(out + i) = o;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[i + k] = o.v[k];
+    }
+}
+template <typename T>
+cudaError_t join_slices(const float *part, int64_t count, int slices, void *out, cudaStream_t s) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((count / 4 + kJoinThreads - 1) / kJoinThreads)), cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+    T *const o = static_cast<T *>(out);
+    return reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0
+               ? cudaLaunchKernelEx(&cfg, k_join_slices<T, true>, part, count, slices, o)
+               : cudaLaunchKernelEx(&cfg, k_join_slices<T, false>, part, count, slices, o);
+}
+
+// Slices of an expert's rows in the weights' gradient: where the tiles are at most
+// half the pairs of CTAs of 152 SMs and experts have 2,048 rows or more, as many
+// slices as the pairs have room for, each of 512 rows at the least (us, with slices
+// and without: one expert, 2,048 rows 256 x 256 10.6 and 14.3, 12,733 rows 216 x 16
+// 14.3 and 68.8, 41,907 rows 456 x 3296 120 and 225; eight experts 512 x 512, 8,192
+// rows 12.6 and 10.7, 16,384 rows 14.9 and 15.2).
+int slices_of(int64_t n, int experts, int N, int K) {
+    const int64_t tiles = (int64_t)experts * ((N + 255) / 256) * ((K + 255) / 256);
+    const int64_t room = 76 / tiles, rows = n / experts, s = room < rows / 512 ? room : rows / 512;
+    return rows < 2048 || s < 2 ? 1 : (int)s;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *p = nullptr;
@@ -785,7 +843,7 @@ cudaError_t product(const void *x, int64_t x_stride, const void *w, bool w_kn, A
 cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bool w_kn, const int32_t *offsets, int64_t n,
                               int experts, int N, int K, bool fp16, void *y, int64_t y_stride, bool y_f32,
                               bool zero_rest, cudaStream_t s) {
-    const gm::Args a{offsets, experts, n, N, 0, K, y, y_stride, y_f32, fp16, zero_rest, 0, 0};
+    const gm::Args a{offsets, experts, 1, n, N, 0, K, y, y_stride, y_f32, fp16, zero_rest, 0, 0};
     // From some 40 rows an expert on the wide tiles of pairs are the faster ones (us, narrow
     // and wide, 16 experts of 2048 x 5120: 32 rows each 56 and 60, 48 rows 64 and 60, 128 rows
     // 102 and 64).
@@ -799,15 +857,27 @@ cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bo
 
 cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, const void *am, int64_t a_stride, int F,
                                       const int32_t *offsets, int64_t n, int experts, bool fp16, void *g_w,
-                                      bool g_f32, cudaStream_t s) {
+                                      bool g_f32, void *workspace, cudaStream_t s) {
     using Cf = gm::Cfg<256, true, false>;
+    const int slices = gm::slices_of(n, experts, C, F);
+    void *const out = slices > 1 ? workspace : g_w;
     CUtensorMap ta, tb, chunk;
-    gm::Args a{offsets, experts, n, F, C, 0, g_w, F, g_f32, fp16, false, 0, 0};
+    gm::Args a{offsets, experts, slices, n, F, C, 0, out, F, g_f32 || slices > 1, fp16, false, 0, 0};
     if (!gm::make_operand_map(&ta, am, fp16, F, n, a_stride, 0, gm::kM / 64, &a.a_whole) ||
         !gm::make_operand_map(&tb, b, fp16, C, n, b_stride, 0, Cf::kOwn / 64, &a.b_whole) ||
         !gm::make_map(&chunk, b, fp16, C, n, b_stride, 0, gm::kSub * gm::kBK))
         return cudaErrorInvalidValue;
-    return gm::launch<256, true, false, true, true>(ta, tb, chunk, a, s);
+    const cudaError_t e = gm::launch<256, true, false, true, true>(ta, tb, chunk, a, s);
+    if (e != cudaSuccess || slices == 1) return e;
+    const float *const part = static_cast<const float *>(workspace);
+    const int64_t count = (int64_t)experts * C * F;
+    if (g_f32) return gm::join_slices<float>(part, count, slices, g_w, s);
+    return fp16 ? gm::join_slices<__half>(part, count, slices, g_w, s) : gm::join_slices<__nv_bfloat16>(part, count, slices, g_w, s);
+}
+
+size_t grouped_mm_weights_workspace_bytes(int64_t n, int experts, int N, int K) {
+    const int slices = gm::slices_of(n, experts, N, K);
+    return slices == 1 ? 0 : (size_t)slices * experts * N * K * 4;
 }
 
 cudaError_t consume_grouped_mm_device_error(cudaStream_t s, unsigned int *flag) {

@@ -39,7 +39,8 @@ cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bo
 // g_w [experts][C][F] = sum over the expert's rows of b[r][c] a[r][f].
 cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, const void *a, int64_t a_stride, int F,
                                       const int32_t *offsets, int64_t n, int experts, bool fp16, void *g_w,
-                                      bool g_f32, cudaStream_t s);
+                                      bool g_f32, void *workspace, cudaStream_t s);
+size_t grouped_mm_weights_workspace_bytes(int64_t n, int experts, int N, int K);
 // as the other files' (hc_launch.h); bit 2: offsets out of order or out of range
 cudaError_t consume_grouped_mm_device_error(cudaStream_t s, unsigned int *flag);
 

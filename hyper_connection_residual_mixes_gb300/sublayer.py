@@ -224,10 +224,12 @@ def hc_grouped_mm(x, w, offsets, transposed=False, y=None, out_dtype=None, strea
     return y
 
 
-def hc_grouped_mm_weights(g_y, x, offsets, transposed=False, g_w=None, out_dtype=None, stream=None):
+def hc_grouped_mm_weights(g_y, x, offsets, transposed=False, g_w=None, out_dtype=None, workspace=None, stream=None):
     """The weights' gradient of hc_grouped_mm: g_y [n, N] and x [n, K] of one type ->
     g_w [experts, N, K] (transposed: [experts, K, N]) of out_dtype (x's type or
-    fp32), the sum over each expert's rows of g_y[r] x[r]^T."""
+    fp32), the sum over each expert's rows of g_y[r] x[r]^T.  workspace: a uint8
+    device tensor of at least the size the library asks for (allocated here when
+    None)."""
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError("offsets must be [experts + 1]")
     E = offsets.shape[0] - 1
@@ -245,13 +247,22 @@ def hc_grouped_mm_weights(g_y, x, offsets, transposed=False, g_w=None, out_dtype
         raise TypeError("out_dtype must be %s or torch.float32, got %s" % (x.dtype, out_dtype))
     if g_w is not None:
         _dense(g_w, "g_w", (out_dtype,), shape, dev)
+    if workspace is not None:
+        _tensor(workspace, "workspace", (torch.uint8,), dev)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
     if stream is not None or _current_device() != dev.index:
         with _at(dev, stream):
-            return hc_grouped_mm_weights(g_y, x, offsets, transposed, g_w, out_dtype)
+            return hc_grouped_mm_weights(g_y, x, offsets, transposed, g_w, out_dtype, workspace)
     if g_w is None:
         g_w = torch.empty(shape, dtype=out_dtype, device=dev)
+    if workspace is None:
+        need = _lib.load().hc_grouped_mm_weights_workspace_bytes(n, E, N, K)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
     _lib.call("hc_grouped_mm_weights", g_y.data_ptr(), gs, x.data_ptr(), xs, offsets.data_ptr(), n, E, N, K,
-              _DTYPE[x.dtype], g_w.data_ptr(), transposed, _DTYPE[out_dtype], _raw_stream(dev.index))
+              _DTYPE[x.dtype], g_w.data_ptr(), transposed, _DTYPE[out_dtype],
+              None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+              _raw_stream(dev.index))
     return g_w
 
 

@@ -121,6 +121,57 @@ def test_many_experts_and_long_contractions():
     _check_weights(g, x, off, False, got["g_w"])
 
 
+@pytest.mark.parametrize("counts,N,K", [([5000], 16, 216), ([4097], 264, 1032), ([1, 0, 20000, 77, 130], 520, 72),
+                                        ([2100, 2300, 2200], 2048, 256), ([0, 9000, 600], 8, 8), ([40000], 512, 328)])
+@pytest.mark.parametrize("t,kn", [("bf16", False), ("fp16", True)])
+def test_gradients_of_few_and_long_experts(counts, N, K, t, kn):
+    """Rows summed in slices: some of them empty, some ending inside a block; NaN in
+    the rows of no expert; outputs at odd places; every repeat gives the same bits."""
+    assert _lib.load().hc_grouped_mm_weights_workspace_bytes(sum(counts) + 3, len(counts), N, K) > 0
+    x, _, g, off = _inputs(counts, N, K, t, kn, rest=3, seed=11)
+    x[sum(counts):], g[sum(counts):] = float("nan"), float("inf")
+    got = hcg.hc_grouped_mm_weights(g, x, off, transposed=kn)
+    _check_weights(g, x, off, kn, got)
+    f32 = hcg.hc_grouped_mm_weights(g, x, off, transposed=kn, out_dtype=torch.float32)
+    _check_weights(g, x, off, kn, f32)
+    assert torch.equal(f32.to(T[t]), got)
+    for out in (T[t], torch.float32):
+        flat = torch.full((got.numel() + 2,), 5.0, dtype=out, device="cuda")
+        odd = flat[1:-1].view(got.shape)
+        hcg.hc_grouped_mm_weights(g, x, off, transposed=kn, g_w=odd)
+        assert torch.equal(odd, got if out is T[t] else f32) and flat[0] == 5 and flat[-1] == 5
+    for _ in range(10):
+        assert torch.equal(hcg.hc_grouped_mm_weights(g, x, off, transposed=kn), got)
+
+
+def test_slices_on_two_streams_and_in_a_graph():
+    """Calls with workspaces of their own at once; a captured call reads new offsets."""
+    x, _, g, off = _inputs([3000, 2500], 264, 136, "bf16", seed=12)
+    x2, _, g2, off2 = _inputs([2500, 3000], 264, 136, "bf16", seed=13)
+    want, want2 = hcg.hc_grouped_mm_weights(g, x, off), hcg.hc_grouped_mm_weights(g2, x2, off2)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(a):
+            got = hcg.hc_grouped_mm_weights(g, x, off)
+        with torch.cuda.stream(b):
+            got2 = hcg.hc_grouped_mm_weights(g2, x2, off2)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(got2, want2)
+    size = _lib.load().hc_grouped_mm_weights_workspace_bytes(5500, 2, 264, 136)
+    ws, out = torch.empty((size,), dtype=torch.uint8, device="cuda"), torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hcg.hc_grouped_mm_weights(g, x, off, g_w=out, workspace=ws)
+        hcg.hc_grouped_mm_weights(g, x, off, g_w=out, workspace=ws)
+    off.copy_(off2)
+    graph.replay()
+    torch.cuda.synchronize()
+    _check_weights(g, x, off2, False, out)
+    with pytest.raises(_lib.HcError):
+        hcg.hc_grouped_mm_weights(g, x, off, workspace=ws[:-16])
+
+
 @pytest.mark.parametrize("kn", [False, True])
 def test_narrow_and_wide_tiles_in_turn(kn):
     """Experts of a few rows between experts of many: tiles of different widths

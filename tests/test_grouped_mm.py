@@ -41,7 +41,7 @@ def test_product_refusals(kw, expect):
 
 def _weights(**kw):
     a = dict(g=A, gs=32, x=A + STEP, xs=64, offsets=A + 2 * STEP, n=16, experts=4, N=32, K=64, type=F16, gw=A + 3 * STEP,
-             transposed=0, gt=F32, stream=None)
+             transposed=0, gt=F32, ws=None, ws_bytes=0, stream=None)
     a.update(kw)
     return _lib.raw("hc_grouped_mm_weights", *a.values())
 
@@ -52,9 +52,28 @@ def _weights(**kw):
     (dict(gs=24), 1), (dict(gs=36), 2), (dict(xs=65), 2), (dict(g=None), 1), (dict(gw=None), 1), (dict(offsets=None), 1),
     (dict(g=A + 2), 3), (dict(x=A + STEP + 8), 3), (dict(gw=A + 3 * STEP + 2), 3),
     (dict(gw=A + 32), 4), (dict(gw=A + 2 * STEP), 4),
+    # one expert of 8,192 rows: 32 x 64 sums in slices, which need room
+    (dict(n=8192, experts=1), 1), (dict(n=8192, experts=1, ws=A + 4 * STEP, ws_bytes=32 * 64 * 8 - 1), 1),
+    (dict(n=8192, experts=1, ws=A + 4 * STEP + 8, ws_bytes=1 << 24), 3),
+    (dict(n=8192, experts=1, ws=A + 64, ws_bytes=1 << 24), 4),
+    (dict(n=8192, experts=1, ws=A + 3 * STEP + 4096, ws_bytes=1 << 24), 4),
 ])
 def test_weights_refusals(kw, expect):
     assert _weights(**kw) == expect
+
+
+def test_workspace_bytes():
+    f = _lib.load().hc_grouped_mm_weights_workspace_bytes
+    assert f(100, 4, 512, 1024) == 0 and f(0, 1, 64, 64) == 0 and f(-1, 1, 64, 64) == 0 and f(1 << 20, 1, 60, 64) == 0
+    assert f(1 << 20, 64, 2048, 5120) == 0   # tiles enough
+    assert f(2047, 1, 256, 256) == 0 and f(2048, 1, 256, 256) == 4 * 256 * 256 * 4
+    assert f(1 << 20, 1, 256, 512) == 38 * 256 * 512 * 4
+    for n in (1, 1000, 5000, 100000):
+        for experts in (1, 3, 20, 1024):
+            for N, K in ((8, 8), (264, 1032), (2048, 5120)):
+                slices = f(n, experts, N, K) / (experts * N * K * 4)
+                assert slices == int(slices) and slices != 1
+                assert slices * experts * -(-N // 256) * -(-K // 256) <= 76
 
 
 def test_binding_refusals():
