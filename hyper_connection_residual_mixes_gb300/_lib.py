@@ -51,7 +51,8 @@ SIGNATURES = {
     "hc_layer_norm_backward_workspace_bytes": [I64, I32],
     "hc_layer_norm_backward": [P, I64, I32, P, I64, I32, P, I32, P, P, I64, I32, P, I64, P, P, P,
                                ctypes.c_size_t, P],
-    "hc_grouped_mm": [P, I64, P, I32, P, I64, I32, I32, I32, I32, P, I64, I32, I32, P],
+    "hc_grouped_mm_workspace_bytes": [I64, I32, I32, I32],
+    "hc_grouped_mm": [P, I64, P, I32, P, I64, I32, I32, I32, I32, P, I64, I32, I32, P, ctypes.c_size_t, P],
     "hc_grouped_mm_weights_workspace_bytes": [I64, I32, I32, I32],
     "hc_grouped_mm_weights": [P, I64, P, I64, P, I64, I32, I32, I32, I32, P, I32, I32, P, ctypes.c_size_t, P],
     "hc_adamw_step": [P, I64, F64, F64, F64, F64, F64, I64, P, P, P, P],
@@ -104,6 +105,7 @@ def load():
         lib.hc_block_step_backward_workspace_bytes.restype = ctypes.c_size_t
         lib.hc_chain_state_bytes.restype = ctypes.c_size_t
         lib.hc_layer_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+        lib.hc_grouped_mm_workspace_bytes.restype = ctypes.c_size_t
         lib.hc_grouped_mm_weights_workspace_bytes.restype = ctypes.c_size_t
         _lib = lib
         return lib

@@ -629,10 +629,15 @@ hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr
                                         grad_scale, stream));
 }
 
+size_t hc_grouped_mm_workspace_bytes(int64_t n, int experts, int N, int K) {
+    if (check_grouped(n, experts, N, K, HC_BF16, HC_F32) != HC_OK) return 0;
+    return hc::grouped_mm_workspace_bytes(n, experts, N, K);
+}
+
 hc_status hc_grouped_mm(const void *x, int64_t x_stride, const void *w, int transposed,
                         const int32_t *offsets, int64_t n, int experts, int N, int K, hc_dtype type,
                         void *y, int64_t y_stride, hc_dtype y_type, int zero_rest,
-                        cudaStream_t stream) {
+                        void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     hc_status st = check_grouped(n, experts, N, K, type, y_type);
     if (st != HC_OK) return st;
     if (x_stride < K || y_stride < N || !rows_fit(n, K, x_stride) || !rows_fit(n, N, y_stride)) return HC_ERR_INVALID_ARG;
@@ -643,10 +648,13 @@ hc_status hc_grouped_mm(const void *x, int64_t x_stride, const void *w, int tran
         return HC_ERR_MISALIGNED;
     const Span ins[] = {rows_span(x, n, K, x_stride, type), span(w, (int64_t)experts * N * K * 2),
                         span(offsets, ((int64_t)experts + 1) * 4)};
-    const Span outs[] = {rows_span(y, n, N, y_stride, y_type)};
-    if ((st = check_alias(outs, 1, ins, 3)) != HC_OK) return st;
+    const size_t need = hc::grouped_mm_workspace_bytes(n, experts, N, K);
+    if (need && (!workspace || workspace_bytes < need)) return HC_ERR_INVALID_ARG;
+    if (need && !aligned16(workspace)) return HC_ERR_MISALIGNED;
+    const Span outs[] = {rows_span(y, n, N, y_stride, y_type), span(need ? workspace : nullptr, (int64_t)need)};
+    if ((st = check_alias(outs, 2, ins, 3)) != HC_OK) return st;
     return cuda_status(hc::launch_grouped_mm(x, x_stride, w, transposed != 0, offsets, n, experts, N, K, type == HC_F16, y,
-                                             y_stride, y_type == HC_F32, zero_rest != 0, stream));
+                                             y_stride, y_type == HC_F32, zero_rest != 0, workspace, stream));
 }
 
 size_t hc_grouped_mm_weights_workspace_bytes(int64_t n, int experts, int N, int K) {

@@ -17,8 +17,9 @@
 // One CTA per SM walks the tiles (warp 0 loads by TMA, warp 1 issues
 // tcgen05.mma, warps 2-9 write finished tiles, warp 10 clears the rows behind an
 // expert's last one in the gradient's operands); two accumulators alternate, so
-// that a tile is written while the next one's products run.  The gradient of few
-// and long experts is summed in slices of their rows, joined by a second launch.  Where the tiles are
+// that a tile is written while the next one's products run.  Where few tiles have
+// long sums (a row of one wide expert, the gradient of few and long experts) these
+// are made in slices, which a second launch adds up.  Where the tiles are
 // large two CTAs work on one (cta_group::2: 256 of f, each CTA with half of A's
 // rows and half of B's columns in its shared memory): an SM then loads 32 KB for a
 // block of 64 of k instead of 48, and what L2 delivers to an SM (some 60 bytes a
@@ -78,7 +79,7 @@ struct Cfg {
 struct Args {
     const int32_t *offsets;
     int experts;
-    int slices;         // weights': an expert's rows are cut in so many, slice s of expert e goes to out[s experts + e]
+    int slices;         // the contraction is cut in so many; slice s goes to the s-th of so many outputs
     int64_t n;          // rows of the row operands
     int F, C, K;        // product: F outputs, K contraction; weights': F x C outputs
     void *out;
@@ -307,7 +308,8 @@ struct Plan {
     const int *start, *end, *first;  // rows of expert e; its first tile (first[experts]: all tiles)
 };
 struct Tile {
-    int e, f0, c0, cols;  // cols: columns of the tile that count (rows of the product)
+    int e, slice;         // (weights': e counts through the slices' experts, their ranges are the slices' own)
+    int f0, c0, cols;     // cols: columns of the tile that count (rows of the product)
     int k0, klen;         // contraction: rows [k0, k0 + klen) of the weights', [0, K) of the product
 };
 // An expert's tiles are walked in groups of kGroup tiles of c, through all of f
@@ -325,7 +327,8 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
     const int local = tile - p.first[e];
     const int rows = p.end[e] - p.start[e];
     Tile t;
-    t.e = e;
+    t.e = kWeights ? e : e % a.experts;
+    t.slice = kWeights ? 0 : e / a.experts;
     const int ft = (a.F + Cfg<BN, kPair, kDeep>::kTileF - 1) / Cfg<BN, kPair, kDeep>::kTileF;
     int f, c;
     if (kWeights) {
@@ -342,8 +345,9 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
         const int at = c * per;
         t.c0 = p.start[e] + at;
         t.cols = rows - at < per ? rows - at : per;
-        t.k0 = 0;
-        t.klen = a.K;
+        const int part = ((a.K + a.slices - 1) / a.slices + kSub * kBK - 1) / (kSub * kBK) * (kSub * kBK);  // whole stages
+        t.k0 = t.slice * part < a.K ? t.slice * part : a.K;
+        t.klen = a.K - t.k0 < part ? a.K - t.k0 : part;
     }
     t.f0 = f * Cfg<BN, kPair, kDeep>::kTileF;
     return t;
@@ -415,9 +419,9 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // every expert's rows and how many tiles they make; a range that is out of
     // order or out of the rows counts as empty and is reported
-    const int parts = kWeights ? a.experts * a.slices : a.experts;
+    const int parts = a.experts * a.slices;
     for (int e = threadIdx.x; e < parts; e += kThreads) {
-        const int slice = kWeights ? e / a.experts : 0, ex = kWeights ? e - slice * a.experts : e;
+        const int slice = e / a.experts, ex = e - slice * a.experts;
         int64_t s = __ldg(a.offsets + ex), t = __ldg(a.offsets + ex + 1);
         if (s < 0 || t < s || t > a.n) {
             if (blockIdx.x == 0) atomicOr(&g_device_error, kErrOffsets);
@@ -652,7 +656,7 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const Tile t = tile_of<BN, kPair, kDeep, kWeights>(a, plan, tile, e);
             const int f = t.f0 + rank * kM + q * 32 + lane;
             uint8_t *o = static_cast<uint8_t *>(a.out) +
-                         ((kWeights ? (int64_t)t.e * a.C + t.c0 : (int64_t)t.c0) * a.out_stride + f) * esize;
+                         ((kWeights ? (int64_t)t.e * a.C + t.c0 : t.slice * a.n + t.c0) * a.out_stride + f) * esize;
             const int64_t step = a.out_stride * esize;
             const bool in = f < a.F;
             if (t.klen == 0) {
@@ -720,6 +724,76 @@ cudaError_t join_slices(const float *part, int64_t count, int slices, void *out,
     return reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0
                ? cudaLaunchKernelEx(&cfg, k_join_slices<T, true>, part, count, slices, o)
                : cudaLaunchKernelEx(&cfg, k_join_slices<T, false>, part, count, slices, o);
+}
+
+// The same for a product: a block adds up 4 * kJoinThreads outputs of a row, if the
+// row is an expert's; others are zeroed (zero_rest: those outside all ranges) or left.
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(kJoinThreads)
+k_join_rows(const float *part, const int32_t *offsets, int experts, int64_t n, int F, int slices, T *out, int64_t stride, int zero_rest) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t row = blockIdx.x;
+    int mine = 0;
+    for (int e = threadIdx.x; e < experts; e += kJoinThreads) {
+        const int64_t s = __ldg(offsets + e), t = __ldg(offsets + e + 1);
+        mine |= s >= 0 && t <= n && s <= row && row < t;
+    }
+    const bool has = __syncthreads_or(mine);
+    const int f = (blockIdx.y * kJoinThreads + threadIdx.x) * 4;
+    if (f >= F) return;  // (F is a multiple of 8)
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (has) {
+        for (int s = 0; s < slices; ++s) {
+            const float4 u = __ldcg(reinterpret_cast<const float4 *>(part + (s * n + row) * F + f));
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+    } else {
+        int64_t lo = __ldg(offsets), hi = __ldg(offsets + experts);
+        lo = lo < 0 ? 0 : lo > n ? n : lo;
+        hi = hi < lo ? lo : hi > n ? n : hi;
+        if (!zero_rest || (row >= lo && row < hi)) return;
+    }
+    T *o = out + row * stride + f;
+    Vec<T, 4> r;
+    put_pair(r, 0, f2_make(v.x, v.y)), put_pair(r, 2, f2_make(v.z, v.w));
+    if (kAligned) {
+        *reinterpret_cast<Vec<T, 4> *>(o) = r;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = r.v[k];
+    }
+}
+template <typename T>
+cudaError_t join_rows(const float *part, const Args &a, int slices, void *out, int64_t stride, int zero_rest, cudaStream_t s) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)a.n, (unsigned)((a.F / 4 + kJoinThreads - 1) / kJoinThreads)), cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+    T *const o = static_cast<T *>(out);
+    return reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0 && stride % 4 == 0
+               ? cudaLaunchKernelEx(&cfg, k_join_rows<T, true>, part, a.offsets, a.experts, a.n, a.F, slices, o, stride, zero_rest)
+               : cudaLaunchKernelEx(&cfg, k_join_rows<T, false>, part, a.offsets, a.experts, a.n, a.F, slices, o, stride, zero_rest);
+}
+
+// Whether a product takes the wide tiles: from some 40 rows an expert on they are
+// the faster ones (us, narrow and wide, 16 experts of 2048 x 5120: 32 rows each 56
+// and 60, 48 rows 64 and 60, 128 rows 102 and 64).
+bool wide_rows(int64_t n, int experts) { return n > 32 * (int64_t)experts; }
+// Narrow tiles of a product at the most: one for each 128 outputs of each expert
+// with rows (and of each 32 rows of one).
+int64_t narrow_tiles(int64_t n, int experts, int N) { return (int64_t)(N + kM - 1) / kM * (n < experts ? n : experts + n / 32); }
+// Slices of a product's contraction: where it is of 4,096 or more and the tiles leave
+// half the 152 SMs (their pairs) without work, as many as there is room for, 512 of it
+// each at the least (us, with slices and without: one row of one expert, 5120 x 4096
+// 12.8 and 19.1, x 8192 19.6 and 34.3, x 2048 9.7 and 11.6, which the second launch
+// takes back where the host is the slower one; three rows 3776 x 5936 13.4 and 26.1;
+// 512 rows 1024 x 8192 16.7 and 40.2; slices of 1,024 at the least 0 to 10 % more).
+int product_slices(int64_t n, int experts, int N, int K) {
+    const int64_t tiles = wide_rows(n, experts) ? (N + 255) / 256 * (experts + n / 256) : narrow_tiles(n, experts, N);
+    const int64_t room = (wide_rows(n, experts) ? 76 : 152) / (tiles > 0 ? tiles : 1), s = room < K / 512 ? room : K / 512;
+    return K < 4096 || s < 2 ? 1 : (int)(s * experts <= kMaxExperts ? s : 1);
 }
 
 // Slices of an expert's rows in the weights' gradient: where the tiles are at most
@@ -842,17 +916,25 @@ cudaError_t product(const void *x, int64_t x_stride, const void *w, bool w_kn, A
 
 cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bool w_kn, const int32_t *offsets, int64_t n,
                               int experts, int N, int K, bool fp16, void *y, int64_t y_stride, bool y_f32,
-                              bool zero_rest, cudaStream_t s) {
-    const gm::Args a{offsets, experts, 1, n, N, 0, K, y, y_stride, y_f32, fp16, zero_rest, 0, 0};
-    // From some 40 rows an expert on the wide tiles of pairs are the faster ones (us, narrow
-    // and wide, 16 experts of 2048 x 5120: 32 rows each 56 and 60, 48 rows 64 and 60, 128 rows
-    // 102 and 64).
-    if (n > 32 * (int64_t)experts) return gm::product<256, true, false>(x, x_stride, w, w_kn, a, n, s);
-    // Few rows an expert: narrow row tiles leave room for more of the weights in flight.  The
-    // tiles are at most one for each 128 outputs of each expert (and of each 32 rows of one).
-    const int64_t with_rows = n < experts ? n : experts + n / 32, tiles = (N + gm::kM - 1) / gm::kM * with_rows;
-    if (tiles <= gm::sm_count()) return gm::product<32, false, true>(x, x_stride, w, w_kn, a, n, s);
-    return gm::product<32, false, false>(x, x_stride, w, w_kn, a, n, s);
+                              bool zero_rest, void *workspace, cudaStream_t s) {
+    const int slices = gm::product_slices(n, experts, N, K);
+    gm::Args a{offsets, experts, slices, n, N, 0, K, y, y_stride, y_f32, fp16, zero_rest, 0, 0};
+    if (slices > 1) a.out = workspace, a.out_stride = N, a.out_f32 = 1, a.zero_rest = 0;
+    cudaError_t e;
+    // (few rows an expert: narrow row tiles leave room for more of the weights in flight)
+    if (gm::wide_rows(n, experts)) e = gm::product<256, true, false>(x, x_stride, w, w_kn, a, n, s);
+    else if (slices * gm::narrow_tiles(n, experts, N) <= gm::sm_count()) e = gm::product<32, false, true>(x, x_stride, w, w_kn, a, n, s);
+    else e = gm::product<32, false, false>(x, x_stride, w, w_kn, a, n, s);
+    if (e != cudaSuccess || slices == 1) return e;
+    const float *const part = static_cast<const float *>(workspace);
+    if (y_f32) return gm::join_rows<float>(part, a, slices, y, y_stride, zero_rest, s);
+    return fp16 ? gm::join_rows<__half>(part, a, slices, y, y_stride, zero_rest, s)
+                : gm::join_rows<__nv_bfloat16>(part, a, slices, y, y_stride, zero_rest, s);
+}
+
+size_t grouped_mm_workspace_bytes(int64_t n, int experts, int N, int K) {
+    const int slices = gm::product_slices(n, experts, N, K);
+    return slices == 1 ? 0 : (size_t)slices * n * N * 4;
 }
 
 cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, const void *am, int64_t a_stride, int F,

@@ -35,7 +35,8 @@ cudaError_t consume_layer_norm_device_error(cudaStream_t s, unsigned int *flag);
 // y [n, N] = x [n, K] w[e]^T, w [experts][N][K] (w_kn: [experts][K][N]).
 cudaError_t launch_grouped_mm(const void *x, int64_t x_stride, const void *w, bool w_kn, const int32_t *offsets, int64_t n,
                               int experts, int N, int K, bool fp16, void *y, int64_t y_stride, bool y_f32,
-                              bool zero_rest, cudaStream_t s);
+                              bool zero_rest, void *workspace, cudaStream_t s);
+size_t grouped_mm_workspace_bytes(int64_t n, int experts, int N, int K);
 // g_w [experts][C][F] = sum over the expert's rows of b[r][c] a[r][f].
 cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, const void *a, int64_t a_stride, int F,
                                       const int32_t *offsets, int64_t n, int experts, bool fp16, void *g_w,

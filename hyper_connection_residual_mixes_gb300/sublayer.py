@@ -148,9 +148,7 @@ def hc_layer_norm_backward(g_y, x, norm_w, mean, rstd, bias=True, g_x=None, work
     _dense(rstd, "rstd", (torch.float32,), x.shape[:-1], dev)
     gxs = d if g_x is None else _like(g_x, "g_x", x, (g_y.dtype,))
     if workspace is not None:
-        _tensor(workspace, "workspace", (torch.uint8,), dev)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+        _scratch(workspace, dev)
     if stream is not None or _current_device() != dev.index:
         with _at(dev, stream):
             return hc_layer_norm_backward(g_y, x, norm_w, mean, rstd, bias, g_x, workspace)
@@ -166,6 +164,12 @@ def hc_layer_norm_backward(g_y, x, norm_w, mean, rstd, bias=True, g_x=None, work
               g_w.data_ptr(), None if g_b is None else g_b.data_ptr(), workspace.data_ptr(), workspace.numel(),
               _raw_stream(dev.index))
     return {"g_x": g_x, "g_norm_w": g_w, "g_norm_b": g_b} if bias else {"g_x": g_x, "g_norm_w": g_w}
+
+
+def _scratch(workspace, dev):
+    _tensor(workspace, "workspace", (torch.uint8,), dev)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
 
 
 _HALF = (torch.bfloat16, torch.float16)
@@ -196,12 +200,14 @@ def _out_rows(y, name, shape, types, dev):
     return step if n > 1 else shape[-1]
 
 
-def hc_grouped_mm(x, w, offsets, transposed=False, y=None, out_dtype=None, stream=None):
+def hc_grouped_mm(x, w, offsets, transposed=False, y=None, out_dtype=None, workspace=None, stream=None):
     """Products of rows grouped by expert: x [n, K] (bf16 or fp16, rows sorted by
     expert), w [experts, N, K] of x's type (with transposed [experts, K, N]),
     offsets [experts + 1] int32 on the device -> y [n, N] of out_dtype (x's type
     or fp32), y[r] = w[e] x[r] for offsets[e] <= r < offsets[e + 1].  Rows of no
-    expert are zeros in a y made here and stay as they are in a y given."""
+    expert are zeros in a y made here and stay as they are in a y given.
+    workspace: a uint8 device tensor of at least the size the library asks for
+    (allocated here when None)."""
     _tensor(w, "w")
     n, xs = _grouped(x, "x", w.shape, offsets)
     dev = x.device
@@ -213,14 +219,21 @@ def hc_grouped_mm(x, w, offsets, transposed=False, y=None, out_dtype=None, strea
     if out_dtype is not x.dtype and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be %s or torch.float32, got %s" % (x.dtype, out_dtype))
     ys = N if y is None else _out_rows(y, "y", (n, N), (out_dtype,), dev)
+    if workspace is not None:
+        _scratch(workspace, dev)
     if stream is not None or _current_device() != dev.index:
         with _at(dev, stream):
-            return hc_grouped_mm(x, w, offsets, transposed, y, out_dtype)
+            return hc_grouped_mm(x, w, offsets, transposed, y, out_dtype, workspace)
     zero = y is None
     if zero:
         y = torch.empty((n, N), dtype=out_dtype, device=dev)
+    if workspace is None:
+        need = _lib.load().hc_grouped_mm_workspace_bytes(n, E, N, K)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
     _lib.call("hc_grouped_mm", x.data_ptr(), xs, w.data_ptr(), transposed, offsets.data_ptr(), n, E, N, K,
-              _DTYPE[x.dtype], y.data_ptr(), ys, _DTYPE[out_dtype], zero, _raw_stream(dev.index))
+              _DTYPE[x.dtype], y.data_ptr(), ys, _DTYPE[out_dtype], zero,
+              None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+              _raw_stream(dev.index))
     return y
 
 
@@ -248,9 +261,7 @@ def hc_grouped_mm_weights(g_y, x, offsets, transposed=False, g_w=None, out_dtype
     if g_w is not None:
         _dense(g_w, "g_w", (out_dtype,), shape, dev)
     if workspace is not None:
-        _tensor(workspace, "workspace", (torch.uint8,), dev)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+        _scratch(workspace, dev)
     if stream is not None or _current_device() != dev.index:
         with _at(dev, stream):
             return hc_grouped_mm_weights(g_y, x, offsets, transposed, g_w, out_dtype, workspace)

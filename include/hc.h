@@ -466,17 +466,20 @@ hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr
  *   on) are left as they are, or with zero_rest written as zeros.
  *   g_y [n, N] of type, rows g_stride >= N apart                             in
  *   g_w [experts, N, K] (transposed: [experts, K, N]) of g_type: type or fp32    out
- *   workspace of hc_grouped_mm_weights_workspace_bytes(n, experts, N, K) bytes (0 but
- *   for few and long experts, whose rows are summed in slices; may be NULL then),
- *   16-byte aligned: scratch of this call, free for others once it has completed.
+ *   workspace of hc_grouped_mm_workspace_bytes or
+ *   hc_grouped_mm_weights_workspace_bytes(n, experts, N, K) bytes, 16-byte aligned:
+ *   scratch of this call, free for others once it has completed.  0 bytes (it may
+ *   be NULL then) but for outputs of few tiles and a long sum, which is made in slices.
  * type is HC_BF16 or HC_F16.  experts <= 1024; n, N and K < 2^31 - 4096; N and K multiples of 8; x, g_y
  * and w start on 16 bytes and x_stride, g_stride are multiples of 8 (the tensor
  * copies' rule; HC_ERR_UNSUPPORTED, HC_ERR_MISALIGNED otherwise).
  */
+size_t hc_grouped_mm_workspace_bytes(int64_t n, int experts, int N, int K);
+
 hc_status hc_grouped_mm(const void *x, int64_t x_stride, const void *w, int transposed,
                         const int32_t *offsets, int64_t n, int experts, int N, int K, hc_dtype type,
                         void *y, int64_t y_stride, hc_dtype y_type, int zero_rest,
-                        cudaStream_t stream);
+                        void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 size_t hc_grouped_mm_weights_workspace_bytes(int64_t n, int experts, int N, int K);
 

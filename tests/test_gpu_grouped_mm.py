@@ -144,6 +144,45 @@ def test_gradients_of_few_and_long_experts(counts, N, K, t, kn):
         assert torch.equal(hcg.hc_grouped_mm_weights(g, x, off, transposed=kn), got)
 
 
+@pytest.mark.parametrize("counts,N,K", [([1], 8, 8200), ([3], 3776, 5936), ([2, 0, 5, 40, 1], 264, 9000), ([700], 136, 16384),
+                                        ([0, 300, 1], 8, 5568), ([20, 1, 33], 1032, 4160)])
+@pytest.mark.parametrize("t,kn", [("bf16", False), ("fp16", True)])
+def test_products_of_few_tiles_and_long_sums(counts, N, K, t, kn):
+    """Contractions in slices, the last of them shorter or empty; rows of no expert
+    before and behind stay, or become zeros; strided and oddly placed outputs."""
+    x, w, _, off = _inputs(counts, N, K, t, kn, rest=3, seed=14)
+    assert _lib.load().hc_grouped_mm_workspace_bytes(x.shape[0], len(counts), N, K) > 0
+    off = off.clone()
+    off[0] = min(1, counts[0])   # a first row of no expert, where there is one to take
+    x[sum(counts):] = float("nan")
+    y = hcg.hc_grouped_mm(x, w, off, transposed=kn)
+    free = _check(x, w, off, kn, y)
+    assert (y[free] == 0).all()
+    f32 = hcg.hc_grouped_mm(x, w, off, transposed=kn, out_dtype=torch.float32)
+    _check(x, w, off, kn, f32)
+    assert torch.equal(f32.to(T[t]), y)
+    for out in (T[t], torch.float32):
+        for pitch, lead in ((0, 1), (5, 3), (8, 0)):
+            flat = torch.full((lead + x.shape[0] * (N + pitch) + 1,), 5.0, dtype=out, device="cuda")
+            rows = flat[lead:-1].view(x.shape[0], N + pitch)
+            hcg.hc_grouped_mm(x, w, off, transposed=kn, y=rows[:, :N])
+            want = (y if out is T[t] else f32).clone()
+            want[free] = 5.0
+            assert torch.equal(rows[:, :N], want) and (rows[:, N:] == 5).all() and (flat[:lead] == 5).all() and flat[-1] == 5
+    for _ in range(10):
+        assert torch.equal(hcg.hc_grouped_mm(x, w, off, transposed=kn), y)
+
+
+def test_bad_offsets_with_slices():
+    x, w, _, off = _inputs([4, 4, 4], 64, 8192, "bf16", seed=15)
+    _lib.raw("hc_consume_device_error", None)
+    bad = torch.tensor([0, 40, 8, 12], dtype=torch.int32, device="cuda")
+    y = torch.full((12, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    hcg.hc_grouped_mm(x, w, bad, y=y)
+    assert _lib.raw("hc_consume_device_error", None) == 1 and _lib.raw("hc_consume_device_error", None) == 0
+    assert (y[:8] == 3).all() and torch.equal(y[8:], hcg.hc_grouped_mm(x, w, off)[8:])
+
+
 def test_slices_on_two_streams_and_in_a_graph():
     """Calls with workspaces of their own at once; a captured call reads new offsets."""
     x, _, g, off = _inputs([3000, 2500], 264, 136, "bf16", seed=12)

@@ -18,7 +18,7 @@ def _built():
 
 def _mm(**kw):
     a = dict(x=A, xs=64, w=A + STEP, transposed=0, offsets=A + 2 * STEP, n=16, experts=4, N=32, K=64, type=BF16,
-             y=A + 3 * STEP, ys=32, yt=BF16, zero=0, stream=None)
+             y=A + 3 * STEP, ys=32, yt=BF16, zero=0, ws=None, ws_bytes=0, stream=None)
     a.update(kw)
     return _lib.raw("hc_grouped_mm", *a.values())
 
@@ -34,6 +34,11 @@ def _mm(**kw):
     (dict(yt=F32, y=A + 3 * STEP + 2), 3),
     (dict(y=A + 64), 4), (dict(y=A + STEP + 100), 4), (dict(y=A + 2 * STEP + 16), 4),
     (dict(n=0), 0), (dict(n=0, x=None, y=None), 0),
+    # a contraction of 8,192 in slices, which need room
+    (dict(K=8192, xs=8192), 1), (dict(K=8192, xs=8192, ws=A + 4 * STEP, ws_bytes=16 * 32 * 4), 1),
+    (dict(K=8192, xs=8192, ws=A + 4 * STEP + 8, ws_bytes=1 << 24), 3),
+    (dict(K=8192, xs=8192, ws=A + 64, ws_bytes=1 << 24), 4),
+    (dict(K=8192, xs=8192, ws=A + 3 * STEP + 512, ws_bytes=1 << 24), 4),
 ])
 def test_product_refusals(kw, expect):
     assert _mm(**kw) == expect
@@ -74,6 +79,18 @@ def test_workspace_bytes():
                 slices = f(n, experts, N, K) / (experts * N * K * 4)
                 assert slices == int(slices) and slices != 1
                 assert slices * experts * -(-N // 256) * -(-K // 256) <= 76
+
+
+def test_product_workspace_bytes():
+    f = _lib.load().hc_grouped_mm_workspace_bytes
+    assert f(100, 4, 512, 1024) == 0 and f(0, 1, 64, 8192) == 0 and f(-1, 1, 64, 8192) == 0 and f(4, 1, 60, 8192) == 0
+    assert f(1, 1, 512, 4088) == 0 and f(1, 1, 512, 4096) == 8 * 512 * 4
+    assert f(768, 64, 5120, 8192) == 0   # tiles enough
+    for n in (1, 40, 1000, 100000):
+        for experts in (1, 3, 20, 1024):
+            for N, K in ((8, 8192), (264, 1 << 20), (2048, 5120), (5120, 16384)):
+                slices = f(n, experts, N, K) / (n * N * 4)
+                assert slices == int(slices) and slices != 1 and slices * experts <= 1024 and slices <= 152
 
 
 def test_binding_refusals():
