@@ -617,7 +617,9 @@ k_ln_backward(const TG *__restrict__ gy, int64_t gs, const TX *__restrict__ x, i
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
                 const float xh = (to_f(xv[i].v[k]) - mean) * rstd;
-                o.v[k] = from_f<TG>(rstd * (to_f(gv[i].v[k]) * wv[i][k] - m1 - xh * m2));
+                // (the product rounded as in the sums: with d = 1 the gradient is 0)
+                const float wg = __fmul_rn(to_f(gv[i].v[k]), wv[i][k]);
+                o.v[k] = from_f<TG>(rstd * (wg - m1 - xh * m2));
             }
             *reinterpret_cast<Vec<TG, VEC> *>(or_ + c) = o;
         }

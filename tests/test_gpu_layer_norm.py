@@ -157,6 +157,16 @@ def test_backward(n, d, x, g, w):
     assert torch.equal(got["g_x"], again["g_x"]) and torch.equal(got["g_norm_w"], again["g_norm_w"])
 
 
+@pytest.mark.parametrize("x,g", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32")])
+def test_rows_of_one_column_have_no_gradient(x, g):
+    """d = 1: x is its own mean, so y does not depend on it."""
+    v, w, b, gr = _inputs(777, 1, x, "fp32", g, seed=6)
+    y, mean, rstd = hcg.hc_layer_norm(v, w, b, return_stats=True)
+    assert torch.equal(y, b.to(y.dtype).expand(777, 1)) and torch.equal(mean, v[:, 0].float())
+    got = hcg.hc_layer_norm_backward(gr, v, w, mean, rstd)
+    assert (got["g_x"] == 0).all() and (got["g_norm_w"] == 0).all()
+
+
 @pytest.mark.parametrize("n,d,pitch,lead", [
     (2500, 1025, 0, 0), (2500, 1026, 0, 0), (2600, 1028, 0, 4), (1800, 1435, 0, 3), (1800, 1438, 2, 2), (900, 2999, 1, 0),
     (700, 5119, 1, 0), (700, 5119, 0, 1), (600, 5118, 0, 0), (600, 5121, 0, 0), (500, 6143, 8, 5), (400, 7001, 0, 7),
