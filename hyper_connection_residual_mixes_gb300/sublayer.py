@@ -315,9 +315,11 @@ class AdamwPlan:
         at = list(map(torch.Tensor.data_ptr, self._tensors))
         if at == self._at:
             return
-        for (t, i, member, numel, dtype), ptr in zip(self._fields, at):
+        # (all of them before the first is described: a refusal leaves the old descriptions whole)
+        for t, i, member, numel, dtype in self._fields:
             if t.numel() != numel or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
                 raise ValueError("%s of tensor %d has changed since the plan was made" % (member, i))
+        for (t, i, member, numel, dtype), ptr in zip(self._fields, at):
             setattr(self._array[i], member, ptr)
             if member == "p":
                 self._array[i].numel = numel

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import hyper_connection_residual_mixes_gb300 as hcg
-from hyper_connection_residual_mixes_gb300 import _lib
+from hyper_connection_residual_mixes_gb300 import _lib, sublayer
 from hyper_connection_residual_mixes_gb300 import build as hc_build
 
 F32, BF16, F16 = 0, 1, 2
@@ -86,3 +86,39 @@ def test_binding_refusals():
         hcg.hc_adamw_step([p], 1e-3, 1)
     codes, scales = hcg.adamw_state(torch.zeros(5, 13), mxfp8=True)[0]
     assert codes.shape == (5, 13) and scales.shape == (3,) and codes.dtype == scales.dtype == torch.uint8
+
+
+@pytest.fixture
+def host_plans(monkeypatch):
+    """adamw_plan on host tensors: its descriptions can be looked at without a device."""
+    def plan(*lists):
+        with monkeypatch.context() as m:
+            m.setattr(sublayer, "_tensor", lambda t, *a, **kw: t)
+            return hcg.adamw_plan(*lists)
+    return plan
+
+
+def _parameters(sizes=((8, 12), (64,), (3, 5, 7))):
+    p, g = [torch.zeros(s) for s in sizes], [torch.ones(s) for s in sizes]
+    states = [hcg.adamw_state(t) for t in p]
+    return p, g, [s[0] for s in states], [s[1] for s in states]
+
+
+def _described(plan, lists):
+    plan._describe()
+    return all(getattr(d, k) == t.data_ptr() for k, ts in zip("pgmv", lists) for d, t in zip(plan._array, ts)) and all(
+        d.numel == t.numel() and d.p_type == d.g_type == F32 for d, t in zip(plan._array, lists[0]))
+
+
+def test_refused_change_leaves_the_description_whole(host_plans):
+    """One tensor moved, another no longer of its size: refused; with both put back
+    the description holds the old places again, not the first one's for a while."""
+    lists = _parameters()
+    plan = host_plans(*lists)
+    assert _described(plan, lists)
+    old, other = lists[0][0].data, lists[0][1].data
+    lists[0][0].data, lists[0][1].data = torch.zeros(8, 12), torch.zeros(7)
+    with pytest.raises(ValueError, match="changed"):
+        plan._describe()
+    lists[0][0].data, lists[0][1].data = old, other
+    assert _described(plan, lists)
