@@ -111,6 +111,21 @@ def load():
         return lib
 
 
+def snapshot():
+    """The function snapshot of the module _tensors: bytes that tell whether any of a
+    list of tensors has changed its place, type, sizes or strides."""
+    import torch
+    try:
+        from . import _tensors
+    except ImportError as e:
+        raise RuntimeError("_tensors.so is not built for this torch (%s); run "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`" % e) from e
+    if _tensors.torch_version != torch.__version__:
+        raise RuntimeError("_tensors.so was built for torch %s, this is %s; run "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`" % (_tensors.torch_version, torch.__version__))
+    return _tensors.snapshot
+
+
 def call(name, *args):
     """Call an entry point and raise HcError on a non-zero status."""
     lib = load()

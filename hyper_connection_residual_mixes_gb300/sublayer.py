@@ -301,28 +301,32 @@ def adamw_state(p, mxfp8=False):
 class AdamwPlan:
     """The tensors of hc_adamw_step, checked and described once (adamw_plan).  It
     keeps them alive; a tensor whose storage has moved since (t.data = ...) is
-    described anew by the next step, one of another shape or type is refused."""
+    described anew by the next step, one of another shape, type or order is
+    refused, also where it begins at the same place."""
 
     def __init__(self, fields, device):
-        self._fields = fields      # (tensor, index of the description, its member, numel, dtype)
+        self._fields = fields      # (tensor, index of the description, its member, shape, dtype)
         self._tensors = [f[0] for f in fields]
         self.device = device
         self.count = 1 + max((f[1] for f in fields), default=-1)
         self._array = (_lib.AdamwTensor * self.count)()
-        self._at = []
+        self._at = None
+        self._snapshot = _lib.snapshot()
 
     def _describe(self):
-        at = list(map(torch.Tensor.data_ptr, self._tensors))
+        # (every step looks at sizes, strides and types too: a pointer alone does not tell a tensor
+        # from its first values, its transpose or another type's view of it)
+        at = self._snapshot(self._tensors)
         if at == self._at:
             return
         # (all of them before the first is described: a refusal leaves the old descriptions whole)
-        for t, i, member, numel, dtype in self._fields:
-            if t.numel() != numel or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
+        for t, i, member, shape, dtype in self._fields:
+            if t.shape != shape or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
                 raise ValueError("%s of tensor %d has changed since the plan was made" % (member, i))
-        for (t, i, member, numel, dtype), ptr in zip(self._fields, at):
-            setattr(self._array[i], member, ptr)
+        for t, i, member, shape, dtype in self._fields:
+            setattr(self._array[i], member, t.data_ptr())
             if member == "p":
-                self._array[i].numel = numel
+                self._array[i].numel = shape.numel()
             if member in ("p", "g", "p_copy"):
                 setattr(self._array[i], "copy_type" if member == "p_copy" else member + "_type", _DTYPE[dtype])
         self._at = at
@@ -355,7 +359,7 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None):
     for i, (p, g, m, v, c) in enumerate(zip(params, grads, exp_avg, exp_avg_sq, copies)):
         def field(t, name, member, dtypes, shape):
             _dense(t, "%s[%d]" % (name, i), dtypes, shape, dev)
-            fields.append((t, i, member, t.numel(), t.dtype))
+            fields.append((t, i, member, t.shape, t.dtype))
         field(p, "params", "p", (p.dtype,), p.shape)
         field(g, "grads", "g", (torch.float32, p.dtype) if p.dtype != torch.float32 else (torch.float32,), p.shape)
         for s, name, member in ((m, "exp_avg", "m"), (v, "exp_avg_sq", "v")):

@@ -122,3 +122,48 @@ def test_refused_change_leaves_the_description_whole(host_plans):
         plan._describe()
     lists[0][0].data, lists[0][1].data = old, other
     assert _described(plan, lists)
+
+
+CHANGES = {
+    "shorter": lambda t: t[:3], "another order": lambda t: t.t(), "another type": lambda t: t.view(torch.int32),
+    "another shape": lambda t: t.view(12, 8), "one value for all": lambda t: t[:1, :1].expand(8, 12),
+    "another type of half the size": lambda t: t.view(torch.bfloat16)[:, :12],
+    "rows over one another": lambda t: t.as_strided((8, 12), (8, 1)),
+}
+
+
+@pytest.mark.parametrize("which", range(4))
+@pytest.mark.parametrize("change", CHANGES)
+@pytest.mark.parametrize("moved", [False, True])
+def test_changed_tensors_are_refused(host_plans, which, change, moved):
+    """Also where the tensor still begins at the same place."""
+    lists = _parameters()
+    plan = host_plans(*lists)
+    assert _described(plan, lists)
+    t = lists[which][0]
+    old = t.data
+    t.data = CHANGES[change](old.clone() if moved else old)
+    assert moved or t.data_ptr() == old.data_ptr()
+    with pytest.raises(ValueError, match=r"%s of tensor 0 has changed" % "pgmv"[which]):
+        plan._describe()
+    t.data = old
+    assert _described(plan, lists)
+    t.data = old.clone()           # moved alone: followed
+    assert _described(plan, lists)
+
+
+@pytest.mark.parametrize("k", range(3))
+def test_changed_copies_and_codes_are_refused(host_plans, k):
+    p, g = [torch.zeros(8, 12)], [torch.ones(8, 12)]
+    m, v = hcg.adamw_state(p[0], mxfp8=True)
+    copy = torch.zeros(8, 12, dtype=torch.bfloat16)
+    plan = host_plans(p, g, [m], [v], [copy])
+    plan._describe()
+    t = (m[0], v[1], copy)[k]
+    old = t.data
+    for change in (old[:1], old.view(torch.int16 if t is copy else torch.int8), old.view(*old.shape[::-1], 1)):
+        t.data = change
+        with pytest.raises(ValueError, match="changed"):
+            plan._describe()
+    t.data = old
+    plan._describe()

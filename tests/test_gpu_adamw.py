@@ -315,3 +315,25 @@ def test_same_tensor_twice_is_refused():
     shared = hcg.adamw_plan([c.p[0], torch.zeros_like(c.p[0])], c.g * 2, [c.m[0], torch.zeros_like(c.m[0])],
                             [c.v[0], torch.zeros_like(c.v[0])])
     hcg.hc_adamw_step(shared, step=1, **HYPER)   # one gradient for two parameters is fine
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_tensors_changed_in_place_are_refused(packed):
+    """A shorter, a transposed and another type's tensor at the same address; put
+    back, the step gives what an untouched one gives."""
+    c, d = Case([4096, 300], "fp32", "fp32", packed, seed=12), Case([4096, 300], "fp32", "fp32", packed, seed=12)
+    hcg.hc_adamw_step(c.plan, step=1, **HYPER)
+    hcg.hc_adamw_step(d.plan, step=1, **HYPER)
+    before = [t.clone() for t in c.tensors()]
+    m = c.m[0][0] if packed else c.m[0]
+    for t in (c.p[0], c.g[0], m):
+        old = t.data
+        for change in (old[:10], old.view(64, 64), old.view(torch.int8 if t.dtype == torch.uint8 else torch.int32), old[::2]):
+            t.data = change
+            with pytest.raises(ValueError, match="changed"):
+                hcg.hc_adamw_step(c.plan, step=2, **HYPER)
+        t.data = old
+    assert all(torch.equal(a, b) for a, b in zip(c.tensors(), before))
+    hcg.hc_adamw_step(c.plan, step=2, **HYPER)
+    hcg.hc_adamw_step(d.plan, step=2, **HYPER)
+    assert all(torch.equal(a, b) for a, b in zip(c.tensors(), d.tensors()))
