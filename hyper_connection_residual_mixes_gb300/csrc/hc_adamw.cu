@@ -110,10 +110,16 @@ __device__ __forceinline__ f32x2 pair_of_codes(const Vec<uint8_t, V> &c, int k) 
     const float2 f = __half22float2(__half2(h));
     return f2_make(f.x, f.y);
 }
+// The larger of two numbers, a NaN if one is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+    return a;
+}
 // Codes of a thread's values; the 32 / V threads of a group agree on its scale,
 // the smallest power of two at or above a / 448.  448 is 1.75 * 2^8, so with
 // a = 1.f * 2^E that power is 2^(E - 8), or 2^(E - 7) where 1.f > 1.75: adding
-// 0x1fffff to the bits carries into the exponent exactly then.
+// 0x1fffff to the bits carries into the exponent exactly then.  A NaN becomes
+// E4M3's NaN and does not count in the scale.
 template <bool kRoot, int V>
 __device__ __forceinline__ Vec<uint8_t, V> encode(const f32x2 (&x)[V / 2], uint8_t &byte) {
     float a = 0.0f;
@@ -139,11 +145,11 @@ __device__ __forceinline__ Vec<uint8_t, V> encode(const f32x2 (&x)[V / 2], uint8
             f2_split(f2_mul(x[k / 2 + h], inv), q0, q1);
             if (kRoot) {
                 // the smallest code stands for 2^-9; x 2^110, cut off at 1, is 1 for every
-                // positive root (they are at least 2^-75) and 0 for zero
+                // positive root (they are at least 2^-75) and 0 for zero and NaN (whose code is q's, a NaN)
                 float x0, x1;
                 f2_split(x[k / 2 + h], x0, x1);
-                q0 = fmaxf(q0, __saturatef(x0 * 0x1p110f) * 0x1p-9f);
-                q1 = fmaxf(q1, __saturatef(x1 * 0x1p110f) * 0x1p-9f);
+                q0 = max_or_nan(q0, __saturatef(x0 * 0x1p110f) * 0x1p-9f);
+                q1 = max_or_nan(q1, __saturatef(x1 * 0x1p110f) * 0x1p-9f);
             }
             two[h] = __nv_cvt_float2_to_fp8x2(make_float2(q0, q1), __NV_SATFINITE, __NV_E4M3);
         }

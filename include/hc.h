@@ -414,8 +414,9 @@ hc_status hc_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dtype g_t
  * 2^(byte - 127); the step writes as scale the smallest power of two at or above
  * amax / 448 (from 2^-126 on), codes to nearest, ties to even, and for a positive
  * r at least the smallest positive code.  All bytes zero stand for zero states.
- * A gradient that is not finite spoils its own value; an infinite one with 8-bit
- * states also the states of its group of 32.
+ * A gradient that is not finite spoils its own value (a NaN stays in p, m and v
+ * with either kind of states); an infinite one with 8-bit states also the states of
+ * its group of 32.
  *
  *   tensors [count], an array in HOST memory; it is read during the call only
  *   p of p_type; g of g_type: fp32 or p_type; p_copy (optional, p_type HC_F32

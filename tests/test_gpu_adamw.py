@@ -337,3 +337,40 @@ def test_tensors_changed_in_place_are_refused(packed):
     hcg.hc_adamw_step(c.plan, step=2, **HYPER)
     hcg.hc_adamw_step(d.plan, step=2, **HYPER)
     assert all(torch.equal(a, b) for a, b in zip(c.tensors(), d.tensors()))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("p,g,offset", [("fp32", "fp32", 0), ("bf16", "bf16", 0), ("fp32", "fp32", 1)])
+def test_non_finite_gradient_in_the_states(p, g, offset, packed, bad):
+    """A NaN stays in both moments of its value and nowhere else; an infinite
+    gradient spoils the 8-bit states of its group at the most."""
+    c, d = Case([4200], p, g, packed, seed=3, offset=offset), Case([4200], p, g, packed, seed=3, offset=offset)
+    c.g[0][70] = bad
+    hcg.hc_adamw_step(c.plan, step=2, **HYPER)
+    hcg.hc_adamw_step(d.plan, step=2, **HYPER)
+    other = torch.ones((4200,), dtype=torch.bool, device="cuda")
+    other[70] = False
+    assert c.p[0][70].isnan() and torch.equal(c.p[0][other], d.p[0][other])
+    group = other.clone()
+    group[64:96] = False
+    for x, y in ((c.m[0], d.m[0]), (c.v[0], d.v[0])):
+        got, want = (_decode(x), _decode(y)) if packed else (x, y)
+        assert torch.equal(got[group if packed else other], want[group if packed else other])
+        if bad != bad:
+            assert got[70].isnan() and got[other].isfinite().all()
+        elif not packed:
+            assert got[70].isinf()
+    if packed and bad != bad:   # its group's scales are those of the other values
+        for x, y in ((c.m[0], d.m[0]), (c.v[0], d.v[0])):
+            top = _decode(y)[64:96][other[64:96]].abs().max()
+            assert (_decode(x)[64:96][other[64:96]].abs().max() - top).abs() <= 2.0 ** -3 * top
+
+
+def test_groups_of_nothing_but_nan():
+    c = Case([128], "fp32", "fp32", True, seed=4)
+    c.g[0][32:64] = float("nan")
+    hcg.hc_adamw_step(c.plan, step=2, **HYPER)
+    for s in (c.m[0], c.v[0]):
+        v = _decode(s)
+        assert v[32:64].isnan().all() and v[:32].isfinite().all() and v[64:].isfinite().all()
