@@ -405,7 +405,8 @@ hc_status hc_layer_norm_backward(const void *g_y, int64_t g_stride, hc_dtype g_t
  * nearest in its own type.  With fp32 states every operation is rounded once in
  * the order written; with 8-bit states products and sums are fused and the root
  * and the reciprocal are the hardware's approximations, each within 2^-23 of its
- * value (and a v below 2^-126 counts as zero).
+ * value (and an eps below 2^-126 counts as zero).  With eps = 0 a value whose v is
+ * zero in fp32 (no gradient yet, or none above some 2^-73) is divided by zero.
  *
  * A tensor's states are fp32 (m_scales and v_scales NULL), or 8 bits: m [numel]
  * E4M3 codes and v [numel] E4M3 codes of r = sqrt(v), with a UE8M0 scale byte per

@@ -374,3 +374,31 @@ def test_groups_of_nothing_but_nan():
     for s in (c.m[0], c.v[0]):
         v = _decode(s)
         assert v[32:64].isnan().all() and v[:32].isfinite().all() and v[64:].isfinite().all()
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-30])
+@pytest.mark.parametrize("p", ["fp32", "bf16"])
+def test_roots_of_tiny_second_moments(p, eps):
+    """8-bit states, gradients whose squares are subnormal in fp32: the step is lr
+    g / (|g| + eps) like any first step.  A sum of subnormal terms is off by half a
+    unit of 2^-149 for each of its (at most three) roundings: relative to v, and
+    half of that in the root."""
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    c = Case([2000], p, "fp32", True, seed=5, zero=True)
+    size = torch.exp2(-66 + 3 * torch.rand((2000,), generator=gen, device="cuda"))
+    c.g[0].copy_(torch.where(torch.rand((2000,), generator=gen, device="cuda") < 0.5, -size, size))
+    b1, b2 = HYPER["betas"]
+    for step in (1, 2, 3):
+        m0, r0, p0, g = _decode(c.m[0]).double(), _decode(c.v[0]).double(), c.p[0].double(), c.g[0].double()
+        hcg.hc_adamw_step(c.plan, step=step, **{**HYPER, "adam_eps": eps})
+        m, v = m0 * b1 + g * (1 - b1), r0 * r0 * b2 + g * g * (1 - b2)
+        am = m0.abs() * b1 + g.abs() * (1 - b1)
+        rate = HYPER["lr"] / (1 - b1 ** step) / ((v / (1 - b2 ** step)).sqrt() + eps)
+        want = p0 * (1 - HYPER["lr"] * HYPER["weight_decay"]) - rate * m
+        room = rate * am * (16 * U + 4 * 2.0 ** -150 / v) + 4 * U * p0.abs()
+        half = torch.finfo(c.p[0].dtype).eps / 2
+        assert ((c.p[0].double() - want).abs() <= room + half * (want.abs() + room)).all()
+        assert ((c.v[0][0] > 0) & (c.v[0][0] < 0x7F)).all()
+        scale = _power(c.v[0][1]).double().repeat_interleave(32)[:2000]
+        root = v.sqrt()
+        assert ((_decode(c.v[0]).double() - root).abs() <= (2.0 ** -4 + 2.0 ** -150 / v) * root + 2.0 ** -9 * scale).all()
