@@ -353,6 +353,23 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Plan &p, int tile, 
     return t;
 }
 
+// Rows [s, t) of an expert; false, and none, for a range that is out of order or out
+// of the n rows.
+__device__ __forceinline__ bool range_of(const int32_t *offsets, int expert, int64_t n, int64_t &s, int64_t &t) {
+    s = __ldg(offsets + expert), t = __ldg(offsets + expert + 1);
+    if (s >= 0 && t >= s && t <= n) return true;
+    s = t = 0;
+    return false;
+}
+// Whether the (not empty) range keeps its rows where some ranges are out of order: it
+// must not begin before the end of an earlier one that kept its own.
+template <typename I>
+__device__ __forceinline__ bool takes_rows(I s, I t, I &end) {
+    if (s < end) return false;
+    end = t;
+    return true;
+}
+
 // Where the i-th stage of `stages` starts.  The gradient begins with an expert's
 // last rows: their clearing then runs while the tile before is still multiplied.
 template <bool kWeights>
@@ -420,12 +437,13 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     // every expert's rows and how many tiles they make; a range that is out of
     // order or out of the rows counts as empty and is reported
     const int parts = a.experts * a.slices;
+    bool wrong = false;
     for (int e = threadIdx.x; e < parts; e += kThreads) {
         const int slice = e / a.experts, ex = e - slice * a.experts;
-        int64_t s = __ldg(a.offsets + ex), t = __ldg(a.offsets + ex + 1);
-        if (s < 0 || t < s || t > a.n) {
+        int64_t s, t;
+        if (!range_of(a.offsets, ex, a.n, s, t)) {
             if (blockIdx.x == 0) atomicOr(&g_device_error, kErrOffsets);
-            s = t = 0;
+            wrong = true;
         }
         if (kWeights && a.slices > 1) {  // whole stages each, the last ones what is left
             const int64_t per = ((t - s + a.slices - 1) / a.slices + kSub * kBK - 1) / (kSub * kBK) * (kSub * kBK);
@@ -437,7 +455,22 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         const int mt = (a.F + C::kTileF - 1) / C::kTileF;
         s_first[e + 1] = kWeights ? mt * ((a.C + BN - 1) / BN) : mt * (int)((t - s + BN - 1) / BN);
     }
-    __syncthreads();
+    // Ranges all in order follow one another.  Where some are not, others may share rows:
+    // two CTAs would write them, and the tiles' number, bounded for n rows, leave 32 bits.
+    if (__syncthreads_or(wrong)) {
+        if (threadIdx.x == 0) {
+            int end = 0;
+            for (int ex = 0; ex < a.experts; ++ex) {
+                const int s = s_start[ex], t = s_end[(a.slices - 1) * a.experts + ex];  // (the last slice's end)
+                if (s >= t || takes_rows(s, t, end)) continue;
+                for (int e = ex; e < parts; e += a.experts) {
+                    s_start[e] = s_end[e] = 0;
+                    if (!kWeights) s_first[e + 1] = 0;
+                }
+            }
+        }
+        __syncthreads();
+    }
     if (warp == 0) {  // running sum of the tile counts
         int carry = 0;
         if (lane == 0) s_first[0] = 0;
@@ -733,18 +766,30 @@ __global__ void __launch_bounds__(kJoinThreads)
 k_join_rows(const float *part, const int32_t *offsets, int experts, int64_t n, int F, int slices, T *out, int64_t stride, int zero_rest) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = blockIdx.x;
-    int mine = 0;
+    bool mine = false, wrong = false;
+    int64_t s, t;
     for (int e = threadIdx.x; e < experts; e += kJoinThreads) {
-        const int64_t s = __ldg(offsets + e), t = __ldg(offsets + e + 1);
-        mine |= s >= 0 && t <= n && s <= row && row < t;
+        wrong |= !range_of(offsets, e, n, s, t);
+        mine |= s <= row && row < t;
     }
-    const bool has = __syncthreads_or(mine);
+    bool has = __syncthreads_or(mine);
+    if (__syncthreads_or(wrong)) {  // (as the kernel before gave out the rows)
+        mine = false;
+        if (threadIdx.x == 0) {
+            int64_t end = 0;
+            for (int e = 0; e < experts; ++e) {
+                range_of(offsets, e, n, s, t);
+                if (s < t && takes_rows(s, t, end)) mine |= s <= row && row < t;
+            }
+        }
+        has = __syncthreads_or(mine);
+    }
     const int f = (blockIdx.y * kJoinThreads + threadIdx.x) * 4;
     if (f >= F) return;  // (F is a multiple of 8)
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (has) {
-        for (int s = 0; s < slices; ++s) {
-            const float4 u = __ldcg(reinterpret_cast<const float4 *>(part + (s * n + row) * F + f));
+        for (int k = 0; k < slices; ++k) {
+            const float4 u = __ldcg(reinterpret_cast<const float4 *>(part + (k * n + row) * F + f));
             v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
         }
     } else {

@@ -462,7 +462,8 @@ hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr
  *   w [experts, N, K] of type, or with transposed [experts, K, N]            in
  *   offsets [experts + 1] int32, DEVICE, ascending within [0, n]: read by the
  *   kernel, so the host need not know them.  An expert whose range is out of order
- *   or out of the rows counts as empty and is reported by hc_consume_device_error.
+ *   or out of the rows, or begins before the end of an earlier one that counts, counts
+ *   as empty; it is reported by hc_consume_device_error.
  *   y [n, N] of y_type: type or fp32, rows y_stride >= N apart               out
  *   Rows of y that belong to no expert (before offsets[0], from offsets[experts]
  *   on) are left as they are, or with zero_rest written as zeros.

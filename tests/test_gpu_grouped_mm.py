@@ -337,3 +337,37 @@ def test_offsets_beyond_32_bits():
         b = a + 1
         xe, we = x[a:b].double(), w[e].double().t()
         _close(y[a:b], xe @ we, xe.abs() @ we.abs(), K)
+
+
+@pytest.mark.parametrize("K,N", [(64, 72), (8192, 64)])
+@pytest.mark.parametrize("bad,taken", [([0, 60, 20, 100, 100], {0}), ([0, 50, 100, 0, 100], {0, 1}), ([90, 10, 40, 30, 100], {1}),
+                                       ([0, 120, 30, 80, 60], {2}), ([0, 100] * 8 + [0, 100], {0}), ([0, 1, 0, 2, 0, 3, 2, 5], {0, 6})])
+def test_ranges_that_share_rows(K, N, bad, taken):
+    """A range that begins before an earlier one's end counts as empty: every row has
+    one expert, also where others' ranges are out of order (K = 8,192: in slices)."""
+    x, w, _, _ = _inputs([100] + [0] * (len(bad) - 2), N, K, "bf16", seed=17)
+    off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    _lib.raw("hc_consume_device_error", None)
+    y = torch.full((100, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    hcg.hc_grouped_mm(x, w, off, y=y)
+    assert _lib.raw("hc_consume_device_error", None) == 1
+    free = torch.ones((100,), dtype=torch.bool, device="cuda")
+    for e in taken:
+        a, b = bad[e], bad[e + 1]
+        free[a:b] = False
+        xe, we = x[a:b].double(), w[e].double().t()
+        _close(y[a:b], xe @ we, xe.abs() @ we.abs(), K)
+    assert (y[free] == 3).all()
+
+
+@pytest.mark.parametrize("scale", [1, 90])
+def test_gradients_of_ranges_that_share_rows(scale):
+    """The weights' gradient likewise, with 9,000 rows in slices."""
+    n = 100 * scale
+    x, _, g, _ = _inputs([n, 0, 0], 72, 64, "bf16", seed=18)
+    assert (_lib.load().hc_grouped_mm_weights_workspace_bytes(n, 3, 72, 64) > 0) == (scale > 1)
+    bad = [b * scale for b in (0, 60, 20, 100)]
+    _lib.raw("hc_consume_device_error", None)
+    got = hcg.hc_grouped_mm_weights(g, x, torch.tensor(bad, dtype=torch.int32, device="cuda"))
+    assert _lib.raw("hc_consume_device_error", None) == 1
+    _check_weights(g, x, torch.tensor([0, 60 * scale, 60 * scale, 60 * scale], device="cuda"), False, got)
