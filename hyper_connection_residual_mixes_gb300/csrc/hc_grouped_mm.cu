@@ -457,7 +457,8 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     }
     // Ranges all in order follow one another.  Where some are not, others may share rows:
     // two CTAs would write them, and the tiles' number, bounded for n rows, leave 32 bits.
-    if (__syncthreads_or(wrong)) {
+    const bool disorder = __syncthreads_or(wrong);
+    if (disorder) {
         if (threadIdx.x == 0) {
             int end = 0;
             for (int ex = 0; ex < a.experts; ++ex) {
@@ -675,13 +676,20 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         // (F is a multiple of 8, so pairs end with a row)
         const bool paired = a.out_stride % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
         if (!kWeights && a.zero_rest) {
-            // rows of no expert: before offsets[0] and from offsets[experts] on
-            int64_t lo = __ldg(a.offsets), hi = __ldg(a.offsets + a.experts);
-            lo = lo < 0 ? 0 : lo > a.n ? a.n : lo;
-            hi = hi < lo ? lo : hi > a.n ? a.n : hi;
-            for (int64_t r = blockIdx.x; r < lo + (a.n - hi); r += gridDim.x) {
-                const int64_t row = r < lo ? r : hi + (r - lo);
-                for (int f = threadIdx.x - 64; f < a.F; f += 32 * kEpilogue) put(a.out, row * a.out_stride + f, 0.0f, a.out_f32, a.fp16);
+            const auto clear = [&](int64_t from, int64_t to) {
+                for (int64_t row = from + blockIdx.x; row < to; row += gridDim.x)
+                    for (int f = threadIdx.x - 64; f < a.F; f += 32 * kEpilogue) put(a.out, row * a.out_stride + f, 0.0f, a.out_f32, a.fp16);
+            };
+            // rows of no expert: before the first one's and from the last one's end on, and
+            // between the ranges that count where some are out of order
+            if (!disorder) {
+                clear(0, __ldg(a.offsets));
+                clear(__ldg(a.offsets + a.experts), a.n);
+            } else {
+                int64_t end = 0;
+                for (int ex = 0; ex < a.experts; ++ex)  // (one slice: the ranges ascend)
+                    if (s_start[ex] < s_end[ex]) clear(end, s_start[ex]), end = s_end[ex];
+                clear(end, a.n);
             }
         }
         int c = 0;
@@ -760,7 +768,7 @@ cudaError_t join_slices(const float *part, int64_t count, int slices, void *out,
 }
 
 // The same for a product: a block adds up 4 * kJoinThreads outputs of a row, if the
-// row is an expert's; others are zeroed (zero_rest: those outside all ranges) or left.
+// row is an expert's; others are zeroed (zero_rest) or left.
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kJoinThreads)
 k_join_rows(const float *part, const int32_t *offsets, int experts, int64_t n, int F, int slices, T *out, int64_t stride, int zero_rest) {
@@ -792,11 +800,8 @@ k_join_rows(const float *part, const int32_t *offsets, int experts, int64_t n, i
             const float4 u = __ldcg(reinterpret_cast<const float4 *>(part + (k * n + row) * F + f));
             v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
         }
-    } else {
-        int64_t lo = __ldg(offsets), hi = __ldg(offsets + experts);
-        lo = lo < 0 ? 0 : lo > n ? n : lo;
-        hi = hi < lo ? lo : hi > n ? n : hi;
-        if (!zero_rest || (row >= lo && row < hi)) return;
+    } else if (!zero_rest) {
+        return;
     }
     T *o = out + row * stride + f;
     Vec<T, 4> r;

@@ -466,7 +466,8 @@ hc_status hc_adamw_step(const hc_adamw_tensor *tensors, int64_t count, double lr
  *   as empty; it is reported by hc_consume_device_error.
  *   y [n, N] of y_type: type or fp32, rows y_stride >= N apart               out
  *   Rows of y that belong to no expert (before offsets[0], from offsets[experts]
- *   on) are left as they are, or with zero_rest written as zeros.
+ *   on, those of ranges that count as empty) are left as they are, or with zero_rest
+ *   written as zeros.
  *   g_y [n, N] of type, rows g_stride >= N apart                             in
  *   g_w [experts, N, K] (transposed: [experts, K, N]) of g_type: type or fp32    out
  *   workspace of hc_grouped_mm_workspace_bytes or

@@ -371,3 +371,30 @@ def test_gradients_of_ranges_that_share_rows(scale):
     got = hcg.hc_grouped_mm_weights(g, x, torch.tensor(bad, dtype=torch.int32, device="cuda"))
     assert _lib.raw("hc_consume_device_error", None) == 1
     _check_weights(g, x, torch.tensor([0, 60 * scale, 60 * scale, 60 * scale], device="cuda"), False, got)
+
+
+@pytest.mark.parametrize("K,N", [(64, 72), (8192, 64)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad,taken", [([0, 60, 101], {0}), ([0, -5, 100], set()), ([0, 70, 60], {0}), ([5, 30, 130, 60, 90], {0, 3}),
+                                       ([-1, 20, 100], {1}), ([100, 0, 0, 0], set())])
+def test_rows_of_refused_ranges_are_zeros(K, N, out, bad, taken):
+    """In a y made by the call; in one that is given they stay.  With K = 8,192 the
+    contraction is summed in slices."""
+    x, w, _, _ = _inputs([100] + [0] * (len(bad) - 2), N, K, "bf16", seed=16)
+    sliced = _lib.load().hc_grouped_mm_workspace_bytes(100, len(bad) - 1, N, K) > 0
+    assert sliced == (K == 8192)
+    off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    _lib.raw("hc_consume_device_error", None)
+    for _ in range(3):
+        torch.full((100, N), 7.0, dtype=out, device="cuda")   # what the next allocation of this size holds
+        y = hcg.hc_grouped_mm(x, w, off, out_dtype=out)
+        given = torch.full((100, N), 3.0, dtype=out, device="cuda")
+        hcg.hc_grouped_mm(x, w, off, y=given)
+        assert _lib.raw("hc_consume_device_error", None) == 1
+        free = torch.ones((100,), dtype=torch.bool, device="cuda")
+        for e in taken:
+            a, b = bad[e], bad[e + 1]
+            free[a:b] = False
+            xe, we = x[a:b].double(), w[e].double().t()
+            _close(y[a:b], xe @ we, xe.abs() @ we.abs(), K)
+        assert (y[free] == 0).all() and (given[free] == 3).all() and torch.equal(given[~free], y[~free])
