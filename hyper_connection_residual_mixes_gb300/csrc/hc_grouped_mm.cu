@@ -931,7 +931,7 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorM
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = C::kSmem, cfg.stream = s;
     cfg.attrs = attrs, cfg.numAttrs = kPair ? 2 : 1;
-    int grid = ctas[dev].load(std::memory_order_relaxed);
+    int grid = ctas[dev].load(std::memory_order_acquire);
     if (!grid) {
         if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&grid, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
@@ -943,7 +943,7 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorM
             grid = grid / 2 < clusters ? grid / 2 * 2 : clusters * 2;
         }
         grid *= C::kPerSm;
-        ctas[dev].store(grid, std::memory_order_relaxed);
+        ctas[dev].store(grid, std::memory_order_release);  // (the attribute is set for whoever reads it)
     }
     cfg.gridDim = dim3((unsigned)grid);
     return cudaLaunchKernelEx(&cfg, k, ta, tb, small, a);

@@ -898,10 +898,13 @@ int current_device() {
     return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices ? dev : 0;
 }
 int sm_count_of_device() {
-    static int sms[kDevices] = {0};
+    static std::atomic<int> sms[kDevices];  // (any host thread may be the first to ask)
     const int dev = current_device();
-    if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
-    return sms[dev];
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    sms[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 // Blocks of a kernel that an SM holds by its threads and registers (handed out to
 // warps in units of 256), and the most dynamic shared memory allowed to it; asked
@@ -910,7 +913,7 @@ template <auto kKernel>
 cudaError_t blocks_per_sm(int threads, int *per_sm) {
     static std::atomic<int> regs[kDevices];
     const int dev = current_device();
-    int r = regs[dev].load(std::memory_order_relaxed);
+    int r = regs[dev].load(std::memory_order_acquire);
     if (!r) {
         cudaFuncAttributes fa{};
         cudaError_t e = cudaFuncGetAttributes(&fa, kKernel);
@@ -919,7 +922,7 @@ cudaError_t blocks_per_sm(int threads, int *per_sm) {
                                      kSmemBlock - (int)fa.sharedSizeBytes);
         if (e != cudaSuccess) return e;
         r = fa.numRegs;
-        regs[dev].store(r, std::memory_order_relaxed);
+        regs[dev].store(r, std::memory_order_release);  // (the attribute is set for whoever reads it)
     }
     const int warps = threads / 32, by_regs = 65536 / ((r * 32 + 255) / 256 * 256 * warps), by_threads = 64 / warps;
     *per_sm = by_regs < by_threads ? by_regs : by_threads;

@@ -7,6 +7,10 @@ streams; then the side's backward, both products' and the norm's, and one
 AdamW step over everything that learns.  Every stage is held to its formula in
 64 bits on the inputs it had, with the bounds of the operators' own tests; and
 the whole step, captured into one graph, gives the eager step's bits."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -163,3 +167,49 @@ def test_steps_on_two_streams():
     for got, want in zip((one, two), ref):
         for a, b in zip(got.state(), want.state()):
             assert torch.equal(a, b)
+
+
+_FIRST_CALLS = """
+import threading, torch
+import hyper_connection_residual_mixes_gb300 as hcg
+torch.cuda.init()
+g = torch.Generator(device="cuda").manual_seed(1)
+r = lambda *s: torch.randn(s, generator=g, device="cuda")
+x, w, gy = r(700, 5120).bfloat16(), r(5120), r(700, 5120)
+rows, weights = r(300, 512).bfloat16(), r(4, 256, 512).bfloat16()
+off = torch.tensor([0, 90, 100, 250, 300], dtype=torch.int32, device="cuda")
+results, errors, go = {}, [], threading.Barrier(8)
+torch.cuda.synchronize()
+
+def work(k):
+    try:
+        p, s = torch.ones(5000, device="cuda"), torch.cuda.Stream()
+        m, v = hcg.adamw_state(p)
+        plan = hcg.adamw_plan([p], [torch.full_like(p, 0.5)], [m], [v])
+        torch.cuda.synchronize()
+        go.wait()
+        with torch.cuda.stream(s):
+            y, mean, rstd = hcg.hc_layer_norm(x, w, return_stats=True)
+            n = hcg.hc_layer_norm_backward(gy, x, w, mean, rstd)
+            b = hcg.hc_grouped_mm_backward(hcg.hc_grouped_mm(rows, weights, off), rows, weights, off)
+            hcg.hc_adamw_step(plan, 1e-3, 1)
+        s.synchronize()
+        results[k] = [y, mean, rstd, *n.values(), *b.values(), p, m, v]
+    except BaseException as e:
+        errors.append(e)
+
+threads = [threading.Thread(target=work, args=(k,)) for k in range(8)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert not errors, errors
+assert all(torch.equal(a, b) for k in range(1, 8) for a, b in zip(results[0], results[k]))
+assert all(t.isfinite().all() for t in results[0])
+print("same")
+"""
+
+
+def test_first_calls_from_several_host_threads():
+    """In a process of its own: eight host threads make its first calls at once."""
+    out = subprocess.run([sys.executable, "-c", _FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert out.returncode == 0 and out.stdout.split() == ["same"], out.stdout + out.stderr
