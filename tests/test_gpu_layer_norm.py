@@ -322,3 +322,30 @@ def test_offsets_beyond_32_bits():
     x.copy_(torch.randn((10, d), generator=torch.Generator(device="cuda").manual_seed(2), device="cuda"))
     w = torch.rand((d,), device="cuda")
     assert torch.equal(hcg.hc_layer_norm(x, w), hcg.hc_layer_norm(x.contiguous(), w))
+
+
+@pytest.mark.parametrize("n,d,pitch,lead", [(2500, 1025, 0, 1), (1800, 1438, 2, 2), (700, 5119, 1, 3), (500, 6143, 8, 5), (320, 8190, 4, 2),
+                                            (170, 16383, 0, 7), (19000, 131, 0, 1), (9800, 258, 2, 0), (5, 1031, 0, 3), (3, 77, 5, 2),
+                                            (1, 2049, 0, 5), (40, 512, 8, 8)])
+@pytest.mark.parametrize("x,g", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32")])
+def test_outputs_lie_in_their_rows(n, d, pitch, lead, x, g):
+    """Outputs in rows of a wider buffer: every value in its place, every NaN around
+    them (before the first row, between rows, behind the last) still there."""
+    v, w, b, gr = _inputs(n, d, x, "fp32", g, seed=7)
+    _, mean, rstd = _check_forward(v, w, b)
+
+    def among_nan(dtype):
+        buf = torch.full((lead + n * (d + pitch) + 16,), float("nan"), dtype=dtype, device="cuda")
+        rows = buf[lead:lead + n * (d + pitch)].view(n, d + pitch)[:, :d]
+        outside = torch.ones_like(buf, dtype=torch.bool)
+        outside[lead:lead + n * (d + pitch)].view(n, d + pitch)[:, :d] = False
+        return buf, rows, outside
+
+    buf, y, outside = among_nan(v.dtype)
+    hcg.hc_layer_norm(v, w, b, y=y)
+    want, _, _, room = _ref(v, w, b, 1e-5)
+    assert ((y.double() - want).abs() <= _half(v.dtype) * (want.abs() + room) + _tiny(v.dtype) + room).all()
+    assert buf[outside].isnan().all()
+    buf, g_x, outside = among_nan(gr.dtype)
+    _check_backward(v, w, gr, mean, rstd, hcg.hc_layer_norm_backward(gr, v, w, mean, rstd, g_x=g_x))
+    assert buf[outside].isnan().all()
