@@ -138,6 +138,9 @@ def hc_layer_norm_backward(g_y, x, norm_w, mean, rstd, bias=True, g_x=None, work
     """The backward of hc_layer_norm: g_y [..., d] (fp32 or x's type), x, norm_w and
     the forward's mean, rstd -> dict of g_x [..., d] of g_y's type and the sums
     over all rows g_norm_w [d] and (unless bias is False) g_norm_b [d], fp32.
+    Of a norm on the path's h (h_pre_out) g_x is the gradient of h = sum_s pre_mix[s]
+    x[s], which hc_block_step_backward does not take: add pre_mix[s] g_x to its
+    g_x[s] and <g_x, x[s]> to its g_pre_mix[s].
     workspace: a uint8 device tensor of at least the size the library asks for
     (allocated here when None)."""
     n, xs, d = _norm_input(x)
@@ -337,7 +340,10 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None):
     on one device.  params[i] fp32, bf16 or fp16; grads[i] of its shape, fp32 or
     its type; exp_avg[i], exp_avg_sq[i] as adamw_state makes them (fp32, or
     (codes, scales) pairs); copies[i] (optional, None where there is none): a
-    bf16 or fp16 tensor that receives an fp32 parameter's new value rounded."""
+    bf16 or fp16 tensor that receives an fp32 parameter's new value rounded.
+    The step reads the gradients where these tensors are: a gradient that a
+    call has allocated anew is copied into its tensor (or that call given the
+    tensor to write to) before the step."""
     params, grads, exp_avg, exp_avg_sq = list(params), list(grads), list(exp_avg), list(exp_avg_sq)
     copies = [None] * len(params) if copies is None else list(copies)
     if not params:

@@ -382,6 +382,9 @@ hc_status hc_layer_norm(const void *x, int64_t x_stride, hc_dtype x_type, const 
  *   g_y [n, d] of g_type: fp32 or x_type                                   in
  *   x, norm_w as in the forward; mean, rstd [n] as it wrote them           in
  *   g_x [n, d] of g_type, rows gx_stride >= d apart                        out
+ *   (of a norm on h_pre_out the gradient of h = sum_s pre_mix[s] x[s], no input of
+ *   hc_block_step_backward: it adds pre_mix[s] g_x to that call's g_x[s] and
+ *   <g_x, x[s]> to its g_pre_mix[s])
  *   g_norm_w [d] fp32; g_norm_b [d] fp32, may be NULL                      out
  *   workspace of hc_layer_norm_backward_workspace_bytes(n, d) bytes,
  *   16-byte aligned: scratch of this call, free for others once it has completed.

@@ -11,9 +11,11 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
+import oracle
 import hyper_connection_residual_mixes_gb300 as hcg
 from hyper_connection_residual_mixes_gb300 import _lib, inputs
 from hyper_connection_residual_mixes_gb300 import build as hc_build
@@ -213,3 +215,97 @@ def test_first_calls_from_several_host_threads():
     out = subprocess.run([sys.executable, "-c", _FIRST_CALLS], capture_output=True, text=True, timeout=300,
                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert out.returncode == 0 and out.stdout.split() == ["same"], out.stdout + out.stderr
+
+
+def test_gradient_of_the_streams_through_the_sublayer():
+    """The sublayer reads h = sum_s pre_mix[s] x[s]; the side's backward takes no gradient
+    of it, so what the layer norm's backward gives is added to the streams' and
+    pre_mix's: g_x[s] += pre_mix[s] g_h, g_pre_mix[s] += <g_h, x[s]>.
+
+    Bounds: the side's own (1e-4 of a value and of the largest), carried on through
+    |W|, and half a step of each rounding to bf16 (2^-8); the norm's backward is
+    linear in its gradient, its own error 1024 u and its fp32 statistics' 8 times that."""
+    n, d = 37, 1024
+    case = inputs.tiny(seed=3, n=n, d=d)
+    x, pm, params = case.x.to(DEV), case.pre_mix.to(DEV), case.params[0].to(DEV).astuple()
+    g = torch.Generator(device=DEV).manual_seed(7)
+    r = lambda *s: torch.randn(s, generator=g, device=DEV)
+    ln_w, ln_b, w, c = 0.5 + torch.rand((d,), generator=g, device=DEV), 0.1 * r(d), (r(3, d, d) / d ** 0.5).bfloat16(), r(n, 4, d)
+    ends = [0, 10, 10, n]
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    h = torch.empty((n, d), dtype=torch.bfloat16, device=DEV)
+    hcg.hc_chain_begin(x, pm, *params[:3], h_pre_out=h)
+    hn, mean, rstd = hcg.hc_layer_norm(h, ln_w, ln_b, return_stats=True)
+    f = hcg.hc_grouped_mm(hn, w, off)
+    side = hcg.hc_block_step_backward(x, pm, f, *params, torch.zeros((n, d), device=DEV), c)
+    g_hn = hcg.hc_grouped_mm(side["g_f"].bfloat16(), w, off, transposed=True)
+    g_h = hcg.hc_layer_norm_backward(g_hn.float(), h, ln_w, mean, rstd)["g_x"]
+    g_x = side["g_x"] + pm[..., None] * g_h[..., None, :]
+    g_pre_mix = side["g_pre_mix"] + (x.float() * g_h[..., None, :]).sum(-1)
+
+    D = lambda t: t.double().cpu().numpy()
+    X, P, W, LW, LB, C, Q = D(x), D(pm), D(w), D(ln_w), D(ln_b), D(c), [D(t) for t in params]
+    experts = [(e, slice(ends[e], ends[e + 1])) for e in range(3)]
+    mean_of = lambda t: t.mean(1, keepdims=True)
+
+    def norm_backward(H, g_n, room):
+        """g_h and its bound from the gradient of the norm's output and its bound."""
+        rs = 1 / np.sqrt(mean_of((H - mean_of(H)) ** 2) + 1e-5)
+        xh, wg, wr = (H - mean_of(H)) * rs, g_n * LW, room * np.abs(LW)
+        linear = lambda t: rs * (t + mean_of(t) + np.abs(xh) * mean_of(t * np.abs(xh)))
+        return rs * (wg - mean_of(wg) - xh * mean_of(wg * xh)), linear(wr) + 8 * 1024 * U * linear(np.abs(wg) + wr)
+
+    ref = oracle.side_backward(X, P, D(f), *Q, np.zeros((n, d)), C, rounded=True)
+    side_room = lambda t: 1e-4 * np.abs(t) + 1e-4 * np.abs(t).max()
+    room_f = side_room(ref["g_f"])
+    room_f = room_f + 2.0 ** -8 * (np.abs(ref["g_f"]) + room_f)
+    g_n, room_n = np.zeros((n, d)), np.zeros((n, d))
+    for e, rows in experts:
+        g_n[rows] = ref["g_f"][rows] @ W[e]
+        room_n[rows] = room_f[rows] @ np.abs(W[e]) + (d / 16 + 2) * 2.0 ** -22 * ((np.abs(ref["g_f"]) + room_f)[rows] @ np.abs(W[e]))
+    room_n = room_n + 2.0 ** -8 * (np.abs(g_n) + room_n)
+    want_h, room_h = norm_backward(D(h), g_n, room_n)
+    assert (np.abs(D(g_h) - want_h) <= room_h).all()
+    want_x, room_x = ref["g_x"] + P[..., None] * want_h[:, None], side_room(ref["g_x"]) + np.abs(P)[..., None] * room_h[:, None]
+    room_x = room_x + 4 * U * (np.abs(ref["g_x"]) + np.abs(P[..., None] * want_h[:, None]))
+    assert (np.abs(D(g_x) - want_x) <= room_x).all()
+    assert (np.abs(D(side["g_x"]) - want_x) > room_x).mean() > 0.5          # (the sublayer's part is no detail)
+    want_p = ref["g_pre_mix"] + (X * want_h[:, None]).sum(-1)
+    room_p = side_room(ref["g_pre_mix"]) + (np.abs(X) * room_h[:, None]).sum(-1) + d * U * (np.abs(X) * np.abs(want_h)[:, None]).sum(-1)
+    assert (np.abs(D(g_pre_mix) - want_p) <= room_p).all()
+
+    # the same chain without roundings against differences of the 64-bit loss, two steps joined
+    def forward(X, P):
+        H = (P[..., None] * X).sum(1)
+        N = (H - mean_of(H)) / np.sqrt(mean_of((H - mean_of(H)) ** 2) + 1e-5) * LW + LB
+        return H, np.concatenate([N[rows] @ W[e].T for e, rows in experts])
+
+    loss = lambda X, P: (C * oracle.side_f64(X, P, forward(X, P)[1], *Q, rounded=False)["y"]).sum()
+    H, F = forward(X, P)
+    exact = oracle.side_backward(X, P, F, *Q, np.zeros((n, d)), C, rounded=False)
+    e_h, _ = norm_backward(H, np.concatenate([exact["g_f"][rows] @ W[e] for e, rows in experts]), np.zeros((n, d)))
+    e_x, e_p = exact["g_x"] + P[..., None] * e_h[:, None], exact["g_pre_mix"] + (X * e_h[:, None]).sum(-1)
+    rng = np.random.default_rng(5)
+    vx, vp = rng.standard_normal(X.shape), rng.standard_normal(P.shape)
+    slope = lambda s: (loss(X + s * vx, P + s * vp) - loss(X - s * vx, P - s * vp)) / (2 * s)
+    limit = (4 * slope(5e-5) - slope(1e-4)) / 3
+    size = np.abs(e_x * vx).sum() + np.abs(e_p * vp).sum()
+    assert abs((e_x * vx).sum() + (e_p * vp).sum() - limit) <= 1e-6 * size
+    assert abs((exact["g_x"] * vx).sum() + (exact["g_pre_mix"] * vp).sum() - limit) > 1e-4 * size
+
+
+def test_readme_example():
+    """The README's training step runs on a side's tensors and moves every parameter."""
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as t:
+        code = t.read().split("```python\n")[1].split("```")[0]
+    s = Side(False)
+    o = s.step()
+    names = dict(torch=torch, x=s.x, pre_mix=s.pre_mix, f=o["f_rows"][s.back], hc_fn=s.hc_fn, hc_scale=s.hc_scale, hc_base=s.hc_base,
+                 norm_w=s.norm_w, ln_w=s.ln_w, ln_b=s.ln_b, up=s.up16, h=o["h"], order=s.order, back=s.back, offsets=s.offsets,
+                 g_a=o["g_a"], g_y=s.c, t=2)
+    before = [v.clone() for v in (s.up16, s.ln_w, s.ln_b, s.hc_fn, s.hc_scale, s.hc_base)]
+    exec(code, names)
+    assert torch.equal(names["h_n"], hcg.hc_layer_norm(o["h"], before[1], before[2]))
+    assert names["g_x"].shape == s.x.shape and names["g_pre_mix"].shape == s.pre_mix.shape
+    for old, new in zip(before, names["params"]):
+        assert new.isfinite().all() and not torch.equal(old, new)
