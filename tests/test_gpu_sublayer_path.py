@@ -309,3 +309,47 @@ def test_readme_example():
     assert names["g_x"].shape == s.x.shape and names["g_pre_mix"].shape == s.pre_mix.shape
     for old, new in zip(before, names["params"]):
         assert new.isfinite().all() and not torch.equal(old, new)
+
+
+_FIRST_CAPTURE = """
+import torch
+import hyper_connection_residual_mixes_gb300 as hcg
+g = torch.Generator(device="cuda").manual_seed(2)
+r = lambda *s: torch.randn(s, generator=g, device="cuda")
+xs, w = [r(700, 5120).bfloat16(), r(9, 320), r(3, 9000).half()], r(9000)
+rows, weights, off = r(300, 512).bfloat16(), r(4, 256, 512).bfloat16(), torch.tensor([0, 90, 100, 250, 300], dtype=torch.int32, device="cuda")
+one, long = r(3, 8192).bfloat16(), r(2, 64, 8192).bfloat16()
+few, many = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda"), torch.tensor([0, 9000], dtype=torch.int32, device="cuda")
+a, b = r(9000, 64).bfloat16(), r(9000, 72).bfloat16()
+params = [[torch.ones(5000, device="cuda"), torch.ones(70, 9, device="cuda")] for _ in range(2)]
+states = [[hcg.adamw_state(p, mxfp8=k == 1) for k, p in enumerate(ps)] for ps in params]
+plans = [hcg.adamw_plan(ps, [torch.full_like(p, 0.25) for p in ps], [s[0] for s in st], [s[1] for s in st]) for ps, st in zip(params, states)]
+
+def work(k):
+    out = []
+    for x in xs:
+        d = x.shape[1]
+        y, mean, rstd = hcg.hc_layer_norm(x, w[:d].contiguous(), return_stats=True)
+        out += [y, mean, rstd, *hcg.hc_layer_norm_backward(y, x, w[:d].contiguous(), mean, rstd).values()]
+    out.append(hcg.hc_grouped_mm(rows, weights, off))
+    out += hcg.hc_grouped_mm_backward(out[-1], rows, weights, off).values()
+    out += [hcg.hc_grouped_mm(one, long, few), hcg.hc_grouped_mm_weights(a, b, many)]
+    hcg.hc_adamw_step(plans[k], 1e-3, 1)
+    return out
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = work(0)
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(captured, work(1)))
+assert all(torch.equal(p, q) for p, q in zip(*params))
+print("same")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """In a process of its own: no kernel has run, or been loaded, before it is captured."""
+    out = subprocess.run([sys.executable, "-c", _FIRST_CAPTURE], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert out.returncode == 0 and out.stdout.split() == ["same"], out.stdout + out.stderr
