@@ -269,7 +269,8 @@ __device__ __forceinline__ void whole_or_end(const Desc &d, int64_t base, const 
 }
 
 // One kernel per kind of states: the 8-bit step needs half the registers, and
-// with four blocks on an SM instead of two its loads hide behind one another.
+// with four blocks on an SM instead of two its loads hide behind one another (at 64
+// registers it spills 224 bytes a thread).
 template <int CAP, bool kPacked>
 __global__ void __launch_bounds__(kThreads, kPacked ? 4 : 2)
 k_adamw(const __grid_constant__ Descs<CAP> t, int count, const __grid_constant__ Scalars c) {

@@ -14,7 +14,7 @@
 // expert's rows are cut into tiles of equal length; the offsets are read on
 // the device, so the host never waits for the router.
 //
-// One CTA per SM walks the tiles (warp 0 loads by TMA, warp 1 issues
+// CTAs walk the tiles, one or two an SM (Cfg::kPerSm; warp 0 loads by TMA, warp 1 issues
 // tcgen05.mma, warps 2-9 write finished tiles, warp 10 clears the rows behind an
 // expert's last one in the gradient's operands); two accumulators alternate, so
 // that a tile is written while the next one's products run.  Where few tiles have
@@ -25,9 +25,14 @@
 // block of 64 of k instead of 48, and what L2 delivers to an SM (some 60 bytes a
 // cycle) is what the products wait for otherwise.
 //
-// 49,152 rows of 64 experts, 2048 x 5120 bf16: 617 us, 1.67 PFLOP/s (0.86 of the
-// measured peak; 1.40 when repeated until the board's power limits it).  768 rows
-// of the same experts: 197 us, the weights at the measured copy rate.
+// 49,152 rows of 64 experts, 2048 x 5120 bf16: 610 us in a burst, 1.69 PFLOP/s (0.88 of
+// the measured burst rate); repeated until the board's power limits the clock, 735 us,
+// 1.40 PFLOP/s (0.80 of the measured sustained rate).  The split into experts costs
+// that last part, not the power alone: the same rows of one expert take 617 us (0.96),
+// a library product of that size 609.  An expert of some 770 rows makes three or four
+// row tiles, each of which reads all of its weights again, and the last round of
+// tiles is not full.  768 rows of the same experts: 201 us, the weights at 0.98 of the
+// measured copy rate.
 #include <atomic>
 
 #include <cuda.h>
@@ -502,7 +507,9 @@ k_grouped_mm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         }
         __syncwarp();
         // (operands are read again by other tiles, outputs by none: 620 -> 613 us, 470 -> 453 us
-        // for the prefill's product and the training batch's gradients)
+        // for the prefill's product and the training batch's gradients.  What it costs the next
+        // kernel: reading 64 MB, 96 MB takes it 14.0, 24.2 us after a decode batch's product,
+        // 13.2, 20.3 after a plain read of as many bytes)
         const uint64_t pol = policy_evict_last();
         int slot = 0, issued = 0;
         uint32_t parity = 1;
@@ -827,34 +834,44 @@ cudaError_t join_rows(const float *part, const Args &a, int slices, void *out, i
                : cudaLaunchKernelEx(&cfg, k_join_rows<T, false>, part, a.offsets, a.experts, a.n, a.F, slices, o, stride, zero_rest);
 }
 
+// SMs of the device that the rules below share work out for.  A constant: they decide
+// the room that a workspace needs and the order of sums, which must not depend on the
+// device that happens to be current when they are asked.  (A device with fewer SMs, or
+// fewer pairs of them that can work together, takes another round of tiles.)
+constexpr int kSms = 152;
 // Whether a product takes the wide tiles: from some 40 rows an expert on they are
 // the faster ones (us, narrow and wide, 16 experts of 2048 x 5120: 32 rows each 56
-// and 60, 48 rows 64 and 60, 128 rows 102 and 64).
+// and 60, 48 rows 64 and 60, 128 rows 102 and 64).  The host knows the mean alone: where
+// few experts have all the rows, narrow tiles read those experts' weights once per 32
+// of them (64 experts of 2048 x 5120: 768 rows evenly spread 206 us, all of one expert
+// 44, 22 if the call names that one alone; 2,048 rows 209, 87 and 29).
 bool wide_rows(int64_t n, int experts) { return n > 32 * (int64_t)experts; }
 // Narrow tiles of a product at the most: one for each 128 outputs of each expert
 // with rows (and of each 32 rows of one).
 int64_t narrow_tiles(int64_t n, int experts, int N) { return (int64_t)(N + kM - 1) / kM * (n < experts ? n : experts + n / 32); }
 // Slices of a product's contraction: where it is of 4,096 or more and the tiles leave
-// half the 152 SMs (their pairs) without work, as many as there is room for, 512 of it
+// half the kSms SMs (their pairs) without work, as many as there is room for, 512 of it
 // each at the least (us, with slices and without: one row of one expert, 5120 x 4096
 // 12.8 and 19.1, x 8192 19.6 and 34.3, x 2048 9.7 and 11.6, which the second launch
 // takes back where the host is the slower one; three rows 3776 x 5936 13.4 and 26.1;
 // 512 rows 1024 x 8192 16.7 and 40.2; slices of 1,024 at the least 0 to 10 % more).
 int product_slices(int64_t n, int experts, int N, int K) {
     const int64_t tiles = wide_rows(n, experts) ? (N + 255) / 256 * (experts + n / 256) : narrow_tiles(n, experts, N);
-    const int64_t room = (wide_rows(n, experts) ? 76 : 152) / (tiles > 0 ? tiles : 1), s = room < K / 512 ? room : K / 512;
+    const int64_t room = (wide_rows(n, experts) ? kSms / 2 : kSms) / (tiles > 0 ? tiles : 1), s = room < K / 512 ? room : K / 512;
     return K < 4096 || s < 2 ? 1 : (int)(s * experts <= kMaxExperts ? s : 1);
 }
 
 // Slices of an expert's rows in the weights' gradient: where the tiles are at most
-// half the pairs of CTAs of 152 SMs and experts have 2,048 rows or more, as many
+// half the pairs of CTAs of kSms SMs and experts have 2,048 rows or more, as many
 // slices as the pairs have room for, each of 512 rows at the least (us, with slices
 // and without: one expert, 2,048 rows 256 x 256 10.6 and 14.3, 12,733 rows 216 x 16
 // 14.3 and 68.8, 41,907 rows 456 x 3296 120 and 225; eight experts 512 x 512, 8,192
-// rows 12.6 and 10.7, 16,384 rows 14.9 and 15.2).
+// rows 12.6 and 10.7, 16,384 rows 14.9 and 15.2).  This too goes by the mean: of 16
+// experts' 512 x 512 one with 30,000 rows and 15 with one take 133 us, the same rows
+// evenly spread 17, that expert alone, in slices, 21; of 2048 x 1024 157, 83 and 82.
 int slices_of(int64_t n, int experts, int N, int K) {
     const int64_t tiles = (int64_t)experts * ((N + 255) / 256) * ((K + 255) / 256);
-    const int64_t room = 76 / tiles, rows = n / experts, s = room < rows / 512 ? room : rows / 512;
+    const int64_t room = kSms / 2 / tiles, rows = n / experts, s = room < rows / 512 ? room : rows / 512;
     return rows < 2048 || s < 2 ? 1 : (int)s;
 }
 
@@ -905,9 +922,9 @@ constexpr int kDevices = 64;
 int sm_count() {
     static std::atomic<int> sms[kDevices];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return kSms;
     if ((n = sms[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return kSms;
     sms[dev].store(n, std::memory_order_relaxed);
     return n;
 }

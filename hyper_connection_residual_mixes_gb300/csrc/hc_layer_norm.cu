@@ -9,8 +9,9 @@
 // All sums run in fp32; y (and g_x) are rounded once, on the way out.
 //
 // Both directions move each row across HBM once and are bound by that: 65,536 rows
-// of 5,120 bf16 take 207 us forward (0.95 of the measured copy rate), 8,192 rows
-// with fp32 gradients 70 us backward (0.89; 4 of them for the column sums).  Rows that
+// of 5,120 bf16 take 208 us forward (0.95 of the measured copy rate), 8,192 rows
+// with fp32 gradients 70 us backward (0.89; 4 of them for the column sums), replayed as
+// a graph.  Rows that
 // start anywhere take the same way, with accesses of one or two values: 65,536 rows of
 // 5,119 bf16 395 us, bound by the loads' and stores' issue.
 #include <atomic>
@@ -24,7 +25,7 @@
 namespace hc {
 
 namespace ln {
-constexpr int kSlots = 6;  // most ring slots (the backward at 5120 columns: 4 80, 6 69.5, 8 70.4 us)
+constexpr int kSlots = 6;  // most ring slots (the backward at 5120 columns, bf16 with fp32 gradients: 4 80, 6 69.5, 7, all that fit, 70.4 us)
 
 // a parameter value (norm_w, norm_b): fp32 or 16 bits, by its type code
 __device__ __forceinline__ float param(const void *p, int type, int i) {

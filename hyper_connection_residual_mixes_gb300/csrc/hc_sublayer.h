@@ -1,6 +1,6 @@
 // hc_sublayer.h -- internal launcher prototypes of the sublayer operators
 // (layer norm, experts' matrix products, AdamW).  Arguments have been
-// validated by hc_api_sublayer.cu before any of these is called.
+// validated by hc_api.cu before any of these is called.
 #pragma once
 
 #include <cstddef>
@@ -42,7 +42,7 @@ cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, co
                                       const int32_t *offsets, int64_t n, int experts, bool fp16, void *g_w,
                                       bool g_f32, void *workspace, cudaStream_t s);
 size_t grouped_mm_weights_workspace_bytes(int64_t n, int experts, int N, int K);
-// as the other files' (hc_launch.h); bit 2: offsets out of order or out of range
+// as the other files' (hc_launch.h); bit 1 (value 2): offsets out of order or out of range
 cudaError_t consume_grouped_mm_device_error(cudaStream_t s, unsigned int *flag);
 
 }  // namespace hc
