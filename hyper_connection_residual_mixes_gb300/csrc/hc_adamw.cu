@@ -27,8 +27,8 @@
 // and gradients with 8-bit states.  All tensors of a call with one kind of states
 // go in one launch (their descriptions are kernel parameters, 448 at the most).
 // 320 fp32 tensors of 39.7M values: 163 us, 0.99 of the measured copy rate; 252M
-// bf16 values with 8-bit states: 416 us, 0.90 (some 40 instructions a value, which
-// keep the issue slots 64 % busy).
+// bf16 values with 8-bit states: 416 us, 0.90 (some 43 instructions a value, which
+// keep the issue slots 66 % busy).
 #include <cuda_fp8.h>
 
 #include "hc_sublayer.h"
