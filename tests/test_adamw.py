@@ -167,3 +167,21 @@ def test_changed_copies_and_codes_are_refused(host_plans, k):
             plan._describe()
     t.data = old
     plan._describe()
+
+
+def test_snapshots(monkeypatch):
+    """Equal for the same tensors, different after any change; refused for what is no list of tensors."""
+    f = _lib.snapshot()
+    ts = [torch.zeros(6, 4), torch.tensor(1.0), torch.zeros(0, 3), torch.nn.Parameter(torch.zeros(5))]
+    base = f(ts)
+    assert f(ts) == base and f([t.detach() for t in ts]) == base and f([]) == b"" and f(ts[:3]) != base
+    for change in (lambda t: t[:5], lambda t: t.view(4, 6), lambda t: t.t(), lambda t: t.view(torch.int32), lambda t: t[:, :3], lambda t: t.clone(),
+                   lambda t: t.as_strided((6, 4), (2, 1)), lambda t: t.unsqueeze(0)):
+        assert f([change(ts[0])] + ts[1:]) != base
+    for bad in (None, 3, tuple(ts), [ts[0], 3], [ts]):
+        with pytest.raises(TypeError, match="list of tensors"):
+            f(bad)
+    from hyper_connection_residual_mixes_gb300 import _tensors
+    monkeypatch.setattr(_tensors, "torch_version", "0.0")
+    with pytest.raises(RuntimeError, match="built for torch 0.0"):
+        _lib.snapshot()
