@@ -16,15 +16,16 @@ from __future__ import annotations
 
 import torch
 
-from . import _lib, sublayer
+from . import _lib, sublayer, sublayer_fp8
 from ._lib import HcError
 from .sublayer import *  # noqa: F401,F403
+from .sublayer_fp8 import *  # noqa: F401,F403
 
 __all__ = ["hc_mixes", "hc_split_sinkhorn", "hc_pre_norm", "hc_post", "hc_block_step",
            "hc_chain_begin", "hc_chain_side", "hc_chain_norm", "chain_state", "hc_mxfp8_cast",
            "hc_pre_norm_mxfp8",
            "hc_block_step_backward", "hc_block_step_backward_no_workspace", "STATE_FLOATS",
-           "HcError", "library_path", "version"] + sublayer.__all__
+           "HcError", "library_path", "version"] + sublayer.__all__ + sublayer_fp8.__all__
 
 HC_EPS = 1e-6
 NORM_EPS = 1e-20

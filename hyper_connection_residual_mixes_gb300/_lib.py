@@ -55,6 +55,11 @@ SIGNATURES = {
     "hc_grouped_mm": [P, I64, P, I32, P, I64, I32, I32, I32, I32, P, I64, I32, I32, P, ctypes.c_size_t, P],
     "hc_grouped_mm_weights_workspace_bytes": [I64, I32, I32, I32],
     "hc_grouped_mm_weights": [P, I64, P, I64, P, I64, I32, I32, I32, I32, P, I32, I32, P, ctypes.c_size_t, P],
+    "hc_fp8_cast": [P, I64, I32, I64, I32, P, I64, P, P],
+    "hc_fp8_cast_weights": [P, I32, I64, I32, I32, P, P, P],
+    "hc_rms_norm": [P, I64, P, I64, I32, P, I32, I64, I32, F32, P, I64, P, I64, P, I64, P, P, P],
+    "hc_rms_norm_backward_workspace_bytes": [I64, I32],
+    "hc_rms_norm_backward": [P, I64, P, I64, I32, P, I64, I32, P, I32, P, I64, I32, P, I64, P, P, ctypes.c_size_t, P],
     "hc_adamw_step": [P, I64, F64, F64, F64, F64, F64, I64, P, P, P, P],
 }
 
@@ -105,6 +110,7 @@ def load():
         lib.hc_block_step_backward_workspace_bytes.restype = ctypes.c_size_t
         lib.hc_chain_state_bytes.restype = ctypes.c_size_t
         lib.hc_layer_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+        lib.hc_rms_norm_backward_workspace_bytes.restype = ctypes.c_size_t
         lib.hc_grouped_mm_workspace_bytes.restype = ctypes.c_size_t
         lib.hc_grouped_mm_weights_workspace_bytes.restype = ctypes.c_size_t
         _lib = lib

@@ -147,6 +147,9 @@ hc_status check_grouped(int64_t n, int experts, int N, int K, hc_dtype type, hc_
     return HC_OK;
 }
 
+// blocks of 128 that share a scale
+int64_t fp8_blocks(int64_t d) { return (d + 127) / 128; }
+
 hc_status check_norm(int64_t n, int d, hc_dtype x_type, hc_dtype w_type) {
     if (n < 0 || d <= 0 || !known(x_type) || !known(w_type)) return HC_ERR_INVALID_ARG;
     if (d > kMaxD || n > INT32_MAX || (w_type != HC_F32 && w_type != x_type)) return HC_ERR_UNSUPPORTED;
@@ -690,6 +693,103 @@ hc_status hc_grouped_mm_weights(const void *g_y, int64_t g_stride, const void *x
                                                              workspace, stream)
                            : hc::launch_grouped_mm_weights(g_y, g_stride, N, x, x_stride, K, offsets, n, experts, f16, g_w, f32,
                                                              workspace, stream));
+}
+
+hc_status hc_fp8_cast(const void *x, int64_t x_stride, hc_dtype type, int64_t n, int d, uint8_t *codes,
+                      int64_t codes_stride, uint8_t *scales, cudaStream_t stream) {
+    if (n < 0 || d <= 0 || !known(type)) return HC_ERR_INVALID_ARG;
+    if (n > INT32_MAX || n * fp8_blocks(d) > INT32_MAX) return HC_ERR_UNSUPPORTED;
+    if (!rows_fit(n, d, x_stride) || !rows_fit(n, d, codes_stride) || (n > 1 && codes_stride < d)) return HC_ERR_INVALID_ARG;
+    if (n == 0) return HC_OK;
+    if (!x || !codes || !scales) return HC_ERR_INVALID_ARG;
+    if (!aligned_to(x, size_of(type))) return HC_ERR_MISALIGNED;
+    const Span ins[] = {rows_span(x, n, d, x_stride, type)};
+    const Span outs[] = {span(codes, (n - 1) * codes_stride + d), span(scales, n * fp8_blocks(d))};
+    const hc_status st = check_alias(outs, 2, ins, 1);
+    if (st != HC_OK) return st;
+    return cuda_status(hc::launch_fp8_cast(x, x_stride, type, n, d, codes, codes_stride, scales, stream));
+}
+
+hc_status hc_fp8_cast_weights(const void *w, hc_dtype type, int64_t count, int N, int K, uint8_t *codes,
+                              uint8_t *scales, cudaStream_t stream) {
+    if (count < 0 || N <= 0 || K <= 0 || !known(type)) return HC_ERR_INVALID_ARG;
+    const int64_t blocks = fp8_blocks(N) * fp8_blocks(K);
+    if (count > INT32_MAX / blocks) return HC_ERR_UNSUPPORTED;
+    if (count == 0) return HC_OK;
+    if (!w || !codes || !scales) return HC_ERR_INVALID_ARG;
+    if (!aligned_to(w, size_of(type))) return HC_ERR_MISALIGNED;
+    const int64_t values = count * N * K;
+    const Span ins[] = {span(w, values * size_of(type))};
+    const Span outs[] = {span(codes, values), span(scales, count * blocks)};
+    const hc_status st = check_alias(outs, 2, ins, 1);
+    if (st != HC_OK) return st;
+    return cuda_status(hc::launch_fp8_cast_weights(w, type, count, N, K, codes, scales, stream));
+}
+
+hc_status hc_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                      hc_dtype type, const void *norm_w, hc_dtype w_type, int64_t n, int d, float eps,
+                      void *r, int64_t r_stride, void *y, int64_t y_stride, uint8_t *codes,
+                      int64_t codes_stride, uint8_t *scales, float *rstd, cudaStream_t stream) {
+    hc_status st = check_norm(n, d, type, w_type);
+    if (st != HC_OK) return st;
+    if (!finite_nonneg(eps) || !rows_fit(n, d, x_stride) || (residual && !rows_fit(n, d, residual_stride)) ||
+        (r && (!rows_fit(n, d, r_stride) || (n > 1 && r_stride < d))) ||
+        (y && (!rows_fit(n, d, y_stride) || (n > 1 && y_stride < d))) ||
+        (codes && (!rows_fit(n, d, codes_stride) || (n > 1 && codes_stride < d))))
+        return HC_ERR_INVALID_ARG;
+    if (n == 0) return HC_OK;
+    if (!x || !norm_w || !residual != !r || !codes != !scales || (!y && !codes)) return HC_ERR_INVALID_ARG;
+    const int64_t b = size_of(type), wb = size_of(w_type);
+    if (!aligned_to(x, b) || !aligned_to(residual, b) || !aligned_to(norm_w, wb) || !aligned_to(r, b) ||
+        !aligned_to(y, b) || !aligned_to(rstd, 4))
+        return HC_ERR_MISALIGNED;
+    // (each row of r is written by those who have read the same values of x and residual)
+    const bool on_x = r == x && r_stride == x_stride, on_residual = r == residual && r_stride == residual_stride;
+    const Span sx = rows_span(x, n, d, x_stride, type), sres = rows_span(residual, residual ? n : 0, d, residual_stride, type);
+    const Span sr = rows_span(r, r ? n : 0, d, r_stride, type), sw = span(norm_w, d * wb);
+    const Span ins[] = {sx, sres, sw, sr};
+    const Span outs[] = {rows_span(y, y ? n : 0, d, y_stride, type), span(codes, codes ? (n - 1) * codes_stride + d : 0),
+                         span(scales, scales ? n * fp8_blocks(d) : 0), span(rstd, rstd ? n * 4 : 0)};
+    if ((st = check_alias(outs, 4, ins, 4)) != HC_OK) return st;
+    if (r && (overlaps(sr, sw) || (!on_x && overlaps(sr, sx)) || (!on_residual && overlaps(sr, sres)))) return HC_ERR_ALIAS;
+    return cuda_status(hc::launch_rms_norm(x, x_stride, residual, residual_stride, type, norm_w, w_type, n, d, eps, r,
+                                           r_stride, y, y_stride, codes, codes_stride, scales, rstd, stream));
+}
+
+size_t hc_rms_norm_backward_workspace_bytes(int64_t n, int d) {
+    if (check_norm(n, d, HC_F32, HC_F32) != HC_OK || n == 0) return 0;
+    return hc::rms_norm_backward_workspace_bytes(n, d);
+}
+
+hc_status hc_rms_norm_backward(const void *g_y, int64_t g_stride, const void *g_r, int64_t g_r_stride,
+                               hc_dtype g_type, const void *r, int64_t r_stride, hc_dtype type,
+                               const void *norm_w, hc_dtype w_type, const float *rstd, int64_t n, int d,
+                               void *g_x, int64_t gx_stride, float *g_norm_w, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+    hc_status st = check_norm(n, d, type, w_type);
+    if (st != HC_OK) return st;
+    if (!known(g_type)) return HC_ERR_INVALID_ARG;
+    if (g_type != HC_F32 && g_type != type) return HC_ERR_UNSUPPORTED;
+    if (!rows_fit(n, d, g_stride) || (g_r && !rows_fit(n, d, g_r_stride)) || !rows_fit(n, d, r_stride) ||
+        !rows_fit(n, d, gx_stride) || (n > 1 && gx_stride < d) || !g_norm_w)
+        return HC_ERR_INVALID_ARG;
+    const size_t need = hc_rms_norm_backward_workspace_bytes(n, d);
+    if (n > 0 && (!g_y || !r || !norm_w || !rstd || !g_x || !workspace || workspace_bytes < need)) return HC_ERR_INVALID_ARG;
+    const int64_t b = size_of(type), gb = size_of(g_type), wb = size_of(w_type);
+    if (!aligned_to(g_y, gb) || !aligned_to(g_r, gb) || !aligned_to(r, b) || !aligned_to(norm_w, wb) || !aligned_to(rstd, 4) ||
+        !aligned_to(g_x, gb) || !aligned_to(g_norm_w, 4) || (n > 0 && !aligned16(workspace)))
+        return HC_ERR_MISALIGNED;
+    // (each row of g_x is written by those who have read the same values of g_r)
+    const bool on_g_r = g_x == g_r && gx_stride == g_r_stride;
+    const Span past = rows_span(g_r, g_r ? n : 0, d, g_r_stride, g_type), sg = rows_span(g_x, n, d, gx_stride, g_type);
+    const Span ins[] = {rows_span(g_y, n, d, g_stride, g_type), rows_span(r, n, d, r_stride, type),
+                        span(norm_w, n > 0 ? d * wb : 0), span(rstd, n * 4)};
+    const Span outs[] = {sg, span(g_norm_w, (int64_t)d * 4), span(workspace, (int64_t)need)};
+    if ((st = check_alias(outs, 3, ins, 4)) != HC_OK) return st;
+    for (int i = on_g_r ? 1 : 0; i < 3; ++i)
+        if (overlaps(outs[i], past)) return HC_ERR_ALIAS;
+    return cuda_status(hc::launch_rms_norm_backward(g_y, g_stride, g_r, g_r_stride, g_type, r, r_stride, type, norm_w, w_type,
+                                                    rstd, n, d, g_x, gx_stride, g_norm_w, workspace, stream));
 }
 
 }  // extern "C"

@@ -38,11 +38,10 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 
-#include "hc_ptx.cuh"
 #include "hc_sublayer.h"
 #include "hc_types.cuh"
+#include "hc_umma.cuh"
 
 namespace hc {
 
@@ -157,128 +156,6 @@ __device__ __forceinline__ void umma4(uint32_t d, uint64_t a0, uint64_t b0, uint
             "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d), "l"(a0), "l"(b0), "r"(id), "r"(accumulate), "n"(kStepA), "n"(kStepB)
             : "memory");
 }
-// One arrival on `bar` (of a pair: of both CTAs) once the MMAs issued so far are done.
-template <bool kPair>
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-    if constexpr (kPair)
-        asm volatile(
-            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-            "h"((uint16_t)3)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-            : "memory");
-}
-// An arrival at the other CTA's barrier that orders nothing: the loads themselves
-// complete on the barrier.  (The releasing form waits for everything this thread
-// has in flight, 2,000 cycles a stage, four times a stage's products.)
-__device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "@q mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
-        : "memory");
-}
-// Tensor loads; of a pair the barrier may be the other CTA's.
-template <bool kPair>
-__device__ __forceinline__ void load_2d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, uint64_t policy) {
-    if constexpr (kPair)
-        asm volatile(
-            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
-            " [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-            " [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
-            : "memory");
-}
-template <bool kPair>
-__device__ __forceinline__ void load_4d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, int c2, int c3,
-                                        uint64_t policy) {
-    if constexpr (kPair)
-        asm volatile(
-            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-            "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
-            " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n\t}" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-            "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-            " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n\t}" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
-            : "memory");
-}
-template <bool kPair>
-__device__ __forceinline__ void load_3d(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1, int c2,
-                                        uint64_t policy) {
-    if constexpr (kPair)
-        asm volatile(
-            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-            "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
-            " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-            "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-            " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
-            : "memory");
-}
-template <bool kPair>
-__device__ __forceinline__ void tmem_get(uint32_t smem_dst, uint32_t ncols) {
-    if constexpr (kPair) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(ncols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else {
-        tmem_alloc(smem_dst, ncols);
-        tmem_relinquish();
-    }
-}
-template <bool kPair>
-__device__ __forceinline__ void tmem_give_back(uint32_t taddr, uint32_t ncols) {
-    if constexpr (kPair)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-    else
-        tmem_dealloc(taddr, ncols);
-}
-// 32 columns of this lane, waited for in the same statement (no register copy
-// can slip between the load and the wait).
-__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(t)
-        : "memory");
-}
-// On the way out: copies and MMAs already issued must land before the CTA
-// leaves, whatever the abort flag says.
-__device__ __forceinline__ void wait_exit(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < (1u << 22); ++i) {
-        if (mbar_try_wait(bar, parity)) return;
-        __nanosleep(128);
-    }
-    atomicOr(&g_device_error, kErrWaitTimeout);
-}
-
 __device__ __forceinline__ void put(void *out, int64_t i, float v, int f32, int fp16) {
     if (f32) static_cast<float *>(out)[i] = v;
     else if (fp16) static_cast<__half *>(out)[i] = __float2half_rn(v);
@@ -873,18 +750,6 @@ int slices_of(int64_t n, int experts, int N, int K) {
     const int64_t tiles = (int64_t)experts * ((N + 255) / 256) * ((K + 255) / 256);
     const int64_t room = kSms / 2 / tiles, rows = n / experts, s = room < rows / 512 ? room : rows / 512;
     return rows < 2048 || s < 2 ? 1 : (int)s;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult qr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
-            qr != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
 }
 
 bool encode(CUtensorMap *m, const void *base, bool fp16, int rank, const cuuint64_t *dims, const cuuint64_t *strides,

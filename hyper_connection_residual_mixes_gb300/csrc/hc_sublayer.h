@@ -1,5 +1,5 @@
 // hc_sublayer.h -- internal launcher prototypes of the sublayer operators
-// (layer norm, experts' matrix products, AdamW).  Arguments have been
+// (norms, experts' matrix products, AdamW, sublayers in 8 bits).  Arguments have been
 // validated by hc_api.cu before any of these is called.
 #pragma once
 
@@ -44,5 +44,20 @@ cudaError_t launch_grouped_mm_weights(const void *b, int64_t b_stride, int C, co
 size_t grouped_mm_weights_workspace_bytes(int64_t n, int experts, int N, int K);
 // as the other files' (hc_launch.h); bit 1 (value 2): offsets out of order or out of range
 cudaError_t consume_grouped_mm_device_error(cudaStream_t s, unsigned int *flag);
+
+// ------------------------------------------------------------ RMS norm, casts to 8 bits (hc_rms_norm.cu)
+cudaError_t launch_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, hc_dtype type,
+                            const void *w, hc_dtype w_type, int64_t n, int d, float eps, void *r, int64_t r_stride, void *y,
+                            int64_t y_stride, uint8_t *codes, int64_t codes_stride, uint8_t *scales, float *rstd,
+                            cudaStream_t s);
+size_t rms_norm_backward_workspace_bytes(int64_t n, int d);
+cudaError_t launch_rms_norm_backward(const void *g_y, int64_t g_stride, const void *g_r, int64_t g_r_stride, hc_dtype g_type,
+                                     const void *r, int64_t r_stride, hc_dtype type, const void *w, hc_dtype w_type,
+                                     const float *rstd, int64_t n, int d, void *g_x, int64_t gx_stride, float *g_w,
+                                     void *workspace, cudaStream_t s);
+cudaError_t launch_fp8_cast(const void *x, int64_t x_stride, hc_dtype type, int64_t n, int d, uint8_t *codes,
+                            int64_t codes_stride, uint8_t *scales, cudaStream_t s);
+cudaError_t launch_fp8_cast_weights(const void *w, hc_dtype type, int64_t count, int64_t N, int K, uint8_t *codes,
+                                    uint8_t *scales, cudaStream_t s);
 
 }  // namespace hc

@@ -1,0 +1,169 @@
+"""Sublayers in 8 bits: RMS norm with the residual and the cast, the casts.
+
+The same kind of binding as the sublayer operators'.  8-bit tensors are E4M3
+codes (uint8) with a scale for each block of 128 values of a row, or of 128 x 128
+of a weight matrix: UE8M0 bytes (uint8), as the casts write them, or fp32.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from .sublayer import (_DTYPE, _NAMES, _at, _current_device, _dense, _like, _norm_input, _norm_weights, _raw_stream, _rows,
+                       _scratch, _tensor)
+
+__all__ = ["hc_fp8_cast", "hc_fp8_cast_weights", "hc_rms_norm", "hc_rms_norm_backward"]
+
+RMS_NORM_EPS = 1e-6
+FP8_BLOCK = 128  # values that share a scale
+
+
+def _blocks(d):
+    return -(-d // FP8_BLOCK)
+
+
+def _input(x, name):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if x.dtype not in _DTYPE:
+        raise TypeError("%s must be %s, got %s" % (name, _NAMES, x.dtype))
+
+
+def _code_rows(codes, scales, shape, dev):
+    """Given codes (evenly spaced rows) and scales of a shape; returns the codes' row stride."""
+    _tensor(codes, "codes", (torch.uint8,), dev)
+    if codes.shape != shape:
+        raise ValueError("codes has shape %s, expected %s" % (tuple(codes.shape), tuple(shape)))
+    _dense(scales, "scales", (torch.uint8,), (*shape[:-1], _blocks(shape[-1])), dev)
+    return _rows(codes, "codes")[1]
+
+
+def _pair(codes, scales):
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales go together")
+
+
+def hc_fp8_cast(x, codes=None, scales=None, stream=None):
+    """Rows x [..., d] (fp32, bf16 or fp16; evenly spaced) -> (codes [..., d], scales
+    [..., ceil(d / 128)]) uint8: E4M3 numbers with a power-of-two scale for every 128
+    values of a row."""
+    _input(x, "x")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., d] with d >= 1")
+    n, xs = _rows(x, "x")
+    d = x.shape[-1]
+    _tensor(x, "x")
+    dev = x.device
+    _pair(codes, scales)
+    cs = d if codes is None else _code_rows(codes, scales, x.shape, dev)
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_fp8_cast(x, codes, scales)
+    if codes is None:
+        codes = torch.empty(x.shape, dtype=torch.uint8, device=dev)
+        scales = torch.empty((*x.shape[:-1], _blocks(d)), dtype=torch.uint8, device=dev)
+    _lib.call("hc_fp8_cast", x.data_ptr(), xs, _DTYPE[x.dtype], n, d, codes.data_ptr(), cs, scales.data_ptr(),
+              _raw_stream(dev.index))
+    return codes, scales
+
+
+def hc_fp8_cast_weights(w, codes=None, scales=None, stream=None):
+    """Weight matrices w [..., N, K] (fp32, bf16 or fp16, contiguous) -> (codes [..., N, K],
+    scales [..., ceil(N / 128), ceil(K / 128)]) uint8: E4M3 numbers with a power-of-two
+    scale for every block of 128 x 128."""
+    _input(w, "w")
+    if w.dim() < 2 or w.shape[-1] < 1 or w.shape[-2] < 1:
+        raise ValueError("w must be [..., N, K] with N, K >= 1")
+    _dense(w, "w", (w.dtype,), w.shape, w.device)
+    dev, lead = w.device, w.shape[:-2]
+    N, K = w.shape[-2:]
+    s_shape = (*lead, _blocks(N), _blocks(K))
+    _pair(codes, scales)
+    if codes is not None:
+        _dense(codes, "codes", (torch.uint8,), w.shape, dev)
+        _dense(scales, "scales", (torch.uint8,), s_shape, dev)
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_fp8_cast_weights(w, codes, scales)
+    if codes is None:
+        codes = torch.empty(w.shape, dtype=torch.uint8, device=dev)
+        scales = torch.empty(s_shape, dtype=torch.uint8, device=dev)
+    _lib.call("hc_fp8_cast_weights", w.data_ptr(), _DTYPE[w.dtype], lead.numel(), N, K, codes.data_ptr(), scales.data_ptr(),
+              _raw_stream(dev.index))
+    return codes, scales
+
+
+def hc_rms_norm(x, norm_w, residual=None, norm_eps=RMS_NORM_EPS, out="y", r=None, y=None, codes=None, scales=None,
+                return_rstd=False, stream=None):
+    """RMS norm of x [..., d] (fp32, bf16 or fp16; evenly spaced rows), to which residual
+    (of x's shape and type) is added first, with norm_w [d] (fp32 or x's type) -> a dict of
+    y [..., d] of x's type (out "y" or "both"), codes and scales as hc_fp8_cast's of the
+    unrounded y (out "fp8" or "both"), with a residual r = x + residual of x's type (the
+    residual of the next norm and what the backward reads), with return_rstd rstd [...]
+    fp32.  r, y, codes and scales may be given; r may be x or residual itself."""
+    n, xs, d = _norm_input(x)
+    dev = x.device
+    _norm_weights(norm_w, None, x, d)
+    if out not in ("y", "fp8", "both"):
+        raise ValueError('out must be "y", "fp8" or "both", got %r' % (out,))
+    wide, narrow = out != "fp8", out != "y"
+    res_s = d if residual is None else _like(residual, "residual", x, (x.dtype,))
+    if r is not None and residual is None:
+        raise ValueError("r is the sum with a residual: none is given")
+    if (y is not None and not wide) or (codes is not None and not narrow):
+        raise ValueError("out=%r does not write what is given" % out)
+    _pair(codes, scales)
+    rs = d if r is None else _like(r, "r", x, (x.dtype,))
+    ys = d if y is None else _like(y, "y", x, (x.dtype,))
+    cs = d if codes is None else _code_rows(codes, scales, x.shape, dev)
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_rms_norm(x, norm_w, residual, norm_eps, out, r, y, codes, scales, return_rstd)
+    res = {}
+    if residual is not None:
+        res["r"] = r = torch.empty(x.shape, dtype=x.dtype, device=dev) if r is None else r
+    if wide:
+        res["y"] = y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else y
+    if narrow:
+        if codes is None:
+            codes = torch.empty(x.shape, dtype=torch.uint8, device=dev)
+            scales = torch.empty((*x.shape[:-1], _blocks(d)), dtype=torch.uint8, device=dev)
+        res["codes"], res["scales"] = codes, scales
+    if return_rstd:
+        res["rstd"] = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _lib.call("hc_rms_norm", x.data_ptr(), xs, None if residual is None else residual.data_ptr(), res_s, _DTYPE[x.dtype],
+              norm_w.data_ptr(), _DTYPE[norm_w.dtype], n, d, norm_eps, None if r is None else r.data_ptr(), rs,
+              y.data_ptr() if wide else None, ys, codes.data_ptr() if narrow else None, cs,
+              scales.data_ptr() if narrow else None, res["rstd"].data_ptr() if return_rstd else None, _raw_stream(dev.index))
+    return res
+
+
+def hc_rms_norm_backward(g_y, r, norm_w, rstd, g_r=None, g_x=None, workspace=None, stream=None):
+    """The backward of hc_rms_norm: g_y [..., d] (fp32 or r's type), r (without a residual:
+    x), norm_w, the forward's rstd, and g_r (of g_y's shape and type), the gradient that
+    reaches r past the norm -> dict of g_x [..., d] of g_y's type, the gradient of x and of
+    the residual, and g_norm_w [d] fp32, the sum over all rows.  A cast's gradient is that
+    of the value it rounds.  g_x may be g_r itself.  workspace: a uint8 device tensor of at
+    least the size the library asks for (allocated here when None)."""
+    n, rs, d = _norm_input(r)
+    dev = r.device
+    _norm_weights(norm_w, None, r, d)
+    gs = _like(g_y, "g_y", r, (torch.float32, r.dtype))
+    _dense(rstd, "rstd", (torch.float32,), r.shape[:-1], dev)
+    grs = d if g_r is None else _like(g_r, "g_r", r, (g_y.dtype,))
+    gxs = d if g_x is None else _like(g_x, "g_x", r, (g_y.dtype,))
+    if workspace is not None:
+        _scratch(workspace, dev)
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_rms_norm_backward(g_y, r, norm_w, rstd, g_r, g_x, workspace)
+    if g_x is None:
+        g_x = torch.empty(r.shape, dtype=g_y.dtype, device=dev)
+    if workspace is None:
+        need = _lib.load().hc_rms_norm_backward_workspace_bytes(n, d)
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+    g_w = torch.empty((d,), dtype=torch.float32, device=dev)
+    _lib.call("hc_rms_norm_backward", g_y.data_ptr(), gs, None if g_r is None else g_r.data_ptr(), grs, _DTYPE[g_y.dtype],
+              r.data_ptr(), rs, _DTYPE[r.dtype], norm_w.data_ptr(), _DTYPE[norm_w.dtype], rstd.data_ptr(), n, d,
+              g_x.data_ptr(), gxs, g_w.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev.index))
+    return {"g_x": g_x, "g_norm_w": g_w}

@@ -355,7 +355,8 @@ hc_status hc_chain_norm(const uint16_t *h_pre, const float *state, const float *
 typedef enum {
     HC_F32 = 0,
     HC_BF16 = 1,
-    HC_F16 = 2
+    HC_F16 = 2,
+    HC_UE8M0 = 3 /* bytes that stand for 2^(byte - 127), 255 for NaN: a type of scales only */
 } hc_dtype;
 
 /*
@@ -494,6 +495,77 @@ hc_status hc_grouped_mm_weights(const void *g_y, int64_t g_stride, const void *x
                                 const int32_t *offsets, int64_t n, int experts, int N, int K,
                                 hc_dtype type, void *g_w, int transposed, hc_dtype g_type,
                                 void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Sublayers in 8 bits: E4M3 codes (as hc_mxfp8_cast's; 0x7F and 0xFF stand for
+ * NaN) with a scale for each block of 128: 128 values of a row (the last block of
+ * a row may be shorter), of a weight matrix 128 x 128 of them (the last row and
+ * column of blocks may be cut off).  The value of a code is its E4M3 value times its
+ * scale.  The casts write scales as UE8M0 bytes; what reads scales also takes fp32.
+ *
+ * The cast of a block: scale = the smallest power of two at or above amax / 448,
+ * from 2^-126 on, amax its largest magnitude; every value v becomes the E4M3 number
+ * nearest to v / scale, ties to even (the division is exact).  A NaN stays one and does
+ * not count for amax; an infinite value makes its block's scale 2^120 and its
+ * own value too large for fp32 again.
+ *
+ * hc_fp8_cast: n rows of d values, of type fp32, bf16 or fp16, x_stride >= 0 apart.
+ *   codes [n, d], rows codes_stride >= d apart; scales [n, ceil(d / 128)]     out
+ * hc_fp8_cast_weights: `count` matrices [N, K], one after the other.
+ *   codes [count, N, K]; scales [count, ceil(N / 128), ceil(K / 128)]         out
+ * n, d, N, K and the number of blocks < 2^31 (HC_ERR_UNSUPPORTED otherwise).
+ */
+hc_status hc_fp8_cast(const void *x, int64_t x_stride, hc_dtype type, int64_t n, int d, uint8_t *codes,
+                      int64_t codes_stride, uint8_t *scales, cudaStream_t stream);
+
+hc_status hc_fp8_cast_weights(const void *w, hc_dtype type, int64_t count, int N, int K, uint8_t *codes,
+                              uint8_t *scales, cudaStream_t stream);
+
+/*
+ * Root-mean-square norm of n rows of d values (1 <= d <= 16384, n < 2^31), the
+ * residual added first, the result as it is and cast to 8 bits:
+ *   r = x + residual, rounded to their type (without a residual r = x),
+ *   rstd = 1 / sqrt(sum r^2 / d + eps),  y = r rstd norm_w,
+ *   codes, scales = hc_fp8_cast of y before it is rounded,
+ * the sum and the statistic in fp32.
+ *   x [n, d] of type, rows x_stride >= 0 apart                             in
+ *   residual the same, rows residual_stride >= 0 apart; may be NULL        in
+ *   norm_w [d] of w_type: fp32 or type                                     in
+ *   r [n, d] of type, rows r_stride >= d apart: the residual of the next norm;
+ *   given exactly when residual is.  It may be the very rows of x or of residual
+ *   (the same pointer and stride)                                          out
+ *   y [n, d] of type, rows y_stride >= d apart; may be NULL                out
+ *   codes, scales as hc_fp8_cast's; may both be NULL (not y as well)       out
+ *   rstd [n] fp32 (for the backward), may be NULL                          out
+ */
+hc_status hc_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                      hc_dtype type, const void *norm_w, hc_dtype w_type, int64_t n, int d, float eps,
+                      void *r, int64_t r_stride, void *y, int64_t y_stride, uint8_t *codes,
+                      int64_t codes_stride, uint8_t *scales, float *rstd, cudaStream_t stream);
+
+/*
+ * The backward of hc_rms_norm.  With xh = r rstd and wg = g_y norm_w:
+ *   g_x = g_r + rstd (wg - xh mean(wg xh))  (the gradient of x and of the residual),
+ *   g_norm_w = sum over rows of g_y xh,
+ * the roundings of r and of the cast passing gradients through unchanged; all sums in
+ * fp32 and in an order fixed by the sizes, the strides' alignment and the device (the same call gives
+ * the same bits).  With n = 0 the sums are written as zeros.
+ *   g_y [n, d] of g_type: fp32 or type; g_r the same, the gradient that reaches r
+ *   past the norm, may be NULL                                             in
+ *   r (without a residual: x) and norm_w as in the forward, rstd as it wrote it    in
+ *   g_x [n, d] of g_type, rows gx_stride >= d apart; it may be the very rows of g_r   out
+ *   g_norm_w [d] fp32                                                      out
+ *   workspace of hc_rms_norm_backward_workspace_bytes(n, d) bytes, 16-byte aligned:
+ *   scratch of this call, free for others once it has completed.
+ */
+size_t hc_rms_norm_backward_workspace_bytes(int64_t n, int d);
+
+hc_status hc_rms_norm_backward(const void *g_y, int64_t g_stride, const void *g_r, int64_t g_r_stride,
+                               hc_dtype g_type, const void *r, int64_t r_stride, hc_dtype type,
+                               const void *norm_w, hc_dtype w_type, const float *rstd, int64_t n, int d,
+                               void *g_x, int64_t gx_stride, float *g_norm_w, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
