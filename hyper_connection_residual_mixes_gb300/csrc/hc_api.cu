@@ -150,6 +150,18 @@ hc_status check_grouped(int64_t n, int experts, int N, int K, hc_dtype type, hc_
 // blocks of 128 that share a scale
 int64_t fp8_blocks(int64_t d) { return (d + 127) / 128; }
 
+bool scale_known(hc_dtype t) { return t == HC_F32 || t == HC_UE8M0; }
+int64_t scale_size(hc_dtype t) { return t == HC_F32 ? 4 : 1; }
+
+hc_status check_fp8_mm(int64_t M, int N, int K, hc_dtype xs, hc_dtype ws, hc_dtype y) {
+    if (M < 0 || N <= 0 || K <= 0 || !scale_known(xs) || !scale_known(ws) || !known(y)) return HC_ERR_INVALID_ARG;
+    if (N % 16 || K % 16 || M > INT32_MAX - 4096 || N > INT32_MAX - 4096 || K > INT32_MAX - 4096)  // (a tile's last row and column fit 32 bits)
+        return HC_ERR_UNSUPPORTED;
+    // sizes that no device memory holds (and whose tile counts would not fit 32 bits)
+    const int64_t most = (int64_t)1 << 40;
+    return M * N > most || M * K > most || (int64_t)N * K > most ? HC_ERR_UNSUPPORTED : HC_OK;
+}
+
 hc_status check_norm(int64_t n, int d, hc_dtype x_type, hc_dtype w_type) {
     if (n < 0 || d <= 0 || !known(x_type) || !known(w_type)) return HC_ERR_INVALID_ARG;
     if (d > kMaxD || n > INT32_MAX || (w_type != HC_F32 && w_type != x_type)) return HC_ERR_UNSUPPORTED;
@@ -178,7 +190,7 @@ int hc_last_cuda_error(void) { return g_last_cuda_error; }
 int hc_version(void) { return 200; }
 
 hc_status hc_consume_device_error(cudaStream_t stream) {
-    unsigned int flag = 0, flag_chain = 0, flag_bwd = 0, flag_proj = 0, flag_grouped = 0, flag_norm = 0;
+    unsigned int flag = 0, flag_chain = 0, flag_bwd = 0, flag_proj = 0, flag_grouped = 0, flag_norm = 0, flag_fp8 = 0;
     hc_status st = cuda_status(hc::consume_device_error(stream, &flag));
     if (st != HC_OK) return st;
     st = cuda_status(hc::consume_slices_device_error(stream, &flag_chain));
@@ -191,8 +203,10 @@ hc_status hc_consume_device_error(cudaStream_t stream) {
     if (st != HC_OK) return st;
     st = cuda_status(hc::consume_layer_norm_device_error(stream, &flag_norm));
     if (st != HC_OK) return st;
+    st = cuda_status(hc::consume_fp8_mm_device_error(stream, &flag_fp8));
+    if (st != HC_OK) return st;
     // (bit 0 of each: a wait ran out; bit 1 of the grouped products': bad offsets)
-    if (flag | flag_norm | flag_chain | flag_bwd | flag_proj | (flag_grouped & 1u)) return HC_ERR_TIMEOUT;
+    if (flag | flag_norm | flag_fp8 | flag_chain | flag_bwd | flag_proj | (flag_grouped & 1u)) return HC_ERR_TIMEOUT;
     return flag_grouped ? HC_ERR_INVALID_ARG : HC_OK;
 }
 
@@ -790,6 +804,35 @@ hc_status hc_rms_norm_backward(const void *g_y, int64_t g_stride, const void *g_
         if (overlaps(outs[i], past)) return HC_ERR_ALIAS;
     return cuda_status(hc::launch_rms_norm_backward(g_y, g_stride, g_r, g_r_stride, g_type, r, r_stride, type, norm_w, w_type,
                                                     rstd, n, d, g_x, gx_stride, g_norm_w, workspace, stream));
+}
+
+size_t hc_fp8_mm_workspace_bytes(int transposed, int64_t M, int N, int K) {
+    if (check_fp8_mm(M, N, K, HC_F32, HC_F32, HC_F32) != HC_OK || M == 0) return 0;
+    return hc::fp8_mm_workspace_bytes(transposed != 0, M, N, K);
+}
+
+hc_status hc_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scales, hc_dtype x_scale_type,
+                    const uint8_t *w, const void *w_scales, hc_dtype w_scale_type, int transposed,
+                    int64_t M, int N, int K, void *y, int64_t y_stride, hc_dtype y_type,
+                    void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    hc_status st = check_fp8_mm(M, N, K, x_scale_type, w_scale_type, y_type);
+    if (st != HC_OK) return st;
+    const int C = transposed ? K : N, L = transposed ? N : K;
+    if (x_stride < L || y_stride < C || !rows_fit(M, L, x_stride) || !rows_fit(M, C, y_stride)) return HC_ERR_INVALID_ARG;
+    if (M == 0) return HC_OK;
+    if (!x || !x_scales || !w || !w_scales || !y) return HC_ERR_INVALID_ARG;
+    if (x_stride % 16 || x_stride >= (int64_t)1 << 38) return HC_ERR_UNSUPPORTED;
+    const size_t need = hc::fp8_mm_workspace_bytes(transposed != 0, M, N, K);
+    if (need && (!workspace || workspace_bytes < need)) return HC_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w) || !aligned_to(y, size_of(y_type)) || (need && !aligned16(workspace)) ||
+        (x_scale_type == HC_F32 && !aligned_to(x_scales, 4)) || (w_scale_type == HC_F32 && !aligned_to(w_scales, 4)))
+        return HC_ERR_MISALIGNED;
+    const Span ins[] = {span(x, (M - 1) * x_stride + L), span(x_scales, M * fp8_blocks(L) * scale_size(x_scale_type)),
+                        span(w, (int64_t)N * K), span(w_scales, fp8_blocks(N) * fp8_blocks(K) * scale_size(w_scale_type))};
+    const Span outs[] = {rows_span(y, M, C, y_stride, y_type), span(need ? workspace : nullptr, (int64_t)need)};
+    if ((st = check_alias(outs, 2, ins, 4)) != HC_OK) return st;
+    return cuda_status(hc::launch_fp8_mm(x, x_stride, x_scales, x_scale_type == HC_F32, w, w_scales, w_scale_type == HC_F32,
+                                         transposed != 0, M, N, K, y, y_stride, y_type, workspace, stream));
 }
 
 }  // extern "C"

@@ -60,4 +60,12 @@ cudaError_t launch_fp8_cast(const void *x, int64_t x_stride, hc_dtype type, int6
 cudaError_t launch_fp8_cast_weights(const void *w, hc_dtype type, int64_t count, int64_t N, int K, uint8_t *codes,
                                     uint8_t *scales, cudaStream_t s);
 
+// ------------------------------------------------------------ products in 8 bits (hc_fp8_mm.cu)
+// y [M, N] = x [M, K] w [N, K]^T; transposed: y [M, K] = x [M, N] w [N, K].
+cudaError_t launch_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scales, bool x_f32, const uint8_t *w,
+                          const void *w_scales, bool w_f32, bool transposed, int64_t M, int N, int K, void *y, int64_t y_stride,
+                          hc_dtype y_type, void *workspace, cudaStream_t s);
+size_t fp8_mm_workspace_bytes(bool transposed, int64_t M, int N, int K);
+cudaError_t consume_fp8_mm_device_error(cudaStream_t s, unsigned int *flag);  // as the other files' (hc_launch.h)
+
 }  // namespace hc

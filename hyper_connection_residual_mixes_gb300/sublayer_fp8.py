@@ -1,4 +1,4 @@
-"""Sublayers in 8 bits: RMS norm with the residual and the cast, the casts.
+"""Sublayers in 8 bits: RMS norm with the residual and the cast, the casts, products.
 
 The same kind of binding as the sublayer operators'.  8-bit tensors are E4M3
 codes (uint8) with a scale for each block of 128 values of a row, or of 128 x 128
@@ -9,13 +9,15 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .sublayer import (_DTYPE, _NAMES, _at, _current_device, _dense, _like, _norm_input, _norm_weights, _raw_stream, _rows,
-                       _scratch, _tensor)
+from .sublayer import (_DTYPE, _NAMES, _at, _current_device, _dense, _like, _norm_input, _norm_weights, _out_rows, _raw_stream,
+                       _rows, _scratch, _tensor)
 
-__all__ = ["hc_fp8_cast", "hc_fp8_cast_weights", "hc_rms_norm", "hc_rms_norm_backward"]
+__all__ = ["hc_fp8_cast", "hc_fp8_cast_weights", "hc_rms_norm", "hc_rms_norm_backward", "hc_fp8_mm"]
 
 RMS_NORM_EPS = 1e-6
 FP8_BLOCK = 128  # values that share a scale
+
+_SCALE = {torch.float32: 0, torch.uint8: 3}  # hc_dtype of scales
 
 
 def _blocks(d):
@@ -167,3 +169,48 @@ def hc_rms_norm_backward(g_y, r, norm_w, rstd, g_r=None, g_x=None, workspace=Non
               r.data_ptr(), rs, _DTYPE[r.dtype], norm_w.data_ptr(), _DTYPE[norm_w.dtype], rstd.data_ptr(), n, d,
               g_x.data_ptr(), gxs, g_w.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev.index))
     return {"g_x": g_x, "g_norm_w": g_w}
+
+
+def hc_fp8_mm(x, x_scales, w, w_scales, transposed=False, y=None, out_dtype=None, workspace=None, stream=None):
+    """Products of 8-bit numbers: x [M, K] codes (evenly spaced rows) with x_scales
+    [M, ceil(K / 128)], w [N, K] codes with w_scales [ceil(N / 128), ceil(K / 128)]
+    (scales UE8M0 bytes or fp32) -> y [M, N] of out_dtype (fp32, bf16, the default, or
+    fp16), y = x w^T.  transposed: x [M, N] with x_scales [M, ceil(N / 128)] -> y [M, K] =
+    x w, the gradient of the rows from the output's, cast by hc_fp8_cast (the weights' is
+    hc_grouped_mm_weights of the 16-bit rows, as one expert's).  N and K are multiples of
+    16.  workspace: a uint8 device tensor of at least the size the library asks for
+    (allocated here when None)."""
+    _tensor(x, "x", (torch.uint8,))
+    dev = x.device
+    _tensor(w, "w", (torch.uint8,), dev)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [M, width] and w [N, K]")
+    _dense(w, "w", (torch.uint8,), w.shape, dev)
+    (N, K), M = w.shape, x.shape[0]
+    C, L = (K, N) if transposed else (N, K)
+    if x.shape[1] != L:
+        raise ValueError("x has shape %s, expected (M, %d)" % (tuple(x.shape), L))
+    n, xs = _rows(x, "x")
+    xs = xs if n > 1 else max(16, -(-L // 16) * 16)  # (a single row may carry any stride)
+    _dense(x_scales, "x_scales", tuple(_SCALE), (M, _blocks(L)), dev)
+    _dense(w_scales, "w_scales", tuple(_SCALE), (_blocks(N), _blocks(K)), dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if y is None else y.dtype
+    if out_dtype not in _DTYPE:
+        raise TypeError("out_dtype must be %s, got %s" % (_NAMES, out_dtype))
+    ys = C if y is None else _out_rows(y, "y", (M, C), (out_dtype,), dev)
+    if workspace is not None:
+        _scratch(workspace, dev)
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_fp8_mm(x, x_scales, w, w_scales, transposed, y, out_dtype, workspace)
+    if y is None:
+        y = torch.empty((M, C), dtype=out_dtype, device=dev)
+    if workspace is None:
+        need = _lib.load().hc_fp8_mm_workspace_bytes(transposed, M, N, K)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    _lib.call("hc_fp8_mm", x.data_ptr(), xs, x_scales.data_ptr(), _SCALE[x_scales.dtype], w.data_ptr(), w_scales.data_ptr(),
+              _SCALE[w_scales.dtype], transposed, M, N, K, y.data_ptr(), ys, _DTYPE[out_dtype],
+              None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+              _raw_stream(dev.index))
+    return y

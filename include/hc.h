@@ -567,6 +567,41 @@ hc_status hc_rms_norm_backward(const void *g_y, int64_t g_stride, const void *g_
                                void *g_x, int64_t gx_stride, float *g_norm_w, void *workspace,
                                size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * The product of 8-bit numbers with scales for blocks of 128 (codes and scales as the
+ * casts write them, or scales in fp32):
+ *   y[m][f] = sum over blocks b of K:  x_scales[m][b] w_scales[f / 128][b]
+ *                                      sum over k in b of x[m][k] w[f][k],
+ * or with transposed, the gradient of the rows (x is then the output's gradient, cast
+ * along N):
+ *   y[m][k] = sum over blocks b of N:  x_scales[m][b] w_scales[b][k / 128]
+ *                                      sum over f in b of x[m][f] w[f][k].
+ * A block's products are summed in fp32 by the tensor cores (whose additions may cut
+ * off rather than round the last bit of a partial sum), scaled and added up in
+ * fp32, and rounded once to y's type.  (The gradient of the weights is
+ * hc_grouped_mm_weights of the 16-bit rows, as one expert's.)
+ *
+ *   x [M, K] codes (transposed: [M, N]), rows x_stride apart                 in
+ *   x_scales [M, ceil(K / 128)] (transposed: [M, ceil(N / 128)]) of x_scale_type:
+ *   HC_F32 or HC_UE8M0                                                     in
+ *   w [N, K] codes, w_scales [ceil(N / 128), ceil(K / 128)] of w_scale_type, in
+ *   both directions                                                        in
+ *   y [M, N] (transposed: [M, K]) of y_type (fp32, bf16 or fp16), rows y_stride
+ *   apart                                                                 out
+ *   workspace of hc_fp8_mm_workspace_bytes(transposed, M, N, K) bytes, 16-byte aligned:
+ *   scratch of this call, free for others once it has completed; it may be NULL where
+ *   that is 0.
+ * M, N and K < 2^31 - 4096; N and K multiples of 16; x and w start on 16 bytes and x_stride is a
+ * multiple of 16 (the tensor copies' rule; HC_ERR_UNSUPPORTED, HC_ERR_MISALIGNED
+ * otherwise).
+ */
+size_t hc_fp8_mm_workspace_bytes(int transposed, int64_t M, int N, int K);
+
+hc_status hc_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scales, hc_dtype x_scale_type,
+                    const uint8_t *w, const void *w_scales, hc_dtype w_scale_type, int transposed,
+                    int64_t M, int N, int K, void *y, int64_t y_stride, hc_dtype y_type,
+                    void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
