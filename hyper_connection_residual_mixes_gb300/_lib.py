@@ -62,6 +62,9 @@ SIGNATURES = {
     "hc_rms_norm_backward": [P, I64, P, I64, I32, P, I64, I32, P, I32, P, I64, I32, P, I64, P, P, ctypes.c_size_t, P],
     "hc_fp8_mm_workspace_bytes": [I32, I64, I32, I32],
     "hc_fp8_mm": [P, I64, P, I32, P, P, I32, I32, I64, I32, I32, P, I64, I32, P, ctypes.c_size_t, P],
+    "hc_moe_tokens_workspace_bytes": [I32, I32, I32],
+    "hc_moe_tokens": [P, I64, I32, I32, I32, I32, I32, I32, P, I32, I32, F32, P, P, P, P, I32, P, P, I32, P, I64, P,
+                      ctypes.c_size_t, P],
     "hc_adamw_step": [P, I64, F64, F64, F64, F64, F64, I64, P, P, P, P],
 }
 
@@ -114,6 +117,7 @@ def load():
         lib.hc_layer_norm_backward_workspace_bytes.restype = ctypes.c_size_t
         lib.hc_rms_norm_backward_workspace_bytes.restype = ctypes.c_size_t
         lib.hc_fp8_mm_workspace_bytes.restype = ctypes.c_size_t
+        lib.hc_moe_tokens_workspace_bytes.restype = ctypes.c_size_t
         lib.hc_grouped_mm_workspace_bytes.restype = ctypes.c_size_t
         lib.hc_grouped_mm_weights_workspace_bytes.restype = ctypes.c_size_t
         _lib = lib

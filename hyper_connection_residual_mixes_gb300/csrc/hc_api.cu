@@ -835,4 +835,49 @@ hc_status hc_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scales, hc
                                          transposed != 0, M, N, K, y, y_stride, y_type, workspace, stream));
 }
 
+size_t hc_moe_tokens_workspace_bytes(int T, int top_k, int inner) {
+    if (T <= 0 || T > 64 || top_k <= 0 || top_k > 16 || inner <= 0 || inner > 65536) return 0;
+    return hc::moe_tokens_workspace_bytes(T, top_k, inner);
+}
+
+hc_status hc_moe_tokens(const void *x, int64_t x_stride, hc_dtype type, int T, int d, int experts,
+                        int inner, int top_k, const float *logits, int score, int normalise,
+                        float scale, int32_t *ids, float *p, const void *w_up, const void *w_down,
+                        hc_dtype w_type, const void *up_scales, const void *down_scales,
+                        hc_dtype scale_type, void *y, int64_t y_stride, void *workspace,
+                        size_t workspace_bytes, cudaStream_t stream) {
+    const bool f8 = w_type == HC_E4M3;
+    if (T < 0 || d <= 0 || experts <= 0 || inner <= 0 || top_k <= 0 || !known(type) || (!known(w_type) && !f8) ||
+        (f8 && !scale_known(scale_type)))
+        return HC_ERR_INVALID_ARG;
+    if (type == HC_F32 || (!f8 && w_type != type) || T > 64 || top_k > 16 || experts > 1024 || d % 16 || inner % 16 ||
+        d > 65536 || inner > 65536)
+        return HC_ERR_UNSUPPORTED;
+    if (logits && (top_k > experts || (score != 0 && score != 1) || !std::isfinite(scale))) return HC_ERR_INVALID_ARG;
+    if (!rows_fit(T, d, x_stride) || !rows_fit(T, d, y_stride) || (T > 1 && y_stride < d)) return HC_ERR_INVALID_ARG;
+    if (T == 0) return HC_OK;
+    const size_t need = hc_moe_tokens_workspace_bytes(T, top_k, inner);
+    if (!x || !w_up || !w_down || !y || (!logits && (!ids || !p)) || f8 != (up_scales != nullptr) ||
+        f8 != (down_scales != nullptr) || !workspace || workspace_bytes < need)
+        return HC_ERR_INVALID_ARG;
+    if (x_stride % 8) return HC_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(w_up) || !aligned16(w_down) || !aligned16(workspace) || !aligned_to(y, 2) ||
+        !aligned_to(logits, 4) || !aligned_to(ids, 4) || !aligned_to(p, 4) ||
+        (f8 && scale_type == HC_F32 && (!aligned_to(up_scales, 4) || !aligned_to(down_scales, 4))))
+        return HC_ERR_MISALIGNED;
+    const int64_t matrix = (int64_t)experts * inner * d * (f8 ? 1 : 2), entries = (int64_t)T * top_k;
+    const int64_t blocks = f8 ? experts * fp8_blocks(inner) * fp8_blocks(d) * scale_size(scale_type) : 0;
+    const Span s_ids = span(ids, ids ? entries * 4 : 0), s_p = span(p, p ? entries * 4 : 0);
+    const Span ins[] = {rows_span(x, T, d, x_stride, type), span(logits, logits ? (int64_t)T * experts * 4 : 0),
+                        span(w_up, 2 * matrix), span(w_down, matrix), span(up_scales, 2 * blocks), span(down_scales, blocks),
+                        logits ? Span{0, 0} : s_ids, logits ? Span{0, 0} : s_p};
+    const Span outs[] = {rows_span(y, T, d, y_stride, type), span(workspace, (int64_t)need), logits ? s_ids : Span{0, 0},
+                         logits ? s_p : Span{0, 0}};
+    const hc_status st = check_alias(outs, 4, ins, 8);
+    if (st != HC_OK) return st;
+    return cuda_status(hc::launch_moe_tokens(x, x_stride, type, T, d, experts, inner, top_k, logits, score == 1, normalise != 0,
+                                             scale, ids, p, w_up, w_down, f8, up_scales, down_scales, scale_type == HC_F32, y,
+                                             y_stride, workspace, stream));
+}
+
 }  // extern "C"

@@ -68,4 +68,11 @@ cudaError_t launch_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scal
 size_t fp8_mm_workspace_bytes(bool transposed, int64_t M, int N, int K);
 cudaError_t consume_fp8_mm_device_error(cudaStream_t s, unsigned int *flag);  // as the other files' (hc_launch.h)
 
+// ------------------------------------------------------------ experts' layer for a few tokens (hc_moe.cu)
+cudaError_t launch_moe_tokens(const void *x, int64_t x_stride, hc_dtype type, int T, int d, int experts, int inner, int top_k,
+                              const float *logits, bool sigmoid, bool normalise, float scale, int32_t *ids, float *p, const void *w_up,
+                              const void *w_down, bool f8, const void *up_scales, const void *down_scales, bool scales_f32, void *y,
+                              int64_t y_stride, void *workspace, cudaStream_t s);
+size_t moe_tokens_workspace_bytes(int T, int top_k, int inner);
+
 }  // namespace hc

@@ -1,4 +1,5 @@
-"""Sublayers in 8 bits: RMS norm with the residual and the cast, the casts, products.
+"""Sublayers in 8 bits: RMS norm with the residual and the cast, the casts, products,
+the experts' layer for a few tokens.
 
 The same kind of binding as the sublayer operators'.  8-bit tensors are E4M3
 codes (uint8) with a scale for each block of 128 values of a row, or of 128 x 128
@@ -9,10 +10,11 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .sublayer import (_DTYPE, _NAMES, _at, _current_device, _dense, _like, _norm_input, _norm_weights, _out_rows, _raw_stream,
+from .sublayer import (_DTYPE, _HALF, _NAMES, _at, _current_device, _dense, _like, _norm_input, _norm_weights, _out_rows, _raw_stream,
                        _rows, _scratch, _tensor)
 
-__all__ = ["hc_fp8_cast", "hc_fp8_cast_weights", "hc_rms_norm", "hc_rms_norm_backward", "hc_fp8_mm"]
+__all__ = ["hc_fp8_cast", "hc_fp8_cast_weights", "hc_rms_norm", "hc_rms_norm_backward", "hc_fp8_mm",
+           "hc_moe_tokens"]
 
 RMS_NORM_EPS = 1e-6
 FP8_BLOCK = 128  # values that share a scale
@@ -214,3 +216,83 @@ def hc_fp8_mm(x, x_scales, w, w_scales, transposed=False, y=None, out_dtype=None
               None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
               _raw_stream(dev.index))
     return y
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def hc_moe_tokens(x, w_up, w_down, ids=None, weights=None, logits=None, top_k=None, score="softmax", normalise=True,
+                  scale=1.0, up_scales=None, down_scales=None, y=None, workspace=None, stream=None):
+    """A whole mixture-of-experts layer for up to 64 tokens: x [T, d] (bf16 or fp16, evenly
+    spaced rows), w_up [experts, 2, inner, d] (the gate's rows, then the other's) and w_down
+    [experts, d, inner], of x's type, or uint8 codes with up_scales [experts, 2,
+    ceil(inner / 128), ceil(d / 128)] and down_scales [experts, ceil(d / 128),
+    ceil(inner / 128)] (UE8M0 bytes or fp32; hc_fp8_cast_weights makes both).  y[t] is the sum
+    over t's experts of weight * w_down[e] (silu(w_up[e, 0] x[t]) * (w_up[e, 1] x[t])).
+
+    The choice is given, ids [T, top_k] int32 and weights [T, top_k] fp32 (an id out of
+    range, such as -1, counts for nothing): -> y [T, d].  Or it is made of logits
+    [T, experts] fp32: the top_k largest, weighted by the softmax over all experts or
+    the sigmoid (score), with normalise divided by their sum over the chosen ones,
+    times scale: -> (y, ids, weights).  d and inner are multiples of 16.  For training and for
+    more tokens: hc_grouped_mm.  workspace: a uint8 device tensor of at least the
+    size the library asks for (allocated here when None)."""
+    _tensor(x, "x", _HALF)
+    dev = x.device
+    if x.dim() != 2:
+        raise ValueError("x must be [T, d]")
+    T, d = x.shape
+    n, xs = _rows(x, "x")
+    xs = xs if n > 1 else -(-d // 8) * 8  # (a single row may carry any stride)
+    if (up_scales is None) != (down_scales is None):
+        raise ValueError("up_scales and down_scales go together")
+    f8 = up_scales is not None
+    kinds = (torch.uint8,) if f8 else (x.dtype,)
+    _tensor(w_up, "w_up", kinds, dev)
+    if w_up.dim() != 4 or w_up.shape[1] != 2 or w_up.shape[3] != d:
+        raise ValueError("w_up has shape %s, expected (experts, 2, inner, %d)" % (tuple(w_up.shape), d))
+    E, inner = w_up.shape[0], w_up.shape[2]
+    _dense(w_up, "w_up", kinds, w_up.shape, dev)
+    _dense(w_down, "w_down", kinds, (E, d, inner), dev)
+    if f8:
+        _dense(up_scales, "up_scales", tuple(_SCALE), (E, 2, _blocks(inner), _blocks(d)), dev)
+        _dense(down_scales, "down_scales", (up_scales.dtype,), (E, _blocks(d), _blocks(inner)), dev)
+    if (logits is None) == (ids is None):
+        raise ValueError("either logits or ids and weights")
+    if logits is not None:
+        if weights is not None:
+            raise ValueError("weights are given with ids")
+        if score not in _SCORES:
+            raise ValueError('score must be "softmax" or "sigmoid", got %r' % (score,))
+        if not isinstance(top_k, int) or top_k < 1:
+            raise ValueError("top_k must be a number from 1 on")
+        _dense(logits, "logits", (torch.float32,), (T, E), dev)
+    else:
+        _tensor(ids, "ids", (torch.int32,), dev)
+        if ids.dim() != 2 or (top_k is not None and ids.shape[1] != top_k):
+            raise ValueError("ids must be [T, top_k]")
+        top_k = ids.shape[1]
+        _dense(ids, "ids", (torch.int32,), (T, top_k), dev)
+        _dense(weights, "weights", (torch.float32,), (T, top_k), dev)
+    ys = d if y is None else _out_rows(y, "y", (T, d), (x.dtype,), dev)
+    if workspace is not None:
+        _scratch(workspace, dev)
+    if stream is not None or _current_device() != dev.index:
+        with _at(dev, stream):
+            return hc_moe_tokens(x, w_up, w_down, ids, weights, logits, None if logits is None else top_k, score, normalise,
+                                 scale, up_scales, down_scales, y, workspace)
+    if y is None:
+        y = torch.empty((T, d), dtype=x.dtype, device=dev)
+    if workspace is None:
+        need = _lib.load().hc_moe_tokens_workspace_bytes(T, top_k, inner)
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+    if logits is not None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    _lib.call("hc_moe_tokens", x.data_ptr(), xs, _DTYPE[x.dtype], T, d, E, inner, top_k,
+              None if logits is None else logits.data_ptr(), _SCORES.get(score, 0), normalise, scale, ids.data_ptr(),
+              weights.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), 4 if f8 else _DTYPE[x.dtype],
+              up_scales.data_ptr() if f8 else None, down_scales.data_ptr() if f8 else None,
+              _SCALE[up_scales.dtype] if f8 else 0, y.data_ptr(), ys, workspace.data_ptr(), workspace.numel(),
+              _raw_stream(dev.index))
+    return y if logits is None else (y, ids, weights)

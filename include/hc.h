@@ -356,7 +356,8 @@ typedef enum {
     HC_F32 = 0,
     HC_BF16 = 1,
     HC_F16 = 2,
-    HC_UE8M0 = 3 /* bytes that stand for 2^(byte - 127), 255 for NaN: a type of scales only */
+    HC_UE8M0 = 3, /* bytes that stand for 2^(byte - 127), 255 for NaN: a type of scales only */
+    HC_E4M3 = 4   /* codes of 8-bit numbers: a type of hc_moe_tokens' weights only */
 } hc_dtype;
 
 /*
@@ -601,6 +602,50 @@ hc_status hc_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scales, hc
                     const uint8_t *w, const void *w_scales, hc_dtype w_scale_type, int transposed,
                     int64_t M, int N, int K, void *y, int64_t y_stride, hc_dtype y_type,
                     void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (1 <= T <= 64; for more:
+ * hc_grouped_mm), in two kernels:
+ *   y[t] = sum over t's chosen experts e of
+ *          p[t, e] w_down[e] (silu(w_up[e, 0] x[t]) * (w_up[e, 1] x[t])),
+ * silu(v) = v / (1 + e^-v).
+ *
+ * The choice.  With logits [T, experts] fp32: each token's top_k largest, of equal ones
+ * the first; an expert whose logit is -infinity or NaN is not chosen.  Their weights
+ * are the softmax over all experts (score 0) or the sigmoid (score 1) of the
+ * logits, with normalise divided by their sum over the chosen ones, then times scale;
+ * ids [T, top_k] and p [T, top_k] are written, in falling order, with id -1 and weight 0
+ * for a place that nothing is left for.  With logits NULL, ids and p are read: a
+ * place whose id is not in [0, experts) counts for nothing, an expert named twice for
+ * a token with both weights.  A token without an expert gets zeros.
+ *
+ * Sums of products are in fp32; the activation is kept in fp32 and goes into the
+ * second product as two bf16 numbers (16 bits of it) for bf16 weights, else as fp16
+ * numbers (11 bits), scaled by a power of two for each block of it; y is rounded once.
+ *
+ *   x [T, d] of type (bf16 or fp16), rows x_stride >= 0 apart                in
+ *   logits [T, experts] fp32, or NULL                                        in
+ *   ids [T, top_k] int32, p [T, top_k] fp32: out with logits (each may be NULL
+ *   then), else                                                              in
+ *   w_up [experts, 2, inner, d] (the gate's rows, then the other's) and
+ *   w_down [experts, d, inner] of w_type: type, or HC_E4M3 codes with scales for
+ *   blocks of 128 x 128 of each matrix, up_scales [experts, 2, ceil(inner / 128),
+ *   ceil(d / 128)] and down_scales [experts, ceil(d / 128), ceil(inner / 128)] of
+ *   scale_type (HC_F32 or HC_UE8M0; NULL without codes)                      in
+ *   y [T, d] of type, rows y_stride >= d apart                              out
+ *   workspace of hc_moe_tokens_workspace_bytes(T, top_k, inner) bytes, 16-byte
+ *   aligned: scratch of this call, free for others once it has completed.
+ * top_k <= 16 and, with logits, <= experts; experts <= 1024; d and inner multiples of 16,
+ * <= 65536; x, w_up and w_down start on 16 bytes and x_stride is a multiple of 8.
+ */
+size_t hc_moe_tokens_workspace_bytes(int T, int top_k, int inner);
+
+hc_status hc_moe_tokens(const void *x, int64_t x_stride, hc_dtype type, int T, int d, int experts,
+                        int inner, int top_k, const float *logits, int score, int normalise,
+                        float scale, int32_t *ids, float *p, const void *w_up, const void *w_down,
+                        hc_dtype w_type, const void *up_scales, const void *down_scales,
+                        hc_dtype scale_type, void *y, int64_t y_stride, void *workspace,
+                        size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
