@@ -33,8 +33,10 @@ namespace moe {
 
 constexpr int kMaxTokens = 64, kMaxTop = 16, kMaxExperts = 1024, kMaxEntries = kMaxTokens * kMaxTop;
 constexpr int kCell = 1024;       // bytes of a piece: 8 rows of 128 bytes
-constexpr int kUpWarps = 16, kUpCells = 8, kUpTiles = 8;  // warps, pieces each has under way, row tiles of a unit (4 of G, 4 of U)
-constexpr int kDownCells = 192, kDownTiles = 6;           // pieces that a block has under way, row tiles of a pass
+constexpr int kWarps = 8;
+constexpr int kUpPairs = 4, kUpDeep = 2;      // pairs of row tiles (of G and of U) of a unit; steps whose pieces are under way
+constexpr int kDownTiles = 6, kDownDeep = 4;  // row tiles of a pass; steps whose pieces are under way
+constexpr int kUpRing = kUpDeep * kUpPairs * 2 * kCell, kDownRing = kDownDeep * kDownTiles * kCell;  // of a warp
 
 struct Args {
     const void *x;
@@ -61,6 +63,7 @@ struct Lists {
     uint16_t active[kMaxExperts];    // experts with entries, ascending
     uint16_t first[kMaxExperts + 1]; // of the i-th of these: its first place in `list`
     uint16_t tiles[kMaxExperts + 1]; // ... and the tiles of 16 entries of those before it
+    uint64_t tokens[kMaxExperts];    // ... its tokens, as bits
     int count[kMaxExperts];
     int n;                           // how many experts have entries
 };
@@ -182,30 +185,28 @@ __device__ __forceinline__ void route(Args a, Lists &l, bool write) {
     for (int i = threadIdx.x; i < entries; i += blockDim.x)
         if (l.id[i] >= 0) l.list[l.count[l.id[i]] + l.rank[i]] = (uint16_t)i;
     __syncthreads();
+    for (int i = threadIdx.x; i < l.n; i += blockDim.x) {
+        uint64_t m = 0;
+        for (int j = l.first[i]; j < l.first[i + 1]; ++j) m |= (uint64_t)1 << (l.list[j] / a.top);
+        l.tokens[i] = m;
+    }
+    __syncthreads();
 }
 
 // ------------------------------------------------------------ pieces
-// A lane's share of a piece: 16 bytes at 16 (lane % 4) and 64 more, of row lane / 4.
-__device__ __forceinline__ void load_piece(uint32_t to, const uint8_t *row, bool is_there, int at, int row_bytes) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const int off = at + 64 * s;
-        const int bytes = is_there && off < row_bytes ? 16 : 0;
-        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to + 512 * s), "l"(bytes ? row + off : row), "r"(bytes)
-                     : "memory");
-    }
+// A lane's share of a piece: 16 bytes at 16 (lane % 4) of the row lane / 4, and 64 bytes on.
+// `there`: whether they are there, else zeros.
+__device__ __forceinline__ void load_piece(uint32_t to, const uint8_t *from, bool there0, bool there1) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there0 ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0 + 512], [%1 + 64], 16, %2;" ::"r"(to), "l"(from), "r"(there1 ? 16 : 0) : "memory");
 }
 struct Piece {
     uint32_t w[8];
 };
 __device__ __forceinline__ Piece read_piece(uint32_t at) {
     Piece p;
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(p.w[4 * s]), "=r"(p.w[4 * s + 1]), "=r"(p.w[4 * s + 2]), "=r"(p.w[4 * s + 3])
-                     : "r"(at + 512 * s)
-                     : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(p.w[0]), "=r"(p.w[1]), "=r"(p.w[2]), "=r"(p.w[3]) : "r"(at) : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + 512];" : "=r"(p.w[4]), "=r"(p.w[5]), "=r"(p.w[6]), "=r"(p.w[7]) : "r"(at) : "memory");
     return p;
 }
 // four codes as two pairs of fp16
@@ -235,22 +236,39 @@ struct Tokens {
             for (int i = 0; i < kPairs; ++i) v[r][i] = 0;
         }
     }
-    // values as they are
-    __device__ __forceinline__ void put16(int r, int i, uint4 u) { v[r][i] = u.x, v[r][i + 1] = u.y, v[r][i + 2] = u.z, v[r][i + 3] = u.w; }
-    // fp32 values -> fp16, the row's largest (over the piece: the lanes of four) brought to
-    // [2^14, 2^15) by a power of two: 11 bits of each value, of small ones 2^-39 of the largest
-    __device__ __forceinline__ void put_scaled(int r, const float (&f)[2 * kPairs]) {
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 2 * kPairs; ++i) amax = fmaxf(amax, fabsf(f[i]));
+    // A row's values -> fp16, the largest (over the piece: the lanes of four) brought to
+    // [2^14, 2^15) by a power of two: 11 bits of each value, of small ones 2^-39 of the largest.
+    // Of that largest: the power of two, and what it undoes.
+    __device__ __forceinline__ float power(int r, float amax) {
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         int b = (int)(__float_as_uint(amax) >> 23);
         b = b < 15 ? 15 : b;
-        const float m = __uint_as_float((uint32_t)(268 - b) << 23);
         unit[r] = __uint_as_float((uint32_t)(b - 14) << 23);
+        return __uint_as_float((uint32_t)(268 - b) << 23);
+    }
+    __device__ __forceinline__ void put_scaled(int r, const float (&f)[2 * kPairs]) {
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * kPairs; ++i) amax = fmaxf(amax, fabsf(f[i]));
+        const float m = power(r, amax);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) v[r][i] = half2_of(f[2 * i] * m, f[2 * i + 1] * m);
+    }
+    // ... of bf16 values in pairs (the product with the power is exact in bf16)
+    __device__ __forceinline__ void put_scaled(int r, const uint32_t (&w)[kPairs]) {
+        const auto pair_of = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
+        __nv_bfloat162 top = __habs2(pair_of(w[0]));
+#pragma unroll
+        for (int i = 1; i < kPairs; ++i) top = __hmax2(top, __habs2(pair_of(w[i])));
+        const float2 t = __bfloat1622float2(top);
+        const __nv_bfloat162 m = __float2bfloat162_rn(power(r, fmaxf(fmaxf(t.x, t.y), 0.0f)));
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const __nv_bfloat162 p = __hmul2(pair_of(w[i]), m);
+            const uint32_t u = *reinterpret_cast<const uint32_t *>(&p);
+            v[r][i] = half2_of(bf16lo(u), bf16hi(u));
+        }
     }
 };
 
@@ -259,16 +277,25 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
     if constexpr (__is_same(T, __nv_bfloat16)) mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
     else mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
 }
-// part += a piece's products
+// even, odd += a piece's products, every second step of k each (two chains of MMAs)
 template <typename T, bool kF8>
-__device__ __forceinline__ void multiply(float (&part)[4], const Tokens<kF8> &x, const Piece &p) {
+__device__ __forceinline__ void multiply(float (&even)[4], float (&odd)[4], const Tokens<kF8> &x, const Piece &p) {
 #pragma unroll
     for (int i = 0; i < Tokens<kF8>::kPairs; i += 2) {
         uint32_t b0, b1;
         if constexpr (kF8) widen(p.w[i / 2], b0, b1);
         else b0 = p.w[i], b1 = p.w[i + 1];
-        mma<T>(part, x.v[0][i], x.v[1][i], x.v[0][i + 1], x.v[1][i + 1], b0, b1);
+        mma<T>(i & 2 ? odd : even, x.v[0][i], x.v[1][i], x.v[0][i + 1], x.v[1][i + 1], b0, b1);
     }
+}
+// acc += a piece's products, scaled: by s (the block's) and what the tokens were divided by
+template <bool kF8>
+__device__ __forceinline__ void multiply_scaled(float (&acc)[4], const Tokens<kF8> &x, const Piece &p, float s) {
+    float even[4] = {0.0f, 0.0f, 0.0f, 0.0f}, odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    multiply<__half, kF8>(even, odd, x, p);
+    const float u0 = s * x.unit[0], u1 = s * x.unit[1];
+    acc[0] = fmaf(even[0] + odd[0], u0, acc[0]), acc[1] = fmaf(even[1] + odd[1], u0, acc[1]);
+    acc[2] = fmaf(even[2] + odd[2], u1, acc[2]), acc[3] = fmaf(even[3] + odd[3], u1, acc[3]);
 }
 
 // ------------------------------------------------------------ G and U
@@ -276,9 +303,9 @@ __device__ __forceinline__ void multiply(float (&part)[4], const Tokens<kF8> &x,
 struct Unit {
     int i, m, row, left;  // the expert (in `active`), tile of entries, next row; rows left of this block's
     int lo, hi;           // the unit's rows
-    __device__ __forceinline__ bool next(const Args &a, const Lists &l) {
+    __device__ __forceinline__ bool next(const Args &a) {
         if (left <= 0) return false;
-        lo = row, hi = (lo & ~7) + 8 * (kUpTiles / 2);
+        lo = row, hi = (lo & ~7) + 8 * kUpPairs;
         if (hi > a.inner) hi = a.inner;
         if (hi - lo > left) hi = lo + left;
         left -= hi - lo, row = hi;
@@ -292,12 +319,14 @@ struct Unit {
     }
 };
 
+// Steps: a unit's pieces, one of 128 bytes of every row at a time, go round the warps.
 template <typename TX, bool kF8>
-__global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
-    constexpr int kBytes = kF8 ? 1 : 2;
+__global__ void __launch_bounds__(32 * kWarps, 1) k_moe_up(const Args a) {
+    constexpr int kBytes = kF8 ? 1 : 2, kOut = kUpPairs * 128;  // kOut: rows by entries of a unit
+    constexpr int kVecs = kF8 ? 4 : 2;  // 16-byte loads of a token's values of a piece
     extern __shared__ __align__(128) uint8_t smem[];
-    Lists &l = *reinterpret_cast<Lists *>(smem + kUpWarps * kUpCells * kCell + kUpWarps * kUpTiles * 4 * 32 * 4);
-    float *const red = reinterpret_cast<float *>(smem + kUpWarps * kUpCells * kCell);  // [warp][tile][4][lane]
+    float *const red = reinterpret_cast<float *>(smem + kWarps * kUpRing);  // [2][warp][G, U][kOut]
+    Lists &l = *reinterpret_cast<Lists *>(red + 2 * kWarps * 2 * kOut);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     route(a, l, true);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -317,216 +346,266 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
     }
     const int row_bytes = a.d * kBytes, pieces = (row_bytes + 127) / 128;
     const int64_t matrix = (int64_t)a.inner * row_bytes;  // G or U of an expert
-
-    // copies run ahead: unit by unit, piece by piece of this warp's, tile by tile
-    Unit ahead = first;
-    bool more = ahead.next(a, l);
-    int au = 0, ak = warp, atile = 0, slot = 0;
-    const uint8_t *abase = nullptr;
-    const auto skip = [&](int u) {  // the warp's first piece of unit u: pieces go round the warps
-        int k = (warp - u * pieces) % kUpWarps;
-        return k < 0 ? k + kUpWarps : k;
+    const auto begin = [&](int u) {  // the warp's first piece of unit u
+        return (warp + u * (kWarps - pieces % kWarps)) % kWarps;
     };
-    const auto expert_base = [&](const Unit &u) { return a.up + (int64_t)l.active[u.i] * 2 * matrix; };
-    if (more) abase = expert_base(ahead);
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kUpCells * kCell + lane * 16);
-    const auto fetch = [&]() {
+
+    // copies run kUpDeep steps ahead
+    Unit ahead = first;
+    bool more = ahead.next(a);
+    int au = 0, ak = warp;
+    uint32_t rows = 0;                // which of the unit's pairs of tiles have this lane's row
+    const uint8_t *lane_row = a.up;   // this lane's row of the first tile
+    const auto aim = [&]() {
+        const int base = ahead.lo & ~7;
+        lane_row = a.up + (int64_t)l.active[ahead.i] * 2 * matrix + (int64_t)(base + g) * row_bytes + t4 * 16;
+        rows = 0;
+#pragma unroll
+        for (int j = 0; j < kUpPairs; ++j) rows |= (uint32_t)(base + 8 * j + g >= ahead.lo && base + 8 * j + g < ahead.hi) << j;
+    };
+    const auto settle = [&]() {  // to the unit that has a piece for this warp
         while (more && ak >= pieces) {
             ahead.step(a, l);
-            more = ahead.next(a, l);
-            if (more) abase = expert_base(ahead), ak = skip(++au);
+            more = ahead.next(a);
+            if (more) aim(), ak = begin(++au);
         }
-        if (more) {
-            const int row = (ahead.lo & ~7) + 8 * (atile >> 1) + g;
-            load_piece(ring + (uint32_t)slot * kCell, abase + (atile & 1) * matrix + (int64_t)row * row_bytes,
-                       row >= ahead.lo && row < ahead.hi, ak * 128 + t4 * 16, row_bytes);
-            if (++atile == kUpTiles) atile = 0, ak += kUpWarps;
-        }
-        cp_async_commit();
-        if (++slot == kUpCells) slot = 0;
+        if (!more) rows = 0;
     };
-    for (int c = 0; c < kUpCells; ++c) fetch();
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kUpRing + lane * 16);
+    const int64_t tile_bytes = 8 * (int64_t)row_bytes;
+    const auto fetch = [&](uint32_t to, int j) {
+        const uint8_t *const p = lane_row + (int64_t)j * tile_bytes + ak * 128;
+        const bool there = rows >> j & 1u, first_half = there && ak * 128 + t4 * 16 < row_bytes,
+                   second_half = there && ak * 128 + t4 * 16 + 64 < row_bytes;
+        load_piece(to, p, first_half, second_half);
+        load_piece(to + kCell, p + matrix, first_half, second_half);
+        cp_async_commit();
+    };
+    if (more) aim();
+    settle();
+#pragma unroll
+    for (int s = 0; s < kUpDeep; ++s) {
+#pragma unroll
+        for (int j = 0; j < kUpPairs; ++j) fetch(ring + (uint32_t)((s * kUpPairs + j) * 2 * kCell), j);
+        ak += kWarps;
+        settle();
+    }
 
     const int row_blocks = (a.inner + kFp8Block - 1) / kFp8Block, col_blocks = (a.d + kFp8Block - 1) / kFp8Block;
+    uint32_t at = ring;  // the step's place
+    int buf = 0;
     Unit u = first;
-    for (int un = 0; u.next(a, l); u.step(a, l), ++un) {
+    for (int un = 0; u.next(a); u.step(a, l), ++un, buf ^= 1) {
         // this lane's two tokens
-        const int e = l.active[u.i], at = l.first[u.i] + 16 * u.m + g, end = l.first[u.i + 1];
-        const bool has[2] = {at < end, at + 8 < end};
-        const bool second = l.first[u.i] + 16 * u.m + 8 < end;  // (of the warp: whether there are more than eight)
+        const int e = l.active[u.i], entry0 = l.first[u.i] + 16 * u.m, end = l.first[u.i + 1];
+        const bool second = entry0 + 8 < end;  // (of the warp: whether there are more than eight)
         const TX *x[2];
+        bool has[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) x[r] = static_cast<const TX *>(a.x) + (has[r] ? (int64_t)(l.list[at + 8 * r] / a.top) * a.xs : 0);
+        for (int r = 0; r < 2; ++r) {
+            has[r] = entry0 + g + 8 * r < end;
+            x[r] = static_cast<const TX *>(a.x) + (has[r] ? (int64_t)(l.list[entry0 + g + 8 * r] / a.top) * a.xs : 0);
+        }
         const int base = u.lo & ~7, tiles = (u.hi - base + 7) / 8;
-        float acc[kUpTiles][4];
+        // lane 2 j + (0: G, 1: U) looks after the scale of pair j
+        int64_t scale_at = 0;
+        if (kF8 && lane < 2 * tiles)
+            scale_at = (((int64_t)e * 2 + (lane & 1)) * row_blocks + (base + 8 * (lane >> 1)) / kFp8Block) * col_blocks;
+        uint4 raw[2][kVecs];
+        float scale = 1.0f;
+        const auto load_tokens = [&](int k) {
 #pragma unroll
-        for (int i = 0; i < kUpTiles; ++i)
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
-        for (int k = skip(un); k < pieces; k += kUpWarps) {
+                for (int s = 0; s < kVecs; ++s) {
+                    const int c = kF8 ? k * 128 + (s >> 1) * 64 + t4 * 16 + (s & 1) * 8 : k * 64 + s * 32 + t4 * 8;
+                    raw[r][s] = make_uint4(0, 0, 0, 0);
+                    if (has[r] && c < a.d) raw[r][s] = __ldg(reinterpret_cast<const uint4 *>(x[r] + c));
+                }
+            if (kF8 && lane < 2 * tiles) scale = a.up_scales.at(scale_at + k);
+        };
+        float acc[kUpPairs][2][4], odd[kF8 ? 1 : kUpPairs][2][4];
+#pragma unroll
+        for (int j = 0; j < kUpPairs; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    acc[j][h][k] = 0.0f;
+                    if (!kF8) odd[kF8 ? 0 : j][h][k] = 0.0f;
+                }
+        int k = begin(un);
+        if (k < pieces) load_tokens(k);
+        for (; k < pieces; k += kWarps) {
             Tokens<kF8> tok;
             tok.clear();
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 if (r == 1 && !second) break;
-                if constexpr (!kF8) {
+                uint32_t w[Tokens<kF8>::kPairs];
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const int c = k * 64 + s * 32 + t4 * 8;
-                        if (has[r] && c < a.d) tok.put16(r, 4 * s, __ldg(reinterpret_cast<const uint4 *>(x[r] + c)));
-                    }
-                } else if constexpr (__is_same(TX, __half)) {
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const int c = k * 128 + s * 64 + t4 * 16;
-                        if (has[r] && c < a.d) {
-                            tok.put16(r, 8 * s, __ldg(reinterpret_cast<const uint4 *>(x[r] + c)));
-                            tok.put16(r, 8 * s + 4, __ldg(reinterpret_cast<const uint4 *>(x[r] + c + 8)));
-                        }
-                    }
+                for (int s = 0; s < kVecs; ++s) w[4 * s] = raw[r][s].x, w[4 * s + 1] = raw[r][s].y, w[4 * s + 2] = raw[r][s].z, w[4 * s + 3] = raw[r][s].w;
+                if constexpr (kF8 && __is_same(TX, __nv_bfloat16)) {
+                    tok.put_scaled(r, w);
                 } else {
-                    float f[32];
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const int c = k * 128 + (s >> 1) * 64 + t4 * 16 + (s & 1) * 8;
-                        uint4 q = make_uint4(0, 0, 0, 0);
-                        if (has[r] && c < a.d) q = __ldg(reinterpret_cast<const uint4 *>(x[r] + c));
-                        f[8 * s] = bf16lo(q.x), f[8 * s + 1] = bf16hi(q.x), f[8 * s + 2] = bf16lo(q.y), f[8 * s + 3] = bf16hi(q.y);
-                        f[8 * s + 4] = bf16lo(q.z), f[8 * s + 5] = bf16hi(q.z), f[8 * s + 6] = bf16lo(q.w), f[8 * s + 7] = bf16hi(q.w);
-                    }
-                    tok.put_scaled(r, f);
+                    for (int i = 0; i < Tokens<kF8>::kPairs; ++i) tok.v[r][i] = w[i];
                 }
             }
+            const float scales = scale;
+            if (k + kWarps < pieces) load_tokens(k + kWarps);
 #pragma unroll
-            for (int i = 0; i < kUpTiles; ++i) {
-                cp_async_wait<kUpCells - 1>();
-                const Piece p = read_piece(ring + (uint32_t)slot * kCell);
-                if ((i >> 1) < tiles) {
+            for (int j = 0; j < kUpPairs; ++j) {
+                cp_async_wait<kUpDeep * kUpPairs - 1>();
+                const uint32_t here = at + (uint32_t)(j * 2 * kCell);
+                const Piece pg = read_piece(here), pu = read_piece(here + kCell);
+                if (j < tiles) {
                     if constexpr (kF8) {
-                        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        multiply<__half, true>(part, tok, p);
-                        // (a tile's rows are of one block of the scales)
-                        const float s = a.up_scales.at((((int64_t)e * 2 + (i & 1)) * row_blocks + (base + 8 * (i >> 1)) / kFp8Block) * col_blocks + k);
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float f = s * tok.unit[r];
-                            acc[i][2 * r] = fmaf(part[2 * r], f, acc[i][2 * r]);
-                            acc[i][2 * r + 1] = fmaf(part[2 * r + 1], f, acc[i][2 * r + 1]);
-                        }
+                        multiply_scaled<true>(acc[j][0], tok, pg, __shfl_sync(0xffffffffu, scales, 2 * j));
+                        multiply_scaled<true>(acc[j][1], tok, pu, __shfl_sync(0xffffffffu, scales, 2 * j + 1));
                     } else {
-                        multiply<TX, false>(acc[i], tok, p);
+                        multiply<TX, false>(acc[j][0], odd[kF8 ? 0 : j][0], tok, pg);
+                        multiply<TX, false>(acc[j][1], odd[kF8 ? 0 : j][1], tok, pu);
                     }
                 }
-                fetch();
+                fetch(here, j);
             }
+            at = at == ring ? ring + kUpRing / kUpDeep : ring;
+            static_assert(kUpDeep == 2, "two places");
+            ak += kWarps;
+            settle();
         }
-        // the warps' sums meet, those that had a piece in the order of their pieces
-        const int from_warps = pieces < kUpWarps ? pieces : kUpWarps;
-        if (skip(un) < pieces) {
+        // the warps' sums meet
+        float *const mine = red + ((buf * kWarps + warp) * 2) * kOut + lane;
+        if (begin(un) < pieces) {
 #pragma unroll
-            for (int i = 0; i < kUpTiles; ++i)
+            for (int j = 0; j < kUpPairs; ++j)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if ((i >> 1) < tiles && (k < 2 || second)) red[((warp * kUpTiles + i) * 4 + k) * 32 + lane] = acc[i][k];
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (j < tiles && (q < 2 || second)) mine[h * kOut + (j * 4 + q) * 32] = acc[j][h][q] + (kF8 ? 0.0f : odd[kF8 ? 0 : j][h][q]);
         }
-        __syncthreads();
-        static_assert(kUpWarps * 32 == kUpTiles / 2 * 128, "a thread for each row and entry of a unit");
-        {
-            const int tile = threadIdx.x >> 7, k = threadIdx.x >> 5 & 3;
-            const int row = base + 8 * tile + 2 * t4 + (k & 1), entry = l.first[u.i] + 16 * u.m + g + 8 * (k >> 1);
-            if (tile < tiles && row >= u.lo && row < u.hi && entry < end) {
-                float gate = 0.0f, up = 0.0f;
-                for (int j = 0, w = un * pieces % kUpWarps; j < from_warps; ++j) {
-                    gate += red[((w * kUpTiles + 2 * tile) * 4 + k) * 32 + lane];
-                    up += red[((w * kUpTiles + 2 * tile + 1) * 4 + k) * 32 + lane];
-                    if (++w == kUpWarps) w = 0;
-                }
-                const int id = l.list[entry];
-                a.a[(int64_t)id * a.inner + row] = gate / (1.0f + expf(-gate)) * up * l.p[id];
+        __syncthreads();  // (two buffers: the next unit's sums are written while a slow warp still reads these)
+        const int meet = pieces < kWarps ? pieces : kWarps, w0 = un * (pieces % kWarps) % kWarps;  // those that had a piece, in their order
+        for (int o = threadIdx.x; o < kOut; o += 32 * kWarps) {
+            const int j = o >> 7, q = o >> 5 & 3;  // (o % 32 is this lane)
+            const int row = base + 8 * j + 2 * t4 + (q & 1), entry = entry0 + g + 8 * (q >> 1);
+            if (j >= tiles || row < u.lo || row >= u.hi || entry >= end) continue;
+            float gate = 0.0f, up = 0.0f;
+            for (int i = 0, w = w0; i < meet; ++i) {
+                const float *from_w = red + ((buf * kWarps + w) * 2) * kOut + o;
+                gate += from_w[0], up += from_w[kOut];
+                if (++w == kWarps) w = 0;
             }
+            const int id = l.list[entry];
+            a.a[(int64_t)id * a.inner + row] = gate / (1.0f + expf(-gate)) * up * l.p[id];
         }
-        __syncthreads();
     }
     cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------ D
-// Rows [from, to) of the output; MT tiles of 16 tokens; kWarps warps share the experts and
-// their contraction.
-template <typename TX, bool kF8, int MT, int kWarps>
+// A block's rows of the output, in passes of kDownTiles tiles of 8; MT tiles of 16 tokens.
+// Steps: a piece of 128 bytes of every row of one expert; they go round the warps.
+template <typename TX, bool kF8, int MT>
 __global__ void __launch_bounds__(32 * kWarps, 1) k_moe_down(const Args a) {
-    constexpr int kBytes = kF8 ? 1 : 2, kCells = kDownCells / kWarps, NT = kDownTiles;
+    constexpr int kBytes = kF8 ? 1 : 2, NT = kDownTiles, V = 2 * Tokens<kF8>::kPairs;
     constexpr bool kSplit = !kF8 && __is_same(TX, __nv_bfloat16);  // a as two bf16 numbers
-    static_assert(kWarps * MT * NT * 4 * 32 * 4 <= kDownCells * kCell && kCells % NT == 0 && kCells >= 2 * NT, "the sums meet where the pieces were");
+    static_assert(MT * NT * 4 * 32 * 4 <= kDownRing, "the sums meet where the pieces were");
     extern __shared__ __align__(128) uint8_t smem[];
-    Lists &l = *reinterpret_cast<Lists *>(smem + kDownCells * kCell);
+    Lists &l = *reinterpret_cast<Lists *>(smem + kWarps * kDownRing);
     float *const red = reinterpret_cast<float *>(smem);  // [warp][tokens' tile][tile][4][lane]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     route(a, l, false);
     const int from = (int)((int64_t)a.d * blockIdx.x / gridDim.x), to = (int)((int64_t)a.d * (blockIdx.x + 1) / gridDim.x);
     const int row_bytes = a.inner * kBytes, pieces = (row_bytes + 127) / 128, all = l.n * pieces;
     const int row_blocks = (a.d + kFp8Block - 1) / kFp8Block, col_blocks = (a.inner + kFp8Block - 1) / kFp8Block;
-    const int64_t matrix = (int64_t)a.d * row_bytes;
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kCells * kCell + lane * 16);
+    const int64_t matrix = (int64_t)a.d * row_bytes, tile_bytes = 8 * (int64_t)row_bytes;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kDownRing + lane * 16);
     bool waited = false;
     for (int base = from & ~7; base < to; base += 8 * NT) {
         const int tiles = (to - base + 7) / 8 < NT ? (to - base + 7) / 8 : NT;
-        int ahead = warp, ai = warp / pieces, ak = warp - ai * pieces, slot = 0;
-        const auto fetch = [&]() {  // a piece of every tile
-            const uint8_t *const m = ahead < all ? a.down + (int64_t)l.active[ai] * matrix : nullptr;
+        uint32_t rows = 0;  // which tiles have this lane's row
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int row = base + 8 * i + g;
-                if (m && i < tiles)
-                    load_piece(ring + (uint32_t)slot * kCell, m + (int64_t)row * row_bytes, row >= from && row < to, ak * 128 + t4 * 16, row_bytes);
-                if (++slot == kCells) slot = 0;
+        for (int i = 0; i < NT; ++i) rows |= (uint32_t)(base + 8 * i + g >= from && base + 8 * i + g < to) << i;
+        int ahead = warp, ai = warp / pieces, ak = warp - ai * pieces;
+        const auto fetch = [&](uint32_t to_step) {  // a step's pieces
+            if (ahead < all) {
+                const uint8_t *const p = a.down + (int64_t)l.active[ai] * matrix + (int64_t)(base + g) * row_bytes + ak * 128 + t4 * 16;
+                const bool first_half = ak * 128 + t4 * 16 < row_bytes, second_half = ak * 128 + t4 * 16 + 64 < row_bytes;
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    if (i < tiles) load_piece(to_step + (uint32_t)(i * kCell), p + i * tile_bytes, (rows >> i & 1u) && first_half, (rows >> i & 1u) && second_half);
             }
             cp_async_commit();
             ahead += kWarps, ak += kWarps;
             while (ak >= pieces) ak -= pieces, ++ai;
         };
-        constexpr int kDeep = kCells / NT;
 #pragma unroll
-        for (int c = 0; c < kDeep; ++c) fetch();
+        for (int s = 0; s < kDownDeep; ++s) fetch(ring + (uint32_t)(s * NT * kCell));
         if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's results are read from here on
         waited = true;
-        float acc[MT][NT][4];
+        float acc[MT][NT][4], odd[kF8 || !kSplit ? 1 : MT][NT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[m][i][k] = 0.0f;
-        int at = 0;  // the block of pieces in the ring
-        for (int b = warp, bi = warp / pieces, bk = warp - bi * pieces; b < all; b += kWarps) {
-            const int e = l.active[bi], first = l.first[bi], end = l.first[bi + 1];
-            cp_async_wait<kDeep - 1>();
+                for (int k = 0; k < 4; ++k) {
+                    acc[m][i][k] = 0.0f;
+                    if (kSplit) odd[kSplit ? m : 0][i][k] = 0.0f;
+                }
+        // this lane's two tokens of a tile of 16: their activations for the expert
+        const auto load_tokens = [&](int m, int i, int k, float4 (&raw)[2][V / 4]) {
+            const uint64_t tokens = l.tokens[i];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                if (r == 1 && a.T <= 8) break;
+                const int t = 16 * m + g + 8 * r;
+                const bool has = tokens >> t & 1u;
+                const float *from_a = a.a;
+                if (has) from_a += (int64_t)l.list[l.first[i] + __popcll(tokens & (((uint64_t)1 << t) - 1))] * a.inner;
+#pragma unroll
+                for (int q = 0; q < V / 4; ++q) {
+                    const int c = kF8 ? k * 128 + (q >> 2) * 64 + t4 * 16 + (q & 3) * 4 : k * 64 + (q >> 1) * 32 + t4 * 8 + (q & 1) * 4;
+                    raw[r][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (has && c < a.inner) raw[r][q] = __ldcg(reinterpret_cast<const float4 *>(from_a + c));
+                }
+            }
+        };
+        const auto load_scale = [&](int i, int k) {  // lane i: tile i's
+            return kF8 && lane < tiles ? a.down_scales.at(((int64_t)l.active[i] * row_blocks + (base + 8 * lane) / kFp8Block) * col_blocks + k) : 1.0f;
+        };
+        float4 raw[2][V / 4];
+        float scale = 1.0f;
+        int bi = warp / pieces, bk = warp - bi * pieces, step = 0;
+        if (warp < all) {
+            if (MT == 1) load_tokens(0, bi, bk, raw);
+            scale = load_scale(bi, bk);
+        }
+        for (int b = warp; b < all; b += kWarps) {
+            const float scales = scale;
+            int ni = bi, nk = bk + kWarps;
+            while (nk >= pieces) nk -= pieces, ++ni;
+            const uint64_t tokens = l.tokens[bi];
+            const uint32_t here = ring + (uint32_t)(step * NT * kCell);
+            cp_async_wait<kDownDeep - 1>();
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                // this lane's two tokens: their entries for this expert
-                int entry[2] = {-1, -1};
-                bool some = false;
-                for (int j = first; j < end; ++j) {
-                    const int id = l.list[j], tok = id / a.top;
-                    some |= tok >> 4 == m;
-                    if (tok == 16 * m + g) entry[0] = id;
-                    if (tok == 16 * m + g + 8) entry[1] = id;
+                if (MT > 1) {
+                    if (!(tokens >> (16 * m) & 0xffffu)) continue;
+                    load_tokens(m, bi, bk, raw);
                 }
-                if (!some) continue;
                 Tokens<kF8> tok, low;
                 tok.clear();
                 if constexpr (kSplit) low.clear();
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    constexpr int V = 2 * Tokens<kF8>::kPairs;
+                    if (r == 1 && a.T <= 8) break;
                     float f[V];
 #pragma unroll
-                    for (int q = 0; q < V / 4; ++q) {
-                        const int c = kF8 ? bk * 128 + (q >> 2) * 64 + t4 * 16 + (q & 3) * 4 : bk * 64 + (q >> 1) * 32 + t4 * 8 + (q & 1) * 4;
-                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (entry[r] >= 0 && c < a.inner) v = __ldcg(reinterpret_cast<const float4 *>(a.a + (int64_t)entry[r] * a.inner + c));
-                        f[4 * q] = v.x, f[4 * q + 1] = v.y, f[4 * q + 2] = v.z, f[4 * q + 3] = v.w;
-                    }
+                    for (int q = 0; q < V / 4; ++q) f[4 * q] = raw[r][q].x, f[4 * q + 1] = raw[r][q].y, f[4 * q + 2] = raw[r][q].z, f[4 * q + 3] = raw[r][q].w;
                     if constexpr (kSplit) {
 #pragma unroll
                         for (int q = 0; q < V / 2; ++q) {
@@ -538,31 +617,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_moe_down(const Args a) {
                         tok.put_scaled(r, f);
                     }
                 }
+                if (MT == 1 && b + kWarps < all) {
+                    load_tokens(0, ni, nk, raw);
+                    scale = load_scale(ni, nk);
+                }
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     if (i >= tiles) continue;
-                    const Piece p = read_piece(ring + (uint32_t)(at * NT + i) * kCell);
+                    const Piece p = read_piece(here + (uint32_t)(i * kCell));
                     if constexpr (kSplit) {
-                        multiply<TX, false>(acc[m][i], tok, p);
-                        multiply<TX, false>(acc[m][i], low, p);
+                        multiply<TX, false>(acc[m][i], odd[kSplit ? m : 0][i], tok, p);
+                        multiply<TX, false>(acc[m][i], odd[kSplit ? m : 0][i], low, p);
                     } else {
-                        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        multiply<__half, kF8>(part, tok, p);
-                        float s = 1.0f;
-                        if constexpr (kF8) s = a.down_scales.at(((int64_t)e * row_blocks + (base + 8 * i) / kFp8Block) * col_blocks + bk);
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float u = s * tok.unit[r];
-                            acc[m][i][2 * r] = fmaf(part[2 * r], u, acc[m][i][2 * r]);
-                            acc[m][i][2 * r + 1] = fmaf(part[2 * r + 1], u, acc[m][i][2 * r + 1]);
-                        }
+                        multiply_scaled<kF8>(acc[m][i], tok, p, __shfl_sync(0xffffffffu, scales, i));
                     }
                 }
             }
-            if (++at == kDeep) at = 0;
-            fetch();
-            bk += kWarps;
-            while (bk >= pieces) bk -= pieces, ++bi;
+            if (MT > 1 && b + kWarps < all) scale = load_scale(ni, nk);
+            bi = ni, bk = nk;
+            if (++step == kDownDeep) step = 0;
+            fetch(here);
         }
         cp_async_wait<0>();
         __syncthreads();
@@ -571,15 +645,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_moe_down(const Args a) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) red[(((warp * MT + m) * NT + i) * 4 + k) * 32 + lane] = acc[m][i][k];
+                for (int k = 0; k < 4; ++k)
+                    red[(((warp * MT + m) * NT + i) * 4 + k) * 32 + lane] = acc[m][i][k] + (kSplit ? odd[kSplit ? m : 0][i][k] : 0.0f);
         __syncthreads();
-        const int warps = all < kWarps ? all : kWarps;
+        const int meet = all < kWarps ? all : kWarps;
         for (int o = threadIdx.x; o < MT * NT * 128; o += 32 * kWarps) {
             const int m = o / (NT * 128), i = o / 128 % NT, k = o / 32 % 4;  // (o % 32 is this lane)
             const int tok = 16 * m + g + 8 * (k >> 1), row = base + 8 * i + 2 * t4 + (k & 1);
             if (tok >= a.T || row < from || row >= to) continue;
             float v = 0.0f;
-            for (int w = 0; w < warps; ++w) v += red[w * MT * NT * 128 + o];
+            for (int w = 0; w < meet; ++w) v += red[w * MT * NT * 128 + o];
             static_cast<TX *>(a.y)[(int64_t)tok * a.ys + row] = from_f<TX>(v);
         }
         __syncthreads();
@@ -587,8 +662,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_moe_down(const Args a) {
 }
 
 constexpr int kDevices = 64;
-constexpr int kUpSmem = kUpWarps * kUpCells * kCell + kUpWarps * kUpTiles * 4 * 32 * 4 + (int)sizeof(Lists);
-constexpr int kDownSmem = kDownCells * kCell + (int)sizeof(Lists);
+constexpr int kUpSmem = kWarps * kUpRing + 2 * kWarps * 2 * kUpPairs * 128 * 4 + (int)sizeof(Lists);
+constexpr int kDownSmem = kWarps * kDownRing + (int)sizeof(Lists);
 static_assert(kUpSmem <= 227 * 1024 && kDownSmem <= 227 * 1024, "an SM's memory");
 
 // SMs of the current device; once per device allows the kernel its shared memory.
@@ -606,10 +681,10 @@ cudaError_t allow(K k, int smem, std::atomic<int> (&sms)[kDevices], int &n) {
     return cudaSuccess;
 }
 
-template <typename TX, bool kF8, int MT, int kWarps>
+template <typename TX, bool kF8, int MT>
 cudaError_t start_down(const Args &a, cudaStream_t s) {
     static std::atomic<int> sms[kDevices];
-    const auto k = k_moe_down<TX, kF8, MT, kWarps>;
+    const auto k = k_moe_down<TX, kF8, MT>;
     int n = 0;
     const cudaError_t e = allow(k, kDownSmem, sms, n);
     if (e != cudaSuccess) return e;
@@ -630,11 +705,11 @@ cudaError_t start(const Args &a, cudaStream_t s) {
     int n = 0;
     cudaError_t e = allow(k, kUpSmem, sms, n);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)n, 32 * kUpWarps, kUpSmem, s>>>(a);
+    k<<<(unsigned)n, 32 * kWarps, kUpSmem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (a.T <= 16) return start_down<TX, kF8, 1, 16>(a, s);
-    if (a.T <= 32) return start_down<TX, kF8, 2, 16>(a, s);
-    return start_down<TX, kF8, 4, 8>(a, s);
+    if (a.T <= 16) return start_down<TX, kF8, 1>(a, s);
+    if (a.T <= 32) return start_down<TX, kF8, 2>(a, s);
+    return start_down<TX, kF8, 4>(a, s);
 }
 
 }  // namespace moe
