@@ -33,10 +33,10 @@ namespace moe {
 
 constexpr int kMaxTokens = 64, kMaxTop = 16, kMaxExperts = 1024, kMaxEntries = kMaxTokens * kMaxTop;
 constexpr int kCell = 1024;       // bytes of a piece: 8 rows of 128 bytes
-constexpr int kWarps = 8;
-constexpr int kUpPairs = 4, kUpDeep = 2;      // pairs of row tiles (of G and of U) of a unit; steps whose pieces are under way
-constexpr int kDownTiles = 6, kDownDeep = 4;  // row tiles of a pass; steps whose pieces are under way
-constexpr int kUpRing = kUpDeep * kUpPairs * 2 * kCell, kDownRing = kDownDeep * kDownTiles * kCell;  // of a warp
+constexpr int kUpWarps = 16, kUpPairs = 4;  // pairs of row tiles (of G and of U) of a unit
+constexpr int kDownPairs = 3;               // pairs of row tiles of a pass
+constexpr int kUpRing = kUpPairs * 2 * kCell, kDownRing = kDownPairs * 2 * kCell;  // of a warp: the pieces of a step
+constexpr int kStaged = 272;                // bytes between staged tokens (16 more than they have: no two of a read meet in a bank)
 
 struct Args {
     const void *x;
@@ -62,7 +62,7 @@ struct Lists {
     uint16_t list[kMaxEntries];      // entries by expert
     uint16_t active[kMaxExperts];    // experts with entries, ascending
     uint16_t first[kMaxExperts + 1]; // of the i-th of these: its first place in `list`
-    uint16_t tiles[kMaxExperts + 1]; // ... and the tiles of 16 entries of those before it
+    uint16_t tiles[kMaxExperts + 1]; // ... and the tiles of 8 entries of those before it
     uint64_t tokens[kMaxExperts];    // ... its tokens, as bits
     int count[kMaxExperts];
     int n;                           // how many experts have entries
@@ -151,7 +151,7 @@ __device__ __forceinline__ void route(Args a, Lists &l, bool write) {
     __syncthreads();
     const int entries = a.T * a.top;
     if (warp == 0) {
-        // an expert's entries in their order (all blocks have to agree on which tile of 16 has one)
+        // an expert's entries in their order (all blocks have to agree on which tile of 8 has one)
         for (int i0 = 0; i0 < entries; i0 += 32) {
             const int i = i0 + lane, e = i < entries ? l.id[i] : -1;
             const uint32_t same = __match_any_sync(0xffffffffu, e), before = same & ((1u << lane) - 1u);
@@ -163,7 +163,7 @@ __device__ __forceinline__ void route(Args a, Lists &l, bool write) {
         int n = 0, at = 0, tiles = 0;
         for (int e0 = 0; e0 < a.experts; e0 += 32) {
             const int e = e0 + lane, c = e < a.experts ? l.count[e] : 0;
-            int before = c, m = (c + 15) / 16;
+            int before = c, m = (c + 7) / 8;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int u = __shfl_up_sync(0xffffffffu, before, o), v = __shfl_up_sync(0xffffffffu, m, o);
@@ -172,7 +172,7 @@ __device__ __forceinline__ void route(Args a, Lists &l, bool write) {
             const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
             if (c > 0) {
                 const int i = n + __popc(some & ((1u << lane) - 1u));
-                l.active[i] = (uint16_t)e, l.first[i] = (uint16_t)(at + before - c), l.tiles[i] = (uint16_t)(tiles + m - (c + 15) / 16);
+                l.active[i] = (uint16_t)e, l.first[i] = (uint16_t)(at + before - c), l.tiles[i] = (uint16_t)(tiles + m - (c + 7) / 8);
                 l.count[e] = at + before - c;  // from here on: the first place in `list`
             }
             n += __popc(some);
@@ -220,139 +220,115 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// The tokens' side of the MMAs over a piece: rows lane / 4 and + 8 of 16, this lane's
-// values of k in pairs.  kF8: 16 of them per 16 bytes of codes (32 a piece), else 8 (16).
+// The tokens' side of the MMAs over a piece: token lane / 4 of 8, this lane's values of k in
+// pairs.  kF8: 16 of them per 16 bytes of codes (32 a piece), else 8 (16).
 template <bool kF8>
-struct Tokens {
-    static constexpr int kPairs = kF8 ? 16 : 8;  // pairs of a row's values in a piece
-    uint32_t v[2][kPairs];
-    float unit[2];  // what a row's values were divided by
+constexpr int kPairsOf = kF8 ? 16 : 8;
 
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            unit[r] = 1.0f;
-#pragma unroll
-            for (int i = 0; i < kPairs; ++i) v[r][i] = 0;
-        }
-    }
-    // A row's values -> fp16, the largest (over the piece: the lanes of four) brought to
-    // [2^14, 2^15) by a power of two: 11 bits of each value, of small ones 2^-39 of the largest.
-    // Of that largest: the power of two, and what it undoes.
-    __device__ __forceinline__ float power(int r, float amax) {
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        int b = (int)(__float_as_uint(amax) >> 23);
-        b = b < 15 ? 15 : b;
-        unit[r] = __uint_as_float((uint32_t)(b - 14) << 23);
-        return __uint_as_float((uint32_t)(268 - b) << 23);
-    }
-    __device__ __forceinline__ void put_scaled(int r, const float (&f)[2 * kPairs]) {
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 2 * kPairs; ++i) amax = fmaxf(amax, fabsf(f[i]));
-        const float m = power(r, amax);
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) v[r][i] = half2_of(f[2 * i] * m, f[2 * i + 1] * m);
-    }
-    // ... of bf16 values in pairs (the product with the power is exact in bf16)
-    __device__ __forceinline__ void put_scaled(int r, const uint32_t (&w)[kPairs]) {
-        const auto pair_of = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
-        __nv_bfloat162 top = __habs2(pair_of(w[0]));
-#pragma unroll
-        for (int i = 1; i < kPairs; ++i) top = __hmax2(top, __habs2(pair_of(w[i])));
-        const float2 t = __bfloat1622float2(top);
-        const __nv_bfloat162 m = __float2bfloat162_rn(power(r, fmaxf(fmaxf(t.x, t.y), 0.0f)));
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-            const __nv_bfloat162 p = __hmul2(pair_of(w[i]), m);
-            const uint32_t u = *reinterpret_cast<const uint32_t *>(&p);
-            v[r][i] = half2_of(bf16lo(u), bf16hi(u));
-        }
-    }
-};
+// fp16 copies of a token's values over a piece carry a power of two that brings the
+// largest to [2^14, 2^15): 11 bits of each value, of small ones 2^-39 of the largest.  Of that
+// largest: the power, and what undoes it.
+__device__ __forceinline__ float power_of(float amax, float &unit) {
+    int b = (int)(__float_as_uint(amax) >> 23);
+    b = b < 15 ? 15 : b;
+    unit = __uint_as_float((uint32_t)(b - 14) << 23);
+    return __uint_as_float((uint32_t)(268 - b) << 23);
+}
 
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     if constexpr (__is_same(T, __nv_bfloat16)) mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
     else mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
 }
-// even, odd += a piece's products, every second step of k each (two chains of MMAs)
-template <typename T, bool kF8>
-__device__ __forceinline__ void multiply(float (&even)[4], float (&odd)[4], const Tokens<kF8> &x, const Piece &p) {
-#pragma unroll
-    for (int i = 0; i < Tokens<kF8>::kPairs; i += 2) {
-        uint32_t b0, b1;
-        if constexpr (kF8) widen(p.w[i / 2], b0, b1);
-        else b0 = p.w[i], b1 = p.w[i + 1];
-        mma<T>(i & 2 ? odd : even, x.v[0][i], x.v[1][i], x.v[0][i + 1], x.v[1][i + 1], b0, b1);
-    }
-}
-// acc += a piece's products, scaled: by s (the block's) and what the tokens were divided by
+// A pair of tiles (rows 0-7 of the MMA, rows 8-15) as its operand: four registers for each two
+// pairs of k.
 template <bool kF8>
-__device__ __forceinline__ void multiply_scaled(float (&acc)[4], const Tokens<kF8> &x, const Piece &p, float s) {
+struct Rows16 {
+    uint32_t a[kPairsOf<kF8> / 2][4];
+    __device__ __forceinline__ Rows16(const Piece &p, const Piece &q) {
+#pragma unroll
+        for (int i = 0; i < kPairsOf<kF8> / 2; ++i) {
+            if constexpr (kF8) widen(p.w[i], a[i][0], a[i][2]), widen(q.w[i], a[i][1], a[i][3]);
+            else a[i][0] = p.w[2 * i], a[i][2] = p.w[2 * i + 1], a[i][1] = q.w[2 * i], a[i][3] = q.w[2 * i + 1];
+        }
+    }
+};
+// even, odd += their products with the tokens, every second step of k each (two chains of MMAs)
+template <typename T, bool kF8>
+__device__ __forceinline__ void multiply(float (&even)[4], float (&odd)[4], const Rows16<kF8> &w, const uint32_t (&x)[kPairsOf<kF8>]) {
+#pragma unroll
+    for (int i = 0; i < kPairsOf<kF8> / 2; ++i) mma<T>(i & 1 ? odd : even, w.a[i][0], w.a[i][1], w.a[i][2], w.a[i][3], x[2 * i], x[2 * i + 1]);
+}
+// acc += ..., times the scales of the two tiles' blocks and what undoes the tokens' powers of two
+template <bool kF8>
+__device__ __forceinline__ void multiply_scaled(float (&acc)[4], const Rows16<kF8> &w, const uint32_t (&x)[kPairsOf<kF8>], float s0,
+                                                float s1, const float (&unit)[2]) {
     float even[4] = {0.0f, 0.0f, 0.0f, 0.0f}, odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    multiply<__half, kF8>(even, odd, x, p);
-    const float u0 = s * x.unit[0], u1 = s * x.unit[1];
-    acc[0] = fmaf(even[0] + odd[0], u0, acc[0]), acc[1] = fmaf(even[1] + odd[1], u0, acc[1]);
-    acc[2] = fmaf(even[2] + odd[2], u1, acc[2]), acc[3] = fmaf(even[3] + odd[3], u1, acc[3]);
+    multiply<__half, kF8>(even, odd, w, x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = fmaf(even[k] + odd[k], (k < 2 ? s0 : s1) * unit[k & 1], acc[k]);
 }
 
 // ------------------------------------------------------------ G and U
-// A unit: up to 32 rows (four tiles of 8) of one expert's G and U, for up to 16 entries.
+// A unit: up to 32 rows (four tiles of 8) of one expert's G and U, for up to 8 entries.  An expert's
+// rows are dealt out by what they cost, its number of such tiles of entries; these follow
+// one another for the same rows, whose weights then come from L2.
 struct Unit {
-    int i, m, row, left;  // the expert (in `active`), tile of entries, next row; rows left of this block's
-    int lo, hi;           // the unit's rows
-    __device__ __forceinline__ bool next(const Args &a) {
-        if (left <= 0) return false;
-        lo = row, hi = (lo & ~7) + 8 * kUpPairs;
-        if (hi > a.inner) hi = a.inner;
-        if (hi - lo > left) hi = lo + left;
-        left -= hi - lo, row = hi;
-        return true;
-    }
-    // (after the unit's expert and tile have been looked at)
-    __device__ __forceinline__ void step(const Args &a, const Lists &l) {
-        if (row < a.inner) return;
-        row = 0;
-        if (++m >= l.tiles[i + 1] - l.tiles[i]) m = 0, ++i;
-    }
-};
-
-// Steps: a unit's pieces, one of 128 bytes of every row at a time, go round the warps.
-template <typename TX, bool kF8>
-__global__ void __launch_bounds__(32 * kWarps, 1) k_moe_up(const Args a) {
-    constexpr int kBytes = kF8 ? 1 : 2, kOut = kUpPairs * 128;  // kOut: rows by entries of a unit
-    constexpr int kVecs = kF8 ? 4 : 2;  // 16-byte loads of a token's values of a piece
-    extern __shared__ __align__(128) uint8_t smem[];
-    float *const red = reinterpret_cast<float *>(smem + kWarps * kUpRing);  // [2][warp][G, U][kOut]
-    Lists &l = *reinterpret_cast<Lists *>(red + 2 * kWarps * 2 * kOut);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    route(a, l, true);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t all = (int64_t)l.tiles[l.n] * a.inner;
-    const int64_t from = all * blockIdx.x / gridDim.x, to = all * (blockIdx.x + 1) / gridDim.x;
-    if (from == to) return;
-    Unit first;
-    {
-        const int tile = (int)(from / a.inner);
-        int lo = 0, hi = l.n;  // the expert whose tiles this one is of
+    int i, m, lo, hi;  // the expert (in `active`), tile of entries, rows
+    int last, end;     // of this block: the last expert and the end of its rows
+    __device__ __forceinline__ int limit(const Args &a) const { return i == last ? end : a.inner; }
+    // The place of the weighted row `at`: the expert, and its row.
+    static __device__ __forceinline__ void place(const Args &a, const Lists &l, int64_t at, int &i, int &row) {
+        const int tile = (int)(at / a.inner);
+        int lo = 0, hi = l.n;
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (l.tiles[mid] <= tile) lo = mid;
             else hi = mid;
         }
-        first.i = lo, first.m = tile - l.tiles[lo], first.row = (int)(from - (int64_t)tile * a.inner), first.left = (int)(to - from);
+        if (tile >= l.tiles[l.n]) i = l.n, row = 0;
+        else i = lo, row = (int)((at - (int64_t)l.tiles[lo] * a.inner) / (l.tiles[lo + 1] - l.tiles[lo]));
     }
+    __device__ __forceinline__ bool chunk(const Args &a, int row) {  // the unit that begins with a row, if there is one
+        while (i < last && row >= a.inner) ++i, row = 0;
+        if (i > last || (i == last && row >= end)) return false;
+        m = 0, lo = row, hi = (row & ~7) + 8 * kUpPairs;
+        if (hi > limit(a)) hi = limit(a);
+        return true;
+    }
+    __device__ __forceinline__ bool next(const Args &a, const Lists &l) {
+        if (++m < l.tiles[i + 1] - l.tiles[i]) return true;
+        return chunk(a, hi);
+    }
+};
+
+// Steps: a unit's pieces, one of 128 bytes of every row at a time, go round the warps.
+template <typename TX, bool kF8>
+__global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
+    constexpr int kBytes = kF8 ? 1 : 2, W = kUpWarps, kSums = kUpPairs * 128;
+    constexpr int kPairs = kPairsOf<kF8>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float *const red = reinterpret_cast<float *>(smem + W * kUpRing);  // [2][warp][pair][4][lane]
+    Lists &l = *reinterpret_cast<Lists *>(red + 2 * W * kSums);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    route(a, l, true);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t all = (int64_t)l.tiles[l.n] * a.inner;
+    if (all == 0) return;
+    Unit u;
+    int row0;
+    Unit::place(a, l, all * (blockIdx.x + 1) / gridDim.x, u.last, u.end);
+    Unit::place(a, l, all * blockIdx.x / gridDim.x, u.i, row0);
+    if (!u.chunk(a, row0)) return;
     const int row_bytes = a.d * kBytes, pieces = (row_bytes + 127) / 128;
     const int64_t matrix = (int64_t)a.inner * row_bytes;  // G or U of an expert
-    const auto begin = [&](int u) {  // the warp's first piece of unit u
-        return (warp + u * (kWarps - pieces % kWarps)) % kWarps;
+    const auto begin = [&](int n) {  // the warp's first piece of the n-th unit
+        return (warp + n * (W - pieces % W)) % W;
     };
 
-    // copies run kUpDeep steps ahead
-    Unit ahead = first;
-    bool more = ahead.next(a);
+    // copies run a step ahead
+    Unit ahead = u;
+    bool more = true;
     int au = 0, ak = warp;
     uint32_t rows = 0;                // which of the unit's pairs of tiles have this lane's row
     const uint8_t *lane_row = a.up;   // this lane's row of the first tile
@@ -365,15 +341,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_moe_up(const Args a) {
     };
     const auto settle = [&]() {  // to the unit that has a piece for this warp
         while (more && ak >= pieces) {
-            ahead.step(a, l);
-            more = ahead.next(a);
+            more = ahead.next(a, l);
             if (more) aim(), ak = begin(++au);
         }
         if (!more) rows = 0;
     };
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kUpRing + lane * 16);
     const int64_t tile_bytes = 8 * (int64_t)row_bytes;
-    const auto fetch = [&](uint32_t to, int j) {
+    const auto fetch = [&](int j) {
+        const uint32_t to = ring + (uint32_t)(j * 2 * kCell);
         const uint8_t *const p = lane_row + (int64_t)j * tile_bytes + ak * 128;
         const bool there = rows >> j & 1u, first_half = there && ak * 128 + t4 * 16 < row_bytes,
                    second_half = there && ak * 128 + t4 * 16 + 64 < row_bytes;
@@ -381,280 +357,314 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_moe_up(const Args a) {
         load_piece(to + kCell, p + matrix, first_half, second_half);
         cp_async_commit();
     };
-    if (more) aim();
+    aim();
     settle();
 #pragma unroll
-    for (int s = 0; s < kUpDeep; ++s) {
-#pragma unroll
-        for (int j = 0; j < kUpPairs; ++j) fetch(ring + (uint32_t)((s * kUpPairs + j) * 2 * kCell), j);
-        ak += kWarps;
-        settle();
-    }
+    for (int j = 0; j < kUpPairs; ++j) fetch(j);
+    ak += W;
+    settle();
 
     const int row_blocks = (a.inner + kFp8Block - 1) / kFp8Block, col_blocks = (a.d + kFp8Block - 1) / kFp8Block;
-    uint32_t at = ring;  // the step's place
-    int buf = 0;
-    Unit u = first;
-    for (int un = 0; u.next(a); u.step(a, l), ++un, buf ^= 1) {
-        // this lane's two tokens
-        const int e = l.active[u.i], entry0 = l.first[u.i] + 16 * u.m, end = l.first[u.i + 1];
-        const bool second = entry0 + 8 < end;  // (of the warp: whether there are more than eight)
-        const TX *x[2];
-        bool has[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            has[r] = entry0 + g + 8 * r < end;
-            x[r] = static_cast<const TX *>(a.x) + (has[r] ? (int64_t)(l.list[entry0 + g + 8 * r] / a.top) * a.xs : 0);
-        }
+    int buf = 0, un = 0;
+    do {
+        // this lane's token
+        const int e = l.active[u.i], entry0 = l.first[u.i] + 8 * u.m, end = l.first[u.i + 1];
+        const bool has = entry0 + g < end;
+        const TX *const x = static_cast<const TX *>(a.x) + (has ? (int64_t)(l.list[entry0 + g] / a.top) * a.xs : 0);
         const int base = u.lo & ~7, tiles = (u.hi - base + 7) / 8;
         // lane 2 j + (0: G, 1: U) looks after the scale of pair j
         int64_t scale_at = 0;
         if (kF8 && lane < 2 * tiles)
             scale_at = (((int64_t)e * 2 + (lane & 1)) * row_blocks + (base + 8 * (lane >> 1)) / kFp8Block) * col_blocks;
-        uint4 raw[2][kVecs];
-        float scale = 1.0f;
-        const auto load_tokens = [&](int k) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int s = 0; s < kVecs; ++s) {
-                    const int c = kF8 ? k * 128 + (s >> 1) * 64 + t4 * 16 + (s & 1) * 8 : k * 64 + s * 32 + t4 * 8;
-                    raw[r][s] = make_uint4(0, 0, 0, 0);
-                    if (has[r] && c < a.d) raw[r][s] = __ldg(reinterpret_cast<const uint4 *>(x[r] + c));
-                }
-            if (kF8 && lane < 2 * tiles) scale = a.up_scales.at(scale_at + k);
-        };
-        float acc[kUpPairs][2][4], odd[kF8 ? 1 : kUpPairs][2][4];
+        float acc[kUpPairs][4], odd[kF8 ? 1 : kUpPairs][4];
 #pragma unroll
         for (int j = 0; j < kUpPairs; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    acc[j][h][k] = 0.0f;
-                    if (!kF8) odd[kF8 ? 0 : j][h][k] = 0.0f;
-                }
-        int k = begin(un);
-        if (k < pieces) load_tokens(k);
-        for (; k < pieces; k += kWarps) {
-            Tokens<kF8> tok;
-            tok.clear();
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                if (r == 1 && !second) break;
-                uint32_t w[Tokens<kF8>::kPairs];
-#pragma unroll
-                for (int s = 0; s < kVecs; ++s) w[4 * s] = raw[r][s].x, w[4 * s + 1] = raw[r][s].y, w[4 * s + 2] = raw[r][s].z, w[4 * s + 3] = raw[r][s].w;
-                if constexpr (kF8 && __is_same(TX, __nv_bfloat16)) {
-                    tok.put_scaled(r, w);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < Tokens<kF8>::kPairs; ++i) tok.v[r][i] = w[i];
-                }
+            for (int k = 0; k < 4; ++k) {
+                acc[j][k] = 0.0f;
+                if (!kF8) odd[kF8 ? 0 : j][k] = 0.0f;
             }
-            const float scales = scale;
-            if (k + kWarps < pieces) load_tokens(k + kWarps);
+        for (int k = begin(un); k < pieces; k += W) {
+            uint32_t tok[kPairs];
+            float unit[2] = {1.0f, 1.0f}, scale = 1.0f;
+            if (kF8 && lane < 2 * tiles) scale = a.up_scales.at(scale_at + k);
+#pragma unroll
+            for (int s = 0; s < kPairs / 4; ++s) {
+                const int c = kF8 ? k * 128 + (s >> 1) * 64 + t4 * 16 + (s & 1) * 8 : k * 64 + s * 32 + t4 * 8;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (has && c < a.d) v = __ldg(reinterpret_cast<const uint4 *>(x + c));
+                tok[4 * s] = v.x, tok[4 * s + 1] = v.y, tok[4 * s + 2] = v.z, tok[4 * s + 3] = v.w;
+            }
+            if constexpr (kF8 && __is_same(TX, __nv_bfloat16)) {  // (the product with a power of two is exact in bf16)
+                const auto pair_of = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+                __nv_bfloat162 top = __habs2(pair_of(tok[0]));
+#pragma unroll
+                for (int i = 1; i < kPairs; ++i) top = __hmax2(top, __habs2(pair_of(tok[i])));
+                const float2 t = __bfloat1622float2(top);
+                float amax = fmaxf(fmaxf(t.x, t.y), 0.0f), mine;
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                const __nv_bfloat162 m = __float2bfloat162_rn(power_of(amax, mine));
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    const __nv_bfloat162 p = __hmul2(pair_of(tok[i]), m);
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(&p);
+                    tok[i] = half2_of(bf16lo(w), bf16hi(w));
+                }
+                unit[0] = __shfl_sync(0xffffffffu, mine, 8 * t4), unit[1] = __shfl_sync(0xffffffffu, mine, 8 * t4 + 4);
+            }
 #pragma unroll
             for (int j = 0; j < kUpPairs; ++j) {
-                cp_async_wait<kUpDeep * kUpPairs - 1>();
-                const uint32_t here = at + (uint32_t)(j * 2 * kCell);
-                const Piece pg = read_piece(here), pu = read_piece(here + kCell);
+                cp_async_wait<kUpPairs - 1>();
+                const uint32_t here = ring + (uint32_t)(j * 2 * kCell);
+                const Rows16<kF8> w(read_piece(here), read_piece(here + kCell));
                 if (j < tiles) {
-                    if constexpr (kF8) {
-                        multiply_scaled<true>(acc[j][0], tok, pg, __shfl_sync(0xffffffffu, scales, 2 * j));
-                        multiply_scaled<true>(acc[j][1], tok, pu, __shfl_sync(0xffffffffu, scales, 2 * j + 1));
-                    } else {
-                        multiply<TX, false>(acc[j][0], odd[kF8 ? 0 : j][0], tok, pg);
-                        multiply<TX, false>(acc[j][1], odd[kF8 ? 0 : j][1], tok, pu);
-                    }
+                    if constexpr (kF8)
+                        multiply_scaled<true>(acc[j], w, tok, __shfl_sync(0xffffffffu, scale, 2 * j), __shfl_sync(0xffffffffu, scale, 2 * j + 1), unit);
+                    else
+                        multiply<TX, false>(acc[j], odd[kF8 ? 0 : j], w, tok);
                 }
-                fetch(here, j);
+                fetch(j);
             }
-            at = at == ring ? ring + kUpRing / kUpDeep : ring;
-            static_assert(kUpDeep == 2, "two places");
-            ak += kWarps;
+            ak += W;
             settle();
         }
         // the warps' sums meet
-        float *const mine = red + ((buf * kWarps + warp) * 2) * kOut + lane;
+        float *const sums = red + buf * W * kSums;
         if (begin(un) < pieces) {
 #pragma unroll
             for (int j = 0; j < kUpPairs; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (j < tiles && (q < 2 || second)) mine[h * kOut + (j * 4 + q) * 32] = acc[j][h][q] + (kF8 ? 0.0f : odd[kF8 ? 0 : j][h][q]);
+                for (int q = 0; q < 4; ++q)
+                    if (j < tiles) sums[warp * kSums + (j * 4 + q) * 32 + lane] = acc[j][q] + (kF8 ? 0.0f : odd[kF8 ? 0 : j][q]);
         }
         __syncthreads();  // (two buffers: the next unit's sums are written while a slow warp still reads these)
-        const int meet = pieces < kWarps ? pieces : kWarps, w0 = un * (pieces % kWarps) % kWarps;  // those that had a piece, in their order
-        for (int o = threadIdx.x; o < kOut; o += 32 * kWarps) {
-            const int j = o >> 7, q = o >> 5 & 3;  // (o % 32 is this lane)
-            const int row = base + 8 * j + 2 * t4 + (q & 1), entry = entry0 + g + 8 * (q >> 1);
-            if (j >= tiles || row < u.lo || row >= u.hi || entry >= end) continue;
-            float gate = 0.0f, up = 0.0f;
-            for (int i = 0, w = w0; i < meet; ++i) {
-                const float *from_w = red + ((buf * kWarps + w) * 2) * kOut + o;
-                gate += from_w[0], up += from_w[kOut];
-                if (++w == kWarps) w = 0;
+        const int meet = pieces < W ? pieces : W, w0 = un * (pieces % W) % W;  // those that had a piece, in their order
+        {
+            const int j = threadIdx.x >> 6, q = threadIdx.x >> 5 & 1;
+            const int row = base + 8 * j + g, entry = entry0 + 2 * t4 + q;
+            if (j < tiles && row >= u.lo && row < u.hi && entry < end) {
+                float gate = 0.0f, up = 0.0f;
+                for (int i = 0, w = w0; i < meet; ++i) {
+                    const float *const of_w = sums + w * kSums + (j * 4 + q) * 32 + lane;
+                    gate += of_w[0], up += of_w[64];
+                    if (++w == W) w = 0;
+                }
+                const int id = l.list[entry];
+                a.a[(int64_t)id * a.inner + row] = gate / (1.0f + expf(-gate)) * up * l.p[id];
             }
-            const int id = l.list[entry];
-            a.a[(int64_t)id * a.inner + row] = gate / (1.0f + expf(-gate)) * up * l.p[id];
         }
-    }
+        ++un, buf ^= 1;
+    } while (u.next(a, l));
     cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------ D
-// A block's rows of the output, in passes of kDownTiles tiles of 8; MT tiles of 16 tokens.
-// Steps: a piece of 128 bytes of every row of one expert; they go round the warps.
-template <typename TX, bool kF8, int MT>
-__global__ void __launch_bounds__(32 * kWarps, 1) k_moe_down(const Args a) {
-    constexpr int kBytes = kF8 ? 1 : 2, NT = kDownTiles, V = 2 * Tokens<kF8>::kPairs;
+// A block's rows of the output, in passes of kDownPairs pairs of tiles of 8; NB tiles of 8
+// tokens, looked at NI at a time.  Steps: a piece of 128 bytes of every row of one expert; they
+// go round the warps.  A warp stages the activations of the expert's tokens over the
+// step's piece, as the MMA wants them, in shared memory.
+template <int NB>
+constexpr int kDownWarps = NB > 2 ? 8 : 16;  // (the sums of 32 and 64 tokens take the registers of 16 warps)
+template <int NB>
+constexpr int kStage = 8 * (NB < 2 ? NB : 2) * (kStaged + 4);  // of a warp: staged tokens, what undoes their powers of two
+
+template <typename TX, bool kF8, int NB>
+__global__ void __launch_bounds__(32 * kDownWarps<NB>, 1) k_moe_down(const Args a) {
+    constexpr int kBytes = kF8 ? 1 : 2, W = kDownWarps<NB>, NP = kDownPairs, NI = NB < 2 ? NB : 2, kPairs = kPairsOf<kF8>;
+    constexpr int D = 16 / W;  // steps whose pieces are under way
+    constexpr int kEach = kPairs / 4;  // a lane's values of a token's piece: 4, or 2
     constexpr bool kSplit = !kF8 && __is_same(TX, __nv_bfloat16);  // a as two bf16 numbers
-    static_assert(MT * NT * 4 * 32 * 4 <= kDownRing, "the sums meet where the pieces were");
+    constexpr int kSums = NB * NP * 128;
     extern __shared__ __align__(128) uint8_t smem[];
-    Lists &l = *reinterpret_cast<Lists *>(smem + kWarps * kDownRing);
-    float *const red = reinterpret_cast<float *>(smem);  // [warp][tokens' tile][tile][4][lane]
+    float *const red = reinterpret_cast<float *>(smem);  // [warp][tokens' tile][pair][4][lane], where the pieces were
+    Lists &l = *reinterpret_cast<Lists *>(smem + 16 * kDownRing + 16 * kStage<2>);
+    static_assert(W * kSums * 4 <= 16 * kDownRing, "the sums meet where the pieces were");
+    static_assert(NB == NI ? D == 1 : D == 2, "a step's pieces are waited for one by one, or all at once");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     route(a, l, false);
     const int from = (int)((int64_t)a.d * blockIdx.x / gridDim.x), to = (int)((int64_t)a.d * (blockIdx.x + 1) / gridDim.x);
     const int row_bytes = a.inner * kBytes, pieces = (row_bytes + 127) / 128, all = l.n * pieces;
     const int row_blocks = (a.d + kFp8Block - 1) / kFp8Block, col_blocks = (a.inner + kFp8Block - 1) / kFp8Block;
     const int64_t matrix = (int64_t)a.d * row_bytes, tile_bytes = 8 * (int64_t)row_bytes;
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kDownRing + lane * 16);
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * D * kDownRing + lane * 16);
+    uint8_t *const staged = smem + 16 * kDownRing + warp * kStage<NB>;
+    float *const units = reinterpret_cast<float *>(staged + 8 * NI * kStaged);
     bool waited = false;
-    for (int base = from & ~7; base < to; base += 8 * NT) {
-        const int tiles = (to - base + 7) / 8 < NT ? (to - base + 7) / 8 : NT;
+    for (int base = from & ~7; base < to; base += 16 * NP) {
+        const int tiles = (to - base + 7) / 8 < 2 * NP ? (to - base + 7) / 8 : 2 * NP;
         uint32_t rows = 0;  // which tiles have this lane's row
 #pragma unroll
-        for (int i = 0; i < NT; ++i) rows |= (uint32_t)(base + 8 * i + g >= from && base + 8 * i + g < to) << i;
+        for (int i = 0; i < 2 * NP; ++i) rows |= (uint32_t)(base + 8 * i + g >= from && base + 8 * i + g < to) << i;
         int ahead = warp, ai = warp / pieces, ak = warp - ai * pieces;
-        const auto fetch = [&](uint32_t to_step) {  // a step's pieces
-            if (ahead < all) {
-                const uint8_t *const p = a.down + (int64_t)l.active[ai] * matrix + (int64_t)(base + g) * row_bytes + ak * 128 + t4 * 16;
-                const bool first_half = ak * 128 + t4 * 16 < row_bytes, second_half = ak * 128 + t4 * 16 + 64 < row_bytes;
+        const uint8_t *lane_row = a.down;
+        uint32_t there = 0;
+        const auto aim = [&]() {
+            there = 0;
+            if (ahead >= all) return;
+            there = rows;
+            lane_row = a.down + (int64_t)l.active[ai] * matrix + (int64_t)(base + g) * row_bytes + ak * 128 + t4 * 16;
+        };
+        uint32_t place = ring;  // the step's
+        const auto fetch = [&](int j) {
+            const uint32_t to_pair = place + (uint32_t)(j * 2 * kCell);
+            const bool first_half = ak * 128 + t4 * 16 < row_bytes, second_half = ak * 128 + t4 * 16 + 64 < row_bytes;
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    if (i < tiles) load_piece(to_step + (uint32_t)(i * kCell), p + i * tile_bytes, (rows >> i & 1u) && first_half, (rows >> i & 1u) && second_half);
+            for (int h = 0; h < 2; ++h) {
+                const bool is = there >> (2 * j + h) & 1u;
+                load_piece(to_pair + h * kCell, lane_row + (2 * j + h) * tile_bytes, is && first_half, is && second_half);
             }
             cp_async_commit();
-            ahead += kWarps, ak += kWarps;
-            while (ak >= pieces) ak -= pieces, ++ai;
         };
+        const auto advance = [&]() {
+            ahead += W, ak += W;
+            while (ak >= pieces) ak -= pieces, ++ai;
+            aim();
+            if (D == 2) place = place == ring ? ring + kDownRing : ring;
+        };
+        aim();
 #pragma unroll
-        for (int s = 0; s < kDownDeep; ++s) fetch(ring + (uint32_t)(s * NT * kCell));
+        for (int s = 0; s < D; ++s) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) fetch(j);
+            advance();
+        }
         if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's results are read from here on
         waited = true;
-        float acc[MT][NT][4], odd[kF8 || !kSplit ? 1 : MT][NT][4];
+        float acc[NB][NP][4], odd[kSplit ? NB : 1][NP][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < NB; ++m)
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int j = 0; j < NP; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    acc[m][i][k] = 0.0f;
-                    if (kSplit) odd[kSplit ? m : 0][i][k] = 0.0f;
+                    acc[m][j][k] = 0.0f;
+                    if (kSplit) odd[kSplit ? m : 0][j][k] = 0.0f;
                 }
-        // this lane's two tokens of a tile of 16: their activations for the expert
-        const auto load_tokens = [&](int m, int i, int k, float4 (&raw)[2][V / 4]) {
-            const uint64_t tokens = l.tokens[i];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                if (r == 1 && a.T <= 8) break;
-                const int t = 16 * m + g + 8 * r;
-                const bool has = tokens >> t & 1u;
-                const float *from_a = a.a;
-                if (has) from_a += (int64_t)l.list[l.first[i] + __popcll(tokens & (((uint64_t)1 << t) - 1))] * a.inner;
-#pragma unroll
-                for (int q = 0; q < V / 4; ++q) {
-                    const int c = kF8 ? k * 128 + (q >> 2) * 64 + t4 * 16 + (q & 3) * 4 : k * 64 + (q >> 1) * 32 + t4 * 8 + (q & 1) * 4;
-                    raw[r][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (has && c < a.inner) raw[r][q] = __ldcg(reinterpret_cast<const float4 *>(from_a + c));
-                }
-            }
-        };
-        const auto load_scale = [&](int i, int k) {  // lane i: tile i's
-            return kF8 && lane < tiles ? a.down_scales.at(((int64_t)l.active[i] * row_blocks + (base + 8 * lane) / kFp8Block) * col_blocks + k) : 1.0f;
-        };
-        float4 raw[2][V / 4];
-        float scale = 1.0f;
-        int bi = warp / pieces, bk = warp - bi * pieces, step = 0;
-        if (warp < all) {
-            if (MT == 1) load_tokens(0, bi, bk, raw);
-            scale = load_scale(bi, bk);
-        }
-        for (int b = warp; b < all; b += kWarps) {
-            const float scales = scale;
-            int ni = bi, nk = bk + kWarps;
-            while (nk >= pieces) nk -= pieces, ++ni;
+        int bi = warp / pieces, bk = warp - bi * pieces;
+        for (int b = warp; b < all; b += W) {
             const uint64_t tokens = l.tokens[bi];
-            const uint32_t here = ring + (uint32_t)(step * NT * kCell);
-            cp_async_wait<kDownDeep - 1>();
+            const int first = l.first[bi], at = bk * (2 * kPairs * 4) + lane * kEach;
+            float scale = 1.0f;  // lane i: tile i's
+            if (kF8 && lane < tiles) scale = a.down_scales.at(((int64_t)l.active[bi] * row_blocks + (base + 8 * lane) / kFp8Block) * col_blocks + bk);
+            if (D == 2) cp_async_wait<NP>();
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (MT > 1) {
-                    if (!(tokens >> (16 * m) & 0xffffu)) continue;
-                    load_tokens(m, bi, bk, raw);
-                }
-                Tokens<kF8> tok, low;
-                tok.clear();
-                if constexpr (kSplit) low.clear();
+            for (int m0 = 0; m0 < NB; m0 += NI) {
+                const bool last = m0 + NI >= NB;
+                const uint32_t here = (uint32_t)(tokens >> (8 * m0)) & (NI == 2 ? 0xffffu : 0xffu);
+                if (!here && !last) continue;
+                // the expert's tokens among these, four at a time
+                __syncwarp();
+                int next = first + __popcll(tokens & (((uint64_t)1 << (8 * m0)) - 1));
+                for (uint32_t left = here; left;) {
+                    float v[4][kEach];
+                    uint32_t rest = left;
+                    int n = 0;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    if (r == 1 && a.T <= 8) break;
-                    float f[V];
+                    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                    for (int q = 0; q < V / 4; ++q) f[4 * q] = raw[r][q].x, f[4 * q + 1] = raw[r][q].y, f[4 * q + 2] = raw[r][q].z, f[4 * q + 3] = raw[r][q].w;
-                    if constexpr (kSplit) {
-#pragma unroll
-                        for (int q = 0; q < V / 2; ++q) {
-                            const uint32_t h = pack_bf16x2(f[2 * q], f[2 * q + 1]);
-                            tok.v[r][q] = h;
-                            low.v[r][q] = pack_bf16x2(f[2 * q] - bf16lo(h), f[2 * q + 1] - bf16hi(h));
+                        for (int q = 0; q < kEach; ++q) v[i][q] = 0.0f;
+                        if (!rest) continue;
+                        rest &= rest - 1, ++n;
+                        const float *const p = a.a + (int64_t)l.list[next + i] * a.inner + at;
+                        if (at >= a.inner) continue;
+                        if constexpr (kEach == 4) {
+                            const float4 f = __ldcg(reinterpret_cast<const float4 *>(p));
+                            v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+                        } else {
+                            const float2 f = __ldcg(reinterpret_cast<const float2 *>(p));
+                            v[i][0] = f.x, v[i][1] = f.y;
                         }
-                    } else {
-                        tok.put_scaled(r, f);
+                    }
+                    next += n;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (!left) continue;
+                        const int t = __ffs(left) - 1;
+                        left &= left - 1;
+                        uint8_t *const o = staged + t * kStaged;
+                        if constexpr (kSplit) {
+                            const uint32_t h = pack_bf16x2(v[i][0], v[i][1]);
+                            *reinterpret_cast<uint32_t *>(o + lane * 4) = h;
+                            *reinterpret_cast<uint32_t *>(o + 128 + lane * 4) = pack_bf16x2(v[i][0] - bf16lo(h), v[i][1] - bf16hi(h));
+                        } else {
+                            float amax = 0.0f, unit;
+#pragma unroll
+                            for (int q = 0; q < kEach; ++q) amax = fmaxf(amax, fabsf(v[i][q]));
+                            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+                            const float m = power_of(amax, unit);
+                            if constexpr (kEach == 4)
+                                *reinterpret_cast<uint2 *>(o + lane * 8) = make_uint2(half2_of(v[i][0] * m, v[i][1] * m), half2_of(v[i][2] * m, v[i][3] * m));
+                            else
+                                *reinterpret_cast<uint32_t *>(o + lane * 4) = half2_of(v[i][0] * m, v[i][1] * m);
+                            if (lane == 0) units[t] = unit;
+                        }
                     }
                 }
-                if (MT == 1 && b + kWarps < all) {
-                    load_tokens(0, ni, nk, raw);
-                    scale = load_scale(ni, nk);
+                __syncwarp();
+                uint32_t tok[NI][kPairs], low[kSplit ? NI : 1][kPairs];
+                float unit[NI][2];
+#pragma unroll
+                for (int m = 0; m < NI; ++m) {
+                    const bool has = here >> (8 * m + g) & 1u;
+                    const uint8_t *const p = staged + (8 * m + g) * kStaged;
+#pragma unroll
+                    for (int s = 0; s < kPairs / 4; ++s) {
+                        const int off = kF8 ? (s >> 1) * 128 + t4 * 32 + (s & 1) * 16 : s * 64 + t4 * 16;
+                        uint4 v = make_uint4(0, 0, 0, 0), w = v;
+                        if (has) {
+                            v = *reinterpret_cast<const uint4 *>(p + off);
+                            if (kSplit) w = *reinterpret_cast<const uint4 *>(p + 128 + off);
+                        }
+                        tok[m][4 * s] = v.x, tok[m][4 * s + 1] = v.y, tok[m][4 * s + 2] = v.z, tok[m][4 * s + 3] = v.w;
+                        if (kSplit) low[kSplit ? m : 0][4 * s] = w.x, low[kSplit ? m : 0][4 * s + 1] = w.y, low[kSplit ? m : 0][4 * s + 2] = w.z, low[kSplit ? m : 0][4 * s + 3] = w.w;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        unit[m][q] = !kSplit && (here >> (8 * m + 2 * t4 + q) & 1u) ? units[8 * m + 2 * t4 + q] : 0.0f;
                 }
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (i >= tiles) continue;
-                    const Piece p = read_piece(here + (uint32_t)(i * kCell));
-                    if constexpr (kSplit) {
-                        multiply<TX, false>(acc[m][i], odd[kSplit ? m : 0][i], tok, p);
-                        multiply<TX, false>(acc[m][i], odd[kSplit ? m : 0][i], low, p);
-                    } else {
-                        multiply_scaled<kF8>(acc[m][i], tok, p, __shfl_sync(0xffffffffu, scales, i));
+                for (int j = 0; j < NP; ++j) {
+                    if (D == 1) cp_async_wait<NP - 1>();
+                    if (here && 2 * j < tiles) {
+                        const uint32_t from_pair = place + (uint32_t)(j * 2 * kCell);
+                        const Rows16<kF8> w(read_piece(from_pair), read_piece(from_pair + kCell));
+                        const float s0 = __shfl_sync(0xffffffffu, scale, 2 * j), s1 = __shfl_sync(0xffffffffu, scale, 2 * j + 1);
+#pragma unroll
+                        for (int m = 0; m < NI; ++m) {
+                            if (!(here >> (8 * m) & 0xffu)) continue;
+                            if constexpr (kSplit) {
+                                multiply<TX, false>(acc[m0 + m][j], odd[kSplit ? m0 + m : 0][j], w, tok[m]);
+                                multiply<TX, false>(acc[m0 + m][j], odd[kSplit ? m0 + m : 0][j], w, low[kSplit ? m : 0]);
+                            } else {
+                                multiply_scaled<kF8>(acc[m0 + m][j], w, tok[m], s0, s1, unit[m]);
+                            }
+                        }
                     }
+                    if (last) fetch(j);
                 }
             }
-            if (MT > 1 && b + kWarps < all) scale = load_scale(ni, nk);
-            bi = ni, bk = nk;
-            if (++step == kDownDeep) step = 0;
-            fetch(here);
+            advance();
+            bk += W;
+            while (bk >= pieces) bk -= pieces, ++bi;
         }
         cp_async_wait<0>();
         __syncthreads();
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < NB; ++m)
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int j = 0; j < NP; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    red[(((warp * MT + m) * NT + i) * 4 + k) * 32 + lane] = acc[m][i][k] + (kSplit ? odd[kSplit ? m : 0][i][k] : 0.0f);
+                    red[warp * kSums + ((m * NP + j) * 4 + k) * 32 + lane] = acc[m][j][k] + (kSplit ? odd[kSplit ? m : 0][j][k] : 0.0f);
         __syncthreads();
-        const int meet = all < kWarps ? all : kWarps;
-        for (int o = threadIdx.x; o < MT * NT * 128; o += 32 * kWarps) {
-            const int m = o / (NT * 128), i = o / 128 % NT, k = o / 32 % 4;  // (o % 32 is this lane)
-            const int tok = 16 * m + g + 8 * (k >> 1), row = base + 8 * i + 2 * t4 + (k & 1);
+        const int meet = all < W ? all : W;
+        for (int o = threadIdx.x; o < kSums; o += 32 * W) {
+            const int m = o / (NP * 128), j = o / 128 % NP, k = o / 32 % 4;  // (o % 32 is this lane)
+            const int tok = 8 * m + 2 * t4 + (k & 1), row = base + 16 * j + 8 * (k >> 1) + g;
             if (tok >= a.T || row < from || row >= to) continue;
             float v = 0.0f;
-            for (int w = 0; w < meet; ++w) v += red[w * MT * NT * 128 + o];
+            for (int w = 0; w < meet; ++w) v += red[w * kSums + o];
             static_cast<TX *>(a.y)[(int64_t)tok * a.ys + row] = from_f<TX>(v);
         }
         __syncthreads();
@@ -662,8 +672,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_moe_down(const Args a) {
 }
 
 constexpr int kDevices = 64;
-constexpr int kUpSmem = kWarps * kUpRing + 2 * kWarps * 2 * kUpPairs * 128 * 4 + (int)sizeof(Lists);
-constexpr int kDownSmem = kWarps * kDownRing + (int)sizeof(Lists);
+constexpr int kUpSmem = kUpWarps * kUpRing + 2 * kUpWarps * kUpPairs * 128 * 4 + (int)sizeof(Lists);
+constexpr int kDownSmem = 16 * kDownRing + 16 * kStage<2> + (int)sizeof(Lists);
 static_assert(kUpSmem <= 227 * 1024 && kDownSmem <= 227 * 1024, "an SM's memory");
 
 // SMs of the current device; once per device allows the kernel its shared memory.
@@ -681,10 +691,10 @@ cudaError_t allow(K k, int smem, std::atomic<int> (&sms)[kDevices], int &n) {
     return cudaSuccess;
 }
 
-template <typename TX, bool kF8, int MT>
+template <typename TX, bool kF8, int NB>
 cudaError_t start_down(const Args &a, cudaStream_t s) {
     static std::atomic<int> sms[kDevices];
-    const auto k = k_moe_down<TX, kF8, MT>;
+    const auto k = k_moe_down<TX, kF8, NB>;
     int n = 0;
     const cudaError_t e = allow(k, kDownSmem, sms, n);
     if (e != cudaSuccess) return e;
@@ -693,7 +703,7 @@ cudaError_t start_down(const Args &a, cudaStream_t s) {
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     const int most = (a.d + 7) / 8;
-    cfg.gridDim = dim3((unsigned)(n < most ? n : most)), cfg.blockDim = dim3(32 * kWarps);
+    cfg.gridDim = dim3((unsigned)(n < most ? n : most)), cfg.blockDim = dim3(32 * kDownWarps<NB>);
     cfg.dynamicSmemBytes = kDownSmem, cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, a);
 }
@@ -705,11 +715,12 @@ cudaError_t start(const Args &a, cudaStream_t s) {
     int n = 0;
     cudaError_t e = allow(k, kUpSmem, sms, n);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)n, 32 * kWarps, kUpSmem, s>>>(a);
+    k<<<(unsigned)n, 32 * kUpWarps, kUpSmem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (a.T <= 16) return start_down<TX, kF8, 1>(a, s);
-    if (a.T <= 32) return start_down<TX, kF8, 2>(a, s);
-    return start_down<TX, kF8, 4>(a, s);
+    if (a.T <= 8) return start_down<TX, kF8, 1>(a, s);
+    if (a.T <= 16) return start_down<TX, kF8, 2>(a, s);
+    if (a.T <= 32) return start_down<TX, kF8, 4>(a, s);
+    return start_down<TX, kF8, 8>(a, s);
 }
 
 }  // namespace moe
