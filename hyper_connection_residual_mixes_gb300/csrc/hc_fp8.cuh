@@ -36,10 +36,12 @@ __device__ __forceinline__ float fp8_scale_value(uint32_t byte) {
 struct Fp8Scales {
     const void *p;
     int f32;
-    __device__ __forceinline__ float at(int64_t i) const {
-        if (f32) return __ldg(static_cast<const float *>(p) + i);
-        return fp8_scale_value(__ldg(static_cast<const uint8_t *>(p) + i));
+    // as it lies in memory (so that what is loaded early need not be looked at early), and its value
+    __device__ __forceinline__ uint32_t raw(int64_t i) const {
+        return f32 ? __ldg(static_cast<const uint32_t *>(p) + i) : __ldg(static_cast<const uint8_t *>(p) + i);
     }
+    __device__ __forceinline__ float value(uint32_t r) const { return f32 ? __uint_as_float(r) : fp8_scale_value(r); }
+    __device__ __forceinline__ float at(int64_t i) const { return value(raw(i)); }
 };
 
 }  // namespace hc

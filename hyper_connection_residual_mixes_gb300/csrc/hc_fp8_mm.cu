@@ -95,6 +95,19 @@ __device__ __forceinline__ void umma_block(uint32_t d, uint64_t a0, uint64_t b0,
             : "memory");
 }
 
+// 64 columns of this lane in pairs, waited for in the same statement (no register copy can
+// slip between the loads and the wait).
+__device__ __forceinline__ void tmem_ld64(uint32_t t, f32x2 (&v)[32]) {
+    asm volatile(
+        "{\n\t.reg .b32 r<64>;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15, r16, r17, r18, r19, r20, r21, r22, r23, r24, r25, r26, r27, r28, r29, r30, r31, r32, r33, r34, r35, r36, r37, r38, r39, r40, r41, r42, r43, r44, r45, r46, r47, r48, r49, r50, r51, r52, r53, r54, r55, r56, r57, r58, r59, r60, r61, r62, r63}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "mov.b64 %0, {r0, r1};\n\tmov.b64 %1, {r2, r3};\n\tmov.b64 %2, {r4, r5};\n\tmov.b64 %3, {r6, r7};\n\tmov.b64 %4, {r8, r9};\n\tmov.b64 %5, {r10, r11};\n\tmov.b64 %6, {r12, r13};\n\tmov.b64 %7, {r14, r15};\n\tmov.b64 %8, {r16, r17};\n\tmov.b64 %9, {r18, r19};\n\tmov.b64 %10, {r20, r21};\n\tmov.b64 %11, {r22, r23};\n\tmov.b64 %12, {r24, r25};\n\tmov.b64 %13, {r26, r27};\n\tmov.b64 %14, {r28, r29};\n\tmov.b64 %15, {r30, r31};\n\tmov.b64 %16, {r32, r33};\n\tmov.b64 %17, {r34, r35};\n\tmov.b64 %18, {r36, r37};\n\tmov.b64 %19, {r38, r39};\n\tmov.b64 %20, {r40, r41};\n\tmov.b64 %21, {r42, r43};\n\tmov.b64 %22, {r44, r45};\n\tmov.b64 %23, {r46, r47};\n\tmov.b64 %24, {r48, r49};\n\tmov.b64 %25, {r50, r51};\n\tmov.b64 %26, {r52, r53};\n\tmov.b64 %27, {r54, r55};\n\tmov.b64 %28, {r56, r57};\n\tmov.b64 %29, {r58, r59};\n\tmov.b64 %30, {r60, r61};\n\tmov.b64 %31, {r62, r63};\n\t}"
+        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]), "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]), "=l"(v[11]), "=l"(v[12]), "=l"(v[13]), "=l"(v[14]), "=l"(v[15]), "=l"(v[16]), "=l"(v[17]), "=l"(v[18]), "=l"(v[19]), "=l"(v[20]), "=l"(v[21]), "=l"(v[22]), "=l"(v[23]), "=l"(v[24]), "=l"(v[25]), "=l"(v[26]), "=l"(v[27]), "=l"(v[28]), "=l"(v[29]), "=l"(v[30]), "=l"(v[31])
+        : "r"(t)
+        : "memory");
+}
+
 // 8 consecutive columns of a row
 template <typename T>
 __device__ __forceinline__ void put8(T *o, const f32x2 *v, int wide) {
@@ -220,7 +233,9 @@ k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUten
             for (int tile = worker; tile < tiles && ok; tile += workers) {
                 for (int i = 0; i < blocks; ++i, ++use) {
                     const uint32_t b = use & 1u;
-                    if (!(ok = mbar_wait_warp<kPair>(smem_u32(&acc_empty[b]), (use >> 1 & 1u) ^ 1u, &s_abort))) break;
+                    // (what the other CTA passes on is that its loads from tensor memory have completed; no
+                    // memory is handed over, so nothing is to be acquired from the cluster, block for block)
+                    if (!(ok = mbar_wait_warp<false>(smem_u32(&acc_empty[b]), (use >> 1 & 1u) ^ 1u, &s_abort))) break;
                     if (!(ok = mbar_wait_warp<false>(smem_u32(&full_bar[slot]), parity, &s_abort))) break;
                     tmem_fence_after_sync();
                     const uint32_t at = (uint32_t)(slot * C::kStage) / 16;
@@ -235,16 +250,15 @@ k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUten
             wait_exit(smem_u32(&done_bar), 0u);
             __syncwarp();
         } else if (warp == kEpilogue + 1) {
-            // The second CTA of a pair passes on that its accumulators have been read: an arrival
-            // at the other CTA waits for what its thread has stored, and this one's has stored nothing.
+            // The second CTA of a pair passes on that its accumulators have been read.  (From a warp of its
+            // own and without a release: that would wait for what the writing warps have stored.)
             uint32_t use = 0;
             bool ok = true;
             for (int tile = worker; tile < tiles && ok; tile += workers) {
                 for (int i = 0; i < blocks; ++i, ++use) {
                     const uint32_t b = use & 1u;
                     if (!(ok = mbar_wait_warp<false>(smem_u32(&acc_read[b]), use >> 1 & 1u, &s_abort))) break;
-                    if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&acc_empty[b]), 0));
-                    __syncwarp();
+                    arrive_remote_relaxed(mapa(smem_u32(&acc_empty[b]), 0));
                 }
             }
         }
@@ -261,24 +275,23 @@ k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUten
             // (rows and columns that are not there take a scale that is)
             const int64_t x_at = (row < a.M ? row : a.M - 1) * blocks;
             const int64_t w_at = (c0 < a.C ? c0 : a.C - 1) / kFp8Block * a.sw_col;
-            float next = a.sx.at(x_at) * a.sw.at(w_at);
+            uint32_t next_x = a.sx.raw(x_at), next_w = a.sw.raw(w_at);
             f32x2 acc[NP];
 #pragma unroll
             for (int j = 0; j < NP; ++j) acc[j] = f2_dup(0.0f);
             for (int i = 0; i < blocks; ++i, ++use) {
                 const uint32_t b = use & 1u;
-                const f32x2 s = f2_dup(next);
-                if (i + 1 < blocks) next = a.sx.at(x_at + i + 1) * a.sw.at(w_at + (i + 1) * a.sw_k);
+                const f32x2 s = f2_dup(a.sx.value(next_x) * a.sw.value(next_w));
+                if (i + 1 < blocks) next_x = a.sx.raw(x_at + i + 1), next_w = a.sw.raw(w_at + (i + 1) * a.sw_k);
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&acc_full[b]), use >> 1 & 1u, &s_abort))) break;
                 tmem_fence_after_sync();
                 const uint32_t ta = tbase + b * BN + (uint32_t)(half * (BN / 2)) + ((uint32_t)(32 * q) << 16);
 #pragma unroll
-                for (int j = 0; j < NP / 16; ++j) {
-                    uint32_t v[32];
-                    tmem_ld32(ta + 32 * j, v);
+                for (int j = 0; j < NP / 32; ++j) {
+                    f32x2 v[32];
+                    tmem_ld64(ta + 64 * j, v);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        acc[16 * j + k] = f2_fma(f2_make(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), s, acc[16 * j + k]);
+                    for (int k = 0; k < 32; ++k) acc[32 * j + k] = f2_fma(v[k], s, acc[32 * j + k]);
                 }
                 tmem_fence_before_sync();
                 __syncwarp();
