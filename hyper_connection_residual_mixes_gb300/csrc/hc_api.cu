@@ -190,7 +190,7 @@ int hc_last_cuda_error(void) { return g_last_cuda_error; }
 int hc_version(void) { return 200; }
 
 hc_status hc_consume_device_error(cudaStream_t stream) {
-    unsigned int flag = 0, flag_chain = 0, flag_bwd = 0, flag_proj = 0, flag_grouped = 0, flag_norm = 0, flag_fp8 = 0;
+    unsigned int flag = 0, flag_chain = 0, flag_bwd = 0, flag_proj = 0, flag_grouped = 0, flag_norm = 0, flag_rms = 0, flag_fp8 = 0;
     hc_status st = cuda_status(hc::consume_device_error(stream, &flag));
     if (st != HC_OK) return st;
     st = cuda_status(hc::consume_slices_device_error(stream, &flag_chain));
@@ -203,10 +203,12 @@ hc_status hc_consume_device_error(cudaStream_t stream) {
     if (st != HC_OK) return st;
     st = cuda_status(hc::consume_layer_norm_device_error(stream, &flag_norm));
     if (st != HC_OK) return st;
+    st = cuda_status(hc::consume_rms_norm_device_error(stream, &flag_rms));
+    if (st != HC_OK) return st;
     st = cuda_status(hc::consume_fp8_mm_device_error(stream, &flag_fp8));
     if (st != HC_OK) return st;
     // (bit 0 of each: a wait ran out; bit 1 of the grouped products': bad offsets)
-    if (flag | flag_norm | flag_fp8 | flag_chain | flag_bwd | flag_proj | (flag_grouped & 1u)) return HC_ERR_TIMEOUT;
+    if (flag | flag_norm | flag_rms | flag_fp8 | flag_chain | flag_bwd | flag_proj | (flag_grouped & 1u)) return HC_ERR_TIMEOUT;
     return flag_grouped ? HC_ERR_INVALID_ARG : HC_OK;
 }
 

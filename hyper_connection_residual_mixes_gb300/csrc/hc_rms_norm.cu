@@ -212,6 +212,183 @@ __global__ void __launch_bounds__(kWarps ? 128 : 1024) k_rms_norm(const Args a) 
     }
 }
 
+// ------------------------------------------------------------ rows through a ring
+// Many long rows: a block walks over rows that bulk copies bring into slots of shared
+// memory ahead of it (one thread issues them; a block barrier of a row's reduction
+// says that a slot has been read).
+constexpr int kMostSlots = 6;
+struct Ring {
+    uint64_t full[kMostSlots];
+    volatile int abort;
+};
+struct Place {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int slots) {
+        if (++slot == slots) slot = 0, parity ^= 1u;
+    }
+};
+// All threads wait for a row; a wait that runs out is reported and the block goes on (its rows are
+// then wrong, but every barrier is met).
+__device__ __forceinline__ void ring_wait(Ring &r, const Place &p) { mbar_wait<false>(smem_u32(&r.full[p.slot]), p.parity, &r.abort); }
+__device__ __forceinline__ void ring_init(Ring &r, int slots) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < slots; ++i) mbar_init(smem_u32(&r.full[i]), 1);
+        r.abort = 0;
+        fence_mbar_init_cluster();
+    }
+    __syncthreads();
+}
+// After a wait that ran out: the copies still in flight must land before the block leaves.
+__device__ __forceinline__ void ring_leave(Ring &r, int64_t its, int slots) {
+    if (threadIdx.x == 0 && r.abort)
+        for (int64_t k = its > slots ? its - slots : 0; k < its; ++k)
+            for (uint32_t i = 0; i < (1u << 22); ++i) {
+                if (mbar_try_wait(smem_u32(&r.full[k % slots]), (uint32_t)(k / slots) & 1u)) break;
+                __nanosleep(128);
+            }
+}
+
+// 16 columns a thread, in runs of 16 bytes.
+template <typename T, int kMaxThreads, int kMinBlocks>
+__global__ void __launch_bounds__(kMaxThreads, kMinBlocks) k_rms_norm_ring(const Args a, int slots) {
+    constexpr int V = 16 / (int)sizeof(T), NV = 16 / V;
+    extern __shared__ __align__(16) uint8_t s_rows[];
+    __shared__ Ring ring;
+    __shared__ float red[2][32];
+    const int t = threadIdx.x, tpr = blockDim.x, warp = t >> 5, lane = t & 31, nw = tpr >> 5, d = a.d;
+    const uint32_t row_bytes = (uint32_t)d * sizeof(T), slot_bytes = row_bytes * (a.residual ? 2 : 1);
+    const int groups = (d + kFp8Block - 1) / kFp8Block;
+    const int64_t rows = (a.n - 1 - blockIdx.x) / gridDim.x + 1;  // of this block (the grid has at most n)
+    ring_init(ring, slots);
+    const auto fetch = [&](int slot, int64_t it) {
+        const uint32_t bar = smem_u32(&ring.full[slot]), to = smem_u32(s_rows) + (uint32_t)slot * slot_bytes;
+        const int64_t row = blockIdx.x + it * gridDim.x;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        bulk_load(to, static_cast<const T *>(a.x) + row * a.xs, row_bytes, bar);
+        if (a.residual) bulk_load(to + row_bytes, static_cast<const T *>(a.residual) + row * a.res_s, row_bytes, bar);
+    };
+    if (t == 0)
+        for (int it = 0; it < slots && it < rows; ++it) fetch(it, it);
+    const float inv_d = 1.0f / (float)d;
+    f32x2 w[NV][V / 2];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float f[V] = {};
+        if ((t + i * tpr) * V < d) params<V>(a.w, a.w_type, (t + i * tpr) * V, f);
+#pragma unroll
+        for (int k = 0; k < V; k += 2) w[i][k / 2] = f2_make(f[k], f[k + 1]);
+    }
+    Place place;
+    int buf = 0;
+    for (int64_t it = 0; it < rows; ++it, buf ^= 1) {
+        const int64_t row = blockIdx.x + it * gridDim.x;
+        ring_wait(ring, place);
+        const uint8_t *const slot = s_rows + (uint32_t)place.slot * slot_bytes;
+        f32x2 v[NV][V / 2], acc = f2_dup(0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * V;
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) v[i][k] = f2_dup(0.0f);
+            if (c >= d) continue;
+            Vec<T, V> x = *reinterpret_cast<const Vec<T, V> *>(slot + c * sizeof(T));
+            if (a.residual) {
+                const Vec<T, V> u = *reinterpret_cast<const Vec<T, V> *>(slot + row_bytes + c * sizeof(T));
+#pragma unroll
+                for (int k = 0; k < V; k += 2) put_pair(x, k, f2_add(pair(x, k), pair(u, k)));
+                *reinterpret_cast<Vec<T, V> *>(static_cast<T *>(a.r) + row * a.rs + c) = x;
+            }
+#pragma unroll
+            for (int k = 0; k < V; k += 2) v[i][k / 2] = pair(x, k), acc = f2_fma(v[i][k / 2], v[i][k / 2], acc);
+        }
+        const float sum = warp_sum(f2_hsum(acc));
+        // (two buffers: a warp writes the next row's while a slow one still reads these)
+        if (lane == 0) red[buf][warp] = sum;
+        __syncthreads();
+        if (t == 0 && it + slots < rows) fetch(place.slot, it + slots);  // every thread has read the slot
+        place.next(slots);
+        const float rstd = rsqrt_newton(fmaf(warp_sum(lane < nw ? red[buf][lane] : 0.0f), inv_d, a.eps));
+        if (t == 0 && a.rstd) a.rstd[row] = rstd;
+        const f32x2 rs = f2_dup(rstd);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * V;
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) v[i][k] = f2_mul(f2_mul(v[i][k], rs), w[i][k]);
+            if (a.y && c < d) {
+                Vec<T, V> o;
+#pragma unroll
+                for (int k = 0; k < V; k += 2) put_pair(o, k, v[i][k / 2]);
+                *reinterpret_cast<Vec<T, V> *>(static_cast<T *>(a.y) + row * a.ys + c) = o;
+            }
+            if (!a.codes) continue;
+            float f[V], amax = 0.0f;
+#pragma unroll
+            for (int k = 0; k < V; k += 2) f2_split(v[i][k / 2], f[k], f[k + 1]);
+#pragma unroll
+            for (int k = 0; k < V; ++k) amax = largest(amax, f[k]);
+            const uint32_t byte = fp8_scale_byte(largest_of_group<V>(amax));
+            if (c >= d) continue;
+            put_codes<V>(a.codes + row * a.cs + c, f, fp8_inverse(byte), a.codes_wide);
+            if (c % kFp8Block == 0) a.scales[row * groups + c / kFp8Block] = (uint8_t)byte;
+        }
+    }
+    ring_leave(ring, rows, slots);
+}
+
+constexpr int kDevices = 64;
+constexpr int kSmemBlock = 227 * 1024, kSmemSm = 228 * 1024;  // shared memory of a block, of an SM
+int current_device() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices ? dev : 0;
+}
+int sm_count() {
+    static std::atomic<int> sms[kDevices];  // (any host thread may be the first to ask)
+    const int dev = current_device();
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    sms[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+// Slots of a ring and blocks of a launch: a grid that fills the SMs once, with as many
+// slots as fit beside the SM's other blocks.  What a kernel needs is asked for and set once per
+// device.
+template <auto kKernel>
+cudaError_t ring_shape(int threads, int slot_bytes, int least, int64_t most, int *slots, int *blocks) {
+    static std::atomic<int> regs[kDevices];
+    const int dev = current_device();
+    int r = regs[dev].load(std::memory_order_acquire);
+    if (!r) {
+        cudaFuncAttributes fa{};
+        cudaError_t e = cudaFuncGetAttributes(&fa, kKernel);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBlock - (int)fa.sharedSizeBytes);
+        if (e != cudaSuccess) return e;
+        r = fa.numRegs;
+        regs[dev].store(r, std::memory_order_release);  // (the attribute is set for whoever reads it)
+    }
+    const int warps = threads / 32, by_regs = 65536 / ((r * 32 + 255) / 256 * 256 * warps), by_threads = 64 / warps;
+    int per_sm = by_regs < by_threads ? by_regs : by_threads;
+    if (per_sm < 1) per_sm = 1;
+    const int extra = 2048;  // a block's other shared memory
+    while (per_sm > 1 && (kSmemSm / per_sm - extra) / slot_bytes < least) --per_sm;
+    const int room = (per_sm > 1 ? kSmemSm / per_sm : kSmemBlock) - extra;
+    *slots = room / slot_bytes < kMostSlots ? room / slot_bytes : kMostSlots;
+    const int64_t grid = (int64_t)per_sm * sm_count();
+    *blocks = (int)(grid < most ? grid : most);
+    return cudaSuccess;
+}
+template <auto kKernel>
+cudaError_t start_ring(const Args &a, int threads, int slot_bytes, cudaStream_t s) {
+    int slots = 0, blocks = 0;
+    const cudaError_t e = ring_shape<kKernel>(threads, slot_bytes, 3, a.n, &slots, &blocks);
+    if (e != cudaSuccess) return e;
+    kKernel<<<blocks, threads, slots * slot_bytes, s>>>(a, slots);
+    return cudaGetLastError();
+}
+
 template <typename T>
 constexpr int kWide = 16 / (int)sizeof(T);  // values of a wide access
 
@@ -235,6 +412,12 @@ cudaError_t forward(Args a, cudaStream_t s) {
     a.codes_wide = multiple(a.codes, a.cs, 1, W);
     // (threads of a block: whole groups of 128 values a pass)
     const int per = wide ? W : 1, need = (a.d + per - 1) / per;
+    // (the ring for many rows)
+    if (wide && a.d > 512 && a.n * a.d >= 16384 * (int64_t)sm_count()) {
+        const int threads = (a.d + 511) / 512 * 32, slot = (int)(a.d * size) * (a.residual ? 2 : 1);
+        if (threads <= 320) return start_ring<k_rms_norm_ring<T, 320, 2>>(a, threads, slot, s);
+        return start_ring<k_rms_norm_ring<T, 1024, 1>>(a, threads, slot, s);
+    }
     if (wide) {
         if (need <= 32) return start<T, W, 1, true>(a, 0, s);
         if (need <= 64) return start<T, W, 2, true>(a, 0, s);
@@ -323,6 +506,7 @@ __global__ void __launch_bounds__(kWarps ? 256 : 1024) k_rms_backward(const Back
             *reinterpret_cast<Vec<TG, VEC> *>(o_row + c) = o;
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float *pw = a.part + (int64_t)blockIdx.x * a.d;
     if constexpr (!kWarps) {
 #pragma unroll
@@ -349,34 +533,148 @@ __global__ void __launch_bounds__(kWarps ? 256 : 1024) k_rms_backward(const Back
     }
 }
 
+// The same with the rows of r, g and g_r through a ring: 8 columns a thread in two runs of 4.
+// Both passes over a row read it from its slot, which is filled again once the next
+// row's barrier has passed.
+template <typename TX, typename TG, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads, 1) k_rms_backward_ring(const BackArgs a, int slots) {
+    extern __shared__ __align__(16) uint8_t s_rows[];
+    __shared__ Ring ring;
+    __shared__ float red[2][32];
+    const int t = threadIdx.x, tpr = blockDim.x, warp = t >> 5, lane = t & 31, nw = tpr >> 5, d = a.d;
+    const uint32_t x_bytes = (uint32_t)d * sizeof(TX), g_bytes = (uint32_t)d * sizeof(TG), slot_bytes = x_bytes + g_bytes * (a.gr ? 2 : 1);
+    const float inv_d = 1.0f / (float)d;
+    const int64_t rows = (a.n - 1 - blockIdx.x) / gridDim.x + 1;
+    ring_init(ring, slots);
+    const auto fetch = [&](int slot, int64_t it) {
+        const uint32_t bar = smem_u32(&ring.full[slot]), to = smem_u32(s_rows) + (uint32_t)slot * slot_bytes;
+        const int64_t row = blockIdx.x + it * gridDim.x;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        bulk_load(to, static_cast<const TX *>(a.r) + row * a.rs, x_bytes, bar);
+        bulk_load(to + x_bytes, static_cast<const TG *>(a.g) + row * a.gs, g_bytes, bar);
+        if (a.gr) bulk_load(to + x_bytes + g_bytes, static_cast<const TG *>(a.gr) + row * a.grs, g_bytes, bar);
+    };
+    if (t == 0)
+        for (int it = 0; it < slots && it < rows; ++it) fetch(it, it);
+    f32x2 w[2][2], aw[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float f[4] = {};
+        if ((t + i * tpr) * 4 < d) params<4>(a.w, a.w_type, (t + i * tpr) * 4, f);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) w[i][k] = f2_make(f[2 * k], f[2 * k + 1]), aw[i][k] = f2_dup(0.0f);
+    }
+    Place place;
+    int before = 0, buf = 0;
+    float rstd_next = __ldg(a.rstd + blockIdx.x);
+    for (int64_t it = 0; it < rows; ++it, buf ^= 1) {
+        const int64_t row = blockIdx.x + it * gridDim.x;
+        const float rstd = rstd_next;
+        if (it + 1 < rows) rstd_next = __ldg(a.rstd + row + gridDim.x);
+        ring_wait(ring, place);
+        const uint8_t *const slot = s_rows + (uint32_t)place.slot * slot_bytes;
+        const f32x2 rs = f2_dup(rstd);
+        f32x2 acc = f2_dup(0.0f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = (t + i * tpr) * 4;
+            if (c >= d) continue;
+            const Vec<TX, 4> x = *reinterpret_cast<const Vec<TX, 4> *>(slot + c * sizeof(TX));
+            const Vec<TG, 4> g = *reinterpret_cast<const Vec<TG, 4> *>(slot + x_bytes + c * sizeof(TG));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const f32x2 xh = f2_mul(pair(x, 2 * k), rs), gk = pair(g, 2 * k);
+                acc = f2_fma(f2_mul(gk, w[i][k]), xh, acc);
+                aw[i][k] = f2_fma(gk, xh, aw[i][k]);
+            }
+        }
+        const float sum = warp_sum(f2_hsum(acc));
+        // (two buffers: a warp writes the next row's while a slow one still reads these)
+        if (lane == 0) red[buf][warp] = sum;
+        __syncthreads();
+        if (t == 0 && it > 0 && it - 1 + slots < rows) fetch(before, it - 1 + slots);  // every thread is done with the row before
+        before = place.slot;
+        place.next(slots);
+        const f32x2 m = f2_dup(-warp_sum(lane < nw ? red[buf][lane] : 0.0f) * inv_d);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = (t + i * tpr) * 4;
+            if (c >= d) continue;
+            const Vec<TX, 4> x = *reinterpret_cast<const Vec<TX, 4> *>(slot + c * sizeof(TX));
+            const Vec<TG, 4> g = *reinterpret_cast<const Vec<TG, 4> *>(slot + x_bytes + c * sizeof(TG));
+            Vec<TG, 4> past, o;
+            if (a.gr) past = *reinterpret_cast<const Vec<TG, 4> *>(slot + x_bytes + g_bytes + c * sizeof(TG));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                f32x2 v = f2_mul(rs, f2_fma(f2_mul(pair(x, 2 * k), rs), m, f2_mul(pair(g, 2 * k), w[i][k])));
+                if (a.gr) v = f2_add(v, pair(past, 2 * k));
+                put_pair(o, 2 * k, v);
+            }
+            *reinterpret_cast<Vec<TG, 4> *>(static_cast<TG *>(a.gx) + row * a.gxs + c) = o;
+        }
+    }
+    ring_leave(ring, rows, slots);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = (t + i * tpr) * 4;
+        if (c >= d) continue;
+        float f[4];
+        f2_split(aw[i][0], f[0], f[1]), f2_split(aw[i][1], f[2], f[3]);
+        *reinterpret_cast<float4 *>(a.part + (int64_t)blockIdx.x * d + c) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+}
+
 // g_w: the blocks' partial sums added in a fixed order.  A block takes 32 columns;
-// its 8 warps share the rows.
-__global__ void __launch_bounds__(256) k_rms_columns(const float *__restrict__ part, int blocks, int d, float *__restrict__ gw) {
-    __shared__ float s[8][32];
+// its warps share the rows.
+constexpr int kColumnWarps = 16;
+__global__ void __launch_bounds__(32 * kColumnWarps) k_rms_columns(const float *__restrict__ part, int blocks, int d, float *__restrict__ gw) {
+    __shared__ float s[kColumnWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float v = 0.0f;
-    if (c < d)
-        for (int b = warp; b < blocks; b += 8) v += part[(int64_t)b * d + c];
+    if (c < d) {
+#pragma unroll 10
+        for (int b = warp; b < blocks; b += kColumnWarps) v += __ldcg(part + (int64_t)b * d + c);
+    }
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < d) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k) v += s[k][lane];
+        for (int k = 1; k < kColumnWarps; ++k) v += s[k][lane];
         gw[c] = v;
     }
 }
 
-// blocks of the backward, and so rows of partial sums: by n alone
-int back_blocks(int64_t n) { return (int)(n < 304 ? (n > 0 ? n : 1) : 304); }
+// most blocks of the backward, and so rows of partial sums
+int64_t most_blocks(int64_t n, int d) {
+    const int64_t most = d < 1024 ? 1216 : d <= 2048 ? 608 : 304;
+    return n < most ? n : most;
+}
 
+cudaError_t start_columns(const BackArgs &a, int blocks, float *gw, cudaStream_t s) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((a.d + 31) / 32)), cfg.blockDim = dim3(32 * kColumnWarps);
+    cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_rms_columns, (const float *)a.part, blocks, a.d, gw);
+}
 template <typename TX, typename TG, int VEC, int NV, bool kWarps>
 cudaError_t start_back(const BackArgs &a, int threads, float *gw, cudaStream_t s) {
-    const int blocks = back_blocks(a.n);
-    k_rms_backward<TX, TG, VEC, NV, kWarps><<<blocks, threads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    int64_t blocks = most_blocks(a.n, a.d);
+    if (kWarps && blocks > (a.n + 7) / 8) blocks = (a.n + 7) / 8;
+    k_rms_backward<TX, TG, VEC, NV, kWarps><<<(unsigned)blocks, threads, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : start_columns(a, (int)blocks, gw, s);
+}
+template <auto kKernel>
+cudaError_t start_back_ring(const BackArgs &a, int threads, int slot_bytes, float *gw, cudaStream_t s) {
+    int slots = 0, blocks = 0;
+    cudaError_t e = ring_shape<kKernel>(threads, slot_bytes, 3, most_blocks(a.n, a.d), &slots, &blocks);
     if (e != cudaSuccess) return e;
-    k_rms_columns<<<(a.d + 31) / 32, 256, 0, s>>>(a.part, blocks, a.d, gw);
-    return cudaGetLastError();
+    kKernel<<<blocks, threads, slots * slot_bytes, s>>>(a, slots);
+    return (e = cudaGetLastError()) != cudaSuccess ? e : start_columns(a, blocks, gw, s);
 }
 
 template <typename TX, typename TG>
@@ -385,18 +683,22 @@ cudaError_t backward(const BackArgs &a, float *gw, cudaStream_t s) {
     const bool wide = a.d % W == 0 && multiple(a.r, a.rs, sizeof(TX), W * sizeof(TX)) &&
                       multiple(a.g, a.gs, sizeof(TG), W * sizeof(TG)) && multiple(a.gr, a.grs, sizeof(TG), W * sizeof(TG)) &&
                       multiple(a.gx, a.gxs, sizeof(TG), W * sizeof(TG)) && multiple(a.w, 0, 1, a.w_type == HC_F32 ? 16 : 8);
-    const int per = wide ? W : 1, need = (a.d + per - 1) / per;
-    const int threads = need > 1024 ? 1024 : (need + 31) / 32 * 32;
+    const bool bulk = wide && a.d * sizeof(TX) % 16 == 0 && a.d * sizeof(TG) % 16 == 0 && multiple(a.r, a.rs, sizeof(TX), 16) &&
+                      multiple(a.g, a.gs, sizeof(TG), 16) && multiple(a.gr, a.grs, sizeof(TG), 16);
+    if (bulk && a.d >= 1024 && a.d <= 8192) {
+        const int threads = (a.d + 255) / 256 * 32, slot = a.d * (int)(sizeof(TX) + sizeof(TG) * (a.gr ? 2 : 1));
+        if (threads <= 640) return start_back_ring<k_rms_backward_ring<TX, TG, 640>>(a, threads, slot, gw, s);
+        return start_back_ring<k_rms_backward_ring<TX, TG, 1024>>(a, threads, slot, gw, s);
+    }
+    // (four vectors a thread where rows are long enough: more rows are under way then)
+    const int per = wide ? W : 1, need = (a.d + per - 1) / per, threads = ((need + 3) / 4 + 31) / 32 * 32;
     if (wide) {
         if (need <= 64) return start_back<TX, TG, W, 2, true>(a, 256, gw, s);
-        if (need <= 1024) return start_back<TX, TG, W, 1, false>(a, threads, gw, s);
-        if (need <= 2048) return start_back<TX, TG, W, 2, false>(a, threads, gw, s);
         return start_back<TX, TG, W, 4, false>(a, threads, gw, s);
     }
     if (need <= 128) return start_back<TX, TG, 1, 4, true>(a, 256, gw, s);
-    if (need <= 1024) return start_back<TX, TG, 1, 1, false>(a, threads, gw, s);
     if (need <= 4096) return start_back<TX, TG, 1, 4, false>(a, threads, gw, s);
-    return start_back<TX, TG, 1, 16, false>(a, threads, gw, s);
+    return start_back<TX, TG, 1, 16, false>(a, 1024, gw, s);
 }
 
 // ------------------------------------------------------------ casts
@@ -546,7 +848,7 @@ cudaError_t launch_rms_norm(const void *x, int64_t x_stride, const void *residua
     return type == HC_BF16 ? rn::forward<__nv_bfloat16>(a, s) : rn::forward<__half>(a, s);
 }
 
-size_t rms_norm_backward_workspace_bytes(int64_t n, int d) { return (size_t)rn::back_blocks(n) * d * 4; }
+size_t rms_norm_backward_workspace_bytes(int64_t n, int d) { return (size_t)rn::most_blocks(n, d) * d * 4; }
 
 cudaError_t launch_rms_norm_backward(const void *g_y, int64_t g_stride, const void *g_r, int64_t g_r_stride, hc_dtype g_type,
                                      const void *r, int64_t r_stride, hc_dtype type, const void *w, hc_dtype w_type,
@@ -573,6 +875,20 @@ cudaError_t launch_fp8_cast_weights(const void *w, hc_dtype type, int64_t count,
     if (type == HC_F32) return rn::cast_weights<float>(w, count, N, K, codes, scales, s);
     return type == HC_BF16 ? rn::cast_weights<__nv_bfloat16>(w, count, N, K, codes, scales, s)
                            : rn::cast_weights<__half>(w, count, N, K, codes, scales, s);
+}
+
+cudaError_t consume_rms_norm_device_error(cudaStream_t s, unsigned int *flag) {
+    cudaError_t e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return e;
+    unsigned int v = 0;
+    e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof v);
+    if (e != cudaSuccess) return e;
+    *flag = v;
+    if (v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof zero);
+    }
+    return e;
 }
 
 }  // namespace hc

@@ -55,6 +55,7 @@ cudaError_t launch_rms_norm_backward(const void *g_y, int64_t g_stride, const vo
                                      const void *r, int64_t r_stride, hc_dtype type, const void *w, hc_dtype w_type,
                                      const float *rstd, int64_t n, int d, void *g_x, int64_t gx_stride, float *g_w,
                                      void *workspace, cudaStream_t s);
+cudaError_t consume_rms_norm_device_error(cudaStream_t s, unsigned int *flag);  // as the other files' (hc_launch.h)
 cudaError_t launch_fp8_cast(const void *x, int64_t x_stride, hc_dtype type, int64_t n, int d, uint8_t *codes,
                             int64_t codes_stride, uint8_t *scales, cudaStream_t s);
 cudaError_t launch_fp8_cast_weights(const void *w, hc_dtype type, int64_t count, int64_t N, int K, uint8_t *codes,
