@@ -259,11 +259,12 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) k_rms_norm_ring(const
     const int t = threadIdx.x, tpr = blockDim.x, warp = t >> 5, lane = t & 31, nw = tpr >> 5, d = a.d;
     const uint32_t row_bytes = (uint32_t)d * sizeof(T), slot_bytes = row_bytes * (a.residual ? 2 : 1);
     const int groups = (d + kFp8Block - 1) / kFp8Block;
-    const int64_t rows = (a.n - 1 - blockIdx.x) / gridDim.x + 1;  // of this block (the grid has at most n)
+    // (a block's rows lie together: 361 us for 65,536 rows of 5,120 bf16, for every gridDim-th row 368)
+    const int64_t first = a.n * blockIdx.x / gridDim.x, rows = a.n * (blockIdx.x + 1) / gridDim.x - first;
     ring_init(ring, slots);
     const auto fetch = [&](int slot, int64_t it) {
         const uint32_t bar = smem_u32(&ring.full[slot]), to = smem_u32(s_rows) + (uint32_t)slot * slot_bytes;
-        const int64_t row = blockIdx.x + it * gridDim.x;
+        const int64_t row = first + it;
         mbar_arrive_expect_tx(bar, slot_bytes);
         bulk_load(to, static_cast<const T *>(a.x) + row * a.xs, row_bytes, bar);
         if (a.residual) bulk_load(to + row_bytes, static_cast<const T *>(a.residual) + row * a.res_s, row_bytes, bar);
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks) k_rms_norm_ring(const
     Place place;
     int buf = 0;
     for (int64_t it = 0; it < rows; ++it, buf ^= 1) {
-        const int64_t row = blockIdx.x + it * gridDim.x;
+        const int64_t row = first + it;
         ring_wait(ring, place);
         const uint8_t *const slot = s_rows + (uint32_t)place.slot * slot_bytes;
         f32x2 v[NV][V / 2], acc = f2_dup(0.0f);
@@ -352,11 +353,11 @@ int sm_count() {
     sms[dev].store(n, std::memory_order_relaxed);
     return n;
 }
-// Slots of a ring and blocks of a launch: a grid that fills the SMs once, with as many
-// slots as fit beside the SM's other blocks.  What a kernel needs is asked for and set once per
-// device.
+// Slots of a ring and blocks of a launch: a grid that fills the SMs once (`most_per_sm` blocks
+// each at the most), with as many slots as fit in `room` bytes of an SM, two at least.  What a kernel
+// needs is asked for and set once per device.
 template <auto kKernel>
-cudaError_t ring_shape(int threads, int slot_bytes, int least, int64_t most, int *slots, int *blocks) {
+cudaError_t ring_shape(int threads, int slot_bytes, int most_per_sm, int room, int64_t most, int *slots, int *blocks) {
     static std::atomic<int> regs[kDevices];
     const int dev = current_device();
     int r = regs[dev].load(std::memory_order_acquire);
@@ -371,19 +372,24 @@ cudaError_t ring_shape(int threads, int slot_bytes, int least, int64_t most, int
     }
     const int warps = threads / 32, by_regs = 65536 / ((r * 32 + 255) / 256 * 256 * warps), by_threads = 64 / warps;
     int per_sm = by_regs < by_threads ? by_regs : by_threads;
+    per_sm = per_sm < most_per_sm ? per_sm : most_per_sm;
     if (per_sm < 1) per_sm = 1;
     const int extra = 2048;  // a block's other shared memory
-    while (per_sm > 1 && (kSmemSm / per_sm - extra) / slot_bytes < least) --per_sm;
-    const int room = (per_sm > 1 ? kSmemSm / per_sm : kSmemBlock) - extra;
-    *slots = room / slot_bytes < kMostSlots ? room / slot_bytes : kMostSlots;
+    while (per_sm > 1 && (kSmemSm / per_sm - extra) / slot_bytes < 2) --per_sm;
+    const int fit = ((per_sm > 1 ? kSmemSm / per_sm : kSmemBlock) - extra) / slot_bytes;
+    int n = room / per_sm / slot_bytes;
+    n = n < 2 ? 2 : n > kMostSlots ? kMostSlots : n;
+    *slots = n < fit ? n : fit;
     const int64_t grid = (int64_t)per_sm * sm_count();
     *blocks = (int)(grid < most ? grid : most);
     return cudaSuccess;
 }
+// (640 threads an SM and some 80 KB of rows on their way to it: of 65,536 rows of 5,120 bf16, to 8 bits,
+// two blocks with two slots each 361 us, with three 405, five 417; three blocks with two 400.)
 template <auto kKernel>
 cudaError_t start_ring(const Args &a, int threads, int slot_bytes, cudaStream_t s) {
     int slots = 0, blocks = 0;
-    const cudaError_t e = ring_shape<kKernel>(threads, slot_bytes, 3, a.n, &slots, &blocks);
+    const cudaError_t e = ring_shape<kKernel>(threads, slot_bytes, threads < 640 ? 640 / threads : 1, 84 * 1024, a.n, &slots, &blocks);
     if (e != cudaSuccess) return e;
     kKernel<<<blocks, threads, slots * slot_bytes, s>>>(a, slots);
     return cudaGetLastError();
@@ -410,7 +416,6 @@ cudaError_t forward(Args a, cudaStream_t s) {
                       multiple(a.r, a.rs, size, 16) && multiple(a.y, a.ys, size, 16) &&
                       multiple(a.w, 0, 1, a.w_type == HC_F32 ? 16 : 8);
     a.codes_wide = multiple(a.codes, a.cs, 1, W);
-    // (threads of a block: whole groups of 128 values a pass)
     const int per = wide ? W : 1, need = (a.d + per - 1) / per;
     // (the ring for many rows)
     if (wide && a.d > 512 && a.n * a.d >= 16384 * (int64_t)sm_count()) {
@@ -427,10 +432,11 @@ cudaError_t forward(Args a, cudaStream_t s) {
         return start<T, W, 4, false>(a, threads, s);
     }
     if (need <= 128) return start<T, 1, 4, true>(a, 0, s);
-    const int threads = need > 1024 ? 1024 : (need + 127) / 128 * 128;
-    if (need <= 1024) return start<T, 1, 1, false>(a, threads, s);
-    if (need <= 4096) return start<T, 1, 4, false>(a, threads, s);
-    return start<T, 1, 16, false>(a, threads, s);
+    // (one by one: whole groups of 128 values a pass)
+    const auto threads = [&](int each) { return (need + each * 128 - 1) / (each * 128) * 128; };
+    if (need <= 1024) return start<T, 1, 4, false>(a, threads(4), s);
+    if (need <= 8192) return start<T, 1, 8, false>(a, threads(8), s);
+    return start<T, 1, 16, false>(a, 1024, s);
 }
 
 // ------------------------------------------------------------ backward
@@ -671,7 +677,7 @@ cudaError_t start_back(const BackArgs &a, int threads, float *gw, cudaStream_t s
 template <auto kKernel>
 cudaError_t start_back_ring(const BackArgs &a, int threads, int slot_bytes, float *gw, cudaStream_t s) {
     int slots = 0, blocks = 0;
-    cudaError_t e = ring_shape<kKernel>(threads, slot_bytes, 3, most_blocks(a.n, a.d), &slots, &blocks);
+    cudaError_t e = ring_shape<kKernel>(threads, slot_bytes, threads < 640 ? 640 / threads : 1, kSmemBlock, most_blocks(a.n, a.d), &slots, &blocks);
     if (e != cudaSuccess) return e;
     kKernel<<<blocks, threads, slots * slot_bytes, s>>>(a, slots);
     return (e = cudaGetLastError()) != cudaSuccess ? e : start_columns(a, blocks, gw, s);
