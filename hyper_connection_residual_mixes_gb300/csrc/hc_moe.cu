@@ -75,81 +75,117 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
-// A warp chooses a token's experts: the `top` largest logits, of equal ones the first.
-__device__ __forceinline__ void choose(const Args &a, Lists &l, int t, int lane) {
-    const float *lg = a.logits + (int64_t)t * a.experts;
+// A warp chooses a token's experts: the `top` largest logits, of equal ones the first.  Up to 256 are kept
+// in registers, of more the ones behind the last choice are looked for in memory again.
+constexpr int kKept = 8;
+__device__ __forceinline__ void choose(const Args &a, Lists &l, int t, int lane, bool write) {
+    const float *const lg = a.logits + (int64_t)t * a.experts;
+    const bool kept = a.experts <= 32 * kKept;
+    uint32_t keys[kKept];
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) keys[i] = kept && lane + 32 * i < a.experts ? order_key(__ldg(lg + lane + 32 * i)) : 0u;
+    float sum = 0.0f, best = 0.0f;
+    if (!a.normalise && !a.sigmoid) {  // of the softmax over all experts
+        uint32_t most = 0;
+        if (kept) {
+#pragma unroll
+            for (int i = 0; i < kKept; ++i) most = keys[i] > most ? keys[i] : most;
+        } else {
+            for (int i = lane; i < a.experts; i += 32) most = max(most, order_key(__ldg(lg + i)));
+        }
+        best = of_key(__reduce_max_sync(0xffffffffu, most));
+        for (int i = lane; i < a.experts; i += 32) {
+            const float v = __ldg(lg + i);
+            if (order_key(v) != 0u) sum += v == best ? 1.0f : expf(v - best);
+        }
+        sum = warp_sum(sum);
+    }
     uint32_t last = 0xffffffffu;
-    int last_e = -1;
-    float best = 0.0f, sum = 0.0f;
+    int last_e = -1, mine_e = -1;
+    float mine = 0.0f, chosen = 0.0f;
     for (int j = 0; j < a.top; ++j) {
-        // the largest behind the one chosen last
         uint32_t key = 0;
         int e = 0x7fffffff;
-        for (int i = lane; i < a.experts; i += 32) {
-            const uint32_t k = order_key(__ldg(lg + i));
-            if ((k < last || (k == last && i > last_e)) && k > key) key = k, e = i;
+        if (kept) {
+#pragma unroll
+            for (int i = 0; i < kKept; ++i)
+                if (keys[i] > key) key = keys[i], e = lane + 32 * i;
+        } else {
+            for (int i = lane; i < a.experts; i += 32) {
+                const uint32_t k = order_key(__ldg(lg + i));
+                if ((k < last || (k == last && i > last_e)) && k > key) key = k, e = i;
+            }
         }
         const uint32_t top = __reduce_max_sync(0xffffffffu, key);
         e = (int)__reduce_min_sync(0xffffffffu, key == top ? (uint32_t)e : 0x7fffffffu);
+        if (top == 0u) break;  // nothing is left
         last = top, last_e = e;
-        float s = 0.0f;
-        if (top != 0u) {
-            const float v = of_key(top);
-            if (j == 0) best = v;
-            s = a.sigmoid ? 1.0f / (1.0f + expf(-v)) : v == best ? 1.0f : expf(v - best);
-        }
-        sum += s;
-        if (lane == 0) {
-            l.id[t * a.top + j] = (int16_t)(top != 0u ? e : -1);
-            l.p[t * a.top + j] = s;
-        }
-        if (top == 0u) last = 0u, last_e = 0x7fffffff;  // nothing is left
+#pragma unroll
+        for (int i = 0; i < kKept; ++i)
+            if (e == lane + 32 * i) keys[i] = 0u;
+        const float v = of_key(top);
+        if (j == 0) best = v;
+        const float s = a.sigmoid ? 1.0f / (1.0f + expf(-v)) : v == best ? 1.0f : expf(v - best);
+        chosen += s;
+        if (lane == j) mine = s, mine_e = e;
     }
-    if (!a.normalise) {
-        if (!a.sigmoid) {  // over all experts
-            sum = 0.0f;
-            for (int i = lane; i < a.experts; i += 32) {
-                const float v = __ldg(lg + i);
-                if (order_key(v) != 0u) sum += v == best ? 1.0f : expf(v - best);
-            }
-            sum = warp_sum(sum);
-        } else {
-            sum = 1.0f;
+    const float by = a.normalise ? chosen : a.sigmoid ? 1.0f : sum;
+    if (lane < a.top) {  // (top is at most 16)
+        const int at = t * a.top + lane;
+        const float p = by > 0.0f ? mine / by * a.scale : 0.0f;
+        l.id[at] = (int16_t)mine_e, l.p[at] = p;
+        if (write && blockIdx.x == 0) {
+            if (a.ids) a.ids[at] = mine_e;
+            if (a.p) a.p[at] = p;
         }
-    }
-    __syncwarp();
-    for (int j = lane; j < a.top; j += 32) {
-        float &p = l.p[t * a.top + j];
-        p = sum > 0.0f ? p / sum * a.scale : 0.0f;
-        if (blockIdx.x != 0) continue;
-        if (a.ids) a.ids[t * a.top + j] = l.id[t * a.top + j];
-        if (a.p) a.p[t * a.top + j] = p;
     }
 }
 
-// All threads: the choice and the lists by expert.  `write`: whether the choice goes to the caller too.
-__device__ __forceinline__ void route(Args a, Lists &l, bool write) {
+// All threads: the choice and the lists by expert.  `write`: in the first kernel, which gives the choice to the
+// caller too.
+__device__ __forceinline__ void route(const Args &a, Lists &l, bool write) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    if (a.logits) {
-        if (!write) a.ids = nullptr, a.p = nullptr;
-        for (int t = warp; t < a.T; t += nw) choose(a, l, t, lane);
-    } else {
-        // given: a place that names no expert has none; of an expert named twice the first
-        // place gets both weights
-        for (int t = threadIdx.x; t < a.T; t += blockDim.x)
-            for (int j = 0; j < a.top; ++j) {
-                const int at = t * a.top + j;
-                int e = __ldg(a.ids + at);
-                float p = __ldg(a.p + at);
-                if (e < 0 || e >= a.experts) e = -1;
-                for (int i = t * a.top; e >= 0 && i < at; ++i)
-                    if (l.id[i] == e) l.p[i] += p, e = -1;
-                l.id[at] = (int16_t)e, l.p[at] = p;
-            }
-    }
-    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) l.count[e] = 0;
-    __syncthreads();
     const int entries = a.T * a.top;
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) l.count[e] = 0;
+    if (a.logits) {
+        for (int t = warp; t < a.T; t += nw) choose(a, l, t, lane, write);
+    } else {
+        // given: a place that names no expert has none; of an expert named twice the first place
+        // gets both weights
+        for (int i = threadIdx.x; i < entries; i += blockDim.x) {
+            const int e = __ldg(a.ids + i);
+            l.p[i] = __ldg(a.p + i);
+            l.id[i] = (int16_t)(e < 0 || e >= a.experts ? -1 : e);
+        }
+        __syncthreads();
+        const auto again = [&](int i) {  // whether an earlier place of the token names the same expert
+            bool is = false;
+            for (int j = i / a.top * a.top; j < i; ++j) is |= l.id[j] == l.id[i];
+            return is && l.id[i] >= 0;
+        };
+        float p[kMaxEntries / 256];
+        uint32_t twice = 0;
+#pragma unroll
+        for (int k = 0; k < kMaxEntries / 256; ++k) {
+            const int i = threadIdx.x + k * blockDim.x;
+            p[k] = 0.0f;
+            if (i >= entries) break;
+            p[k] = l.p[i];
+            if (again(i)) twice |= 1u << k;
+            else
+                for (int j = i + 1; j < (i / a.top + 1) * a.top; ++j)
+                    if (l.id[j] == l.id[i]) p[k] += l.p[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kMaxEntries / 256; ++k) {
+            const int i = threadIdx.x + k * blockDim.x;
+            if (i >= entries) break;
+            l.p[i] = p[k];
+            if (twice >> k & 1u) l.id[i] = -1;
+        }
+    }
+    __syncthreads();
     if (warp == 0) {
         // an expert's entries in their order (all blocks have to agree on which tile of 8 has one)
         for (int i0 = 0; i0 < entries; i0 += 32) {
@@ -185,7 +221,8 @@ __device__ __forceinline__ void route(Args a, Lists &l, bool write) {
     for (int i = threadIdx.x; i < entries; i += blockDim.x)
         if (l.id[i] >= 0) l.list[l.count[l.id[i]] + l.rank[i]] = (uint16_t)i;
     __syncthreads();
-    for (int i = threadIdx.x; i < l.n; i += blockDim.x) {
+    if (write) return;
+    for (int i = threadIdx.x; i < l.n; i += blockDim.x) {  // (the second kernel's alone)
         uint64_t m = 0;
         for (int j = l.first[i]; j < l.first[i + 1]; ++j) m |= (uint64_t)1 << (l.list[j] / a.top);
         l.tokens[i] = m;
@@ -253,20 +290,20 @@ struct Rows16 {
         }
     }
 };
-// even, odd += their products with the tokens, every second step of k each (two chains of MMAs)
+// acc += their products with the tokens
 template <typename T, bool kF8>
-__device__ __forceinline__ void multiply(float (&even)[4], float (&odd)[4], const Rows16<kF8> &w, const uint32_t (&x)[kPairsOf<kF8>]) {
+__device__ __forceinline__ void multiply(float (&acc)[4], const Rows16<kF8> &w, const uint32_t (&x)[kPairsOf<kF8>]) {
 #pragma unroll
-    for (int i = 0; i < kPairsOf<kF8> / 2; ++i) mma<T>(i & 1 ? odd : even, w.a[i][0], w.a[i][1], w.a[i][2], w.a[i][3], x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < kPairsOf<kF8> / 2; ++i) mma<T>(acc, w.a[i][0], w.a[i][1], w.a[i][2], w.a[i][3], x[2 * i], x[2 * i + 1]);
 }
 // acc += ..., times the scales of the two tiles' blocks and what undoes the tokens' powers of two
 template <bool kF8>
 __device__ __forceinline__ void multiply_scaled(float (&acc)[4], const Rows16<kF8> &w, const uint32_t (&x)[kPairsOf<kF8>], float s0,
                                                 float s1, const float (&unit)[2]) {
-    float even[4] = {0.0f, 0.0f, 0.0f, 0.0f}, odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    multiply<__half, kF8>(even, odd, w, x);
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    multiply<__half, kF8>(part, w, x);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = fmaf(even[k] + odd[k], (k < 2 ? s0 : s1) * unit[k & 1], acc[k]);
+    for (int k = 0; k < 4; ++k) acc[k] = fmaf(part[k], (k < 2 ? s0 : s1) * unit[k & 1], acc[k]);
 }
 
 // ------------------------------------------------------------ G and U
@@ -376,14 +413,11 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
         int64_t scale_at = 0;
         if (kF8 && lane < 2 * tiles)
             scale_at = (((int64_t)e * 2 + (lane & 1)) * row_blocks + (base + 8 * (lane >> 1)) / kFp8Block) * col_blocks;
-        float acc[kUpPairs][4], odd[kF8 ? 1 : kUpPairs][4];
+        float acc[kUpPairs][4];
 #pragma unroll
         for (int j = 0; j < kUpPairs; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                acc[j][k] = 0.0f;
-                if (!kF8) odd[kF8 ? 0 : j][k] = 0.0f;
-            }
+            for (int k = 0; k < 4; ++k) acc[j][k] = 0.0f;
         for (int k = begin(un); k < pieces; k += W) {
             uint32_t tok[kPairs];
             float unit[2] = {1.0f, 1.0f}, scale = 1.0f;
@@ -422,7 +456,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
                     if constexpr (kF8)
                         multiply_scaled<true>(acc[j], w, tok, __shfl_sync(0xffffffffu, scale, 2 * j), __shfl_sync(0xffffffffu, scale, 2 * j + 1), unit);
                     else
-                        multiply<TX, false>(acc[j], odd[kF8 ? 0 : j], w, tok);
+                        multiply<TX, false>(acc[j], w, tok);
                 }
                 fetch(j);
             }
@@ -436,7 +470,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
             for (int j = 0; j < kUpPairs; ++j)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (j < tiles) sums[warp * kSums + (j * 4 + q) * 32 + lane] = acc[j][q] + (kF8 ? 0.0f : odd[kF8 ? 0 : j][q]);
+                    if (j < tiles) sums[warp * kSums + (j * 4 + q) * 32 + lane] = acc[j][q];
         }
         __syncthreads();  // (two buffers: the next unit's sums are written while a slow warp still reads these)
         const int meet = pieces < W ? pieces : W, w0 = un * (pieces % W) % W;  // those that had a piece, in their order
@@ -473,6 +507,7 @@ template <typename TX, bool kF8, int NB>
 __global__ void __launch_bounds__(32 * kDownWarps<NB>, 1) k_moe_down(const Args a) {
     constexpr int kBytes = kF8 ? 1 : 2, W = kDownWarps<NB>, NP = kDownPairs, NI = NB < 2 ? NB : 2, kPairs = kPairsOf<kF8>;
     constexpr int D = 16 / W;  // steps whose pieces are under way
+    constexpr int kAtOnce = 8 * NI, kBatch = NB > 2 ? 8 : 4;  // tokens staged at a time, and loaded at a time
     constexpr int kEach = kPairs / 4;  // a lane's values of a token's piece: 4, or 2
     constexpr bool kSplit = !kF8 && __is_same(TX, __nv_bfloat16);  // a as two bf16 numbers
     constexpr int kSums = NB * NP * 128;
@@ -531,16 +566,13 @@ __global__ void __launch_bounds__(32 * kDownWarps<NB>, 1) k_moe_down(const Args 
         }
         if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's results are read from here on
         waited = true;
-        float acc[NB][NP][4], odd[kSplit ? NB : 1][NP][4];
+        float acc[NB][NP][4];
 #pragma unroll
         for (int m = 0; m < NB; ++m)
 #pragma unroll
             for (int j = 0; j < NP; ++j)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    acc[m][j][k] = 0.0f;
-                    if (kSplit) odd[kSplit ? m : 0][j][k] = 0.0f;
-                }
+                for (int k = 0; k < 4; ++k) acc[m][j][k] = 0.0f;
         int bi = warp / pieces, bk = warp - bi * pieces;
         for (int b = warp; b < all; b += W) {
             const uint64_t tokens = l.tokens[bi];
@@ -548,66 +580,91 @@ __global__ void __launch_bounds__(32 * kDownWarps<NB>, 1) k_moe_down(const Args 
             float scale = 1.0f;  // lane i: tile i's
             if (kF8 && lane < tiles) scale = a.down_scales.at(((int64_t)l.active[bi] * row_blocks + (base + 8 * lane) / kFp8Block) * col_blocks + bk);
             if (D == 2) cp_async_wait<NP>();
+            const auto value = [&](int id, float (&v)[kEach]) {
 #pragma unroll
-            for (int m0 = 0; m0 < NB; m0 += NI) {
-                const bool last = m0 + NI >= NB;
-                const uint32_t here = (uint32_t)(tokens >> (8 * m0)) & (NI == 2 ? 0xffffu : 0xffu);
-                if (!here && !last) continue;
-                // the expert's tokens among these, four at a time
+                for (int q = 0; q < kEach; ++q) v[q] = 0.0f;
+                if (at >= a.inner) return;
+                const float *const p = a.a + (int64_t)id * a.inner + at;
+                if constexpr (kEach == 4) {
+                    const float4 f = __ldcg(reinterpret_cast<const float4 *>(p));
+                    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+                } else {
+                    const float2 f = __ldcg(reinterpret_cast<const float2 *>(p));
+                    v[0] = f.x, v[1] = f.y;
+                }
+            };
+            const auto stage = [&](int row, const float (&v)[kEach]) {
+                uint8_t *const o = staged + row * kStaged;
+                if constexpr (kSplit) {
+                    const uint32_t h = pack_bf16x2(v[0], v[1]);
+                    *reinterpret_cast<uint32_t *>(o + lane * 4) = h;
+                    *reinterpret_cast<uint32_t *>(o + 128 + lane * 4) = pack_bf16x2(v[0] - bf16lo(h), v[1] - bf16hi(h));
+                } else {
+                    float amax = 0.0f, unit;
+#pragma unroll
+                    for (int q = 0; q < kEach; ++q) amax = fmaxf(amax, fabsf(v[q]));
+                    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+                    const float m = power_of(amax, unit);
+                    if constexpr (kEach == 4)
+                        *reinterpret_cast<uint2 *>(o + lane * 8) = make_uint2(half2_of(v[0] * m, v[1] * m), half2_of(v[2] * m, v[3] * m));
+                    else
+                        *reinterpret_cast<uint32_t *>(o + lane * 4) = half2_of(v[0] * m, v[1] * m);
+                    if (lane == 0) units[row] = unit;
+                }
+            };
+            // The expert's tokens are staged 16 at a time in their order, where all that there are fit
+            // at the token's place.
+            constexpr bool kOnce = NB == NI;
+            const int n = kOnce ? 1 : l.first[bi + 1] - first;
+            for (int c0 = 0; c0 < n; c0 += kAtOnce) {
+                uint64_t staged_tokens = tokens;
                 __syncwarp();
-                int next = first + __popcll(tokens & (((uint64_t)1 << (8 * m0)) - 1));
-                for (uint32_t left = here; left;) {
-                    float v[4][kEach];
-                    uint32_t rest = left;
-                    int n = 0;
+                if constexpr (kOnce) {
+                    int next = first;
+                    for (uint32_t left = (uint32_t)tokens; left; next += kBatch) {
+                        float v[kBatch][kEach];
+                        const int some = __popc(left);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < kBatch; ++i)
+                            if (i < some) value(l.list[next + i], v[i]);
 #pragma unroll
-                        for (int q = 0; q < kEach; ++q) v[i][q] = 0.0f;
-                        if (!rest) continue;
-                        rest &= rest - 1, ++n;
-                        const float *const p = a.a + (int64_t)l.list[next + i] * a.inner + at;
-                        if (at >= a.inner) continue;
-                        if constexpr (kEach == 4) {
-                            const float4 f = __ldcg(reinterpret_cast<const float4 *>(p));
-                            v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
-                        } else {
-                            const float2 f = __ldcg(reinterpret_cast<const float2 *>(p));
-                            v[i][0] = f.x, v[i][1] = f.y;
+                        for (int i = 0; i < kBatch; ++i) {
+                            if (!left) continue;
+                            stage(__ffs(left) - 1, v[i]);
+                            left &= left - 1;
                         }
                     }
-                    next += n;
+                } else {
+                    const int cn = n - c0 < kAtOnce ? n - c0 : kAtOnce;
+                    for (int j0 = 0; j0 < cn; j0 += kBatch) {
+                        float v[kBatch][kEach];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (!left) continue;
-                        const int t = __ffs(left) - 1;
-                        left &= left - 1;
-                        uint8_t *const o = staged + t * kStaged;
-                        if constexpr (kSplit) {
-                            const uint32_t h = pack_bf16x2(v[i][0], v[i][1]);
-                            *reinterpret_cast<uint32_t *>(o + lane * 4) = h;
-                            *reinterpret_cast<uint32_t *>(o + 128 + lane * 4) = pack_bf16x2(v[i][0] - bf16lo(h), v[i][1] - bf16hi(h));
-                        } else {
-                            float amax = 0.0f, unit;
+                        for (int i = 0; i < kBatch; ++i)
+                            if (j0 + i < cn) value(l.list[first + c0 + j0 + i], v[i]);
 #pragma unroll
-                            for (int q = 0; q < kEach; ++q) amax = fmaxf(amax, fabsf(v[i][q]));
-                            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-                            const float m = power_of(amax, unit);
-                            if constexpr (kEach == 4)
-                                *reinterpret_cast<uint2 *>(o + lane * 8) = make_uint2(half2_of(v[i][0] * m, v[i][1] * m), half2_of(v[i][2] * m, v[i][3] * m));
-                            else
-                                *reinterpret_cast<uint32_t *>(o + lane * 4) = half2_of(v[i][0] * m, v[i][1] * m);
-                            if (lane == 0) units[t] = unit;
-                        }
+                        for (int i = 0; i < kBatch; ++i)
+                            if (j0 + i < cn) stage(j0 + i, v[i]);
+                    }
+                    if (n > kAtOnce) {  // without the tokens of the times before and after
+                        for (int i = 0; i < c0; ++i) staged_tokens &= staged_tokens - 1;
+                        uint64_t rest = staged_tokens;
+                        for (int i = 0; i < cn; ++i) rest &= rest - 1;
+                        staged_tokens &= ~rest;
                     }
                 }
                 __syncwarp();
+                const auto place_of = [&](int t) { return kOnce ? t : __popcll(staged_tokens & (((uint64_t)1 << t) - 1)); };
+#pragma unroll
+                for (int m0 = 0; m0 < NB; m0 += NI) {
+                const bool last = c0 + kAtOnce >= n && m0 + NI >= NB;
+                const uint32_t here = (uint32_t)(staged_tokens >> (8 * m0)) & (NI == 2 ? 0xffffu : 0xffu);
+                if (!here && !last) continue;
                 uint32_t tok[NI][kPairs], low[kSplit ? NI : 1][kPairs];
                 float unit[NI][2];
 #pragma unroll
                 for (int m = 0; m < NI; ++m) {
                     const bool has = here >> (8 * m + g) & 1u;
-                    const uint8_t *const p = staged + (8 * m + g) * kStaged;
+                    const uint8_t *const p = staged + place_of(8 * (m0 + m) + g) * kStaged;
 #pragma unroll
                     for (int s = 0; s < kPairs / 4; ++s) {
                         const int off = kF8 ? (s >> 1) * 128 + t4 * 32 + (s & 1) * 16 : s * 64 + t4 * 16;
@@ -621,7 +678,7 @@ __global__ void __launch_bounds__(32 * kDownWarps<NB>, 1) k_moe_down(const Args 
                     }
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
-                        unit[m][q] = !kSplit && (here >> (8 * m + 2 * t4 + q) & 1u) ? units[8 * m + 2 * t4 + q] : 0.0f;
+                        unit[m][q] = !kSplit && (here >> (8 * m + 2 * t4 + q) & 1u) ? units[place_of(8 * (m0 + m) + 2 * t4 + q)] : 0.0f;
                 }
 #pragma unroll
                 for (int j = 0; j < NP; ++j) {
@@ -634,14 +691,15 @@ __global__ void __launch_bounds__(32 * kDownWarps<NB>, 1) k_moe_down(const Args 
                         for (int m = 0; m < NI; ++m) {
                             if (!(here >> (8 * m) & 0xffu)) continue;
                             if constexpr (kSplit) {
-                                multiply<TX, false>(acc[m0 + m][j], odd[kSplit ? m0 + m : 0][j], w, tok[m]);
-                                multiply<TX, false>(acc[m0 + m][j], odd[kSplit ? m0 + m : 0][j], w, low[kSplit ? m : 0]);
+                                multiply<TX, false>(acc[m0 + m][j], w, tok[m]);
+                                multiply<TX, false>(acc[m0 + m][j], w, low[kSplit ? m : 0]);
                             } else {
                                 multiply_scaled<kF8>(acc[m0 + m][j], w, tok[m], s0, s1, unit[m]);
                             }
                         }
                     }
                     if (last) fetch(j);
+                }
                 }
             }
             advance();
@@ -656,7 +714,7 @@ __global__ void __launch_bounds__(32 * kDownWarps<NB>, 1) k_moe_down(const Args 
             for (int j = 0; j < NP; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    red[warp * kSums + ((m * NP + j) * 4 + k) * 32 + lane] = acc[m][j][k] + (kSplit ? odd[kSplit ? m : 0][j][k] : 0.0f);
+                    red[warp * kSums + ((m * NP + j) * 4 + k) * 32 + lane] = acc[m][j][k];
         __syncthreads();
         const int meet = all < W ? all : W;
         for (int o = threadIdx.x; o < kSums; o += 32 * W) {
