@@ -124,9 +124,7 @@ def load():
         return lib
 
 
-def snapshot():
-    """The function snapshot of the module _tensors: bytes that tell whether any of a
-    list of tensors has changed its place, type, sizes or strides."""
+def _checked_tensors():
     import torch
     try:
         from . import _tensors
@@ -136,7 +134,24 @@ def snapshot():
     if _tensors.torch_version != torch.__version__:
         raise RuntimeError("_tensors.so was built for torch %s, this is %s; run "
                            "`python -c 'import __graft_entry__ as g; g.build()'`" % (_tensors.torch_version, torch.__version__))
-    return _tensors.snapshot
+    return _tensors
+
+
+_tensors_module = None
+
+
+def tensors():
+    """The module _tensors (csrc/py_tensors.cpp), looked for once."""
+    global _tensors_module
+    if _tensors_module is None:
+        _tensors_module = _checked_tensors()
+    return _tensors_module
+
+
+def snapshot():
+    """The function snapshot of the module _tensors: bytes that tell whether any of a
+    list of tensors has changed its place, type, sizes or strides."""
+    return _checked_tensors().snapshot
 
 
 def call(name, *args):
