@@ -34,9 +34,8 @@ namespace moe {
 constexpr int kMaxTokens = 64, kMaxTop = 16, kMaxExperts = 1024, kMaxEntries = kMaxTokens * kMaxTop;
 constexpr int kCell = 1024;       // bytes of a piece: 8 rows of 128 bytes
 constexpr int kUpWarps = 16, kUpPairs = 4;  // pairs of row tiles (of G and of U) of a unit
-constexpr int kDownPairs = 3;               // pairs of row tiles of a pass
+constexpr int kDownWarps = 16, kDownPairs = 3;  // ... of a pass
 constexpr int kUpRing = kUpPairs * 2 * kCell, kDownRing = kDownPairs * 2 * kCell;  // of a warp: the pieces of a step
-constexpr int kStaged = 272;                // bytes between staged tokens (16 more than they have: no two of a read meet in a bank)
 
 struct Args {
     const void *x;
@@ -63,7 +62,8 @@ struct Lists {
     uint16_t active[kMaxExperts];    // experts with entries, ascending
     uint16_t first[kMaxExperts + 1]; // of the i-th of these: its first place in `list`
     uint16_t tiles[kMaxExperts + 1]; // ... and the tiles of 8 entries of those before it
-    uint64_t tokens[kMaxExperts];    // ... its tokens, as bits
+    uint16_t of_tile[kMaxEntries];   // of a tile of 8 entries: which of these
+    uint8_t token[kMaxEntries];      // of a place in `list`: its token
     int count[kMaxExperts];
     int n;                           // how many experts have entries
 };
@@ -219,14 +219,12 @@ __device__ __forceinline__ void route(const Args &a, Lists &l, bool write) {
     }
     __syncthreads();
     for (int i = threadIdx.x; i < entries; i += blockDim.x)
-        if (l.id[i] >= 0) l.list[l.count[l.id[i]] + l.rank[i]] = (uint16_t)i;
-    __syncthreads();
-    if (write) return;
-    for (int i = threadIdx.x; i < l.n; i += blockDim.x) {  // (the second kernel's alone)
-        uint64_t m = 0;
-        for (int j = l.first[i]; j < l.first[i + 1]; ++j) m |= (uint64_t)1 << (l.list[j] / a.top);
-        l.tokens[i] = m;
-    }
+        if (l.id[i] >= 0) {
+            const int at = l.count[l.id[i]] + l.rank[i];
+            l.list[at] = (uint16_t)i, l.token[at] = (uint8_t)(i / a.top);
+        }
+    for (int i = threadIdx.x; i < l.n; i += blockDim.x)
+        for (int t = l.tiles[i]; t < l.tiles[i + 1]; ++t) l.of_tile[t] = (uint16_t)i;
     __syncthreads();
 }
 
@@ -317,14 +315,8 @@ struct Unit {
     // The place of the weighted row `at`: the expert, and its row.
     static __device__ __forceinline__ void place(const Args &a, const Lists &l, int64_t at, int &i, int &row) {
         const int tile = (int)(at / a.inner);
-        int lo = 0, hi = l.n;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (l.tiles[mid] <= tile) lo = mid;
-            else hi = mid;
-        }
         if (tile >= l.tiles[l.n]) i = l.n, row = 0;
-        else i = lo, row = (int)((at - (int64_t)l.tiles[lo] * a.inner) / (l.tiles[lo + 1] - l.tiles[lo]));
+        else i = l.of_tile[tile], row = (int)((at - (int64_t)l.tiles[i] * a.inner) / (l.tiles[i + 1] - l.tiles[i]));
     }
     __device__ __forceinline__ bool chunk(const Args &a, int row) {  // the unit that begins with a row, if there is one
         while (i < last && row >= a.inner) ++i, row = 0;
@@ -407,7 +399,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
         // this lane's token
         const int e = l.active[u.i], entry0 = l.first[u.i] + 8 * u.m, end = l.first[u.i + 1];
         const bool has = entry0 + g < end;
-        const TX *const x = static_cast<const TX *>(a.x) + (has ? (int64_t)(l.list[entry0 + g] / a.top) * a.xs : 0);
+        const TX *const x = static_cast<const TX *>(a.x) + (has ? (int64_t)l.token[entry0 + g] * a.xs : 0);
         const int base = u.lo & ~7, tiles = (u.hi - base + 7) / 8;
         // lane 2 j + (0: G, 1: U) looks after the scale of pair j
         int64_t scale_at = 0;
@@ -494,55 +486,47 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
 }
 
 // ------------------------------------------------------------ D
-// A block's rows of the output, in passes of kDownPairs pairs of tiles of 8; NB tiles of 8
-// tokens, looked at NI at a time.  Steps: a piece of 128 bytes of every row of one expert; they
-// go round the warps.  A warp stages the activations of the expert's tokens over the
-// step's piece, as the MMA wants them, in shared memory.
-template <int NB>
-constexpr int kDownWarps = NB > 2 ? 8 : 16;  // (the sums of 32 and 64 tokens take the registers of 16 warps)
-template <int NB>
-constexpr int kStage = 8 * (NB < 2 ? NB : 2) * (kStaged + 4);  // of a warp: staged tokens, what undoes their powers of two
-
-template <typename TX, bool kF8, int NB>
-__global__ void __launch_bounds__(32 * kDownWarps<NB>, 1) k_moe_down(const Args a) {
-    constexpr int kBytes = kF8 ? 1 : 2, W = kDownWarps<NB>, NP = kDownPairs, NI = NB < 2 ? NB : 2, kPairs = kPairsOf<kF8>;
-    constexpr int D = 16 / W;  // steps whose pieces are under way
-    constexpr int kAtOnce = 8 * NI, kBatch = NB > 2 ? 8 : 4;  // tokens staged at a time, and loaded at a time
-    constexpr int kEach = kPairs / 4;  // a lane's values of a token's piece: 4, or 2
+// A block's rows of the output, in passes of kDownPairs pairs of tiles of 8 rows.  The tiles of 8
+// entries follow one another in rounds: of a tile's contraction each warp has a piece, or several
+// tiles share a round where pieces are few.  The warps' sums meet in shared memory, where each
+// token's are added up expert by expert.
+template <typename TX, bool kF8>
+__global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
+    constexpr int kBytes = kF8 ? 1 : 2, W = kDownWarps, NP = kDownPairs, kPairs = kPairsOf<kF8>, kRows = 16 * NP;
     constexpr bool kSplit = !kF8 && __is_same(TX, __nv_bfloat16);  // a as two bf16 numbers
-    constexpr int kSums = NB * NP * 128;
     extern __shared__ __align__(128) uint8_t smem[];
-    float *const red = reinterpret_cast<float *>(smem);  // [warp][tokens' tile][pair][4][lane], where the pieces were
-    Lists &l = *reinterpret_cast<Lists *>(smem + 16 * kDownRing + 16 * kStage<2>);
-    static_assert(W * kSums * 4 <= 16 * kDownRing, "the sums meet where the pieces were");
-    static_assert(NB == NI ? D == 1 : D == 2, "a step's pieces are waited for one by one, or all at once");
+    float *const red = reinterpret_cast<float *>(smem + W * kDownRing);  // [2][warp][pair][4][lane]
+    float *const out = red + 2 * W * NP * 128;                           // [token][row]
+    Lists &l = *reinterpret_cast<Lists *>(out + kMaxTokens * kRows);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     route(a, l, false);
     const int from = (int)((int64_t)a.d * blockIdx.x / gridDim.x), to = (int)((int64_t)a.d * (blockIdx.x + 1) / gridDim.x);
-    const int row_bytes = a.inner * kBytes, pieces = (row_bytes + 127) / 128, all = l.n * pieces;
+    const int row_bytes = a.inner * kBytes, pieces = (row_bytes + 127) / 128, all = l.tiles[l.n];
     const int row_blocks = (a.d + kFp8Block - 1) / kFp8Block, col_blocks = (a.inner + kFp8Block - 1) / kFp8Block;
     const int64_t matrix = (int64_t)a.d * row_bytes, tile_bytes = 8 * (int64_t)row_bytes;
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * D * kDownRing + lane * 16);
-    uint8_t *const staged = smem + 16 * kDownRing + warp * kStage<NB>;
-    float *const units = reinterpret_cast<float *>(staged + 8 * NI * kStaged);
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kDownRing + lane * 16);
+    // tiles of a round, this warp's among them and its first piece
+    const int share = pieces <= W / 2 ? W / pieces : 1, mine = share > 1 ? warp / pieces : 0, k0 = share > 1 ? warp - mine * pieces : warp;
+    const bool works = mine < share && k0 < pieces;
     bool waited = false;
-    for (int base = from & ~7; base < to; base += 16 * NP) {
+    for (int base = from & ~7; base < to; base += kRows) {
         const int tiles = (to - base + 7) / 8 < 2 * NP ? (to - base + 7) / 8 : 2 * NP;
         uint32_t rows = 0;  // which tiles have this lane's row
 #pragma unroll
         for (int i = 0; i < 2 * NP; ++i) rows |= (uint32_t)(base + 8 * i + g >= from && base + 8 * i + g < to) << i;
-        int ahead = warp, ai = warp / pieces, ak = warp - ai * pieces;
-        const uint8_t *lane_row = a.down;
+        for (int o = threadIdx.x; o < a.T * kRows; o += 32 * W) out[o] = 0.0f;
+        // copies run a step ahead
+        int ahead = works ? mine : all, ak = k0;
         uint32_t there = 0;
+        const uint8_t *lane_row = a.down;
         const auto aim = [&]() {
             there = 0;
             if (ahead >= all) return;
             there = rows;
-            lane_row = a.down + (int64_t)l.active[ai] * matrix + (int64_t)(base + g) * row_bytes + ak * 128 + t4 * 16;
+            lane_row = a.down + (int64_t)l.active[l.of_tile[ahead]] * matrix + (int64_t)(base + g) * row_bytes + ak * 128 + t4 * 16;
         };
-        uint32_t place = ring;  // the step's
         const auto fetch = [&](int j) {
-            const uint32_t to_pair = place + (uint32_t)(j * 2 * kCell);
+            const uint32_t to_pair = ring + (uint32_t)(j * 2 * kCell);
             const bool first_half = ak * 128 + t4 * 16 < row_bytes, second_half = ak * 128 + t4 * 16 + 64 < row_bytes;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -551,179 +535,117 @@ __global__ void __launch_bounds__(32 * kDownWarps<NB>, 1) k_moe_down(const Args 
             }
             cp_async_commit();
         };
-        const auto advance = [&]() {
-            ahead += W, ak += W;
-            while (ak >= pieces) ak -= pieces, ++ai;
-            aim();
-            if (D == 2) place = place == ring ? ring + kDownRing : ring;
+        const auto advance = [&](int &tile, int &k) {  // this warp's next step
+            k += W;
+            if (k >= pieces) k = k0, tile += share;
         };
         aim();
 #pragma unroll
-        for (int s = 0; s < D; ++s) {
-#pragma unroll
-            for (int j = 0; j < NP; ++j) fetch(j);
-            advance();
-        }
+        for (int j = 0; j < NP; ++j) fetch(j);
+        advance(ahead, ak);
+        aim();
         if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's results are read from here on
         waited = true;
-        float acc[NB][NP][4];
+        // a step's activations (token lane / 4 of the tile) and scales (lane i: row tile i's), a step ahead too
+        float4 raw[kPairs / 2];
+        float scale_next = 1.0f;
+        const auto load_tokens = [&](int tile, int k) {
+            if (tile >= all) return;
+            const int i = l.of_tile[tile], entry = l.first[i] + 8 * (tile - l.tiles[i]) + g;
+            const bool has = entry < l.first[i + 1];
+            const float *const p = a.a + (has ? (int64_t)l.list[entry] * a.inner : 0);
 #pragma unroll
-        for (int m = 0; m < NB; ++m)
+            for (int q = 0; q < kPairs / 2; ++q) {
+                const int c = kF8 ? k * 128 + (q >> 2) * 64 + t4 * 16 + (q & 3) * 4 : k * 64 + (q >> 1) * 32 + t4 * 8 + (q & 1) * 4;
+                raw[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (has && c < a.inner) raw[q] = __ldcg(reinterpret_cast<const float4 *>(p + c));
+            }
+            if (kF8 && lane < tiles) scale_next = a.down_scales.at(((int64_t)l.active[i] * row_blocks + (base + 8 * lane) / kFp8Block) * col_blocks + k);
+        };
+        int tile = works ? mine : all, k = k0, buf = 0;
+        load_tokens(tile, k);
+        for (int r0 = 0; r0 < all; r0 += share, buf ^= 1) {
+            float *const sums = red + buf * W * NP * 128;
+            if (tile < all) {
+                float acc[NP][4];
 #pragma unroll
-            for (int j = 0; j < NP; ++j)
+                for (int j = 0; j < NP; ++j)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[m][j][k] = 0.0f;
-        int bi = warp / pieces, bk = warp - bi * pieces;
-        for (int b = warp; b < all; b += W) {
-            const uint64_t tokens = l.tokens[bi];
-            const int first = l.first[bi], at = bk * (2 * kPairs * 4) + lane * kEach;
-            float scale = 1.0f;  // lane i: tile i's
-            if (kF8 && lane < tiles) scale = a.down_scales.at(((int64_t)l.active[bi] * row_blocks + (base + 8 * lane) / kFp8Block) * col_blocks + bk);
-            if (D == 2) cp_async_wait<NP>();
-            const auto value = [&](int id, float (&v)[kEach]) {
+                    for (int q = 0; q < 4; ++q) acc[j][q] = 0.0f;
+                bool more = true;
+                while (more) {
+                    uint32_t tok[kPairs], low[kSplit ? kPairs : 1];
+                    float unit[2] = {1.0f, 1.0f};
+                    const float *const f = reinterpret_cast<const float *>(raw);
+                    if constexpr (kSplit) {
 #pragma unroll
-                for (int q = 0; q < kEach; ++q) v[q] = 0.0f;
-                if (at >= a.inner) return;
-                const float *const p = a.a + (int64_t)id * a.inner + at;
-                if constexpr (kEach == 4) {
-                    const float4 f = __ldcg(reinterpret_cast<const float4 *>(p));
-                    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-                } else {
-                    const float2 f = __ldcg(reinterpret_cast<const float2 *>(p));
-                    v[0] = f.x, v[1] = f.y;
-                }
-            };
-            const auto stage = [&](int row, const float (&v)[kEach]) {
-                uint8_t *const o = staged + row * kStaged;
-                if constexpr (kSplit) {
-                    const uint32_t h = pack_bf16x2(v[0], v[1]);
-                    *reinterpret_cast<uint32_t *>(o + lane * 4) = h;
-                    *reinterpret_cast<uint32_t *>(o + 128 + lane * 4) = pack_bf16x2(v[0] - bf16lo(h), v[1] - bf16hi(h));
-                } else {
-                    float amax = 0.0f, unit;
-#pragma unroll
-                    for (int q = 0; q < kEach; ++q) amax = fmaxf(amax, fabsf(v[q]));
-                    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-                    const float m = power_of(amax, unit);
-                    if constexpr (kEach == 4)
-                        *reinterpret_cast<uint2 *>(o + lane * 8) = make_uint2(half2_of(v[0] * m, v[1] * m), half2_of(v[2] * m, v[3] * m));
-                    else
-                        *reinterpret_cast<uint32_t *>(o + lane * 4) = half2_of(v[0] * m, v[1] * m);
-                    if (lane == 0) units[row] = unit;
-                }
-            };
-            // The expert's tokens are staged 16 at a time in their order, where all that there are fit
-            // at the token's place.
-            constexpr bool kOnce = NB == NI;
-            const int n = kOnce ? 1 : l.first[bi + 1] - first;
-            for (int c0 = 0; c0 < n; c0 += kAtOnce) {
-                uint64_t staged_tokens = tokens;
-                __syncwarp();
-                if constexpr (kOnce) {
-                    int next = first;
-                    for (uint32_t left = (uint32_t)tokens; left; next += kBatch) {
-                        float v[kBatch][kEach];
-                        const int some = __popc(left);
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            if (i < some) value(l.list[next + i], v[i]);
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i) {
-                            if (!left) continue;
-                            stage(__ffs(left) - 1, v[i]);
-                            left &= left - 1;
+                        for (int q = 0; q < kPairs; ++q) {
+                            tok[q] = pack_bf16x2(f[2 * q], f[2 * q + 1]);
+                            low[kSplit ? q : 0] = pack_bf16x2(f[2 * q] - bf16lo(tok[q]), f[2 * q + 1] - bf16hi(tok[q]));
                         }
+                    } else {
+                        float amax = 0.0f, own;
+#pragma unroll
+                        for (int q = 0; q < 2 * kPairs; ++q) amax = fmaxf(amax, fabsf(f[q]));
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                        const float m = power_of(amax, own);
+#pragma unroll
+                        for (int q = 0; q < kPairs; ++q) tok[q] = half2_of(f[2 * q] * m, f[2 * q + 1] * m);
+                        unit[0] = __shfl_sync(0xffffffffu, own, 8 * t4), unit[1] = __shfl_sync(0xffffffffu, own, 8 * t4 + 4);
                     }
-                } else {
-                    const int cn = n - c0 < kAtOnce ? n - c0 : kAtOnce;
-                    for (int j0 = 0; j0 < cn; j0 += kBatch) {
-                        float v[kBatch][kEach];
+                    const float scale = scale_next;
+                    const int was = tile;
+                    advance(tile, k);
+                    load_tokens(tile, k);
 #pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            if (j0 + i < cn) value(l.list[first + c0 + j0 + i], v[i]);
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            if (j0 + i < cn) stage(j0 + i, v[i]);
-                    }
-                    if (n > kAtOnce) {  // without the tokens of the times before and after
-                        for (int i = 0; i < c0; ++i) staged_tokens &= staged_tokens - 1;
-                        uint64_t rest = staged_tokens;
-                        for (int i = 0; i < cn; ++i) rest &= rest - 1;
-                        staged_tokens &= ~rest;
-                    }
-                }
-                __syncwarp();
-                const auto place_of = [&](int t) { return kOnce ? t : __popcll(staged_tokens & (((uint64_t)1 << t) - 1)); };
-#pragma unroll
-                for (int m0 = 0; m0 < NB; m0 += NI) {
-                const bool last = c0 + kAtOnce >= n && m0 + NI >= NB;
-                const uint32_t here = (uint32_t)(staged_tokens >> (8 * m0)) & (NI == 2 ? 0xffffu : 0xffu);
-                if (!here && !last) continue;
-                uint32_t tok[NI][kPairs], low[kSplit ? NI : 1][kPairs];
-                float unit[NI][2];
-#pragma unroll
-                for (int m = 0; m < NI; ++m) {
-                    const bool has = here >> (8 * m + g) & 1u;
-                    const uint8_t *const p = staged + place_of(8 * (m0 + m) + g) * kStaged;
-#pragma unroll
-                    for (int s = 0; s < kPairs / 4; ++s) {
-                        const int off = kF8 ? (s >> 1) * 128 + t4 * 32 + (s & 1) * 16 : s * 64 + t4 * 16;
-                        uint4 v = make_uint4(0, 0, 0, 0), w = v;
-                        if (has) {
-                            v = *reinterpret_cast<const uint4 *>(p + off);
-                            if (kSplit) w = *reinterpret_cast<const uint4 *>(p + 128 + off);
-                        }
-                        tok[m][4 * s] = v.x, tok[m][4 * s + 1] = v.y, tok[m][4 * s + 2] = v.z, tok[m][4 * s + 3] = v.w;
-                        if (kSplit) low[kSplit ? m : 0][4 * s] = w.x, low[kSplit ? m : 0][4 * s + 1] = w.y, low[kSplit ? m : 0][4 * s + 2] = w.z, low[kSplit ? m : 0][4 * s + 3] = w.w;
-                    }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        unit[m][q] = !kSplit && (here >> (8 * m + 2 * t4 + q) & 1u) ? units[place_of(8 * (m0 + m) + 2 * t4 + q)] : 0.0f;
-                }
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    if (D == 1) cp_async_wait<NP - 1>();
-                    if (here && 2 * j < tiles) {
-                        const uint32_t from_pair = place + (uint32_t)(j * 2 * kCell);
-                        const Rows16<kF8> w(read_piece(from_pair), read_piece(from_pair + kCell));
-                        const float s0 = __shfl_sync(0xffffffffu, scale, 2 * j), s1 = __shfl_sync(0xffffffffu, scale, 2 * j + 1);
-#pragma unroll
-                        for (int m = 0; m < NI; ++m) {
-                            if (!(here >> (8 * m) & 0xffu)) continue;
+                    for (int j = 0; j < NP; ++j) {
+                        cp_async_wait<NP - 1>();
+                        if (2 * j < tiles) {
+                            const uint32_t from_pair = ring + (uint32_t)(j * 2 * kCell);
+                            const Rows16<kF8> w(read_piece(from_pair), read_piece(from_pair + kCell));
                             if constexpr (kSplit) {
-                                multiply<TX, false>(acc[m0 + m][j], w, tok[m]);
-                                multiply<TX, false>(acc[m0 + m][j], w, low[kSplit ? m : 0]);
+                                multiply<TX, false>(acc[j], w, tok);
+                                multiply<TX, false>(acc[j], w, low);
                             } else {
-                                multiply_scaled<kF8>(acc[m0 + m][j], w, tok[m], s0, s1, unit[m]);
+                                multiply_scaled<kF8>(acc[j], w, tok, __shfl_sync(0xffffffffu, scale, 2 * j), __shfl_sync(0xffffffffu, scale, 2 * j + 1), unit);
                             }
                         }
+                        fetch(j);
                     }
-                    if (last) fetch(j);
+                    advance(ahead, ak);
+                    aim();
+                    more = tile == was;
                 }
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) sums[(warp * NP + j) * 128 + q * 32 + lane] = acc[j][q];
+            }
+            __syncthreads();  // (two buffers: the next round's sums are written while a slow warp still reads these)
+            // A thread has a row and every eighth token: nobody else adds to its sums.
+            const int row = (int)threadIdx.x % kRows, eighth = (int)threadIdx.x / kRows;
+            if (eighth < 8) {
+                const int j = row >> 4, h = row >> 3 & 1;
+                for (int t = 0; t < share && r0 + t < all; ++t) {
+                    const int i = l.of_tile[r0 + t], entry0 = l.first[i] + 8 * (r0 + t - l.tiles[i]), n = l.first[i + 1] - entry0;
+                    const int first = share > 1 ? t * pieces : 0, meet = share > 1 || pieces < W ? pieces : W;
+                    for (int e = 0; e < 8 && e < n; ++e) {
+                        const int token = l.token[entry0 + e];
+                        if ((token & 7) != eighth) continue;
+                        const float *const of_w = sums + (first * NP + j) * 128 + (2 * h + (e & 1)) * 32 + (row & 7) * 4 + (e >> 1);
+                        float v = 0.0f;
+                        for (int w = 0; w < meet; ++w) v += of_w[w * NP * 128];
+                        out[token * kRows + row] += v;
+                    }
                 }
             }
-            advance();
-            bk += W;
-            while (bk >= pieces) bk -= pieces, ++bi;
         }
         cp_async_wait<0>();
         __syncthreads();
-#pragma unroll
-        for (int m = 0; m < NB; ++m)
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    red[warp * kSums + ((m * NP + j) * 4 + k) * 32 + lane] = acc[m][j][k];
-        __syncthreads();
-        const int meet = all < W ? all : W;
-        for (int o = threadIdx.x; o < kSums; o += 32 * W) {
-            const int m = o / (NP * 128), j = o / 128 % NP, k = o / 32 % 4;  // (o % 32 is this lane)
-            const int tok = 8 * m + 2 * t4 + (k & 1), row = base + 16 * j + 8 * (k >> 1) + g;
-            if (tok >= a.T || row < from || row >= to) continue;
-            float v = 0.0f;
-            for (int w = 0; w < meet; ++w) v += red[w * kSums + o];
-            static_cast<TX *>(a.y)[(int64_t)tok * a.ys + row] = from_f<TX>(v);
+        for (int o = threadIdx.x; o < a.T * kRows; o += 32 * W) {
+            const int token = o / kRows, row = base + o - token * kRows;
+            if (row >= from && row < to) static_cast<TX *>(a.y)[(int64_t)token * a.ys + row] = from_f<TX>(out[o]);
         }
         __syncthreads();
     }
@@ -731,7 +653,7 @@ __global__ void __launch_bounds__(32 * kDownWarps<NB>, 1) k_moe_down(const Args 
 
 constexpr int kDevices = 64;
 constexpr int kUpSmem = kUpWarps * kUpRing + 2 * kUpWarps * kUpPairs * 128 * 4 + (int)sizeof(Lists);
-constexpr int kDownSmem = 16 * kDownRing + 16 * kStage<2> + (int)sizeof(Lists);
+constexpr int kDownSmem = kDownWarps * kDownRing + 2 * kDownWarps * kDownPairs * 128 * 4 + kMaxTokens * 16 * kDownPairs * 4 + (int)sizeof(Lists);
 static_assert(kUpSmem <= 227 * 1024 && kDownSmem <= 227 * 1024, "an SM's memory");
 
 // SMs of the current device; once per device allows the kernel its shared memory.
@@ -749,10 +671,10 @@ cudaError_t allow(K k, int smem, std::atomic<int> (&sms)[kDevices], int &n) {
     return cudaSuccess;
 }
 
-template <typename TX, bool kF8, int NB>
+template <typename TX, bool kF8>
 cudaError_t start_down(const Args &a, cudaStream_t s) {
     static std::atomic<int> sms[kDevices];
-    const auto k = k_moe_down<TX, kF8, NB>;
+    const auto k = k_moe_down<TX, kF8>;
     int n = 0;
     const cudaError_t e = allow(k, kDownSmem, sms, n);
     if (e != cudaSuccess) return e;
@@ -761,7 +683,7 @@ cudaError_t start_down(const Args &a, cudaStream_t s) {
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     const int most = (a.d + 7) / 8;
-    cfg.gridDim = dim3((unsigned)(n < most ? n : most)), cfg.blockDim = dim3(32 * kDownWarps<NB>);
+    cfg.gridDim = dim3((unsigned)(n < most ? n : most)), cfg.blockDim = dim3(32 * kDownWarps);
     cfg.dynamicSmemBytes = kDownSmem, cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, a);
 }
@@ -775,10 +697,7 @@ cudaError_t start(const Args &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     k<<<(unsigned)n, 32 * kUpWarps, kUpSmem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (a.T <= 8) return start_down<TX, kF8, 1>(a, s);
-    if (a.T <= 16) return start_down<TX, kF8, 2>(a, s);
-    if (a.T <= 32) return start_down<TX, kF8, 4>(a, s);
-    return start_down<TX, kF8, 8>(a, s);
+    return start_down<TX, kF8>(a, s);
 }
 
 }  // namespace moe
