@@ -386,25 +386,37 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
         load_piece(to + kCell, p + matrix, first_half, second_half);
         cp_async_commit();
     };
+    const int row_blocks = (a.inner + kFp8Block - 1) / kFp8Block, col_blocks = (a.d + kFp8Block - 1) / kFp8Block;
+    // ... and so do the tokens' values (token lane / 4 of the tile) and the scales (lane 2 j + (0: G, 1: U):
+    // of pair j)
+    uint4 raw[kPairs / 4];
+    float scale_next = 1.0f;
+    const auto load_tokens = [&]() {
+        if (!more) return;
+        const int entry = l.first[ahead.i] + 8 * ahead.m + g, base = ahead.lo & ~7;
+        const bool has = entry < l.first[ahead.i + 1];
+        const TX *const x = static_cast<const TX *>(a.x) + (has ? (int64_t)l.token[entry] * a.xs : 0);
+#pragma unroll
+        for (int s = 0; s < kPairs / 4; ++s) {
+            const int c = kF8 ? ak * 128 + (s >> 1) * 64 + t4 * 16 + (s & 1) * 8 : ak * 64 + s * 32 + t4 * 8;
+            raw[s] = make_uint4(0, 0, 0, 0);
+            if (has && c < a.d) raw[s] = __ldg(reinterpret_cast<const uint4 *>(x + c));
+        }
+        if (kF8 && lane < 2 * kUpPairs && base + 8 * (lane >> 1) < ahead.hi)
+            scale_next = a.up_scales.at((((int64_t)l.active[ahead.i] * 2 + (lane & 1)) * row_blocks + (base + 8 * (lane >> 1)) / kFp8Block) * col_blocks + ak);
+    };
     aim();
     settle();
+    load_tokens();
 #pragma unroll
     for (int j = 0; j < kUpPairs; ++j) fetch(j);
     ak += W;
     settle();
 
-    const int row_blocks = (a.inner + kFp8Block - 1) / kFp8Block, col_blocks = (a.d + kFp8Block - 1) / kFp8Block;
     int buf = 0, un = 0;
     do {
-        // this lane's token
-        const int e = l.active[u.i], entry0 = l.first[u.i] + 8 * u.m, end = l.first[u.i + 1];
-        const bool has = entry0 + g < end;
-        const TX *const x = static_cast<const TX *>(a.x) + (has ? (int64_t)l.token[entry0 + g] * a.xs : 0);
+        const int entry0 = l.first[u.i] + 8 * u.m, end = l.first[u.i + 1];
         const int base = u.lo & ~7, tiles = (u.hi - base + 7) / 8;
-        // lane 2 j + (0: G, 1: U) looks after the scale of pair j
-        int64_t scale_at = 0;
-        if (kF8 && lane < 2 * tiles)
-            scale_at = (((int64_t)e * 2 + (lane & 1)) * row_blocks + (base + 8 * (lane >> 1)) / kFp8Block) * col_blocks;
         float acc[kUpPairs][4];
 #pragma unroll
         for (int j = 0; j < kUpPairs; ++j)
@@ -412,15 +424,10 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
             for (int k = 0; k < 4; ++k) acc[j][k] = 0.0f;
         for (int k = begin(un); k < pieces; k += W) {
             uint32_t tok[kPairs];
-            float unit[2] = {1.0f, 1.0f}, scale = 1.0f;
-            if (kF8 && lane < 2 * tiles) scale = a.up_scales.at(scale_at + k);
+            float unit[2] = {1.0f, 1.0f};
+            const float scale = scale_next;
 #pragma unroll
-            for (int s = 0; s < kPairs / 4; ++s) {
-                const int c = kF8 ? k * 128 + (s >> 1) * 64 + t4 * 16 + (s & 1) * 8 : k * 64 + s * 32 + t4 * 8;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (has && c < a.d) v = __ldg(reinterpret_cast<const uint4 *>(x + c));
-                tok[4 * s] = v.x, tok[4 * s + 1] = v.y, tok[4 * s + 2] = v.z, tok[4 * s + 3] = v.w;
-            }
+            for (int s = 0; s < kPairs / 4; ++s) tok[4 * s] = raw[s].x, tok[4 * s + 1] = raw[s].y, tok[4 * s + 2] = raw[s].z, tok[4 * s + 3] = raw[s].w;
             if constexpr (kF8 && __is_same(TX, __nv_bfloat16)) {  // (the product with a power of two is exact in bf16)
                 const auto pair_of = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
                 __nv_bfloat162 top = __habs2(pair_of(tok[0]));
@@ -439,6 +446,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
                 }
                 unit[0] = __shfl_sync(0xffffffffu, mine, 8 * t4), unit[1] = __shfl_sync(0xffffffffu, mine, 8 * t4 + 4);
             }
+            load_tokens();
 #pragma unroll
             for (int j = 0; j < kUpPairs; ++j) {
                 cp_async_wait<kUpPairs - 1>();
