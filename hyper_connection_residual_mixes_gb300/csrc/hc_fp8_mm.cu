@@ -15,6 +15,7 @@
 #include <cuda.h>
 
 #include "hc_fp8.cuh"
+#include "hc_pieces.cuh"
 #include "hc_sublayer.h"
 #include "hc_types.cuh"
 #include "hc_umma.cuh"
@@ -296,6 +297,149 @@ k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUten
     if (warp == kEpilogue + 1) tmem_give_back<false>(tbase, C::kTmemCols);
 }
 
+// ------------------------------------------------------------ up to 16 rows
+// Few rows leave nothing but the reading of w: it goes past each SM once (hc_pieces.cuh), the SM's
+// rows of w in chunks of 64; a chunk's pieces go round the warps, whose sums meet in
+// shared memory.  NB tiles of 8 rows of x.
+constexpr int kFewPairs = 4;  // pairs of row tiles of a chunk
+template <int NB>
+constexpr int kFewWarps = NB == 1 ? 16 : 12;  // (the sums of two tiles of x do not fit the registers of 16)
+template <int NB>
+constexpr int kFewSmem = kFewWarps<NB> * kFewPairs * (2 * kCell + NB * 128 * 4);
+
+template <typename T>
+__device__ __forceinline__ void put1(void *y, int64_t at, float v) {
+    static_cast<T *>(y)[at] = from_f<T>(v);
+}
+
+template <int NB>
+__global__ void __launch_bounds__(32 * kFewWarps<NB>, 1) k_fp8_few(const Args a, const uint8_t *__restrict__ x, int64_t xs, const uint8_t *__restrict__ w) {
+    constexpr int W = kFewWarps<NB>, NP = kFewPairs, kRing = NP * 2 * kCell, kSums = NP * NB * 128;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float *const red = reinterpret_cast<float *>(smem + W * kRing);  // [warp][pair][tile of x][4][lane]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int from = (int)((int64_t)a.C * blockIdx.x / gridDim.x), to = (int)((int64_t)a.C * (blockIdx.x + 1) / gridDim.x);
+    const int pieces = (a.L + 127) / 128;
+    const auto begin = [&](int n) { return (warp + n * (W - pieces % W)) % W; };  // the warp's first piece of the n-th chunk
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // copies, codes of x and scales run a step ahead: an: the chunk, ak: the piece
+    int abase = from & ~7, an = 0, ak = warp;
+    uint32_t rows = 0;  // which of the chunk's tiles have this lane's row
+    const auto aim = [&]() {
+        rows = 0;
+#pragma unroll
+        for (int i = 0; i < 2 * NP; ++i) rows |= (uint32_t)(abase + 8 * i + g >= from && abase + 8 * i + g < to) << i;
+    };
+    const auto settle = [&]() {
+        while (abase < to && ak >= pieces) abase += 16 * NP, ak = begin(++an), aim();
+    };
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kRing + lane * 16);
+    const auto fetch = [&](int j) {
+        const uint32_t at = ring + (uint32_t)(j * 2 * kCell);
+        const uint8_t *const p = w + (int64_t)(abase + 16 * j + g) * a.L + ak * 128 + t4 * 16;
+        const bool first_half = ak * 128 + t4 * 16 < a.L, second_half = ak * 128 + t4 * 16 + 64 < a.L;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool there = rows >> (2 * j + h) & 1u;
+            load_piece(at + h * kCell, p + (int64_t)(8 * h) * a.L, there && first_half, there && second_half);
+        }
+        cp_async_commit();
+    };
+    uint4 raw[NB][2];
+    uint32_t raw_x[NB], raw_w = 0;
+    const auto load_rows = [&]() {
+        if (abase >= to) return;
+#pragma unroll
+        for (int m = 0; m < NB; ++m) {
+            const bool has = 8 * m + g < a.M;
+            const int64_t row = has ? 8 * m + g : 0;
+            raw_x[m] = a.sx.raw(row * pieces + ak);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int c = ak * 128 + s * 64 + t4 * 16;
+                raw[m][s] = make_uint4(0, 0, 0, 0);
+                if (has && c < a.L) raw[m][s] = __ldg(reinterpret_cast<const uint4 *>(x + row * xs + c));
+            }
+        }
+        // (lane i: tile i's)
+        if (lane < 2 * NP && abase + 8 * lane < to) raw_w = a.sw.raw((abase + 8 * lane) / kFp8Block * a.sw_col + ak * a.sw_k);
+    };
+    aim();
+    settle();
+    load_rows();
+#pragma unroll
+    for (int j = 0; j < NP; ++j) fetch(j);
+    ak += W;
+    settle();
+    int n = 0;
+    for (int base = from & ~7; base < to; base += 16 * NP, ++n) {
+        float acc[NP][NB][4];
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+#pragma unroll
+            for (int m = 0; m < NB; ++m)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[j][m][q] = 0.0f;
+        for (int k = begin(n); k < pieces; k += W) {
+            uint32_t tok[NB][16];
+            float unit[NB][2];
+#pragma unroll
+            for (int m = 0; m < NB; ++m) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    widen(raw[m][s].x, tok[m][8 * s], tok[m][8 * s + 1]), widen(raw[m][s].y, tok[m][8 * s + 2], tok[m][8 * s + 3]);
+                    widen(raw[m][s].z, tok[m][8 * s + 4], tok[m][8 * s + 5]), widen(raw[m][s].w, tok[m][8 * s + 6], tok[m][8 * s + 7]);
+                }
+                const float own = a.sx.value(raw_x[m]);
+                unit[m][0] = __shfl_sync(0xffffffffu, own, 8 * t4), unit[m][1] = __shfl_sync(0xffffffffu, own, 8 * t4 + 4);
+            }
+            const float scale = a.sw.value(raw_w);
+            load_rows();
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                cp_async_wait<NP - 1>();
+                if (base + 16 * j < to) {
+                    const uint32_t here = ring + (uint32_t)(j * 2 * kCell);
+                    const Rows16<true> rows16(read_piece(here), read_piece(here + kCell));
+                    const float s0 = __shfl_sync(0xffffffffu, scale, 2 * j), s1 = __shfl_sync(0xffffffffu, scale, 2 * j + 1);
+#pragma unroll
+                    for (int m = 0; m < NB; ++m) multiply_scaled<true>(acc[j][m], rows16, tok[m], s0, s1, unit[m]);
+                }
+                fetch(j);
+            }
+            ak += W;
+            settle();
+        }
+        if (begin(n) < pieces) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+#pragma unroll
+                for (int m = 0; m < NB; ++m)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) red[warp * kSums + ((j * NB + m) * 4 + q) * 32 + lane] = acc[j][m][q];
+        }
+        __syncthreads();
+        const int meet = pieces < W ? pieces : W, w0 = n * (pieces % W) % W;  // the warps that had a piece, in their order
+        for (int o = threadIdx.x; o < kSums; o += 32 * W) {
+            const int j = o / (NB * 128), m = o / 128 % NB, q = o / 32 % 4;  // (o % 32 is this lane)
+            const int row = 8 * m + 2 * t4 + (q & 1), col = base + 16 * j + 8 * (q >> 1) + g;
+            if (row >= a.M || col < from || col >= to) continue;
+            float v = 0.0f;
+            for (int i = 0, f = w0; i < meet; ++i) {
+                v += red[f * kSums + o];
+                if (++f == W) f = 0;
+            }
+            const int64_t at = row * a.ys + col;
+            if (a.y_type == HC_F32) put1<float>(a.y, at, v);
+            else if (a.y_type == HC_BF16) put1<__nv_bfloat16>(a.y, at, v);
+            else put1<__half>(a.y, at, v);
+        }
+        __syncthreads();
+    }
+    cp_async_wait<0>();
+}
+
 // A matrix of codes [rows][width], rows `stride` bytes apart, boxes of 128 x 128, 128-byte
 // swizzle, zeros outside.
 bool make_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, int64_t stride) {
@@ -340,6 +484,29 @@ cudaError_t launch(const CUtensorMap &tx, const CUtensorMap &tw, const Args &a, 
     return cudaLaunchKernelEx(&cfg, k, tx, tw, a);
 }
 
+template <int NB>
+cudaError_t launch_few(const Args &a, const uint8_t *x, int64_t xs, const uint8_t *w, cudaStream_t s) {
+    const auto k = k_fp8_few<NB>;
+    static std::atomic<int> sms[kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    int n = sms[dev].load(std::memory_order_acquire);
+    if (!n) {
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem<NB>)) != cudaSuccess) return e;
+        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        sms[dev].store(n, std::memory_order_release);  // (the attribute is set for whoever reads it)
+    }
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.C / 8 < n ? a.C / 8 : n)), cfg.blockDim = dim3(32 * kFewWarps<NB>);
+    cfg.dynamicSmemBytes = kFewSmem<NB>, cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a, x, xs, w);
+}
+
 }  // namespace f8
 
 cudaError_t launch_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scales, bool x_f32, const uint8_t *w,
@@ -351,6 +518,8 @@ cudaError_t launch_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scal
     const int64_t size = y_type == HC_F32 ? 4 : 2;
     const f8::Args a{{x_scales, x_f32}, {w_scales, w_f32}, transposed ? 1 : row, transposed ? row : 1, M, C, L, y, y_stride,
                      y_type, reinterpret_cast<uintptr_t>(y) % 16 == 0 && y_stride * size % 16 == 0};
+    if (!transposed && M <= 8) return f8::launch_few<1>(a, x, x_stride, w, s);
+    if (!transposed && M <= 16) return f8::launch_few<2>(a, x, x_stride, w, s);
     CUtensorMap tx, tw;
     if (!f8::make_map(&tx, x, L, M, x_stride) || !f8::make_map(&tw, w, K, N, K)) return cudaErrorInvalidValue;
     // (128 x 256 tiles where they give half the SMs work: an SM then loads a third less for a product)

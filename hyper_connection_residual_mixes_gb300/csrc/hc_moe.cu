@@ -23,7 +23,7 @@
 #include <cuda.h>
 
 #include "hc_fp8.cuh"
-#include "hc_ptx.cuh"
+#include "hc_pieces.cuh"
 #include "hc_sublayer.h"
 #include "hc_types.cuh"
 
@@ -32,7 +32,6 @@ namespace hc {
 namespace moe {
 
 constexpr int kMaxTokens = 64, kMaxTop = 16, kMaxExperts = 1024, kMaxEntries = kMaxTokens * kMaxTop;
-constexpr int kCell = 1024;       // bytes of a piece: 8 rows of 128 bytes
 constexpr int kUpWarps = 16, kUpPairs = 4;  // pairs of row tiles (of G and of U) of a unit
 constexpr int kDownWarps = 16, kDownPairs = 3;  // ... of a pass
 constexpr int kUpRing = kUpPairs * 2 * kCell, kDownRing = kDownPairs * 2 * kCell;  // of a warp: the pieces of a step
@@ -228,38 +227,6 @@ __device__ __forceinline__ void route(const Args &a, Lists &l, bool write) {
     __syncthreads();
 }
 
-// ------------------------------------------------------------ pieces
-// A lane's share of a piece: 16 bytes at 16 (lane % 4) of the row lane / 4, and 64 bytes on.
-// `there`: whether they are there, else zeros.
-__device__ __forceinline__ void load_piece(uint32_t to, const uint8_t *from, bool there0, bool there1) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there0 ? 16 : 0) : "memory");
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0 + 512], [%1 + 64], 16, %2;" ::"r"(to), "l"(from), "r"(there1 ? 16 : 0) : "memory");
-}
-struct Piece {
-    uint32_t w[8];
-};
-__device__ __forceinline__ Piece read_piece(uint32_t at) {
-    Piece p;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(p.w[0]), "=r"(p.w[1]), "=r"(p.w[2]), "=r"(p.w[3]) : "r"(at) : "memory");
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + 512];" : "=r"(p.w[4]), "=r"(p.w[5]), "=r"(p.w[6]), "=r"(p.w[7]) : "r"(at) : "memory");
-    return p;
-}
-// four codes as two pairs of fp16
-__device__ __forceinline__ void widen(uint32_t c, uint32_t &lo, uint32_t &hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(c));
-}
-__device__ __forceinline__ uint32_t half2_of(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// The tokens' side of the MMAs over a piece: token lane / 4 of 8, this lane's values of k in
-// pairs.  kF8: 16 of them per 16 bytes of codes (32 a piece), else 8 (16).
-template <bool kF8>
-constexpr int kPairsOf = kF8 ? 16 : 8;
-
 // fp16 copies of a token's values over a piece carry a power of two that brings the
 // largest to [2^14, 2^15): 11 bits of each value, of small ones 2^-39 of the largest.  Of that
 // largest: the power, and what undoes it.
@@ -268,40 +235,6 @@ __device__ __forceinline__ float power_of(float amax, float &unit) {
     b = b < 15 ? 15 : b;
     unit = __uint_as_float((uint32_t)(b - 14) << 23);
     return __uint_as_float((uint32_t)(268 - b) << 23);
-}
-
-template <typename T>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    if constexpr (__is_same(T, __nv_bfloat16)) mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
-    else mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
-}
-// A pair of tiles (rows 0-7 of the MMA, rows 8-15) as its operand: four registers for each two
-// pairs of k.
-template <bool kF8>
-struct Rows16 {
-    uint32_t a[kPairsOf<kF8> / 2][4];
-    __device__ __forceinline__ Rows16(const Piece &p, const Piece &q) {
-#pragma unroll
-        for (int i = 0; i < kPairsOf<kF8> / 2; ++i) {
-            if constexpr (kF8) widen(p.w[i], a[i][0], a[i][2]), widen(q.w[i], a[i][1], a[i][3]);
-            else a[i][0] = p.w[2 * i], a[i][2] = p.w[2 * i + 1], a[i][1] = q.w[2 * i], a[i][3] = q.w[2 * i + 1];
-        }
-    }
-};
-// acc += their products with the tokens
-template <typename T, bool kF8>
-__device__ __forceinline__ void multiply(float (&acc)[4], const Rows16<kF8> &w, const uint32_t (&x)[kPairsOf<kF8>]) {
-#pragma unroll
-    for (int i = 0; i < kPairsOf<kF8> / 2; ++i) mma<T>(acc, w.a[i][0], w.a[i][1], w.a[i][2], w.a[i][3], x[2 * i], x[2 * i + 1]);
-}
-// acc += ..., times the scales of the two tiles' blocks and what undoes the tokens' powers of two
-template <bool kF8>
-__device__ __forceinline__ void multiply_scaled(float (&acc)[4], const Rows16<kF8> &w, const uint32_t (&x)[kPairsOf<kF8>], float s0,
-                                                float s1, const float (&unit)[2]) {
-    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    multiply<__half, kF8>(part, w, x);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = fmaf(part[k], (k < 2 ? s0 : s1) * unit[k & 1], acc[k]);
 }
 
 // ------------------------------------------------------------ G and U
