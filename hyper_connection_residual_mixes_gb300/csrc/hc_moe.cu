@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
 template <typename TX, bool kF8>
 __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
     constexpr int kBytes = kF8 ? 1 : 2, W = kDownWarps, NP = kDownPairs, kPairs = kPairsOf<kF8>, kRows = 16 * NP;
-    constexpr bool kSplit = !kF8 && __is_same(TX, __nv_bfloat16);  // a as two bf16 numbers
+    // a as two numbers: of bf16 weights' type, or (fp16 outputs, whose rounding is no coarser than that of one) fp16
+    constexpr bool kSplit = !kF8 && __is_same(TX, __nv_bfloat16), kTwo = kSplit || __is_same(TX, __half);
     extern __shared__ __align__(128) uint8_t smem[];
     float *const red = reinterpret_cast<float *>(smem + W * kDownRing);  // [2][warp][pair][4][lane]
     float *const out = red + 2 * W * NP * 128;                           // [token][row]
@@ -515,14 +516,14 @@ __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
                     for (int q = 0; q < 4; ++q) acc[j][q] = 0.0f;
                 bool more = true;
                 while (more) {
-                    uint32_t tok[kPairs], low[kSplit ? kPairs : 1];
+                    uint32_t tok[kPairs], low[kTwo ? kPairs : 1];
                     float unit[2] = {1.0f, 1.0f};
                     const float *const f = reinterpret_cast<const float *>(raw);
                     if constexpr (kSplit) {
 #pragma unroll
                         for (int q = 0; q < kPairs; ++q) {
                             tok[q] = pack_bf16x2(f[2 * q], f[2 * q + 1]);
-                            low[kSplit ? q : 0] = pack_bf16x2(f[2 * q] - bf16lo(tok[q]), f[2 * q + 1] - bf16hi(tok[q]));
+                            low[kTwo ? q : 0] = pack_bf16x2(f[2 * q] - bf16lo(tok[q]), f[2 * q + 1] - bf16hi(tok[q]));
                         }
                     } else {
                         float amax = 0.0f, own;
@@ -532,7 +533,13 @@ __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
                         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                         const float m = power_of(amax, own);
 #pragma unroll
-                        for (int q = 0; q < kPairs; ++q) tok[q] = half2_of(f[2 * q] * m, f[2 * q + 1] * m);
+                        for (int q = 0; q < kPairs; ++q) {
+                            tok[q] = half2_of(f[2 * q] * m, f[2 * q + 1] * m);
+                            if constexpr (kTwo) {
+                                const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&tok[q]));
+                                low[q] = half2_of(fmaf(f[2 * q], m, -h.x), fmaf(f[2 * q + 1], m, -h.y));
+                            }
+                        }
                         unit[0] = __shfl_sync(0xffffffffu, own, 8 * t4), unit[1] = __shfl_sync(0xffffffffu, own, 8 * t4 + 4);
                     }
                     const float scale = scale_next;
@@ -548,6 +555,13 @@ __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
                             if constexpr (kSplit) {
                                 multiply<TX, false>(acc[j], w, tok);
                                 multiply<TX, false>(acc[j], w, low);
+                            } else if constexpr (kTwo) {
+                                const float s0 = __shfl_sync(0xffffffffu, scale, 2 * j), s1 = __shfl_sync(0xffffffffu, scale, 2 * j + 1);
+                                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                multiply<__half, kF8>(part, w, low);
+                                multiply<__half, kF8>(part, w, tok);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) acc[j][q] = fmaf(part[q], (q < 2 ? s0 : s1) * unit[q & 1], acc[j][q]);
                             } else {
                                 multiply_scaled<kF8>(acc[j], w, tok, __shfl_sync(0xffffffffu, scale, 2 * j), __shfl_sync(0xffffffffu, scale, 2 * j + 1), unit);
                             }

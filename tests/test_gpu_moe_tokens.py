@@ -1,7 +1,7 @@
 """GPU: the experts' layer for a few tokens against its formulas in 64 bits.
 
 Bounds.  With a = p silu(g) u, u = 2^-24 and h the half step of the type that a goes into
-the second product with (2^-16 for the two bf16 numbers of bf16 weights, 2^-11 for fp16):
+the second product with (2^-16 for the two bf16 numbers of bf16 weights, 2^-22 for two fp16 numbers, 2^-11 for one):
  - g and u' are sums of d products in fp32: a lane of the tensor cores adds them in
    some order and may cut off the last bit, then up to 16 warps' sums, each scaled:
    (d + 40) * 2^-23 of S, the sum of their terms' sizes (x is exact in fp16 to 2^-39 of its
@@ -71,7 +71,7 @@ def _check(y, x, w, ids, p):
     E, _, inner, d = w["up"].shape
     xd = x.double()
     want, room = torch.zeros_like(xd), torch.zeros_like(xd)
-    h = 2.0 ** -16 if x.dtype == torch.bfloat16 and w["up_scales"] is None else 2.0 ** -11
+    h = 2.0 ** -22 if x.dtype == torch.float16 else 2.0 ** -16 if w["up_scales"] is None else 2.0 ** -11
     for e in range(E):
         t, j = (ids == e).nonzero(as_tuple=True)
         if t.numel() == 0:
