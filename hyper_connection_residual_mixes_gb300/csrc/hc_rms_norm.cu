@@ -709,9 +709,10 @@ cudaError_t backward(const BackArgs &a, float *gw, cudaStream_t s) {
 
 // ------------------------------------------------------------ casts
 // Rows in groups of 128: VEC values a thread, 128 / VEC threads a group, kCastVectors
-// groups a thread one after the other, their loads all under way at once.
+// groups a thread one after the other, their loads all under way at once.  kFlat: dense rows of
+// whole groups, whose places need no division.
 constexpr int kCastThreads = 256, kCastVectors = 4;
-template <typename T, int VEC>
+template <typename T, int VEC, bool kFlat>
 __global__ void __launch_bounds__(kCastThreads)
 k_fp8_cast(const T *__restrict__ x, int64_t xs, int64_t n, int d, int groups, uint8_t *__restrict__ codes, int64_t cs,
            uint8_t *__restrict__ scales, int wide) {
@@ -719,24 +720,29 @@ k_fp8_cast(const T *__restrict__ x, int64_t xs, int64_t n, int d, int groups, ui
     const int t = threadIdx.x % kTeam;
     const int64_t first = (int64_t)blockIdx.x * (kTeams * kCastVectors) + threadIdx.x / kTeam, count = n * groups;
     Vec<T, VEC> v[kCastVectors];
+    bool in[kCastVectors];
+    int64_t to[kCastVectors];
 #pragma unroll
     for (int i = 0; i < kCastVectors; ++i) {
-        const int64_t g = first + i * kTeams, row = g / groups;
-        const int c = (int)(g - row * groups) * kFp8Block + t * VEC;
-        if (g < count && c < d) v[i] = *reinterpret_cast<const Vec<T, VEC> *>(x + row * xs + c);
+        const int64_t g = first + i * kTeams;
+        int64_t from = to[i] = g * kFp8Block + t * VEC;
+        in[i] = g < count;
+        if (!kFlat) {
+            const int64_t row = g / groups;
+            const int c = (int)(g - row * groups) * kFp8Block + t * VEC;
+            from = row * xs + c, to[i] = row * cs + c, in[i] &= c < d;
+        }
+        if (in[i]) v[i] = *reinterpret_cast<const Vec<T, VEC> *>(x + from);
     }
 #pragma unroll
     for (int i = 0; i < kCastVectors; ++i) {
-        const int64_t g = first + i * kTeams, row = g / groups;
-        const int c = (int)(g - row * groups) * kFp8Block + t * VEC;
-        const bool in = g < count && c < d;
         float f[VEC], amax = 0.0f;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) f[k] = in ? to_f(v[i].v[k]) : 0.0f, amax = largest(amax, f[k]);
+        for (int k = 0; k < VEC; ++k) f[k] = in[i] ? to_f(v[i].v[k]) : 0.0f, amax = largest(amax, f[k]);
         const uint32_t byte = fp8_scale_byte(largest_of_group<VEC>(amax));
-        if (!in) continue;
-        put_codes<VEC>(codes + row * cs + c, f, fp8_inverse(byte), wide);
-        if (t == 0) scales[g] = (uint8_t)byte;
+        if (!in[i]) continue;
+        put_codes<VEC>(codes + to[i], f, fp8_inverse(byte), wide);
+        if (t == 0) scales[first + i * kTeams] = (uint8_t)byte;
     }
 }
 // ... of rows that start anywhere: a warp a group, four values a lane, one by one
@@ -767,8 +773,12 @@ cudaError_t cast(const void *x, int64_t xs, int64_t n, int d, uint8_t *codes, in
     const T *const p = static_cast<const T *>(x);
     if (d % W == 0 && multiple(x, xs, sizeof(T), 16)) {
         constexpr int kEach = kCastThreads / (kFp8Block / W) * kCastVectors;
-        k_fp8_cast<T, W><<<(unsigned)((count + kEach - 1) / kEach), kCastThreads, 0, s>>>(p, xs, n, d, groups, codes, cs, scales,
-                                                                                         multiple(codes, cs, 1, W));
+        const unsigned grid = (unsigned)((count + kEach - 1) / kEach);
+        const int codes_wide = multiple(codes, cs, 1, W);
+        if (d % kFp8Block == 0 && (n == 1 || (xs == d && cs == d)))
+            k_fp8_cast<T, W, true><<<grid, kCastThreads, 0, s>>>(p, xs, n, d, groups, codes, cs, scales, codes_wide);
+        else
+            k_fp8_cast<T, W, false><<<grid, kCastThreads, 0, s>>>(p, xs, n, d, groups, codes, cs, scales, codes_wide);
     } else {
         k_fp8_cast_any<T><<<(unsigned)((count + 7) / 8), kCastThreads, 0, s>>>(p, xs, n, d, groups, codes, cs, scales);
     }
