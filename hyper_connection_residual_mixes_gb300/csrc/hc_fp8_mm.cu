@@ -51,6 +51,8 @@ struct Args {
     void *y;
     int64_t ys;
     int y_type, y_wide;    // y_wide: rows take 16-byte stores
+    int slices, per;       // (of a product that is cut: slices of the contraction, blocks of 128 in each)
+    float *part;           // ... and its sums by slice: [slice][column / 4][row][column % 4], the order in which lanes have them
 };
 
 // Shared-memory matrix descriptors.  K-major, 128-byte swizzle: rows of 128 codes, 8-row
@@ -145,6 +147,18 @@ __device__ __forceinline__ void put_row(const Args &a, int64_t row, int c, const
         else put8(static_cast<__half *>(a.y) + at, acc + j, a.y_wide);
     }
 }
+template <int NP>
+__device__ __forceinline__ void put_part(const Args &a, int slice, int64_t row, int c, const f32x2 (&acc)[NP]) {
+    if (row >= a.M) return;
+    float4 *const o = reinterpret_cast<float4 *>(a.part) + ((int64_t)slice * (a.C / 4) + c / 4) * a.M + row;
+#pragma unroll
+    for (int j = 0; j < NP; j += 2) {
+        if (c + 2 * j >= a.C) return;
+        float4 v;
+        f2_split(acc[j], v.x, v.y), f2_split(acc[j + 1], v.z, v.w);
+        o[j / 2 * a.M] = v;
+    }
+}
 
 // Tiles are walked in groups of kGroup tiles of rows, through all columns before the
 // next group: what the CTAs read at one time is then about as wide as long.
@@ -156,7 +170,7 @@ __device__ __forceinline__ void place_of(int tile, int mt, int ct, int &m, int &
 }
 
 // kMn: w lies MN-major (transposed).
-template <int BN, bool kMn>
+template <int BN, bool kMn, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Args a) {
     using C = Cfg<BN>;
@@ -167,7 +181,7 @@ k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUten
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int mt = (int)((a.M + kM - 1) / kM), ct = (a.C + BN - 1) / BN, tiles = mt * ct;
+    const int mt = (int)((a.M + kM - 1) / kM), ct = (a.C + BN - 1) / BN, of_slice = mt * ct, tiles = kSplit ? of_slice * a.slices : of_slice;
     const int blocks = (a.L + kBK - 1) / kBK;
 
     if (threadIdx.x == 0) {
@@ -196,9 +210,10 @@ k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUten
             bool ok = true;
             for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
                 int m, c;
-                place_of(tile, mt, ct, m, c);
+                const int slice = kSplit ? tile / of_slice : 0, i0 = kSplit ? slice * a.per : 0, i1 = kSplit && i0 + a.per < blocks ? i0 + a.per : blocks;
+                place_of(tile - slice * of_slice, mt, ct, m, c);
                 m = __shfl_sync(0xffffffffu, m * kM, 0), c = __shfl_sync(0xffffffffu, c * BN, 0);
-                for (int i = 0; i < blocks; ++i) {
+                for (int i = i0; i < i1; ++i) {
                     if (!(ok = mbar_wait_warp<false>(smem_u32(&done_bar[slot]), parity, &s_abort))) break;
                     const uint32_t sa = sbase + (uint32_t)slot * C::kStage;
                     const uint32_t bar = smem_u32(&full_bar[slot]);
@@ -230,7 +245,8 @@ k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUten
             const uint64_t da0 = desc(sbase), db0 = desc(sbase + C::kABytes);
             constexpr uint32_t kStepA = 32 >> 4, kStepB = (kMn ? 4096 : 32) >> 4, id = idesc(kMn, kM, BN);
             for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                for (int i = 0; i < blocks; ++i) {
+                const int i0 = kSplit ? tile / of_slice * a.per : 0, i1 = kSplit && i0 + a.per < blocks ? i0 + a.per : blocks;
+                for (int i = i0; i < i1; ++i) {
                     if (!__all_sync(0xffffffffu, stage_ready) && !(ok = mbar_wait_warp<false>(smem_u32(&full_bar[slot]), parity, &s_abort))) break;
                     if (!__all_sync(0xffffffffu, acc_ready) && !(ok = mbar_wait_warp<false>(smem_u32(&acc_empty[b]), b_parity, &s_abort))) break;
                     const uint32_t at = (uint32_t)(slot * C::kStage) / 16, d = tbase + b * BN, done = smem_u32(&done_bar[slot]);
@@ -256,21 +272,22 @@ k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUten
         bool ok = true;
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
             int m, c;
-            place_of(tile, mt, ct, m, c);
+            const int slice = kSplit ? tile / of_slice : 0, i0 = kSplit ? slice * a.per : 0, i1 = kSplit && i0 + a.per < blocks ? i0 + a.per : blocks;
+            place_of(tile - slice * of_slice, mt, ct, m, c);
             const int64_t row = (int64_t)m * kM + q * 32 + lane;
             const int c0 = c * BN + half * (BN / 2);
             // (rows and columns that are not there take a scale that is)
             const int64_t x_at = (row < a.M ? row : a.M - 1) * blocks;
             const int64_t w_at = (c0 < a.C ? c0 : a.C - 1) / kFp8Block * a.sw_col;
-            uint32_t next_x = a.sx.raw(x_at), next_w = a.sw.raw(w_at);
+            uint32_t next_x = a.sx.raw(x_at + i0), next_w = a.sw.raw(w_at + i0 * a.sw_k);
             f32x2 acc[2][NP];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < NP; ++j) acc[h][j] = f2_dup(0.0f);
-            for (int i = 0; i < blocks; ++i) {
+            for (int i = i0; i < i1; ++i) {
                 const f32x2 s = f2_dup(a.sx.value(next_x) * a.sw.value(next_w));
-                if (i + 1 < blocks) next_x = a.sx.raw(x_at + i + 1), next_w = a.sw.raw(w_at + (i + 1) * a.sw_k);
+                if (i + 1 < i1) next_x = a.sx.raw(x_at + i + 1), next_w = a.sw.raw(w_at + (i + 1) * a.sw_k);
                 if (!(ok = mbar_wait_warp<false>(smem_u32(&done_bar[slot]), parity, &s_abort))) break;
                 if (++slot == S) slot = 0, parity ^= 1u;
                 tmem_fence_after_sync();
@@ -288,7 +305,8 @@ k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUten
 #pragma unroll
                 for (int k = 0; k < NP; ++k) acc[1][k] = f2_fma(v[k], s, acc[1][k]);
             }
-            if (ok) put_row<NP>(a, row, c0, acc[0]), put_row<NP>(a, row, c0 + 2 * NP, acc[1]);
+            if (ok && kSplit) put_part<NP>(a, slice, row, c0, acc[0]), put_part<NP>(a, slice, row, c0 + 2 * NP, acc[1]);
+            if (ok && !kSplit) put_row<NP>(a, row, c0, acc[0]), put_row<NP>(a, row, c0 + 2 * NP, acc[1]);
         }
     }
     tmem_fence_before_sync();
@@ -455,10 +473,10 @@ constexpr int kDevices = 64;
 
 // Launches on every SM, once per
 // kernel and device finding out how many and allowing the shared memory.
-template <int BN, bool kMn>
+template <int BN, bool kMn, bool kSplit>
 cudaError_t launch(const CUtensorMap &tx, const CUtensorMap &tw, const Args &a, cudaStream_t s) {
     using C = Cfg<BN>;
-    const auto k = k_fp8_mm<BN, kMn>;
+    const auto k = k_fp8_mm<BN, kMn, kSplit>;
     static std::atomic<int> ctas[kDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -479,10 +497,73 @@ cudaError_t launch(const CUtensorMap &tx, const CUtensorMap &tw, const Args &a, 
         if ((e = cudaDeviceGetAttribute(&grid, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         ctas[dev].store(grid, std::memory_order_release);  // (the attribute is set for whoever reads it)
     }
-    const int64_t tiles = (a.M + kM - 1) / kM * ((a.C + BN - 1) / BN);
+    const int64_t tiles = (a.M + kM - 1) / kM * ((a.C + BN - 1) / BN) * (kSplit ? a.slices : 1);
     cfg.gridDim = dim3((unsigned)(tiles < grid ? tiles : grid));
     return cudaLaunchKernelEx(&cfg, k, tx, tw, a);
 }
+
+// The sum over slices, one after the other (the same call gives the same bits), rounded to
+// the output's type: 8 columns of a row a thread, 8 rows x 128 columns a block.
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) k_join(const Args a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x % 32, c = blockIdx.x * 128 + (threadIdx.x / 32 * 4 + lane / 8) * 8;
+    const int64_t row = (int64_t)blockIdx.y * 8 + lane % 8;
+    if (row >= a.M || c >= a.C) return;
+    const float4 *p = reinterpret_cast<const float4 *>(a.part) + (int64_t)(c / 4) * a.M + row;
+    const int64_t slice = (int64_t)(a.C / 4) * a.M;
+    f32x2 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = f2_dup(0.0f);
+#pragma unroll 4
+    for (int i = 0; i < a.slices; ++i, p += slice) {
+        const float4 lo = __ldcg(p), hi = __ldcg(p + a.M);
+        v[0] = f2_add(v[0], f2_make(lo.x, lo.y)), v[1] = f2_add(v[1], f2_make(lo.z, lo.w));
+        v[2] = f2_add(v[2], f2_make(hi.x, hi.y)), v[3] = f2_add(v[3], f2_make(hi.z, hi.w));
+    }
+    const int64_t at = row * a.ys + c;
+    if (a.y_type == HC_F32) put8(static_cast<float *>(a.y) + at, v, a.y_wide);
+    else if (a.y_type == HC_BF16) put8(static_cast<__nv_bfloat16 *>(a.y) + at, v, a.y_wide);
+    else put8(static_cast<__half *>(a.y) + at, v, a.y_wide);
+}
+cudaError_t join(const Args &a, cudaStream_t s) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((a.C + 127) / 128), (unsigned)((a.M + 7) / 8)), cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_join, a);
+}
+
+// How a product is cut: into tiles of 128 x bn and, where few tiles leave SMs idle, the
+// contraction into slices of `per` blocks that k_join adds up.  The rule counts cycles:
+// a block of 128 takes an SM some 1,050 with 256 columns and 860 with 128 (the signals and
+// the sums, not the MMAs); the joining launch 1,500, a slice 1,500 more, and its sums 2.2 per 1,000
+// to write and read.  Measured, against the better of the whole contractions (us): 17 x 5,120 x
+// 5,120 17.9 -> 10.5 (5 slices; 2: 14.0, 7: 11.9), 128 rows 19.6 -> 12.9, 256 rows 20.0 -> 15.2 (3),
+// 256 x 2,048 x 8,192 27.9 -> 14.0 (8); but 256 x 8,192 x 2,048 10.3 -> 12.3 (2) and 128 x 16,384 x
+// 5,120 19.8 -> 21.1 (2), which the rule leaves whole.  A constant number of SMs: the
+// cut decides the workspace and the order of the sums, which must not depend on the device.
+constexpr int kSms = 152, kMostSlices = 32;
+struct Cut {
+    int bn, slices, per;
+};
+Cut cut(int64_t M, int C, int L) {
+    const int64_t rows = (M + kM - 1) / kM, blocks = (L + kBK - 1) / kBK;
+    const int64_t wide = rows * ((C + 255) / 256), narrow = rows * ((C + 127) / 128);
+    Cut best{128, 1, (int)blocks};
+    double least = (double)((narrow + kSms - 1) / kSms * blocks) * 860;
+    for (int64_t s = 1; s == 1 || (s <= kMostSlices && s <= blocks && wide * s <= kSms); ++s) {
+        const int64_t per = (blocks + s - 1) / s;
+        if ((blocks + per - 1) / per != s) continue;
+        const double cycles = (double)((wide * s + kSms - 1) / kSms * per) * 1050 +
+                              (s == 1 ? 0 : 1500 + 1500 * (double)s + 0.0022 * (double)(s * M * C));
+        if (cycles <= least) least = cycles, best = Cut{256, (int)s, (int)per};
+    }
+    return best;
+}
+bool few(bool transposed, int64_t M) { return !transposed && M <= 16; }
 
 template <int NB>
 cudaError_t launch_few(const Args &a, const uint8_t *x, int64_t xs, const uint8_t *w, cudaStream_t s) {
@@ -512,25 +593,30 @@ cudaError_t launch_few(const Args &a, const uint8_t *x, int64_t xs, const uint8_
 cudaError_t launch_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scales, bool x_f32, const uint8_t *w,
                           const void *w_scales, bool w_f32, bool transposed, int64_t M, int N, int K, void *y, int64_t y_stride,
                           hc_dtype y_type, void *workspace, cudaStream_t s) {
-    (void)workspace;
     const int C = transposed ? K : N, L = transposed ? N : K;
     const int64_t row = (K + kFp8Block - 1) / kFp8Block;  // scales of w in a row of blocks
     const int64_t size = y_type == HC_F32 ? 4 : 2;
+    const bool few = f8::few(transposed, M);
+    const f8::Cut cut = few ? f8::Cut{0, 1, 0} : f8::cut(M, C, L);
     const f8::Args a{{x_scales, x_f32}, {w_scales, w_f32}, transposed ? 1 : row, transposed ? row : 1, M, C, L, y, y_stride,
-                     y_type, reinterpret_cast<uintptr_t>(y) % 16 == 0 && y_stride * size % 16 == 0};
-    if (!transposed && M <= 8) return f8::launch_few<1>(a, x, x_stride, w, s);
-    if (!transposed && M <= 16) return f8::launch_few<2>(a, x, x_stride, w, s);
+                         y_type, reinterpret_cast<uintptr_t>(y) % 16 == 0 && y_stride * size % 16 == 0, cut.slices, cut.per,
+                      static_cast<float *>(workspace)};
+    if (few) return M <= 8 ? f8::launch_few<1>(a, x, x_stride, w, s) : f8::launch_few<2>(a, x, x_stride, w, s);
     CUtensorMap tx, tw;
     if (!f8::make_map(&tx, x, L, M, x_stride) || !f8::make_map(&tw, w, K, N, K)) return cudaErrorInvalidValue;
-    // (128 x 256 tiles where they give half the SMs work: an SM then loads a third less for a product)
-    const bool large = ((M + 127) / 128) * ((C + 255) / 256) > 76;
-    if (large) return transposed ? f8::launch<256, true>(tx, tw, a, s) : f8::launch<256, false>(tx, tw, a, s);
-    return transposed ? f8::launch<128, true>(tx, tw, a, s) : f8::launch<128, false>(tx, tw, a, s);
+    if (cut.slices > 1) {
+        const cudaError_t e = transposed ? f8::launch<256, true, true>(tx, tw, a, s) : f8::launch<256, false, true>(tx, tw, a, s);
+        return e == cudaSuccess ? f8::join(a, s) : e;
+    }
+    if (cut.bn == 256) return transposed ? f8::launch<256, true, false>(tx, tw, a, s) : f8::launch<256, false, false>(tx, tw, a, s);
+    return transposed ? f8::launch<128, true, false>(tx, tw, a, s) : f8::launch<128, false, false>(tx, tw, a, s);
 }
 
 size_t fp8_mm_workspace_bytes(bool transposed, int64_t M, int N, int K) {
-    (void)transposed, (void)M, (void)N, (void)K;
-    return 0;
+    const int C = transposed ? K : N;
+    if (f8::few(transposed, M)) return 0;
+    const f8::Cut cut = f8::cut(M, C, transposed ? N : K);
+    return cut.slices == 1 ? 0 : (size_t)cut.slices * M * C * 4;
 }
 
 cudaError_t consume_fp8_mm_device_error(cudaStream_t s, unsigned int *flag) {

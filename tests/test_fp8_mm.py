@@ -45,6 +45,26 @@ def test_workspace_bytes():
         for M in (1, 40, 1000, 100000):
             for N, K in ((16, 16), (272, 1040), (2048, 5120)):
                 assert f(t, M, N, K) >= 0
+    assert f(0, 100, 32, 64) == 0 and f(0, 16, 272, 8192) == 0    # one block; few rows
+    # sums by slice, 2 to 32 of them, of the output's size; none where the tiles fill the SMs
+    for t, N, K in ((0, 272, 8192), (1, 8192, 272), (0, 16, 65536), (0, 5120, 5120)):
+        for M in (17, 130):
+            n, rest = divmod(f(t, M, N, K), M * (K if t else N) * 4)
+            assert rest == 0 and 2 <= n <= 32, (t, M, N, K, n)
+        assert f(t, 100000, N, K) == 0
+    for M in (17, 130, 1000, 5000, (1 << 31) - 4097):
+        for N, K in ((16, 16), (144, 5120), (4096, 65536), (65536, 4096)):
+            assert f(0, M, N, K) <= 152 * 128 * 256 * 4
+            assert f(1, M, K, N) == f(0, M, N, K) or M <= 16
+
+
+def test_workspace_refusals():
+    need = _lib.load().hc_fp8_mm_workspace_bytes(0, 100, 32, 4096)
+    cut = dict(K=4096, xs=4096)
+    assert need > 0
+    assert _mm(**cut, ws=None) == 1 and _mm(**cut, ws_bytes=need - 1) == 1
+    assert _mm(**cut, ws=A + 5 * STEP + 8) == 3
+    assert _mm(**cut, ws=A) == 4 and _mm(**cut, ws=A + 4 * STEP) == 4
 
 
 def test_binding_refusals():

@@ -122,6 +122,56 @@ def test_strided_rows(M, N, K, transposed, pitch, lead):
         assert (buf[:, :lead] == 9).all() and (buf[:, lead + C:] == 9).all()
 
 
+CUT = [(17, 1040, 5120), (64, 640, 4112), (129, 272, 8192), (130, 16, 16384), (300, 1296, 2576), (257, 2064, 4096)]
+
+
+@pytest.mark.parametrize("M,N,K", CUT)
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("t", sorted(T))
+def test_cut_contraction(M, N, K, transposed, t):
+    """Few tiles and a long contraction, which is cut into slices: a workspace of the very
+    size, what lies behind it and around the output untouched, the same bits each time."""
+    if transposed:
+        N, K = K, N
+    need = _lib.load().hc_fp8_mm_workspace_bytes(transposed, M, N, K)
+    C = K if transposed else N
+    assert need >= 2 * M * C * 4 and need % (M * C * 4) == 0
+    i = _inputs(M, N, K, transposed, "fp32", "ue8m0", pitch=16)
+    room = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+    first = None
+    for lead in (8, 1):
+        buf = torch.full((M, C + 16), 9.0, dtype=T[t], device="cuda")
+        y = hcg.hc_fp8_mm(*i, transposed=transposed, y=buf[:, lead:lead + C], workspace=room[:need])
+        _check(y, *i, transposed)
+        assert (buf[:, :lead] == 9).all() and (buf[:, lead + C:] == 9).all() and (room[need:] == 255).all()
+        assert first is None or torch.equal(first, y)
+        first = y.clone()
+        room[:need] = 255
+    assert torch.equal(first, hcg.hc_fp8_mm(*i, transposed=transposed, out_dtype=T[t]))
+    with pytest.raises(RuntimeError):
+        hcg.hc_fp8_mm(*i, transposed=transposed, workspace=room[:need - 1])
+
+
+def test_cut_contractions_share_a_workspace():
+    """Graphs of products of one workspace, replayed in turn on one stream; NaN codes."""
+    a, b = _inputs(64, 640, 4112, False, "ue8m0", "fp32"), _inputs(33, 272, 8192, False, "fp32", "fp32", seed=5)
+    want = [hcg.hc_fp8_mm(*i) for i in (a, b)]
+    room = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    outs, graphs = [torch.empty_like(w) for w in want], []
+    for i, o in zip((a, b), outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            hcg.hc_fp8_mm(*i, y=o, workspace=room)
+    for _ in range(20):
+        for o, g in zip(outs, graphs):
+            o.fill_(7)
+            g.replay()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    x, sx, w, sw = a
+    y = hcg.hc_fp8_mm(_put(x, (2, 4100), 0x7f), sx, w, sw)
+    assert y[2].isnan().all() and torch.equal(y[:2], want[0][:2]) and torch.equal(y[3:], want[0][3:])
+
+
 def test_nan_codes_and_scales():
     """A NaN among the codes or scales spoils what it goes into, nothing else."""
     for M in (4, 300):
