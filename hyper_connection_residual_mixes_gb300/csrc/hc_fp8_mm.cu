@@ -10,6 +10,16 @@
 // while the next block's products run into the other half of the tensor memory.  Rows
 // lie on the MMA's M side, so that a thread, which holds a row, has one scale for all
 // its columns of a block of the matrix.
+//
+// What bounds it: a block of 128 x 256 x 128 takes the tensor cores 512 cycles, but 1,050
+// pass, in which the eight writing warps load 32,768 sums from tensor memory and add each to its
+// accumulator (a packed FMA for two), on the same issue slots as all else.  16,384 x
+// 10,240 x 5,120: 750 us, 2.29 PFLOP/s; transposed 2.30.  What other shapes of the same took there, in us:
+// pairs of CTAs on 256 x 256 787 (1,187 with a releasing arrival at the other CTA for each block), 128 x 128
+// tiles 1,022 in four parts of columns, three issuing warps in turn 753, the next sums loaded
+// between the FMAs of the last 772, MMAs held back to even the issue 768 and more.
+// Small products are cut to fill the SMs (cut), up to 16 rows stream the matrix past mma.sync
+// (k_fp8_few: 16 x 16,384 x 5,120 in 20 us, 0.62 of the copy rate, 1 x 512 x 1,024 in 3.1).
 #include <atomic>
 
 #include <cuda.h>
@@ -29,7 +39,7 @@ constexpr int kBK = 128;  // contraction per stage: one block of scales, one 128
 constexpr int kGroup = 8; // tiles of rows that are walked together
 constexpr int kEpilogue = 8, kThreads = 32 * (kEpilogue + 4);  // (whole groups of four warps: registers are moved between these)
 // Registers a thread: what a block of kThreads is launched with, and of that what the
-// writing warps take (128 accumulators at BN = 256) and the others keep.
+// writing warps take (128 accumulators and 64 loaded sums at BN = 256) and the others keep.
 constexpr int kRegs = 168, kRegsWriting = 216, kRegsOther = 72;
 static_assert(kEpilogue * kRegsWriting + 4 * kRegsOther <= (kEpilogue + 4) * kRegs, "the block's registers");
 
@@ -471,8 +481,8 @@ bool make_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, int
 
 constexpr int kDevices = 64;
 
-// Launches on every SM, once per
-// kernel and device finding out how many and allowing the shared memory.
+// Launches on every SM, once per kernel and device finding out how many there are and
+// allowing the shared memory.
 template <int BN, bool kMn, bool kSplit>
 cudaError_t launch(const CUtensorMap &tx, const CUtensorMap &tw, const Args &a, cudaStream_t s) {
     using C = Cfg<BN>;

@@ -8,6 +8,15 @@
 // Backward, with xh = r rstd and wg = g_y w:
 //   g_x = g_r + rstd (wg - xh mean(wg xh)),  g_w = sum over rows of g_y xh.
 // All sums run in fp32.
+//
+// Bound by HBM: each input is read once, each output written once, and a row stays in
+// registers (forward) or in its slot of shared memory (backward) between the sums and what
+// needs them.  Long runs of rows come through a ring of bulk copies, short ones and rows that do not
+// line up straight into registers.  Measured, in us, and of 6,767 GB/s (a plain
+// copy): forward of 65,536 x 5,120 bf16 with residual and 8-bit output 361 (0.96), backward of
+// 8,192 x 5,120 with fp32 gradients 89 (0.97), 16 rows of 5,120 2.6 (one row's load, sum and write
+// after another), 1,501 x 1,031 fp32 backward 12.  Rows that do not line up: 0.1 to 0.25, single
+// values make too many loads.
 #include <atomic>
 
 #include <cuda.h>
@@ -417,7 +426,8 @@ cudaError_t forward(Args a, cudaStream_t s) {
                       multiple(a.w, 0, 1, a.w_type == HC_F32 ? 16 : 8);
     a.codes_wide = multiple(a.codes, a.cs, 1, W);
     const int per = wide ? W : 1, need = (a.d + per - 1) / per;
-    // (the ring for many rows)
+    // (the ring for rows that fill it several times: 16,384 values an SM.  65,536 x 5,120 bf16: 361 us against
+    // 417 of a block a row; for 16 rows of 5,120 a block a row 2.6 us, the ring's set-up alone takes 2)
     if (wide && a.d > 512 && a.n * a.d >= 16384 * (int64_t)sm_count()) {
         const int threads = (a.d + 511) / 512 * 32, slot = (int)(a.d * size) * (a.residual ? 2 : 1);
         if (threads <= 320) return start_ring<k_rms_norm_ring<T, 320, 2>>(a, threads, slot, s);
@@ -441,7 +451,7 @@ cudaError_t forward(Args a, cudaStream_t s) {
 
 // ------------------------------------------------------------ backward
 // A block walks over rows, its threads own columns and keep their sums of g xh; it
-// leaves a row of partial sums in the workspace, k_columns adds these in a fixed
+// leaves a row of partial sums in the workspace, k_rms_columns adds these in a fixed
 // order.  The second pass over a row reads it again, from L1 or L2.
 struct BackArgs {
     const void *g, *gr, *r, *w;
@@ -541,7 +551,8 @@ __global__ void __launch_bounds__(kWarps ? 256 : 1024) k_rms_backward(const Back
 
 // The same with the rows of r, g and g_r through a ring: 8 columns a thread in two runs of 4.
 // Both passes over a row read it from its slot, which is filled again once the next
-// row's barrier has passed.
+// row's barrier has passed.  8,192 x 5,120, fp32 gradients: 179 us with rows read twice through
+// L2, 89 here.  Rows past 8,192 leave fewer than three slots and take the kernel above (0.53 of HBM).
 template <typename TX, typename TG, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads, 1) k_rms_backward_ring(const BackArgs a, int slots) {
     extern __shared__ __align__(16) uint8_t s_rows[];
@@ -710,7 +721,7 @@ cudaError_t backward(const BackArgs &a, float *gw, cudaStream_t s) {
 // ------------------------------------------------------------ casts
 // Rows in groups of 128: VEC values a thread, 128 / VEC threads a group, kCastVectors
 // groups a thread one after the other, their loads all under way at once.  kFlat: dense rows of
-// whole groups, whose places need no division.
+// whole groups, whose places need no division (8,192 x 10,240 bf16: 68 us against 96).
 constexpr int kCastThreads = 256, kCastVectors = 4;
 template <typename T, int VEC, bool kFlat>
 __global__ void __launch_bounds__(kCastThreads)
