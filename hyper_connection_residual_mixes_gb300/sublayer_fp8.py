@@ -299,7 +299,7 @@ def hc_moe_tokens(x, w_up, w_down, ids=None, weights=None, logits=None, top_k=No
         fits = up is not None and down is not None and (down_scales is not None) == f8
         us = ds = None
         if f8 and fits:
-            bits = 1 << (_F32 if up_scales.dtype is torch.float32 else _U8)
+            bits = 1 << (_F32 if getattr(up_scales, "dtype", None) is torch.float32 else _U8)
             bi, bd = -(-inner // FP8_BLOCK), -(-d // FP8_BLOCK)
             us, ds = X.dense(up_scales, bits, dev, E, 2, bi, bd), X.dense(down_scales, bits, dev, E, bd, bi)
             fits = us is not None and ds is not None

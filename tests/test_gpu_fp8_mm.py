@@ -172,6 +172,24 @@ def test_cut_contractions_share_a_workspace():
     assert y[2].isnan().all() and torch.equal(y[:2], want[0][:2]) and torch.equal(y[3:], want[0][3:])
 
 
+@pytest.mark.parametrize("M", [3, 16, 40])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_offsets_past_32_bits(M, transposed):
+    """The last columns of products with a matrix of 65,552 x 65,536 codes."""
+    N, K = 65552, 65536
+    g = _gen(M)
+    w = torch.randint(0, 120, (N, K), generator=g, dtype=torch.uint8, device="cuda")
+    C, L = (K, N) if transposed else (N, K)
+    x, sx = _codes((M, L), g), _scales((M, _blocks(L)), "ue8m0", g)
+    sw = _scales((_blocks(N), _blocks(K)), "fp32", g)
+    y = hcg.hc_fp8_mm(x, sx, w, sw, transposed=transposed)
+    assert y.shape == (M, C)
+    for c in (0, C // 256 * 128, (C - 1) // 128 * 128):
+        part = w[:, c:c + 128] if transposed else w[c:c + 128]
+        s = sw[:, c // 128:c // 128 + 1] if transposed else sw[c // 128:c // 128 + 1]
+        _check(y[:, c:c + 128], x, sx, part.contiguous(), s.contiguous(), transposed)
+
+
 def test_nan_codes_and_scales():
     """A NaN among the codes or scales spoils what it goes into, nothing else."""
     for M in (4, 300):

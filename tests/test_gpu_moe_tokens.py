@@ -117,6 +117,30 @@ def test_given_choice(T_, E, k, d, inner, x, w):
     assert torch.equal(y, _call(xv, wv, ids=ids, weights=p))
 
 
+def test_offsets_past_32_bits():
+    """Experts whose weights lie more than 2^32 bytes behind the first's."""
+    E, d, inner = 66, 8192, 8192
+    g = torch.Generator(device="cuda").manual_seed(5)
+    codes = lambda *shape: torch.randint(0, 100, shape, generator=g, dtype=torch.uint8, device="cuda") | torch.randint(0, 2, (shape[-1],), generator=g, dtype=torch.uint8, device="cuda") << 7
+    scales = lambda *shape: torch.randint(108, 112, shape, generator=g, dtype=torch.uint8, device="cuda")
+    w = {"up": codes(E, 2, inner, d), "down": codes(E, d, inner),
+         "up_scales": scales(E, 2, inner // 128, d // 128), "down_scales": scales(E, d // 128, inner // 128)}
+    x = torch.randn((3, d), generator=g, device="cuda").bfloat16()
+    ids = torch.tensor([[65, 0], [64, 65], [33, 1]], dtype=torch.int32, device="cuda")
+    p = torch.rand((3, 2), generator=g, device="cuda")
+    _check(_call(x, w, ids=ids, weights=p), x, w, ids, p)
+
+
+def test_scales_that_are_no_tensors():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, w = torch.randn((2, 64), generator=g, device="cuda").bfloat16(), _weights(4, 64, 32, "bf16", "fp32", g)
+    lg = torch.randn((2, 4), generator=g, device="cuda")
+    with pytest.raises(TypeError, match="up_scales must be"):
+        hcg.hc_moe_tokens(x, w["up"], w["down"], logits=lg, top_k=2, up_scales=1.0, down_scales=w["down_scales"])
+    with pytest.raises(TypeError, match="down_scales must be"):
+        hcg.hc_moe_tokens(x, w["up"], w["down"], logits=lg, top_k=2, up_scales=w["up_scales"], down_scales=1.0)
+
+
 @pytest.mark.parametrize("T_", list(range(1, 20)) + [31, 32, 33, 47, 48, 49, 63, 64])
 def test_every_count_of_tokens(T_):
     """... all of them to one expert, and to the same two of four."""

@@ -122,6 +122,37 @@ def test_forward_many_rows(d, x):
     _check_forward(r(1999, d).to(T[x]), r(d), r(1999, d).to(T[x]))
 
 
+@pytest.mark.parametrize("n,d", [(400, 8192), (320, 12288), (310, 16384)])
+@pytest.mark.parametrize("x", ["bf16", "fp32"])
+def test_many_wide_rows(n, d, x):
+    """Rows of which few, or one, fit into an SM's memory at a time."""
+    r = _rand(d)
+    xv, w, res = r(n, d).to(T[x]), r(d), r(n, d).to(T[x])
+    got = _check_forward(xv, w, res)
+    _check_forward(xv, w, None)
+    gy, gr = r(n, d), r(n, d)
+    _check_backward(gy, xv, w, got["rstd"], gr, hcg.hc_rms_norm_backward(gy, xv, w, got["rstd"], g_r=gr))
+
+
+def test_offsets_past_32_bits():
+    """The last of 840,000 rows of 5,120, more than 2^32 values."""
+    n, d = 840000, 5120
+    x, w = torch.empty((n, d), dtype=torch.bfloat16, device="cuda"), _rand(1)(d)
+    x[:64], x[-64:] = _rand(2)(64, d), _rand(3)(64, d)
+    x[64:-64] = 1
+    got = hcg.hc_rms_norm(x, w, out="both", return_rstd=True)
+    _, rstd, y = _ref(x[-64:], w, None, 1e-6)
+    assert ((got["y"][-64:].double() - y).abs() <= (_half(x.dtype) + 100 * U) * y.abs() + _tiny(x.dtype)).all()
+    _check_codes(y, got["codes"][-64:], got["scales"][-64:], 100 * U)
+    codes, scales = hcg.hc_fp8_cast(got["y"], codes=got["codes"], scales=got["scales"])
+    again = hcg.hc_fp8_cast(got["y"][-64:].clone())
+    assert torch.equal(codes[-64:], again[0]) and torch.equal(scales[-64:], again[1])
+    back = hcg.hc_rms_norm_backward(x, x, w, got["rstd"], g_x=got["y"])     # (g_x over y, which nothing reads)
+    gy = x[-64:]
+    alone = hcg.hc_rms_norm_backward(gy.contiguous(), gy.contiguous(), w, got["rstd"][-64:].contiguous())
+    _check_backward(gy, gy, w, got["rstd"][-64:], None, {"g_x": back["g_x"][-64:], "g_norm_w": alone["g_norm_w"]})
+
+
 @pytest.mark.parametrize("d,pitch,lead", [(512, 8, 0), (512, 1, 0), (512, 7, 1), (100, 4, 4), (5120, 5120, 0), (1030, 2, 2)])
 @pytest.mark.parametrize("x,g", [("bf16", "fp32"), ("fp32", "fp32"), ("fp16", "fp16")])
 def test_strided_rows(d, pitch, lead, x, g):
