@@ -20,6 +20,7 @@
 // between the FMAs of the last 772, MMAs held back to even the issue 768 and more.
 // Small products are cut to fill the SMs (cut), up to 16 rows stream the matrix past mma.sync
 // (k_fp8_few: 16 x 16,384 x 5,120 in 20 us, 0.62 of the copy rate, 1 x 512 x 1,024 in 3.1).
+#include <algorithm>
 #include <atomic>
 
 #include <cuda.h>
@@ -549,12 +550,13 @@ cudaError_t join(const Args &a, cudaStream_t s) {
 // How a product is cut: into tiles of 128 x bn and, where few tiles leave SMs idle, the
 // contraction into slices of `per` blocks that k_join adds up.  The rule counts cycles:
 // a block of 128 takes an SM some 1,050 with 256 columns and 860 with 128 (the signals and
-// the sums, not the MMAs); the joining launch 1,500, a slice 1,500 more, and its sums 2.2 per 1,000
-// to write and read.  Measured, against the better of the whole contractions (us): 17 x 5,120 x
-// 5,120 17.9 -> 10.5 (5 slices; 2: 14.0, 7: 11.9), 128 rows 19.6 -> 12.9, 256 rows 20.0 -> 15.2 (3),
-// 256 x 2,048 x 8,192 27.9 -> 14.0 (8); but 256 x 8,192 x 2,048 10.3 -> 12.3 (2) and 128 x 16,384 x
-// 5,120 19.8 -> 21.1 (2), which the rule leaves whole.  A constant number of SMs: the
-// cut decides the workspace and the order of the sums, which must not depend on the device.
+// the sums, not the MMAs), but w comes in at 2,700 bytes a cycle at the most; the joining launch 1,500,
+// a slice 1,500 more, and its sums 2.2 per 1,000 to write and read.  Measured with w in HBM, against the
+// better of the whole contractions (us): 17 x 5,120 x 5,120 18.3 -> 12.4 (4 slices; 2: 15.0, 7: 13.2),
+// 128 rows 20.0 -> 14.6 (4), 256 rows 20.6 -> 16.4 (3), 256 x 2,048 x 8,192 28.3 -> 15.3 (5); but
+// 256 x 8,192 x 2,048 10.6 -> 13.6 (2) and 64 x 16,384 x 5,120 19.8 -> 21.9 (2), which the rule leaves
+// whole.  A constant number of SMs: the cut decides the workspace and the order of the sums,
+// which must not depend on the device.
 constexpr int kSms = 152, kMostSlices = 32;
 struct Cut {
     int bn, slices, per;
@@ -563,11 +565,12 @@ Cut cut(int64_t M, int C, int L) {
     const int64_t rows = (M + kM - 1) / kM, blocks = (L + kBK - 1) / kBK;
     const int64_t wide = rows * ((C + 255) / 256), narrow = rows * ((C + 127) / 128);
     Cut best{128, 1, (int)blocks};
-    double least = (double)((narrow + kSms - 1) / kSms * blocks) * 860;
+    const double reading = (double)C * L / 2700;
+    double least = std::max(reading, (double)((narrow + kSms - 1) / kSms * blocks) * 860);
     for (int64_t s = 1; s == 1 || (s <= kMostSlices && s <= blocks && wide * s <= kSms); ++s) {
         const int64_t per = (blocks + s - 1) / s;
         if ((blocks + per - 1) / per != s) continue;
-        const double cycles = (double)((wide * s + kSms - 1) / kSms * per) * 1050 +
+        const double cycles = std::max(reading, (double)((wide * s + kSms - 1) / kSms * per) * 1050) +
                               (s == 1 ? 0 : 1500 + 1500 * (double)s + 0.0022 * (double)(s * M * C));
         if (cycles <= least) least = cycles, best = Cut{256, (int)s, (int)per};
     }
