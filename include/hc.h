@@ -579,7 +579,9 @@ hc_status hc_rms_norm_backward(const void *g_y, int64_t g_stride, const void *g_
  *                                      sum over f in b of x[m][f] w[f][k].
  * A block's products are summed in fp32 by the tensor cores (whose additions may cut
  * off rather than round the last bit of a partial sum), scaled and added up in
- * fp32, and rounded once to y's type.  (The gradient of the weights is
+ * fp32, and rounded once to y's type.  Where few rows meet a long contraction it is cut
+ * into slices, whose sums go through the workspace and are added in their order: the
+ * same call gives the same bits, on any device.  (The gradient of the weights is
  * hc_grouped_mm_weights of the 16-bit rows, as one expert's.)
  *
  *   x [M, K] codes (transposed: [M, N]), rows x_stride apart                 in

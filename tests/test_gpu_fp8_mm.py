@@ -4,7 +4,9 @@ Bounds.  Products of two codes are exact.  A block's 128 of them are added by th
 tensor cores, which may cut off the last bit: at most 132 steps of 2^-23 of the sum of
 their sizes; the scaled blocks are added in fp32: a half step each.  With S the
 sum of all terms' sizes and B the number of blocks
-    |d y| <= (half a step of y's type) |y| + (132 * 2^-23 + (B + 4) * 2^-24) S."""
+    |d y| <= (half a step of y's type) |y| + (132 * 2^-23 + (B + 4) * 2^-24) S.
+(A contraction that is cut adds the blocks of a slice, then the slices: no more than B
+roundings.)"""
 import pytest
 import torch
 
