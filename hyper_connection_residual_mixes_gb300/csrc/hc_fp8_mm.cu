@@ -95,16 +95,6 @@ __device__ __forceinline__ void umma_block(uint32_t d, uint64_t a0, uint64_t b0,
         : "memory");
 }
 
-// A box of a matrix, whose map has a third dimension that is always 0 (see make_map).
-__device__ __forceinline__ void load_box(uint32_t dst, const void *tmap, uint32_t bar, int c, int row, uint64_t policy) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c), "r"(row), "r"(0), "r"(bar), "l"(policy)
-        : "memory");
-}
-
 // Whether a barrier's phase is complete, without waiting for it.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -240,11 +230,11 @@ k_fp8_mm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUten
                     const uint32_t bar = smem_u32(&full_bar[slot]);
                     expect_bytes(bar, C::kStage);
                     ++issued;
-                    load_box(sa, &tm_x, bar, i * kBK, m, pol);
+                    load_2d<false>(sa, &tm_x, bar, i * kBK, m, pol);
 #pragma unroll
                     for (int j = 0; j < BN; j += 128) {
-                        if (kMn) load_box(sa + C::kABytes + j * kBK, &tm_w, bar, c + j, i * kBK, pol);
-                        else load_box(sa + C::kABytes + j * kBK, &tm_w, bar, i * kBK, c + j, pol);
+                        if (kMn) load_2d<false>(sa + C::kABytes + j * kBK, &tm_w, bar, c + j, i * kBK, pol);
+                        else load_2d<false>(sa + C::kABytes + j * kBK, &tm_w, bar, i * kBK, c + j, pol);
                     }
                     if (++slot == S) slot = 0, parity ^= 1u;
                 }
@@ -480,15 +470,12 @@ __global__ void __launch_bounds__(32 * kFewWarps<NB>, 1) k_fp8_few(const Args a,
 }
 
 // A matrix of codes [rows][width], rows `stride` bytes apart, boxes of 128 x 128, 128-byte
-// swizzle, zeros outside: the first of two such matrices, so far apart that the map spans 128 KB and
-// more; the second is never read.  Loads through maps that span less are slow: 17 x 16,384 x
-// 5,120 took 25 us with a plain map of x, 26 rows (133,120 bytes) 19.5, and both take 19.5 with this one.
+// swizzle, zeros outside.
 bool make_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, int64_t stride) {
     const auto enc = encoder();
-    const int64_t least = (131072 + stride - 1) / stride, apart = stride * (rows > least ? rows : least);
-    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, 2}, strides[2] = {(cuuint64_t)stride, (cuuint64_t)apart};
-    const cuuint32_t box[3] = {kBK, 128, 1}, one[3] = {1, 1, 1};
-    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, one,
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
+    const cuuint32_t box[2] = {kBK, 128}, one[2] = {1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, one,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
