@@ -20,13 +20,16 @@ __device__ __forceinline__ void load_piece(uint32_t to, const uint8_t *from, boo
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there0 ? 16 : 0) : "memory");
     asm volatile("cp.async.cg.shared.global.L2::128B [%0 + 512], [%1 + 64], 16, %2;" ::"r"(to), "l"(from), "r"(there1 ? 16 : 0) : "memory");
 }
+// 16 bytes of shared memory
+__device__ __forceinline__ void read16(uint32_t *w, uint32_t at) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+}
 struct Piece {
     uint32_t w[8];
 };
 __device__ __forceinline__ Piece read_piece(uint32_t at) {
     Piece p;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(p.w[0]), "=r"(p.w[1]), "=r"(p.w[2]), "=r"(p.w[3]) : "r"(at) : "memory");
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + 512];" : "=r"(p.w[4]), "=r"(p.w[5]), "=r"(p.w[6]), "=r"(p.w[7]) : "r"(at) : "memory");
+    read16(p.w, at), read16(p.w + 4, at + 512);
     return p;
 }
 // four codes as two pairs of fp16
@@ -68,6 +71,16 @@ template <typename T, bool kF8>
 __device__ __forceinline__ void multiply(float (&acc)[4], const Rows16<kF8> &w, const uint32_t (&x)[kPairsOf<kF8>]) {
 #pragma unroll
     for (int i = 0; i < kPairsOf<kF8> / 2; ++i) mma<T>(acc, w.a[i][0], w.a[i][1], w.a[i][2], w.a[i][3], x[2 * i], x[2 * i + 1]);
+}
+// ... with two operands, in two chains of MMAs that do not wait for one another
+template <typename T, bool kF8>
+__device__ __forceinline__ void multiply_both(float (&acc)[4], const Rows16<kF8> &w, const uint32_t (&x)[kPairsOf<kF8>], float (&acc2)[4],
+                                              const uint32_t (&x2)[kPairsOf<kF8>]) {
+#pragma unroll
+    for (int i = 0; i < kPairsOf<kF8> / 2; ++i) {
+        mma<T>(acc2, w.a[i][0], w.a[i][1], w.a[i][2], w.a[i][3], x2[2 * i], x2[2 * i + 1]);
+        mma<T>(acc, w.a[i][0], w.a[i][1], w.a[i][2], w.a[i][3], x[2 * i], x[2 * i + 1]);
+    }
 }
 // acc += ..., times the scales of the two tiles' blocks and what undoes the tokens' powers of two
 template <bool kF8>

@@ -622,9 +622,9 @@ hc_status hc_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scales, hc
  * a token with both weights.  A token without an expert gets zeros.
  *
  * Sums of products are in fp32; the activation is kept in fp32 and goes into the
- * second product as two bf16 numbers (16 bits of it) for bf16 weights, as two fp16
- * numbers (22 bits) for fp16 outputs and as one (11 bits, 3 more than y has) for bf16
- * outputs of 8-bit weights, scaled by a power of two for each block of it; y is rounded once.
+ * second product as two bf16 numbers (16 bits of it) for bf16 weights, else as two fp16
+ * numbers, scaled by a power of two for each block of it (22 bits; of values below 2^-17 of
+ * the largest of their block what is above 2^-39 of that); y is rounded once.
  *
  *   x [T, d] of type (bf16 or fp16), rows x_stride >= 0 apart                in
  *   logits [T, experts] fp32, or NULL                                        in
