@@ -446,7 +446,8 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
 template <typename TX, bool kF8>
 __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
     constexpr int kBytes = kF8 ? 1 : 2, W = kDownWarps, NP = kDownPairs, kPairs = kPairsOf<kF8>, kRows = 16 * NP;
-    // a goes into the products as two numbers: bf16 for bf16 weights (16 bits of it), else fp16 (22 bits)
+    // a goes into the products as three bf16 numbers for bf16 weights (all 24 bits of it), else as two
+    // fp16 numbers (22 bits)
     constexpr bool kBf16 = !kF8 && __is_same(TX, __nv_bfloat16);
     extern __shared__ __align__(128) uint8_t smem[];
     float *const red = reinterpret_cast<float *>(smem + W * kDownRing);  // [2][warp][pair][4][lane]
@@ -531,14 +532,16 @@ __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
                     for (int q = 0; q < 4; ++q) acc[j][q] = 0.0f;
                 bool more = true;
                 while (more) {
-                    uint32_t tok[kPairs], low[kPairs];
+                    uint32_t tok[kPairs], low[kPairs], last[kBf16 ? kPairs : 1];
                     float unit[2] = {1.0f, 1.0f};
                     const float *const f = reinterpret_cast<const float *>(raw);
-                    if constexpr (kBf16) {
+                    if constexpr (kBf16) {  // (cut off after 8 bits each time, so that what is left is exact)
 #pragma unroll
                         for (int q = 0; q < kPairs; ++q) {
-                            tok[q] = pack_bf16x2(f[2 * q], f[2 * q + 1]);
-                            low[q] = pack_bf16x2(f[2 * q] - bf16lo(tok[q]), f[2 * q + 1] - bf16hi(tok[q]));
+                            tok[q] = cut_bf16x2(f[2 * q], f[2 * q + 1]);
+                            const float a0 = f[2 * q] - bf16lo(tok[q]), a1 = f[2 * q + 1] - bf16hi(tok[q]);
+                            low[q] = cut_bf16x2(a0, a1);
+                            last[kBf16 ? q : 0] = cut_bf16x2(a0 - bf16lo(low[q]), a1 - bf16hi(low[q]));
                         }
                     } else {
                         float amax = 0.0f, own;
@@ -570,21 +573,28 @@ __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
                             const uint32_t from_pair = ring + (uint32_t)(j * 2 * kCell);
                             const Rows16<kF8> w(read_piece(from_pair), read_piece(from_pair + kCell));
                             if constexpr (kBf16) {
-                                multiply<TX, false>(acc[j], w, tok);
-                                multiply<TX, false>(acc[j], w, low);
+                                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                multiply<TX, false>(part, w, last);
+                                multiply_both<TX, false>(acc[j], w, tok, part, low);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) acc[j][q] += part[q];
                             } else {
-                                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f}, more_bits[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s0, s1;
                                 if constexpr (kF8) {
+                                    float more[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                                     for (int q = 0; q < 4; ++q) read16(low + 4 * q, smem_u32(lows + 32 * q));
-                                    multiply_both<__half, kF8>(part, w, tok, more_bits, low);
+                                    multiply_both<__half, kF8>(part, w, tok, more, low);
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) part[q] += more[q];
+                                    s0 = __shfl_sync(0xffffffffu, scale, 2 * j), s1 = __shfl_sync(0xffffffffu, scale, 2 * j + 1);
                                 } else {
+                                    s0 = __shfl_sync(0xffffffffu, scale, 2 * j), s1 = __shfl_sync(0xffffffffu, scale, 2 * j + 1);
                                     multiply<__half, kF8>(part, w, low);
                                     multiply<__half, kF8>(part, w, tok);
                                 }
-                                const float s0 = __shfl_sync(0xffffffffu, scale, 2 * j), s1 = __shfl_sync(0xffffffffu, scale, 2 * j + 1);
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) acc[j][q] = fmaf(part[q] + more_bits[q], (q < 2 ? s0 : s1) * unit[q & 1], acc[j][q]);
+                                for (int q = 0; q < 4; ++q) acc[j][q] = fmaf(part[q], (q < 2 ? s0 : s1) * unit[q & 1], acc[j][q]);
                             }
                         }
                         fetch(j);
@@ -629,8 +639,10 @@ __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
 
 constexpr int kDevices = 64;
 constexpr int kUpSmem = kUpWarps * kUpRing + 2 * kUpWarps * kUpPairs * 128 * 4 + (int)sizeof(Lists);
-constexpr int kDownSmem = kDownWarps * kDownRing + 2 * kDownWarps * kDownPairs * 128 * 4 + kMaxTokens * 16 * kDownPairs * 4 + (int)sizeof(Lists) + kLows;
-static_assert(kUpSmem <= 227 * 1024 && kDownSmem <= 227 * 1024, "an SM's memory");
+template <bool kF8>
+constexpr int kDownSmem = kDownWarps * kDownRing + 2 * kDownWarps * kDownPairs * 128 * 4 + kMaxTokens * 16 * kDownPairs * 4 + (int)sizeof(Lists) +
+                          (kF8 ? kLows : 0);
+static_assert(kUpSmem <= 227 * 1024 && kDownSmem<true> <= 227 * 1024, "an SM's memory");
 
 // SMs of the current device; once per device allows the kernel its shared memory.
 template <typename K>
@@ -652,7 +664,7 @@ cudaError_t start_down(const Args &a, cudaStream_t s) {
     static std::atomic<int> sms[kDevices];
     const auto k = k_moe_down<TX, kF8>;
     int n = 0;
-    const cudaError_t e = allow(k, kDownSmem, sms, n);
+    const cudaError_t e = allow(k, kDownSmem<kF8>, sms, n);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -660,7 +672,7 @@ cudaError_t start_down(const Args &a, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
     const int most = (a.d + 7) / 8;
     cfg.gridDim = dim3((unsigned)(n < most ? n : most)), cfg.blockDim = dim3(32 * kDownWarps);
-    cfg.dynamicSmemBytes = kDownSmem, cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = kDownSmem<kF8>, cfg.stream = s, cfg.attrs = &early, cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 

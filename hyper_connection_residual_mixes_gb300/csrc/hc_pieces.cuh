@@ -38,6 +38,8 @@ __device__ __forceinline__ void widen(uint32_t c, uint32_t &lo, uint32_t &hi) {
         : "=r"(lo), "=r"(hi)
         : "r"(c));
 }
+// two values cut off to bf16
+__device__ __forceinline__ uint32_t cut_bf16x2(float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); }
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);

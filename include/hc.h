@@ -622,7 +622,7 @@ hc_status hc_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scales, hc
  * a token with both weights.  A token without an expert gets zeros.
  *
  * Sums of products are in fp32; the activation is kept in fp32 and goes into the
- * second product as two bf16 numbers (16 bits of it) for bf16 weights, else as two fp16
+ * second product as three bf16 numbers (all 24 bits of it) for bf16 weights, else as two fp16
  * numbers, scaled by a power of two for each block of it (22 bits; of values below 2^-17 of
  * the largest of their block what is above 2^-39 of that); y is rounded once.
  *

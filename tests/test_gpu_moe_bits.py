@@ -31,7 +31,7 @@ def _built():
     _lib.load()
 
 
-@pytest.mark.parametrize("x,w,h", [("bf16", "ue8m0", 2.0 ** -22), ("bf16", "fp32", 2.0 ** -22),
+@pytest.mark.parametrize("x,w,h", [("bf16", "ue8m0", 2.0 ** -22), ("bf16", "fp32", 2.0 ** -22), ("bf16", "same", 0.0),
                                    ("fp16", "ue8m0", 2.0 ** -22), ("fp16", "same", 2.0 ** -22)])
 @pytest.mark.parametrize("tokens", [1, 8, 33])
 def test_differences_of_activations(x, w, h, tokens):
