@@ -113,7 +113,7 @@ __device__ __forceinline__ void choose(const Args &a, Lists &l, int t, int lane,
     }
     uint32_t last = 0xffffffffu;
     int last_e = -1, mine_e = -1;
-    float mine = 0.0f, chosen = 0.0f;
+    float mine = 0.0f, chosen = 0.0f, from = 0.0f;
     for (int j = 0; j < a.top; ++j) {
         uint32_t key = 0;
         int e = 0x7fffffff;
@@ -135,8 +135,10 @@ __device__ __forceinline__ void choose(const Args &a, Lists &l, int t, int lane,
         for (int i = 0; i < kKept; ++i)
             if (e == lane + 32 * i) keys[i] = 0u;
         const float v = of_key(top);
-        if (j == 0) best = v;
-        const float s = a.sigmoid ? 1.0f / (1.0f + expf(-v)) : v == best ? 1.0f : expf(v - best);
+        if (j == 0) best = v, from = a.normalise && v < -20.0f ? v : 0.0f;
+        // (below -20 the sigmoid is e^v to 2^-28 of itself; divided by the sum its largest may be taken out,
+        // and has to be: below -87 the exponentials leave the normal numbers)
+        const float s = a.sigmoid ? v < -20.0f ? expf(v - from) : 1.0f / (1.0f + expf(-v)) : v == best ? 1.0f : expf(v - best);
         chosen += s;
         if (lane == j) mine = s, mine_e = e;
     }
