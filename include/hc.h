@@ -579,7 +579,9 @@ hc_status hc_rms_norm_backward(const void *g_y, int64_t g_stride, const void *g_
  *                                      sum over f in b of x[m][f] w[f][k].
  * A block's products are summed in fp32 by the tensor cores (whose additions may cut
  * off rather than round the last bit of a partial sum), scaled and added up in
- * fp32, and rounded once to y's type.  Where few rows meet a long contraction it is cut
+ * fp32, and rounded once to y's type.  The two scales of a block are multiplied with one another
+ * first, and their product is an fp32 number: below 2^-126 it keeps fewer bits, to steps of 2^-149 (of
+ * a block's sum, at most 2^25), and from 2^128 on it is infinite (times a sum of 0: NaN).  Where few rows meet a long contraction it is cut
  * into slices, whose sums go through the workspace and are added in their order: the
  * same call gives the same bits, on any device.  (The gradient of the weights is
  * hc_grouped_mm_weights of the 16-bit rows, as one expert's.)
