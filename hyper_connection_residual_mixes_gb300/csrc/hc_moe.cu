@@ -241,13 +241,16 @@ __device__ __forceinline__ void route(const Args &a, Lists &l, bool write) {
     __syncthreads();
 }
 
-// fp16 copies of a token's values over a piece carry a power of two that brings the
-// largest to [2^14, 2^15): 11 bits of each value, of small ones 2^-39 of the largest.  Of that
-// largest: the power, and what undoes it.
-__device__ __forceinline__ float power_of(float amax, float &unit) {
-    int b = (int)(__float_as_uint(amax) >> 23);
+// fp16 copies of a token's values over a piece carry an even power of two that brings the
+// largest to [2^13, 2^15): 11 bits of each value, of small ones 2^-38 of the largest.  Of that
+// largest: the power, and the root of what undoes it.  One root goes to the sums (0 or from 2^-33 to 2^31), the
+// other to the weights' scales, so that both stay normal numbers for scales from 2^-63 to 2^70 and any
+// token, from 2^-100 for tokens of 2^-38 and more.  (Undone in one product with the scales, tokens of 2^-100 and
+// scales of 2^-34, whose result scales of 2^100 bring back, had lost all their bits.)
+__device__ __forceinline__ float power_of(float amax, float &root) {
+    int b = (int)(__float_as_uint(amax) >> 23) | 1;
     b = b < 15 ? 15 : b;
-    unit = __uint_as_float((uint32_t)(b - 14) << 23);
+    root = __uint_as_float((uint32_t)((b - 141) / 2 + 127) << 23);
     return __uint_as_float((uint32_t)(268 - b) << 23);
 }
 
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
             for (int k = 0; k < 4; ++k) acc[j][k] = 0.0f;
         for (int k = begin(un); k < pieces; k += W) {
             uint32_t tok[kPairs];
-            float unit[2] = {1.0f, 1.0f};
+            float root[2] = {1.0f, 1.0f};
             const float scale = scale_next;
 #pragma unroll
             for (int s = 0; s < kPairs / 4; ++s) tok[4 * s] = raw[s].x, tok[4 * s + 1] = raw[s].y, tok[4 * s + 2] = raw[s].z, tok[4 * s + 3] = raw[s].w;
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
                     const uint32_t w = *reinterpret_cast<const uint32_t *>(&p);
                     tok[i] = half2_of(bf16lo(w), bf16hi(w));
                 }
-                unit[0] = __shfl_sync(0xffffffffu, mine, 8 * t4), unit[1] = __shfl_sync(0xffffffffu, mine, 8 * t4 + 4);
+                root[0] = __shfl_sync(0xffffffffu, mine, 8 * t4), root[1] = __shfl_sync(0xffffffffu, mine, 8 * t4 + 4);
             }
             load_tokens();
 #pragma unroll
@@ -400,10 +403,14 @@ __global__ void __launch_bounds__(32 * kUpWarps, 1) k_moe_up(const Args a) {
                 const uint32_t here = ring + (uint32_t)(j * 2 * kCell);
                 const Rows16<kF8> w(read_piece(here), read_piece(here + kCell));
                 if (j < tiles) {
-                    if constexpr (kF8)
-                        multiply_scaled<true>(acc[j], w, tok, __shfl_sync(0xffffffffu, scale, 2 * j), __shfl_sync(0xffffffffu, scale, 2 * j + 1), unit);
-                    else
+                    if constexpr (kF8) {
+                        const float s0 = __shfl_sync(0xffffffffu, scale, 2 * j), s1 = __shfl_sync(0xffffffffu, scale, 2 * j + 1);
+                        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        multiply<__half, true>(part, w, tok);
+                        add_scaled(acc[j], part, s0, s1, root);
+                    } else {
                         multiply<TX, false>(acc[j], w, tok);
+                    }
                 }
                 fetch(j);
             }
@@ -535,7 +542,7 @@ __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
                 bool more = true;
                 while (more) {
                     uint32_t tok[kPairs], low[kPairs], last[kBf16 ? kPairs : 1];
-                    float unit[2] = {1.0f, 1.0f};
+                    float root[2] = {1.0f, 1.0f};
                     const float *const f = reinterpret_cast<const float *>(raw);
                     if constexpr (kBf16) {  // (cut off after 8 bits each time, so that what is left is exact)
 #pragma unroll
@@ -562,7 +569,7 @@ __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
 #pragma unroll
                             for (int q = 0; q < 4; ++q) lows[32 * q] = make_uint4(low[4 * q], low[4 * q + 1], low[4 * q + 2], low[4 * q + 3]);
                         }
-                        unit[0] = __shfl_sync(0xffffffffu, own, 8 * t4), unit[1] = __shfl_sync(0xffffffffu, own, 8 * t4 + 4);
+                        root[0] = __shfl_sync(0xffffffffu, own, 8 * t4), root[1] = __shfl_sync(0xffffffffu, own, 8 * t4 + 4);
                     }
                     const float scale = scale_next;
                     const int was = tile;
@@ -595,8 +602,7 @@ __global__ void __launch_bounds__(32 * kDownWarps, 1) k_moe_down(const Args a) {
                                     multiply<__half, kF8>(part, w, low);
                                     multiply<__half, kF8>(part, w, tok);
                                 }
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) acc[j][q] = fmaf(part[q], (q < 2 ? s0 : s1) * unit[q & 1], acc[j][q]);
+                                add_scaled(acc[j], part, s0, s1, root);
                             }
                         }
                         fetch(j);

@@ -84,7 +84,7 @@ __device__ __forceinline__ void multiply_both(float (&acc)[4], const Rows16<kF8>
         mma<T>(acc, w.a[i][0], w.a[i][1], w.a[i][2], w.a[i][3], x[2 * i], x[2 * i + 1]);
     }
 }
-// acc += ..., times the scales of the two tiles' blocks and what undoes the tokens' powers of two
+// acc += ..., times the scales of the two tiles' blocks and of the tokens' values
 template <bool kF8>
 __device__ __forceinline__ void multiply_scaled(float (&acc)[4], const Rows16<kF8> &w, const uint32_t (&x)[kPairsOf<kF8>], float s0,
                                                 float s1, const float (&unit)[2]) {
@@ -92,6 +92,11 @@ __device__ __forceinline__ void multiply_scaled(float (&acc)[4], const Rows16<kF
     multiply<__half, kF8>(part, w, x);
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] = fmaf(part[k], (k < 2 ? s0 : s1) * unit[k & 1], acc[k]);
+}
+// acc += sums of products, times the scales of the two tiles' blocks and the square of a power of two for each token
+__device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&part)[4], float s0, float s1, const float (&root)[2]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = fmaf(part[k] * root[k & 1], (k < 2 ? s0 : s1) * root[k & 1], acc[k]);
 }
 
 }  // namespace hc

@@ -625,8 +625,9 @@ hc_status hc_fp8_mm(const uint8_t *x, int64_t x_stride, const void *x_scales, hc
  *
  * Sums of products are in fp32; the activation is kept in fp32 and goes into the
  * second product as three bf16 numbers (all 24 bits of it) for bf16 weights, else as two fp16
- * numbers, scaled by a power of two for each block of it (22 bits; of values below 2^-17 of
- * the largest of their block what is above 2^-39 of that); y is rounded once.
+ * numbers, scaled by a power of two for each block of it (22 bits; of values below 2^-16 of
+ * the largest of their block what is above 2^-38 of that); y is rounded once.  Scales of 8-bit
+ * weights lie between 2^-100 and 2^70 (smaller ones may lose bits, larger ones be infinite).
  *
  *   x [T, d] of type (bf16 or fp16), rows x_stride >= 0 apart                in
  *   logits [T, experts] fp32, or NULL                                        in
