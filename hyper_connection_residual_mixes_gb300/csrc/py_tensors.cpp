@@ -15,6 +15,7 @@
 #include <string>
 
 #include <ATen/ops/empty.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 namespace {
@@ -125,8 +126,10 @@ PyObject *dense(PyObject *, PyObject *const *args, Py_ssize_t count) {
     }
 }
 
-// empty(type, device, *sizes): a new contiguous CUDA tensor, of the device's current stream.
+// empty(type, device, *sizes): a new contiguous CUDA tensor, of the device's current stream.  (Errors become
+// what PyTorch's own calls raise: without room torch.OutOfMemoryError.)
 PyObject *empty(PyObject *, PyObject *const *args, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
     int64_t v[2 + kMostAxes];
     if (count < 2 || count > 2 + kMostAxes) {
         PyErr_SetString(PyExc_TypeError, "empty takes a type, a device and sizes");
@@ -137,13 +140,9 @@ PyObject *empty(PyObject *, PyObject *const *args, Py_ssize_t count) {
         PyErr_SetString(PyExc_ValueError, "empty: no such type");
         return nullptr;
     }
-    try {
-        return THPVariable_Wrap(at::empty(at::IntArrayRef(v + 2, (size_t)count - 2),
-                                          at::TensorOptions().dtype(kTypes[v[0]]).device(at::kCUDA, (at::DeviceIndex)v[1])));
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
-    }
+    return THPVariable_Wrap(at::empty(at::IntArrayRef(v + 2, (size_t)count - 2),
+                                      at::TensorOptions().dtype(kTypes[v[0]]).device(at::kCUDA, (at::DeviceIndex)v[1])));
+    END_HANDLE_TH_ERRORS
 }
 
 PyMethodDef methods[] = {{"snapshot", snapshot, METH_O, "Bytes that tell whether any of a list of tensors has changed."},
