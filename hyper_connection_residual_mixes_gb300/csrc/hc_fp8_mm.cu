@@ -470,8 +470,10 @@ __global__ void __launch_bounds__(32 * kFewWarps<NB>, 1) k_fp8_few(const Args a,
 }
 
 // A matrix of codes [rows][width], rows `stride` bytes apart, boxes of 128 x 128, 128-byte
-// swizzle, zeros outside.  (Maps of less than 128 KB load slowly, but one that spans more than
-// the matrix touches what lies behind it: an illegal address.)
+// swizzle, zeros outside: the map names the rows and columns that are there and nothing else.  (Maps of less than
+// 128 KB load slowly.  Maps with a third dimension that no load used, to reach that length, were followed by an illegal
+// address in a captured product of 100 rows, in one of some six runs of the tests: the suspected cause is memory behind
+// the matrix that such a map names.)
 bool make_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, int64_t stride) {
     const auto enc = encoder();
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};

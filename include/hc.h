@@ -598,7 +598,8 @@ hc_status hc_rms_norm_backward(const void *g_y, int64_t g_stride, const void *g_
  *   that is 0.
  * M, N and K < 2^31 - 4096; N and K multiples of 16; x and w start on 16 bytes and x_stride is a
  * multiple of 16 (the tensor copies' rule; HC_ERR_UNSUPPORTED, HC_ERR_MISALIGNED
- * otherwise).
+ * otherwise).  What lies between x's rows, before the first and behind the last
+ * goes into no result; loads bring whole lines of 256 bytes, from 256-byte boundaries on, into the L2 cache.
  */
 size_t hc_fp8_mm_workspace_bytes(int transposed, int64_t M, int N, int K);
 
