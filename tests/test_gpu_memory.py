@@ -21,6 +21,7 @@ def test_no_room_for_the_output():
     """The process's own limit is set, so that the refusal is the allocator's and nothing is filled."""
     x, w = torch.ones((1, 1024), device="cuda").expand(1 << 20, 1024), torch.ones((1024,), device="cuda")
     torch.cuda.synchronize()
+    torch.cuda.empty_cache()  # (what earlier calls left in the cache would be room)
     room = (torch.cuda.memory_reserved() + (64 << 20)) / torch.cuda.get_device_properties(0).total_memory
     torch.cuda.set_per_process_memory_fraction(room)
     try:
