@@ -14,7 +14,7 @@
 // What bounds it: a block of 128 x 256 x 128 takes the tensor cores 512 cycles, but 1,050
 // pass, in which the eight writing warps load 32,768 sums from tensor memory and add each to its
 // accumulator (a packed FMA for two), on the same issue slots as all else.  16,384 x
-// 10,240 x 5,120: 750 us, 2.29 PFLOP/s; transposed 2.30.  What other shapes of the same took there, in us:
+// 10,240 x 5,120: 750 to 795 us, by the board's clocks, 2.16 to 2.29 PFLOP/s.  What other shapes of the same took beside 750, in us:
 // pairs of CTAs on 256 x 256 787 (1,187 with a releasing arrival at the other CTA for each block), 128 x 128
 // tiles 1,022 in four parts of columns, three issuing warps in turn 753, the next sums loaded
 // between the FMAs of the last 772, MMAs held back to even the issue 768 and more.

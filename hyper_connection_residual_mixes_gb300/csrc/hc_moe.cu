@@ -24,11 +24,11 @@
 // in shared memory, experts in ascending order.  It is launched early and has made its lists and
 // asked for its first weights when the first kernel ends.
 //
-// Measured (64 experts, 6 a token, 5,120 -> 2,048, 8-bit weights), in us, and of 6,767 GB/s for the
-// chosen experts' weights: 16 tokens 288 (0.82), one token 52 (0.54; 189 MB, of which each SM has too
-// little to reach the full rate), 64 tokens 568; 8 tokens of 8 experts, 16-bit weights, 0.89 (bf16)
-// and 0.97 (fp16).  37 tokens of 13 experts, 1,072 -> 336: 42, latency of two kernels' choices
-// and of the rounds.
+// Measured (64 experts, 6 a token, 5,120 -> 2,048, 8-bit weights, bf16 outputs), in us, and of 6,767 GB/s for
+// the chosen experts' weights: 16 tokens 309 (0.77), one token 55 (0.50), 64 tokens 597 (0.50); with the activation as
+// one fp16 number, 11 bits of it, 290, 53 and 570.  fp16 outputs 307 and 589.  8 tokens, 2 of 8 experts, 16-bit
+// weights, 79 (0.85; as two bf16 numbers 77.6).  37 tokens, 3 of 13 experts, 1,072 -> 336, 16-bit weights: 43 (bf16),
+// 42 (fp16), latency: what of it the choices, the rounds and the two starts are has not been measured.
 #include <atomic>
 
 #include <cuda.h>

@@ -10,9 +10,10 @@
 // All sums run in fp32.
 //
 // Bound by HBM: each input is read once, each output written once, and a row stays in
-// registers (forward) or in its slot of shared memory (backward) between the sums and what
+// registers (forward) or in its slot of shared memory (backward, in the ring) between the sums and what
 // needs them.  Long runs of rows come through a ring of bulk copies, short ones and rows that do not
-// line up straight into registers.  Measured, in us, and of 6,767 GB/s (a plain
+// line up straight into registers; in the backward these, and rows of less than 1,024 or more than 8,192
+// columns, are read twice, the second time from L1 or L2.  Measured, in us, and of 6,767 GB/s (a plain
 // copy): forward of 65,536 x 5,120 bf16 with residual and 8-bit output 361 (0.96), backward of
 // 8,192 x 5,120 with fp32 gradients 89 (0.97), 16 rows of 5,120 2.6 (one row's load, sum and write
 // after another), 1,501 x 1,031 fp32 backward 12.  Rows that do not line up: 0.1 to 0.25, single
@@ -363,7 +364,8 @@ int sm_count() {
     return n;
 }
 // Slots of a ring and blocks of a launch: a grid that fills the SMs once (`most_per_sm` blocks
-// each at the most), with as many slots as fit in `room` bytes of an SM, two at least.  What a kernel
+// each at the most), with as many slots as fit in `room` bytes of an SM, two where two fit
+// (of fp32 rows of 16,384 with a residual one does).  What a kernel
 // needs is asked for and set once per device.
 template <auto kKernel>
 cudaError_t ring_shape(int threads, int slot_bytes, int most_per_sm, int room, int64_t most, int *slots, int *blocks) {
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(kWarps ? 256 : 1024) k_rms_backward(const Back
 // The same with the rows of r, g and g_r through a ring: 8 columns a thread in two runs of 4.
 // Both passes over a row read it from its slot, which is filled again once the next
 // row's barrier has passed.  8,192 x 5,120, fp32 gradients: 179 us with rows read twice through
-// L2, 89 here.  Rows past 8,192 leave fewer than three slots and take the kernel above (0.53 of HBM).
+// L2, 89 here.  A block has 1,024 threads at the most, so rows past 8,192 take the kernel above (0.53 of HBM).
 template <typename TX, typename TG, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads, 1) k_rms_backward_ring(const BackArgs a, int slots) {
     extern __shared__ __align__(16) uint8_t s_rows[];
@@ -798,7 +800,8 @@ cudaError_t cast(const void *x, int64_t xs, int64_t n, int d, uint8_t *codes, in
 }
 
 // A matrix [N, K] in blocks of 128 x 128: a thread block each, thread t the columns
-// 4 (t % 32) .. + 3 of the rows t / 32 + 8 i.
+// 4 (t % 32) .. + 3 of the rows t / 32 + 8 i.  16,384 x 5,120: 178 us of bf16 (0.21 of HBM), 185 of fp32
+// (0.33); one by one, 5,121 wide, 367 and 388.  Weights are cast once: nothing was done about it yet.
 template <typename T, bool kVector>
 __global__ void __launch_bounds__(256)
 k_fp8_cast_weights(const T *__restrict__ w, int64_t N, int K, int64_t row_blocks, int col_blocks, uint8_t *__restrict__ codes,

@@ -586,7 +586,7 @@ hc_status hc_rms_norm_backward(const void *g_y, int64_t g_stride, const void *g_
  * same call gives the same bits, on any device.  (The gradient of the weights is
  * hc_grouped_mm_weights of the 16-bit rows, as one expert's.)
  *
- *   x [M, K] codes (transposed: [M, N]), rows x_stride apart                 in
+ *   x [M, K] codes (transposed: [M, N]), rows x_stride >= the width apart    in
  *   x_scales [M, ceil(K / 128)] (transposed: [M, ceil(N / 128)]) of x_scale_type:
  *   HC_F32 or HC_UE8M0                                                     in
  *   w [N, K] codes, w_scales [ceil(N / 128), ceil(K / 128)] of w_scale_type, in
